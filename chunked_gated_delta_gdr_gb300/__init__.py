@@ -26,6 +26,20 @@ from .api import (  # noqa: F401
     wait_selftest,
     workspace_bytes,
 )
+from .mixer import (  # noqa: F401
+    conv_bwd,
+    conv_fwd,
+    conv_step,
+    delta_step,
+    qk_bwd,
+    qk_fwd,
+    qk_norm_rotate,
+    selective_ssm,
+    short_conv,
+    ssm_bwd,
+    ssm_fwd,
+    ssm_step,
+)
 from ._native import GdrError  # noqa: F401
 
 __version__ = "0.1.0"

@@ -16,6 +16,7 @@ STATUS = {
     -4: "GDR_ERR_STRIDE", -5: "GDR_ERR_DIM", -6: "GDR_ERR_HEADS", -7: "GDR_ERR_NSEQ",
     -8: "GDR_ERR_WORKSPACE", -9: "GDR_ERR_PATH", -10: "GDR_ERR_CUDA", -11: "GDR_ERR_ALIGN",
     -12: "GDR_ERR_DEVICE", -13: "GDR_ERR_SCRATCH_LIMIT", -14: "GDR_ERR_CKPT",
+    -15: "GDR_ERR_OPTION",
 }
 
 # Every function the header declares, with its ctypes signature.
@@ -54,6 +55,23 @@ SIGNATURES = {
     "gdr_device_status": (ctypes.c_int, [_vp]),
     "gdr_debug_wait_selftest": (ctypes.c_int, [ctypes.c_uint32, _vp]),
     "gdr_clear_device_status": (ctypes.c_int, []),
+    # tensors of the mixer's operators are passed as addresses of descriptors
+    "gdr_conv_fwd": (ctypes.c_int, [_vp] * 5 + [_i32] * 2 + [_vp] * 3),
+    "gdr_conv_bwd": (ctypes.c_int, [_vp] * 5 + [_i32] * 2 + [_vp] * 7 + [_sz, _vp]),
+    "gdr_conv_bwd_workspace_bytes": (_sz, [_i64, _i32, _i32]),
+    "gdr_conv_step": (ctypes.c_int, [_vp] * 5 + [_i32] + [_vp] * 2),
+    "gdr_ssm_fwd": (ctypes.c_int, [_vp] * 8 + [_i32] + [_vp] * 2 + [_i32] + [_vp] * 3
+                    + [_sz, _vp]),
+    "gdr_ssm_fwd_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
+    "gdr_ssm_bwd": (ctypes.c_int, [_vp] * 8 + [_i32] + [_vp] * 2 + [_i32] + [_vp] * 12
+                    + [_sz, _vp]),
+    "gdr_ssm_bwd_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
+    "gdr_ssm_step": (ctypes.c_int, [_vp] * 8 + [_i32] + [_vp] * 4),
+    "gdr_qk_fwd": (ctypes.c_int, [_vp] * 4 + [_i32, _f32] + [_vp] * 3 + [_i32] + [_vp] * 3),
+    "gdr_qk_bwd": (ctypes.c_int, [_vp] * 4 + [_i32, _f32] + [_vp] * 3 + [_i32] + [_vp] * 7
+                   + [_sz, _vp]),
+    "gdr_qk_bwd_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
+    "gdr_delta_step": (ctypes.c_int, [_vp] * 5 + [_f32] + [_vp] * 4),
     "gdr_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "gdr_version": (ctypes.c_int, []),
 }

@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include "gdr_bwd.cuh"
+#include "gdr_desc.cuh"
 #include "gdr_internal.cuh"
 #include "gdr_sched.cuh"
 
@@ -12,63 +13,7 @@ using namespace gdr;
 
 namespace {
 
-struct Desc {
-  void *p;
-  int ndim;
-  int64_t shape[4];
-  int64_t stride[4];
-};
-
-int read_desc(const gdr_tensor_t *t, int dtype, int ndim, Desc *d) {
-  if (!t) return GDR_ERR_NULL;
-  if (t->dtype != dtype) return GDR_ERR_DTYPE;
-  if (t->ndim != ndim) return GDR_ERR_SHAPE;
-  int64_t numel = 1;
-  for (int i = 0; i < ndim; ++i) {
-    if (t->shape[i] < 0) return GDR_ERR_SHAPE;
-    d->shape[i] = t->shape[i];
-    numel *= t->shape[i];
-  }
-  if (!t->data && numel > 0) return GDR_ERR_NULL;
-  d->p = t->data;
-  d->ndim = ndim;
-  if (t->strides) {
-    for (int i = 0; i < ndim; ++i) {
-      if (t->strides[i] < 0) return GDR_ERR_STRIDE;
-      d->stride[i] = t->strides[i];
-    }
-    if (d->shape[ndim - 1] > 1 && d->stride[ndim - 1] != 1) return GDR_ERR_STRIDE;
-    d->stride[ndim - 1] = 1;
-  } else {
-    int64_t s = 1;
-    for (int i = ndim - 1; i >= 0; --i) {
-      d->stride[i] = s;
-      s *= d->shape[i];
-    }
-  }
-  return GDR_OK;
-}
-
-bool compact(const Desc &d) {
-  int64_t s = 1;
-  for (int i = d.ndim - 1; i >= 0; --i) {
-    if (d.shape[i] > 1 && d.stride[i] != s) return false;
-    s *= d.shape[i];
-  }
-  return true;
-}
-
 View view_of(const Desc &d) { return View{d.p, d.stride[0], d.ndim > 1 ? d.stride[1] : 0}; }
-
-int device_ok() {
-  int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return GDR_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-    return GDR_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return GDR_ERR_CUDA;
-  return (major == 10 && minor == 3) ? GDR_OK : GDR_ERR_DEVICE;
-}
 
 // Validated problem: extents and views of every operand of the forward.
 struct Problem {
@@ -327,6 +272,7 @@ const char *gdr_status_string(int status) {
       return "problem too large for the 4 MiB static scratch of gdr_chunk_out_noalloc";
     case GDR_ERR_CKPT:
       return "checkpoint interval not a positive multiple of 64, or checkpoint buffers wrong";
+    case GDR_ERR_OPTION: return "unknown option, or options that do not go together";
     default: return "unknown status";
   }
 }

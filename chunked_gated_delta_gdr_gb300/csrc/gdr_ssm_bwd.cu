@@ -1,0 +1,768 @@
+// gdr_ssm_bwd.cu -- backward of the selective state space scan.  With y's gradient after the gate
+// dy = dout z sigmoid(z), a_t = e^{dt_t A} and the states' gradient
+//
+//   g_t = C_t dy_t + a_{t+1} g_{t+1}      (+ the final state's gradient at the segment's end)
+//
+//   dC_t = sum_d dy h_t,   dB_t = sum_d dt x g_t,   p_t = sum_n B g_t,   c_t = a_t h_{t-1} g_t,
+//   dx = dt p + D dy,   ddt = (x p + sum_n A c_t) sigmoid(raw),   dA = sum_t dt c_t,
+//   dD = sum_t dy x,   dz = dout y (z sigmoid(z))',   dh0 = a g at the segment's first token.
+//
+// The token axis is cut into ranges as in the forward.  Pass 1 runs each range once, forwards,
+// from a zero state: it keeps the state at its end and, with the running product of the a, the
+// gradient that its own tokens send to the state before it.  A short kernel chains both over the
+// ranges.  Pass 2 then has a range's true state at its start and true gradient at its end: it
+// sweeps forwards keeping the state before every tile of 8 tokens in shared memory, then takes the
+// tiles last to first, recomputes a tile's states into registers and walks back through them.
+// Sums over states (p, c A, y) are left as partial sums of LN lanes in shared memory; sums over
+// channels (dB, dC) go over the warp's lanes by a transposing butterfly, over its warps in shared
+// memory and over the blocks in a last kernel, always in the same order.
+//
+// About 16 products and 3 exponentials for each token, channel and state: bound by the fp32 pipes.
+#include "gdr_ssm.cuh"
+
+namespace gdr {
+namespace ssm {
+namespace {
+
+using namespace mix;
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kBT = 8;       // tokens of a tile of pass 2
+constexpr int kRange = 64;   // tokens of a range
+
+struct BwdWork {
+  int n;            // ranges
+  float *state;     // [n][D][N]: states at the ranges' ends, then at their starts, then dA's parts
+  float *grad;      // [n][D][N]: gradients at the ranges' starts, then at their ends
+  float *sum;       // [n][D]: sum of dt
+  float *pd, *pb;   // [n][D]: parts of dD and ddt_bias
+  int *reset;       // [n]
+  float *bc;        // [channel tiles][T][2][NP]: parts of dB and dC
+  size_t bytes;
+};
+
+template <typename E, int M>
+struct Elems {
+  E v[M];
+};
+template <bool VEC, typename E, int M>
+__device__ __forceinline__ Elems<E, M> ldm(const E *p, int n) {
+  Elems<E, M> r;
+  constexpr int bytes = M * (int)sizeof(E);
+  if constexpr (VEC && bytes >= 4) {
+    constexpr int w = bytes >= 16 ? 16 : bytes;
+    if constexpr (w == 16) {
+      uint4 q[bytes / 16];
+#pragma unroll
+      for (int i = 0; i < bytes / 16; ++i)
+        q[i] = n > 0 ? reinterpret_cast<const uint4 *>(p)[i] : make_uint4(0, 0, 0, 0);
+      memcpy(&r, q, bytes);
+    } else if constexpr (w == 8) {
+      const uint2 q = n > 0 ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0, 0);
+      memcpy(&r, &q, 8);
+    } else {
+      const uint32_t q = n > 0 ? *reinterpret_cast<const uint32_t *>(p) : 0u;
+      memcpy(&r, &q, 4);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < M; ++i) r.v[i] = i < n ? p[i] : E(0.f);
+  }
+  return r;
+}
+template <bool VEC, typename E, int M>
+__device__ __forceinline__ void stm(E *p, const float (&f)[M], int n) {
+  Elems<E, M> r;
+#pragma unroll
+  for (int i = 0; i < M; ++i) st1(&r.v[i], f[i]);
+  constexpr int bytes = M * (int)sizeof(E);
+  if constexpr (VEC && bytes >= 4) {
+    if (n <= 0) return;
+    if constexpr (bytes >= 16) {
+      uint4 q[bytes / 16];
+      memcpy(q, &r, bytes);
+#pragma unroll
+      for (int i = 0; i < bytes / 16; ++i) reinterpret_cast<uint4 *>(p)[i] = q[i];
+    } else if constexpr (bytes == 8) {
+      uint2 q;
+      memcpy(&q, &r, 8);
+      *reinterpret_cast<uint2 *>(p) = q;
+    } else {
+      uint32_t q;
+      memcpy(&q, &r, 4);
+      *reinterpret_cast<uint32_t *>(p) = q;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+      if (i < n) p[i] = r.v[i];
+  }
+}
+
+// What the two passes share: a block's channels and a thread's states.
+template <int LN>
+struct Place {
+  using Y = Lay<LN>;
+  int tid, warp, lane, nl, cl, ct, r, grp, c0, nch;
+  int ch[2];
+  __device__ __forceinline__ Place(const SsmArgs &a, int tiles_per_group) {
+    tid = threadIdx.x;
+    warp = tid >> 5;
+    lane = tid & 31;
+    nl = lane % LN;
+    cl = lane / LN;
+    const int ctiles = tiles_per_group * a.G, Dg = a.D / a.G;
+    ct = blockIdx.x % ctiles;
+    r = blockIdx.x / ctiles;
+    grp = ct / tiles_per_group;
+    c0 = grp * Dg + ct % tiles_per_group * Y::CH;
+    nch = min(Y::CH, (grp + 1) * Dg - c0);
+    ch[0] = Y::channel(warp, lane, 0);
+    ch[1] = Y::channel(warp, lane, 1);
+  }
+  __device__ __forceinline__ void read(const SsmArgs &a, const float *p, int64_t row,
+                                       float (&h)[2][4]) const {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = nl * 4 + j;
+        h[k][j] = (p && ch[k] < nch && n < a.N) ? p[(row * a.D + c0 + ch[k]) * a.N + n] : 0.f;
+      }
+  }
+  __device__ __forceinline__ void write(const SsmArgs &a, float *p, int64_t row,
+                                        const float (&h)[2][4]) const {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = nl * 4 + j;
+        if (ch[k] < nch && n < a.N) p[(row * a.D + c0 + ch[k]) * a.N + n] = h[k][j];
+      }
+  }
+};
+
+// The whole range's segment bounds: marks, and each token's segment.
+struct RangeSegs {
+  int mark[kRange + 1], seg[kRange], any;
+  int red[64];
+};
+__device__ __forceinline__ void range_segments(const SsmArgs &a, int t0, int n, RangeSegs &s) {
+  SegCursor c = seg_find(a.cu, a.n_seq, a.T, t0, s.red);
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int base = c.j - 1;
+    const bool any = seg_marks(a.cu, a.n_seq, a.T, t0, n, s.mark, c);
+    if (!any)
+      for (int i = lane; i <= n; i += 32) s.mark[i] = -1;
+    __syncwarp();
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      int v = i0 + lane < n ? s.mark[i0 + lane] : -1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = max(v, u);
+      }
+      v = max(v, base);
+      if (i0 + lane < n) s.seg[i0 + lane] = v;
+      base = __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) s.any = any;
+  }
+  __syncthreads();
+}
+
+template <int LN>
+struct Tile1 {
+  using Y = Lay<LN>;
+  float2 pair[Y::L * Y::CH];
+  float dy[Y::L * Y::CH];
+  float b[Y::L * Y::NP], c[Y::L * Y::NP];
+  RangeSegs s;
+};
+
+// Pass 1.
+template <typename E, int LN, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+    k_ssm_bwd_ends(const SsmArgs a, const BwdWork w, int tiles_per_group) {
+  using Y = Lay<LN>;
+  constexpr int L = Y::L, NP = Y::NP, CH = Y::CH;
+  extern __shared__ __align__(16) char smem_raw[];
+  Tile1<LN> &s = *reinterpret_cast<Tile1<LN> *>(smem_raw);
+  const Place<LN> P(a, tiles_per_group);
+  const int t0 = P.r * kRange, n = min(kRange, a.T - t0);
+  float A2[2][4], h[2][4], pr[2][4], gs[2][4], S[2] = {0.f, 0.f};
+  P.read(a, a.A, 0, A2);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      A2[k][j] *= kLog2e;
+      h[k][j] = gs[k][j] = 0.f;
+      pr[k][j] = 1.f;
+    }
+  const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
+  const int64_t c = P.c0 + lc;
+  const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
+  const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
+  range_segments(a, t0, n, s.s);
+  bool reset = false, active = true;
+  int seg = -1;
+  for (int i0 = 0; i0 < n; i0 += L) {
+    const int m = min(L, n - i0), t = t0 + i0 + lt;
+    const int sg = lt < m ? s.s.seg[i0 + lt] : -1;
+    const int ok = sg >= 0 && sg < a.n_seq ? nv : 0;
+    float x[8], d[8], g[8], z[8];
+    unpack8(ld8<VEC>(reinterpret_cast<const E *>(a.x.p) + t * a.x.st + c, ok), x);
+    unpack8(ld8<VEC>(reinterpret_cast<const E *>(a.dt.p) + t * a.dt.st + c, ok), d);
+    unpack8(ld8<VEC>(reinterpret_cast<const E *>(a.dout.p) + t * a.dout.st + c, ok), g);
+    if (a.z.p) unpack8(ld8<VEC>(reinterpret_cast<const E *>(a.z.p) + t * a.z.st + c, ok), z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v = d[i] + ((a.dt_bias && i < nv) ? a.dt_bias[c + i] : 0.f);
+      if (a.softplus) v = softplusf(v);
+      if (a.z.p) g[i] *= z[i] * sigmoidf(z[i]);
+      const int at = Y::pair_at(lt, lc + i);
+      s.pair[at] = make_float2(v, v * x[i]);
+      s.dy[at] = g[i];
+    }
+    for (int e = P.tid; e < L * NP; e += kThreads) {
+      const int i = e / NP, q = e % NP;
+      const bool in = i < m && q < a.N && s.s.seg[i0 + i] >= 0 && s.s.seg[i0 + i] < a.n_seq;
+      s.b[e] = in ? ld1(Bp + (int64_t)(t0 + i0 + i) * a.B_st + q) : 0.f;
+      s.c[e] = in ? ld1(Cp + (int64_t)(t0 + i0 + i) * a.C_st + q) : 0.f;
+    }
+    __syncthreads();
+    auto scan = [&](int from, int to) {
+#pragma unroll 4
+      for (int i = from; i < to; ++i) {
+        const int at = i * CH + Y::pair_slot(i, P.warp, P.cl) * 2;
+        const float4 q = *reinterpret_cast<const float4 *>(&s.pair[at]);
+        const float2 dyv = *reinterpret_cast<const float2 *>(&s.dy[at]);
+        const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
+        const float4 C = *reinterpret_cast<const float4 *>(&s.c[i * NP + P.nl * 4]);
+        const float dt[2] = {q.x, q.z}, dx[2] = {q.y, q.w}, dy[2] = {dyv.x, dyv.y};
+        const float Bv[4] = {B.x, B.y, B.z, B.w}, Cv[4] = {C.x, C.y, C.z, C.w};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          S[k] += dt[k];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float e = ex2(dt[k] * A2[k][j]);
+            h[k][j] = fmaf(e, h[k][j], dx[k] * Bv[j]);
+            pr[k][j] *= e;
+            gs[k][j] = fmaf(pr[k][j], Cv[j] * dy[k], gs[k][j]);
+          }
+        }
+      }
+    };
+    for (int i = 0; i < m;) {
+      if (s.s.mark[i0 + i] >= 0) {
+        const int next = s.s.mark[i0 + i];
+        P.read(a, next < a.n_seq ? a.h0 : nullptr, next, h);
+        S[0] = S[1] = 0.f;
+        reset = true;
+        if (active) {  // nothing from here on reaches the state before the range
+          active = false;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pr[k][j] = 0.f;
+        }
+      }
+      int e = i + 1;
+      while (e < m && s.s.mark[i0 + e] < 0) ++e;
+      seg = s.s.seg[i0 + i];
+      if (seg >= 0 && seg < a.n_seq) {
+        scan(i, e);
+        if (active && s.s.mark[i0 + e] >= 0 && a.dht) {
+          float f[2][4];
+          P.read(a, a.dht, seg, f);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) gs[k][j] = fmaf(pr[k][j], f[k][j], gs[k][j]);
+        }
+      }
+      i = e;
+    }
+    __syncthreads();
+  }
+  P.write(a, w.state, P.r, h);
+  P.write(a, w.grad, P.r, gs);
+  if (P.nl == 0) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (P.ch[k] < P.nch) w.sum[(int64_t)P.r * a.D + P.c0 + P.ch[k]] = S[k];
+  }
+  if (P.ct == 0 && P.tid == 0) w.reset[P.r] = reset;
+}
+
+// States forwards to the ranges' starts, gradients backwards to the ranges' ends.
+__global__ void k_ssm_bwd_chain(const float *A, const BwdWork w, int D, int N) {
+  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, size = (int64_t)D * N;
+  if (i >= size) return;
+  const float A2 = A[i] * kLog2e;
+  const int d = (int)(i / N);
+  constexpr int U = 8;
+  const bool back = blockIdx.y != 0;
+  float *val = back ? w.grad : w.state;
+  float cur = 0.f;
+  for (int r0 = 0; r0 < w.n; r0 += U) {
+    float own[U], sum[U];
+    int rs[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool ok = r0 + u < w.n;
+      const int64_t r = !ok ? 0 : back ? w.n - 1 - (r0 + u) : r0 + u;
+      own[u] = ok ? val[r * size + i] : 0.f;
+      sum[u] = ok ? w.sum[r * D + d] : 0.f;
+      rs[u] = ok ? w.reset[r] : 1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r0 + u < w.n) {
+        const int64_t r = back ? w.n - 1 - (r0 + u) : r0 + u;
+        val[r * size + i] = cur;
+        cur = rs[u] ? own[u] : fmaf(ex2(A2 * sum[u]), cur, own[u]);
+      }
+  }
+}
+
+template <int LN>
+struct Tile2 {
+  using Y = Lay<LN>;
+  float4 kept[kRange / kBT][2][kThreads];  // the state before each tile
+  float2 pair[kBT * Y::CH];                // (dt, dt x)
+  float dy[kBT * Y::CH];
+  float b[kBT * Y::NP], c[kBT * Y::NP];
+  float pp[kBT * Y::CH * LN], pc[kBT * Y::CH * LN], py[kBT * Y::CH * LN];
+  float red[kThreads / 32][kBT][2 * Y::NP];
+  RangeSegs s;
+};
+
+// Sums v[0..3] (dB) and v[4..7] (dC) over the lanes that hold the same states; each lane is left
+// with 8 / CW of the sums, the first being number `first`.
+template <int LN>
+__device__ __forceinline__ int channel_sums(float (&v)[8], int lane) {
+  int first = 0;
+  auto half = [&](int off, int cnt) {
+    const bool up = lane & off;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < cnt) {
+        const float send = up ? v[i] : v[i + cnt], keep = up ? v[i + cnt] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+      }
+    if (up) first += cnt;
+  };
+  half(16, 4);
+  if (LN <= 8) half(8, 2);
+  if (LN <= 4) half(4, 1);
+  if (LN <= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+  return first;
+}
+
+// Pass 2.
+template <typename E, int LN, bool VEC>
+__global__ void __launch_bounds__(kThreads, 3)
+    k_ssm_bwd(const SsmArgs a, const BwdWork w, int tiles_per_group) {
+  using Y = Lay<LN>;
+  constexpr int NP = Y::NP, CH = Y::CH;
+  constexpr int M = kBT * CH / kThreads;  // elements of x a thread has of a tile
+  constexpr int LEFT = LN <= 4 ? 1 : LN / 4;  // channel sums left to a lane
+  extern __shared__ __align__(16) char smem_raw[];
+  Tile2<LN> &s = *reinterpret_cast<Tile2<LN> *>(smem_raw);
+  const Place<LN> P(a, tiles_per_group);
+  if (P.r == w.n) {  // initial states' gradients of the segments without tokens
+    for_empty_segments(a.cu, a.n_seq, a.T, s.s.red, [&](int q) {
+      const int64_t at = ((int64_t)q * a.D + P.c0) * a.N;
+      for (int i = P.tid; i < P.nch * a.N; i += kThreads)
+        a.dh0[at + i] = a.dht ? a.dht[at + i] : 0.f;
+    });
+    return;
+  }
+  const int t0 = P.r * kRange, n = min(kRange, a.T - t0), tiles = (n + kBT - 1) / kBT;
+  float A2[2][4], h[2][4], g[2][4], dA[2][4];
+  P.read(a, a.A, 0, A2);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      A2[k][j] *= kLog2e;
+      dA[k][j] = 0.f;
+    }
+  const int lt = P.tid / (CH / M), lc = P.tid % (CH / M) * M, nv = max(0, min(M, P.nch - lc));
+  const int64_t c = P.c0 + lc;
+  const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
+  const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
+  float bias[M], skip[M], sd[M], sb[M];
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    bias[i] = (a.dt_bias && i < nv) ? a.dt_bias[c + i] : 0.f;
+    skip[i] = (a.Dskip && i < nv) ? a.Dskip[c + i] : 0.f;
+    sd[i] = sb[i] = 0.f;
+  }
+  range_segments(a, t0, n, s.s);
+  const bool marks = s.s.any;
+  auto covered = [&](int i) { return i < n && s.s.seg[i] >= 0 && s.s.seg[i] < a.n_seq; };
+  auto clear = [&](float (&v)[2][4]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[k][j] = 0.f;
+  };
+  auto start_state = [&](int seg, float (&v)[2][4]) {
+    P.read(a, seg < a.n_seq ? a.h0 : nullptr, seg, v);
+  };
+  auto end_grad = [&](int i, float (&v)[2][4]) {  // token i is the last of its segment
+    P.read(a, covered(i) ? a.dht : nullptr, s.s.seg[i], v);
+  };
+  const E *xp = reinterpret_cast<const E *>(a.x.p) + c, *dp = reinterpret_cast<const E *>(a.dt.p) + c;
+  const E *gp = reinterpret_cast<const E *>(a.dout.p) + c;
+  const E *zp = a.z.p ? reinterpret_cast<const E *>(a.z.p) + c : nullptr;
+
+  // a token without a segment, and one past the end, is neutral: dt, dt x, dy = 0
+  auto put_pairs = [&](const Elems<E, M> &x, const Elems<E, M> &d, bool in) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      float v = ld1(&d.v[i]) + bias[i];
+      if (a.softplus) v = softplusf(v);
+      s.pair[Y::pair_at(lt, lc + i)] =
+          in ? make_float2(v, v * ld1(&x.v[i])) : make_float2(0.f, 0.f);
+    }
+  };
+
+  // the sweep: states before each tile
+  if (w.n > 1 && P.r > 0 && covered(0) && s.s.mark[0] < 0)
+    P.read(a, w.state, P.r, h);
+  else
+    clear(h);
+  for (int q = 0; q < tiles; ++q) {
+    s.kept[q][0][P.tid] = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
+    s.kept[q][1][P.tid] = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
+    if (q + 1 == tiles) break;
+    const int i0 = q * kBT, t = t0 + i0 + lt;
+    const bool in = covered(i0 + lt);
+    put_pairs(ldm<VEC, E, M>(xp + t * a.x.st, in ? nv : 0),
+              ldm<VEC, E, M>(dp + t * a.dt.st, in ? nv : 0), in);
+    for (int e = P.tid; e < kBT * NP; e += kThreads) {
+      const int i = e / NP, m = e % NP;
+      s.b[e] = covered(i0 + i) && m < a.N ? ld1(Bp + (int64_t)(t0 + i0 + i) * a.B_st + m) : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kBT; ++i) {
+      if (marks && s.s.mark[i0 + i] >= 0) start_state(s.s.mark[i0 + i], h);
+      const float4 v = *reinterpret_cast<const float4 *>(
+          &s.pair[i * CH + Y::pair_slot(i, P.warp, P.cl) * 2]);
+      const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
+      const float dt[2] = {v.x, v.z}, dx[2] = {v.y, v.w}, Bv[4] = {B.x, B.y, B.z, B.w};
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          h[k][j] = fmaf(ex2(dt[k] * A2[k][j]), h[k][j], dx[k] * Bv[j]);
+    }
+    __syncthreads();
+  }
+
+  // the gradient that arrives at the range's end
+  if (s.s.mark[n] >= 0)
+    end_grad(n - 1, g);
+  else if (w.n > 1)
+    P.read(a, w.grad, P.r, g);
+  else
+    clear(g);
+
+  for (int q = tiles - 1; q >= 0; --q) {
+    const int i0 = q * kBT, t = t0 + i0 + lt;
+    const bool in = covered(i0 + lt);
+    const int m = in ? nv : 0;
+    const Elems<E, M> rx = ldm<VEC, E, M>(xp + t * a.x.st, m), rd = ldm<VEC, E, M>(dp + t * a.dt.st, m),
+                      rg = ldm<VEC, E, M>(gp + t * a.dout.st, m);
+    Elems<E, M> rz = rx;
+    if (zp) rz = ldm<VEC, E, M>(zp + t * a.z.st, m);
+    put_pairs(rx, rd, in);
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const float z = ld1(&rz.v[i]);
+      s.dy[Y::pair_at(lt, lc + i)] = ld1(&rg.v[i]) * (zp ? z * sigmoidf(z) : 1.f);
+    }
+    for (int e = P.tid; e < kBT * NP; e += kThreads) {
+      const int i = e / NP, j = e % NP;
+      const bool ok = covered(i0 + i) && j < a.N;
+      s.b[e] = ok ? ld1(Bp + (int64_t)(t0 + i0 + i) * a.B_st + j) : 0.f;
+      s.c[e] = ok ? ld1(Cp + (int64_t)(t0 + i0 + i) * a.C_st + j) : 0.f;
+    }
+    __syncthreads();
+    float hist[kBT][2][4], before[2][4];
+    {
+      const float4 u = s.kept[q][0][P.tid], v = s.kept[q][1][P.tid];
+      before[0][0] = u.x; before[0][1] = u.y; before[0][2] = u.z; before[0][3] = u.w;
+      before[1][0] = v.x; before[1][1] = v.y; before[1][2] = v.z; before[1][3] = v.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[k][j] = before[k][j];
+#pragma unroll
+    for (int i = 0; i < kBT; ++i) {
+      if (marks && i0 + i < n && s.s.mark[i0 + i] >= 0) start_state(s.s.mark[i0 + i], h);
+      const float4 v = *reinterpret_cast<const float4 *>(
+          &s.pair[i * CH + Y::pair_slot(i, P.warp, P.cl) * 2]);
+      const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
+      const float dt[2] = {v.x, v.z}, dx[2] = {v.y, v.w}, Bv[4] = {B.x, B.y, B.z, B.w};
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          h[k][j] = fmaf(ex2(dt[k] * A2[k][j]), h[k][j], dx[k] * Bv[j]);
+          hist[i][k][j] = h[k][j];
+        }
+      if (zp) {
+        const float4 C = *reinterpret_cast<const float4 *>(&s.c[i * NP + P.nl * 4]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          s.py[Y::part_at(i, P.ch[k]) + P.nl] =
+              fmaf(h[k][0], C.x, h[k][1] * C.y) + fmaf(h[k][2], C.z, h[k][3] * C.w);
+      }
+    }
+#pragma unroll
+    for (int i = kBT - 1; i >= 0; --i) {
+      const int at = i * CH + Y::pair_slot(i, P.warp, P.cl) * 2;
+      const float4 v = *reinterpret_cast<const float4 *>(&s.pair[at]);
+      const float2 dyv = *reinterpret_cast<const float2 *>(&s.dy[at]);
+      const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
+      const float4 C = *reinterpret_cast<const float4 *>(&s.c[i * NP + P.nl * 4]);
+      const float dt[2] = {v.x, v.z}, dx[2] = {v.y, v.w}, dy[2] = {dyv.x, dyv.y};
+      const float Bv[4] = {B.x, B.y, B.z, B.w}, Cv[4] = {C.x, C.y, C.z, C.w};
+      const bool first = marks && i0 + i < n && s.s.mark[i0 + i] >= 0;
+      float prev[2][4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) prev[k][j] = i > 0 ? hist[i > 0 ? i - 1 : 0][k][j] : before[k][j];
+      if (first) start_state(s.s.mark[i0 + i], prev);
+      float bc[8];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float p = 0.f, cs = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          g[k][j] = fmaf(Cv[j], dy[k], g[k][j]);
+          bc[j] = k ? fmaf(dx[k], g[k][j], bc[j]) : dx[k] * g[k][j];
+          bc[4 + j] = k ? fmaf(dy[k], hist[i][k][j], bc[4 + j]) : dy[k] * hist[i][k][j];
+          p = fmaf(g[k][j], Bv[j], p);
+          g[k][j] *= ex2(dt[k] * A2[k][j]);
+          const float cr = g[k][j] * prev[k][j];
+          dA[k][j] = fmaf(dt[k], cr, dA[k][j]);
+          cs = fmaf(cr, A2[k][j], cs);
+        }
+        const int o = Y::part_at(i, P.ch[k]) + P.nl;
+        s.pp[o] = p;
+        s.pc[o] = cs;
+      }
+      const int f = channel_sums<LN>(bc, P.lane);
+      if (LN > 2 || !(P.lane & 2)) {
+#pragma unroll
+        for (int u = 0; u < LEFT; ++u)
+          s.red[P.warp][i][((f + u) >> 2) * NP + P.nl * 4 + ((f + u) & 3)] = bc[u];
+      }
+      if (first) {
+        const int seg = s.s.mark[i0 + i];
+        if (a.dh0 && seg < a.n_seq) P.write(a, a.dh0, seg, g);
+        if (i0 + i > 0)
+          end_grad(i0 + i - 1, g);
+        else
+          clear(g);
+      }
+    }
+    __syncthreads();
+    if (i0 + lt < n) {
+      float ox[M], od[M], oz[M];
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        const int o = Y::part_at(lt, lc + i);
+        const float p = sum_parts<LN>(&s.pp[o]), cs = sum_parts<LN>(&s.pc[o]) * kLn2;
+        const float x = ld1(&rx.v[i]), raw = ld1(&rd.v[i]) + bias[i], go = ld1(&rg.v[i]);
+        const float dt = a.softplus ? softplusf(raw) : raw;
+        float dy = go;
+        if (zp) {
+          const float z = ld1(&rz.v[i]), sg = sigmoidf(z);
+          dy = go * z * sg;
+          oz[i] = go * fmaf(skip[i], x, sum_parts<LN>(&s.py[o])) * dsilu(z, sg);
+        }
+        ox[i] = fmaf(dt, p, skip[i] * dy);
+        od[i] = fmaf(x, p, cs);
+        if (a.softplus) od[i] *= sigmoidf(raw);
+        if (in) {
+          sd[i] = fmaf(dy, x, sd[i]);
+          sb[i] += od[i];
+        } else {
+          ox[i] = od[i] = oz[i] = 0.f;
+        }
+      }
+      stm<VEC, E, M>(reinterpret_cast<E *>(a.dx.p) + t * a.dx.st + c, ox, nv);
+      stm<VEC, E, M>(reinterpret_cast<E *>(a.ddt.p) + t * a.ddt.st + c, od, nv);
+      if (zp) stm<VEC, E, M>(reinterpret_cast<E *>(a.dz.p) + t * a.dz.st + c, oz, nv);
+    }
+    for (int e = P.tid; e < kBT * 2 * NP; e += kThreads) {
+      const int i = e / (2 * NP), o = e % (2 * NP);
+      if (i0 + i < n)
+        w.bc[((int64_t)P.ct * a.T + t0 + i0 + i) * (2 * NP) + o] =
+            (s.red[0][i][o] + s.red[1][i][o]) + (s.red[2][i][o] + s.red[3][i][o]);
+    }
+    __syncthreads();
+  }
+  P.write(a, w.state, P.r, dA);
+  // dD and ddt_bias: over the threads that hold the same channels
+  float *part = s.pp;
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    part[lt * CH + lc + i] = sd[i];
+    part[(kBT + lt) * CH + lc + i] = sb[i];
+  }
+  __syncthreads();
+  for (int e = P.tid; e < P.nch; e += kThreads) {
+    float u = 0.f, v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBT; ++i) {
+      u += part[i * CH + e];
+      v += part[(kBT + i) * CH + e];
+    }
+    w.pd[(int64_t)P.r * a.D + P.c0 + e] = u;
+    w.pb[(int64_t)P.r * a.D + P.c0 + e] = v;
+  }
+}
+
+// out[i] = sum over n parts of in[r * size + i], for up to three arrays (blockIdx.y).
+struct PartSums {
+  const float *in[3];
+  float *out[3];
+  int64_t size[3];
+  int n;
+};
+__global__ void k_ssm_part_sums(const PartSums p) {
+  const int y = blockIdx.y;
+  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, size = p.size[y];
+  if (!p.out[y] || i >= size) return;
+  const float *q = p.in[y] + i;
+  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  int r = 0;
+  for (; r + 8 <= p.n; r += 8)
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s[u] += q[(r + u) * size];
+  for (; r < p.n; ++r) s[0] += q[r * size];
+  p.out[y][i] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+}
+
+// dB and dC: over the channel tiles of a group.
+template <typename E>
+__global__ void k_ssm_bc_sums(const float *bc, int64_t T, int G, int N, int NP, int tpg, E *dB,
+                              E *dC) {
+  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  const int64_t t = i / (G * 2 * N);
+  if (t >= T) return;
+  const int rest = (int)(i % (G * 2 * N)), grp = rest / (2 * N), m = rest % N;
+  const int kind = rest / N & 1;  // 0: dB, 1: dC
+  const float *q = bc + ((int64_t)grp * tpg * T + t) * (2 * NP) + kind * NP + m;
+  const int64_t st = T * (2 * NP);
+  float s[4] = {0, 0, 0, 0};
+  int r = 0;
+  for (; r + 4 <= tpg; r += 4)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) s[u] += q[(r + u) * st];
+  for (; r < tpg; ++r) s[0] += q[r * st];
+  st1((kind ? dC : dB) + (t * G + grp) * N + m, (s[0] + s[1]) + (s[2] + s[3]));
+}
+
+BwdWork carve(void *work, int64_t T, int32_t D, int32_t N, int32_t G) {
+  BwdWork w{};
+  w.n = (int)ceil_div64(T, kRange);
+  const int LN = lanes_for(N);
+  const int64_t ctiles = channel_tiles(D, G, LN), R = w.n < 1 ? 1 : w.n;
+  char *p = reinterpret_cast<char *>(work);
+  size_t off = 0;
+  auto take = [&](int64_t floats) {
+    float *q = reinterpret_cast<float *>(p + off);
+    off += align256((size_t)floats * 4);
+    return q;
+  };
+  w.state = take(R * D * N);
+  w.grad = take(R * D * N);
+  w.sum = take(R * D);
+  w.pd = take(R * D);
+  w.pb = take(R * D);
+  w.reset = reinterpret_cast<int *>(take(R));
+  w.bc = take(ctiles * T * 2 * 4 * LN);
+  w.bytes = off;
+  return w;
+}
+
+template <typename E, int LN, bool VEC>
+cudaError_t run_bwd(const SsmArgs &a, cudaStream_t stream) {
+  const int tpg = (int)ceil_div64(a.D / a.G, Lay<LN>::CH), ctiles = tpg * a.G;
+  const BwdWork w = carve(a.work, a.T, a.D, a.N, a.G);
+  constexpr int smem1 = (int)sizeof(Tile1<LN>), smem2 = (int)sizeof(Tile2<LN>);
+  cudaError_t e = cudaFuncSetAttribute(k_ssm_bwd<E, LN, VEC>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem2);
+  if (e != cudaSuccess) return e;
+  if (smem1 > 48 * 1024 &&
+      (e = cudaFuncSetAttribute(k_ssm_bwd_ends<E, LN, VEC>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem1)) != cudaSuccess)
+    return e;
+  const int64_t size = (int64_t)a.D * a.N;
+  if (w.n > 1) {
+    k_ssm_bwd_ends<E, LN, VEC>
+        <<<(unsigned)((int64_t)ctiles * w.n), kThreads, smem1, stream>>>(a, w, tpg);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    k_ssm_bwd_chain<<<dim3((unsigned)ceil_div64(size, 128), 2), 128, 0, stream>>>(a.A, w, a.D,
+                                                                                  a.N);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const int64_t blocks = (int64_t)ctiles * (w.n + (a.dh0 ? 1 : 0));
+  if (blocks > 0) {
+    k_ssm_bwd<E, LN, VEC><<<(unsigned)blocks, kThreads, smem2, stream>>>(a, w, tpg);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const PartSums ps{{w.state, w.pd, w.pb}, {a.dA, a.dD, a.ddt_bias}, {size, a.D, a.D}, w.n};
+  k_ssm_part_sums<<<dim3((unsigned)ceil_div64(size, 128), 3), 128, 0, stream>>>(ps);
+  if ((e = cudaGetLastError()) != cudaSuccess || a.T == 0) return e;
+  k_ssm_bc_sums<E><<<(unsigned)ceil_div64((int64_t)a.T * a.G * 2 * a.N, 256), 256, 0, stream>>>(
+      w.bc, a.T, a.G, a.N, Lay<LN>::NP, tpg, reinterpret_cast<E *>(a.dB),
+      reinterpret_cast<E *>(a.dC));
+  return cudaGetLastError();
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool rows_ok(const Mat &m, bool f32) {
+  return !m.p || (aligned16(m.p) && m.st % (f32 ? 4 : 8) == 0);
+}
+
+template <typename E>
+cudaError_t by_lanes(const SsmArgs &a, bool vec, cudaStream_t stream) {
+  switch (lanes_for(a.N)) {
+    case 2: return vec ? run_bwd<E, 2, true>(a, stream) : run_bwd<E, 2, false>(a, stream);
+    case 4: return vec ? run_bwd<E, 4, true>(a, stream) : run_bwd<E, 4, false>(a, stream);
+    case 8: return vec ? run_bwd<E, 8, true>(a, stream) : run_bwd<E, 8, false>(a, stream);
+    default: return vec ? run_bwd<E, 16, true>(a, stream) : run_bwd<E, 16, false>(a, stream);
+  }
+}
+
+}  // namespace
+}  // namespace ssm
+
+size_t ssm_bwd_workspace(int64_t T, int32_t D, int32_t N, int32_t G) {
+  return ssm::carve(nullptr, T, D, N, G).bytes;
+}
+
+cudaError_t launch_ssm_bwd(const SsmArgs &a, cudaStream_t stream) {
+  using namespace ssm;
+  const bool vec = (a.D / a.G) % 8 == 0 && rows_ok(a.x, a.f32) && rows_ok(a.dt, a.f32) &&
+                   rows_ok(a.z, a.f32) && rows_ok(a.dout, a.f32) && rows_ok(a.dx, a.f32) &&
+                   rows_ok(a.ddt, a.f32) && rows_ok(a.dz, a.f32);
+  return a.f32 ? by_lanes<float>(a, vec, stream) : by_lanes<__nv_bfloat16>(a, vec, stream);
+}
+
+}  // namespace gdr

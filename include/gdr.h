@@ -70,8 +70,10 @@ enum gdr_status {
   GDR_ERR_ALIGN = -11,    /* a base pointer or row stride is not 16-byte aligned */
   GDR_ERR_DEVICE = -12,   /* the current device is not sm_103 (GB300)            */
   GDR_ERR_SCRATCH_LIMIT = -13, /* problem too large for gdr_chunk_out_noalloc's static scratch */
-  GDR_ERR_CKPT = -14           /* checkpoint interval not a positive multiple of 64, or
+  GDR_ERR_CKPT = -14,          /* checkpoint interval not a positive multiple of 64, or
                                   checkpoint buffer of the wrong type, shape or size  */
+  GDR_ERR_OPTION = -15         /* unknown activation, norm or flag, or options that do not go
+                                  together                                            */
 };
 
 /* Execution paths of the forward. */
@@ -341,6 +343,153 @@ int gdr_chunk_out_noalloc(const gdr_tensor_t *q, const gdr_tensor_t *k,
                           const gdr_tensor_t *v_new, const gdr_tensor_t *h,
                           const gdr_tensor_t *gcum, float scale, const int32_t *cu_seqlens,
                           int32_t n_seq, gdr_tensor_t *o, cudaStream_t stream);
+
+/*
+ * ---- The operators around the delta rule in a token mixer -------------------------------
+ *
+ * Short convolution, selective state space, per-head q/k norm with rotation, and the delta
+ * rule for single tokens.  Shared conventions, beside those at the top:
+ * - Activations are bf16 or f32, all of one call in the same type; sums, states of the state
+ *   space and the delta rule, and parameter gradients are f32.
+ * - Rows may have any stride >= their extent (innermost contiguous); 16-byte aligned rows take
+ *   the fast path, others a slower one with the same results.  States are compact.
+ * - Outputs must not overlap inputs or each other.
+ * - cu_seqlens NULL with n_seq = 1 means one segment of all T tokens.
+ * - Packed calls: tokens outside every segment are not written by a forward and get zero
+ *   gradients from a backward; their values, infinities and NaN among them, reach no output.
+ * - Single-token calls work on a pool of state slots, in place.  state_indices is a DEVICE
+ *   int32 array with each row's slot, or NULL (row i uses slot i).  A slot < 0 or >= the
+ *   number of slots marks a padded row: its outputs are zero, no state is touched.  A slot
+ *   named by two rows of one call is written by both, in no fixed order.
+ * - Deterministic: no atomics on results; parameter gradients are added in a fixed order.
+ * - T, B and the channel count are at most 0x7ff00000.
+ */
+enum gdr_activation { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 };
+enum gdr_norm { GDR_NORM_RMS = 0, GDR_NORM_L2 = 1 };
+
+/*
+ * gdr_conv_fwd -- causal convolution of each channel over the tokens of its segment:
+ *   u_t = bias + sum_{k < W} weight[c, k] x_{t-W+1+k},   y = u or u sigmoid(u).
+ *   x, y    [T, C]; weight [C, W], W = 2, 3 or 4, bias [C] or NULL: f32 or bf16 (both alike)
+ *   h0      [n_seq, W - 1, C] in x's type: the inputs before each segment, oldest first, or
+ *           NULL for zeros;  ht the same shape, out or NULL: the last W - 1 inputs of each
+ *           segment, reaching into h0 where it is shorter (an empty segment: h0's rows)
+ * Errors: GDR_ERR_DIM for another W, GDR_ERR_OPTION for an unknown activation.
+ */
+int gdr_conv_fwd(const gdr_tensor_t *x, const gdr_tensor_t *weight, const gdr_tensor_t *bias,
+                 const gdr_tensor_t *h0, const int32_t *cu_seqlens, int32_t n_seq,
+                 int32_t activation, gdr_tensor_t *y, gdr_tensor_t *ht, cudaStream_t stream);
+
+/*
+ * gdr_conv_bwd -- gradients of gdr_conv_fwd (the forward is recomputed).
+ *   dy      [T, C], dL/dy;  dht [n_seq, W - 1, C], dL/dht, or NULL for zero: x's type
+ *   dx      [T, C] out, dh0 [n_seq, W - 1, C] out or NULL: x's type
+ *   dweight [C, W], dbias [C] or NULL: f32 compact out
+ *   workspace  256-byte aligned, >= gdr_conv_bwd_workspace_bytes(T, C, W) bytes
+ */
+int gdr_conv_bwd(const gdr_tensor_t *x, const gdr_tensor_t *weight, const gdr_tensor_t *bias,
+                 const gdr_tensor_t *h0, const int32_t *cu_seqlens, int32_t n_seq,
+                 int32_t activation, const gdr_tensor_t *dy, const gdr_tensor_t *dht,
+                 gdr_tensor_t *dx, gdr_tensor_t *dweight, gdr_tensor_t *dbias,
+                 gdr_tensor_t *dh0, void *workspace, size_t workspace_bytes,
+                 cudaStream_t stream);
+size_t gdr_conv_bwd_workspace_bytes(int64_t T, int32_t C, int32_t W);
+
+/*
+ * gdr_conv_step -- one token for each of B requests: y from the slot's W - 1 inputs and x,
+ * which then moves into the slot (the oldest drops out).
+ *   x, y [B, C]; state [slots, W - 1, C] compact, x's type
+ */
+int gdr_conv_step(const gdr_tensor_t *x, const gdr_tensor_t *weight, const gdr_tensor_t *bias,
+                  gdr_tensor_t *state, const int32_t *state_indices, int32_t activation,
+                  gdr_tensor_t *y, cudaStream_t stream);
+
+/*
+ * gdr_ssm_fwd -- selective state space scan, for each channel d, state n and segment:
+ *   dt = softplus(dt_raw + dt_bias) (dt_softplus = 0: dt_raw + dt_bias)
+ *   h_t = exp(dt A[d, n]) h_{t-1} + dt x B[n],   y = sum_n C[n] h_t + D[d] x,
+ *   y *= z sigmoid(z) if z is given.
+ *   x, dt, z, y  [T, Dm]; B, C [T, G, N], Dm % G == 0 (channel d reads group d / (Dm / G));
+ *   A [Dm, N], D [Dm], dt_bias [Dm]: f32 compact; z, D, dt_bias may be NULL
+ *   h0, ht  [n_seq, Dm, N] f32 compact, or NULL (ht of an empty segment: h0's, or zeros)
+ *   N = 1 .. 64
+ *   workspace  256-byte aligned, >= gdr_ssm_fwd_workspace_bytes(T, Dm, N, G) bytes (may be 0)
+ */
+int gdr_ssm_fwd(const gdr_tensor_t *x, const gdr_tensor_t *dt, const gdr_tensor_t *A,
+                const gdr_tensor_t *B, const gdr_tensor_t *C, const gdr_tensor_t *D,
+                const gdr_tensor_t *z, const gdr_tensor_t *dt_bias, int32_t dt_softplus,
+                const gdr_tensor_t *h0, const int32_t *cu_seqlens, int32_t n_seq,
+                gdr_tensor_t *y, gdr_tensor_t *ht, void *workspace, size_t workspace_bytes,
+                cudaStream_t stream);
+size_t gdr_ssm_fwd_workspace_bytes(int64_t T, int32_t Dm, int32_t N, int32_t G);
+
+/*
+ * gdr_ssm_bwd -- gradients of gdr_ssm_fwd (the forward is recomputed).
+ *   dy [T, Dm]; dht [n_seq, Dm, N] f32 or NULL
+ *   dx, ddt, dz [T, Dm] (dz iff z), dB, dC [T, G, N] compact: out, x's type
+ *   dA [Dm, N], dD [Dm] (or NULL), ddt_bias [Dm] (or NULL), dh0 [n_seq, Dm, N] (or NULL):
+ *   f32 compact out
+ *   workspace  256-byte aligned, >= gdr_ssm_bwd_workspace_bytes(T, Dm, N, G) bytes
+ */
+int gdr_ssm_bwd(const gdr_tensor_t *x, const gdr_tensor_t *dt, const gdr_tensor_t *A,
+                const gdr_tensor_t *B, const gdr_tensor_t *C, const gdr_tensor_t *D,
+                const gdr_tensor_t *z, const gdr_tensor_t *dt_bias, int32_t dt_softplus,
+                const gdr_tensor_t *h0, const int32_t *cu_seqlens, int32_t n_seq,
+                const gdr_tensor_t *dy, const gdr_tensor_t *dht, gdr_tensor_t *dx,
+                gdr_tensor_t *ddt, gdr_tensor_t *dA, gdr_tensor_t *dB, gdr_tensor_t *dC,
+                gdr_tensor_t *dD, gdr_tensor_t *dz, gdr_tensor_t *ddt_bias, gdr_tensor_t *dh0,
+                void *workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t gdr_ssm_bwd_workspace_bytes(int64_t T, int32_t Dm, int32_t N, int32_t G);
+
+/*
+ * gdr_ssm_step -- one token of gdr_ssm_fwd for each of the rows of x.
+ *   x, dt, z, y [rows, Dm]; B, C [rows, G, N]; state [slots, Dm, N] f32 compact, 16-byte
+ *   aligned, in place
+ */
+int gdr_ssm_step(const gdr_tensor_t *x, const gdr_tensor_t *dt, const gdr_tensor_t *A,
+                 const gdr_tensor_t *B, const gdr_tensor_t *C, const gdr_tensor_t *D,
+                 const gdr_tensor_t *z, const gdr_tensor_t *dt_bias, int32_t dt_softplus,
+                 gdr_tensor_t *state, const int32_t *state_indices, gdr_tensor_t *y,
+                 cudaStream_t stream);
+
+/*
+ * gdr_qk_fwd -- norm of each row (token, head) of q and k, then the position rotation:
+ *   u = x r weight,  r = (mean x^2 + eps)^-1/2 (RMS) or (sum x^2 + eps)^-1/2 (L2)
+ *   pairs (a, b) of u's first `rot` elements -> (a cos - b sin, b cos + a sin): element i with
+ *   i + rot / 2, or interleaved 2 i with 2 i + 1
+ *   q, q_out [T, Hq, d]; k, k_out [T, Hk, d]; d = 1 .. 256;  q_weight, k_weight [d] f32 or
+ *   bf16, or NULL (ones)
+ *   cos, sin  [places, rot / 2] f32 compact, rot <= d even; both NULL: no rotation
+ *   positions DEVICE int32 [T]: each token's row of the tables (clamped to them)
+ */
+int gdr_qk_fwd(const gdr_tensor_t *q, const gdr_tensor_t *k, const gdr_tensor_t *q_weight,
+               const gdr_tensor_t *k_weight, int32_t norm, float eps, const gdr_tensor_t *cos,
+               const gdr_tensor_t *sin, const int32_t *positions, int32_t interleaved,
+               gdr_tensor_t *q_out, gdr_tensor_t *k_out, cudaStream_t stream);
+
+/*
+ * gdr_qk_bwd -- gradients of gdr_qk_fwd: dq_out, dk_out -> dq, dk (activations' type) and
+ * dq_weight, dk_weight [d] f32 (or NULL).  workspace: 256-byte aligned, >=
+ * gdr_qk_bwd_workspace_bytes(T, Hq, Hk, d) bytes.
+ */
+int gdr_qk_bwd(const gdr_tensor_t *q, const gdr_tensor_t *k, const gdr_tensor_t *q_weight,
+               const gdr_tensor_t *k_weight, int32_t norm, float eps, const gdr_tensor_t *cos,
+               const gdr_tensor_t *sin, const int32_t *positions, int32_t interleaved,
+               const gdr_tensor_t *dq_out, const gdr_tensor_t *dk_out, gdr_tensor_t *dq,
+               gdr_tensor_t *dk, gdr_tensor_t *dq_weight, gdr_tensor_t *dk_weight,
+               void *workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t gdr_qk_bwd_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t d);
+
+/*
+ * gdr_delta_step -- one token of gdr_chunk_fwd's recurrence for each of B requests, states in
+ * place: S = exp(g)(I - beta k k^T) S + beta k v^T, o = scale S^T q.
+ *   q, k [B, Hk, dk] bf16; v, o [B, H, dv] bf16; g [B, H] f32; beta [B, H] bf16;
+ *   state [slots, H, dk, dv] f32 compact, 16-byte aligned; dk = dv in {64, 128}
+ */
+int gdr_delta_step(const gdr_tensor_t *q, const gdr_tensor_t *k, const gdr_tensor_t *v,
+                   const gdr_tensor_t *g, const gdr_tensor_t *beta, float scale,
+                   gdr_tensor_t *state, const int32_t *state_indices, gdr_tensor_t *o,
+                   cudaStream_t stream);
 
 /* Human-readable text for a gdr_status code (static storage). */
 const char *gdr_status_string(int status);
