@@ -83,6 +83,8 @@ _lib = None
 def lib():
     """Load libgdr.so (raises if it has not been built: there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

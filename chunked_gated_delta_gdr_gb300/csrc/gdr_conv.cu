@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kTile = 16;  // tokens between two looks at the segment bounds
+constexpr int kFwdCtas = 3;  // blocks on each SM of the forward: all of them run at once
 
 // Marks of one tile, written by warp 0 one tile ahead.
 struct Marks {
@@ -99,8 +100,17 @@ __device__ void empty_rows(const ConvArgs &a, int rows, const void *src, void *d
   });
 }
 
+template <typename E>
+__device__ __forceinline__ Raw8<E> activated(float (&v)[8], int silu) {
+  if (silu) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= sigmoidf(v[e]);
+  }
+  return pack8(v, E{});
+}
+
 template <typename E, int W, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kFwdCtas)
     k_conv_fwd(const ConvArgs a, int range, int cblocks, int nranges) {
   __shared__ Marks m;
   constexpr int U = sizeof(E) == 2 ? 8 : 4;  // tokens loaded ahead
@@ -113,18 +123,19 @@ __global__ void __launch_bounds__(kThreads)
   const int t0 = r * range, t1 = min(a.T, t0 + range);
   const Rows<E, W, VEC> rows{reinterpret_cast<const E *>(a.x.p), a.x.st,
                              reinterpret_cast<const E *>(a.h0), a.C, c0, nv};
-  E *y = reinterpret_cast<E *>(a.y.p);
+  E *y = reinterpret_cast<E *>(a.y.p) + c0;
   E *ht = reinterpret_cast<E *>(a.ht);
-  Raw8<E> cur[U], nxt[U];
+  // ring[u] is token tb + u0 + u; its place is taken by the token U later as soon as it is used
+  Raw8<E> ring[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) cur[u] = t0 + u < t1 ? rows.load(t0 + u) : zero8<E>();
+  for (int u = 0; u < U; ++u) ring[u] = t0 + u < t1 ? rows.load(t0 + u) : zero8<E>();
   float w[W][8], bias[8], win[W - 1][8];
   load_taps<W>(a, c0, nv, w, bias);
-  SegCursor cur_seg = seg_find(a.cu, a.n_seq, a.T, t0, m.red);
-  int seg = cur_seg.j - 1;
+  SegCursor cursor = seg_find(a.cu, a.n_seq, a.T, t0, m.red);
+  int seg = cursor.j - 1;
   if (threadIdx.x < 32) {
-    const int start = cur_seg.b;
-    const bool any = seg_marks(a.cu, a.n_seq, a.T, t0, min(kTile, t1 - t0), m.mark[0], cur_seg);
+    const int start = cursor.b;
+    const bool any = seg_marks(a.cu, a.n_seq, a.T, t0, min(kTile, t1 - t0), m.mark[0], cursor);
     if (threadIdx.x == 0) {
       m.any[0] = any;
       m.start = start;
@@ -143,35 +154,45 @@ __global__ void __launch_bounds__(kThreads)
   for (int tb = t0; tb < t1; tb += kTile, buf ^= 1) {
     if (threadIdx.x < 32 && tb + kTile < t1) {
       const bool any = seg_marks(a.cu, a.n_seq, a.T, tb + kTile, min(kTile, t1 - tb - kTile),
-                                 m.mark[buf ^ 1], cur_seg);
+                                 m.mark[buf ^ 1], cursor);
       if (threadIdx.x == 0) m.any[buf ^ 1] = any;
     }
     const bool any = m.any[buf];
     const int *mark = m.mark[buf];
 #pragma unroll 1
     for (int u0 = 0; u0 < kTile; u0 += U) {
+      const int tu = tb + u0;
+      if (!any && tu + U <= t1 && seg >= 0 && seg < a.n_seq) {
+        // inside one segment: no bounds to look at, the window moves by renaming
+        const E *next = rows.x + (int64_t)(tu + U) * a.x.st + c0;
+        E *to = y + (int64_t)tu * a.y.st;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + u0 + U + u;
-        nxt[u] = t < t1 ? rows.load(t) : zero8<E>();
+        for (int u = 0; u < U; ++u) {
+          float x[8], v[8];
+          unpack8(ring[u], x);
+          if (tu + U + u < t1) ring[u] = ld8<VEC>(next, nv);
+          next += a.x.st;
+          taps<W>(w, bias, win, x, v);
+          st8<VEC>(to, activated<E>(v, a.silu), nv);
+          to += a.y.st;
+          shift<W>(win, x);
+        }
+        continue;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = u0 + u, t = tb + i;
         if (t < t1) {
+          float x[8], v[8];
+          unpack8(ring[u], x);
+          if (t + U < t1) ring[u] = rows.load(t + U);
           if (any && mark[i] >= 0) {
             seg = mark[i];
             if (seg < a.n_seq) rows.fill(win, seg, t, 0);
           }
           if (seg >= 0 && seg < a.n_seq) {
-            float x[8], v[8];
-            unpack8(cur[u], x);
             taps<W>(w, bias, win, x, v);
-            if (a.silu) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = __fdividef(v[e], 1.f + ex2(-v[e] * kLog2e));
-            }
-            st8<VEC>(y + (int64_t)t * a.y.st + c0, pack8(v, E{}), nv);
+            st8<VEC>(y + (int64_t)t * a.y.st, activated<E>(v, a.silu), nv);
             shift<W>(win, x);
             if (any && ht && mark[i + 1] >= 0) {
 #pragma unroll
@@ -181,8 +202,6 @@ __global__ void __launch_bounds__(kThreads)
           }
         }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) cur[u] = nxt[u];
     }
     __syncthreads();
   }
@@ -384,11 +403,7 @@ __global__ void __launch_bounds__(kThreads) k_conv_step(const ConvStepArgs a, in
   for (int k = 0; k < W - 1; ++k) unpack8(old[k], win[k]);
   unpack8(rx, x);
   taps<W>(w, bias, win, x, v);
-  if (a.silu) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __fdividef(v[e], 1.f + ex2(-v[e] * kLog2e));
-  }
-  st8<VEC>(y, pack8(v, E{}), nv);
+  st8<VEC>(y, activated<E>(v, a.silu), nv);
 #pragma unroll
   for (int k = 0; k + 1 < W - 1; ++k) st8<VEC>(s + (int64_t)k * a.C, old[k + 1], nv);
   st8<VEC>(s + (int64_t)(W - 2) * a.C, rx, nv);
@@ -415,7 +430,7 @@ int range_of(int64_t T, int n) {
 template <typename E, int W, bool VEC>
 cudaError_t run_fwd(const ConvArgs &a, cudaStream_t stream) {
   const int cblocks = (int)ceil_div64(a.C, kThreads * 8);
-  const int range = range_of(a.T, conv_ranges(a.T, a.C, 8));
+  const int range = range_of(a.T, conv_ranges(a.T, a.C, kFwdCtas));
   const int nranges = (int)ceil_div64(a.T, range);
   const int64_t blocks = (int64_t)cblocks * (nranges + (a.ht ? 1 : 0));
   if (blocks == 0) return cudaSuccess;

@@ -53,13 +53,17 @@ inline bool compact(const Desc &d) {
 }
 
 inline int device_ok() {
+  static bool fits[64] = {false};  // devices found to be sm_103: a device does not change
   int dev = 0, major = 0, minor = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GDR_ERR_CUDA;
+  if (dev >= 0 && dev < 64 && fits[dev]) return GDR_OK;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
     return GDR_ERR_CUDA;
   if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
     return GDR_ERR_CUDA;
-  return (major == 10 && minor == 3) ? GDR_OK : GDR_ERR_DEVICE;
+  if (major != 10 || minor != 3) return GDR_ERR_DEVICE;
+  if (dev >= 0 && dev < 64) fits[dev] = true;
+  return GDR_OK;
 }
 
 }  // namespace gdr

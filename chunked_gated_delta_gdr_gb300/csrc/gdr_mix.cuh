@@ -150,15 +150,27 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 1 / (1 + e^-x): 2^(-x log2 e) overflows to inf for very negative x, whose reciprocal is 0
-__device__ __forceinline__ float sigmoidf(float x) {
-  return __fdividef(1.f, 1.f + ex2(-x * kLog2e));
+// 1 / x on the special-function unit (1 ulp; subnormal results flushed to zero)
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+// 1 / (1 + e^-x): 2^(-x log2 e) overflows to inf for very negative x, whose reciprocal is 0
+__device__ __forceinline__ float sigmoidf(float x) { return rcp(1.f + ex2(-x * kLog2e)); }
 // d/dx of x sigmoid(x), from s = sigmoid(x)
 __device__ __forceinline__ float dsilu(float x, float s) { return s * (1.f + x * (1.f - s)); }
-// log(1 + e^x), accurate for every x
+// log(1 + e^x) = max(x, 0) + log(1 + t), t = e^-|x|, and log(1 + t) = 2 atanh(s), s = t / (2 + t)
+// <= 1/3, accurate relative to itself for small t too: 2 atanh(s) / s as a polynomial in s^2,
+// interpolated at the Chebyshev points of [0, 1/9] (4e-9 off at most).
 __device__ __forceinline__ float softplusf(float x) {
-  return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
+  const float t = ex2(-fabsf(x) * kLog2e), s = t * rcp(2.f + t), q = s * s;
+  float p = 0.28157778f;
+  p = fmaf(p, q, 0.27965158f);
+  p = fmaf(p, q, 0.40024595f);
+  p = fmaf(p, q, 0.66666322f);
+  p = fmaf(p, q, 2.f);
+  return fmaf(p, s, fmaxf(x, 0.f));
 }
 
 // A parameter vector in fp32 or bf16.

@@ -19,54 +19,75 @@ namespace mix {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kCtas = 4;  // blocks on each SM; each runs over many tokens
 
 __device__ __forceinline__ int place_of(const QkArgs &a, int64_t t) {
   return min(max(a.pos[t], 0), a.places - 1);
 }
 
-template <int LR>
-__device__ __forceinline__ float row_sum(float v) {
+// Sums four values of each lane over the LR lanes of a group: every lane gets all four.  A
+// transposing butterfly: two exchanges leave a lane with one of the four sums, the rest of the
+// butterfly completes it.  f is applied to the four sums, once a lane.
+template <int LR, typename F>
+__device__ __forceinline__ void four_sums(float (&v)[4], int gl, F f) {
+  const bool hi = gl & (LR / 2), lo = gl & (LR / 4);
+  const float a0 = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], LR / 2);
+  const float a1 = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], LR / 2);
+  float b = (lo ? a1 : a0) + __shfl_xor_sync(0xffffffffu, lo ? a0 : a1, LR / 4);
 #pragma unroll
-  for (int o = LR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = LR / 8; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
+  b = f(b, (hi ? 2 : 0) + (lo ? 1 : 0));
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    v[k] = __shfl_sync(0xffffffffu, b, (k >> 1) * (LR / 2) + (k & 1) * (LR / 4), LR);
 }
 
-// Cosines and sines of a lane's 8 elements (interleaved pairs: the first 4).
+// Cosines and sines of a lane's 8 elements, the sine with its sign for the forward rotation
+// (u_e cos + u_partner sin); all 8 elements are in the rotated part or none.
+struct Angles {
+  float c[8], s[8];
+};
 template <bool INTER>
-__device__ __forceinline__ void angles(const QkArgs &a, int64_t t, int e0, float (&c)[8],
-                                       float (&s)[8]) {
-  const int half = a.rot >> 1;
-  const int64_t base = (int64_t)place_of(a, t) * half;
+__device__ __forceinline__ void load_angles(const QkArgs &a, int64_t t, int e0, float4 (&c)[2],
+                                            float4 (&s)[2]) {
+  const int half = a.rot >> 1, at = INTER ? e0 >> 1 : (e0 < half ? e0 : e0 - half);
+  const int64_t base = (int64_t)place_of(a, t) * half + at;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int at = INTER ? (e0 >> 1) + i : (e0 + i < half ? e0 + i : e0 + i - half);
-    const bool ok = INTER ? (i < 4 && e0 + 2 * i < a.rot) : e0 + i < a.rot;
-    c[i] = ok ? a.cos[base + at] : 1.f;
-    s[i] = ok ? a.sin[base + at] : 0.f;
+  for (int i = 0; i < (INTER ? 1 : 2); ++i) {
+    c[i] = reinterpret_cast<const float4 *>(a.cos + base)[i];
+    s[i] = reinterpret_cast<const float4 *>(a.sin + base)[i];
   }
 }
+template <bool INTER>
+__device__ __forceinline__ Angles signed_angles(const float4 (&c)[2], const float4 (&s)[2],
+                                                bool lower) {
+  Angles r;
+  const float cc[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
+  const float ss[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    r.c[i] = cc[INTER ? i >> 1 : i];
+    const float v = ss[INTER ? i >> 1 : i];
+    r.s[i] = (INTER ? (i & 1) == 0 : lower) ? -v : v;
+  }
+  return r;
+}
 
-// The rotation (back: its transpose) of a row spread over the lanes.
-template <int LR, bool INTER>
-__device__ __forceinline__ void rotate(float (&u)[8], const float (&c)[8], const float (&s)[8],
-                                       int gl, int rot, bool back) {
+// The partners of a lane's 8 elements.
+template <typename E, int LR, bool INTER>
+__device__ __forceinline__ void partners(const Raw8<E> &own, int other, float (&v)[8]) {
   if (INTER) {
+    float u[8];
+    unpack8(own, u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float p = u[2 * i], q = u[2 * i + 1], n = back ? -s[i] : s[i];
-      u[2 * i] = p * c[i] - q * n;
-      u[2 * i + 1] = q * c[i] + p * n;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = u[i ^ 1];
   } else {
-    const int ro = rot >> 4;  // lanes of half the rotated part
-    const bool lower = gl < ro;
-    const int other = gl < 2 * ro ? (lower ? gl + ro : gl - ro) : gl;
+    Raw8<E> r = own;
+    uint32_t *w = reinterpret_cast<uint32_t *>(&r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = __shfl_sync(0xffffffffu, u[i], other, LR);
-      const float n = lower != back ? -s[i] : s[i];
-      u[i] = fmaf(v, n, u[i] * c[i]);
-    }
+    for (int i = 0; i < (int)(sizeof(r) / 4); ++i)
+      w[i] = __shfl_sync(0xffffffffu, w[i], other, LR);
+    unpack8(r, v);
   }
 }
 
@@ -75,87 +96,175 @@ struct Groups {
   int tp;  // tokens of a block
 };
 
+// A block runs over tokens tb, tb + gridDim.x, ...; for each, over batches of the heads of q, then
+// of k: U rows a lane group, the next batch's rows (and the next token's angles) on their way.
+// The weights' products with the angles are formed once a token:
+//   y_e = r (x_e (w_e cos_e) + x_partner (w_partner sin_e)).
 template <typename E, int LR, bool INTER, bool BWD>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas)
     k_qk(const QkArgs a, const Groups gr, int64_t token_blocks) {
   constexpr int RP = kThreads / LR;
-  constexpr int U = BWD ? 2 : 4;  // rows in flight
+  constexpr int U = BWD ? 2 : 4;
+  __shared__ __align__(16) float ws[2][LR * 8];
   const int grp = threadIdx.x / LR, gl = threadIdx.x % LR, e0 = gl * 8;
-  const int heads = a.Hq + a.Hk;
+  const int first = grp % gr.hp;
+  const bool rotated = a.rot > 0, turned = e0 < a.rot, lower = e0 < (a.rot >> 1);
+  const int ro = a.rot >> 4;  // lanes of half the rotated part
+  const int other = INTER || !turned ? gl : (lower ? gl + ro : gl - ro);
   const float inv = a.rms ? 1.f / (float)a.d : 1.f;
-  float w[2][8], dw[2][8];
+  for (int i = threadIdx.x; i < 2 * LR * 8; i += kThreads) {
+    const mix::Param &w = i < LR * 8 ? a.w[0] : a.w[1];
+    ws[i / (LR * 8)][i % (LR * 8)] = w.p ? ldp(w, i % (LR * 8)) : 1.f;
+  }
+  float dw[2][8];
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+  for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
+  __syncthreads();
+
+  auto token = [&](int64_t tb) { return tb * gr.tp + grp / gr.hp; };
+  auto alive = [&](int64_t tb) {
+    return tb < token_blocks && grp < gr.hp * gr.tp && token(tb) < a.T;
+  };
+  Raw8<E> rx[U], rd[U];
+  auto fetch = [&](int64_t tb, int j, int h0) {
+    const int heads = j ? a.Hk : a.Hq;
+    const int64_t t = token(tb);
+    const int n = alive(tb) ? 8 : 0;
+    const E *p = reinterpret_cast<const E *>(a.x[j]) + t * a.x_st[j] + (h0 + first) * a.x_sh[j] + e0;
+    const int64_t step = gr.hp * a.x_sh[j];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[j][i] = a.w[j].p ? ldp(a.w[j], e0 + i) : 1.f;
-      dw[j][i] = 0.f;
+    for (int u = 0; u < U; ++u) {
+      rx[u] = ld8<true>(p, h0 + u * gr.hp + first < heads ? n : 0);
+      p += step;
     }
+    if (BWD) {
+      p = reinterpret_cast<const E *>(a.y[j]) + t * a.y_st[j] + (h0 + first) * a.y_sh[j] + e0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        rd[u] = ld8<true>(p, h0 + u * gr.hp + first < heads ? n : 0);
+        p += gr.hp * a.y_sh[j];
+      }
+    }
+  };
+  float4 ca[2], sa[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    ca[i] = make_float4(1.f, 1.f, 1.f, 1.f);
+    sa[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  if (turned && alive(blockIdx.x)) load_angles<INTER>(a, token(blockIdx.x), e0, ca, sa);
+  int j = a.Hq > 0 ? 0 : 1, h0 = 0;
+  fetch(blockIdx.x, j, 0);
   for (int64_t tb = blockIdx.x; tb < token_blocks; tb += gridDim.x) {
-    const int64_t t = tb * gr.tp + grp / gr.hp;
-    const bool live = grp < gr.hp * gr.tp && t < a.T;
-    float c[8], s[8];
-    if (a.rot > 0 && live) {
-      angles<INTER>(a, t, e0, c, s);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = 1.f;
-        s[i] = 0.f;
-      }
-    }
-    // the loop runs the same number of times in every lane: shuffles inside
-    const int first = grp % gr.hp;
-    for (int h0 = 0; h0 < heads; h0 += gr.hp * U) {
-      Raw8<E> rx[U], rd[U];
+    const int64_t t = token(tb);
+    const bool live = alive(tb);
+    const Angles ang = signed_angles<INTER>(ca, sa, lower);
+    if (turned && alive(tb + gridDim.x)) load_angles<INTER>(a, token(tb + gridDim.x), e0, ca, sa);
+    float cw[8], sw[8];
+    int formed = -1;  // the tensor that cw, sw are of
+    for (bool last = false; !last;) {
+      const int jj = j, hh = h0, heads = jj ? a.Hk : a.Hq;
+      Raw8<E> cx[U], cd[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * gr.hp + first;
-        const bool ok = live && h < heads;
-        const int j = h < a.Hq ? 0 : 1, hj = j ? h - a.Hq : h;
-        rx[u] = ld8<true>(reinterpret_cast<const E *>(a.x[j]) + t * a.x_st[j] + hj * a.x_sh[j] + e0,
-                          ok ? 8 : 0);
-        if (BWD)
-          rd[u] = ld8<true>(
-              reinterpret_cast<const E *>(a.y[j]) + t * a.y_st[j] + hj * a.y_sh[j] + e0, ok ? 8 : 0);
+        cx[u] = rx[u];
+        if (BWD) cd[u] = rd[u];
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (h0 + u * gr.hp >= heads) break;  // no lane group has a row left
-        const int h = h0 + u * gr.hp + first;
-        const bool ok = live && h < heads;
-        const int j = h < a.Hq ? 0 : 1, hj = j ? h - a.Hq : h;
-        float x[8], v[8], q = 0.f;
-        unpack8(rx[u], x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q = fmaf(x[i], x[i], q);
-        q = row_sum<LR>(q);
-        const float r = ok ? rsqrtf(fmaf(q, inv, a.eps)) : 0.f;  // eps may be 0
-        if (!BWD) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = x[i] * r * (j ? w[1][i] : w[0][i]);
-          if (a.rot > 0) rotate<LR, INTER>(v, c, s, gl, a.rot, false);
-          st8<true>(reinterpret_cast<E *>(a.y[j]) + t * a.y_st[j] + hj * a.y_sh[j] + e0,
-                    pack8(v, E{}), ok ? 8 : 0);
+      h0 += gr.hp * U;
+      if (h0 >= heads) {
+        h0 = 0;
+        if (jj == 0 && a.Hk > 0) {
+          j = 1;
         } else {
-          unpack8(rd[u], v);
-          if (a.rot > 0) rotate<LR, INTER>(v, c, s, gl, a.rot, true);
-          float dot = 0.f;
+          j = a.Hq > 0 ? 0 : 1;
+          last = true;
+        }
+      }
+      fetch(last ? tb + gridDim.x : tb, j, h0);
+      if (formed != jj) {
+        formed = jj;
+        float w[8], wp[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const float4 u = *reinterpret_cast<const float4 *>(&ws[jj][e0 + i]);
+          const float4 v = *reinterpret_cast<const float4 *>(&ws[jj][other * 8 + i]);
+          w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
+          wp[i] = v.x; wp[i + 1] = v.y; wp[i + 2] = v.z; wp[i + 3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          cw[i] = BWD ? w[i] : w[i] * ang.c[i];
+          sw[i] = (INTER ? w[i ^ 1] : wp[i]) * ang.s[i];
+        }
+      }
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (!BWD) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float x[8];
+          unpack8(cx[u], x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[u] = fmaf(x[i], x[i], v[u]);
+        }
+        four_sums<LR>(v, gl, [&](float q, int) { return rsqrtf(fmaf(q, inv, a.eps)); });
+        E *p = reinterpret_cast<E *>(a.y[jj]) + t * a.y_st[jj] + (hh + first) * a.y_sh[jj] + e0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (hh + u * gr.hp >= heads) break;  // no lane group has a row left
+          float x[8], o[8];
+          unpack8(cx[u], x);
+          if (rotated) {
+            partners<E, LR, INTER>(cx[u], other, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = fmaf(x[i], cw[i], o[i] * sw[i]) * v[u];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = x[i] * cw[i] * v[u];
+          }
+          st8<true>(p, pack8(o, E{}), live && hh + u * gr.hp + first < heads ? 8 : 0);
+          p += gr.hp * a.y_sh[jj];
+        }
+      } else {
+        float e[U][8];  // the rotation undone
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float x[8];
+          unpack8(cx[u], x);
+          unpack8(cd[u], e[u]);
+          if (rotated) {
+            float o[8];
+            partners<E, LR, INTER>(cd[u], other, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[u][i] = fmaf(e[u][i], ang.c[i], -o[i] * ang.s[i]);
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float g = v[i] * x[i] * r;  // rows past the end are zero
-            if (j)
-              dw[1][i] += g;
-            else
-              dw[0][i] += g;
-            v[i] *= j ? w[1][i] : w[0][i];
-            dot = fmaf(v[i], x[i], dot);
+            v[u] = fmaf(x[i], x[i], v[u]);
+            v[2 + u] = fmaf(e[u][i] * cw[i], x[i], v[2 + u]);
           }
-          dot = row_sum<LR>(dot) * inv * r * r * r;
+        }
+        four_sums<LR>(v, gl, [&](float q, int k) {
+          return k < 2 ? rsqrtf(fmaf(q, inv, a.eps)) : q * inv;
+        });
+        E *p = reinterpret_cast<E *>(a.dx[jj]) + t * a.dx_st[jj] + (hh + first) * a.dx_sh[jj] + e0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], r, -x[i] * dot);
-          st8<true>(reinterpret_cast<E *>(a.dx[j]) + t * a.dx_st[j] + hj * a.dx_sh[j] + e0,
-                    pack8(v, E{}), ok ? 8 : 0);
+        for (int u = 0; u < U; ++u) {
+          if (hh + u * gr.hp >= heads) break;
+          const bool ok = live && hh + u * gr.hp + first < heads;
+          const float r = ok ? v[u] : 0.f, d = v[2 + u] * r * r * r;  // eps may be 0
+          float x[8], o[8];
+          unpack8(cx[u], x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float g = e[u][i] * x[i];  // rows past the end are zero
+            if (jj)
+              dw[1][i] = fmaf(g, r, dw[1][i]);
+            else
+              dw[0][i] = fmaf(g, r, dw[0][i]);
+            o[i] = fmaf(e[u][i] * cw[i], r, -x[i] * d);
+          }
+          st8<true>(p, pack8(o, E{}), ok ? 8 : 0);
+          p += gr.hp * a.dx_sh[jj];
         }
       }
     }
@@ -294,7 +403,8 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 bool fast_rows(const QkArgs &a, bool bwd) {
   const int g = a.f32 ? 4 : 8;
   const bool pow2 = a.d == 64 || a.d == 128 || a.d == 256;
-  if (!pow2 || (!a.interleaved && a.rot % 16 != 0)) return false;
+  if (!pow2 || a.rot % (a.interleaved ? 8 : 16) != 0) return false;
+  if (!aligned16(a.cos) || !aligned16(a.sin)) return false;
   for (int j = 0; j < 2; ++j) {
     if (!aligned16(a.x[j]) || a.x_st[j] % g || a.x_sh[j] % g) return false;
     if (!aligned16(a.y[j]) || a.y_st[j] % g || a.y_sh[j] % g) return false;
@@ -310,17 +420,14 @@ Groups groups_for(const QkArgs &a) {
   return Groups{hp, rp / hp};
 }
 
-constexpr int kBwdCtas = 6;  // blocks on each SM of the backward, which keeps dw in registers
-
-int64_t bwd_blocks() { return (int64_t)sm_count() * kBwdCtas; }
+int64_t most_blocks() { return (int64_t)sm_count() * kCtas; }
 
 template <typename E, int LR, bool BWD>
 cudaError_t run_fast(const QkArgs &a, cudaStream_t stream, int *blocks_out) {
   const Groups gr = groups_for(a);
   const int64_t tb = ceil_div64(a.T, gr.tp);
   int64_t blocks = tb;
-  if (BWD && blocks > bwd_blocks()) blocks = bwd_blocks();
-  if (blocks > 0x7fffffff) blocks = 0x7fffffff;
+  if (blocks > most_blocks()) blocks = most_blocks();
   *blocks_out = (int)blocks;
   if (a.interleaved)
     k_qk<E, LR, true, BWD><<<(unsigned)blocks, kThreads, 0, stream>>>(a, gr, tb);
@@ -340,7 +447,7 @@ cudaError_t run(const QkArgs &a, cudaStream_t stream, int *blocks) {
     return run_fast<E, 32, BWD>(a, stream, blocks);
   }
   int64_t n = ceil_div64(rows, kThreads / 32);
-  if (n > bwd_blocks()) n = bwd_blocks();
+  if (n > most_blocks()) n = most_blocks();
   *blocks = (int)n;
   k_qk_any<E, BWD><<<(unsigned)n, kThreads, 0, stream>>>(a, rows);
   return cudaGetLastError();
@@ -356,7 +463,7 @@ cudaError_t launch_qk_fwd(const QkArgs &a, cudaStream_t stream) {
 }
 
 size_t qk_bwd_workspace(int64_t, int32_t, int32_t, int32_t d) {
-  return align256((size_t)mix::bwd_blocks() * 2 * d * sizeof(float));
+  return align256((size_t)mix::most_blocks() * 2 * d * sizeof(float));
 }
 
 cudaError_t launch_qk_bwd(const QkArgs &a, cudaStream_t stream) {

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           v[i] = fmaf(skip[i], x[i], sum_parts<LN>(&s.part[Y::part_at(lt, lc + i)]));
-          if (zp) v[i] *= __fdividef(z[i], 1.f + ex2(-z[i] * kLog2e));
+          if (zp) v[i] *= z[i] * sigmoidf(z[i]);
         }
         st8<VEC>(yp + (int64_t)(tb + lt) * a.y.st, pack8(v, E{}), nv);
       }
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads)
     if (a.Dskip) part = fmaf(a.Dskip[d], x, part);
     if (a.z.p) {
       const float z = ld1(reinterpret_cast<const E *>(a.z.p) + (int64_t)row * a.z.st + d);
-      part *= __fdividef(z, 1.f + ex2(-z * kLog2e));
+      part *= z * sigmoidf(z);
     }
     st1(y, part);
   }

@@ -8,7 +8,9 @@ to as well).  Device tensors only.  Layouts and formulas are those of include/gd
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
+import threading
 from typing import Optional, Tuple
 
 import torch
@@ -19,47 +21,82 @@ _DT = {torch.bfloat16: nat.GDR_BF16, torch.float32: nat.GDR_F32}
 _ACT = {None: 0, "none": 0, "silu": 1}
 _NORM = {"rms": 0, "l2": 1}
 
+# Calls of one token cost a few microseconds on the GPU, so the marshalling is kept short: the
+# stream's handle comes without a Stream object, and descriptors are packed into one buffer for
+# each thread (the library reads them during the call only).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
 # a gdr_tensor_t (56 bytes: address, type, rank, extents, strides' address), then its strides
-_DESC = [struct.Struct("@Qii%dq%dxQ%dq" % (n, 8 * (4 - n), n)) for n in range(5)]
-_SIZE = 96
+_COMPACT = [struct.Struct("@Qii%dq%dxQ" % (n, 8 * (4 - n))) for n in range(5)]
+_STRIDED = [struct.Struct("@Qii%dq%dxQ%dq" % (n, 8 * (4 - n), n)) for n in range(5)]
+_SIZE, _MOST = 96, 24
 
 
-class _Descs:
-    """Descriptors of a call's tensors in one buffer; ``self[i]`` is the i-th one's address
-    (None for a tensor that is None).  All tensors must be on one CUDA device."""
+class _Buffer(threading.local):
+    def __init__(self):
+        self.buf = (ctypes.c_char * (_SIZE * _MOST))()
+        self.base = ctypes.addressof(self.buf)
 
-    def __init__(self, tensors):
-        self.buf = buf = bytearray(_SIZE * len(tensors))
-        self.keep = (ctypes.c_char * len(buf)).from_buffer(buf)
-        base = ctypes.addressof(self.keep)
-        self.at = at = []
-        index = None
-        off = 0
-        for t in tensors:
-            if t is None:
-                at.append(None)
-            else:
-                if not t.is_cuda:
-                    raise ValueError("tensors must be on a CUDA device")
-                if index is None:
-                    index = t.get_device()
-                elif t.get_device() != index:
-                    raise ValueError("tensors must be on one device")
-                code = _DT.get(t.dtype)
-                if code is None:
-                    raise TypeError(f"unsupported dtype {t.dtype}")
-                shape = t.shape
-                n = len(shape)
-                if n < 1 or n > 4:
-                    raise ValueError("tensors must have 1..4 dims")
-                _DESC[n].pack_into(buf, off, t.data_ptr(), code, n, *shape, base + off + 56,
-                                   *t.stride())
-                at.append(base + off)
-            off += _SIZE
-        self.index = index
 
-    def __getitem__(self, i):
-        return self.at[i]
+_local = _Buffer()
+
+
+def _descs(index: int, *tensors):
+    """Addresses of descriptors of the tensors (None for None), valid until the thread's next
+    call.  All tensors must be on CUDA device ``index``."""
+    buf, base = _local.buf, _local.base
+    at = []
+    off = 0
+    for t in tensors:
+        if t is None:
+            at.append(None)
+            continue
+        if t.get_device() != index:
+            raise ValueError("tensors must be on one CUDA device")
+        code = _DT.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        shape = t.shape
+        n = len(shape)
+        if n < 1 or n > 4:
+            raise ValueError("tensors must have 1..4 dims")
+        if t.is_contiguous():
+            _COMPACT[n].pack_into(buf, off, t.data_ptr(), code, n, *shape, 0)
+        else:
+            _STRIDED[n].pack_into(buf, off, t.data_ptr(), code, n, *shape, base + off + 56,
+                                  *t.stride())
+        at.append(base + off)
+        off += _SIZE
+    return at
+
+
+def _device_call(f):
+    """Runs f with its first tensor's device current and, where ``stream`` is given, with that
+    stream current too, so that what the call allocates belongs to it."""
+
+    name = f.__code__.co_varnames[0]
+
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        index = (args[0] if args else kw[name]).get_device()
+        if index < 0:
+            raise ValueError("tensors must be on a CUDA device")
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return f(*args, **kw)
+        if index != _current_device():
+            with torch.cuda.device(index):
+                return f(*args, **kw)
+        return f(*args, **kw)
+
+    return call
+
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """An uninitialised compact tensor of t's shape and type."""
+    return (torch.empty_like(t) if t.is_contiguous()
+            else torch.empty(t.shape, dtype=t.dtype, device=t.device))
 
 
 def _indices(t: Optional[torch.Tensor], name: str, n: Optional[int], index: int):
@@ -70,7 +107,7 @@ def _indices(t: Optional[torch.Tensor], name: str, n: Optional[int], index: int)
         raise TypeError(f"{name} must be int32")
     if t.dim() != 1 or (n is not None and t.shape[0] != n) or not t.is_contiguous():
         raise ValueError(f"{name} must be compact, one-dimensional and of the call's length")
-    if not t.is_cuda or t.get_device() != index:
+    if t.get_device() != index:
         raise ValueError(f"{name} must be on the call's device")
     return t.data_ptr()
 
@@ -82,32 +119,6 @@ def _segments(cu: Optional[torch.Tensor], index: int):
     if cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError("cu_seqlens must hold n_seq + 1 offsets")
     return _indices(cu, "cu_seqlens", None, index), cu.shape[0] - 1
-
-
-class _On:
-    """The call's device made current, and its stream (with ``stream``: also torch's current one,
-    so that what the call allocates belongs to it)."""
-
-    __slots__ = ("dev", "ctx")
-
-    def __init__(self, t: torch.Tensor, stream):
-        self.ctx = None
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
-        if stream is not None:
-            self.ctx = torch.cuda.stream(stream)
-        elif t.get_device() != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(t.get_device())
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        return False
 
 
 def _option(table, value, name):
@@ -124,16 +135,19 @@ def _rows(t: torch.Tensor, dims: int, name: str):
     return t.shape
 
 
-def _scratch(nbytes: int, workspace: Optional[torch.Tensor], device):
+def _scratch(nbytes: int, workspace: Optional[torch.Tensor], x: torch.Tensor):
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    elif workspace.get_device() != x.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be compact and on the call's device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 # ---------------------------------------------------------------- short convolution
 
+@_device_call
 def conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
              initial_state: Optional[torch.Tensor] = None,
              cu_seqlens: Optional[torch.Tensor] = None, activation: Optional[str] = "silu",
@@ -148,22 +162,24 @@ def conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]
     int32 (None: one segment); activation "silu" or None.  Returns (y [T, C], final_state
     [N, W - 1, C] or None).
     """
-    with _On(x, stream) as st:
-        _rows(x, 2, "x")
-        _rows(weight, 2, "weight")
-        cu, n_seq = _segments(cu_seqlens, x.get_device())
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        ht = None
-        if output_final_state:
-            ht = (torch.empty(n_seq, weight.shape[1] - 1, x.shape[1], dtype=x.dtype,
-                              device=x.device) if final_state is None else final_state)
-        d = _Descs((x, weight, bias, initial_state, y, ht))
-        rc = nat.lib().gdr_conv_fwd(d[0], d[1], d[2], d[3], cu, n_seq,
-                                    _option(_ACT, activation, "activation"), d[4], d[5], st)
-        nat.check(rc, "gdr_conv_fwd")
+    index = x.get_device()
+    _rows(x, 2, "x")
+    _rows(weight, 2, "weight")
+    cu, n_seq = _segments(cu_seqlens, index)
+    y = _like(x) if out is None else out
+    ht = None
+    if output_final_state:
+        ht = (torch.empty(n_seq, weight.shape[1] - 1, x.shape[1], dtype=x.dtype,
+                          device=x.device) if final_state is None else final_state)
+    d = _descs(index, x, weight, bias, initial_state, y, ht)
+    rc = nat.lib().gdr_conv_fwd(d[0], d[1], d[2], d[3], cu, n_seq,
+                                _option(_ACT, activation, "activation"), d[4], d[5],
+                                _raw_stream(index))
+    nat.check(rc, "gdr_conv_fwd")
     return y, ht
 
 
+@_device_call
 def conv_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
              bias: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
              cu_seqlens: Optional[torch.Tensor] = None, activation: Optional[str] = "silu",
@@ -172,25 +188,26 @@ def conv_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
              stream: Optional[torch.cuda.Stream] = None):
     """Gradients of ``conv_fwd`` (libgdr ``gdr_conv_bwd``): (dx [T, C] in x's type, dweight
     [C, W] fp32, dbias [C] fp32 or None, dinitial_state [N, W - 1, C] in x's type or None)."""
-    with _On(x, stream) as st:
-        T, C = _rows(x, 2, "x")
-        W = _rows(weight, 2, "weight")[1]
-        cu, n_seq = _segments(cu_seqlens, x.get_device())
-        dev = x.device
-        dx = torch.empty(T, C, dtype=x.dtype, device=dev)
-        dw = torch.empty(C, W, dtype=torch.float32, device=dev)
-        db = torch.empty(C, dtype=torch.float32, device=dev) if bias is not None else None
-        dh0 = (torch.empty(n_seq, W - 1, C, dtype=x.dtype, device=dev) if want_dinitial else None)
-        d = _Descs((x, weight, bias, initial_state, dy, dfinal_state, dx, dw, db, dh0))
-        lib = nat.lib()
-        ws, wp, wn = _scratch(lib.gdr_conv_bwd_workspace_bytes(T, C, W), workspace, dev)
-        rc = lib.gdr_conv_bwd(d[0], d[1], d[2], d[3], cu, n_seq,
-                              _option(_ACT, activation, "activation"), d[4], d[5], d[6], d[7],
-                              d[8], d[9], wp, wn, st)
-        nat.check(rc, "gdr_conv_bwd")
+    index = x.get_device()
+    T, C = _rows(x, 2, "x")
+    W = _rows(weight, 2, "weight")[1]
+    cu, n_seq = _segments(cu_seqlens, index)
+    dev = x.device
+    dx = _like(x)
+    dw = torch.empty(C, W, dtype=torch.float32, device=dev)
+    db = torch.empty(C, dtype=torch.float32, device=dev) if bias is not None else None
+    dh0 = (torch.empty(n_seq, W - 1, C, dtype=x.dtype, device=dev) if want_dinitial else None)
+    d = _descs(index, x, weight, bias, initial_state, dy, dfinal_state, dx, dw, db, dh0)
+    lib = nat.lib()
+    ws, wp, wn = _scratch(lib.gdr_conv_bwd_workspace_bytes(T, C, W), workspace, x)
+    rc = lib.gdr_conv_bwd(d[0], d[1], d[2], d[3], cu, n_seq,
+                          _option(_ACT, activation, "activation"), d[4], d[5], d[6], d[7],
+                          d[8], d[9], wp, wn, _raw_stream(index))
+    nat.check(rc, "gdr_conv_bwd")
     return dx, dw, db, dh0
 
 
+@_device_call
 def conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor,
               bias: Optional[torch.Tensor] = None, activation: Optional[str] = "silu",
               state_indices: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
@@ -198,19 +215,21 @@ def conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor,
     """One token of ``conv_fwd`` for each row of x [B, C]: returns y [B, C] and moves x into
     state [slots, W - 1, C], in place.  state_indices [B] int32: each row's slot (None: row i,
     slot i; outside the pool: a padded row, y = 0)."""
-    with _On(x, stream) as st:
-        B, _ = _rows(x, 2, "x")
-        idx = _indices(state_indices, "state_indices", B, x.get_device())
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        d = _Descs((x, weight, bias, state, y))
-        rc = nat.lib().gdr_conv_step(d[0], d[1], d[2], d[3], idx,
-                                     _option(_ACT, activation, "activation"), d[4], st)
-        nat.check(rc, "gdr_conv_step")
+    index = x.get_device()
+    B, _ = _rows(x, 2, "x")
+    idx = _indices(state_indices, "state_indices", B, index)
+    y = _like(x) if out is None else out
+    d = _descs(index, x, weight, bias, state, y)
+    rc = nat.lib().gdr_conv_step(d[0], d[1], d[2], d[3], idx,
+                                 _option(_ACT, activation, "activation"), d[4],
+                                _raw_stream(index))
+    nat.check(rc, "gdr_conv_step")
     return y
 
 
 # ---------------------------------------------------------------- selective state space
 
+@_device_call
 def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
             C: torch.Tensor, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
             dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = True,
@@ -226,24 +245,25 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     initial_state [N_seq, Dm, N] fp32; cu_seqlens [N_seq + 1] int32 (None: one segment).
     Returns (y [T, Dm], final_state [N_seq, Dm, N] fp32 or None).
     """
-    with _On(x, stream) as st:
-        T, Dm = _rows(x, 2, "x")
-        _, G, N = _rows(B, 3, "B")
-        cu, n_seq = _segments(cu_seqlens, x.get_device())
-        y = torch.empty(T, Dm, dtype=x.dtype, device=x.device) if out is None else out
-        ht = None
-        if output_final_state:
-            ht = (torch.empty(n_seq, Dm, N, dtype=torch.float32, device=x.device)
-                  if final_state is None else final_state)
-        d = _Descs((x, dt, A, B, C, D, z, dt_bias, initial_state, y, ht))
-        lib = nat.lib()
-        ws, wp, wn = _scratch(lib.gdr_ssm_fwd_workspace_bytes(T, Dm, N, G), workspace, x.device)
-        rc = lib.gdr_ssm_fwd(d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7], int(dt_softplus),
-                             d[8], cu, n_seq, d[9], d[10], wp, wn, st)
-        nat.check(rc, "gdr_ssm_fwd")
+    index = x.get_device()
+    T, Dm = _rows(x, 2, "x")
+    _, G, N = _rows(B, 3, "B")
+    cu, n_seq = _segments(cu_seqlens, index)
+    y = _like(x) if out is None else out
+    ht = None
+    if output_final_state:
+        ht = (torch.empty(n_seq, Dm, N, dtype=torch.float32, device=x.device)
+              if final_state is None else final_state)
+    d = _descs(index, x, dt, A, B, C, D, z, dt_bias, initial_state, y, ht)
+    lib = nat.lib()
+    ws, wp, wn = _scratch(lib.gdr_ssm_fwd_workspace_bytes(T, Dm, N, G), workspace, x)
+    rc = lib.gdr_ssm_fwd(d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7], int(dt_softplus),
+                         d[8], cu, n_seq, d[9], d[10], wp, wn, _raw_stream(index))
+    nat.check(rc, "gdr_ssm_fwd")
     return y, ht
 
 
+@_device_call
 def ssm_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
             C: torch.Tensor, dy: torch.Tensor, D: Optional[torch.Tensor] = None,
             z: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
@@ -255,30 +275,30 @@ def ssm_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     """Gradients of ``ssm_fwd`` (libgdr ``gdr_ssm_bwd``): (dx, ddt [T, Dm], dA [Dm, N] fp32,
     dB, dC [T, G, N], dD [Dm] fp32 or None, dz [T, Dm] or None, ddt_bias [Dm] fp32 or None,
     dinitial_state [N_seq, Dm, N] fp32 or None); the activations' in x's type."""
-    with _On(x, stream) as st:
-        T, Dm = _rows(x, 2, "x")
-        _, G, N = _rows(B, 3, "B")
-        cu, n_seq = _segments(cu_seqlens, x.get_device())
-        act = dict(dtype=x.dtype, device=x.device)
-        f32 = dict(dtype=torch.float32, device=x.device)
-        dx, ddt = torch.empty(T, Dm, **act), torch.empty(T, Dm, **act)
-        dA = torch.empty(Dm, N, **f32)
-        dB, dC = torch.empty(T, G, N, **act), torch.empty(T, G, N, **act)
-        dD = torch.empty(Dm, **f32) if D is not None else None
-        dz = torch.empty(T, Dm, **act) if z is not None else None
-        dbias = torch.empty(Dm, **f32) if dt_bias is not None else None
-        dh0 = torch.empty(n_seq, Dm, N, **f32) if want_dinitial else None
-        d = _Descs((x, dt, A, B, C, D, z, dt_bias, initial_state, dy, dfinal_state, dx, ddt, dA,
-                    dB, dC, dD, dz, dbias, dh0))
-        lib = nat.lib()
-        ws, wp, wn = _scratch(lib.gdr_ssm_bwd_workspace_bytes(T, Dm, N, G), workspace, x.device)
-        rc = lib.gdr_ssm_bwd(d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7], int(dt_softplus),
-                             d[8], cu, n_seq, d[9], d[10], d[11], d[12], d[13], d[14], d[15],
-                             d[16], d[17], d[18], d[19], wp, wn, st)
-        nat.check(rc, "gdr_ssm_bwd")
+    index = x.get_device()
+    T, Dm = _rows(x, 2, "x")
+    _, G, N = _rows(B, 3, "B")
+    cu, n_seq = _segments(cu_seqlens, index)
+    f32 = dict(dtype=torch.float32, device=x.device)
+    dx, ddt = _like(x), _like(dt)
+    dA = torch.empty(Dm, N, **f32)
+    dB, dC = _like(B), _like(C)
+    dD = torch.empty(Dm, **f32) if D is not None else None
+    dz = _like(z) if z is not None else None
+    dbias = torch.empty(Dm, **f32) if dt_bias is not None else None
+    dh0 = torch.empty(n_seq, Dm, N, **f32) if want_dinitial else None
+    d = _descs(index, x, dt, A, B, C, D, z, dt_bias, initial_state, dy, dfinal_state, dx, ddt, dA,
+                dB, dC, dD, dz, dbias, dh0)
+    lib = nat.lib()
+    ws, wp, wn = _scratch(lib.gdr_ssm_bwd_workspace_bytes(T, Dm, N, G), workspace, x)
+    rc = lib.gdr_ssm_bwd(d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7], int(dt_softplus),
+                         d[8], cu, n_seq, d[9], d[10], d[11], d[12], d[13], d[14], d[15],
+                         d[16], d[17], d[18], d[19], wp, wn, _raw_stream(index))
+    nat.check(rc, "gdr_ssm_bwd")
     return dx, ddt, dA, dB, dC, dD, dz, dbias, dh0
 
 
+@_device_call
 def ssm_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
              C: torch.Tensor, state: torch.Tensor, D: Optional[torch.Tensor] = None,
              z: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
@@ -287,19 +307,20 @@ def ssm_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor
              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """One token of ``ssm_fwd`` for each row: x, dt, z [R, Dm], B, C [R, G, N]; state
     [slots, Dm, N] fp32 in place; state_indices as in ``conv_step``.  Returns y [R, Dm]."""
-    with _On(x, stream) as st:
-        R, _ = _rows(x, 2, "x")
-        idx = _indices(state_indices, "state_indices", R, x.get_device())
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        d = _Descs((x, dt, A, B, C, D, z, dt_bias, state, y))
-        rc = nat.lib().gdr_ssm_step(d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7],
-                                    int(dt_softplus), d[8], idx, d[9], st)
-        nat.check(rc, "gdr_ssm_step")
+    index = x.get_device()
+    R, _ = _rows(x, 2, "x")
+    idx = _indices(state_indices, "state_indices", R, index)
+    y = _like(x) if out is None else out
+    d = _descs(index, x, dt, A, B, C, D, z, dt_bias, state, y)
+    rc = nat.lib().gdr_ssm_step(d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7],
+                                int(dt_softplus), d[8], idx, d[9], _raw_stream(index))
+    nat.check(rc, "gdr_ssm_step")
     return y
 
 
 # ---------------------------------------------------------------- q/k norm with rotation
 
+@_device_call
 def qk_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
            k_weight: Optional[torch.Tensor] = None, norm: str = "rms", eps: float = 1e-6,
            cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None,
@@ -311,19 +332,19 @@ def qk_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = 
     elements by the tables' rows cos, sin [places, rot / 2] fp32 at positions [T] int32 (no
     tables: no rotation).  Pairs are element i with i + rot / 2, or interleaved 2 i with 2 i + 1.
     Returns new (q, k) (libgdr ``gdr_qk_fwd``)."""
-    with _On(q, stream) as st:
-        T = _rows(q, 3, "q")[0]
-        pos = _indices(positions, "positions", T, q.get_device())
-        if out is None:
-            out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-                   torch.empty(k.shape, dtype=k.dtype, device=k.device))
-        d = _Descs((q, k, q_weight, k_weight, cos, sin, out[0], out[1]))
-        rc = nat.lib().gdr_qk_fwd(d[0], d[1], d[2], d[3], _option(_NORM, norm, "norm"), eps, d[4],
-                                  d[5], pos, int(interleaved), d[6], d[7], st)
-        nat.check(rc, "gdr_qk_fwd")
+    index = q.get_device()
+    T = _rows(q, 3, "q")[0]
+    pos = _indices(positions, "positions", T, index)
+    if out is None:
+        out = (_like(q), _like(k))
+    d = _descs(index, q, k, q_weight, k_weight, cos, sin, out[0], out[1])
+    rc = nat.lib().gdr_qk_fwd(d[0], d[1], d[2], d[3], _option(_NORM, norm, "norm"), eps, d[4],
+                              d[5], pos, int(interleaved), d[6], d[7], _raw_stream(index))
+    nat.check(rc, "gdr_qk_fwd")
     return out
 
 
+@_device_call
 def qk_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_out: torch.Tensor,
            q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
            norm: str = "rms", eps: float = 1e-6, cos: Optional[torch.Tensor] = None,
@@ -332,27 +353,27 @@ def qk_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_out: torch
            stream: Optional[torch.cuda.Stream] = None):
     """Gradients of ``qk_fwd`` (libgdr ``gdr_qk_bwd``): (dq, dk in the activations' type,
     dq_weight, dk_weight [d] fp32 or None)."""
-    with _On(q, stream) as st:
-        T, Hq, dim = _rows(q, 3, "q")
-        Hk = _rows(k, 3, "k")[1]
-        pos = _indices(positions, "positions", T, q.get_device())
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        f32 = dict(dtype=torch.float32, device=q.device)
-        dqw = torch.empty(dim, **f32) if q_weight is not None else None
-        dkw = torch.empty(dim, **f32) if k_weight is not None else None
-        d = _Descs((q, k, q_weight, k_weight, cos, sin, dq_out, dk_out, dq, dk, dqw, dkw))
-        lib = nat.lib()
-        ws, wp, wn = _scratch(lib.gdr_qk_bwd_workspace_bytes(T, Hq, Hk, dim), workspace, q.device)
-        rc = lib.gdr_qk_bwd(d[0], d[1], d[2], d[3], _option(_NORM, norm, "norm"), eps, d[4], d[5],
-                            pos, int(interleaved), d[6], d[7], d[8], d[9], d[10], d[11], wp, wn,
-                            st)
-        nat.check(rc, "gdr_qk_bwd")
+    index = q.get_device()
+    T, Hq, dim = _rows(q, 3, "q")
+    Hk = _rows(k, 3, "k")[1]
+    pos = _indices(positions, "positions", T, index)
+    dq, dk = _like(q), _like(k)
+    f32 = dict(dtype=torch.float32, device=q.device)
+    dqw = torch.empty(dim, **f32) if q_weight is not None else None
+    dkw = torch.empty(dim, **f32) if k_weight is not None else None
+    d = _descs(index, q, k, q_weight, k_weight, cos, sin, dq_out, dk_out, dq, dk, dqw, dkw)
+    lib = nat.lib()
+    ws, wp, wn = _scratch(lib.gdr_qk_bwd_workspace_bytes(T, Hq, Hk, dim), workspace, q)
+    rc = lib.gdr_qk_bwd(d[0], d[1], d[2], d[3], _option(_NORM, norm, "norm"), eps, d[4], d[5],
+                        pos, int(interleaved), d[6], d[7], d[8], d[9], d[10], d[11], wp, wn,
+                        _raw_stream(index))
+    nat.check(rc, "gdr_qk_bwd")
     return dq, dk, dqw, dkw
 
 
 # ---------------------------------------------------------------- delta rule, single tokens
 
+@_device_call
 def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
                beta: torch.Tensor, state: torch.Tensor, scale: Optional[float] = None,
                state_indices: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
@@ -361,15 +382,15 @@ def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     ``gdr_delta_step``): q, k [B, Hk, dk], v [B, H, dv], beta [B, H] bf16, g [B, H] fp32; state
     [slots, H, dk, dv] fp32 in place (``chunk_fwd``'s final states continue here);
     state_indices as in ``conv_step``.  Returns o [B, H, dv] bf16."""
-    with _On(q, stream) as st:
-        B, _, dim = _rows(q, 3, "q")
-        idx = _indices(state_indices, "state_indices", B, q.get_device())
-        o = torch.empty(v.shape, dtype=v.dtype, device=v.device) if out is None else out
-        d = _Descs((q, k, v, g, beta, state, o))
-        rc = nat.lib().gdr_delta_step(d[0], d[1], d[2], d[3], d[4],
-                                      dim ** -0.5 if scale is None else scale, d[5], idx, d[6],
-                                      st)
-        nat.check(rc, "gdr_delta_step")
+    index = q.get_device()
+    B, _, dim = _rows(q, 3, "q")
+    idx = _indices(state_indices, "state_indices", B, index)
+    o = _like(v) if out is None else out
+    d = _descs(index, q, k, v, g, beta, state, o)
+    rc = nat.lib().gdr_delta_step(d[0], d[1], d[2], d[3], d[4],
+                                  dim ** -0.5 if scale is None else scale, d[5], idx, d[6],
+                                  _raw_stream(index))
+    nat.check(rc, "gdr_delta_step")
     return o
 
 
