@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kTile = 16;  // tokens between two looks at the segment bounds
+constexpr int kAhead = 4;    // groups of 4 tokens in a forward thread's ring (bf16; fp32 half)
 constexpr int kFwdCtas = 3;  // blocks on each SM of the forward: all of them run at once
 
 // Marks of one tile, written by warp 0 one tile ahead.
@@ -109,11 +110,60 @@ __device__ __forceinline__ Raw8<E> activated(float (&v)[8], int silu) {
   return pack8(v, E{});
 }
 
+// A thread's next rows of x on their way into shared memory: groups of G tokens, S of them in a
+// ring in which each thread reads only what it copied itself.  Without 16-byte alignment rows are
+// loaded when they are used.
+template <typename E, bool VEC>
+struct Ahead {
+  static constexpr int G = 4;
+  static constexpr int P = (int)sizeof(E) / 2;  // 16-byte parts of a row's 8 elements
+  static constexpr int S = kAhead / P;
+  static constexpr int kBytes = VEC ? S * G * P * kThreads * 16 : 0;
+  uint4 *ring;
+  const E *x;
+  int64_t st;
+  int nv, end;
+
+  __device__ __forceinline__ uint4 *at(int s, int g) const {
+    return ring + ((s * G + g) * P) * kThreads + threadIdx.x;
+  }
+  __device__ __forceinline__ void issue(int s, int t) const {
+    if (VEC) {
+      const E *p = x + (int64_t)t * st;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        if (t + g < end && nv > 0) {
+#pragma unroll
+          for (int i = 0; i < P; ++i) copy16(at(s, g) + i * kThreads, p + i * 4);
+        }
+        p += st;
+      }
+      copies_commit();
+    }
+  }
+  __device__ __forceinline__ void wait() const {
+    if (VEC) copies_wait<S - 1>();
+  }
+  __device__ __forceinline__ Raw8<E> get(int s, int g, int t) const {
+    Raw8<E> r;
+    if (VEC) {
+      uint4 *w = reinterpret_cast<uint4 *>(&r);
+#pragma unroll
+      for (int i = 0; i < P; ++i) w[i] = at(s, g)[i * kThreads];
+    } else {
+      r = ld8<VEC>(x + (int64_t)t * st, nv);
+    }
+    return r;
+  }
+};
+
 template <typename E, int W, bool VEC>
 __global__ void __launch_bounds__(kThreads, kFwdCtas)
     k_conv_fwd(const ConvArgs a, int range, int cblocks, int nranges) {
+  using R = Ahead<E, VEC>;
+  constexpr int G = R::G, S = R::S;
   __shared__ Marks m;
-  constexpr int U = sizeof(E) == 2 ? 8 : 4;  // tokens loaded ahead
+  extern __shared__ __align__(16) uint4 ring[];
   const int cb = blockIdx.x % cblocks, r = blockIdx.x / cblocks;
   const int c0 = (cb * kThreads + threadIdx.x) * 8, nv = max(0, min(8, a.C - c0));
   if (r == nranges) {
@@ -123,12 +173,11 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
   const int t0 = r * range, t1 = min(a.T, t0 + range);
   const Rows<E, W, VEC> rows{reinterpret_cast<const E *>(a.x.p), a.x.st,
                              reinterpret_cast<const E *>(a.h0), a.C, c0, nv};
+  const R in{ring, rows.x + c0, a.x.st, nv, t1};
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) in.issue(s, t0 + s * G);
   E *y = reinterpret_cast<E *>(a.y.p) + c0;
   E *ht = reinterpret_cast<E *>(a.ht);
-  // ring[u] is token tb + u0 + u; its place is taken by the token U later as soon as it is used
-  Raw8<E> ring[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) ring[u] = t0 + u < t1 ? rows.load(t0 + u) : zero8<E>();
   float w[W][8], bias[8], win[W - 1][8];
   load_taps<W>(a, c0, nv, w, bias);
   SegCursor cursor = seg_find(a.cu, a.n_seq, a.T, t0, m.red);
@@ -150,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
 #pragma unroll
       for (int i = 0; i < 8; ++i) win[k][i] = 0.f;
   }
-  int buf = 0;
+  int buf = 0, stage = 0;
   for (int tb = t0; tb < t1; tb += kTile, buf ^= 1) {
     if (threadIdx.x < 32 && tb + kTile < t1) {
       const bool any = seg_marks(a.cu, a.n_seq, a.T, tb + kTile, min(kTile, t1 - tb - kTile),
@@ -160,39 +209,35 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
     const bool any = m.any[buf];
     const int *mark = m.mark[buf];
 #pragma unroll 1
-    for (int u0 = 0; u0 < kTile; u0 += U) {
-      const int tu = tb + u0;
-      if (!any && tu + U <= t1 && seg >= 0 && seg < a.n_seq) {
+    for (int tu = tb; tu < min(tb + kTile, t1); tu += G) {
+      in.issue(stage == 0 ? S - 1 : stage - 1, tu + (S - 1) * G);
+      in.wait();
+      E *to = y + (int64_t)tu * a.y.st;
+      if (!any && tu + G <= t1 && seg >= 0 && seg < a.n_seq) {
         // inside one segment: no bounds to look at, the window moves by renaming
-        const E *next = rows.x + (int64_t)(tu + U) * a.x.st + c0;
-        E *to = y + (int64_t)tu * a.y.st;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int g = 0; g < G; ++g) {
           float x[8], v[8];
-          unpack8(ring[u], x);
-          if (tu + U + u < t1) ring[u] = ld8<VEC>(next, nv);
-          next += a.x.st;
+          unpack8(in.get(stage, g, tu + g), x);
           taps<W>(w, bias, win, x, v);
           st8<VEC>(to, activated<E>(v, a.silu), nv);
           to += a.y.st;
           shift<W>(win, x);
         }
-        continue;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = u0 + u, t = tb + i;
-        if (t < t1) {
+      } else {
+#pragma unroll 1
+        for (int g = 0; g < G; ++g) {
+          const int t = tu + g, i = t - tb;
+          if (t >= t1) break;
           float x[8], v[8];
-          unpack8(ring[u], x);
-          if (t + U < t1) ring[u] = rows.load(t + U);
+          unpack8(in.get(stage, g, t), x);
           if (any && mark[i] >= 0) {
             seg = mark[i];
             if (seg < a.n_seq) rows.fill(win, seg, t, 0);
           }
           if (seg >= 0 && seg < a.n_seq) {
             taps<W>(w, bias, win, x, v);
-            st8<VEC>(y + (int64_t)t * a.y.st, activated<E>(v, a.silu), nv);
+            st8<VEC>(to, activated<E>(v, a.silu), nv);
             shift<W>(win, x);
             if (any && ht && mark[i + 1] >= 0) {
 #pragma unroll
@@ -200,8 +245,10 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
                 st8<VEC>(ht + ((int64_t)seg * (W - 1) + k) * a.C + c0, pack8(win[k], E{}), nv);
             }
           }
+          to += a.y.st;
         }
       }
+      stage = stage + 1 == S ? 0 : stage + 1;
     }
     __syncthreads();
   }
@@ -434,7 +481,9 @@ cudaError_t run_fwd(const ConvArgs &a, cudaStream_t stream) {
   const int nranges = (int)ceil_div64(a.T, range);
   const int64_t blocks = (int64_t)cblocks * (nranges + (a.ht ? 1 : 0));
   if (blocks == 0) return cudaSuccess;
-  k_conv_fwd<E, W, VEC><<<(unsigned)blocks, kThreads, 0, stream>>>(a, range, cblocks, nranges);
+  constexpr int smem = Ahead<E, VEC>::kBytes;
+  static_assert(smem <= 46 * 1024, "more shared memory than a launch has without asking");
+  k_conv_fwd<E, W, VEC><<<(unsigned)blocks, kThreads, smem, stream>>>(a, range, cblocks, nranges);
   return cudaGetLastError();
 }
 

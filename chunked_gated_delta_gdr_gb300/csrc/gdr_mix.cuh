@@ -142,6 +142,66 @@ __device__ __forceinline__ void st8(float *p, const Raw8<float> &r, int n) {
   }
 }
 
+// Pairs of fp32 values: one instruction for two products.  They cost the fp32 pipes as much as two
+// single ones and save an issue slot: for kernels bound by instruction issue.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(f2 v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ void unpack4(const Raw8<__nv_bfloat16> &r, f2 (&f)[4]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = pair(lo_bf(w[i]), hi_bf(w[i]));
+}
+__device__ __forceinline__ void unpack4(const Raw8<float> &r, f2 (&f)[4]) {
+  float v[8];
+  unpack8(r, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = pair(v[2 * i], v[2 * i + 1]);
+}
+template <typename E>
+__device__ __forceinline__ Raw8<E> pack4(const f2 (&f)[4]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpair(f[i], v[2 * i], v[2 * i + 1]);
+  return pack8(v, E{});
+}
+
+// 16 bytes of global memory into shared memory, asynchronously (ok false: zeros instead).
+__device__ __forceinline__ void copy16(uint4 *dst, const void *src, bool ok) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  const int n = ok ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void copy16(uint4 *dst, const void *src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Until at most N of this thread's groups of copies are on their way.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ------------------------------------------------------------------ functions of one value
 
 // 2^x on the special-function unit (2 ulp; subnormal results flushed to zero)

@@ -19,33 +19,46 @@ namespace mix {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kCtas = 4;  // blocks on each SM; each runs over many tokens
+constexpr int kCtas = 4;    // blocks on each SM; each runs over many tokens
+constexpr int kStages = 4;  // batches of rows on their way or in use (bf16)
 
 __device__ __forceinline__ int place_of(const QkArgs &a, int64_t t) {
   return min(max(a.pos[t], 0), a.places - 1);
 }
 
-// Sums four values of each lane over the LR lanes of a group: every lane gets all four.  A
-// transposing butterfly: two exchanges leave a lane with one of the four sums, the rest of the
-// butterfly completes it.  f is applied to the four sums, once a lane.
-template <int LR, typename F>
-__device__ __forceinline__ void four_sums(float (&v)[4], int gl, F f) {
-  const bool hi = gl & (LR / 2), lo = gl & (LR / 4);
-  const float a0 = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], LR / 2);
-  const float a1 = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], LR / 2);
-  float b = (lo ? a1 : a0) + __shfl_xor_sync(0xffffffffu, lo ? a0 : a1, LR / 4);
+// Sums K (2 or 4) values of each lane over the LR lanes of a group: every lane gets all of them.
+// A transposing butterfly: log2 K exchanges leave a lane with one of the sums, the rest of the
+// butterfly completes it.  f is applied to the sums, once a lane.
+template <int LR, int K, typename F>
+__device__ __forceinline__ void group_sums(float (&v)[K], int gl, F f) {
+  float b;
+  int k = 0;
+  const bool hi = gl & (LR / 2);
+  if (K == 4) {
+    const bool lo = gl & (LR / 4);
+    const float a0 = (hi ? v[K - 2] : v[0]) +
+                     __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[K - 2], LR / 2);
+    const float a1 = (hi ? v[K - 1] : v[1]) +
+                     __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[K - 1], LR / 2);
+    b = (lo ? a1 : a0) + __shfl_xor_sync(0xffffffffu, lo ? a0 : a1, LR / 4);
+    k = (hi ? 2 : 0) + (lo ? 1 : 0);
+  } else {
+    b = (hi ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[1], LR / 2);
+    k = hi;
+  }
 #pragma unroll
-  for (int o = LR / 8; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
-  b = f(b, (hi ? 2 : 0) + (lo ? 1 : 0));
+  for (int o = LR / (2 * K); o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
+  b = f(b, k);
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    v[k] = __shfl_sync(0xffffffffu, b, (k >> 1) * (LR / 2) + (k & 1) * (LR / 4), LR);
+  for (int i = 0; i < K; ++i)
+    v[i] = __shfl_sync(0xffffffffu, b,
+                       K == 4 ? (i >> 1) * (LR / 2) + (i & 1) * (LR / 4) : i * (LR / 2), LR);
 }
 
 // Cosines and sines of a lane's 8 elements, the sine with its sign for the forward rotation
 // (u_e cos + u_partner sin); all 8 elements are in the rotated part or none.
 struct Angles {
-  float c[8], s[8];
+  f2 c[4], s[4];
 };
 template <bool INTER>
 __device__ __forceinline__ void load_angles(const QkArgs &a, int64_t t, int e0, float4 (&c)[2],
@@ -65,29 +78,33 @@ __device__ __forceinline__ Angles signed_angles(const float4 (&c)[2], const floa
   const float cc[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
   const float ss[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    r.c[i] = cc[INTER ? i >> 1 : i];
-    const float v = ss[INTER ? i >> 1 : i];
-    r.s[i] = (INTER ? (i & 1) == 0 : lower) ? -v : v;
+  for (int i = 0; i < 4; ++i) {
+    if (INTER) {
+      r.c[i] = pair(cc[i], cc[i]);
+      r.s[i] = pair(-ss[i], ss[i]);
+    } else {
+      r.c[i] = pair(cc[2 * i], cc[2 * i + 1]);
+      r.s[i] = lower ? pair(-ss[2 * i], -ss[2 * i + 1]) : pair(ss[2 * i], ss[2 * i + 1]);
+    }
   }
   return r;
 }
 
 // The partners of a lane's 8 elements.
 template <typename E, int LR, bool INTER>
-__device__ __forceinline__ void partners(const Raw8<E> &own, int other, float (&v)[8]) {
+__device__ __forceinline__ void partners(const Raw8<E> &own, int other, f2 (&v)[4]) {
   if (INTER) {
     float u[8];
     unpack8(own, u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = u[i ^ 1];
+    for (int i = 0; i < 4; ++i) v[i] = pair(u[2 * i + 1], u[2 * i]);
   } else {
     Raw8<E> r = own;
     uint32_t *w = reinterpret_cast<uint32_t *>(&r);
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(r) / 4); ++i)
       w[i] = __shfl_sync(0xffffffffu, w[i], other, LR);
-    unpack8(r, v);
+    unpack4(r, v);
   }
 }
 
@@ -96,174 +113,236 @@ struct Groups {
   int tp;  // tokens of a block
 };
 
-// A block runs over tokens tb, tb + gridDim.x, ...; for each, over batches of the heads of q, then
-// of k: U rows a lane group, the next batch's rows (and the next token's angles) on their way.
-// The weights' products with the angles are formed once a token:
+// Where a block is in its work: batches of the heads of q, then of k, of token tb, tb + gridDim.x
+// and so on.
+struct Batch {
+  int64_t tb;
+  int j, h0;
+  __device__ __forceinline__ void next(const QkArgs &a, int rows) {
+    h0 += rows;
+    if (h0 < (j ? a.Hk : a.Hq)) return;
+    h0 = 0;
+    if (j == 0 && a.Hk > 0) {
+      j = 1;
+    } else {
+      j = a.Hq > 0 ? 0 : 1;
+      tb += gridDim.x;
+    }
+  }
+};
+
+template <typename E, bool BWD>
+struct Ring {
+  static constexpr int U = 2;                           // rows of a lane group in a batch
+  static constexpr int P = (int)sizeof(E) / 2;          // 16-byte parts of a lane's 8 elements
+  static constexpr int S = sizeof(E) == 2 ? kStages : 2;  // batches in the ring
+  static constexpr int kSlot = U * (BWD ? 2 : 1) * P;
+  static constexpr int kBytes = S * kSlot * kThreads * 16;
+};
+
+// A block runs over batches of U rows a lane group; the next S - 1 batches are on their way into
+// a ring in shared memory in which each thread reads only what it copied itself.  The weights'
+// products with the angles are formed once a token:
 //   y_e = r (x_e (w_e cos_e) + x_partner (w_partner sin_e)).
 template <typename E, int LR, bool INTER, bool BWD>
 __global__ void __launch_bounds__(kThreads, kCtas)
     k_qk(const QkArgs a, const Groups gr, int64_t token_blocks) {
-  constexpr int RP = kThreads / LR;
-  constexpr int U = BWD ? 2 : 4;
+  using R = Ring<E, BWD>;
+  constexpr int RP = kThreads / LR, U = R::U, S = R::S;
   __shared__ __align__(16) float ws[2][LR * 8];
+  extern __shared__ __align__(16) uint4 ring[];
   const int grp = threadIdx.x / LR, gl = threadIdx.x % LR, e0 = gl * 8;
-  const int first = grp % gr.hp;
+  const int first = grp % gr.hp, rows = gr.hp * U;
   const bool rotated = a.rot > 0, turned = e0 < a.rot, lower = e0 < (a.rot >> 1);
   const int ro = a.rot >> 4;  // lanes of half the rotated part
   const int other = INTER || !turned ? gl : (lower ? gl + ro : gl - ro);
   const float inv = a.rms ? 1.f / (float)a.d : 1.f;
-  for (int i = threadIdx.x; i < 2 * LR * 8; i += kThreads) {
-    const mix::Param &w = i < LR * 8 ? a.w[0] : a.w[1];
-    ws[i / (LR * 8)][i % (LR * 8)] = w.p ? ldp(w, i % (LR * 8)) : 1.f;
-  }
-  float dw[2][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
-  __syncthreads();
-
   auto token = [&](int64_t tb) { return tb * gr.tp + grp / gr.hp; };
   auto alive = [&](int64_t tb) {
     return tb < token_blocks && grp < gr.hp * gr.tp && token(tb) < a.T;
   };
-  Raw8<E> rx[U], rd[U];
-  auto fetch = [&](int64_t tb, int j, int h0) {
-    const int heads = j ? a.Hk : a.Hq;
-    const int64_t t = token(tb);
-    const int n = alive(tb) ? 8 : 0;
-    const E *p = reinterpret_cast<const E *>(a.x[j]) + t * a.x_st[j] + (h0 + first) * a.x_sh[j] + e0;
-    const int64_t step = gr.hp * a.x_sh[j];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      rx[u] = ld8<true>(p, h0 + u * gr.hp + first < heads ? n : 0);
-      p += step;
-    }
-    if (BWD) {
-      p = reinterpret_cast<const E *>(a.y[j]) + t * a.y_st[j] + (h0 + first) * a.y_sh[j] + e0;
+  auto slot = [&](int s, int u, int q) {
+    return ring + ((s * R::kSlot + (u * (BWD ? 2 : 1) + q) * R::P) * kThreads + threadIdx.x);
+  };
+  // whether every lane group of the block has a row in each of the batch's places
+  auto whole = [&](const Batch &b) {
+    return gr.hp * gr.tp == RP && (b.tb + 1) * gr.tp <= a.T &&
+           b.h0 + rows <= (b.j ? a.Hk : a.Hq);
+  };
+  auto issue = [&](int s, const Batch &b) {
+    const int heads = b.j ? a.Hk : a.Hq;
+    const int64_t t = token(b.tb);
+    const bool live = alive(b.tb), full = whole(b);
+    auto put = [&](const void *base, int64_t st, int64_t sh, int q) {
+      const E *p = reinterpret_cast<const E *>(base) + t * st + (b.h0 + first) * sh + e0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        rd[u] = ld8<true>(p, h0 + u * gr.hp + first < heads ? n : 0);
-        p += gr.hp * a.y_sh[j];
+        if (full) {
+#pragma unroll
+          for (int i = 0; i < R::P; ++i) copy16(slot(s, u, q) + i * kThreads, p + i * 4);
+        } else {
+          const bool ok = live && b.h0 + u * gr.hp + first < heads;
+#pragma unroll
+          for (int i = 0; i < R::P; ++i)
+            copy16(slot(s, u, q) + i * kThreads, ok ? p + i * 4 : reinterpret_cast<const E *>(base),
+                   ok);
+        }
+        p += gr.hp * sh;
       }
+    };
+    if (b.tb < token_blocks) {
+      put(b.j ? a.x[1] : a.x[0], b.j ? a.x_st[1] : a.x_st[0], b.j ? a.x_sh[1] : a.x_sh[0], 0);
+      if (BWD)
+        put(b.j ? a.y[1] : a.y[0], b.j ? a.y_st[1] : a.y_st[0], b.j ? a.y_sh[1] : a.y_sh[0], 1);
     }
+    copies_commit();
   };
+  auto row = [&](int s, int u, int q) {
+    Raw8<E> r;
+    uint4 *w = reinterpret_cast<uint4 *>(&r);
+#pragma unroll
+    for (int i = 0; i < R::P; ++i) w[i] = slot(s, u, q)[i * kThreads];
+    return r;
+  };
+  Batch cur{(int64_t)blockIdx.x, a.Hq > 0 ? 0 : 1, 0}, ahead = cur;
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) {
+    issue(s, ahead);
+    ahead.next(a, rows);
+  }
   float4 ca[2], sa[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     ca[i] = make_float4(1.f, 1.f, 1.f, 1.f);
     sa[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  if (turned && alive(blockIdx.x)) load_angles<INTER>(a, token(blockIdx.x), e0, ca, sa);
-  int j = a.Hq > 0 ? 0 : 1, h0 = 0;
-  fetch(blockIdx.x, j, 0);
-  for (int64_t tb = blockIdx.x; tb < token_blocks; tb += gridDim.x) {
-    const int64_t t = token(tb);
+  if (turned && alive(cur.tb)) load_angles<INTER>(a, token(cur.tb), e0, ca, sa);
+  for (int i = threadIdx.x; i < 2 * LR * 8; i += kThreads) {
+    const mix::Param &w = i < LR * 8 ? a.w[0] : a.w[1];
+    ws[i / (LR * 8)][i % (LR * 8)] = w.p ? ldp(w, i % (LR * 8)) : 1.f;
+  }
+  f2 dw[2][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = pair(0.f, 0.f);
+  __syncthreads();
+
+  int stage = 0;
+  while (cur.tb < token_blocks) {
+    const int64_t t = token(cur.tb), tb = cur.tb;
     const bool live = alive(tb);
     const Angles ang = signed_angles<INTER>(ca, sa, lower);
     if (turned && alive(tb + gridDim.x)) load_angles<INTER>(a, token(tb + gridDim.x), e0, ca, sa);
-    float cw[8], sw[8];
+    f2 cw[4], sw[4];
     int formed = -1;  // the tensor that cw, sw are of
-    for (bool last = false; !last;) {
-      const int jj = j, hh = h0, heads = jj ? a.Hk : a.Hq;
+    while (cur.tb == tb) {
+      const int jj = cur.j, hh = cur.h0, heads = jj ? a.Hk : a.Hq;
+      const bool full = whole(cur);
+      issue(stage == 0 ? S - 1 : stage - 1, ahead);
+      ahead.next(a, rows);
+      cur.next(a, rows);
+      if (formed != jj) {
+        formed = jj;
+        f2 w[4], wp[4];
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float4 u = *reinterpret_cast<const float4 *>(&ws[jj][e0 + 2 * i]);
+          w[i] = pair(u.x, u.y);
+          w[i + 1] = pair(u.z, u.w);
+          const float4 v = *reinterpret_cast<const float4 *>(&ws[jj][other * 8 + 2 * i]);
+          wp[i] = INTER ? pair(u.y, u.x) : pair(v.x, v.y);
+          wp[i + 1] = INTER ? pair(u.w, u.z) : pair(v.z, v.w);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cw[i] = BWD ? w[i] : mul2(w[i], ang.c[i]);
+          sw[i] = mul2(wp[i], ang.s[i]);
+        }
+      }
+      copies_wait<S - 1>();
       Raw8<E> cx[U], cd[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        cx[u] = rx[u];
-        if (BWD) cd[u] = rd[u];
+        cx[u] = row(stage, u, 0);
+        if (BWD) cd[u] = row(stage, u, 1);
       }
-      h0 += gr.hp * U;
-      if (h0 >= heads) {
-        h0 = 0;
-        if (jj == 0 && a.Hk > 0) {
-          j = 1;
-        } else {
-          j = a.Hq > 0 ? 0 : 1;
-          last = true;
-        }
-      }
-      fetch(last ? tb + gridDim.x : tb, j, h0);
-      if (formed != jj) {
-        formed = jj;
-        float w[8], wp[8];
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 u = *reinterpret_cast<const float4 *>(&ws[jj][e0 + i]);
-          const float4 v = *reinterpret_cast<const float4 *>(&ws[jj][other * 8 + i]);
-          w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
-          wp[i] = v.x; wp[i + 1] = v.y; wp[i + 2] = v.z; wp[i + 3] = v.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          cw[i] = BWD ? w[i] : w[i] * ang.c[i];
-          sw[i] = (INTER ? w[i ^ 1] : wp[i]) * ang.s[i];
-        }
-      }
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      stage = stage + 1 == S ? 0 : stage + 1;
       if (!BWD) {
+        float v[U];
+        f2 x[U][4];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          float x[8];
-          unpack8(cx[u], x);
+          unpack4(cx[u], x[u]);
+          f2 q = mul2(x[u][0], x[u][0]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[u] = fmaf(x[i], x[i], v[u]);
+          for (int i = 1; i < 4; ++i) q = fma2(x[u][i], x[u][i], q);
+          float q0, q1;
+          unpair(q, q0, q1);
+          v[u] = q0 + q1;
         }
-        four_sums<LR>(v, gl, [&](float q, int) { return rsqrtf(fmaf(q, inv, a.eps)); });
+        group_sums<LR>(v, gl, [&](float q, int) { return rsqrtf(fmaf(q, inv, a.eps)); });
         E *p = reinterpret_cast<E *>(a.y[jj]) + t * a.y_st[jj] + (hh + first) * a.y_sh[jj] + e0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (hh + u * gr.hp >= heads) break;  // no lane group has a row left
-          float x[8], o[8];
-          unpack8(cx[u], x);
+          f2 o[4];
+          const f2 r = pair(v[u], v[u]);
           if (rotated) {
             partners<E, LR, INTER>(cx[u], other, o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = fmaf(x[i], cw[i], o[i] * sw[i]) * v[u];
+            for (int i = 0; i < 4; ++i) o[i] = mul2(fma2(x[u][i], cw[i], mul2(o[i], sw[i])), r);
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = x[i] * cw[i] * v[u];
+            for (int i = 0; i < 4; ++i) o[i] = mul2(mul2(x[u][i], cw[i]), r);
           }
-          st8<true>(p, pack8(o, E{}), live && hh + u * gr.hp + first < heads ? 8 : 0);
+          if (full || (live && hh + u * gr.hp + first < heads)) st8<true>(p, pack4<E>(o), 8);
           p += gr.hp * a.y_sh[jj];
         }
       } else {
-        float e[U][8];  // the rotation undone
+        f2 e[U][4], x[U][4];  // e: the rotation undone
+        float v[2 * U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          float x[8];
-          unpack8(cx[u], x);
-          unpack8(cd[u], e[u]);
+          unpack4(cx[u], x[u]);
+          unpack4(cd[u], e[u]);
           if (rotated) {
-            float o[8];
+            f2 o[4];
             partners<E, LR, INTER>(cd[u], other, o);
+            const f2 minus = pair(-1.f, -1.f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[u][i] = fmaf(e[u][i], ang.c[i], -o[i] * ang.s[i]);
+            for (int i = 0; i < 4; ++i)
+              e[u][i] = fma2(e[u][i], ang.c[i], mul2(mul2(o[i], minus), ang.s[i]));
           }
+          f2 q = mul2(x[u][0], x[u][0]), d = mul2(mul2(e[u][0], cw[0]), x[u][0]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[u] = fmaf(x[i], x[i], v[u]);
-            v[2 + u] = fmaf(e[u][i] * cw[i], x[i], v[2 + u]);
+          for (int i = 1; i < 4; ++i) {
+            q = fma2(x[u][i], x[u][i], q);
+            d = fma2(mul2(e[u][i], cw[i]), x[u][i], d);
           }
+          float q0, q1;
+          unpair(q, q0, q1);
+          v[u] = q0 + q1;
+          unpair(d, q0, q1);
+          v[U + u] = q0 + q1;
         }
-        four_sums<LR>(v, gl, [&](float q, int k) {
-          return k < 2 ? rsqrtf(fmaf(q, inv, a.eps)) : q * inv;
+        group_sums<LR>(v, gl, [&](float q, int k) {
+          return k < U ? rsqrtf(fmaf(q, inv, a.eps)) : q * inv;
         });
         E *p = reinterpret_cast<E *>(a.dx[jj]) + t * a.dx_st[jj] + (hh + first) * a.dx_sh[jj] + e0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (hh + u * gr.hp >= heads) break;
-          const bool ok = live && hh + u * gr.hp + first < heads;
-          const float r = ok ? v[u] : 0.f, d = v[2 + u] * r * r * r;  // eps may be 0
-          float x[8], o[8];
-          unpack8(cx[u], x);
+          const bool ok = full || (live && hh + u * gr.hp + first < heads);
+          const float rr = ok ? v[u] : 0.f, dd = -v[U + u] * rr * rr * rr;  // eps may be 0
+          const f2 r = pair(rr, rr), d = pair(dd, dd);
+          f2 o[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float g = e[u][i] * x[i];  // rows past the end are zero
+          for (int i = 0; i < 4; ++i) {
+            const f2 g = mul2(e[u][i], x[u][i]);  // rows past the end are zero
             if (jj)
-              dw[1][i] = fmaf(g, r, dw[1][i]);
+              dw[1][i] = fma2(g, r, dw[1][i]);
             else
-              dw[0][i] = fmaf(g, r, dw[0][i]);
-            o[i] = fmaf(e[u][i] * cw[i], r, -x[i] * d);
+              dw[0][i] = fma2(g, r, dw[0][i]);
+            o[i] = fma2(mul2(e[u][i], cw[i]), r, mul2(x[u][i], d));
           }
-          st8<true>(p, pack8(o, E{}), ok ? 8 : 0);
+          if (ok) st8<true>(p, pack4<E>(o), 8);
           p += gr.hp * a.dx_sh[jj];
         }
       }
@@ -276,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     for (int j = 0; j < 2; ++j) {
       if (!a.dw[j]) continue;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) part[grp][e0 + i] = dw[j][i];
+      for (int i = 0; i < 4; ++i)
+        unpair(dw[j][i], part[grp][e0 + 2 * i], part[grp][e0 + 2 * i + 1]);
       __syncthreads();
       for (int e = threadIdx.x; e < a.d; e += kThreads) {
         float v = 0.f;
@@ -429,10 +509,13 @@ cudaError_t run_fast(const QkArgs &a, cudaStream_t stream, int *blocks_out) {
   int64_t blocks = tb;
   if (blocks > most_blocks()) blocks = most_blocks();
   *blocks_out = (int)blocks;
+  constexpr int smem = Ring<E, BWD>::kBytes;
+  static_assert(smem + 2 * LR * 8 * 4 <= 48 * 1024 && smem + kThreads * 8 * 4 <= 46 * 1024 + 2048,
+                "more shared memory than a launch has without asking");
   if (a.interleaved)
-    k_qk<E, LR, true, BWD><<<(unsigned)blocks, kThreads, 0, stream>>>(a, gr, tb);
+    k_qk<E, LR, true, BWD><<<(unsigned)blocks, kThreads, smem, stream>>>(a, gr, tb);
   else
-    k_qk<E, LR, false, BWD><<<(unsigned)blocks, kThreads, 0, stream>>>(a, gr, tb);
+    k_qk<E, LR, false, BWD><<<(unsigned)blocks, kThreads, smem, stream>>>(a, gr, tb);
   return cudaGetLastError();
 }
 
