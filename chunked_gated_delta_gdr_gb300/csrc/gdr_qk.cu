@@ -113,24 +113,6 @@ struct Groups {
   int tp;  // tokens of a block
 };
 
-// Where a block is in its work: batches of the heads of q, then of k, of token tb, tb + gridDim.x
-// and so on.
-struct Batch {
-  int64_t tb;
-  int j, h0;
-  __device__ __forceinline__ void next(const QkArgs &a, int rows) {
-    h0 += rows;
-    if (h0 < (j ? a.Hk : a.Hq)) return;
-    h0 = 0;
-    if (j == 0 && a.Hk > 0) {
-      j = 1;
-    } else {
-      j = a.Hq > 0 ? 0 : 1;
-      tb += gridDim.x;
-    }
-  }
-};
-
 template <typename E, bool BWD>
 struct Ring {
   static constexpr int U = 2;                           // rows of a lane group in a batch
@@ -140,60 +122,98 @@ struct Ring {
   static constexpr int kBytes = S * kSlot * kThreads * 16;
 };
 
-// A block runs over batches of U rows a lane group; the next S - 1 batches are on their way into
-// a ring in shared memory in which each thread reads only what it copied itself.  The weights'
-// products with the angles are formed once a token:
+// A block runs over tokens tb, tb + gridDim.x and so on, and for each over batches of the heads of
+// q, then of k, U rows a lane group.  The next S - 1 batches are on their way into a ring in shared
+// memory in which each thread reads only what it copied itself.  The weights' products with the
+// angles are formed once a token:
 //   y_e = r (x_e (w_e cos_e) + x_partner (w_partner sin_e)).
 template <typename E, int LR, bool INTER, bool BWD>
 __global__ void __launch_bounds__(kThreads, kCtas)
-    k_qk(const QkArgs a, const Groups gr, int64_t token_blocks) {
+    k_qk(const QkArgs a, const Groups gr, int token_blocks) {
   using R = Ring<E, BWD>;
   constexpr int RP = kThreads / LR, U = R::U, S = R::S;
   __shared__ __align__(16) float ws[2][LR * 8];
   extern __shared__ __align__(16) uint4 ring[];
   const int grp = threadIdx.x / LR, gl = threadIdx.x % LR, e0 = gl * 8;
-  const int first = grp % gr.hp, rows = gr.hp * U;
+  const int hp = gr.hp, first = grp % hp, mine = grp / hp, rows = hp * U;
   const bool rotated = a.rot > 0, turned = e0 < a.rot, lower = e0 < (a.rot >> 1);
   const int ro = a.rot >> 4;  // lanes of half the rotated part
   const int other = INTER || !turned ? gl : (lower ? gl + ro : gl - ro);
   const float inv = a.rms ? 1.f / (float)a.d : 1.f;
-  auto token = [&](int64_t tb) { return tb * gr.tp + grp / gr.hp; };
-  auto alive = [&](int64_t tb) {
-    return tb < token_blocks && grp < gr.hp * gr.tp && token(tb) < a.T;
-  };
+  const int stride = gridDim.x, j0 = a.Hq > 0 ? 0 : 1;
+  // whether a batch of q (k) has a row in every place, for a block of tokens inside T
+  const bool even[2] = {hp * gr.tp == RP && a.Hq % rows == 0, hp * gr.tp == RP && a.Hk % rows == 0};
+  auto inside = [&](int tb) { return (int64_t)(tb + 1) * gr.tp <= a.T; };
+  auto alive = [&](int tb) { return mine < gr.tp && (int64_t)tb * gr.tp + mine < a.T; };
   auto slot = [&](int s, int u, int q) {
     return ring + ((s * R::kSlot + (u * (BWD ? 2 : 1) + q) * R::P) * kThreads + threadIdx.x);
   };
-  // whether every lane group of the block has a row in each of the batch's places
-  auto whole = [&](const Batch &b) {
-    return gr.hp * gr.tp == RP && (b.tb + 1) * gr.tp <= a.T &&
-           b.h0 + rows <= (b.j ? a.Hk : a.Hq);
+  // this lane group's first row of a tensor at its first token, and the step to its next token
+  const int64_t t0 = (int64_t)blockIdx.x * gr.tp + mine, tstep = (int64_t)stride * gr.tp;
+  auto start = [&](const void *base, int64_t st, int64_t sh) {
+    return reinterpret_cast<const E *>(base) + t0 * st + first * sh + e0;
   };
-  auto issue = [&](int s, const Batch &b) {
-    const int heads = b.j ? a.Hk : a.Hq;
-    const int64_t t = token(b.tb);
-    const bool live = alive(b.tb), full = whole(b);
-    auto put = [&](const void *base, int64_t st, int64_t sh, int q) {
-      const E *p = reinterpret_cast<const E *>(base) + t * st + (b.h0 + first) * sh + e0;
+
+  // the copies' place: block of tokens, tensor, head, stage; the first rows at that token
+  int at_tb = blockIdx.x, at_j = j0, at_h = 0, at_s = 0;
+  const E *xb[2], *gb[2];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (full) {
-#pragma unroll
-          for (int i = 0; i < R::P; ++i) copy16(slot(s, u, q) + i * kThreads, p + i * 4);
-        } else {
-          const bool ok = live && b.h0 + u * gr.hp + first < heads;
-#pragma unroll
-          for (int i = 0; i < R::P; ++i)
-            copy16(slot(s, u, q) + i * kThreads, ok ? p + i * 4 : reinterpret_cast<const E *>(base),
-                   ok);
-        }
-        p += gr.hp * sh;
+  for (int j = 0; j < 2; ++j) {
+    xb[j] = start(a.x[j], a.x_st[j], a.x_sh[j]);
+    gb[j] = start(a.y[j], a.y_st[j], a.y_sh[j]);
+  }
+  auto issue = [&]() {
+    if (at_tb < token_blocks) {
+      const bool k = at_j;
+      const int heads = k ? a.Hk : a.Hq;
+      const int64_t xs = hp * (k ? a.x_sh[1] : a.x_sh[0]), gs = hp * (k ? a.y_sh[1] : a.y_sh[0]);
+      const E *x = k ? xb[1] : xb[0], *g = k ? gb[1] : gb[0];
+      if (at_h > 0) {
+        x += at_h * (k ? a.x_sh[1] : a.x_sh[0]);
+        if (BWD) g += at_h * (k ? a.y_sh[1] : a.y_sh[0]);
       }
-    };
-    if (b.tb < token_blocks) {
-      put(b.j ? a.x[1] : a.x[0], b.j ? a.x_st[1] : a.x_st[0], b.j ? a.x_sh[1] : a.x_sh[0], 0);
-      if (BWD)
-        put(b.j ? a.y[1] : a.y[0], b.j ? a.y_st[1] : a.y_st[0], b.j ? a.y_sh[1] : a.y_sh[0], 1);
+      if ((k ? even[1] : even[0]) && inside(at_tb)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int i = 0; i < R::P; ++i) {
+            copy16(slot(at_s, u, 0) + i * kThreads, x + i * 4);
+            if (BWD) copy16(slot(at_s, u, 1) + i * kThreads, g + i * 4);
+          }
+          x += xs;
+          if (BWD) g += gs;
+        }
+      } else {
+        const bool live = alive(at_tb);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const bool ok = live && at_h + u * hp + first < heads;
+#pragma unroll
+          for (int i = 0; i < R::P; ++i) {  // without a row: zeros, from no address
+            copy16(slot(at_s, u, 0) + i * kThreads,
+                   ok ? x + i * 4 : reinterpret_cast<const E *>(k ? a.x[1] : a.x[0]), ok);
+            if (BWD)
+              copy16(slot(at_s, u, 1) + i * kThreads,
+                     ok ? g + i * 4 : reinterpret_cast<const E *>(k ? a.y[1] : a.y[0]), ok);
+          }
+          x += xs;
+          if (BWD) g += gs;
+        }
+      }
+      at_s = at_s + 1 == S ? 0 : at_s + 1;
+      at_h += rows;
+      if (at_h >= heads) {
+        at_h = 0;
+        at_j = !k && a.Hk > 0 ? 1 : j0;
+        if (k || a.Hk == 0) {
+          at_tb += stride;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            xb[j] += tstep * a.x_st[j];
+            if (BWD) gb[j] += tstep * a.y_st[j];
+          }
+        }
+      }
     }
     copies_commit();
   };
@@ -204,146 +224,141 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     for (int i = 0; i < R::P; ++i) w[i] = slot(s, u, q)[i * kThreads];
     return r;
   };
-  Batch cur{(int64_t)blockIdx.x, a.Hq > 0 ? 0 : 1, 0}, ahead = cur;
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) {
-    issue(s, ahead);
-    ahead.next(a, rows);
-  }
+  for (int s = 0; s < S - 1; ++s) issue();
   float4 ca[2], sa[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     ca[i] = make_float4(1.f, 1.f, 1.f, 1.f);
     sa[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  if (turned && alive(cur.tb)) load_angles<INTER>(a, token(cur.tb), e0, ca, sa);
+  if (turned && alive(blockIdx.x)) load_angles<INTER>(a, t0, e0, ca, sa);
   for (int i = threadIdx.x; i < 2 * LR * 8; i += kThreads) {
-    const mix::Param &w = i < LR * 8 ? a.w[0] : a.w[1];
+    const Param &w = i < LR * 8 ? a.w[0] : a.w[1];
     ws[i / (LR * 8)][i % (LR * 8)] = w.p ? ldp(w, i % (LR * 8)) : 1.f;
   }
   f2 dw[2][4];
+  E *ob[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = pair(0.f, 0.f);
+  for (int j = 0; j < 2; ++j) {
+    ob[j] = const_cast<E *>(BWD ? start(a.dx[j], a.dx_st[j], a.dx_sh[j])
+                                : start(a.y[j], a.y_st[j], a.y_sh[j]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dw[j][i] = pair(0.f, 0.f);
+  }
   __syncthreads();
 
   int stage = 0;
-  while (cur.tb < token_blocks) {
-    const int64_t t = token(cur.tb), tb = cur.tb;
-    const bool live = alive(tb);
+  for (int tb = blockIdx.x; tb < token_blocks; tb += stride) {
+    const bool live = alive(tb), in = inside(tb);
     const Angles ang = signed_angles<INTER>(ca, sa, lower);
-    if (turned && alive(tb + gridDim.x)) load_angles<INTER>(a, token(tb + gridDim.x), e0, ca, sa);
-    f2 cw[4], sw[4];
-    int formed = -1;  // the tensor that cw, sw are of
-    while (cur.tb == tb) {
-      const int jj = cur.j, hh = cur.h0, heads = jj ? a.Hk : a.Hq;
-      const bool full = whole(cur);
-      issue(stage == 0 ? S - 1 : stage - 1, ahead);
-      ahead.next(a, rows);
-      cur.next(a, rows);
-      if (formed != jj) {
-        formed = jj;
-        f2 w[4], wp[4];
+    if (turned && tb + stride < token_blocks && alive(tb + stride))
+      load_angles<INTER>(a, (int64_t)(tb + stride) * gr.tp + mine, e0, ca, sa);
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          const float4 u = *reinterpret_cast<const float4 *>(&ws[jj][e0 + 2 * i]);
-          w[i] = pair(u.x, u.y);
-          w[i + 1] = pair(u.z, u.w);
-          const float4 v = *reinterpret_cast<const float4 *>(&ws[jj][other * 8 + 2 * i]);
-          wp[i] = INTER ? pair(u.y, u.x) : pair(v.x, v.y);
-          wp[i + 1] = INTER ? pair(u.w, u.z) : pair(v.z, v.w);
-        }
+    for (int j = 0; j < 2; ++j) {
+      const int heads = j ? a.Hk : a.Hq;
+      const bool full = in && even[j];
+      const int64_t os = hp * (BWD ? a.dx_sh[j] : a.y_sh[j]);
+      E *p = ob[j];
+      ob[j] += tstep * (BWD ? a.dx_st[j] : a.y_st[j]);
+      f2 cw[4], sw[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          cw[i] = BWD ? w[i] : mul2(w[i], ang.c[i]);
-          sw[i] = mul2(wp[i], ang.s[i]);
+      for (int i = 0; i < 4; i += 2) {
+        const float4 u = *reinterpret_cast<const float4 *>(&ws[j][e0 + 2 * i]);
+        const float4 v = *reinterpret_cast<const float4 *>(&ws[j][other * 8 + 2 * i]);
+        cw[i] = pair(u.x, u.y);
+        cw[i + 1] = pair(u.z, u.w);
+        if (!BWD) {
+          cw[i] = mul2(cw[i], ang.c[i]);
+          cw[i + 1] = mul2(cw[i + 1], ang.c[i + 1]);
+          sw[i] = mul2(INTER ? pair(u.y, u.x) : pair(v.x, v.y), ang.s[i]);
+          sw[i + 1] = mul2(INTER ? pair(u.w, u.z) : pair(v.z, v.w), ang.s[i + 1]);
         }
       }
-      copies_wait<S - 1>();
-      Raw8<E> cx[U], cd[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        cx[u] = row(stage, u, 0);
-        if (BWD) cd[u] = row(stage, u, 1);
-      }
-      stage = stage + 1 == S ? 0 : stage + 1;
-      if (!BWD) {
-        float v[U];
-        f2 x[U][4];
+#pragma unroll 1
+      for (int h = 0; h < heads; h += rows) {
+        issue();
+        copies_wait<S - 1>();
+        Raw8<E> cx[U], cd[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          unpack4(cx[u], x[u]);
-          f2 q = mul2(x[u][0], x[u][0]);
-#pragma unroll
-          for (int i = 1; i < 4; ++i) q = fma2(x[u][i], x[u][i], q);
-          float q0, q1;
-          unpair(q, q0, q1);
-          v[u] = q0 + q1;
+          cx[u] = row(stage, u, 0);
+          if (BWD) cd[u] = row(stage, u, 1);
         }
-        group_sums<LR>(v, gl, [&](float q, int) { return rsqrtf(fmaf(q, inv, a.eps)); });
-        E *p = reinterpret_cast<E *>(a.y[jj]) + t * a.y_st[jj] + (hh + first) * a.y_sh[jj] + e0;
+        stage = stage + 1 == S ? 0 : stage + 1;
+        if (!BWD) {
+          float v[U];
+          f2 x[U][4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          f2 o[4];
-          const f2 r = pair(v[u], v[u]);
-          if (rotated) {
-            partners<E, LR, INTER>(cx[u], other, o);
+          for (int u = 0; u < U; ++u) {
+            unpack4(cx[u], x[u]);
+            f2 q = mul2(x[u][0], x[u][0]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = mul2(fma2(x[u][i], cw[i], mul2(o[i], sw[i])), r);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = mul2(mul2(x[u][i], cw[i]), r);
+            for (int i = 1; i < 4; ++i) q = fma2(x[u][i], x[u][i], q);
+            float q0, q1;
+            unpair(q, q0, q1);
+            v[u] = q0 + q1;
           }
-          if (full || (live && hh + u * gr.hp + first < heads)) st8<true>(p, pack4<E>(o), 8);
-          p += gr.hp * a.y_sh[jj];
-        }
-      } else {
-        f2 e[U][4], x[U][4];  // e: the rotation undone
-        float v[2 * U];
+          group_sums<LR>(v, gl, [&](float q, int) { return rsqrtf(fmaf(q, inv, a.eps)); });
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          unpack4(cx[u], x[u]);
-          unpack4(cd[u], e[u]);
-          if (rotated) {
+          for (int u = 0; u < U; ++u) {
             f2 o[4];
-            partners<E, LR, INTER>(cd[u], other, o);
-            const f2 minus = pair(-1.f, -1.f);
+            const f2 r = pair(v[u], v[u]);
+            if (rotated) {
+              partners<E, LR, INTER>(cx[u], other, o);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              e[u][i] = fma2(e[u][i], ang.c[i], mul2(mul2(o[i], minus), ang.s[i]));
+              for (int i = 0; i < 4; ++i) o[i] = mul2(fma2(x[u][i], cw[i], mul2(o[i], sw[i])), r);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[i] = mul2(mul2(x[u][i], cw[i]), r);
+            }
+            if (full || (live && h + u * hp + first < heads)) st8<true>(p, pack4<E>(o), 8);
+            p += os;
           }
-          f2 q = mul2(x[u][0], x[u][0]), d = mul2(mul2(e[u][0], cw[0]), x[u][0]);
+        } else {
+          f2 e[U][4], x[U][4];  // e: the rotation undone
+          float v[2 * U];
 #pragma unroll
-          for (int i = 1; i < 4; ++i) {
-            q = fma2(x[u][i], x[u][i], q);
-            d = fma2(mul2(e[u][i], cw[i]), x[u][i], d);
+          for (int u = 0; u < U; ++u) {
+            unpack4(cx[u], x[u]);
+            unpack4(cd[u], e[u]);
+            if (rotated) {
+              f2 o[4];
+              partners<E, LR, INTER>(cd[u], other, o);
+              const f2 minus = pair(-1.f, -1.f);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                e[u][i] = fma2(e[u][i], ang.c[i], mul2(mul2(o[i], minus), ang.s[i]));
+            }
+            f2 q = mul2(x[u][0], x[u][0]), d = mul2(mul2(e[u][0], cw[0]), x[u][0]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) {
+              q = fma2(x[u][i], x[u][i], q);
+              d = fma2(mul2(e[u][i], cw[i]), x[u][i], d);
+            }
+            float q0, q1;
+            unpair(q, q0, q1);
+            v[u] = q0 + q1;
+            unpair(d, q0, q1);
+            v[U + u] = q0 + q1;
           }
-          float q0, q1;
-          unpair(q, q0, q1);
-          v[u] = q0 + q1;
-          unpair(d, q0, q1);
-          v[U + u] = q0 + q1;
-        }
-        group_sums<LR>(v, gl, [&](float q, int k) {
-          return k < U ? rsqrtf(fmaf(q, inv, a.eps)) : q * inv;
-        });
-        E *p = reinterpret_cast<E *>(a.dx[jj]) + t * a.dx_st[jj] + (hh + first) * a.dx_sh[jj] + e0;
+          group_sums<LR>(v, gl, [&](float q, int k) {
+            return k < U ? rsqrtf(fmaf(q, inv, a.eps)) : q * inv;
+          });
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const bool ok = full || (live && hh + u * gr.hp + first < heads);
-          const float rr = ok ? v[u] : 0.f, dd = -v[U + u] * rr * rr * rr;  // eps may be 0
-          const f2 r = pair(rr, rr), d = pair(dd, dd);
-          f2 o[4];
+          for (int u = 0; u < U; ++u) {
+            const bool ok = full || (live && h + u * hp + first < heads);
+            const float rr = ok ? v[u] : 0.f, dd = -v[U + u] * rr * rr * rr;  // eps may be 0
+            const f2 r = pair(rr, rr), d = pair(dd, dd);
+            f2 o[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const f2 g = mul2(e[u][i], x[u][i]);  // rows past the end are zero
-            if (jj)
-              dw[1][i] = fma2(g, r, dw[1][i]);
-            else
-              dw[0][i] = fma2(g, r, dw[0][i]);
-            o[i] = fma2(mul2(e[u][i], cw[i]), r, mul2(x[u][i], d));
+            for (int i = 0; i < 4; ++i) {
+              dw[j][i] = fma2(mul2(e[u][i], x[u][i]), r, dw[j][i]);  // no row: zeros
+              o[i] = fma2(mul2(e[u][i], cw[i]), r, mul2(x[u][i], d));
+            }
+            if (ok) st8<true>(p, pack4<E>(o), 8);
+            p += os;
           }
-          if (ok) st8<true>(p, pack4<E>(o), 8);
-          p += gr.hp * a.dx_sh[jj];
         }
       }
     }
@@ -461,21 +476,22 @@ __global__ void __launch_bounds__(kThreads) k_qk_any(const QkArgs a, int64_t row
 }
 
 // dw: the blocks' parts, added by one block for each (tensor, 32 elements) in a fixed order.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     k_qk_sum(const float *work, int blocks, int d, float *dwq, float *dwk) {
-  __shared__ float part[8][32];
-  const int e = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5, j = blockIdx.y;
+  __shared__ float part[32][33];
+  const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, j = blockIdx.y;
+  const int e = blockIdx.x * 32 + lane;
   float *out = j ? dwk : dwq;
   if (!out) return;
   float v = 0.f;
-  if (e < d)
-    for (int b = k; b < blocks; b += 8) v += work[((int64_t)b * 2 + j) * d + e];
-  part[k][threadIdx.x & 31] = v;
-  __syncthreads();
-  if (k == 0 && e < d) {
-    for (int i = 1; i < 8; ++i) v += part[i][threadIdx.x];
-    out[e] = v;
+  if (e < d) {
+#pragma unroll 8
+    for (int b = k; b < blocks; b += 32) v += work[((int64_t)b * 2 + j) * d + e];
   }
+  part[k][lane] = v;
+  __syncthreads();
+  v = warp_sum(part[lane][k]);  // element k of the 32, over the rows
+  if (lane == 0 && blockIdx.x * 32 + k < d) out[blockIdx.x * 32 + k] = v;
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -513,9 +529,9 @@ cudaError_t run_fast(const QkArgs &a, cudaStream_t stream, int *blocks_out) {
   static_assert(smem + 2 * LR * 8 * 4 <= 48 * 1024 && smem + kThreads * 8 * 4 <= 46 * 1024 + 2048,
                 "more shared memory than a launch has without asking");
   if (a.interleaved)
-    k_qk<E, LR, true, BWD><<<(unsigned)blocks, kThreads, smem, stream>>>(a, gr, tb);
+    k_qk<E, LR, true, BWD><<<(unsigned)blocks, kThreads, smem, stream>>>(a, gr, (int)tb);
   else
-    k_qk<E, LR, false, BWD><<<(unsigned)blocks, kThreads, smem, stream>>>(a, gr, tb);
+    k_qk<E, LR, false, BWD><<<(unsigned)blocks, kThreads, smem, stream>>>(a, gr, (int)tb);
   return cudaGetLastError();
 }
 
@@ -554,7 +570,7 @@ cudaError_t launch_qk_bwd(const QkArgs &a, cudaStream_t stream) {
   cudaError_t e = a.f32 ? mix::run<float, true>(a, stream, &blocks)
                         : mix::run<__nv_bfloat16, true>(a, stream, &blocks);
   if (e != cudaSuccess || (!a.dw[0] && !a.dw[1])) return e;
-  mix::k_qk_sum<<<dim3((unsigned)ceil_div64(a.d, 32), 2), 256, 0, stream>>>(
+  mix::k_qk_sum<<<dim3((unsigned)ceil_div64(a.d, 32), 2), 1024, 0, stream>>>(
       reinterpret_cast<const float *>(a.work), blocks, a.d, a.dw[0], a.dw[1]);
   return cudaGetLastError();
 }

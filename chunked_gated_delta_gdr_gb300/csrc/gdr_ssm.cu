@@ -21,6 +21,9 @@ namespace {
 
 using namespace mix;
 
+constexpr int kFwdCtas = 4;  // blocks of pass 2 on each SM: the ranges are cut to run all at once
+constexpr int kEndCtas = 5;
+
 struct Ranges {
   int range, n;      // tokens of a range, ranges
   float *state;      // [n][D][N]: pass 1 the state at the end, after the chain the one at the start
@@ -28,186 +31,260 @@ struct Ranges {
   int *reset;        // [n]: a segment starts in the range
 };
 
+// A tile of B (or C) in shared memory as fp32, padded to NP states; read from global memory one
+// tile ahead.
+template <typename E, int LN>
+struct BcTile {
+  static constexpr int NP = Lay<LN>::NP, L = Lay<LN>::L, M = (L * NP + kThreads - 1) / kThreads;
+  E v[M];
+  __device__ __forceinline__ void fetch(const E *p, int64_t st, int tb, int t1, int N) {
+#pragma unroll
+    for (int q = 0; q < M; ++q) {
+      const int e = threadIdx.x + q * kThreads, t = tb + e / NP, n = e % NP;
+      v[q] = e < L * NP && t < t1 && n < N ? p[t * st + n] : E(0.f);
+    }
+  }
+  __device__ __forceinline__ void put(float *s) const {
+#pragma unroll
+    for (int q = 0; q < M; ++q) {
+      const int e = threadIdx.x + q * kThreads;
+      if (e < L * NP) s[e] = ld1(&v[q]);
+    }
+  }
+};
+
+// (dt, dt x) of a thread's 8 elements of a tile.
+template <typename E, int LN>
+__device__ __forceinline__ void put_pairs(float2 *pair, const float *bias, int softplus, int lt,
+                                          int lc, const Raw8<E> &rx, const Raw8<E> &rd) {
+  float x[8], d[8];
+  unpack8(rx, x);
+  unpack8(rd, d);
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    const float4 b = *reinterpret_cast<const float4 *>(bias + lc + i);
+    d[i] += b.x;
+    d[i + 1] += b.y;
+    d[i + 2] += b.z;
+    d[i + 3] += b.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = softplus ? softplusf(d[i]) : d[i];
+    pair[Lay<LN>::pair_at(lt, lc + i)] = make_float2(v, v * x[i]);
+  }
+}
+
 template <int LN>
-struct Tile {  // shared memory of one tile
+__device__ __forceinline__ void load_decays(const SsmArgs &a, const Place<LN> &P,
+                                            float (&A2)[2][4]) {
+  P.read(a, a.A, 0, A2);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) A2[k][j] *= kLog2e;
+}
+
+// Calls f(i) for tokens [i0, i1) of a tile; a whole tile is unrolled, so that its addresses are
+// constants.
+template <int L, typename F>
+__device__ __forceinline__ void tile_tokens(int i0, int i1, F f) {
+  constexpr int U = L < 16 ? L : 16;
+  if (i1 - i0 == L) {
+#pragma unroll 1
+    for (int i = 0; i < L; i += U)
+#pragma unroll
+      for (int u = 0; u < U; ++u) f(i + u);
+  } else {
+#pragma unroll 2
+    for (int i = i0; i < i1; ++i) f(i);
+  }
+}
+
+template <int LN>
+struct Tile1 {
+  using Y = Lay<LN>;
+  float2 pair[Y::L * Y::CH];
+  float b[Y::L * Y::NP];
+  float bias[Y::CH];
+  int red[64];
+};
+
+// Pass 1: the state at the end of a range.  Only the segment alive there counts, from its start or
+// the range's on.
+template <typename E, int LN, bool VEC>
+__global__ void __launch_bounds__(kThreads, kEndCtas)
+    k_ssm_ends(const SsmArgs a, const Ranges rg, int tiles_per_group) {
+  using Y = Lay<LN>;
+  constexpr int L = Y::L, NP = Y::NP, CH = Y::CH;
+  extern __shared__ __align__(16) char smem_raw[];
+  Tile1<LN> &s = *reinterpret_cast<Tile1<LN> *>(smem_raw);
+  const Place<LN> P(a, tiles_per_group);
+  const int r0 = P.r * rg.range, t1 = min(a.T, r0 + rg.range);
+  const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
+  const E *xp = reinterpret_cast<const E *>(a.x.p) + P.c0 + lc;
+  const E *dp = reinterpret_cast<const E *>(a.dt.p) + P.c0 + lc;
+  const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
+  for (int i = P.tid; i < CH; i += kThreads)
+    s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
+  float A2[2][4], h[2][4], S[2] = {0.f, 0.f};
+  load_decays(a, P, A2);
+  const SegCursor c = seg_find(a.cu, a.n_seq, a.T, t1, s.red);
+  const int seg = c.j - 1;
+  const bool covered = seg >= 0 && seg < a.n_seq, reset = seg >= 0 && c.b >= r0;
+  const int t0 = reset ? c.b : r0;
+  P.read(a, covered && reset ? a.h0 : nullptr, seg, h);
+  if (covered) {
+    Raw8<E> rx, rd;
+    BcTile<E, LN> rb;
+    auto fetch = [&](int tb) {
+      const int n = tb + lt < t1 ? nv : 0;
+      rx = ld8<VEC>(xp + (int64_t)(tb + lt) * a.x.st, n);
+      rd = ld8<VEC>(dp + (int64_t)(tb + lt) * a.dt.st, n);
+      rb.fetch(Bp, a.B_st, tb, t1, a.N);
+    };
+    fetch(t0);
+    __syncthreads();
+    for (int tb = t0; tb < t1; tb += L) {
+      put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, rx, rd);
+      rb.put(s.b);
+      if (tb + L < t1) fetch(tb + L);
+      __syncthreads();
+      tile_tokens<L>(0, min(L, t1 - tb), [&](int i) {
+        const float4 d = *reinterpret_cast<const float4 *>(
+            &s.pair[i * CH + Y::pair_slot(i, P.warp, P.cl) * 2]);
+        const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
+        const float dt[2] = {d.x, d.z}, dx[2] = {d.y, d.w}, Bv[4] = {B.x, B.y, B.z, B.w};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          S[k] += dt[k];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            h[k][j] = fmaf(ex2(dt[k] * A2[k][j]), h[k][j], dx[k] * Bv[j]);
+        }
+      });
+      __syncthreads();
+    }
+  }
+  P.write(a, rg.state, P.r, h);
+  if (P.nl == 0) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (P.ch[k] < P.nch) rg.sum[(int64_t)P.r * a.D + P.c0 + P.ch[k]] = S[k];
+  }
+  if (P.ct == 0 && P.tid == 0) rg.reset[P.r] = reset;
+}
+
+template <int LN>
+struct Tile2 {  // shared memory of one tile of pass 2
   using Y = Lay<LN>;
   float2 pair[Y::L * Y::CH];  // (dt, dt x)
   float b[Y::L * Y::NP], c[Y::L * Y::NP];
   float part[Y::L * Y::CH * LN];
+  float bias[Y::CH], skip[Y::CH];
   int mark[Y::L + 1], seg[Y::L], any, same;
   int red[64];
 };
 
-// One range.  ENDS: pass 1 (no y).  VEC: every group of 8 channels is whole and 16-byte aligned.
-template <typename E, int LN, bool ENDS, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+// Pass 2: a range from its true state.
+template <typename E, int LN, bool VEC>
+__global__ void __launch_bounds__(kThreads, kFwdCtas)
     k_ssm_fwd(const SsmArgs a, const Ranges rg, int tiles_per_group) {
   using Y = Lay<LN>;
   constexpr int L = Y::L, NP = Y::NP, CH = Y::CH;
-  constexpr int NB = (L * NP + kThreads - 1) / kThreads;  // elements of B a thread loads for a tile
   extern __shared__ __align__(16) char smem_raw[];
-  Tile<LN> &s = *reinterpret_cast<Tile<LN> *>(smem_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int ctiles = tiles_per_group * a.G;
-  const int ct = blockIdx.x % ctiles, r = blockIdx.x / ctiles;
-  const int grp = ct / tiles_per_group, Dg = a.D / a.G;
-  const int c0 = grp * Dg + ct % tiles_per_group * CH;
-  const int nch = min(CH, (grp + 1) * Dg - c0);
-  const int N = a.N;
-
-  if (!ENDS && r == rg.n) {  // final states of the segments without tokens
+  Tile2<LN> &s = *reinterpret_cast<Tile2<LN> *>(smem_raw);
+  const Place<LN> P(a, tiles_per_group);
+  if (P.r == rg.n) {  // final states of the segments without tokens
     for_empty_segments(a.cu, a.n_seq, a.T, s.red, [&](int n) {
-      const int64_t at = ((int64_t)n * a.D + c0) * N;
-      for (int i = tid; i < nch * N; i += kThreads) a.ht[at + i] = a.h0 ? a.h0[at + i] : 0.f;
+      const int64_t at = ((int64_t)n * a.D + P.c0) * a.N;
+      for (int i = P.tid; i < P.nch * a.N; i += kThreads)
+        a.ht[at + i] = a.h0 ? a.h0[at + i] : 0.f;
     });
     return;
   }
-  const int t0 = r * rg.range, t1 = min(a.T, t0 + rg.range);
-
-  // this thread's states: channels ch[k], states 4 nl .. 4 nl + 3
-  const int nl = lane % LN, cl = lane / LN;
-  float A2[2][4], h[2][4], S[2] = {0.f, 0.f};
-  int ch[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    ch[k] = Y::channel(warp, lane, k);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = nl * 4 + j;
-      A2[k][j] = (ch[k] < nch && n < N) ? a.A[(int64_t)(c0 + ch[k]) * N + n] * kLog2e : 0.f;
-      h[k][j] = 0.f;
-    }
+  const int t0 = P.r * rg.range, t1 = min(a.T, t0 + rg.range);
+  const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
+  const E *xp = reinterpret_cast<const E *>(a.x.p) + P.c0 + lc;
+  const E *dp = reinterpret_cast<const E *>(a.dt.p) + P.c0 + lc;
+  const E *zp = a.z.p ? reinterpret_cast<const E *>(a.z.p) + P.c0 + lc : nullptr;
+  E *yp = reinterpret_cast<E *>(a.y.p) + P.c0 + lc;
+  const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
+  const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
+  for (int i = P.tid; i < CH; i += kThreads) {
+    s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
+    s.skip[i] = a.Dskip && i < P.nch ? a.Dskip[P.c0 + i] : 0.f;
   }
-  auto read_state = [&](const float *p, int64_t row) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = nl * 4 + j;
-        h[k][j] = (p && ch[k] < nch && n < N) ? p[(row * a.D + c0 + ch[k]) * N + n] : 0.f;
-      }
-  };
-  auto write_state = [&](float *p, int64_t row) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = nl * 4 + j;
-        if (ch[k] < nch && n < N) p[(row * a.D + c0 + ch[k]) * N + n] = h[k][j];
-      }
-  };
-
-  // this thread's 8 elements of a tile of x, dt, z and y
-  const int lt = tid / Y::CG, lc = tid % Y::CG * 8, nv = max(0, min(8, nch - lc));
-  const E *xp = reinterpret_cast<const E *>(a.x.p) + c0 + lc;
-  const E *dp = reinterpret_cast<const E *>(a.dt.p) + c0 + lc;
-  const E *zp = a.z.p ? reinterpret_cast<const E *>(a.z.p) + c0 + lc : nullptr;
-  E *yp = reinterpret_cast<E *>(a.y.p) + c0 + lc;
-  const E *Bp = reinterpret_cast<const E *>(a.B) + grp * a.B_sg;
-  const E *Cp = reinterpret_cast<const E *>(a.C) + grp * a.C_sg;
-  float bias[8], skip[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bias[i] = (a.dt_bias && i < nv) ? a.dt_bias[c0 + lc + i] : 0.f;
-    skip[i] = (!ENDS && a.Dskip && i < nv) ? a.Dskip[c0 + lc + i] : 0.f;
-  }
-
   Raw8<E> rx, rd, rz = zero8<E>();
-  E rb[NB], rc[NB];
+  BcTile<E, LN> rb, rc;
   auto fetch = [&](int tb) {
-    const int t = tb + lt, n = t < t1 ? nv : 0;
-    rx = ld8<VEC>(xp + (int64_t)t * a.x.st, n);
-    rd = ld8<VEC>(dp + (int64_t)t * a.dt.st, n);
-    if (!ENDS && zp) rz = ld8<VEC>(zp + (int64_t)t * a.z.st, n);
+    const int n = tb + lt < t1 ? nv : 0;
+    rx = ld8<VEC>(xp + (int64_t)(tb + lt) * a.x.st, n);
+    rd = ld8<VEC>(dp + (int64_t)(tb + lt) * a.dt.st, n);
+    if (zp) rz = ld8<VEC>(zp + (int64_t)(tb + lt) * a.z.st, n);
+    rb.fetch(Bp, a.B_st, tb, t1, a.N);
+    rc.fetch(Cp, a.C_st, tb, t1, a.N);
   };
-  auto fetch_bc = [&](int tb) {
-#pragma unroll
-    for (int q = 0; q < NB; ++q) {
-      const int e = tid + q * kThreads, t = tb + e / NP, n = e % NP;
-      const bool ok = e < L * NP && t < t1 && n < N;
-      rb[q] = ok ? Bp[t * a.B_st + n] : E(0.f);
-      if (!ENDS) rc[q] = ok ? Cp[t * a.C_st + n] : E(0.f);
-    }
-  };
-
+  fetch(t0);
+  float A2[2][4], h[2][4];
+  load_decays(a, P, A2);
   SegCursor cursor = seg_find(a.cu, a.n_seq, a.T, t0, s.red);
   int seg = cursor.j - 1;
-  bool reset = false;
-  if (!ENDS && r > 0 && seg >= 0 && seg < a.n_seq) read_state(rg.state, r);
-  fetch(t0);
-  fetch_bc(t0);
+  P.read(a, P.r > 0 && seg >= 0 && seg < a.n_seq ? rg.state : nullptr, P.r, h);
+  __syncthreads();
 
-  // the scan of tokens [i0, i1) of the tile
+  // where this thread's partial sums of its two channels go in a token's row
+  int po[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) po[k] = Y::part_at(0, P.ch[k]) + P.nl;
   auto scan = [&](int i0, int i1) {
-#pragma unroll 4
-    for (int i = i0; i < i1; ++i) {
+    tile_tokens<L>(i0, i1, [&](int i) {
       const float4 d = *reinterpret_cast<const float4 *>(
-          &s.pair[i * CH + Y::pair_slot(i, warp, cl) * 2]);
-      const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + nl * 4]);
+          &s.pair[i * CH + Y::pair_slot(i, P.warp, P.cl) * 2]);
+      const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
+      const float4 C = *reinterpret_cast<const float4 *>(&s.c[i * NP + P.nl * 4]);
       const float dt[2] = {d.x, d.z}, dx[2] = {d.y, d.w}, Bv[4] = {B.x, B.y, B.z, B.w};
-      float4 C;
-      if (!ENDS) C = *reinterpret_cast<const float4 *>(&s.c[i * NP + nl * 4]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           h[k][j] = fmaf(ex2(dt[k] * A2[k][j]), h[k][j], dx[k] * Bv[j]);
-        if (ENDS)
-          S[k] += dt[k];
-        else
-          s.part[Y::part_at(i, ch[k]) + nl] =
-              fmaf(h[k][0], C.x, h[k][1] * C.y) + fmaf(h[k][2], C.z, h[k][3] * C.w);
+        s.part[po[k] + i * CH * LN] =
+            fmaf(h[k][0], C.x, fmaf(h[k][1], C.y, fmaf(h[k][2], C.z, h[k][3] * C.w)));
       }
-    }
+    });
   };
 
   for (int tb = t0; tb < t1; tb += L) {
     const int n = min(L, t1 - tb);
     // this tile's elements into shared memory, the next tile's from global memory
-    float x[8], d[8], z[8];
-    unpack8(rx, x);
-    unpack8(rd, d);
-    unpack8(rz, z);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v = d[i] + bias[i];
-      if (a.softplus) v = softplusf(v);
-      s.pair[Y::pair_at(lt, lc + i)] = make_float2(v, v * x[i]);
-    }
-#pragma unroll
-    for (int q = 0; q < NB; ++q) {
-      const int e = tid + q * kThreads;
-      if (e < L * NP) {
-        s.b[e] = ld1(&rb[q]);
-        if (!ENDS) s.c[e] = ld1(&rc[q]);
-      }
-    }
-    if (warp == 0) {
+    put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, rx, rd);
+    rb.put(s.b);
+    rc.put(s.c);
+    const Raw8<E> cx = rx, cz = rz;
+    if (P.warp == 0) {
       const int carry = cursor.j - 1;
       const bool any = seg_marks(a.cu, a.n_seq, a.T, tb, n, s.mark, cursor);
       if (any) {
         int base = carry;
         for (int i0 = 0; i0 < L; i0 += 32) {
-          int v = i0 + lane < n ? s.mark[i0 + lane] : -1;
+          int v = i0 + P.lane < n ? s.mark[i0 + P.lane] : -1;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v = max(v, u);
+            if (P.lane >= o) v = max(v, u);
           }
           v = max(v, base);
-          if (i0 + lane < L) s.seg[i0 + lane] = v;
+          if (i0 + P.lane < L) s.seg[i0 + P.lane] = v;
           base = __shfl_sync(0xffffffffu, v, 31);
         }
       }
-      if (lane == 0) {
+      if (P.lane == 0) {
         s.any = any;
         s.same = carry;
       }
     }
-    if (tb + L < t1) {
-      fetch(tb + L);
-      fetch_bc(tb + L);
-    }
+    if (tb + L < t1) fetch(tb + L);
     __syncthreads();
     const bool any = s.any;
     if (!any) {
@@ -216,42 +293,33 @@ __global__ void __launch_bounds__(kThreads)
       for (int i = 0; i < n;) {
         if (s.mark[i] >= 0) {
           seg = s.mark[i];
-          if (seg < a.n_seq) read_state(a.h0, seg);
-          S[0] = S[1] = 0.f;
-          reset = true;
+          P.read(a, seg < a.n_seq ? a.h0 : nullptr, seg, h);
         }
         int e = i + 1;
         while (e < n && s.mark[e] < 0) ++e;
         if (seg >= 0 && seg < a.n_seq) {
           scan(i, e);
-          if (!ENDS && a.ht && s.mark[e] >= 0) write_state(a.ht, seg);
+          if (a.ht && s.mark[e] >= 0) P.write(a, a.ht, seg, h);
         }
         i = e;
       }
     }
     __syncthreads();
-    if (!ENDS) {
-      const int own = any ? s.seg[lt] : s.same;
-      if (lt < n && own >= 0 && own < a.n_seq) {
-        float v[8];
+    const int own = any ? s.seg[lt] : s.same;
+    if (lt < n && own >= 0 && own < a.n_seq) {
+      float x[8], v[8];
+      unpack8(cx, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[i] = fmaf(skip[i], x[i], sum_parts<LN>(&s.part[Y::part_at(lt, lc + i)]));
-          if (zp) v[i] *= z[i] * sigmoidf(z[i]);
-        }
-        st8<VEC>(yp + (int64_t)(tb + lt) * a.y.st, pack8(v, E{}), nv);
+      for (int i = 0; i < 8; ++i)
+        v[i] = fmaf(s.skip[lc + i], x[i], sum_parts<LN>(&s.part[Y::part_at(lt, lc + i)]));
+      if (zp) {
+        unpack8(cz, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= x[i] * sigmoidf(x[i]);
       }
-      __syncthreads();
+      st8<VEC>(yp + (int64_t)(tb + lt) * a.y.st, pack8(v, E{}), nv);
     }
-  }
-  if (ENDS) {
-    write_state(rg.state, r);
-    if (nl == 0) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (ch[k] < nch) rg.sum[(int64_t)r * a.D + c0 + ch[k]] = S[k];
-    }
-    if (ct == 0 && tid == 0) rg.reset[r] = reset;
+    __syncthreads();
   }
 }
 
@@ -343,9 +411,17 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <int LN>
-int fwd_range(int64_t T, int D, int G) {
-  return range_tokens(T, channel_tiles(D, G, LN), Lay<LN>::L, 8, 128);
+// Tokens of a range: as many ranges as run at once, of at least 8 tiles.  Fewer would leave SMs
+// idle, more would only repeat pass 1 for more tokens.
+int range_for(int64_t T, int32_t D, int32_t N, int32_t G) {
+  const int LN = lanes_for(N), tile = 4 * LN;
+  const int64_t ctiles = channel_tiles(D, G, LN);
+  int64_t n = (int64_t)sm_count() * kFwdCtas / ctiles;
+  const int64_t most = ceil_div64(T, 8 * tile);
+  if (n > most) n = most;
+  if (n < 1) n = 1;
+  const int64_t r = ceil_div64(ceil_div64(T, n), tile) * tile;
+  return (int)(r < tile ? tile : r);
 }
 
 struct Carve {
@@ -368,15 +444,6 @@ Carve carve(void *work, int64_t T, int32_t D, int32_t N, int range) {
   return c;
 }
 
-int range_for(int64_t T, int32_t D, int32_t N, int32_t G) {
-  switch (lanes_for(N)) {
-    case 2: return fwd_range<2>(T, D, G);
-    case 4: return fwd_range<4>(T, D, G);
-    case 8: return fwd_range<8>(T, D, G);
-    default: return fwd_range<16>(T, D, G);
-  }
-}
-
 template <typename K>
 cudaError_t allow_smem(K k, int bytes) {
   return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -385,16 +452,14 @@ cudaError_t allow_smem(K k, int bytes) {
 template <typename E, int LN, bool VEC>
 cudaError_t run_fwd(const SsmArgs &a, cudaStream_t stream) {
   const int tpg = (int)ceil_div64(a.D / a.G, Lay<LN>::CH), ctiles = tpg * a.G;
-  const Carve c = carve(a.work, a.T, a.D, a.N, fwd_range<LN>(a.T, a.D, a.G));
-  constexpr int smem = (int)sizeof(Tile<LN>);
+  const Carve c = carve(a.work, a.T, a.D, a.N, range_for(a.T, a.D, a.N, a.G));
+  constexpr int smem1 = (int)sizeof(Tile1<LN>), smem2 = (int)sizeof(Tile2<LN>);
   cudaError_t e;
-  if (smem > 48 * 1024) {
-    if ((e = allow_smem(k_ssm_fwd<E, LN, true, VEC>, smem)) != cudaSuccess) return e;
-    if ((e = allow_smem(k_ssm_fwd<E, LN, false, VEC>, smem)) != cudaSuccess) return e;
-  }
   if (c.rg.n > 1) {
-    k_ssm_fwd<E, LN, true, VEC>
-        <<<(unsigned)((int64_t)ctiles * (c.rg.n - 1)), kThreads, smem, stream>>>(a, c.rg, tpg);
+    if (smem1 > 48 * 1024 && (e = allow_smem(k_ssm_ends<E, LN, VEC>, smem1)) != cudaSuccess)
+      return e;
+    k_ssm_ends<E, LN, VEC>
+        <<<(unsigned)((int64_t)ctiles * (c.rg.n - 1)), kThreads, smem1, stream>>>(a, c.rg, tpg);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     k_ssm_chain<<<(unsigned)ceil_div64((int64_t)a.D * a.N, 128), 128, 0, stream>>>(a.A, c.rg, a.D,
                                                                                    a.N);
@@ -402,13 +467,9 @@ cudaError_t run_fwd(const SsmArgs &a, cudaStream_t stream) {
   }
   const int64_t blocks = (int64_t)ctiles * (c.rg.n + (a.ht ? 1 : 0));
   if (blocks == 0) return cudaSuccess;
-  k_ssm_fwd<E, LN, false, VEC><<<(unsigned)blocks, kThreads, smem, stream>>>(a, c.rg, tpg);
+  if (smem2 > 48 * 1024 && (e = allow_smem(k_ssm_fwd<E, LN, VEC>, smem2)) != cudaSuccess) return e;
+  k_ssm_fwd<E, LN, VEC><<<(unsigned)blocks, kThreads, smem2, stream>>>(a, c.rg, tpg);
   return cudaGetLastError();
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-bool rows_ok(const Mat &m, bool f32) {
-  return !m.p || (aligned16(m.p) && m.st % (f32 ? 4 : 8) == 0);
 }
 
 template <typename E>

@@ -44,6 +44,49 @@ struct Lay {
   }
 };
 
+// A block's range and channels, a thread's channels and states (4 nl .. 4 nl + 3 of both).
+template <int LN>
+struct Place {
+  using Y = Lay<LN>;
+  int tid, warp, lane, nl, cl, ct, r, grp, c0, nch;
+  int ch[2];
+  __device__ __forceinline__ Place(const SsmArgs &a, int tiles_per_group) {
+    tid = threadIdx.x;
+    warp = tid >> 5;
+    lane = tid & 31;
+    nl = lane % LN;
+    cl = lane / LN;
+    const int ctiles = tiles_per_group * a.G, Dg = a.D / a.G;
+    ct = blockIdx.x % ctiles;
+    r = blockIdx.x / ctiles;
+    grp = ct / tiles_per_group;
+    c0 = grp * Dg + ct % tiles_per_group * Y::CH;
+    nch = min(Y::CH, (grp + 1) * Dg - c0);
+    ch[0] = Y::channel(warp, lane, 0);
+    ch[1] = Y::channel(warp, lane, 1);
+  }
+  __device__ __forceinline__ void read(const SsmArgs &a, const float *p, int64_t row,
+                                       float (&h)[2][4]) const {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = nl * 4 + j;
+        h[k][j] = (p && ch[k] < nch && n < a.N) ? p[(row * a.D + c0 + ch[k]) * a.N + n] : 0.f;
+      }
+  }
+  __device__ __forceinline__ void write(const SsmArgs &a, float *p, int64_t row,
+                                        const float (&h)[2][4]) const {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = nl * 4 + j;
+        if (ch[k] < nch && n < a.N) p[(row * a.D + c0 + ch[k]) * a.N + n] = h[k][j];
+      }
+  }
+};
+
 template <int LN>
 __device__ __forceinline__ float sum_parts(const float *p) {
   if constexpr (LN == 2) {
@@ -60,14 +103,10 @@ __device__ __forceinline__ float sum_parts(const float *p) {
   }
 }
 
-// Tokens of a range of the scan (a multiple of the tile) for `want` blocks on each SM.
-inline int range_tokens(int64_t T, int64_t ctiles, int tile, int want, int least) {
-  int64_t n = (int64_t)mix::sm_count() * want / (ctiles < 1 ? 1 : ctiles);
-  const int64_t most = ceil_div64(T, least);
-  if (n > most) n = most;
-  if (n < 1) n = 1;
-  const int64_t r = ceil_div64(ceil_div64(T, n), tile) * tile;
-  return (int)(r < tile ? tile : r);
+// Rows that may be read 16 bytes at a time, and B and C two elements at a time.
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline bool rows_ok(const Mat &m, bool f32) {
+  return !m.p || (aligned16(m.p) && m.st % (f32 ? 4 : 8) == 0);
 }
 
 inline int lanes_for(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }

@@ -99,49 +99,6 @@ __device__ __forceinline__ void stm(E *p, const float (&f)[M], int n) {
   }
 }
 
-// What the two passes share: a block's channels and a thread's states.
-template <int LN>
-struct Place {
-  using Y = Lay<LN>;
-  int tid, warp, lane, nl, cl, ct, r, grp, c0, nch;
-  int ch[2];
-  __device__ __forceinline__ Place(const SsmArgs &a, int tiles_per_group) {
-    tid = threadIdx.x;
-    warp = tid >> 5;
-    lane = tid & 31;
-    nl = lane % LN;
-    cl = lane / LN;
-    const int ctiles = tiles_per_group * a.G, Dg = a.D / a.G;
-    ct = blockIdx.x % ctiles;
-    r = blockIdx.x / ctiles;
-    grp = ct / tiles_per_group;
-    c0 = grp * Dg + ct % tiles_per_group * Y::CH;
-    nch = min(Y::CH, (grp + 1) * Dg - c0);
-    ch[0] = Y::channel(warp, lane, 0);
-    ch[1] = Y::channel(warp, lane, 1);
-  }
-  __device__ __forceinline__ void read(const SsmArgs &a, const float *p, int64_t row,
-                                       float (&h)[2][4]) const {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = nl * 4 + j;
-        h[k][j] = (p && ch[k] < nch && n < a.N) ? p[(row * a.D + c0 + ch[k]) * a.N + n] : 0.f;
-      }
-  }
-  __device__ __forceinline__ void write(const SsmArgs &a, float *p, int64_t row,
-                                        const float (&h)[2][4]) const {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = nl * 4 + j;
-        if (ch[k] < nch && n < a.N) p[(row * a.D + c0 + ch[k]) * a.N + n] = h[k][j];
-      }
-  }
-};
-
 // The whole range's segment bounds: marks, and each token's segment.
 struct RangeSegs {
   int mark[kRange + 1], seg[kRange], any;
@@ -733,11 +690,6 @@ cudaError_t run_bwd(const SsmArgs &a, cudaStream_t stream) {
       w.bc, a.T, a.G, a.N, Lay<LN>::NP, tpg, reinterpret_cast<E *>(a.dB),
       reinterpret_cast<E *>(a.dC));
   return cudaGetLastError();
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-bool rows_ok(const Mat &m, bool f32) {
-  return !m.p || (aligned16(m.p) && m.st % (f32 ? 4 : 8) == 0);
 }
 
 template <typename E>
