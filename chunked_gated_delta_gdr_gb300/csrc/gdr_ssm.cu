@@ -13,6 +13,10 @@
 // and keeps the state at its end and the sum of dt (a range's decay is e^{A sum dt}); a short
 // kernel chains these ends over the ranges; pass 2 runs each range from its true state and writes
 // y.  When one range is enough, only pass 2 runs.
+#include <string.h>
+
+#include <type_traits>
+
 #include "gdr_ssm.cuh"
 
 namespace gdr {
@@ -32,24 +36,40 @@ struct Ranges {
 };
 
 // A tile of B (or C) in shared memory as fp32, padded to NP states; read from global memory one
-// tile ahead.
-template <typename E, int LN>
+// tile ahead, two elements at a time (VEC: N and the strides are even, addresses aligned).
+template <typename E, int LN, bool VEC>
 struct BcTile {
-  static constexpr int NP = Lay<LN>::NP, L = Lay<LN>::L, M = (L * NP + kThreads - 1) / kThreads;
-  E v[M];
+  static constexpr int NP = Lay<LN>::NP, L = Lay<LN>::L, M = (L * NP / 2 + kThreads - 1) / kThreads;
+  using Two = typename std::conditional<sizeof(E) == 2, uint32_t, uint2>::type;
+  Two v[M];
   __device__ __forceinline__ void fetch(const E *p, int64_t st, int tb, int t1, int N) {
 #pragma unroll
     for (int q = 0; q < M; ++q) {
-      const int e = threadIdx.x + q * kThreads, t = tb + e / NP, n = e % NP;
-      v[q] = e < L * NP && t < t1 && n < N ? p[t * st + n] : E(0.f);
+      const int e = (threadIdx.x + q * kThreads) * 2, t = tb + e / NP, n = e % NP;
+      const bool row = e < L * NP && t < t1;
+      v[q] = Two{};
+      if (VEC) {
+        if (row && n < N) v[q] = *reinterpret_cast<const Two *>(p + t * st + n);
+      } else {
+        E w[2] = {E(0.f), E(0.f)};
+        if (row && n < N) w[0] = p[t * st + n];
+        if (row && n + 1 < N) w[1] = p[t * st + n + 1];
+        memcpy(&v[q], w, sizeof(Two));
+      }
     }
   }
   __device__ __forceinline__ void put(float *s) const {
 #pragma unroll
     for (int q = 0; q < M; ++q) {
-      const int e = threadIdx.x + q * kThreads;
-      if (e < L * NP) s[e] = ld1(&v[q]);
+      const int e = (threadIdx.x + q * kThreads) * 2;
+      if (e < L * NP) *reinterpret_cast<float2 *>(s + e) = both(v[q]);
     }
+  }
+  static __device__ __forceinline__ float2 both(uint32_t u) {
+    return make_float2(lo_bf(u), hi_bf(u));
+  }
+  static __device__ __forceinline__ float2 both(uint2 u) {
+    return make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
   }
 };
 
@@ -71,7 +91,7 @@ __device__ __forceinline__ void put_pairs(float2 *pair, const float *bias, int s
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float v = softplus ? softplusf(d[i]) : d[i];
-    pair[Lay<LN>::pair_at(lt, lc + i)] = make_float2(v, v * x[i]);
+    pair[Lay<LN>::pair_at(lt, lc) + Lay<LN>::pair_at(0, i)] = make_float2(v, v * x[i]);
   }
 }
 
@@ -104,7 +124,7 @@ __device__ __forceinline__ void tile_tokens(int i0, int i1, F f) {
 template <int LN>
 struct Tile1 {
   using Y = Lay<LN>;
-  float2 pair[Y::L * Y::CH];
+  float2 pair[Y::L * Y::PT];
   float b[Y::L * Y::NP];
   float bias[Y::CH];
   int red[64];
@@ -136,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
   P.read(a, covered && reset ? a.h0 : nullptr, seg, h);
   if (covered) {
     Raw8<E> rx, rd;
-    BcTile<E, LN> rb;
+    BcTile<E, LN, VEC> rb;
     auto fetch = [&](int tb) {
       const int n = tb + lt < t1 ? nv : 0;
       rx = ld8<VEC>(xp + (int64_t)(tb + lt) * a.x.st, n);
@@ -152,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
       __syncthreads();
       tile_tokens<L>(0, min(L, t1 - tb), [&](int i) {
         const float4 d = *reinterpret_cast<const float4 *>(
-            &s.pair[i * CH + Y::pair_slot(i, P.warp, P.cl) * 2]);
+            &s.pair[i * Y::PT + P.pair]);
         const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
         const float dt[2] = {d.x, d.z}, dx[2] = {d.y, d.w}, Bv[4] = {B.x, B.y, B.z, B.w};
 #pragma unroll
@@ -178,9 +198,9 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
 template <int LN>
 struct Tile2 {  // shared memory of one tile of pass 2
   using Y = Lay<LN>;
-  float2 pair[Y::L * Y::CH];  // (dt, dt x)
+  float2 pair[Y::L * Y::PT];  // (dt, dt x)
   float b[Y::L * Y::NP], c[Y::L * Y::NP];
-  float part[Y::L * Y::CH * LN];
+  float part[Y::L * Y::ST];
   float bias[Y::CH], skip[Y::CH];
   int mark[Y::L + 1], seg[Y::L], any, same;
   int red[64];
@@ -216,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
     s.skip[i] = a.Dskip && i < P.nch ? a.Dskip[P.c0 + i] : 0.f;
   }
   Raw8<E> rx, rd, rz = zero8<E>();
-  BcTile<E, LN> rb, rc;
+  BcTile<E, LN, VEC> rb, rc;
   auto fetch = [&](int tb) {
     const int n = tb + lt < t1 ? nv : 0;
     rx = ld8<VEC>(xp + (int64_t)(tb + lt) * a.x.st, n);
@@ -240,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
   auto scan = [&](int i0, int i1) {
     tile_tokens<L>(i0, i1, [&](int i) {
       const float4 d = *reinterpret_cast<const float4 *>(
-          &s.pair[i * CH + Y::pair_slot(i, P.warp, P.cl) * 2]);
+          &s.pair[i * Y::PT + P.pair]);
       const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
       const float4 C = *reinterpret_cast<const float4 *>(&s.c[i * NP + P.nl * 4]);
       const float dt[2] = {d.x, d.z}, dx[2] = {d.y, d.w}, Bv[4] = {B.x, B.y, B.z, B.w};
@@ -249,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           h[k][j] = fmaf(ex2(dt[k] * A2[k][j]), h[k][j], dx[k] * Bv[j]);
-        s.part[po[k] + i * CH * LN] =
+        s.part[po[k] + i * Y::ST] =
             fmaf(h[k][0], C.x, fmaf(h[k][1], C.y, fmaf(h[k][2], C.z, h[k][3] * C.w)));
       }
     });
@@ -310,8 +330,14 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
       float x[8], v[8];
       unpack8(cx, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = fmaf(s.skip[lc + i], x[i], sum_parts<LN>(&s.part[Y::part_at(lt, lc + i)]));
+      for (int i = 0; i < 8; i += 4) {
+        const float4 k = *reinterpret_cast<const float4 *>(&s.skip[lc + i]);
+        const float *part = &s.part[Y::part_at(lt, lc) + i * LN];
+        v[i] = fmaf(k.x, x[i], sum_parts<LN>(part));
+        v[i + 1] = fmaf(k.y, x[i + 1], sum_parts<LN>(part + LN));
+        v[i + 2] = fmaf(k.z, x[i + 2], sum_parts<LN>(part + 2 * LN));
+        v[i + 3] = fmaf(k.w, x[i + 3], sum_parts<LN>(part + 3 * LN));
+      }
       if (zp) {
         unpack8(cz, x);
 #pragma unroll
@@ -511,7 +537,7 @@ size_t ssm_fwd_workspace(int64_t T, int32_t D, int32_t N, int32_t G) {
 cudaError_t launch_ssm_fwd(const SsmArgs &a, cudaStream_t stream) {
   using namespace ssm;
   const bool vec = (a.D / a.G) % 8 == 0 && rows_ok(a.x, a.f32) && rows_ok(a.dt, a.f32) &&
-                   rows_ok(a.z, a.f32) && rows_ok(a.y, a.f32);
+                   rows_ok(a.z, a.f32) && rows_ok(a.y, a.f32) && bc_ok(a);
   return a.f32 ? fwd_by_lanes<float>(a, vec, stream)
                : fwd_by_lanes<__nv_bfloat16>(a, vec, stream);
 }

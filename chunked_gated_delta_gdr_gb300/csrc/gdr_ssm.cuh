@@ -24,23 +24,18 @@ struct Lay {
   static __device__ __forceinline__ int channel(int warp, int lane, int k) {
     return warp * 2 * CW + k * CW + lane / LN;
   }
-  // A token's pairs (two floats for each channel) in shared memory: a thread's two channels are
-  // neighbours, one 16-byte load.  The XOR spreads the stores of 8 neighbouring channels, which
-  // stand 16 bytes apart, over the banks.
-  static __device__ __forceinline__ int pair_slot(int t, int warp, int cl) {
-    const int f = CW >= 8 ? (warp + ((t & 1) << 2)) & 7 : 0;
-    return warp * CW + (cl ^ f);
-  }
-  // index (in float2) of channel ch's pair of token t
+  // A token's pairs (two floats for each channel) in shared memory, in float2: a thread's two
+  // channels are neighbours, one 16-byte load.  Two more pairs behind each warp's channels spread
+  // the stores of a thread's 8 neighbouring channels, and the next token's, over the banks.
+  static constexpr int PW = 2 * CW + 2, PT = 4 * PW;
   static __device__ __forceinline__ int pair_at(int t, int ch) {
-    const int warp = ch / (2 * CW), k = (ch / CW) & 1, cl = ch % CW;
-    return t * CH + pair_slot(t, warp, cl) * 2 + k;
+    return t * PT + ch / (2 * CW) * PW + ch % CW * 2 + (ch / CW & 1);
   }
-  // index of channel ch's LN partial sums of token t; the XOR spreads the reads of a thread's 8
-  // channels
+  // A token's LN partial sums of each channel, in floats: one more place behind every 8 channels
+  // spreads the reads of a thread's 8 channels.
+  static constexpr int ST = (CH + CG) * LN;
   static __device__ __forceinline__ int part_at(int t, int ch) {
-    const int g = ch >> 3;
-    return (t * CH + g * 8 + ((ch & 7) ^ (g & 7))) * LN;
+    return t * ST + (ch + (ch >> 3)) * LN;
   }
 };
 
@@ -50,6 +45,7 @@ struct Place {
   using Y = Lay<LN>;
   int tid, warp, lane, nl, cl, ct, r, grp, c0, nch;
   int ch[2];
+  int pair;  // where this thread's pairs are in a token's row
   __device__ __forceinline__ Place(const SsmArgs &a, int tiles_per_group) {
     tid = threadIdx.x;
     warp = tid >> 5;
@@ -64,6 +60,7 @@ struct Place {
     nch = min(Y::CH, (grp + 1) * Dg - c0);
     ch[0] = Y::channel(warp, lane, 0);
     ch[1] = Y::channel(warp, lane, 1);
+    pair = Y::pair_at(0, ch[0]);
   }
   __device__ __forceinline__ void read(const SsmArgs &a, const float *p, int64_t row,
                                        float (&h)[2][4]) const {
@@ -107,6 +104,12 @@ __device__ __forceinline__ float sum_parts(const float *p) {
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 inline bool rows_ok(const Mat &m, bool f32) {
   return !m.p || (aligned16(m.p) && m.st % (f32 ? 4 : 8) == 0);
+}
+
+inline bool bc_ok(const SsmArgs &a) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.B) | reinterpret_cast<uintptr_t>(a.C);
+  return a.N % 2 == 0 && a.B_st % 2 == 0 && a.B_sg % 2 == 0 && a.C_st % 2 == 0 &&
+         a.C_sg % 2 == 0 && (at & (a.f32 ? 7 : 3)) == 0;
 }
 
 inline int lanes_for(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }

@@ -132,8 +132,8 @@ __device__ __forceinline__ void range_segments(const SsmArgs &a, int t0, int n, 
 template <int LN>
 struct Tile1 {
   using Y = Lay<LN>;
-  float2 pair[Y::L * Y::CH];
-  float dy[Y::L * Y::CH];
+  float2 pair[Y::L * Y::PT];
+  float dy[Y::L * Y::PT];
   float b[Y::L * Y::NP], c[Y::L * Y::NP];
   RangeSegs s;
 };
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads)
     auto scan = [&](int from, int to) {
 #pragma unroll 4
       for (int i = from; i < to; ++i) {
-        const int at = i * CH + Y::pair_slot(i, P.warp, P.cl) * 2;
+        const int at = i * Y::PT + P.pair;
         const float4 q = *reinterpret_cast<const float4 *>(&s.pair[at]);
         const float2 dyv = *reinterpret_cast<const float2 *>(&s.dy[at]);
         const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
@@ -290,10 +290,10 @@ template <int LN>
 struct Tile2 {
   using Y = Lay<LN>;
   float4 kept[kRange / kBT][2][kThreads];  // the state before each tile
-  float2 pair[kBT * Y::CH];                // (dt, dt x)
-  float dy[kBT * Y::CH];
+  float2 pair[kBT * Y::PT];                // (dt, dt x)
+  float dy[kBT * Y::PT];
   float b[kBT * Y::NP], c[kBT * Y::NP];
-  float pp[kBT * Y::CH * LN], pc[kBT * Y::CH * LN], py[kBT * Y::CH * LN];
+  float pp[kBT * Y::ST], pc[kBT * Y::ST], py[kBT * Y::ST];
   float red[kThreads / 32][kBT][2 * Y::NP];
   RangeSegs s;
 };
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     for (int i = 0; i < kBT; ++i) {
       if (marks && s.s.mark[i0 + i] >= 0) start_state(s.s.mark[i0 + i], h);
       const float4 v = *reinterpret_cast<const float4 *>(
-          &s.pair[i * CH + Y::pair_slot(i, P.warp, P.cl) * 2]);
+          &s.pair[i * Y::PT + P.pair]);
       const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
       const float dt[2] = {v.x, v.z}, dx[2] = {v.y, v.w}, Bv[4] = {B.x, B.y, B.z, B.w};
 #pragma unroll
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     for (int i = 0; i < kBT; ++i) {
       if (marks && i0 + i < n && s.s.mark[i0 + i] >= 0) start_state(s.s.mark[i0 + i], h);
       const float4 v = *reinterpret_cast<const float4 *>(
-          &s.pair[i * CH + Y::pair_slot(i, P.warp, P.cl) * 2]);
+          &s.pair[i * Y::PT + P.pair]);
       const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
       const float dt[2] = {v.x, v.z}, dx[2] = {v.y, v.w}, Bv[4] = {B.x, B.y, B.z, B.w};
 #pragma unroll
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
 #pragma unroll
     for (int i = kBT - 1; i >= 0; --i) {
-      const int at = i * CH + Y::pair_slot(i, P.warp, P.cl) * 2;
+      const int at = i * Y::PT + P.pair;
       const float4 v = *reinterpret_cast<const float4 *>(&s.pair[at]);
       const float2 dyv = *reinterpret_cast<const float2 *>(&s.dy[at]);
       const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
