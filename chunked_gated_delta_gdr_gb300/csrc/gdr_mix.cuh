@@ -410,6 +410,7 @@ cudaError_t launch_conv_step(const ConvStepArgs &a, cudaStream_t stream);
 struct SsmArgs {
   int32_t T, D, N, G, n_seq, softplus;
   bool f32;
+  bool n4;  // states in fours, 16-byte aligned (set by the launchers)
   const int32_t *cu;
   Mat x, dt, z, y;
   const void *B, *C;

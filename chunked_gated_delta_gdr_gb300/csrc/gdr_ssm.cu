@@ -13,10 +13,6 @@
 // and keeps the state at its end and the sum of dt (a range's decay is e^{A sum dt}); a short
 // kernel chains these ends over the ranges; pass 2 runs each range from its true state and writes
 // y.  When one range is enough, only pass 2 runs.
-#include <string.h>
-
-#include <type_traits>
-
 #include "gdr_ssm.cuh"
 
 namespace gdr {
@@ -34,92 +30,6 @@ struct Ranges {
   float *sum;        // [n][D]: sum of dt from the last segment start in the range (or its start)
   int *reset;        // [n]: a segment starts in the range
 };
-
-// A tile of B (or C) in shared memory as fp32, padded to NP states; read from global memory one
-// tile ahead, two elements at a time (VEC: N and the strides are even, addresses aligned).
-template <typename E, int LN, bool VEC>
-struct BcTile {
-  static constexpr int NP = Lay<LN>::NP, L = Lay<LN>::L, M = (L * NP / 2 + kThreads - 1) / kThreads;
-  using Two = typename std::conditional<sizeof(E) == 2, uint32_t, uint2>::type;
-  Two v[M];
-  __device__ __forceinline__ void fetch(const E *p, int64_t st, int tb, int t1, int N) {
-#pragma unroll
-    for (int q = 0; q < M; ++q) {
-      const int e = (threadIdx.x + q * kThreads) * 2, t = tb + e / NP, n = e % NP;
-      const bool row = e < L * NP && t < t1;
-      v[q] = Two{};
-      if (VEC) {
-        if (row && n < N) v[q] = *reinterpret_cast<const Two *>(p + t * st + n);
-      } else {
-        E w[2] = {E(0.f), E(0.f)};
-        if (row && n < N) w[0] = p[t * st + n];
-        if (row && n + 1 < N) w[1] = p[t * st + n + 1];
-        memcpy(&v[q], w, sizeof(Two));
-      }
-    }
-  }
-  __device__ __forceinline__ void put(float *s) const {
-#pragma unroll
-    for (int q = 0; q < M; ++q) {
-      const int e = (threadIdx.x + q * kThreads) * 2;
-      if (e < L * NP) *reinterpret_cast<float2 *>(s + e) = both(v[q]);
-    }
-  }
-  static __device__ __forceinline__ float2 both(uint32_t u) {
-    return make_float2(lo_bf(u), hi_bf(u));
-  }
-  static __device__ __forceinline__ float2 both(uint2 u) {
-    return make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
-  }
-};
-
-// (dt, dt x) of a thread's 8 elements of a tile.
-template <typename E, int LN>
-__device__ __forceinline__ void put_pairs(float2 *pair, const float *bias, int softplus, int lt,
-                                          int lc, const Raw8<E> &rx, const Raw8<E> &rd) {
-  float x[8], d[8];
-  unpack8(rx, x);
-  unpack8(rd, d);
-#pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    const float4 b = *reinterpret_cast<const float4 *>(bias + lc + i);
-    d[i] += b.x;
-    d[i + 1] += b.y;
-    d[i + 2] += b.z;
-    d[i + 3] += b.w;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = softplus ? softplusf(d[i]) : d[i];
-    pair[Lay<LN>::pair_at(lt, lc) + Lay<LN>::pair_at(0, i)] = make_float2(v, v * x[i]);
-  }
-}
-
-template <int LN>
-__device__ __forceinline__ void load_decays(const SsmArgs &a, const Place<LN> &P,
-                                            float (&A2)[2][4]) {
-  P.read(a, a.A, 0, A2);
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) A2[k][j] *= kLog2e;
-}
-
-// Calls f(i) for tokens [i0, i1) of a tile; a whole tile is unrolled, so that its addresses are
-// constants.
-template <int L, typename F>
-__device__ __forceinline__ void tile_tokens(int i0, int i1, F f) {
-  constexpr int U = L < 16 ? L : 16;
-  if (i1 - i0 == L) {
-#pragma unroll 1
-    for (int i = 0; i < L; i += U)
-#pragma unroll
-      for (int u = 0; u < U; ++u) f(i + u);
-  } else {
-#pragma unroll 2
-    for (int i = i0; i < i1; ++i) f(i);
-  }
-}
 
 template <int LN>
 struct Tile1 {
@@ -148,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
   for (int i = P.tid; i < CH; i += kThreads)
     s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
   float A2[2][4], h[2][4], S[2] = {0.f, 0.f};
-  load_decays(a, P, A2);
+  P.decays(a, A2);
   const SegCursor c = seg_find(a.cu, a.n_seq, a.T, t1, s.red);
   const int seg = c.j - 1;
   const bool covered = seg >= 0 && seg < a.n_seq, reset = seg >= 0 && c.b >= r0;
@@ -156,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
   P.read(a, covered && reset ? a.h0 : nullptr, seg, h);
   if (covered) {
     Raw8<E> rx, rd;
-    BcTile<E, LN, VEC> rb;
+    BcTile<E, NP, L, VEC> rb;
     auto fetch = [&](int tb) {
       const int n = tb + lt < t1 ? nv : 0;
       rx = ld8<VEC>(xp + (int64_t)(tb + lt) * a.x.st, n);
@@ -236,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
     s.skip[i] = a.Dskip && i < P.nch ? a.Dskip[P.c0 + i] : 0.f;
   }
   Raw8<E> rx, rd, rz = zero8<E>();
-  BcTile<E, LN, VEC> rb, rc;
+  BcTile<E, NP, L, VEC> rb, rc;
   auto fetch = [&](int tb) {
     const int n = tb + lt < t1 ? nv : 0;
     rx = ld8<VEC>(xp + (int64_t)(tb + lt) * a.x.st, n);
@@ -247,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
   };
   fetch(t0);
   float A2[2][4], h[2][4];
-  load_decays(a, P, A2);
+  P.decays(a, A2);
   SegCursor cursor = seg_find(a.cu, a.n_seq, a.T, t0, s.red);
   int seg = cursor.j - 1;
   P.read(a, P.r > 0 && seg >= 0 && seg < a.n_seq ? rg.state : nullptr, P.r, h);
@@ -534,8 +444,10 @@ size_t ssm_fwd_workspace(int64_t T, int32_t D, int32_t N, int32_t G) {
   return ssm::carve(nullptr, T, D, N, ssm::range_for(T, D, N, G)).bytes;
 }
 
-cudaError_t launch_ssm_fwd(const SsmArgs &a, cudaStream_t stream) {
+cudaError_t launch_ssm_fwd(const SsmArgs &args, cudaStream_t stream) {
   using namespace ssm;
+  SsmArgs a = args;
+  a.n4 = states_ok(a);
   const bool vec = (a.D / a.G) % 8 == 0 && rows_ok(a.x, a.f32) && rows_ok(a.dt, a.f32) &&
                    rows_ok(a.z, a.f32) && rows_ok(a.y, a.f32) && bc_ok(a);
   return a.f32 ? fwd_by_lanes<float>(a, vec, stream)

@@ -5,6 +5,10 @@
 // that a token's B and C, read from shared memory, serve 8 states.
 #pragma once
 
+#include <string.h>
+
+#include <type_traits>
+
 #include "gdr_mix.cuh"
 
 namespace gdr {
@@ -62,25 +66,48 @@ struct Place {
     ch[1] = Y::channel(warp, lane, 1);
     pair = Y::pair_at(0, ch[0]);
   }
+  // h = the states of this row of p [rows, D, N], zeros where p is null; and back
   __device__ __forceinline__ void read(const SsmArgs &a, const float *p, int64_t row,
                                        float (&h)[2][4]) const {
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k) {
+      const float *q = p + ((row * a.D + c0 + ch[k]) * a.N + nl * 4);
+      const bool in = p && ch[k] < nch;
+      if (a.n4) {
+        const float4 v = in && nl * 4 < a.N ? *reinterpret_cast<const float4 *>(q)
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+        h[k][0] = v.x;
+        h[k][1] = v.y;
+        h[k][2] = v.z;
+        h[k][3] = v.w;
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = nl * 4 + j;
-        h[k][j] = (p && ch[k] < nch && n < a.N) ? p[(row * a.D + c0 + ch[k]) * a.N + n] : 0.f;
+        for (int j = 0; j < 4; ++j) h[k][j] = in && nl * 4 + j < a.N ? q[j] : 0.f;
       }
+    }
   }
   __device__ __forceinline__ void write(const SsmArgs &a, float *p, int64_t row,
                                         const float (&h)[2][4]) const {
 #pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float *q = p + ((row * a.D + c0 + ch[k]) * a.N + nl * 4);
+      if (ch[k] >= nch) continue;
+      if (a.n4) {
+        if (nl * 4 < a.N)
+          *reinterpret_cast<float4 *>(q) = make_float4(h[k][0], h[k][1], h[k][2], h[k][3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (nl * 4 + j < a.N) q[j] = h[k][j];
+      }
+    }
+  }
+  __device__ __forceinline__ void decays(const SsmArgs &a, float (&A2)[2][4]) const {
+    read(a, a.A, 0, A2);
+#pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = nl * 4 + j;
-        if (ch[k] < nch && n < a.N) p[(row * a.D + c0 + ch[k]) * a.N + n] = h[k][j];
-      }
+      for (int j = 0; j < 4; ++j) A2[k][j] *= mix::kLog2e;
   }
 };
 
@@ -100,6 +127,82 @@ __device__ __forceinline__ float sum_parts(const float *p) {
   }
 }
 
+// A tile of B (or C) in shared memory as fp32, padded to NP states; read from global memory one
+// tile ahead, two elements at a time (VEC: N and the strides are even, addresses aligned).
+template <typename E, int NP, int L, bool VEC>
+struct BcTile {
+  static constexpr int M = (L * NP / 2 + kThreads - 1) / kThreads;
+  using Two = typename std::conditional<sizeof(E) == 2, uint32_t, uint2>::type;
+  Two v[M];
+  __device__ __forceinline__ void fetch(const E *p, int64_t st, int tb, int t1, int N) {
+#pragma unroll
+    for (int q = 0; q < M; ++q) {
+      const int e = (threadIdx.x + q * kThreads) * 2, t = tb + e / NP, n = e % NP;
+      const bool row = e < L * NP && t < t1;
+      v[q] = Two{};
+      if (VEC) {
+        if (row && n < N) v[q] = *reinterpret_cast<const Two *>(p + t * st + n);
+      } else {
+        E w[2] = {E(0.f), E(0.f)};
+        if (row && n < N) w[0] = p[t * st + n];
+        if (row && n + 1 < N) w[1] = p[t * st + n + 1];
+        memcpy(&v[q], w, sizeof(Two));
+      }
+    }
+  }
+  __device__ __forceinline__ void put(float *s) const {
+#pragma unroll
+    for (int q = 0; q < M; ++q) {
+      const int e = (threadIdx.x + q * kThreads) * 2;
+      if (e < L * NP) *reinterpret_cast<float2 *>(s + e) = both(v[q]);
+    }
+  }
+  static __device__ __forceinline__ float2 both(uint32_t u) {
+    return make_float2(mix::lo_bf(u), mix::hi_bf(u));
+  }
+  static __device__ __forceinline__ float2 both(uint2 u) {
+    return make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+  }
+};
+
+// (dt, dt x) of a thread's 8 elements of a tile.
+template <typename E, int LN>
+__device__ __forceinline__ void put_pairs(float2 *pair, const float *bias, int softplus, int lt,
+                                          int lc, const mix::Raw8<E> &rx, const mix::Raw8<E> &rd) {
+  float x[8], d[8];
+  mix::unpack8(rx, x);
+  mix::unpack8(rd, d);
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    const float4 b = *reinterpret_cast<const float4 *>(bias + lc + i);
+    d[i] += b.x;
+    d[i + 1] += b.y;
+    d[i + 2] += b.z;
+    d[i + 3] += b.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = softplus ? mix::softplusf(d[i]) : d[i];
+    pair[Lay<LN>::pair_at(lt, lc) + Lay<LN>::pair_at(0, i)] = make_float2(v, v * x[i]);
+  }
+}
+
+// Calls f(i) for tokens [i0, i1) of a tile; a whole tile is unrolled, so that its addresses are
+// constants.
+template <int L, typename F>
+__device__ __forceinline__ void tile_tokens(int i0, int i1, F f) {
+  constexpr int U = L < 16 ? L : 16;
+  if (i1 - i0 == L) {
+#pragma unroll 1
+    for (int i = 0; i < L; i += U)
+#pragma unroll
+      for (int u = 0; u < U; ++u) f(i + u);
+  } else {
+#pragma unroll 2
+    for (int i = i0; i < i1; ++i) f(i);
+  }
+}
+
 // Rows that may be read 16 bytes at a time, and B and C two elements at a time.
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 inline bool rows_ok(const Mat &m, bool f32) {
@@ -110,6 +213,11 @@ inline bool bc_ok(const SsmArgs &a) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.B) | reinterpret_cast<uintptr_t>(a.C);
   return a.N % 2 == 0 && a.B_st % 2 == 0 && a.B_sg % 2 == 0 && a.C_st % 2 == 0 &&
          a.C_sg % 2 == 0 && (at & (a.f32 ? 7 : 3)) == 0;
+}
+
+inline bool states_ok(const SsmArgs &a) {
+  return a.N % 4 == 0 && aligned16(a.A) && aligned16(a.h0) && aligned16(a.ht) &&
+         aligned16(a.dht) && aligned16(a.dh0);
 }
 
 inline int lanes_for(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }

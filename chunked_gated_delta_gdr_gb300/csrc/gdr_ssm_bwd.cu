@@ -7,18 +7,24 @@
 //   dx = dt p + D dy,   ddt = (x p + sum_n A c_t) sigmoid(raw),   dA = sum_t dt c_t,
 //   dD = sum_t dy x,   dz = dout y (z sigmoid(z))',   dh0 = a g at the segment's first token.
 //
-// The token axis is cut into ranges as in the forward.  Pass 1 runs each range once, forwards,
-// from a zero state: it keeps the state at its end and, with the running product of the a, the
-// gradient that its own tokens send to the state before it.  A short kernel chains both over the
-// ranges.  Pass 2 then has a range's true state at its start and true gradient at its end: it
-// sweeps forwards keeping the state before every tile of 8 tokens in shared memory, then takes the
-// tiles last to first, recomputes a tile's states into registers and walks back through them.
+// The token axis is cut into ranges of 128 tokens.  Pass 1 runs each range once, forwards, from a
+// zero state: it keeps the state at its end and, with the running product of the a, the gradient
+// that its own tokens send to the state before it.  A short kernel chains both over the ranges.
+// Pass 2 then has a range's true state at its start and true gradient at its end.  It takes the
+// range in tiles of up to 8 tokens of one segment: a sweep forwards keeps the state before every
+// tile that continues a segment, then the tiles go last to first, each recomputing its states into
+// registers and walking back through them.  The kept states (8 fp32 a thread and tile) live in
+// Tensor Memory, 128 columns a block, each thread reading back its own lane: in shared memory they
+// would leave room for 2 blocks on an SM instead of 3.
+//
 // Sums over states (p, c A, y) are left as partial sums of LN lanes in shared memory; sums over
 // channels (dB, dC) go over the warp's lanes by a transposing butterfly, over its warps in shared
 // memory and over the blocks in a last kernel, always in the same order.
 //
-// About 16 products and 3 exponentials for each token, channel and state: bound by the fp32 pipes.
+// About 16 products and 3 exponentials for each token, channel and state in pass 2, and 6 and 1 in
+// pass 1: bound by instruction issue.
 #include "gdr_ssm.cuh"
+#include "gdr_tc.cuh"
 
 namespace gdr {
 namespace ssm {
@@ -27,8 +33,10 @@ namespace {
 using namespace mix;
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kBT = 8;       // tokens of a tile of pass 2
-constexpr int kRange = 64;   // tokens of a range
+constexpr int kBT = 8;        // tokens of a tile of pass 2
+constexpr int kRange = 128;   // tokens of a range
+constexpr int kKept = kRange / kBT;  // states kept at most: tiles that continue a segment
+constexpr uint32_t kCols = 8 * kKept;  // Tensor Memory columns for them
 
 struct BwdWork {
   int n;            // ranges
@@ -101,32 +109,50 @@ __device__ __forceinline__ void stm(E *p, const float (&f)[M], int n) {
 
 // The whole range's segment bounds: marks, and each token's segment.
 struct RangeSegs {
-  int mark[kRange + 1], seg[kRange], any;
+  int mark[kRange + 1], seg[kRange];
   int red[64];
 };
+__device__ __forceinline__ int warp_max_scan(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v = max(v, u);
+  }
+  return v;
+}
+// All threads; only the first warp has filled s on return.
 __device__ __forceinline__ void range_segments(const SsmArgs &a, int t0, int n, RangeSegs &s) {
   SegCursor c = seg_find(a.cu, a.n_seq, a.T, t0, s.red);
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int base = c.j - 1;
-    const bool any = seg_marks(a.cu, a.n_seq, a.T, t0, n, s.mark, c);
-    if (!any)
+    if (!seg_marks(a.cu, a.n_seq, a.T, t0, n, s.mark, c))
       for (int i = lane; i <= n; i += 32) s.mark[i] = -1;
     __syncwarp();
     for (int i0 = 0; i0 < n; i0 += 32) {
-      int v = i0 + lane < n ? s.mark[i0 + lane] : -1;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v = max(v, u);
-      }
-      v = max(v, base);
+      const int v = max(warp_max_scan(i0 + lane < n ? s.mark[i0 + lane] : -1, lane), base);
       if (i0 + lane < n) s.seg[i0 + lane] = v;
       base = __shfl_sync(0xffffffffu, v, 31);
     }
-    if (lane == 0) s.any = any;
+    __syncwarp();
   }
-  __syncthreads();
+}
+// The first warp: cuts the range into tiles of up to kBT tokens that cross no bound; tile q is
+// tokens at[q] .. at[q + 1] - 1.  Returns their number.
+__device__ __forceinline__ int range_tiles(int n, const RangeSegs &s, int *at) {
+  const int lane = threadIdx.x;
+  int base = 0, count = 0;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    const int run = max(warp_max_scan(i < n && s.mark[i] >= 0 ? i : 0, lane), base);
+    base = __shfl_sync(0xffffffffu, run, 31);
+    const bool first = i < n && (i - run) % kBT == 0;
+    const unsigned m = __ballot_sync(0xffffffffu, first);
+    if (first) at[count + __popc(m & ((1u << lane) - 1))] = i;
+    count += __popc(m);
+  }
+  if (lane == 0) at[count] = n;
+  return count;
 }
 
 template <int LN>
@@ -135,64 +161,71 @@ struct Tile1 {
   float2 pair[Y::L * Y::PT];
   float dy[Y::L * Y::PT];
   float b[Y::L * Y::NP], c[Y::L * Y::NP];
+  float bias[Y::CH];
   RangeSegs s;
 };
 
 // Pass 1.
 template <typename E, int LN, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     k_ssm_bwd_ends(const SsmArgs a, const BwdWork w, int tiles_per_group) {
   using Y = Lay<LN>;
-  constexpr int L = Y::L, NP = Y::NP, CH = Y::CH;
+  constexpr int L = Y::L, NP = Y::NP;
   extern __shared__ __align__(16) char smem_raw[];
   Tile1<LN> &s = *reinterpret_cast<Tile1<LN> *>(smem_raw);
   const Place<LN> P(a, tiles_per_group);
   const int t0 = P.r * kRange, n = min(kRange, a.T - t0);
+  const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
+  const int64_t c = P.c0 + lc;
+  const E *xp = reinterpret_cast<const E *>(a.x.p) + c, *dp = reinterpret_cast<const E *>(a.dt.p) + c;
+  const E *gp = reinterpret_cast<const E *>(a.dout.p) + c;
+  const E *zp = a.z.p ? reinterpret_cast<const E *>(a.z.p) + c : nullptr;
+  const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
+  const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
+  Raw8<E> rx, rd, rg, rz = zero8<E>();
+  BcTile<E, NP, L, VEC> rb, rc;
+  auto fetch = [&](int i0) {
+    const int m = i0 + lt < n ? nv : 0;
+    const int64_t t = t0 + i0 + lt;
+    rx = ld8<VEC>(xp + t * a.x.st, m);
+    rd = ld8<VEC>(dp + t * a.dt.st, m);
+    rg = ld8<VEC>(gp + t * a.dout.st, m);
+    if (zp) rz = ld8<VEC>(zp + t * a.z.st, m);
+    rb.fetch(Bp, a.B_st, t0 + i0, t0 + n, a.N);
+    rc.fetch(Cp, a.C_st, t0 + i0, t0 + n, a.N);
+  };
+  fetch(0);
+  for (int i = P.tid; i < Y::CH; i += kThreads)
+    s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
   float A2[2][4], h[2][4], pr[2][4], gs[2][4], S[2] = {0.f, 0.f};
-  P.read(a, a.A, 0, A2);
+  P.decays(a, A2);
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      A2[k][j] *= kLog2e;
       h[k][j] = gs[k][j] = 0.f;
       pr[k][j] = 1.f;
     }
-  const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
-  const int64_t c = P.c0 + lc;
-  const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
-  const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
   range_segments(a, t0, n, s.s);
-  bool reset = false, active = true;
-  int seg = -1;
+  __syncthreads();
+  bool reset = false;  // a segment has started: nothing from here on reaches the state before
   for (int i0 = 0; i0 < n; i0 += L) {
-    const int m = min(L, n - i0), t = t0 + i0 + lt;
-    const int sg = lt < m ? s.s.seg[i0 + lt] : -1;
-    const int ok = sg >= 0 && sg < a.n_seq ? nv : 0;
-    float x[8], d[8], g[8], z[8];
-    unpack8(ld8<VEC>(reinterpret_cast<const E *>(a.x.p) + t * a.x.st + c, ok), x);
-    unpack8(ld8<VEC>(reinterpret_cast<const E *>(a.dt.p) + t * a.dt.st + c, ok), d);
-    unpack8(ld8<VEC>(reinterpret_cast<const E *>(a.dout.p) + t * a.dout.st + c, ok), g);
-    if (a.z.p) unpack8(ld8<VEC>(reinterpret_cast<const E *>(a.z.p) + t * a.z.st + c, ok), z);
+    const int m = min(L, n - i0);
+    put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, rx, rd);
+    {
+      float g[8], z[8];
+      unpack8(rg, g);
+      unpack8(rz, z);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v = d[i] + ((a.dt_bias && i < nv) ? a.dt_bias[c + i] : 0.f);
-      if (a.softplus) v = softplusf(v);
-      if (a.z.p) g[i] *= z[i] * sigmoidf(z[i]);
-      const int at = Y::pair_at(lt, lc + i);
-      s.pair[at] = make_float2(v, v * x[i]);
-      s.dy[at] = g[i];
+      for (int i = 0; i < 8; ++i)
+        s.dy[Y::pair_at(lt, lc) + Y::pair_at(0, i)] = zp ? g[i] * z[i] * sigmoidf(z[i]) : g[i];
     }
-    for (int e = P.tid; e < L * NP; e += kThreads) {
-      const int i = e / NP, q = e % NP;
-      const bool in = i < m && q < a.N && s.s.seg[i0 + i] >= 0 && s.s.seg[i0 + i] < a.n_seq;
-      s.b[e] = in ? ld1(Bp + (int64_t)(t0 + i0 + i) * a.B_st + q) : 0.f;
-      s.c[e] = in ? ld1(Cp + (int64_t)(t0 + i0 + i) * a.C_st + q) : 0.f;
-    }
+    rb.put(s.b);
+    rc.put(s.c);
+    if (i0 + L < n) fetch(i0 + L);
     __syncthreads();
     auto scan = [&](int from, int to) {
-#pragma unroll 4
-      for (int i = from; i < to; ++i) {
+      tile_tokens<L>(from, to, [&](int i) {
         const int at = i * Y::PT + P.pair;
         const float4 q = *reinterpret_cast<const float4 *>(&s.pair[at]);
         const float2 dyv = *reinterpret_cast<const float2 *>(&s.dy[at]);
@@ -211,7 +244,7 @@ __global__ void __launch_bounds__(kThreads)
             gs[k][j] = fmaf(pr[k][j], Cv[j] * dy[k], gs[k][j]);
           }
         }
-      }
+      });
     };
     for (int i = 0; i < m;) {
       if (s.s.mark[i0 + i] >= 0) {
@@ -219,20 +252,17 @@ __global__ void __launch_bounds__(kThreads)
         P.read(a, next < a.n_seq ? a.h0 : nullptr, next, h);
         S[0] = S[1] = 0.f;
         reset = true;
-        if (active) {  // nothing from here on reaches the state before the range
-          active = false;
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) pr[k][j] = 0.f;
-        }
+          for (int j = 0; j < 4; ++j) pr[k][j] = 0.f;
       }
       int e = i + 1;
       while (e < m && s.s.mark[i0 + e] < 0) ++e;
-      seg = s.s.seg[i0 + i];
+      const int seg = s.s.seg[i0 + i];
       if (seg >= 0 && seg < a.n_seq) {
         scan(i, e);
-        if (active && s.s.mark[i0 + e] >= 0 && a.dht) {
+        if (!reset && s.s.mark[i0 + e] >= 0 && a.dht) {
           float f[2][4];
           P.read(a, a.dht, seg, f);
 #pragma unroll
@@ -261,7 +291,7 @@ __global__ void k_ssm_bwd_chain(const float *A, const BwdWork w, int D, int N) {
   if (i >= size) return;
   const float A2 = A[i] * kLog2e;
   const int d = (int)(i / N);
-  constexpr int U = 8;
+  constexpr int U = 16;
   const bool back = blockIdx.y != 0;
   float *val = back ? w.grad : w.state;
   float cur = 0.f;
@@ -289,14 +319,35 @@ __global__ void k_ssm_bwd_chain(const float *A, const BwdWork w, int D, int N) {
 template <int LN>
 struct Tile2 {
   using Y = Lay<LN>;
-  float4 kept[kRange / kBT][2][kThreads];  // the state before each tile
   float2 pair[kBT * Y::PT];                // (dt, dt x)
   float dy[kBT * Y::PT];
   float b[kBT * Y::NP], c[kBT * Y::NP];
   float pp[kBT * Y::ST], pc[kBT * Y::ST], py[kBT * Y::ST];
   float red[kThreads / 32][kBT][2 * Y::NP];
+  float bias[Y::CH], skip[Y::CH];
   RangeSegs s;
+  int at[kRange + 1], tiles;
+  uint32_t tmem;
 };
+
+// 8 of a thread's own fp32 values in its lane of Tensor Memory.  Whole warps.
+__device__ __forceinline__ void keep8(uint32_t addr, const float (&h)[2][4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+               "f"(h[0][0]), "f"(h[0][1]), "f"(h[0][2]), "f"(h[0][3]), "f"(h[1][0]), "f"(h[1][1]),
+               "f"(h[1][2]), "f"(h[1][3])
+               : "memory");
+}
+__device__ __forceinline__ void kept8(uint32_t addr, float (&h)[2][4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(h[0][0]), "=f"(h[0][1]), "=f"(h[0][2]), "=f"(h[0][3]), "=f"(h[1][0]),
+                 "=f"(h[1][1]), "=f"(h[1][2]), "=f"(h[1][3])
+               : "r"(addr)
+               : "memory");
+  // the values are tied to the wait, so that no use moves before it
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(h[0][0]), "+f"(h[0][1]), "+f"(h[0][2]), "+f"(h[0][3]), "+f"(h[1][0]),
+                 "+f"(h[1][1]), "+f"(h[1][2]), "+f"(h[1][3])::"memory");
+}
 
 // Sums v[0..3] (dB) and v[4..7] (dC) over the lanes that hold the same states; each lane is left
 // with 8 / CW of the sums, the first being number `first`.
@@ -339,150 +390,141 @@ __global__ void __launch_bounds__(kThreads, 3)
     });
     return;
   }
-  const int t0 = P.r * kRange, n = min(kRange, a.T - t0), tiles = (n + kBT - 1) / kBT;
-  float A2[2][4], h[2][4], g[2][4], dA[2][4];
-  P.read(a, a.A, 0, A2);
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      A2[k][j] *= kLog2e;
-      dA[k][j] = 0.f;
-    }
+  if (P.warp == 0) {
+    tc::tmem_alloc(&s.tmem, kCols);
+    tc::tmem_relinquish();
+  }
+  const int t0 = P.r * kRange, n = min(kRange, a.T - t0);
   const int lt = P.tid / (CH / M), lc = P.tid % (CH / M) * M, nv = max(0, min(M, P.nch - lc));
   const int64_t c = P.c0 + lc;
-  const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
-  const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
-  float bias[M], skip[M], sd[M], sb[M];
-#pragma unroll
-  for (int i = 0; i < M; ++i) {
-    bias[i] = (a.dt_bias && i < nv) ? a.dt_bias[c + i] : 0.f;
-    skip[i] = (a.Dskip && i < nv) ? a.Dskip[c + i] : 0.f;
-    sd[i] = sb[i] = 0.f;
-  }
-  range_segments(a, t0, n, s.s);
-  const bool marks = s.s.any;
-  auto covered = [&](int i) { return i < n && s.s.seg[i] >= 0 && s.s.seg[i] < a.n_seq; };
-  auto clear = [&](float (&v)[2][4]) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[k][j] = 0.f;
-  };
-  auto start_state = [&](int seg, float (&v)[2][4]) {
-    P.read(a, seg < a.n_seq ? a.h0 : nullptr, seg, v);
-  };
-  auto end_grad = [&](int i, float (&v)[2][4]) {  // token i is the last of its segment
-    P.read(a, covered(i) ? a.dht : nullptr, s.s.seg[i], v);
-  };
   const E *xp = reinterpret_cast<const E *>(a.x.p) + c, *dp = reinterpret_cast<const E *>(a.dt.p) + c;
   const E *gp = reinterpret_cast<const E *>(a.dout.p) + c;
   const E *zp = a.z.p ? reinterpret_cast<const E *>(a.z.p) + c : nullptr;
+  const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
+  const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
+  for (int i = P.tid; i < CH; i += kThreads) {
+    s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
+    s.skip[i] = a.Dskip && i < P.nch ? a.Dskip[P.c0 + i] : 0.f;
+  }
+  float A2[2][4], h[2][4];
+  P.decays(a, A2);
+  range_segments(a, t0, n, s.s);
+  if (P.warp == 0) {
+    const int tiles = range_tiles(n, s.s, s.at);
+    if (P.lane == 0) s.tiles = tiles;
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t kept = s.tmem + ((uint32_t)(P.warp * 32) << 16);
+  const int tiles = s.tiles;
+  auto covered = [&](int i) { return s.s.seg[i] >= 0 && s.s.seg[i] < a.n_seq; };
+  auto starts = [&](int q) { return s.s.mark[s.at[q]] >= 0; };
 
-  // a token without a segment, and one past the end, is neutral: dt, dt x, dy = 0
-  auto put_pairs = [&](const Elems<E, M> &x, const Elems<E, M> &d, bool in) {
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
-      float v = ld1(&d.v[i]) + bias[i];
-      if (a.softplus) v = softplusf(v);
-      s.pair[Y::pair_at(lt, lc + i)] =
-          in ? make_float2(v, v * ld1(&x.v[i])) : make_float2(0.f, 0.f);
+  Elems<E, M> rx, rd, rg, rz;
+  BcTile<E, NP, kBT, VEC> rb, rc;
+  // a tile's elements; a token without a segment, and one past the tile, is neutral: zeros
+  auto fetch = [&](int q, bool all) {
+    const int i0 = s.at[q], m = s.at[q + 1] - i0, live = covered(i0) ? m : 0;
+    const int64_t t = t0 + i0 + lt;
+    const int k = lt < live ? nv : 0;
+    rx = ldm<VEC, E, M>(xp + t * a.x.st, k);
+    rd = ldm<VEC, E, M>(dp + t * a.dt.st, k);
+    rb.fetch(Bp, a.B_st, t0 + i0, t0 + i0 + live, a.N);
+    if (all) {
+      rg = ldm<VEC, E, M>(gp + t * a.dout.st, k);
+      if (zp) rz = ldm<VEC, E, M>(zp + t * a.z.st, k);
+      rc.fetch(Cp, a.C_st, t0 + i0, t0 + i0 + live, a.N);
     }
   };
-
-  // the sweep: states before each tile
-  if (w.n > 1 && P.r > 0 && covered(0) && s.s.mark[0] < 0)
-    P.read(a, w.state, P.r, h);
-  else
-    clear(h);
-  for (int q = 0; q < tiles; ++q) {
-    s.kept[q][0][P.tid] = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
-    s.kept[q][1][P.tid] = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
-    if (q + 1 == tiles) break;
-    const int i0 = q * kBT, t = t0 + i0 + lt;
-    const bool in = covered(i0 + lt);
-    put_pairs(ldm<VEC, E, M>(xp + t * a.x.st, in ? nv : 0),
-              ldm<VEC, E, M>(dp + t * a.dt.st, in ? nv : 0), in);
-    for (int e = P.tid; e < kBT * NP; e += kThreads) {
-      const int i = e / NP, m = e % NP;
-      s.b[e] = covered(i0 + i) && m < a.N ? ld1(Bp + (int64_t)(t0 + i0 + i) * a.B_st + m) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kBT; ++i) {
-      if (marks && s.s.mark[i0 + i] >= 0) start_state(s.s.mark[i0 + i], h);
-      const float4 v = *reinterpret_cast<const float4 *>(
-          &s.pair[i * Y::PT + P.pair]);
-      const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
-      const float dt[2] = {v.x, v.z}, dx[2] = {v.y, v.w}, Bv[4] = {B.x, B.y, B.z, B.w};
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          h[k][j] = fmaf(ex2(dt[k] * A2[k][j]), h[k][j], dx[k] * Bv[j]);
-    }
-    __syncthreads();
-  }
-
-  // the gradient that arrives at the range's end
-  if (s.s.mark[n] >= 0)
-    end_grad(n - 1, g);
-  else if (w.n > 1)
-    P.read(a, w.grad, P.r, g);
-  else
-    clear(g);
-
-  for (int q = tiles - 1; q >= 0; --q) {
-    const int i0 = q * kBT, t = t0 + i0 + lt;
-    const bool in = covered(i0 + lt);
-    const int m = in ? nv : 0;
-    const Elems<E, M> rx = ldm<VEC, E, M>(xp + t * a.x.st, m), rd = ldm<VEC, E, M>(dp + t * a.dt.st, m),
-                      rg = ldm<VEC, E, M>(gp + t * a.dout.st, m);
-    Elems<E, M> rz = rx;
-    if (zp) rz = ldm<VEC, E, M>(zp + t * a.z.st, m);
-    put_pairs(rx, rd, in);
+  auto put = [&](bool in) {
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-      const float z = ld1(&rz.v[i]);
-      s.dy[Y::pair_at(lt, lc + i)] = ld1(&rg.v[i]) * (zp ? z * sigmoidf(z) : 1.f);
+      float v = ld1(&rd.v[i]) + s.bias[lc + i];
+      if (a.softplus) v = softplusf(v);
+      s.pair[Y::pair_at(lt, lc + i)] =
+          in ? make_float2(v, v * ld1(&rx.v[i])) : make_float2(0.f, 0.f);
     }
-    for (int e = P.tid; e < kBT * NP; e += kThreads) {
-      const int i = e / NP, j = e % NP;
-      const bool ok = covered(i0 + i) && j < a.N;
-      s.b[e] = ok ? ld1(Bp + (int64_t)(t0 + i0 + i) * a.B_st + j) : 0.f;
-      s.c[e] = ok ? ld1(Cp + (int64_t)(t0 + i0 + i) * a.C_st + j) : 0.f;
-    }
-    __syncthreads();
-    float hist[kBT][2][4], before[2][4];
-    {
-      const float4 u = s.kept[q][0][P.tid], v = s.kept[q][1][P.tid];
-      before[0][0] = u.x; before[0][1] = u.y; before[0][2] = u.z; before[0][3] = u.w;
-      before[1][0] = v.x; before[1][1] = v.y; before[1][2] = v.z; before[1][3] = v.w;
-    }
+    rb.put(s.b);
+  };
+  auto advance = [&](int i, float (&v)[2][4]) {  // the state after token i of the tile
+    const float4 q = *reinterpret_cast<const float4 *>(&s.pair[i * Y::PT + P.pair]);
+    const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
+    const float dt[2] = {q.x, q.z}, dx[2] = {q.y, q.w}, Bv[4] = {B.x, B.y, B.z, B.w};
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[k][j] = before[k][j];
+      for (int j = 0; j < 4; ++j) v[k][j] = fmaf(ex2(dt[k] * A2[k][j]), v[k][j], dx[k] * Bv[j]);
+  };
+
+  // the sweep: the state before each tile that continues a segment
+  P.read(a, P.r > 0 && covered(0) ? w.state : nullptr, P.r, h);
+  fetch(0, false);
+  for (int q = 0; q < tiles; ++q) {
+    const int i0 = s.at[q];
+    if (starts(q))
+      P.read(a, covered(i0) ? a.h0 : nullptr, s.s.seg[i0], h);
+    else
+      keep8(kept + (i0 / kBT) * 8, h);
+    if (q + 1 == tiles) break;
+    const bool on = !starts(q + 1);  // the next tile goes on from here
+    if (on) {
+      put(covered(i0) && lt < s.at[q + 1] - i0);
+    }
+    fetch(q + 1, false);
+    if (on) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kBT; ++i) advance(i, h);
+      __syncthreads();
+    }
+  }
+  tc::tmem_st_wait();
+
+  float g[2][4], dA[2][4], sd[M], sb[M];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dA[k][j] = 0.f;
+#pragma unroll
+  for (int i = 0; i < M; ++i) sd[i] = sb[i] = 0.f;
+  // the gradient that arrives at the range's end
+  P.read(a, w.n > 1 ? w.grad : nullptr, P.r, g);
+  fetch(tiles - 1, true);
+  for (int q = tiles - 1; q >= 0; --q) {
+    const int i0 = s.at[q], m = s.at[q + 1] - i0;
+    const bool live = covered(i0), in = live && lt < m, first = starts(q);
+    const int64_t t = t0 + i0 + lt;
+    if (s.s.mark[i0 + m] >= 0) P.read(a, live ? a.dht : nullptr, s.s.seg[i0], g);
+    put(in);
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const float z = ld1(&rz.v[i]);
+      s.dy[Y::pair_at(lt, lc + i)] = in ? ld1(&rg.v[i]) * (zp ? z * sigmoidf(z) : 1.f) : 0.f;
+    }
+    rc.put(s.c);
+    const Elems<E, M> cx = rx, cd = rd, cg = rg, cz = rz;
+    if (q > 0) fetch(q - 1, true);
+    __syncthreads();
+    float hist[kBT][2][4], before[2][4];
+    if (first)
+      P.read(a, live ? a.h0 : nullptr, s.s.seg[i0], before);
+    else
+      kept8(kept + (i0 / kBT) * 8, before);
 #pragma unroll
     for (int i = 0; i < kBT; ++i) {
-      if (marks && i0 + i < n && s.s.mark[i0 + i] >= 0) start_state(s.s.mark[i0 + i], h);
-      const float4 v = *reinterpret_cast<const float4 *>(
-          &s.pair[i * Y::PT + P.pair]);
-      const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
-      const float dt[2] = {v.x, v.z}, dx[2] = {v.y, v.w}, Bv[4] = {B.x, B.y, B.z, B.w};
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h[k][j] = fmaf(ex2(dt[k] * A2[k][j]), h[k][j], dx[k] * Bv[j]);
-          hist[i][k][j] = h[k][j];
-        }
+        for (int j = 0; j < 4; ++j) hist[i][k][j] = i > 0 ? hist[i > 0 ? i - 1 : 0][k][j] : before[k][j];
+      advance(i, hist[i]);
       if (zp) {
         const float4 C = *reinterpret_cast<const float4 *>(&s.c[i * NP + P.nl * 4]);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           s.py[Y::part_at(i, P.ch[k]) + P.nl] =
-              fmaf(h[k][0], C.x, h[k][1] * C.y) + fmaf(h[k][2], C.z, h[k][3] * C.w);
+              fmaf(hist[i][k][0], C.x,
+                   fmaf(hist[i][k][1], C.y, fmaf(hist[i][k][2], C.z, hist[i][k][3] * C.w)));
       }
     }
 #pragma unroll
@@ -494,13 +536,6 @@ __global__ void __launch_bounds__(kThreads, 3)
       const float4 C = *reinterpret_cast<const float4 *>(&s.c[i * NP + P.nl * 4]);
       const float dt[2] = {v.x, v.z}, dx[2] = {v.y, v.w}, dy[2] = {dyv.x, dyv.y};
       const float Bv[4] = {B.x, B.y, B.z, B.w}, Cv[4] = {C.x, C.y, C.z, C.w};
-      const bool first = marks && i0 + i < n && s.s.mark[i0 + i] >= 0;
-      float prev[2][4];
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) prev[k][j] = i > 0 ? hist[i > 0 ? i - 1 : 0][k][j] : before[k][j];
-      if (first) start_state(s.s.mark[i0 + i], prev);
       float bc[8];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -510,11 +545,11 @@ __global__ void __launch_bounds__(kThreads, 3)
           g[k][j] = fmaf(Cv[j], dy[k], g[k][j]);
           bc[j] = k ? fmaf(dx[k], g[k][j], bc[j]) : dx[k] * g[k][j];
           bc[4 + j] = k ? fmaf(dy[k], hist[i][k][j], bc[4 + j]) : dy[k] * hist[i][k][j];
-          p = fmaf(g[k][j], Bv[j], p);
+          p = j ? fmaf(g[k][j], Bv[j], p) : g[k][j] * Bv[j];
           g[k][j] *= ex2(dt[k] * A2[k][j]);
-          const float cr = g[k][j] * prev[k][j];
+          const float cr = g[k][j] * (i > 0 ? hist[i > 0 ? i - 1 : 0][k][j] : before[k][j]);
           dA[k][j] = fmaf(dt[k], cr, dA[k][j]);
-          cs = fmaf(cr, A2[k][j], cs);
+          cs = j ? fmaf(cr, A2[k][j], cs) : cr * A2[k][j];
         }
         const int o = Y::part_at(i, P.ch[k]) + P.nl;
         s.pp[o] = p;
@@ -526,49 +561,37 @@ __global__ void __launch_bounds__(kThreads, 3)
         for (int u = 0; u < LEFT; ++u)
           s.red[P.warp][i][((f + u) >> 2) * NP + P.nl * 4 + ((f + u) & 3)] = bc[u];
       }
-      if (first) {
-        const int seg = s.s.mark[i0 + i];
-        if (a.dh0 && seg < a.n_seq) P.write(a, a.dh0, seg, g);
-        if (i0 + i > 0)
-          end_grad(i0 + i - 1, g);
-        else
-          clear(g);
-      }
     }
+    if (first && live && a.dh0) P.write(a, a.dh0, s.s.seg[i0], g);
     __syncthreads();
-    if (i0 + lt < n) {
+    if (lt < m) {
       float ox[M], od[M], oz[M];
 #pragma unroll
       for (int i = 0; i < M; ++i) {
         const int o = Y::part_at(lt, lc + i);
         const float p = sum_parts<LN>(&s.pp[o]), cs = sum_parts<LN>(&s.pc[o]) * kLn2;
-        const float x = ld1(&rx.v[i]), raw = ld1(&rd.v[i]) + bias[i], go = ld1(&rg.v[i]);
-        const float dt = a.softplus ? softplusf(raw) : raw;
+        const float x = ld1(&cx.v[i]), go = ld1(&cg.v[i]), skip = s.skip[lc + i];
+        const float dt = s.pair[Y::pair_at(lt, lc + i)].x;
         float dy = go;
         if (zp) {
-          const float z = ld1(&rz.v[i]), sg = sigmoidf(z);
+          const float z = ld1(&cz.v[i]), sg = sigmoidf(z);
           dy = go * z * sg;
-          oz[i] = go * fmaf(skip[i], x, sum_parts<LN>(&s.py[o])) * dsilu(z, sg);
+          oz[i] = in ? go * fmaf(skip, x, sum_parts<LN>(&s.py[o])) * dsilu(z, sg) : 0.f;
         }
-        ox[i] = fmaf(dt, p, skip[i] * dy);
-        od[i] = fmaf(x, p, cs);
-        if (a.softplus) od[i] *= sigmoidf(raw);
-        if (in) {
-          sd[i] = fmaf(dy, x, sd[i]);
-          sb[i] += od[i];
-        } else {
-          ox[i] = od[i] = oz[i] = 0.f;
-        }
+        ox[i] = in ? fmaf(dt, p, skip * dy) : 0.f;
+        od[i] = in ? fmaf(x, p, cs) : 0.f;
+        if (a.softplus) od[i] *= sigmoidf(ld1(&cd.v[i]) + s.bias[lc + i]);
+        sd[i] = fmaf(in ? dy : 0.f, x, sd[i]);
+        sb[i] += od[i];
       }
       stm<VEC, E, M>(reinterpret_cast<E *>(a.dx.p) + t * a.dx.st + c, ox, nv);
       stm<VEC, E, M>(reinterpret_cast<E *>(a.ddt.p) + t * a.ddt.st + c, od, nv);
       if (zp) stm<VEC, E, M>(reinterpret_cast<E *>(a.dz.p) + t * a.dz.st + c, oz, nv);
     }
-    for (int e = P.tid; e < kBT * 2 * NP; e += kThreads) {
+    float *bc = w.bc + ((int64_t)P.ct * a.T + t0 + i0) * (2 * NP);
+    for (int e = P.tid; e < m * 2 * NP; e += kThreads) {
       const int i = e / (2 * NP), o = e % (2 * NP);
-      if (i0 + i < n)
-        w.bc[((int64_t)P.ct * a.T + t0 + i0 + i) * (2 * NP) + o] =
-            (s.red[0][i][o] + s.red[1][i][o]) + (s.red[2][i][o] + s.red[3][i][o]);
+      bc[e] = (s.red[0][i][o] + s.red[1][i][o]) + (s.red[2][i][o] + s.red[3][i][o]);
     }
     __syncthreads();
   }
@@ -580,7 +603,10 @@ __global__ void __launch_bounds__(kThreads, 3)
     part[lt * CH + lc + i] = sd[i];
     part[(kBT + lt) * CH + lc + i] = sb[i];
   }
+  tc::tc_fence_before();
   __syncthreads();
+  tc::tc_fence_after();
+  if (P.warp == 0) tc::tmem_dealloc(s.tmem, kCols);
   for (int e = P.tid; e < P.nch; e += kThreads) {
     float u = 0.f, v = 0.f;
 #pragma unroll
@@ -593,25 +619,38 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
 }
 
-// out[i] = sum over n parts of in[r * size + i], for up to three arrays (blockIdx.y).
+// out[i] = sum over n parts of in[r * size + i], for up to three arrays (blockIdx.y): 32 columns a
+// block, its 8 warps taking every 8th part.
 struct PartSums {
   const float *in[3];
   float *out[3];
   int64_t size[3];
   int n;
 };
-__global__ void k_ssm_part_sums(const PartSums p) {
-  const int y = blockIdx.y;
-  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, size = p.size[y];
-  if (!p.out[y] || i >= size) return;
-  const float *q = p.in[y] + i;
-  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  int r = 0;
-  for (; r + 8 <= p.n; r += 8)
+__global__ void __launch_bounds__(256) k_ssm_part_sums(const PartSums p) {
+  __shared__ float part[8][32];
+  const int y = blockIdx.y, lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const int64_t i = blockIdx.x * (int64_t)32 + lane;
+  const int64_t size = y == 0 ? p.size[0] : y == 1 ? p.size[1] : p.size[2];
+  const float *in = y == 0 ? p.in[0] : y == 1 ? p.in[1] : p.in[2];
+  float *out = y == 0 ? p.out[0] : y == 1 ? p.out[1] : p.out[2];
+  if (!out || blockIdx.x * (int64_t)32 >= size) return;
+  float s[4] = {0, 0, 0, 0};
+  if (i < size) {
+    int r = k;
+    for (; r + 24 < p.n; r += 32)
 #pragma unroll
-    for (int u = 0; u < 8; ++u) s[u] += q[(r + u) * size];
-  for (; r < p.n; ++r) s[0] += q[r * size];
-  p.out[y][i] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+      for (int u = 0; u < 4; ++u) s[u] += in[(r + 8 * u) * size + i];
+    for (; r < p.n; r += 8) s[0] += in[r * size + i];
+  }
+  part[k][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (k == 0 && i < size) {
+    float v = part[0][lane];
+#pragma unroll
+    for (int u = 1; u < 8; ++u) v += part[u][lane];
+    out[i] = v;
+  }
 }
 
 // dB and dC: over the channel tiles of a group.
@@ -684,7 +723,7 @@ cudaError_t run_bwd(const SsmArgs &a, cudaStream_t stream) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const PartSums ps{{w.state, w.pd, w.pb}, {a.dA, a.dD, a.ddt_bias}, {size, a.D, a.D}, w.n};
-  k_ssm_part_sums<<<dim3((unsigned)ceil_div64(size, 128), 3), 128, 0, stream>>>(ps);
+  k_ssm_part_sums<<<dim3((unsigned)ceil_div64(size, 32), 3), 256, 0, stream>>>(ps);
   if ((e = cudaGetLastError()) != cudaSuccess || a.T == 0) return e;
   k_ssm_bc_sums<E><<<(unsigned)ceil_div64((int64_t)a.T * a.G * 2 * a.N, 256), 256, 0, stream>>>(
       w.bc, a.T, a.G, a.N, Lay<LN>::NP, tpg, reinterpret_cast<E *>(a.dB),
@@ -709,11 +748,13 @@ size_t ssm_bwd_workspace(int64_t T, int32_t D, int32_t N, int32_t G) {
   return ssm::carve(nullptr, T, D, N, G).bytes;
 }
 
-cudaError_t launch_ssm_bwd(const SsmArgs &a, cudaStream_t stream) {
+cudaError_t launch_ssm_bwd(const SsmArgs &args, cudaStream_t stream) {
   using namespace ssm;
+  SsmArgs a = args;
+  a.n4 = states_ok(a);
   const bool vec = (a.D / a.G) % 8 == 0 && rows_ok(a.x, a.f32) && rows_ok(a.dt, a.f32) &&
                    rows_ok(a.z, a.f32) && rows_ok(a.dout, a.f32) && rows_ok(a.dx, a.f32) &&
-                   rows_ok(a.ddt, a.f32) && rows_ok(a.dz, a.f32);
+                   rows_ok(a.ddt, a.f32) && rows_ok(a.dz, a.f32) && bc_ok(a);
   return a.f32 ? by_lanes<float>(a, vec, stream) : by_lanes<__nv_bfloat16>(a, vec, stream);
 }
 
