@@ -7,15 +7,15 @@
 //   dx = dt p + D dy,   ddt = (x p + sum_n A c_t) sigmoid(raw),   dA = sum_t dt c_t,
 //   dD = sum_t dy x,   dz = dout y (z sigmoid(z))',   dh0 = a g at the segment's first token.
 //
-// The token axis is cut into ranges of 128 tokens.  Pass 1 runs each range once, forwards, from a
+// The token axis is cut into ranges of 64 tokens.  Pass 1 runs each range once, forwards, from a
 // zero state: it keeps the state at its end and, with the running product of the a, the gradient
 // that its own tokens send to the state before it.  A short kernel chains both over the ranges.
 // Pass 2 then has a range's true state at its start and true gradient at its end.  It takes the
 // range in tiles of up to 8 tokens of one segment: a sweep forwards keeps the state before every
-// tile that continues a segment, then the tiles go last to first, each recomputing its states into
-// registers and walking back through them.  The kept states (8 fp32 a thread and tile) live in
-// Tensor Memory, 128 columns a block, each thread reading back its own lane: in shared memory they
-// would leave room for 2 blocks on an SM instead of 3.
+// tile that continues a segment, then the tiles go last to first, each recomputing its states and
+// walking back through them.  Both the kept states and a tile's states (8 fp32 a thread each) live
+// in Tensor Memory, 128 columns a block, each thread reading back its own lane: in registers and
+// shared memory they would leave room for 3 blocks on an SM instead of 4.
 //
 // Sums over states (p, c A, y) are left as partial sums of LN lanes in shared memory; sums over
 // channels (dB, dC) go over the warp's lanes by a transposing butterfly, over its warps in shared
@@ -34,9 +34,9 @@ using namespace mix;
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBT = 8;        // tokens of a tile of pass 2
-constexpr int kRange = 128;   // tokens of a range
+constexpr int kRange = 64;    // tokens of a range
 constexpr int kKept = kRange / kBT;  // states kept at most: tiles that continue a segment
-constexpr uint32_t kCols = 8 * kKept;  // Tensor Memory columns for them
+constexpr uint32_t kCols = 8 * (kKept + kBT);  // Tensor Memory columns: kept, then a tile's
 
 struct BwdWork {
   int n;            // ranges
@@ -337,16 +337,36 @@ __device__ __forceinline__ void keep8(uint32_t addr, const float (&h)[2][4]) {
                "f"(h[1][2]), "f"(h[1][3])
                : "memory");
 }
-__device__ __forceinline__ void kept8(uint32_t addr, float (&h)[2][4]) {
+// The read is complete after got8 of the same values.
+__device__ __forceinline__ void get8(uint32_t addr, float (&h)[2][4]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=f"(h[0][0]), "=f"(h[0][1]), "=f"(h[0][2]), "=f"(h[0][3]), "=f"(h[1][0]),
                  "=f"(h[1][1]), "=f"(h[1][2]), "=f"(h[1][3])
                : "r"(addr)
                : "memory");
-  // the values are tied to the wait, so that no use moves before it
+}
+__device__ __forceinline__ void got8(float (&h)[2][4]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(h[0][0]), "+f"(h[0][1]), "+f"(h[0][2]), "+f"(h[0][3]), "+f"(h[1][0]),
                  "+f"(h[1][1]), "+f"(h[1][2]), "+f"(h[1][3])::"memory");
+}
+
+// M floats of shared memory.
+template <int M>
+__device__ __forceinline__ void lds(const float *p, float (&v)[M]) {
+  if constexpr (M % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < M; i += 4) {
+      const float4 q = *reinterpret_cast<const float4 *>(p + i);
+      v[i] = q.x;
+      v[i + 1] = q.y;
+      v[i + 2] = q.z;
+      v[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < M; ++i) v[i] = p[i];
+  }
 }
 
 // Sums v[0..3] (dB) and v[4..7] (dC) over the lanes that hold the same states; each lane is left
@@ -373,7 +393,7 @@ __device__ __forceinline__ int channel_sums(float (&v)[8], int lane) {
 
 // Pass 2.
 template <typename E, int LN, bool VEC>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     k_ssm_bwd(const SsmArgs a, const BwdWork w, int tiles_per_group) {
   using Y = Lay<LN>;
   constexpr int NP = Y::NP, CH = Y::CH;
@@ -417,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t kept = s.tmem + ((uint32_t)(P.warp * 32) << 16);
+  const uint32_t hist = kept + 8 * kKept;
   const int tiles = s.tiles;
   auto covered = [&](int i) { return s.s.seg[i] >= 0 && s.s.seg[i] < a.n_seq; };
   auto starts = [&](int q) { return s.s.mark[s.at[q]] >= 0; };
@@ -438,12 +459,18 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
   };
   auto put = [&](bool in) {
+    if (in) {
+      float b[M];
+      lds<M>(&s.bias[lc], b);
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-      float v = ld1(&rd.v[i]) + s.bias[lc + i];
-      if (a.softplus) v = softplusf(v);
-      s.pair[Y::pair_at(lt, lc + i)] =
-          in ? make_float2(v, v * ld1(&rx.v[i])) : make_float2(0.f, 0.f);
+      for (int i = 0; i < M; ++i) {
+        float v = ld1(&rd.v[i]) + b[i];
+        if (a.softplus) v = softplusf(v);
+        s.pair[Y::pair_at(lt, lc + i)] = make_float2(v, v * ld1(&rx.v[i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < M; ++i) s.pair[Y::pair_at(lt, lc + i)] = make_float2(0.f, 0.f);
     }
     rb.put(s.b);
   };
@@ -497,38 +524,54 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int64_t t = t0 + i0 + lt;
     if (s.s.mark[i0 + m] >= 0) P.read(a, live ? a.dht : nullptr, s.s.seg[i0], g);
     put(in);
+    if (in) {
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-      const float z = ld1(&rz.v[i]);
-      s.dy[Y::pair_at(lt, lc + i)] = in ? ld1(&rg.v[i]) * (zp ? z * sigmoidf(z) : 1.f) : 0.f;
+      for (int i = 0; i < M; ++i) {
+        float dy = ld1(&rg.v[i]);
+        if (zp) {
+          const float z = ld1(&rz.v[i]);
+          dy *= z * sigmoidf(z);
+        }
+        s.dy[Y::pair_at(lt, lc + i)] = dy;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < M; ++i) s.dy[Y::pair_at(lt, lc + i)] = 0.f;
     }
     rc.put(s.c);
     const Elems<E, M> cx = rx, cd = rd, cg = rg, cz = rz;
     if (q > 0) fetch(q - 1, true);
     __syncthreads();
-    float hist[kBT][2][4], before[2][4];
-    if (first)
+    float now[2][4], before[2][4], next[2][4];  // states after token i, before it, before that
+    if (first) {
       P.read(a, live ? a.h0 : nullptr, s.s.seg[i0], before);
-    else
-      kept8(kept + (i0 / kBT) * 8, before);
+    } else {
+      get8(kept + (i0 / kBT) * 8, before);
+      got8(before);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) now[k][j] = before[k][j];
+    keep8(hist, now);
 #pragma unroll
     for (int i = 0; i < kBT; ++i) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) hist[i][k][j] = i > 0 ? hist[i > 0 ? i - 1 : 0][k][j] : before[k][j];
-      advance(i, hist[i]);
+      advance(i, now);
+      if (i + 1 < kBT) keep8(hist + (i + 1) * 8, now);
       if (zp) {
         const float4 C = *reinterpret_cast<const float4 *>(&s.c[i * NP + P.nl * 4]);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           s.py[Y::part_at(i, P.ch[k]) + P.nl] =
-              fmaf(hist[i][k][0], C.x,
-                   fmaf(hist[i][k][1], C.y, fmaf(hist[i][k][2], C.z, hist[i][k][3] * C.w)));
+              fmaf(now[k][0], C.x, fmaf(now[k][1], C.y, fmaf(now[k][2], C.z, now[k][3] * C.w)));
       }
     }
+    tc::tmem_st_wait();
+    get8(hist + (kBT - 1) * 8, before);
+    got8(before);
 #pragma unroll
     for (int i = kBT - 1; i >= 0; --i) {
+      if (i > 0) get8(hist + (i - 1) * 8, next);
       const int at = i * Y::PT + P.pair;
       const float4 v = *reinterpret_cast<const float4 *>(&s.pair[at]);
       const float2 dyv = *reinterpret_cast<const float2 *>(&s.dy[at]);
@@ -544,10 +587,10 @@ __global__ void __launch_bounds__(kThreads, 3)
         for (int j = 0; j < 4; ++j) {
           g[k][j] = fmaf(Cv[j], dy[k], g[k][j]);
           bc[j] = k ? fmaf(dx[k], g[k][j], bc[j]) : dx[k] * g[k][j];
-          bc[4 + j] = k ? fmaf(dy[k], hist[i][k][j], bc[4 + j]) : dy[k] * hist[i][k][j];
+          bc[4 + j] = k ? fmaf(dy[k], now[k][j], bc[4 + j]) : dy[k] * now[k][j];
           p = j ? fmaf(g[k][j], Bv[j], p) : g[k][j] * Bv[j];
           g[k][j] *= ex2(dt[k] * A2[k][j]);
-          const float cr = g[k][j] * (i > 0 ? hist[i > 0 ? i - 1 : 0][k][j] : before[k][j]);
+          const float cr = g[k][j] * before[k][j];
           dA[k][j] = fmaf(dt[k], cr, dA[k][j]);
           cs = j ? fmaf(cr, A2[k][j], cs) : cr * A2[k][j];
         }
@@ -561,28 +604,43 @@ __global__ void __launch_bounds__(kThreads, 3)
         for (int u = 0; u < LEFT; ++u)
           s.red[P.warp][i][((f + u) >> 2) * NP + P.nl * 4 + ((f + u) & 3)] = bc[u];
       }
+      if (i > 0) {
+        got8(next);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            now[k][j] = before[k][j];
+            before[k][j] = next[k][j];
+          }
+      }
     }
     if (first && live && a.dh0) P.write(a, a.dh0, s.s.seg[i0], g);
     __syncthreads();
     if (lt < m) {
       float ox[M], od[M], oz[M];
+      if (in) {
+        float skip[M], b[M];
+        lds<M>(&s.skip[lc], skip);
+        lds<M>(&s.bias[lc], b);
 #pragma unroll
-      for (int i = 0; i < M; ++i) {
-        const int o = Y::part_at(lt, lc + i);
-        const float p = sum_parts<LN>(&s.pp[o]), cs = sum_parts<LN>(&s.pc[o]) * kLn2;
-        const float x = ld1(&cx.v[i]), go = ld1(&cg.v[i]), skip = s.skip[lc + i];
-        const float dt = s.pair[Y::pair_at(lt, lc + i)].x;
-        float dy = go;
-        if (zp) {
-          const float z = ld1(&cz.v[i]), sg = sigmoidf(z);
-          dy = go * z * sg;
-          oz[i] = in ? go * fmaf(skip, x, sum_parts<LN>(&s.py[o])) * dsilu(z, sg) : 0.f;
+        for (int i = 0; i < M; ++i) {
+          const int o = Y::part_at(lt, lc + i), at = Y::pair_at(lt, lc + i);
+          const float p = sum_parts<LN>(&s.pp[o]), cs = sum_parts<LN>(&s.pc[o]) * kLn2;
+          const float x = ld1(&cx.v[i]), dt = s.pair[at].x, dy = s.dy[at];
+          if (zp) {
+            const float z = ld1(&cz.v[i]), sg = sigmoidf(z);
+            oz[i] = ld1(&cg.v[i]) * fmaf(skip[i], x, sum_parts<LN>(&s.py[o])) * dsilu(z, sg);
+          }
+          ox[i] = fmaf(dt, p, skip[i] * dy);
+          od[i] = fmaf(x, p, cs);
+          if (a.softplus) od[i] *= sigmoidf(ld1(&cd.v[i]) + b[i]);
+          sd[i] = fmaf(dy, x, sd[i]);
+          sb[i] += od[i];
         }
-        ox[i] = in ? fmaf(dt, p, skip * dy) : 0.f;
-        od[i] = in ? fmaf(x, p, cs) : 0.f;
-        if (a.softplus) od[i] *= sigmoidf(ld1(&cd.v[i]) + s.bias[lc + i]);
-        sd[i] = fmaf(in ? dy : 0.f, x, sd[i]);
-        sb[i] += od[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < M; ++i) ox[i] = od[i] = oz[i] = 0.f;
       }
       stm<VEC, E, M>(reinterpret_cast<E *>(a.dx.p) + t * a.dx.st + c, ox, nv);
       stm<VEC, E, M>(reinterpret_cast<E *>(a.ddt.p) + t * a.ddt.st + c, od, nv);
