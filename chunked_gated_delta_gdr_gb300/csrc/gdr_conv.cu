@@ -20,8 +20,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kTile = 16;  // tokens between two looks at the segment bounds
-constexpr int kAhead = 4;    // groups of 4 tokens in a forward thread's ring (bf16; fp32 half)
-constexpr int kFwdCtas = 3;  // blocks on each SM of the forward: all of them run at once
+constexpr int kFwdCtas = 3;  // blocks on each SM: all of them run at once
+constexpr int kBwdCtas = 2;
 
 // Marks of one tile, written by warp 0 one tile ahead.
 struct Marks {
@@ -41,7 +41,7 @@ struct Rows {  // 8 channels of x and of the states
     return ld8<VEC>(x + (int64_t)t * st + c0, nv);
   }
   // the W - 1 inputs before place p of segment seg (token t); win[W - 2] is the newest
-  __device__ __forceinline__ void fill(float (&win)[W - 1][8], int seg, int t, int p) const {
+  __device__ __forceinline__ void fill(f2 (&win)[W - 1][4], int seg, int t, int p) const {
 #pragma unroll
     for (int b = 1; b < W; ++b) {
       Raw8<E> r = zero8<E>();
@@ -49,43 +49,53 @@ struct Rows {  // 8 channels of x and of the states
         r = load(t - b);
       else if (h0)
         r = ld8<VEC>(h0 + ((int64_t)seg * (W - 1) + (W - 1 + p - b)) * C + c0, nv);
-      unpack8(r, win[W - 1 - b]);
+      unpack4(r, win[W - 1 - b]);
     }
   }
 };
 
+template <int N>
+__device__ __forceinline__ void clear(f2 (&v)[N][4]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[k][i] = pair(0.f, 0.f);
+}
+
 template <int W>
-__device__ __forceinline__ void load_taps(const ConvArgs &a, int c0, int nv, float (&w)[W][8],
-                                          float (&bias)[8]) {
+__device__ __forceinline__ void load_taps(const Param &weight, const Param &b, int c0, int nv,
+                                          f2 (&w)[W][4], f2 (&bias)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    const bool lo = 2 * i < nv, hi = 2 * i + 1 < nv;
+    const int64_t c = c0 + 2 * i;
 #pragma unroll
-    for (int k = 0; k < W; ++k) w[k][i] = i < nv ? ldp(a.w, (int64_t)(c0 + i) * W + k) : 0.f;
-    bias[i] = (i < nv && a.b.p) ? ldp(a.b, c0 + i) : 0.f;
+    for (int k = 0; k < W; ++k)
+      w[k][i] = pair(lo ? ldp(weight, c * W + k) : 0.f, hi ? ldp(weight, (c + 1) * W + k) : 0.f);
+    bias[i] = pair(lo && b.p ? ldp(b, c) : 0.f, hi && b.p ? ldp(b, c + 1) : 0.f);
   }
 }
 
 template <int W>
-__device__ __forceinline__ void taps(const float (&w)[W][8], const float (&bias)[8],
-                                     const float (&win)[W - 1][8], const float (&x)[8],
-                                     float (&u)[8]) {
+__device__ __forceinline__ void taps(const f2 (&w)[W][4], const f2 (&bias)[4],
+                                     const f2 (&win)[W - 1][4], const f2 (&x)[4], f2 (&u)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float s = bias[i];
+  for (int i = 0; i < 4; ++i) {
+    u[i] = bias[i];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) s = fmaf(w[k][i], win[k][i], s);
-    u[i] = fmaf(w[W - 1][i], x[i], s);
+    for (int k = 0; k < W - 1; ++k) u[i] = fma2(w[k][i], win[k][i], u[i]);
+    u[i] = fma2(w[W - 1][i], x[i], u[i]);
   }
 }
 
 template <int W>
-__device__ __forceinline__ void shift(float (&win)[W - 1][8], const float (&x)[8]) {
+__device__ __forceinline__ void shift(f2 (&win)[W - 1][4], const f2 (&x)[4]) {
 #pragma unroll
-  for (int k = 0; k + 1 < W - 1; ++k)
+  for (int i = 0; i < 4; ++i) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) win[k][i] = win[k + 1][i];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) win[W - 2][i] = x[i];
+    for (int k = 0; k + 1 < W - 1; ++k) win[k][i] = win[k + 1][i];
+    win[W - 2][i] = x[i];
+  }
 }
 
 // Copies the state rows of segments without tokens (src null: zeros).
@@ -101,24 +111,37 @@ __device__ void empty_rows(const ConvArgs &a, int rows, const void *src, void *d
   });
 }
 
-template <typename E>
-__device__ __forceinline__ Raw8<E> activated(float (&v)[8], int silu) {
-  if (silu) {
+// The forward's output: single products, which it has the issue slots for; pairs measured 7 %
+// slower here (554 against 519 us for 65,536 x 12,288), their latency longer.
+template <typename E, int W>
+__device__ __forceinline__ Raw8<E> output(const f2 (&w)[W][4], const f2 (&bias)[4],
+                                          const f2 (&win)[W - 1][4], const f2 (&x)[4], int silu) {
+  float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= sigmoidf(v[e]);
+  for (int i = 0; i < 4; ++i) {
+    float a, b, c, d, e, f;
+    unpair(bias[i], a, b);
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      unpair(w[k][i], c, d);
+      unpair(k < W - 1 ? win[k < W - 1 ? k : 0][i] : x[i], e, f);
+      a = fmaf(c, e, a);
+      b = fmaf(d, f, b);
+    }
+    v[2 * i] = silu ? a * sigmoidf(a) : a;
+    v[2 * i + 1] = silu ? b * sigmoidf(b) : b;
   }
   return pack8(v, E{});
 }
 
-// A thread's next rows of x on their way into shared memory: groups of G tokens, S of them in a
-// ring in which each thread reads only what it copied itself.  Without 16-byte alignment rows are
-// loaded when they are used.
-template <typename E, bool VEC>
+// A thread's next rows on their way into shared memory: groups of G tokens, S of them in a ring in
+// which each thread reads only what it copied itself.  Without 16-byte alignment rows are loaded
+// when they are used.
+template <typename E, bool VEC, int G_, int S_>
 struct Ahead {
-  static constexpr int G = 4;
+  static constexpr int G = G_, S = S_;
   static constexpr int P = (int)sizeof(E) / 2;  // 16-byte parts of a row's 8 elements
-  static constexpr int S = kAhead / P;
-  static constexpr int kBytes = VEC ? S * G * P * kThreads * 16 : 0;
+  static constexpr int kSlots = VEC ? S * G * P * kThreads : 0;
   uint4 *ring;
   const E *x;
   int64_t st;
@@ -138,10 +161,12 @@ struct Ahead {
         }
         p += st;
       }
-      copies_commit();
     }
   }
-  __device__ __forceinline__ void wait() const {
+  static __device__ __forceinline__ void commit() {
+    if (VEC) copies_commit();
+  }
+  static __device__ __forceinline__ void wait() {
     if (VEC) copies_wait<S - 1>();
   }
   __device__ __forceinline__ Raw8<E> get(int s, int g, int t) const {
@@ -156,11 +181,16 @@ struct Ahead {
     return r;
   }
 };
+// the forward's and the backward's (x and dy), less deep in fp32: a row is twice the bytes
+template <typename E, bool VEC>
+using FwdAhead = Ahead<E, VEC, 4, sizeof(E) == 2 ? 4 : 2>;
+template <typename E, bool VEC>
+using BwdAhead = Ahead<E, VEC, sizeof(E) == 2 ? 4 : 2, 2>;
 
 template <typename E, int W, bool VEC>
 __global__ void __launch_bounds__(kThreads, kFwdCtas)
     k_conv_fwd(const ConvArgs a, int range, int cblocks, int nranges) {
-  using R = Ahead<E, VEC>;
+  using R = FwdAhead<E, VEC>;
   constexpr int G = R::G, S = R::S;
   __shared__ Marks m;
   extern __shared__ __align__(16) uint4 ring[];
@@ -175,11 +205,15 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
                              reinterpret_cast<const E *>(a.h0), a.C, c0, nv};
   const R in{ring, rows.x + c0, a.x.st, nv, t1};
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) in.issue(s, t0 + s * G);
+  for (int s = 0; s < S - 1; ++s) {
+    in.issue(s, t0 + s * G);
+    in.commit();
+  }
   E *y = reinterpret_cast<E *>(a.y.p) + c0;
   E *ht = reinterpret_cast<E *>(a.ht);
-  float w[W][8], bias[8], win[W - 1][8];
-  load_taps<W>(a, c0, nv, w, bias);
+  f2 w[W][4], bias[4], win[W - 1][4];
+  load_taps<W>(a.w, a.b, c0, nv, w, bias);
+  clear<W - 1>(win);
   SegCursor cursor = seg_find(a.cu, a.n_seq, a.T, t0, m.red);
   int seg = cursor.j - 1;
   if (threadIdx.x < 32) {
@@ -191,14 +225,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
     }
   }
   __syncthreads();
-  if (seg >= 0 && seg < a.n_seq) {
-    rows.fill(win, seg, t0, t0 - m.start);
-  } else {
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) win[k][i] = 0.f;
-  }
+  if (seg >= 0 && seg < a.n_seq) rows.fill(win, seg, t0, t0 - m.start);
   int buf = 0, stage = 0;
   for (int tb = t0; tb < t1; tb += kTile, buf ^= 1) {
     if (threadIdx.x < 32 && tb + kTile < t1) {
@@ -211,16 +238,16 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
 #pragma unroll 1
     for (int tu = tb; tu < min(tb + kTile, t1); tu += G) {
       in.issue(stage == 0 ? S - 1 : stage - 1, tu + (S - 1) * G);
+      in.commit();
       in.wait();
       E *to = y + (int64_t)tu * a.y.st;
       if (!any && tu + G <= t1 && seg >= 0 && seg < a.n_seq) {
         // inside one segment: no bounds to look at, the window moves by renaming
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          float x[8], v[8];
-          unpack8(in.get(stage, g, tu + g), x);
-          taps<W>(w, bias, win, x, v);
-          st8<VEC>(to, activated<E>(v, a.silu), nv);
+          f2 x[4];
+          unpack4(in.get(stage, g, tu + g), x);
+          st8<VEC>(to, output<E, W>(w, bias, win, x, a.silu), nv);
           to += a.y.st;
           shift<W>(win, x);
         }
@@ -229,20 +256,19 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
         for (int g = 0; g < G; ++g) {
           const int t = tu + g, i = t - tb;
           if (t >= t1) break;
-          float x[8], v[8];
-          unpack8(in.get(stage, g, t), x);
+          f2 x[4];
+          unpack4(in.get(stage, g, t), x);
           if (any && mark[i] >= 0) {
             seg = mark[i];
             if (seg < a.n_seq) rows.fill(win, seg, t, 0);
           }
           if (seg >= 0 && seg < a.n_seq) {
-            taps<W>(w, bias, win, x, v);
-            st8<VEC>(to, activated<E>(v, a.silu), nv);
+            st8<VEC>(to, output<E, W>(w, bias, win, x, a.silu), nv);
             shift<W>(win, x);
             if (any && ht && mark[i + 1] >= 0) {
 #pragma unroll
               for (int k = 0; k < W - 1; ++k)
-                st8<VEC>(ht + ((int64_t)seg * (W - 1) + k) * a.C + c0, pack8(win[k], E{}), nv);
+                st8<VEC>(ht + ((int64_t)seg * (W - 1) + k) * a.C + c0, pack4<E>(win[k]), nv);
             }
           }
           to += a.y.st;
@@ -258,10 +284,12 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
 // until its last tap is in.  A range owns the gradients of its own tokens and of the initial
 // states of the segments that start in it; it runs on W - 1 tokens into the next range for them.
 template <typename E, int W, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBwdCtas)
     k_conv_bwd(const ConvArgs a, int range, int cblocks, int nranges) {
+  using R = BwdAhead<E, VEC>;
+  constexpr int G = R::G, S = R::S;
   __shared__ Marks m;
-  constexpr int U = 4;
+  extern __shared__ __align__(16) uint4 ring[];
   const int cb = blockIdx.x % cblocks, r = blockIdx.x / cblocks;
   const int c0 = (cb * kThreads + threadIdx.x) * 8, nv = max(0, min(8, a.C - c0));
   if (r == nranges) {
@@ -271,20 +299,23 @@ __global__ void __launch_bounds__(kThreads)
   const int t0 = r * range, t1 = min(a.T, t0 + range), t2 = min(a.T, t1 + W - 1);
   const Rows<E, W, VEC> rows{reinterpret_cast<const E *>(a.x.p), a.x.st,
                              reinterpret_cast<const E *>(a.h0), a.C, c0, nv};
-  const E *dy = reinterpret_cast<const E *>(a.dy.p) + c0;
+  const R inx{ring, rows.x + c0, a.x.st, nv, t2};
+  const R ing{ring + R::kSlots, reinterpret_cast<const E *>(a.dy.p) + c0, a.dy.st, nv, t2};
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) {
+    inx.issue(s, t0 + s * G);
+    ing.issue(s, t0 + s * G);
+    R::commit();
+  }
   E *dx = reinterpret_cast<E *>(a.dx.p) + c0;
   E *dh0 = reinterpret_cast<E *>(a.dh0);
   const E *dht = reinterpret_cast<const E *>(a.dht);
-  float w[W][8], bias[8], win[W - 1][8], acc[W - 1][8], dw[W][8], db[8];
-  load_taps<W>(a, c0, nv, w, bias);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    db[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) dw[k][i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) acc[k][i] = win[k][i] = 0.f;
-  }
+  f2 w[W][4], bias[4], win[W - 1][4], acc[W - 1][4], dw[W][4], db[1][4];
+  load_taps<W>(a.w, a.b, c0, nv, w, bias);
+  clear<W - 1>(win);
+  clear<W - 1>(acc);
+  clear<W>(dw);
+  clear<1>(db);
   SegCursor cursor = seg_find(a.cu, a.n_seq, a.T, t0, m.red);
   int seg = cursor.j - 1;
   if (threadIdx.x < 32) {
@@ -299,15 +330,44 @@ __global__ void __launch_bounds__(kThreads)
   int start = m.start;
   if (seg >= 0 && seg < a.n_seq) rows.fill(win, seg, t0, t0 - start);
 
-  auto emit = [&](int t, const float (&v)[8]) {  // the finished gradient of the input of token t
+  // one token: its x and dy; `done` is the finished gradient of the input W - 1 tokens back
+  auto token = [&](const Raw8<E> &rx, const Raw8<E> &rg, bool own, f2 (&done)[4]) {
+    f2 x[4], g[4];
+    unpack4(rx, x);
+    unpack4(rg, g);
+    if (a.silu) {
+      f2 u[4];
+      taps<W>(w, bias, win, x, u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], dsilu2(u[i], sigmoid2(u[i])));
+    }
+    if (own) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        db[0][i] = add2(db[0][i], g[i]);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) dw[k][i] = fma2(g[i], win[k][i], dw[k][i]);
+        dw[W - 1][i] = fma2(g[i], x[i], dw[W - 1][i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      done[i] = fma2(w[0][i], g[i], acc[W - 2][i]);
+#pragma unroll
+      for (int j = W - 2; j > 0; --j) acc[j][i] = fma2(w[W - 1 - j][i], g[i], acc[j - 1][i]);
+      acc[0][i] = mul2(w[W - 1][i], g[i]);
+    }
+    shift<W>(win, x);
+  };
+  auto emit = [&](int t, const f2 (&v)[4]) {  // the finished gradient of the input of token t
     if (t >= start) {
-      if (t >= t0 && t < t1) st8<VEC>(dx + (int64_t)t * a.dx.st, pack8(v, E{}), nv);
+      if (t >= t0 && t < t1) st8<VEC>(dx + (int64_t)t * a.dx.st, pack4<E>(v), nv);
     } else if (dh0 && start >= t0) {
-      st8<VEC>(dh0 + ((int64_t)seg * (W - 1) + (W - 1 + t - start)) * a.C + c0, pack8(v, E{}), nv);
+      st8<VEC>(dh0 + ((int64_t)seg * (W - 1) + (W - 1 + t - start)) * a.C + c0, pack4<E>(v), nv);
     }
   };
 
-  int buf = 0;
+  int buf = 0, stage = 0;
   bool stop = false;
   for (int tb = t0; tb < t2; tb += kTile, buf ^= 1) {
     if (threadIdx.x < 32 && tb + kTile < t2) {
@@ -318,107 +378,106 @@ __global__ void __launch_bounds__(kThreads)
     const bool any = m.any[buf];
     const int *mark = m.mark[buf];
 #pragma unroll 1
-    for (int u0 = 0; u0 < kTile && !stop; u0 += U) {
-      Raw8<E> rx[U], rd[U];
+    for (int tu = tb; tu < min(tb + kTile, t2) && !stop; tu += G) {
+      const int ahead = stage == 0 ? S - 1 : stage - 1;
+      inx.issue(ahead, tu + (S - 1) * G);
+      ing.issue(ahead, tu + (S - 1) * G);
+      R::commit();
+      R::wait();
+      if (!any && tu + G <= t1 && seg >= 0 && seg < a.n_seq && tu - (W - 1) >= max(t0, start)) {
+        // inside one segment, all finished gradients this range's own
+        E *to = dx + (int64_t)(tu - (W - 1)) * a.dx.st;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + u0 + u;
-        rx[u] = t < t2 ? rows.load(t) : zero8<E>();
-        rd[u] = t < t2 ? ld8<VEC>(dy + (int64_t)t * a.dy.st, nv) : zero8<E>();
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = u0 + u, t = tb + i;
-        if (t < t2 && !stop) {
+        for (int g = 0; g < G; ++g) {
+          f2 done[4];
+          token(inx.get(stage, g, tu + g), ing.get(stage, g, tu + g), true, done);
+          st8<VEC>(to, pack4<E>(done), nv);
+          to += a.dx.st;
+        }
+      } else {
+#pragma unroll 1
+        for (int g = 0; g < G; ++g) {
+          const int t = tu + g, i = t - tb;
+          if (t >= t2) break;
           if (any && mark[i] >= 0) {
-            if (t >= t1) {
+            if (t >= t1) {  // the next range's segment
               stop = true;
-            } else {
-              seg = mark[i];
-              start = t;
-              if (seg < a.n_seq) rows.fill(win, seg, t, 0);
-#pragma unroll
-              for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+              break;
             }
+            seg = mark[i];
+            start = t;
+            if (seg < a.n_seq) rows.fill(win, seg, t, 0);
+            clear<W - 1>(acc);
           }
-          if (!stop) {
-            if (seg >= 0 && seg < a.n_seq) {
-              float x[8], g[8];
-              unpack8(rx[u], x);
-              unpack8(rd[u], g);
-              if (a.silu) {
-                float v[8];
-                taps<W>(w, bias, win, x, v);
+          if (seg >= 0 && seg < a.n_seq) {
+            f2 done[4];
+            token(inx.get(stage, g, t), ing.get(stage, g, t), t < t1, done);
+            emit(t - (W - 1), done);
+            if (any && mark[i + 1] >= 0) {  // the segment's last token
 #pragma unroll
-                for (int e = 0; e < 8; ++e) g[e] *= dsilu(v[e], sigmoidf(v[e]));
-              }
-              if (t < t1) {
+              for (int j = 0; j < W - 1; ++j) {
+                if (dht) {
+                  f2 f[4];
+                  unpack4(ld8<VEC>(dht + ((int64_t)seg * (W - 1) + (W - 2 - j)) * a.C + c0, nv), f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  db[e] += g[e];
-#pragma unroll
-                  for (int k = 0; k < W - 1; ++k) dw[k][e] = fmaf(g[e], win[k][e], dw[k][e]);
-                  dw[W - 1][e] = fmaf(g[e], x[e], dw[W - 1][e]);
+                  for (int e = 0; e < 4; ++e) acc[j][e] = add2(acc[j][e], f[e]);
                 }
+                emit(t - j, acc[j]);
               }
-              float done[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                done[e] = fmaf(w[0][e], g[e], acc[W - 2][e]);
-#pragma unroll
-                for (int j = W - 2; j > 0; --j)
-                  acc[j][e] = fmaf(w[W - 1 - j][e], g[e], acc[j - 1][e]);
-                acc[0][e] = w[W - 1][e] * g[e];
-              }
-              emit(t - (W - 1), done);
-              shift<W>(win, x);
-              if (any && mark[i + 1] >= 0) {  // the segment's last token
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) {
-                  if (dht) {
-                    float f[8];
-                    unpack8(ld8<VEC>(dht + ((int64_t)seg * (W - 1) + (W - 2 - j)) * a.C + c0, nv),
-                            f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[j][e] += f[e];
-                  }
-                  emit(t - j, acc[j]);
-                }
-              }
-            } else if (t < t1) {  // no segment: no gradient
-              st8<VEC>(dx + (int64_t)t * a.dx.st, zero8<E>(), nv);
             }
+          } else if (t < t1) {  // no segment: no gradient
+            st8<VEC>(dx + (int64_t)t * a.dx.st, zero8<E>(), nv);
           }
         }
       }
+      stage = stage + 1 == S ? 0 : stage + 1;
     }
     __syncthreads();
   }
-  float *work = reinterpret_cast<float *>(a.work) + (int64_t)r * (W + 1) * a.C;
+  if (VEC) copies_wait<0>();  // a range that stopped early has copies on their way
+  float *work = reinterpret_cast<float *>(a.work) + (int64_t)r * (W + 1) * a.C + c0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < nv) {
+  for (int k = 0; k <= W; ++k) {
+    float v[8];
 #pragma unroll
-      for (int k = 0; k < W; ++k) work[(int64_t)k * a.C + c0 + i] = dw[k][i];
-      work[(int64_t)W * a.C + c0 + i] = db[i];
+    for (int i = 0; i < 4; ++i) unpair(k < W ? dw[k < W ? k : 0][i] : db[0][i], v[2 * i], v[2 * i + 1]);
+    if (VEC) {
+      if (nv > 0) {
+        float4 *q = reinterpret_cast<float4 *>(work + (int64_t)k * a.C);
+        q[0] = make_float4(v[0], v[1], v[2], v[3]);
+        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < nv) work[(int64_t)k * a.C + i] = v[i];
     }
+  }
 }
 
-// Sums the ranges' parts of dw and db in range order.
-__global__ void k_conv_sum(const float *work, int nranges, int C, int W, float *dw, float *db) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x, k = blockIdx.y;
-  if (c >= C || (k == W && !db)) return;
-  const float *p = work + (int64_t)k * C + c;
+// Sums the ranges' parts of dw and db: 32 channels a block, its 8 warps taking every 8th range.
+__global__ void __launch_bounds__(256)
+    k_conv_sum(const float *work, int nranges, int C, int W, float *dw, float *db) {
+  __shared__ float part[8][32];
+  const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane, k = blockIdx.y;
+  if (k == W && !db) return;
   const int64_t st = (int64_t)(W + 1) * C;
-  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  int r = 0;
-  for (; r + 8 <= nranges; r += 8)
+  float s[4] = {0, 0, 0, 0};
+  if (c < C) {
+    const float *p = work + (int64_t)k * C + c;
+    int r = q;
+    for (; r + 24 < nranges; r += 32)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] += p[(r + i) * st];
-  for (; r < nranges; ++r) s[0] += p[r * st];
-  const float v = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+      for (int i = 0; i < 4; ++i) s[i] += p[(r + 8 * i) * st];
+    for (; r < nranges; r += 8) s[0] += p[r * st];
+  }
+  part[q][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (q != 0 || c >= C) return;
+  float v = part[0][lane];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) v += part[i][lane];
   if (k < W)
     dw[(int64_t)c * W + k] = v;
   else
@@ -441,16 +500,12 @@ __global__ void __launch_bounds__(kThreads) k_conv_step(const ConvStepArgs a, in
   Raw8<E> old[W - 1];
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) old[k] = ld8<VEC>(s + (int64_t)k * a.C, nv);
-  float win[W - 1][8], w[W][8], bias[8], x[8], v[8];
-  ConvArgs ca{};
-  ca.w = a.w;
-  ca.b = a.b;
-  load_taps<W>(ca, c0, nv, w, bias);
+  f2 win[W - 1][4], w[W][4], bias[4], x[4];
+  load_taps<W>(a.w, a.b, c0, nv, w, bias);
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) unpack8(old[k], win[k]);
-  unpack8(rx, x);
-  taps<W>(w, bias, win, x, v);
-  st8<VEC>(y, activated<E>(v, a.silu), nv);
+  for (int k = 0; k < W - 1; ++k) unpack4(old[k], win[k]);
+  unpack4(rx, x);
+  st8<VEC>(y, output<E, W>(w, bias, win, x, a.silu), nv);
 #pragma unroll
   for (int k = 0; k + 1 < W - 1; ++k) st8<VEC>(s + (int64_t)k * a.C, old[k + 1], nv);
   st8<VEC>(s + (int64_t)(W - 2) * a.C, rx, nv);
@@ -481,7 +536,7 @@ cudaError_t run_fwd(const ConvArgs &a, cudaStream_t stream) {
   const int nranges = (int)ceil_div64(a.T, range);
   const int64_t blocks = (int64_t)cblocks * (nranges + (a.ht ? 1 : 0));
   if (blocks == 0) return cudaSuccess;
-  constexpr int smem = Ahead<E, VEC>::kBytes;
+  constexpr int smem = FwdAhead<E, VEC>::kSlots * 16;
   static_assert(smem <= 46 * 1024, "more shared memory than a launch has without asking");
   k_conv_fwd<E, W, VEC><<<(unsigned)blocks, kThreads, smem, stream>>>(a, range, cblocks, nranges);
   return cudaGetLastError();
@@ -490,14 +545,16 @@ cudaError_t run_fwd(const ConvArgs &a, cudaStream_t stream) {
 template <typename E, int W, bool VEC>
 cudaError_t run_bwd(const ConvArgs &a, cudaStream_t stream) {
   const int cblocks = (int)ceil_div64(a.C, kThreads * 8);
-  const int range = range_of(a.T, conv_ranges(a.T, a.C, 4));
+  const int range = range_of(a.T, conv_ranges(a.T, a.C, kBwdCtas));
   const int nranges = (int)ceil_div64(a.T, range);
   const int64_t blocks = (int64_t)cblocks * (nranges + (a.dh0 ? 1 : 0));
+  constexpr int smem = 2 * BwdAhead<E, VEC>::kSlots * 16;
+  static_assert(smem <= 46 * 1024, "more shared memory than a launch has without asking");
   if (blocks > 0)
-    k_conv_bwd<E, W, VEC><<<(unsigned)blocks, kThreads, 0, stream>>>(a, range, cblocks, nranges);
+    k_conv_bwd<E, W, VEC><<<(unsigned)blocks, kThreads, smem, stream>>>(a, range, cblocks, nranges);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  k_conv_sum<<<dim3((unsigned)ceil_div64(a.C, 256), W + 1), 256, 0, stream>>>(
+  k_conv_sum<<<dim3((unsigned)ceil_div64(a.C, 32), W + 1), 256, 0, stream>>>(
       reinterpret_cast<const float *>(a.work), nranges, a.C, W, a.dw, a.db);
   return cudaGetLastError();
 }
@@ -537,7 +594,7 @@ cudaError_t launch_conv_fwd(const ConvArgs &a, cudaStream_t stream) {
 }
 
 size_t conv_bwd_workspace(int64_t T, int32_t C, int32_t W) {
-  const int range = mix::range_of(T, mix::conv_ranges(T, C, 4));
+  const int range = mix::range_of(T, mix::conv_ranges(T, C, mix::kBwdCtas));
   return align256((size_t)ceil_div64(T, range) * (W + 1) * C * sizeof(float));
 }
 

@@ -163,6 +163,11 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ void unpack4(const Raw8<__nv_bfloat16> &r, f2 (&f)[4]) {
   const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
@@ -218,8 +223,17 @@ __device__ __forceinline__ float rcp(float x) {
 }
 // 1 / (1 + e^-x): 2^(-x log2 e) overflows to inf for very negative x, whose reciprocal is 0
 __device__ __forceinline__ float sigmoidf(float x) { return rcp(1.f + ex2(-x * kLog2e)); }
+__device__ __forceinline__ f2 sigmoid2(f2 x) {
+  float a, b;
+  unpair(mul2(x, pair(-kLog2e, -kLog2e)), a, b);
+  unpair(add2(pair(ex2(a), ex2(b)), pair(1.f, 1.f)), a, b);
+  return pair(rcp(a), rcp(b));
+}
 // d/dx of x sigmoid(x), from s = sigmoid(x)
 __device__ __forceinline__ float dsilu(float x, float s) { return s * (1.f + x * (1.f - s)); }
+__device__ __forceinline__ f2 dsilu2(f2 x, f2 s) {
+  return fma2(x, fma2(mul2(s, pair(-1.f, -1.f)), s, s), s);
+}
 // log(1 + e^x) = max(x, 0) + log(1 + t), t = e^-|x|, and log(1 + t) = 2 atanh(s), s = t / (2 + t)
 // <= 1/3, accurate relative to itself for small t too: 2 atanh(s) / s as a polynomial in s^2,
 // interpolated at the Chebyshev points of [0, 1/9] (4e-9 off at most).
