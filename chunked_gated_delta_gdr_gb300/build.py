@@ -1,4 +1,5 @@
-"""Build libgdr.so in-tree with nvcc for sm_103a (GB300) only.
+"""Build libgdr.so in-tree with nvcc for sm_103a (GB300) only, and _mixer.so, the Python binding of
+the mixer's operators, with the host compiler against the installed PyTorch.
 
 Each translation unit compiles in parallel; the shared library links the
 static CUDA runtime so it loads on machines without a driver (the library's
@@ -18,6 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdr.so")
+BINDING = os.path.join(PKG, "_mixer.so")
+BINDING_SOURCE = "mixer_binding.cpp"
 
 SOURCES = ["gdr_api.cu", "gdr_index.cu", "gdr_staged.cu", "gdr_fused.cu", "gdr_split.cu",
            "gdr_bwd.cu", "gdr_bwd_tc.cu", "gdr_mix_api.cu", "gdr_conv.cu", "gdr_ssm.cu",
@@ -44,10 +47,43 @@ def _deps():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+        return True
+    if os.path.getmtime(os.path.join(CSRC, BINDING_SOURCE)) > os.path.getmtime(BINDING):
         return True
     t = os.path.getmtime(LIB)
     return any(os.path.getmtime(f) > t for f in _deps())
+
+
+def _compile_binding() -> str:
+    """The binding's object file; linked once libgdr.so is there."""
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, os.path.splitext(BINDING_SOURCE)[0] + ".o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", root,
+           "-I", os.path.join(root, "torch", "csrc", "api", "include"), "-I", cuda,
+           "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {BINDING_SOURCE}:\n{r.stderr[-4000:]}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-l:libgdr.so",
+           "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stderr[-4000:]}")
+    os.replace(tmp, BINDING)
 
 
 def _compile(src: str) -> str:
@@ -64,18 +100,22 @@ def _compile(src: str) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA source and link libgdr.so; returns its path."""
+    """Compile every source, link libgdr.so and the binding; returns the library's path."""
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
-        objs = list(ex.map(_compile, SOURCES))
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        # the longest translation units first
+        todo = sorted(SOURCES, key=lambda f: -os.path.getsize(os.path.join(CSRC, f)))
+        binding = ex.submit(_compile_binding)
+        objs = list(ex.map(_compile, todo))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *GENCODE, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIB)
+    _link_binding(binding.result())
     if verbose:
         for src in SOURCES:
             log = os.path.join(BUILD, os.path.splitext(src)[0] + ".o.log")

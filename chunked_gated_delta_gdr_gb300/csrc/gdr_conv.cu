@@ -62,17 +62,54 @@ __device__ __forceinline__ void clear(f2 (&v)[N][4]) {
     for (int i = 0; i < 4; ++i) v[k][i] = pair(0.f, 0.f);
 }
 
+// n contiguous parameters, a multiple of 8 of them 16-byte aligned
+template <int N>
+__device__ __forceinline__ void load_params(const Param &p, int64_t at, float (&v)[N]) {
+  if (p.bf16) {
+    const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(p.p) + at);
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      float f[8];
+      unpack8(Raw8<__nv_bfloat16>{q[i]}, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[8 * i + j] = f[j];
+    }
+  } else {
+    const float4 *q = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p.p) + at);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 f = q[i];
+      v[4 * i] = f.x;
+      v[4 * i + 1] = f.y;
+      v[4 * i + 2] = f.z;
+      v[4 * i + 3] = f.w;
+    }
+  }
+}
+
+// The taps and bias of 8 channels (those from nv on are zero).
 template <int W>
 __device__ __forceinline__ void load_taps(const Param &weight, const Param &b, int c0, int nv,
                                           f2 (&w)[W][4], f2 (&bias)[4]) {
+  float v[8 * W], u[8];
+  const uintptr_t at = reinterpret_cast<uintptr_t>(weight.p) | reinterpret_cast<uintptr_t>(b.p);
+  if (nv == 8 && (at & 15) == 0) {
+    load_params<8 * W>(weight, (int64_t)c0 * W, v);
+    if (b.p) load_params<8>(b, c0, u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int k = 0; k < W; ++k)
+        v[i * W + k] = i < nv ? ldp(weight, (int64_t)(c0 + i) * W + k) : 0.f;
+      u[i] = i < nv && b.p ? ldp(b, c0 + i) : 0.f;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const bool lo = 2 * i < nv, hi = 2 * i + 1 < nv;
-    const int64_t c = c0 + 2 * i;
 #pragma unroll
-    for (int k = 0; k < W; ++k)
-      w[k][i] = pair(lo ? ldp(weight, c * W + k) : 0.f, hi ? ldp(weight, (c + 1) * W + k) : 0.f);
-    bias[i] = pair(lo && b.p ? ldp(b, c) : 0.f, hi && b.p ? ldp(b, c + 1) : 0.f);
+    for (int k = 0; k < W; ++k) w[k][i] = pair(v[2 * i * W + k], v[(2 * i + 1) * W + k]);
+    bias[i] = b.p ? pair(u[2 * i], u[2 * i + 1]) : pair(0.f, 0.f);
   }
 }
 

@@ -23,6 +23,7 @@ using namespace mix;
 
 constexpr int kFwdCtas = 4;  // blocks of pass 2 on each SM: the ranges are cut to run all at once
 constexpr int kEndCtas = 5;
+constexpr int kAhead = 3;    // tiles in the rings
 
 struct Ranges {
   int range, n;      // tokens of a range, ranges
@@ -32,7 +33,7 @@ struct Ranges {
 };
 
 template <int LN>
-struct Tile1 {
+struct __align__(16) Tile1 {
   using Y = Lay<LN>;
   float2 pair[Y::L * Y::PT];
   float b[Y::L * Y::NP];
@@ -46,14 +47,16 @@ template <typename E, int LN, bool VEC>
 __global__ void __launch_bounds__(kThreads, kEndCtas)
     k_ssm_ends(const SsmArgs a, const Ranges rg, int tiles_per_group) {
   using Y = Lay<LN>;
-  constexpr int L = Y::L, NP = Y::NP, CH = Y::CH;
+  using R = TileRing<E, VEC, kAhead>;
+  constexpr int L = Y::L, NP = Y::NP, CH = Y::CH, Q = R::S;
   extern __shared__ __align__(16) char smem_raw[];
   Tile1<LN> &s = *reinterpret_cast<Tile1<LN> *>(smem_raw);
+  uint4 *ring = reinterpret_cast<uint4 *>(&s + 1);
   const Place<LN> P(a, tiles_per_group);
   const int r0 = P.r * rg.range, t1 = min(a.T, r0 + rg.range);
   const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
-  const E *xp = reinterpret_cast<const E *>(a.x.p) + P.c0 + lc;
-  const E *dp = reinterpret_cast<const E *>(a.dt.p) + P.c0 + lc;
+  const R xr{ring, reinterpret_cast<const E *>(a.x.p) + P.c0 + lc, a.x.st};
+  const R dr{ring + R::kSlots, reinterpret_cast<const E *>(a.dt.p) + P.c0 + lc, a.dt.st};
   const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
   for (int i = P.tid; i < CH; i += kThreads)
     s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
@@ -65,20 +68,27 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
   const int t0 = reset ? c.b : r0;
   P.read(a, covered && reset ? a.h0 : nullptr, seg, h);
   if (covered) {
-    Raw8<E> rx, rd;
     BcTile<E, NP, L, VEC> rb;
-    auto fetch = [&](int tb) {
+    auto issue = [&](int q, int tb) {
       const int n = tb + lt < t1 ? nv : 0;
-      rx = ld8<VEC>(xp + (int64_t)(tb + lt) * a.x.st, n);
-      rd = ld8<VEC>(dp + (int64_t)(tb + lt) * a.dt.st, n);
-      rb.fetch(Bp, a.B_st, tb, t1, a.N);
+      xr.issue(q, tb + lt, n);
+      dr.issue(q, tb + lt, n);
+      copies_commit();
     };
-    fetch(t0);
+#pragma unroll
+    for (int q = 0; q < Q - 1; ++q) issue(q, t0 + q * L);
+    rb.fetch(Bp, a.B_st, t0, t1, a.N);
     __syncthreads();
+    int stage = 0;
     for (int tb = t0; tb < t1; tb += L) {
-      put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, rx, rd);
+      issue(stage == 0 ? Q - 1 : stage - 1, tb + (Q - 1) * L);
+      copies_wait<Q - 1>();
+      const int n = tb + lt < t1 ? nv : 0;
+      put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, xr.get(stage, tb + lt, n),
+                       dr.get(stage, tb + lt, n));
+      stage = stage + 1 == Q ? 0 : stage + 1;
       rb.put(s.b);
-      if (tb + L < t1) fetch(tb + L);
+      if (tb + L < t1) rb.fetch(Bp, a.B_st, tb + L, t1, a.N);
       __syncthreads();
       tile_tokens<L>(0, min(L, t1 - tb), [&](int i) {
         const float4 d = *reinterpret_cast<const float4 *>(
@@ -106,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
 }
 
 template <int LN>
-struct Tile2 {  // shared memory of one tile of pass 2
+struct __align__(16) Tile2 {  // shared memory of one tile of pass 2
   using Y = Lay<LN>;
   float2 pair[Y::L * Y::PT];  // (dt, dt x)
   float b[Y::L * Y::NP], c[Y::L * Y::NP];
@@ -121,9 +131,11 @@ template <typename E, int LN, bool VEC>
 __global__ void __launch_bounds__(kThreads, kFwdCtas)
     k_ssm_fwd(const SsmArgs a, const Ranges rg, int tiles_per_group) {
   using Y = Lay<LN>;
-  constexpr int L = Y::L, NP = Y::NP, CH = Y::CH;
+  using R = TileRing<E, VEC, kAhead>;
+  constexpr int L = Y::L, NP = Y::NP, CH = Y::CH, Q = R::S;
   extern __shared__ __align__(16) char smem_raw[];
   Tile2<LN> &s = *reinterpret_cast<Tile2<LN> *>(smem_raw);
+  uint4 *ring = reinterpret_cast<uint4 *>(&s + 1);
   const Place<LN> P(a, tiles_per_group);
   if (P.r == rg.n) {  // final states of the segments without tokens
     for_empty_segments(a.cu, a.n_seq, a.T, s.red, [&](int n) {
@@ -135,9 +147,10 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
   }
   const int t0 = P.r * rg.range, t1 = min(a.T, t0 + rg.range);
   const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
-  const E *xp = reinterpret_cast<const E *>(a.x.p) + P.c0 + lc;
-  const E *dp = reinterpret_cast<const E *>(a.dt.p) + P.c0 + lc;
-  const E *zp = a.z.p ? reinterpret_cast<const E *>(a.z.p) + P.c0 + lc : nullptr;
+  const R xr{ring, reinterpret_cast<const E *>(a.x.p) + P.c0 + lc, a.x.st};
+  const R dr{ring + R::kSlots, reinterpret_cast<const E *>(a.dt.p) + P.c0 + lc, a.dt.st};
+  const R zr{ring + 2 * R::kSlots, reinterpret_cast<const E *>(a.z.p) + P.c0 + lc, a.z.st};
+  const bool gated = a.z.p != nullptr;
   E *yp = reinterpret_cast<E *>(a.y.p) + P.c0 + lc;
   const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
   const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
@@ -145,17 +158,18 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
     s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
     s.skip[i] = a.Dskip && i < P.nch ? a.Dskip[P.c0 + i] : 0.f;
   }
-  Raw8<E> rx, rd, rz = zero8<E>();
   BcTile<E, NP, L, VEC> rb, rc;
-  auto fetch = [&](int tb) {
+  auto issue = [&](int q, int tb) {
     const int n = tb + lt < t1 ? nv : 0;
-    rx = ld8<VEC>(xp + (int64_t)(tb + lt) * a.x.st, n);
-    rd = ld8<VEC>(dp + (int64_t)(tb + lt) * a.dt.st, n);
-    if (zp) rz = ld8<VEC>(zp + (int64_t)(tb + lt) * a.z.st, n);
-    rb.fetch(Bp, a.B_st, tb, t1, a.N);
-    rc.fetch(Cp, a.C_st, tb, t1, a.N);
+    xr.issue(q, tb + lt, n);
+    dr.issue(q, tb + lt, n);
+    if (gated) zr.issue(q, tb + lt, n);
+    copies_commit();
   };
-  fetch(t0);
+#pragma unroll
+  for (int q = 0; q < Q - 1; ++q) issue(q, t0 + q * L);
+  rb.fetch(Bp, a.B_st, t0, t1, a.N);
+  rc.fetch(Cp, a.C_st, t0, t1, a.N);
   float A2[2][4], h[2][4];
   P.decays(a, A2);
   SegCursor cursor = seg_find(a.cu, a.n_seq, a.T, t0, s.red);
@@ -185,13 +199,15 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
     });
   };
 
+  int stage = 0;
   for (int tb = t0; tb < t1; tb += L) {
-    const int n = min(L, t1 - tb);
-    // this tile's elements into shared memory, the next tile's from global memory
-    put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, rx, rd);
+    const int n = min(L, t1 - tb), k = lt < n ? nv : 0;
+    issue(stage == 0 ? Q - 1 : stage - 1, tb + (Q - 1) * L);
+    copies_wait<Q - 1>();
+    put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, xr.get(stage, tb + lt, k),
+                     dr.get(stage, tb + lt, k));
     rb.put(s.b);
     rc.put(s.c);
-    const Raw8<E> cx = rx, cz = rz;
     if (P.warp == 0) {
       const int carry = cursor.j - 1;
       const bool any = seg_marks(a.cu, a.n_seq, a.T, tb, n, s.mark, cursor);
@@ -214,7 +230,10 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
         s.same = carry;
       }
     }
-    if (tb + L < t1) fetch(tb + L);
+    if (tb + L < t1) {
+      rb.fetch(Bp, a.B_st, tb + L, t1, a.N);
+      rc.fetch(Cp, a.C_st, tb + L, t1, a.N);
+    }
     __syncthreads();
     const bool any = s.any;
     if (!any) {
@@ -238,23 +257,24 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
     const int own = any ? s.seg[lt] : s.same;
     if (lt < n && own >= 0 && own < a.n_seq) {
       float x[8], v[8];
-      unpack8(cx, x);
+      unpack8(xr.get(stage, tb + lt, k), x);
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
-        const float4 k = *reinterpret_cast<const float4 *>(&s.skip[lc + i]);
+        const float4 w = *reinterpret_cast<const float4 *>(&s.skip[lc + i]);
         const float *part = &s.part[Y::part_at(lt, lc) + i * LN];
-        v[i] = fmaf(k.x, x[i], sum_parts<LN>(part));
-        v[i + 1] = fmaf(k.y, x[i + 1], sum_parts<LN>(part + LN));
-        v[i + 2] = fmaf(k.z, x[i + 2], sum_parts<LN>(part + 2 * LN));
-        v[i + 3] = fmaf(k.w, x[i + 3], sum_parts<LN>(part + 3 * LN));
+        v[i] = fmaf(w.x, x[i], sum_parts<LN>(part));
+        v[i + 1] = fmaf(w.y, x[i + 1], sum_parts<LN>(part + LN));
+        v[i + 2] = fmaf(w.z, x[i + 2], sum_parts<LN>(part + 2 * LN));
+        v[i + 3] = fmaf(w.w, x[i + 3], sum_parts<LN>(part + 3 * LN));
       }
-      if (zp) {
-        unpack8(cz, x);
+      if (gated) {
+        unpack8(zr.get(stage, tb + lt, k), x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= x[i] * sigmoidf(x[i]);
       }
       st8<VEC>(yp + (int64_t)(tb + lt) * a.y.st, pack8(v, E{}), nv);
     }
+    stage = stage + 1 == Q ? 0 : stage + 1;
     __syncthreads();
   }
 }
@@ -287,63 +307,86 @@ __global__ void k_ssm_chain(const float *A, const Ranges rg, int D, int N) {
   }
 }
 
-// One token for each row: state slot idx[row] in place.  A thread holds 4 states of one channel.
-template <typename E, int LN>
+// One token for each row: state slot idx[row] in place.  A thread holds 4 states of one channel for
+// R rows: the channel's parameters are read once, and R states are on their way at a time.
+template <typename E, int LN, int R>
 __global__ void __launch_bounds__(kThreads)
     k_ssm_step(const SsmArgs a, float *state, int slots, const int32_t *idx, int cblocks) {
   constexpr int CB = kThreads / LN;  // channels of a block
-  const int row = blockIdx.x / cblocks, d = blockIdx.x % cblocks * CB + threadIdx.x / LN;
-  const int nl = threadIdx.x % LN, N = a.N;
+  const int row0 = blockIdx.x / cblocks * R, d = blockIdx.x % cblocks * CB + threadIdx.x / LN;
+  const int n0 = threadIdx.x % LN * 4, N = a.N;
   const bool in = d < a.D;
-  const int slot = idx ? idx[row] : row;
-  E *y = reinterpret_cast<E *>(a.y.p) + (int64_t)row * a.y.st + d;
-  if (slot < 0 || slot >= slots) {
-    if (in && nl == 0) st1(y, 0.f);
-    return;
+  const int64_t at = (int64_t)d * N + n0;
+  int slot[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = row0 + r;
+    slot[r] = row < a.T ? (idx ? idx[row] : row) : -1;
+    if (slot[r] >= slots) slot[r] = -1;
   }
-  float part = 0.f, x = 0.f;
-  if (in) {
-    const int grp = d / (a.D / a.G);
-    const E *B = reinterpret_cast<const E *>(a.B) + row * a.B_st + grp * a.B_sg;
-    const E *C = reinterpret_cast<const E *>(a.C) + row * a.C_st + grp * a.C_sg;
-    float *s = state + ((int64_t)slot * a.D + d) * N;
-    const float *A = a.A + (int64_t)d * N;
-    x = ld1(reinterpret_cast<const E *>(a.x.p) + (int64_t)row * a.x.st + d);
-    float dt = ld1(reinterpret_cast<const E *>(a.dt.p) + (int64_t)row * a.dt.st + d);
-    if (a.dt_bias) dt += a.dt_bias[d];
-    if (a.softplus) dt = softplusf(dt);
-    const float dx = dt * x;
-    const int n0 = nl * 4;
-    if (N % 4 == 0) {
-      if (n0 < N) {
-        const float4 h = *reinterpret_cast<const float4 *>(s + n0);
-        const float4 Av = *reinterpret_cast<const float4 *>(A + n0);
-        float4 o;
-        o.x = fmaf(ex2(dt * (Av.x * kLog2e)), h.x, dx * ld1(B + n0));
-        o.y = fmaf(ex2(dt * (Av.y * kLog2e)), h.y, dx * ld1(B + n0 + 1));
-        o.z = fmaf(ex2(dt * (Av.z * kLog2e)), h.z, dx * ld1(B + n0 + 2));
-        o.w = fmaf(ex2(dt * (Av.w * kLog2e)), h.w, dx * ld1(B + n0 + 3));
-        *reinterpret_cast<float4 *>(s + n0) = o;
-        part = fmaf(o.x, ld1(C + n0), o.y * ld1(C + n0 + 1)) +
-               fmaf(o.z, ld1(C + n0 + 2), o.w * ld1(C + n0 + 3));
-      }
+  float h[R][4], A2[4], x[R], dt[R], z[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    x[r] = dt[r] = z[r] = 0.f;
+    const float *s = state + ((int64_t)slot[r] * a.D * N + at);
+    const bool live = in && slot[r] >= 0;
+    if (a.n4) {
+      const float4 v = live && n0 < N ? *reinterpret_cast<const float4 *>(s)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      h[r][0] = v.x;
+      h[r][1] = v.y;
+      h[r][2] = v.z;
+      h[r][3] = v.w;
     } else {
-      for (int n = n0; n < min(N, n0 + 4); ++n) {
-        const float o = fmaf(ex2(dt * (A[n] * kLog2e)), s[n], dx * ld1(B + n));
-        s[n] = o;
-        part = fmaf(o, ld1(C + n), part);
-      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[r][j] = live && n0 + j < N ? s[j] : 0.f;
+    }
+    if (live) {
+      const int64_t row = row0 + r;
+      x[r] = ld1(reinterpret_cast<const E *>(a.x.p) + row * a.x.st + d);
+      dt[r] = ld1(reinterpret_cast<const E *>(a.dt.p) + row * a.dt.st + d);
+      if (a.z.p) z[r] = ld1(reinterpret_cast<const E *>(a.z.p) + row * a.z.st + d);
     }
   }
 #pragma unroll
-  for (int o = LN / 2; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-  if (in && nl == 0) {
-    if (a.Dskip) part = fmaf(a.Dskip[d], x, part);
-    if (a.z.p) {
-      const float z = ld1(reinterpret_cast<const E *>(a.z.p) + (int64_t)row * a.z.st + d);
-      part *= z * sigmoidf(z);
+  for (int j = 0; j < 4; ++j) A2[j] = in && n0 + j < N ? a.A[at + j] * kLog2e : 0.f;
+  const float bias = in && a.dt_bias ? a.dt_bias[d] : 0.f;
+  const float skip = in && a.Dskip ? a.Dskip[d] : 0.f;
+  const int grp = in ? d / (a.D / a.G) : 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (row0 + r >= a.T) break;  // the same in every lane
+    const int64_t row = row0 + r;
+    float part = 0.f;
+    if (in && slot[r] >= 0) {
+      const E *B = reinterpret_cast<const E *>(a.B) + row * a.B_st + grp * a.B_sg + n0;
+      const E *C = reinterpret_cast<const E *>(a.C) + row * a.C_st + grp * a.C_sg + n0;
+      float v = dt[r] + bias;
+      if (a.softplus) v = softplusf(v);
+      const float dx = v * x[r];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n0 + j < N) {
+          h[r][j] = fmaf(ex2(v * A2[j]), h[r][j], dx * ld1(B + j));
+          part = fmaf(h[r][j], ld1(C + j), part);
+        }
+      float *s = state + ((int64_t)slot[r] * a.D * N + at);
+      if (a.n4) {
+        if (n0 < N)
+          *reinterpret_cast<float4 *>(s) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n0 + j < N) s[j] = h[r][j];
+      }
     }
-    st1(y, part);
+#pragma unroll
+    for (int o = LN / 2; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (in && n0 == 0) {
+      part = fmaf(skip, x[r], part);
+      if (a.z.p) part *= z[r] * sigmoidf(z[r]);
+      st1(reinterpret_cast<E *>(a.y.p) + row * a.y.st + d, slot[r] >= 0 ? part : 0.f);
+    }
   }
 }
 
@@ -389,7 +432,9 @@ template <typename E, int LN, bool VEC>
 cudaError_t run_fwd(const SsmArgs &a, cudaStream_t stream) {
   const int tpg = (int)ceil_div64(a.D / a.G, Lay<LN>::CH), ctiles = tpg * a.G;
   const Carve c = carve(a.work, a.T, a.D, a.N, range_for(a.T, a.D, a.N, a.G));
-  constexpr int smem1 = (int)sizeof(Tile1<LN>), smem2 = (int)sizeof(Tile2<LN>);
+  constexpr int slots = TileRing<E, VEC, kAhead>::kSlots * 16;
+  constexpr int smem1 = (int)sizeof(Tile1<LN>) + 2 * slots,
+                smem2 = (int)sizeof(Tile2<LN>) + 3 * slots;
   cudaError_t e;
   if (c.rg.n > 1) {
     if (smem1 > 48 * 1024 && (e = allow_smem(k_ssm_ends<E, LN, VEC>, smem1)) != cudaSuccess)
@@ -421,9 +466,14 @@ cudaError_t fwd_by_lanes(const SsmArgs &a, bool vec, cudaStream_t stream) {
 template <typename E, int LN>
 cudaError_t run_step(const SsmArgs &a, float *state, int32_t slots, const int32_t *idx,
                      cudaStream_t stream) {
-  const int cblocks = (int)ceil_div64(a.D, kThreads / LN);
-  k_ssm_step<E, LN><<<(unsigned)((int64_t)cblocks * a.T), kThreads, 0, stream>>>(a, state, slots,
-                                                                                 idx, cblocks);
+  const int64_t cblocks = ceil_div64(a.D, kThreads / LN);
+  // rows in fours only where that leaves every SM its 16 blocks: few rows are a matter of latency
+  if (cblocks * ceil_div64(a.T, 4) >= (int64_t)sm_count() * 16)
+    k_ssm_step<E, LN, 4><<<(unsigned)(cblocks * ceil_div64(a.T, 4)), kThreads, 0, stream>>>(
+        a, state, slots, idx, (int)cblocks);
+  else
+    k_ssm_step<E, LN, 1><<<(unsigned)(cblocks * a.T), kThreads, 0, stream>>>(a, state, slots, idx,
+                                                                            (int)cblocks);
   return cudaGetLastError();
 }
 template <typename E>
@@ -454,9 +504,11 @@ cudaError_t launch_ssm_fwd(const SsmArgs &args, cudaStream_t stream) {
                : fwd_by_lanes<__nv_bfloat16>(a, vec, stream);
 }
 
-cudaError_t launch_ssm_step(const SsmArgs &a, float *state, int32_t slots, const int32_t *idx,
+cudaError_t launch_ssm_step(const SsmArgs &args, float *state, int32_t slots, const int32_t *idx,
                             cudaStream_t stream) {
-  if (a.T == 0) return cudaSuccess;
+  if (args.T == 0) return cudaSuccess;
+  SsmArgs a = args;
+  a.n4 = a.N % 4 == 0;  // the entry point has checked the state's alignment
   return a.f32 ? ssm::step_by_lanes<float>(a, state, slots, idx, stream)
                : ssm::step_by_lanes<__nv_bfloat16>(a, state, slots, idx, stream);
 }

@@ -165,6 +165,35 @@ struct BcTile {
   }
 };
 
+// A thread's 8 elements of each tile of x (dt, z, dout) on their way into shared memory, S tiles
+// in a ring in which each thread reads only what it copied itself: they take no registers while
+// they wait.  Elements that were not copied (n = 0: no token or no channel) read as anything.
+// Without 16-byte alignment they are loaded when they are used.
+template <typename E, bool VEC, int S_>
+struct TileRing {
+  static constexpr int S = S_, P = (int)sizeof(E) / 2;
+  static constexpr int kSlots = VEC ? S * P * kThreads : 0;
+  uint4 *ring;
+  const E *p;
+  int64_t st;
+
+  __device__ __forceinline__ void issue(int s, int t, int n) const {
+    if (VEC && n > 0) {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        mix::copy16(ring + (s * P + i) * kThreads + threadIdx.x, p + t * st + i * 4);
+    }
+  }
+  __device__ __forceinline__ mix::Raw8<E> get(int s, int t, int n) const {
+    if (!VEC) return mix::ld8<VEC>(p + t * st, n);
+    mix::Raw8<E> r;
+    uint4 *w = reinterpret_cast<uint4 *>(&r);
+#pragma unroll
+    for (int i = 0; i < P; ++i) w[i] = ring[(s * P + i) * kThreads + threadIdx.x];
+    return r;
+  }
+};
+
 // (dt, dt x) of a thread's 8 elements of a tile.
 template <typename E, int LN>
 __device__ __forceinline__ void put_pairs(float2 *pair, const float *bias, int softplus, int lt,

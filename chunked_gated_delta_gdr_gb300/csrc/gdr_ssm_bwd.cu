@@ -156,7 +156,7 @@ __device__ __forceinline__ int range_tiles(int n, const RangeSegs &s, int *at) {
 }
 
 template <int LN>
-struct Tile1 {
+struct __align__(16) Tile1 {
   using Y = Lay<LN>;
   float2 pair[Y::L * Y::PT];
   float dy[Y::L * Y::PT];
@@ -170,31 +170,35 @@ template <typename E, int LN, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4)
     k_ssm_bwd_ends(const SsmArgs a, const BwdWork w, int tiles_per_group) {
   using Y = Lay<LN>;
-  constexpr int L = Y::L, NP = Y::NP;
+  using R = TileRing<E, VEC, 2>;
+  constexpr int L = Y::L, NP = Y::NP, Q = R::S;
   extern __shared__ __align__(16) char smem_raw[];
   Tile1<LN> &s = *reinterpret_cast<Tile1<LN> *>(smem_raw);
+  uint4 *ring = reinterpret_cast<uint4 *>(&s + 1);
   const Place<LN> P(a, tiles_per_group);
   const int t0 = P.r * kRange, n = min(kRange, a.T - t0);
   const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
   const int64_t c = P.c0 + lc;
-  const E *xp = reinterpret_cast<const E *>(a.x.p) + c, *dp = reinterpret_cast<const E *>(a.dt.p) + c;
-  const E *gp = reinterpret_cast<const E *>(a.dout.p) + c;
-  const E *zp = a.z.p ? reinterpret_cast<const E *>(a.z.p) + c : nullptr;
+  const R xr{ring, reinterpret_cast<const E *>(a.x.p) + c, a.x.st};
+  const R dr{ring + R::kSlots, reinterpret_cast<const E *>(a.dt.p) + c, a.dt.st};
+  const R gr{ring + 2 * R::kSlots, reinterpret_cast<const E *>(a.dout.p) + c, a.dout.st};
+  const R zr{ring + 3 * R::kSlots, reinterpret_cast<const E *>(a.z.p) + c, a.z.st};
+  const bool gated = a.z.p != nullptr;
   const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
   const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
-  Raw8<E> rx, rd, rg, rz = zero8<E>();
   BcTile<E, NP, L, VEC> rb, rc;
-  auto fetch = [&](int i0) {
-    const int m = i0 + lt < n ? nv : 0;
-    const int64_t t = t0 + i0 + lt;
-    rx = ld8<VEC>(xp + t * a.x.st, m);
-    rd = ld8<VEC>(dp + t * a.dt.st, m);
-    rg = ld8<VEC>(gp + t * a.dout.st, m);
-    if (zp) rz = ld8<VEC>(zp + t * a.z.st, m);
-    rb.fetch(Bp, a.B_st, t0 + i0, t0 + n, a.N);
-    rc.fetch(Cp, a.C_st, t0 + i0, t0 + n, a.N);
+  auto issue = [&](int q, int i0) {
+    const int m = i0 + lt < n ? nv : 0, t = t0 + i0 + lt;
+    xr.issue(q, t, m);
+    dr.issue(q, t, m);
+    gr.issue(q, t, m);
+    if (gated) zr.issue(q, t, m);
+    copies_commit();
   };
-  fetch(0);
+#pragma unroll
+  for (int q = 0; q < Q - 1; ++q) issue(q, q * L);
+  rb.fetch(Bp, a.B_st, t0, t0 + n, a.N);
+  rc.fetch(Cp, a.C_st, t0, t0 + n, a.N);
   for (int i = P.tid; i < Y::CH; i += kThreads)
     s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
   float A2[2][4], h[2][4], pr[2][4], gs[2][4], S[2] = {0.f, 0.f};
@@ -209,20 +213,31 @@ __global__ void __launch_bounds__(kThreads, 4)
   range_segments(a, t0, n, s.s);
   __syncthreads();
   bool reset = false;  // a segment has started: nothing from here on reaches the state before
+  int stage = 0;
   for (int i0 = 0; i0 < n; i0 += L) {
-    const int m = min(L, n - i0);
-    put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, rx, rd);
+    const int m = min(L, n - i0), t = t0 + i0 + lt, k = lt < m ? nv : 0;
+    issue(stage == 0 ? Q - 1 : stage - 1, i0 + (Q - 1) * L);
+    copies_wait<Q - 1>();
+    put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, xr.get(stage, t, k),
+                     dr.get(stage, t, k));
     {
       float g[8], z[8];
-      unpack8(rg, g);
-      unpack8(rz, z);
+      unpack8(gr.get(stage, t, k), g);
+      if (gated) {
+        unpack8(zr.get(stage, t, k), z);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        s.dy[Y::pair_at(lt, lc) + Y::pair_at(0, i)] = zp ? g[i] * z[i] * sigmoidf(z[i]) : g[i];
+        for (int i = 0; i < 8; ++i) g[i] *= z[i] * sigmoidf(z[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s.dy[Y::pair_at(lt, lc) + Y::pair_at(0, i)] = g[i];
     }
+    stage = stage + 1 == Q ? 0 : stage + 1;
     rb.put(s.b);
     rc.put(s.c);
-    if (i0 + L < n) fetch(i0 + L);
+    if (i0 + L < n) {
+      rb.fetch(Bp, a.B_st, t0 + i0 + L, t0 + n, a.N);
+      rc.fetch(Cp, a.C_st, t0 + i0 + L, t0 + n, a.N);
+    }
     __syncthreads();
     auto scan = [&](int from, int to) {
       tile_tokens<L>(from, to, [&](int i) {
@@ -758,7 +773,8 @@ template <typename E, int LN, bool VEC>
 cudaError_t run_bwd(const SsmArgs &a, cudaStream_t stream) {
   const int tpg = (int)ceil_div64(a.D / a.G, Lay<LN>::CH), ctiles = tpg * a.G;
   const BwdWork w = carve(a.work, a.T, a.D, a.N, a.G);
-  constexpr int smem1 = (int)sizeof(Tile1<LN>), smem2 = (int)sizeof(Tile2<LN>);
+  constexpr int smem1 = (int)sizeof(Tile1<LN>) + 4 * 16 * TileRing<E, VEC, 2>::kSlots;
+  constexpr int smem2 = (int)sizeof(Tile2<LN>);
   cudaError_t e = cudaFuncSetAttribute(k_ssm_bwd<E, LN, VEC>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem2);
   if (e != cudaSuccess) return e;
