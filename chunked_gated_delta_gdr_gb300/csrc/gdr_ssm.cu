@@ -307,86 +307,124 @@ __global__ void k_ssm_chain(const float *A, const Ranges rg, int D, int N) {
   }
 }
 
-// One token for each row: state slot idx[row] in place.  A thread holds 4 states of one channel for
-// R rows: the channel's parameters are read once, and R states are on their way at a time.
-template <typename E, int LN, int R>
+// Four neighbouring elements as fp32, in one read (VEC) or the first n of them.
+template <bool VEC>
+__device__ __forceinline__ void four(const __nv_bfloat16 *p, int n, float (&f)[4]) {
+  if (VEC) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    f[0] = lo_bf(v.x);
+    f[1] = hi_bf(v.x);
+    f[2] = lo_bf(v.y);
+    f[3] = hi_bf(v.y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = i < n ? ld1(p + i) : 0.f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void four(const float *p, int n, float (&f)[4]) {
+  if (VEC) {
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    f[0] = v.x;
+    f[1] = v.y;
+    f[2] = v.z;
+    f[3] = v.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = i < n ? p[i] : 0.f;
+  }
+}
+
+// One token for each row: state slot idx[row] in place.  Bound by HBM: the states are read and
+// written once.  A thread holds 4 states of 4 neighbouring channels, so that a row's B and C serve
+// four channels and everything is read four elements at a time, all of it before anything is used.
+// VEC: every group of four (channels of a group, states) is whole and aligned.
+template <typename E, int LN, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     k_ssm_step(const SsmArgs a, float *state, int slots, const int32_t *idx, int cblocks) {
-  constexpr int CB = kThreads / LN;  // channels of a block
-  const int row0 = blockIdx.x / cblocks * R, d = blockIdx.x % cblocks * CB + threadIdx.x / LN;
-  const int n0 = threadIdx.x % LN * 4, N = a.N;
-  const bool in = d < a.D;
-  const int64_t at = (int64_t)d * N + n0;
-  int slot[R];
+  constexpr int CB = kThreads / LN * 4;  // channels of a block
+  const int row = blockIdx.x / cblocks;
+  const int d0 = blockIdx.x % cblocks * CB + threadIdx.x / LN * 4, n0 = threadIdx.x % LN * 4;
+  const int nd = max(0, min(4, a.D - d0)), nn = max(0, min(4, a.N - n0));
+  const int slot = idx ? idx[row] : row;
+  E *y = reinterpret_cast<E *>(a.y.p) + (int64_t)row * a.y.st + d0;
+  if (slot < 0 || slot >= slots) {
+    if (n0 == 0) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int row = row0 + r;
-    slot[r] = row < a.T ? (idx ? idx[row] : row) : -1;
-    if (slot[r] >= slots) slot[r] = -1;
-  }
-  float h[R][4], A2[4], x[R], dt[R], z[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    x[r] = dt[r] = z[r] = 0.f;
-    const float *s = state + ((int64_t)slot[r] * a.D * N + at);
-    const bool live = in && slot[r] >= 0;
-    if (a.n4) {
-      const float4 v = live && n0 < N ? *reinterpret_cast<const float4 *>(s)
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-      h[r][0] = v.x;
-      h[r][1] = v.y;
-      h[r][2] = v.z;
-      h[r][3] = v.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[r][j] = live && n0 + j < N ? s[j] : 0.f;
+      for (int c = 0; c < 4; ++c)
+        if (c < nd) st1(y + c, 0.f);
     }
-    if (live) {
-      const int64_t row = row0 + r;
-      x[r] = ld1(reinterpret_cast<const E *>(a.x.p) + row * a.x.st + d);
-      dt[r] = ld1(reinterpret_cast<const E *>(a.dt.p) + row * a.dt.st + d);
-      if (a.z.p) z[r] = ld1(reinterpret_cast<const E *>(a.z.p) + row * a.z.st + d);
+    return;
+  }
+  const bool on = nd > 0 && nn > 0;
+  const int64_t at = (int64_t)d0 * a.N + n0;
+  float *s = state + (int64_t)slot * a.D * a.N + at;
+  float h[4][4], A[4][4], x[4], dt[4], z[4], bias[4], skip[4], B[4], C[4], part[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    x[c] = dt[c] = z[c] = bias[c] = skip[c] = B[c] = C[c] = part[c] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[c][j] = A[c][j] = 0.f;
+  }
+  const int Dg = a.D / a.G;
+  const E *Bp = reinterpret_cast<const E *>(a.B) + (int64_t)row * a.B_st + n0;
+  const E *Cp = reinterpret_cast<const E *>(a.C) + (int64_t)row * a.C_st + n0;
+  if (on) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (VEC || c < nd) {
+        four<VEC>(s + c * a.N, nn, h[c]);
+        four<VEC>(a.A + at + c * a.N, nn, A[c]);
+      }
+    if (VEC) {
+      four<VEC>(Bp + d0 / Dg * a.B_sg, nn, B);
+      four<VEC>(Cp + d0 / Dg * a.C_sg, nn, C);
     }
   }
+  if (nd > 0) {
+    four<VEC>(reinterpret_cast<const E *>(a.x.p) + (int64_t)row * a.x.st + d0, nd, x);
+    four<VEC>(reinterpret_cast<const E *>(a.dt.p) + (int64_t)row * a.dt.st + d0, nd, dt);
+    if (a.z.p) four<VEC>(reinterpret_cast<const E *>(a.z.p) + (int64_t)row * a.z.st + d0, nd, z);
+    if (a.dt_bias) four<VEC>(a.dt_bias + d0, nd, bias);
+    if (a.Dskip) four<VEC>(a.Dskip + d0, nd, skip);
+  }
+  if (on) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) A2[j] = in && n0 + j < N ? a.A[at + j] * kLog2e : 0.f;
-  const float bias = in && a.dt_bias ? a.dt_bias[d] : 0.f;
-  const float skip = in && a.Dskip ? a.Dskip[d] : 0.f;
-  const int grp = in ? d / (a.D / a.G) : 0;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (row0 + r >= a.T) break;  // the same in every lane
-    const int64_t row = row0 + r;
-    float part = 0.f;
-    if (in && slot[r] >= 0) {
-      const E *B = reinterpret_cast<const E *>(a.B) + row * a.B_st + grp * a.B_sg + n0;
-      const E *C = reinterpret_cast<const E *>(a.C) + row * a.C_st + grp * a.C_sg + n0;
-      float v = dt[r] + bias;
+    for (int c = 0; c < 4; ++c) {
+      if (!VEC) {
+        if (c >= nd) break;
+        four<VEC>(Bp + (d0 + c) / Dg * a.B_sg, nn, B);
+        four<VEC>(Cp + (d0 + c) / Dg * a.C_sg, nn, C);
+      }
+      float v = dt[c] + bias[c];
       if (a.softplus) v = softplusf(v);
-      const float dx = v * x[r];
+      const float dx = v * x[c];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (n0 + j < N) {
-          h[r][j] = fmaf(ex2(v * A2[j]), h[r][j], dx * ld1(B + j));
-          part = fmaf(h[r][j], ld1(C + j), part);
-        }
-      float *s = state + ((int64_t)slot[r] * a.D * N + at);
-      if (a.n4) {
-        if (n0 < N)
-          *reinterpret_cast<float4 *>(s) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
+      for (int j = 0; j < 4; ++j) {
+        h[c][j] = fmaf(ex2(v * (A[c][j] * kLog2e)), h[c][j], dx * B[j]);
+        part[c] = fmaf(h[c][j], C[j], part[c]);
+      }
+      if (VEC) {
+        *reinterpret_cast<float4 *>(s + c * a.N) =
+            make_float4(h[c][0], h[c][1], h[c][2], h[c][3]);
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (n0 + j < N) s[j] = h[r][j];
+          if (j < nn) s[c * a.N + j] = h[c][j];
       }
     }
+  }
 #pragma unroll
-    for (int o = LN / 2; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-    if (in && n0 == 0) {
-      part = fmaf(skip, x[r], part);
-      if (a.z.p) part *= z[r] * sigmoidf(z[r]);
-      st1(reinterpret_cast<E *>(a.y.p) + row * a.y.st + d, slot[r] >= 0 ? part : 0.f);
-    }
+  for (int c = 0; c < 4; ++c) {
+#pragma unroll
+    for (int o = LN / 2; o > 0; o >>= 1) part[c] += __shfl_xor_sync(0xffffffffu, part[c], o);
+    part[c] = fmaf(skip[c], x[c], part[c]);
+    if (a.z.p) part[c] *= z[c] * sigmoidf(z[c]);
+  }
+  if (n0 == 0) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c < nd) st1(y + c, part[c]);
   }
 }
 
@@ -466,14 +504,20 @@ cudaError_t fwd_by_lanes(const SsmArgs &a, bool vec, cudaStream_t stream) {
 template <typename E, int LN>
 cudaError_t run_step(const SsmArgs &a, float *state, int32_t slots, const int32_t *idx,
                      cudaStream_t stream) {
-  const int64_t cblocks = ceil_div64(a.D, kThreads / LN);
-  // rows in fours only where that leaves every SM its 16 blocks: few rows are a matter of latency
-  if (cblocks * ceil_div64(a.T, 4) >= (int64_t)sm_count() * 16)
-    k_ssm_step<E, LN, 4><<<(unsigned)(cblocks * ceil_div64(a.T, 4)), kThreads, 0, stream>>>(
-        a, state, slots, idx, (int)cblocks);
+  const int64_t cblocks = ceil_div64(a.D, kThreads / LN * 4);
+  const unsigned blocks = (unsigned)(cblocks * a.T);
+  const uintptr_t four = a.f32 ? 15 : 7;  // four activations
+  auto fit = [&](const void *p, int64_t st, int64_t sg) {
+    return (reinterpret_cast<uintptr_t>(p) & four) == 0 && ((st | sg) & 3) == 0;
+  };
+  const bool vec = a.N % 4 == 0 && (a.D / a.G) % 4 == 0 && fit(a.B, a.B_st, a.B_sg) &&
+                   fit(a.C, a.C_st, a.C_sg) && fit(a.x.p, a.x.st, 0) &&
+                   fit(a.dt.p, a.dt.st, 0) && fit(a.z.p, a.z.st, 0) && aligned16(a.dt_bias) &&
+                   aligned16(a.Dskip);  // the entry point has checked the states and A
+  if (vec)
+    k_ssm_step<E, LN, true><<<blocks, kThreads, 0, stream>>>(a, state, slots, idx, (int)cblocks);
   else
-    k_ssm_step<E, LN, 1><<<(unsigned)(cblocks * a.T), kThreads, 0, stream>>>(a, state, slots, idx,
-                                                                            (int)cblocks);
+    k_ssm_step<E, LN, false><<<blocks, kThreads, 0, stream>>>(a, state, slots, idx, (int)cblocks);
   return cudaGetLastError();
 }
 template <typename E>
@@ -504,11 +548,9 @@ cudaError_t launch_ssm_fwd(const SsmArgs &args, cudaStream_t stream) {
                : fwd_by_lanes<__nv_bfloat16>(a, vec, stream);
 }
 
-cudaError_t launch_ssm_step(const SsmArgs &args, float *state, int32_t slots, const int32_t *idx,
+cudaError_t launch_ssm_step(const SsmArgs &a, float *state, int32_t slots, const int32_t *idx,
                             cudaStream_t stream) {
-  if (args.T == 0) return cudaSuccess;
-  SsmArgs a = args;
-  a.n4 = a.N % 4 == 0;  // the entry point has checked the state's alignment
+  if (a.T == 0) return cudaSuccess;
   return a.f32 ? ssm::step_by_lanes<float>(a, state, slots, idx, stream)
                : ssm::step_by_lanes<__nv_bfloat16>(a, state, slots, idx, stream);
 }
