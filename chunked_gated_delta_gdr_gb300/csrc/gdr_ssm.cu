@@ -10,9 +10,9 @@
 //
 // The token axis is cut into ranges of equal length, whatever the segments are, so that a long
 // prompt fills the GPU and ragged ones stay balanced.  Pass 1 runs each range from a zero state
-// and keeps the state at its end and the sum of dt (a range's decay is e^{A sum dt}); a short
-// kernel chains these ends over the ranges; pass 2 runs each range from its true state and writes
-// y.  When one range is enough, only pass 2 runs.
+// and keeps the state at its end and the sum of dt (a range's decay is e^{A sum dt}); pass 2
+// chains the ends before its range, runs it from its true state and writes y.  When one range is
+// enough, only pass 2 runs.
 #include "gdr_ssm.cuh"
 
 namespace gdr {
@@ -24,10 +24,12 @@ using namespace mix;
 constexpr int kFwdCtas = 4;  // blocks of pass 2 on each SM: the ranges are cut to run all at once
 constexpr int kEndCtas = 5;
 constexpr int kAhead = 3;    // tiles in the rings
+constexpr int kLeast = 4;    // tiles of a range at least
+constexpr int kMostRanges = 32;
 
 struct Ranges {
   int range, n;      // tokens of a range, ranges
-  float *state;      // [n][D][N]: pass 1 the state at the end, after the chain the one at the start
+  float *state;      // [n][D][N]: the state at the end, from a zero state at the start
   float *sum;        // [n][D]: sum of dt from the last segment start in the range (or its start)
   int *reset;        // [n]: a segment starts in the range
 };
@@ -55,8 +57,8 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
   const Place<LN> P(a, tiles_per_group);
   const int r0 = P.r * rg.range, t1 = min(a.T, r0 + rg.range);
   const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
-  const R xr{ring, reinterpret_cast<const E *>(a.x.p) + P.c0 + lc, a.x.st};
-  const R dr{ring + R::kSlots, reinterpret_cast<const E *>(a.dt.p) + P.c0 + lc, a.dt.st};
+  R xr(ring, a.x.p, P.c0 + lc, a.x.st);
+  R dr(ring + R::kSlots, a.dt.p, P.c0 + lc, a.dt.st);
   const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
   for (int i = P.tid; i < CH; i += kThreads)
     s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
@@ -84,8 +86,8 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
       issue(stage == 0 ? Q - 1 : stage - 1, tb + (Q - 1) * L);
       copies_wait<Q - 1>();
       const int n = tb + lt < t1 ? nv : 0;
-      put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, xr.get(stage, tb + lt, n),
-                       dr.get(stage, tb + lt, n));
+      put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, xr.get(stage),
+                       dr.get(stage));
       stage = stage + 1 == Q ? 0 : stage + 1;
       rb.put(s.b);
       if (tb + L < t1) rb.fetch(Bp, a.B_st, tb + L, t1, a.N);
@@ -113,6 +115,32 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
       if (P.ch[k] < P.nch) rg.sum[(int64_t)P.r * a.D + P.c0 + P.ch[k]] = S[k];
   }
   if (P.ct == 0 && P.tid == 0) rg.reset[P.r] = reset;
+}
+
+// h = the state that enters range r: over the ranges before it, next = e^{A sum} state + end, or the
+// end alone where a segment starts in the range.  The ranges are few: each block of pass 2 does
+// this itself.
+template <int LN>
+__device__ __forceinline__ void entering_state(const SsmArgs &a, const Ranges &rg,
+                                               const Place<LN> &P, int r,
+                                               const float (&A2)[2][4], float (&h)[2][4]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[k][j] = 0.f;
+#pragma unroll 4
+  for (int q = 0; q < r; ++q) {
+    float end[2][4];
+    P.read(a, rg.state, q, end);
+    const bool reset = rg.reset[q] != 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float sum = P.ch[k] < P.nch ? rg.sum[(int64_t)q * a.D + P.c0 + P.ch[k]] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        h[k][j] = reset ? end[k][j] : fmaf(ex2(A2[k][j] * sum), h[k][j], end[k][j]);
+    }
+  }
 }
 
 template <int LN>
@@ -147,9 +175,9 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
   }
   const int t0 = P.r * rg.range, t1 = min(a.T, t0 + rg.range);
   const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
-  const R xr{ring, reinterpret_cast<const E *>(a.x.p) + P.c0 + lc, a.x.st};
-  const R dr{ring + R::kSlots, reinterpret_cast<const E *>(a.dt.p) + P.c0 + lc, a.dt.st};
-  const R zr{ring + 2 * R::kSlots, reinterpret_cast<const E *>(a.z.p) + P.c0 + lc, a.z.st};
+  R xr(ring, a.x.p, P.c0 + lc, a.x.st);
+  R dr(ring + R::kSlots, a.dt.p, P.c0 + lc, a.dt.st);
+  R zr(ring + 2 * R::kSlots, a.z.p, P.c0 + lc, a.z.st);
   const bool gated = a.z.p != nullptr;
   E *yp = reinterpret_cast<E *>(a.y.p) + P.c0 + lc;
   const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
@@ -174,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
   P.decays(a, A2);
   SegCursor cursor = seg_find(a.cu, a.n_seq, a.T, t0, s.red);
   int seg = cursor.j - 1;
-  P.read(a, P.r > 0 && seg >= 0 && seg < a.n_seq ? rg.state : nullptr, P.r, h);
+  entering_state<LN>(a, rg, P, seg >= 0 && seg < a.n_seq ? P.r : 0, A2, h);
   __syncthreads();
 
   // where this thread's partial sums of its two channels go in a token's row
@@ -204,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
     const int n = min(L, t1 - tb), k = lt < n ? nv : 0;
     issue(stage == 0 ? Q - 1 : stage - 1, tb + (Q - 1) * L);
     copies_wait<Q - 1>();
-    put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, xr.get(stage, tb + lt, k),
-                     dr.get(stage, tb + lt, k));
+    put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, xr.get(stage),
+                     dr.get(stage));
     rb.put(s.b);
     rc.put(s.c);
     if (P.warp == 0) {
@@ -257,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
     const int own = any ? s.seg[lt] : s.same;
     if (lt < n && own >= 0 && own < a.n_seq) {
       float x[8], v[8];
-      unpack8(xr.get(stage, tb + lt, k), x);
+      unpack8(xr.get(stage), x);
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
         const float4 w = *reinterpret_cast<const float4 *>(&s.skip[lc + i]);
@@ -268,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
         v[i + 3] = fmaf(w.w, x[i + 3], sum_parts<LN>(part + 3 * LN));
       }
       if (gated) {
-        unpack8(zr.get(stage, tb + lt, k), x);
+        unpack8(zr.get(stage), x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= x[i] * sigmoidf(x[i]);
       }
@@ -276,34 +304,6 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
     }
     stage = stage + 1 == Q ? 0 : stage + 1;
     __syncthreads();
-  }
-}
-
-// The state at the start of each range from the ends of pass 1: next = e^{A sum} state + end, or
-// the end alone where a segment starts in the range.
-__global__ void k_ssm_chain(const float *A, const Ranges rg, int D, int N) {
-  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, size = (int64_t)D * N;
-  if (i >= size) return;
-  const float A2 = A[i] * kLog2e;
-  const int d = (int)(i / N);
-  float cur = 0.f;
-  constexpr int U = 8;
-  for (int r0 = 0; r0 < rg.n; r0 += U) {
-    float end[U], sum[U];
-    int rs[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool ok = r0 + u < rg.n - 1;  // the last range's end goes nowhere
-      end[u] = ok ? rg.state[(r0 + u) * size + i] : 0.f;
-      sum[u] = ok ? rg.sum[(int64_t)(r0 + u) * D + d] : 0.f;
-      rs[u] = ok ? rg.reset[r0 + u] : 1;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (r0 + u < rg.n) {
-        rg.state[(r0 + u) * size + i] = cur;
-        cur = rs[u] ? end[u] : fmaf(ex2(A2 * sum[u]), cur, end[u]);
-      }
   }
 }
 
@@ -428,14 +428,15 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Tokens of a range: as many ranges as run at once, of at least 8 tiles.  Fewer would leave SMs
+// Tokens of a range: as many ranges as run at once, of at least kLeast tiles.  Fewer would leave SMs
 // idle, more would only repeat pass 1 for more tokens.
 int range_for(int64_t T, int32_t D, int32_t N, int32_t G) {
   const int LN = lanes_for(N), tile = 4 * LN;
   const int64_t ctiles = channel_tiles(D, G, LN);
   int64_t n = (int64_t)sm_count() * kFwdCtas / ctiles;
-  const int64_t most = ceil_div64(T, 8 * tile);
+  const int64_t most = ceil_div64(T, kLeast * tile);
   if (n > most) n = most;
+  if (n > kMostRanges) n = kMostRanges;
   if (n < 1) n = 1;
   const int64_t r = ceil_div64(ceil_div64(T, n), tile) * tile;
   return (int)(r < tile ? tile : r);
@@ -479,9 +480,6 @@ cudaError_t run_fwd(const SsmArgs &a, cudaStream_t stream) {
       return e;
     k_ssm_ends<E, LN, VEC>
         <<<(unsigned)((int64_t)ctiles * (c.rg.n - 1)), kThreads, smem1, stream>>>(a, c.rg, tpg);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    k_ssm_chain<<<(unsigned)ceil_div64((int64_t)a.D * a.N, 128), 128, 0, stream>>>(a.A, c.rg, a.D,
-                                                                                   a.N);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const int64_t blocks = (int64_t)ctiles * (c.rg.n + (a.ht ? 1 : 0));

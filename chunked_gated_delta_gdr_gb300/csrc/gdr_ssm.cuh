@@ -168,24 +168,35 @@ struct BcTile {
 // A thread's 8 elements of each tile of x (dt, z, dout) on their way into shared memory, S tiles
 // in a ring in which each thread reads only what it copied itself: they take no registers while
 // they wait.  Elements that were not copied (n = 0: no token or no channel) read as anything.
-// Without 16-byte alignment they are loaded when they are used.
+// Without 16-byte alignment they wait in registers, one tile ahead.  issue is called for each tile
+// in turn, S - 1 tiles before its get.
 template <typename E, bool VEC, int S_>
 struct TileRing {
-  static constexpr int S = S_, P = (int)sizeof(E) / 2;
+  static constexpr int S = VEC ? S_ : 2, P = (int)sizeof(E) / 2;
   static constexpr int kSlots = VEC ? S * P * kThreads : 0;
   uint4 *ring;
   const E *p;
   int64_t st;
+  mix::Raw8<E> now, next;
 
-  __device__ __forceinline__ void issue(int s, int t, int n) const {
-    if (VEC && n > 0) {
+  __device__ __forceinline__ TileRing(uint4 *ring_, const void *base, int64_t at, int64_t st_)
+      : ring(ring_), p(reinterpret_cast<const E *>(base) + at), st(st_) {
+    if (!VEC) now = next = mix::zero8<E>();
+  }
+  __device__ __forceinline__ void issue(int s, int t, int n) {
+    if (VEC) {
+      if (n > 0) {
 #pragma unroll
-      for (int i = 0; i < P; ++i)
-        mix::copy16(ring + (s * P + i) * kThreads + threadIdx.x, p + t * st + i * 4);
+        for (int i = 0; i < P; ++i)
+          mix::copy16(ring + (s * P + i) * kThreads + threadIdx.x, p + t * st + i * 4);
+      }
+    } else {
+      now = next;
+      next = mix::ld8<false>(p + t * st, n);
     }
   }
-  __device__ __forceinline__ mix::Raw8<E> get(int s, int t, int n) const {
-    if (!VEC) return mix::ld8<VEC>(p + t * st, n);
+  __device__ __forceinline__ mix::Raw8<E> get(int s) const {
+    if (!VEC) return now;
     mix::Raw8<E> r;
     uint4 *w = reinterpret_cast<uint4 *>(&r);
 #pragma unroll

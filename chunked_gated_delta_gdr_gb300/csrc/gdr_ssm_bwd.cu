@@ -179,10 +179,10 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int t0 = P.r * kRange, n = min(kRange, a.T - t0);
   const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
   const int64_t c = P.c0 + lc;
-  const R xr{ring, reinterpret_cast<const E *>(a.x.p) + c, a.x.st};
-  const R dr{ring + R::kSlots, reinterpret_cast<const E *>(a.dt.p) + c, a.dt.st};
-  const R gr{ring + 2 * R::kSlots, reinterpret_cast<const E *>(a.dout.p) + c, a.dout.st};
-  const R zr{ring + 3 * R::kSlots, reinterpret_cast<const E *>(a.z.p) + c, a.z.st};
+  R xr(ring, a.x.p, c, a.x.st);
+  R dr(ring + R::kSlots, a.dt.p, c, a.dt.st);
+  R gr(ring + 2 * R::kSlots, a.dout.p, c, a.dout.st);
+  R zr(ring + 3 * R::kSlots, a.z.p, c, a.z.st);
   const bool gated = a.z.p != nullptr;
   const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
   const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
@@ -218,13 +218,13 @@ __global__ void __launch_bounds__(kThreads, 4)
     const int m = min(L, n - i0), t = t0 + i0 + lt, k = lt < m ? nv : 0;
     issue(stage == 0 ? Q - 1 : stage - 1, i0 + (Q - 1) * L);
     copies_wait<Q - 1>();
-    put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, xr.get(stage, t, k),
-                     dr.get(stage, t, k));
+    put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, xr.get(stage),
+                     dr.get(stage));
     {
       float g[8], z[8];
-      unpack8(gr.get(stage, t, k), g);
+      unpack8(gr.get(stage), g);
       if (gated) {
-        unpack8(zr.get(stage, t, k), z);
+        unpack8(zr.get(stage), z);
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] *= z[i] * sigmoidf(z[i]);
       }
