@@ -27,13 +27,6 @@ constexpr int kAhead = 3;    // tiles in the rings
 constexpr int kLeast = 4;    // tiles of a range at least
 constexpr int kMostRanges = 32;
 
-struct Ranges {
-  int range, n;      // tokens of a range, ranges
-  float *state;      // [n][D][N]: the state at the end, from a zero state at the start
-  float *sum;        // [n][D]: sum of dt from the last segment start in the range (or its start)
-  int *reset;        // [n]: a segment starts in the range
-};
-
 template <int LN>
 struct __align__(16) Tile1 {
   using Y = Lay<LN>;
@@ -442,35 +435,10 @@ int range_for(int64_t T, int32_t D, int32_t N, int32_t G) {
   return (int)(r < tile ? tile : r);
 }
 
-struct Carve {
-  Ranges rg;
-  size_t bytes;
-};
-Carve carve(void *work, int64_t T, int32_t D, int32_t N, int range) {
-  Carve c{};
-  c.rg.range = range;
-  c.rg.n = (int)ceil_div64(T, range);
-  if (c.rg.n <= 1) return c;
-  char *p = reinterpret_cast<char *>(work);
-  c.rg.state = reinterpret_cast<float *>(p);
-  size_t off = align256((size_t)c.rg.n * D * N * sizeof(float));
-  c.rg.sum = reinterpret_cast<float *>(p + off);
-  off += align256((size_t)c.rg.n * D * sizeof(float));
-  c.rg.reset = reinterpret_cast<int *>(p + off);
-  off += align256((size_t)c.rg.n * sizeof(int));
-  c.bytes = off;
-  return c;
-}
-
-template <typename K>
-cudaError_t allow_smem(K k, int bytes) {
-  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <typename E, int LN, bool VEC>
 cudaError_t run_fwd(const SsmArgs &a, cudaStream_t stream) {
   const int tpg = (int)ceil_div64(a.D / a.G, Lay<LN>::CH), ctiles = tpg * a.G;
-  const Carve c = carve(a.work, a.T, a.D, a.N, range_for(a.T, a.D, a.N, a.G));
+  const Carve c = carve_ranges(a.work, a.T, a.D, a.N, range_for(a.T, a.D, a.N, a.G));
   constexpr int slots = TileRing<E, VEC, kAhead>::kSlots * 16;
   constexpr int smem1 = (int)sizeof(Tile1<LN>) + 2 * slots,
                 smem2 = (int)sizeof(Tile2<LN>) + 3 * slots;
@@ -533,7 +501,11 @@ cudaError_t step_by_lanes(const SsmArgs &a, float *state, int32_t slots, const i
 }  // namespace ssm
 
 size_t ssm_fwd_workspace(int64_t T, int32_t D, int32_t N, int32_t G) {
-  return ssm::carve(nullptr, T, D, N, ssm::range_for(T, D, N, G)).bytes;
+  // the layout also goes by the tensors' alignment: room for either
+  const size_t lanes = ssm::carve_ranges(nullptr, T, D, N, ssm::range_for(T, D, N, G)).bytes;
+  const int wide = ssm::wide_range(T, D, N, G);
+  const size_t bytes = wide ? ssm::carve_ranges(nullptr, T, D, N, wide).bytes : 0;
+  return bytes > lanes ? bytes : lanes;
 }
 
 cudaError_t launch_ssm_fwd(const SsmArgs &args, cudaStream_t stream) {
@@ -542,6 +514,8 @@ cudaError_t launch_ssm_fwd(const SsmArgs &args, cudaStream_t stream) {
   a.n4 = states_ok(a);
   const bool vec = (a.D / a.G) % 8 == 0 && rows_ok(a.x, a.f32) && rows_ok(a.dt, a.f32) &&
                    rows_ok(a.z, a.f32) && rows_ok(a.y, a.f32) && bc_ok(a);
+  const int wide = vec ? wide_range(a.T, a.D, a.N, a.G) : 0;
+  if (wide) return launch_wide(a, wide, stream);
   return a.f32 ? fwd_by_lanes<float>(a, vec, stream)
                : fwd_by_lanes<__nv_bfloat16>(a, vec, stream);
 }

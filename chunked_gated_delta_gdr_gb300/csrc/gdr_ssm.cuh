@@ -262,6 +262,44 @@ inline bool states_ok(const SsmArgs &a) {
 
 inline int lanes_for(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
+// The ranges of the forward's scan, and what pass 1 leaves of each.
+struct Ranges {
+  int range, n;      // tokens of a range, ranges
+  float *state;      // [n][D][N]: the state at the end, from a zero state at the start
+  float *sum;        // [n][D]: sum of dt from the last segment start in the range (or its start)
+  int *reset;        // [n]: a segment starts in the range
+};
+
+struct Carve {
+  Ranges rg;
+  size_t bytes;
+};
+inline Carve carve_ranges(void *work, int64_t T, int32_t D, int32_t N, int range) {
+  Carve c{};
+  c.rg.range = range;
+  c.rg.n = (int)ceil_div64(T, range);
+  if (c.rg.n <= 1) return c;
+  char *p = reinterpret_cast<char *>(work);
+  c.rg.state = reinterpret_cast<float *>(p);
+  size_t off = align256((size_t)c.rg.n * D * N * sizeof(float));
+  c.rg.sum = reinterpret_cast<float *>(p + off);
+  off += align256((size_t)c.rg.n * D * sizeof(float));
+  c.rg.reset = reinterpret_cast<int *>(p + off);
+  off += align256((size_t)c.rg.n * sizeof(int));
+  c.bytes = off;
+  return c;
+}
+
+template <typename K>
+cudaError_t allow_smem(K k, int bytes) {
+  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// The layout of one thread a channel (gdr_ssm_wide.cu): its tokens of a range where it is worth
+// while (aligned rows), else 0.
+int wide_range(int64_t T, int32_t D, int32_t N, int32_t G);
+cudaError_t launch_wide(const SsmArgs &a, int range, cudaStream_t stream);
+
 inline int64_t channel_tiles(int D, int G, int LN) {
   return (int64_t)G * ceil_div64(D / G, 256 / LN);
 }

@@ -746,7 +746,7 @@ __global__ void k_ssm_bc_sums(const float *bc, int64_t T, int G, int N, int NP, 
   st1((kind ? dC : dB) + (t * G + grp) * N + m, (s[0] + s[1]) + (s[2] + s[3]));
 }
 
-BwdWork carve(void *work, int64_t T, int32_t D, int32_t N, int32_t G) {
+BwdWork carve_bwd(void *work, int64_t T, int32_t D, int32_t N, int32_t G) {
   BwdWork w{};
   w.n = (int)ceil_div64(T, kRange);
   const int LN = lanes_for(N);
@@ -772,7 +772,7 @@ BwdWork carve(void *work, int64_t T, int32_t D, int32_t N, int32_t G) {
 template <typename E, int LN, bool VEC>
 cudaError_t run_bwd(const SsmArgs &a, cudaStream_t stream) {
   const int tpg = (int)ceil_div64(a.D / a.G, Lay<LN>::CH), ctiles = tpg * a.G;
-  const BwdWork w = carve(a.work, a.T, a.D, a.N, a.G);
+  const BwdWork w = carve_bwd(a.work, a.T, a.D, a.N, a.G);
   constexpr int smem1 = (int)sizeof(Tile1<LN>) + 4 * 16 * TileRing<E, VEC, 2>::kSlots;
   constexpr int smem2 = (int)sizeof(Tile2<LN>);
   cudaError_t e = cudaFuncSetAttribute(k_ssm_bwd<E, LN, VEC>,
@@ -819,7 +819,7 @@ cudaError_t by_lanes(const SsmArgs &a, bool vec, cudaStream_t stream) {
 }  // namespace ssm
 
 size_t ssm_bwd_workspace(int64_t T, int32_t D, int32_t N, int32_t G) {
-  return ssm::carve(nullptr, T, D, N, G).bytes;
+  return ssm::carve_bwd(nullptr, T, D, N, G).bytes;
 }
 
 cudaError_t launch_ssm_bwd(const SsmArgs &args, cudaStream_t stream) {

@@ -277,6 +277,27 @@ def test_ssm_long_prompt_cut_into_ranges_agrees_with_one_range():
     assert_close(ht, hr, 400, "final state")
 
 
+@pytest.mark.parametrize("N,G,dtype,z,state", [(16, 1, BF16, True, True), (6, 2, F32, False, True),
+                                               (12, 1, F32, True, False)])
+def test_ssm_with_much_work(N, G, dtype, z, state):
+    """Enough tokens and channels for the layout of one thread a channel, with segments that start,
+    end and are missing inside its ranges.  The steps remembered are about 1 / (dt |A|): 400."""
+    T, D = 5003, 4096 if G == 1 else 3872
+    cu = [3, 3, 700, 701, 2900, 2900, 2917, 4980]
+    i = ssm_inputs(T, 7, D, N, G, dtype, z, True, True, True, state, 21)
+    y0 = torch.full((T, D), 7.0, dtype=dtype, device=DEV)
+    y, ht = gdr.ssm_fwd(*[dev(i[k]) for k in ("x", "dt", "A", "B", "C")], D=dev(i["D"]),
+                        z=dev(i["z"]), dt_bias=dev(i["dt_bias"]), initial_state=dev(i["h0"]),
+                        cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV),
+                        output_final_state=True, out=y0)
+    d = {k: None if v is None else v.double() for k, v in i.items()}
+    yr, hr, mask = ref.ssm(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], d["z"], d["dt_bias"],
+                           True, d["h0"], cu)
+    assert_close(y.cpu()[mask], yr[mask], 400, "y")
+    assert torch.all(y.cpu()[~mask] == 7.0)
+    assert_close(ht, hr, 400, "final state")
+
+
 @pytest.mark.parametrize("B,D,N,G,dtype,odd", [(1, 64, 16, 1, BF16, False),
                                                (5, 100, 16, 2, F32, False),
                                                (4, 48, 5, 1, BF16, True),
