@@ -18,7 +18,7 @@ namespace gdr {
 namespace mix {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;  // of a step's block; the others' TH: 128, or 32 for few channels
 constexpr int kTile = 16;  // tokens between two looks at the segment bounds
 constexpr int kFwdCtas = 3;  // blocks on each SM: all of them run at once
 constexpr int kBwdCtas = 2;
@@ -174,18 +174,18 @@ __device__ __forceinline__ Raw8<E> output(const f2 (&w)[W][4], const f2 (&bias)[
 // A thread's next rows on their way into shared memory: groups of G tokens, S of them in a ring in
 // which each thread reads only what it copied itself.  Without 16-byte alignment rows are loaded
 // when they are used.
-template <typename E, bool VEC, int G_, int S_>
+template <typename E, bool VEC, int G_, int S_, int TH>
 struct Ahead {
   static constexpr int G = G_, S = S_;
   static constexpr int P = (int)sizeof(E) / 2;  // 16-byte parts of a row's 8 elements
-  static constexpr int kSlots = VEC ? S * G * P * kThreads : 0;
+  static constexpr int kSlots = VEC ? S * G * P * TH : 0;
   uint4 *ring;
   const E *x;
   int64_t st;
   int nv, end;
 
   __device__ __forceinline__ uint4 *at(int s, int g) const {
-    return ring + ((s * G + g) * P) * kThreads + threadIdx.x;
+    return ring + ((s * G + g) * P) * TH + threadIdx.x;
   }
   __device__ __forceinline__ void issue(int s, int t) const {
     if (VEC) {
@@ -194,7 +194,7 @@ struct Ahead {
       for (int g = 0; g < G; ++g) {
         if (t + g < end && nv > 0) {
 #pragma unroll
-          for (int i = 0; i < P; ++i) copy16(at(s, g) + i * kThreads, p + i * 4);
+          for (int i = 0; i < P; ++i) copy16(at(s, g) + i * TH, p + i * 4);
         }
         p += st;
       }
@@ -211,7 +211,7 @@ struct Ahead {
     if (VEC) {
       uint4 *w = reinterpret_cast<uint4 *>(&r);
 #pragma unroll
-      for (int i = 0; i < P; ++i) w[i] = at(s, g)[i * kThreads];
+      for (int i = 0; i < P; ++i) w[i] = at(s, g)[i * TH];
     } else {
       r = ld8<VEC>(x + (int64_t)t * st, nv);
     }
@@ -219,20 +219,20 @@ struct Ahead {
   }
 };
 // the forward's and the backward's (x and dy), less deep in fp32: a row is twice the bytes
-template <typename E, bool VEC>
-using FwdAhead = Ahead<E, VEC, 4, sizeof(E) == 2 ? 4 : 2>;
-template <typename E, bool VEC>
-using BwdAhead = Ahead<E, VEC, sizeof(E) == 2 ? 4 : 2, 2>;
+template <typename E, bool VEC, int TH>
+using FwdAhead = Ahead<E, VEC, 4, sizeof(E) == 2 ? 4 : 2, TH>;
+template <typename E, bool VEC, int TH>
+using BwdAhead = Ahead<E, VEC, sizeof(E) == 2 ? 4 : 2, 2, TH>;
 
-template <typename E, int W, bool VEC>
-__global__ void __launch_bounds__(kThreads, kFwdCtas)
+template <typename E, int W, bool VEC, int TH>
+__global__ void __launch_bounds__(TH, kFwdCtas * kThreads / TH)
     k_conv_fwd(const ConvArgs a, int range, int cblocks, int nranges) {
-  using R = FwdAhead<E, VEC>;
+  using R = FwdAhead<E, VEC, TH>;
   constexpr int G = R::G, S = R::S;
   __shared__ Marks m;
   extern __shared__ __align__(16) uint4 ring[];
   const int cb = blockIdx.x % cblocks, r = blockIdx.x / cblocks;
-  const int c0 = (cb * kThreads + threadIdx.x) * 8, nv = max(0, min(8, a.C - c0));
+  const int c0 = (cb * TH + threadIdx.x) * 8, nv = max(0, min(8, a.C - c0));
   if (r == nranges) {
     empty_rows<E, VEC>(a, W - 1, a.h0, a.ht, c0, nv, m.red);
     return;
@@ -320,15 +320,15 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
 // The backward over the same ranges.  acc[j] gathers the gradient of the input j + 1 tokens back
 // until its last tap is in.  A range owns the gradients of its own tokens and of the initial
 // states of the segments that start in it; it runs on W - 1 tokens into the next range for them.
-template <typename E, int W, bool VEC>
-__global__ void __launch_bounds__(kThreads, kBwdCtas)
+template <typename E, int W, bool VEC, int TH>
+__global__ void __launch_bounds__(TH, kBwdCtas * kThreads / TH)
     k_conv_bwd(const ConvArgs a, int range, int cblocks, int nranges) {
-  using R = BwdAhead<E, VEC>;
+  using R = BwdAhead<E, VEC, TH>;
   constexpr int G = R::G, S = R::S;
   __shared__ Marks m;
   extern __shared__ __align__(16) uint4 ring[];
   const int cb = blockIdx.x % cblocks, r = blockIdx.x / cblocks;
-  const int c0 = (cb * kThreads + threadIdx.x) * 8, nv = max(0, min(8, a.C - c0));
+  const int c0 = (cb * TH + threadIdx.x) * 8, nv = max(0, min(8, a.C - c0));
   if (r == nranges) {
     empty_rows<E, VEC>(a, W - 1, a.dht, a.dh0, c0, nv, m.red);
     return;
@@ -554,46 +554,62 @@ bool rows_ok(const Mat &m, bool f32) {
   return !m.p || (aligned16(m.p) && m.st % (f32 ? 4 : 8) == 0);
 }
 
-int conv_ranges(int64_t T, int32_t C, int ctas_per_sm) {
-  const int64_t cblocks = ceil_div64(C, kThreads * 8);
-  int64_t n = (int64_t)sm_count() * ctas_per_sm / cblocks;
-  const int64_t most = ceil_div64(T, 4 * kTile);
+// How the channels and tokens are cut: blocks of 32 threads (256 channels) where blocks of 128
+// would leave a quarter of their threads without channels, and as many ranges as run at once, of
+// at least one tile of tokens.
+struct Plan {
+  int threads, cblocks, range, nranges;
+};
+Plan plan_for(int64_t T, int32_t C, int ctas) {
+  Plan p;
+  p.threads = ceil_div64(C, kThreads * 8) * kThreads * 8 * 3 > (int64_t)C * 4 ? 32 : kThreads;
+  p.cblocks = (int)ceil_div64(C, p.threads * 8);
+  int64_t n = (int64_t)sm_count() * ctas * (kThreads / p.threads) / p.cblocks;
+  const int64_t most = ceil_div64(T, kTile);
   if (n > most) n = most;
-  return (int)(n < 1 ? 1 : n);
-}
-int range_of(int64_t T, int n) {
+  if (n < 1) n = 1;
   const int64_t r = ceil_div64(ceil_div64(T, n), kTile) * kTile;
-  return (int)(r < kTile ? kTile : r);
+  p.range = (int)(r < kTile ? kTile : r);
+  p.nranges = (int)ceil_div64(T, p.range);
+  return p;
 }
 
-template <typename E, int W, bool VEC>
-cudaError_t run_fwd(const ConvArgs &a, cudaStream_t stream) {
-  const int cblocks = (int)ceil_div64(a.C, kThreads * 8);
-  const int range = range_of(a.T, conv_ranges(a.T, a.C, kFwdCtas));
-  const int nranges = (int)ceil_div64(a.T, range);
-  const int64_t blocks = (int64_t)cblocks * (nranges + (a.ht ? 1 : 0));
+template <typename E, int W, bool VEC, int TH>
+cudaError_t fwd_threads(const ConvArgs &a, const Plan &p, cudaStream_t stream) {
+  const int64_t blocks = (int64_t)p.cblocks * (p.nranges + (a.ht ? 1 : 0));
   if (blocks == 0) return cudaSuccess;
-  constexpr int smem = FwdAhead<E, VEC>::kSlots * 16;
+  constexpr int smem = FwdAhead<E, VEC, TH>::kSlots * 16;
   static_assert(smem <= 46 * 1024, "more shared memory than a launch has without asking");
-  k_conv_fwd<E, W, VEC><<<(unsigned)blocks, kThreads, smem, stream>>>(a, range, cblocks, nranges);
+  k_conv_fwd<E, W, VEC, TH><<<(unsigned)blocks, TH, smem, stream>>>(a, p.range, p.cblocks,
+                                                                    p.nranges);
   return cudaGetLastError();
 }
-
 template <typename E, int W, bool VEC>
-cudaError_t run_bwd(const ConvArgs &a, cudaStream_t stream) {
-  const int cblocks = (int)ceil_div64(a.C, kThreads * 8);
-  const int range = range_of(a.T, conv_ranges(a.T, a.C, kBwdCtas));
-  const int nranges = (int)ceil_div64(a.T, range);
-  const int64_t blocks = (int64_t)cblocks * (nranges + (a.dh0 ? 1 : 0));
-  constexpr int smem = 2 * BwdAhead<E, VEC>::kSlots * 16;
+cudaError_t run_fwd(const ConvArgs &a, cudaStream_t stream) {
+  const Plan p = plan_for(a.T, a.C, kFwdCtas);
+  return p.threads == 32 ? fwd_threads<E, W, VEC, 32>(a, p, stream)
+                         : fwd_threads<E, W, VEC, kThreads>(a, p, stream);
+}
+
+template <typename E, int W, bool VEC, int TH>
+cudaError_t bwd_threads(const ConvArgs &a, const Plan &p, cudaStream_t stream) {
+  const int64_t blocks = (int64_t)p.cblocks * (p.nranges + (a.dh0 ? 1 : 0));
+  constexpr int smem = 2 * BwdAhead<E, VEC, TH>::kSlots * 16;
   static_assert(smem <= 46 * 1024, "more shared memory than a launch has without asking");
   if (blocks > 0)
-    k_conv_bwd<E, W, VEC><<<(unsigned)blocks, kThreads, smem, stream>>>(a, range, cblocks, nranges);
+    k_conv_bwd<E, W, VEC, TH><<<(unsigned)blocks, TH, smem, stream>>>(a, p.range, p.cblocks,
+                                                                      p.nranges);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   k_conv_sum<<<dim3((unsigned)ceil_div64(a.C, 32), W + 1), 256, 0, stream>>>(
-      reinterpret_cast<const float *>(a.work), nranges, a.C, W, a.dw, a.db);
+      reinterpret_cast<const float *>(a.work), p.nranges, a.C, W, a.dw, a.db);
   return cudaGetLastError();
+}
+template <typename E, int W, bool VEC>
+cudaError_t run_bwd(const ConvArgs &a, cudaStream_t stream) {
+  const Plan p = plan_for(a.T, a.C, kBwdCtas);
+  return p.threads == 32 ? bwd_threads<E, W, VEC, 32>(a, p, stream)
+                         : bwd_threads<E, W, VEC, kThreads>(a, p, stream);
 }
 
 template <typename E, int W, bool VEC>
@@ -631,8 +647,8 @@ cudaError_t launch_conv_fwd(const ConvArgs &a, cudaStream_t stream) {
 }
 
 size_t conv_bwd_workspace(int64_t T, int32_t C, int32_t W) {
-  const int range = mix::range_of(T, mix::conv_ranges(T, C, mix::kBwdCtas));
-  return align256((size_t)ceil_div64(T, range) * (W + 1) * C * sizeof(float));
+  return align256((size_t)mix::plan_for(T, C, mix::kBwdCtas).nranges * (W + 1) * C *
+                  sizeof(float));
 }
 
 cudaError_t launch_conv_bwd(const ConvArgs &a, cudaStream_t stream) {

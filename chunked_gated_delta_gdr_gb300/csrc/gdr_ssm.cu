@@ -25,7 +25,6 @@ constexpr int kFwdCtas = 4;  // blocks of pass 2 on each SM: the ranges are cut 
 constexpr int kEndCtas = 5;
 constexpr int kAhead = 3;    // tiles in the rings
 constexpr int kLeast = 4;    // tiles of a range at least
-constexpr int kMostRanges = 32;
 
 template <int LN>
 struct __align__(16) Tile1 {
@@ -111,8 +110,8 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
 }
 
 // h = the state that enters range r: over the ranges before it, next = e^{A sum} state + end, or the
-// end alone where a segment starts in the range.  The ranges are few: each block of pass 2 does
-// this itself.
+// end alone where a segment starts in the range.  Where the ranges are few, each block of pass 2
+// does this itself: a launch less.
 template <int LN>
 __device__ __forceinline__ void entering_state(const SsmArgs &a, const Ranges &rg,
                                                const Place<LN> &P, int r,
@@ -133,6 +132,34 @@ __device__ __forceinline__ void entering_state(const SsmArgs &a, const Ranges &r
       for (int j = 0; j < 4; ++j)
         h[k][j] = reset ? end[k][j] : fmaf(ex2(A2[k][j] * sum), h[k][j], end[k][j]);
     }
+  }
+}
+
+// The states that enter the ranges, in the places of their ends: by a kernel of its own where the
+// ranges are many (chained).
+__global__ void k_ssm_chain(const float *A, const Ranges rg, int D, int N) {
+  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, size = (int64_t)D * N;
+  if (i >= size) return;
+  const float A2 = A[i] * kLog2e;
+  const int d = (int)(i / N);
+  float cur = 0.f;
+  constexpr int U = 16;
+  for (int r0 = 0; r0 < rg.n; r0 += U) {
+    float end[U], sum[U];
+    int rs[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool ok = r0 + u < rg.n - 1;  // the last range's end goes nowhere
+      end[u] = ok ? rg.state[(r0 + u) * size + i] : 0.f;
+      sum[u] = ok ? rg.sum[(int64_t)(r0 + u) * D + d] : 0.f;
+      rs[u] = ok ? rg.reset[r0 + u] : 1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r0 + u < rg.n) {
+        rg.state[(r0 + u) * size + i] = cur;
+        cur = rs[u] ? end[u] : fmaf(ex2(A2 * sum[u]), cur, end[u]);
+      }
   }
 }
 
@@ -195,7 +222,11 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
   P.decays(a, A2);
   SegCursor cursor = seg_find(a.cu, a.n_seq, a.T, t0, s.red);
   int seg = cursor.j - 1;
-  entering_state<LN>(a, rg, P, seg >= 0 && seg < a.n_seq ? P.r : 0, A2, h);
+  const bool enters = P.r > 0 && seg >= 0 && seg < a.n_seq;
+  if (rg.n > kChainRanges)
+    P.read(a, enters ? rg.state : nullptr, P.r, h);
+  else
+    entering_state<LN>(a, rg, P, enters ? P.r : 0, A2, h);
   __syncthreads();
 
   // where this thread's partial sums of its two channels go in a token's row
@@ -429,7 +460,6 @@ int range_for(int64_t T, int32_t D, int32_t N, int32_t G) {
   int64_t n = (int64_t)sm_count() * kFwdCtas / ctiles;
   const int64_t most = ceil_div64(T, kLeast * tile);
   if (n > most) n = most;
-  if (n > kMostRanges) n = kMostRanges;
   if (n < 1) n = 1;
   const int64_t r = ceil_div64(ceil_div64(T, n), tile) * tile;
   return (int)(r < tile ? tile : r);
@@ -449,6 +479,11 @@ cudaError_t run_fwd(const SsmArgs &a, cudaStream_t stream) {
     k_ssm_ends<E, LN, VEC>
         <<<(unsigned)((int64_t)ctiles * (c.rg.n - 1)), kThreads, smem1, stream>>>(a, c.rg, tpg);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (c.rg.n > kChainRanges) {
+      k_ssm_chain<<<(unsigned)ceil_div64((int64_t)a.D * a.N, 128), 128, 0, stream>>>(a.A, c.rg,
+                                                                                     a.D, a.N);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
   }
   const int64_t blocks = (int64_t)ctiles * (c.rg.n + (a.ht ? 1 : 0));
   if (blocks == 0) return cudaSuccess;

@@ -262,6 +262,8 @@ inline bool states_ok(const SsmArgs &a) {
 
 inline int lanes_for(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
+constexpr int kChainRanges = 16;  // more ranges than this are chained by a kernel of its own
+
 // The ranges of the forward's scan, and what pass 1 leaves of each.
 struct Ranges {
   int range, n;      // tokens of a range, ranges
