@@ -343,6 +343,12 @@ QK = [  # T, Hq, Hk, d, rot, interleaved, norm, weights, type, odd strides, eps
     (700, 1, 1, 64, 64, False, "rms", True, BF16, False, 1e-6),
     (5, 1, 0, 1, 0, False, "rms", True, F32, False, 1e-6),
     (0, 4, 4, 128, 128, False, "rms", True, BF16, False, 1e-6),
+    (33, 20, 5, 40, 40, False, "rms", True, BF16, False, 1e-6),
+    (18, 6, 3, 96, 96, False, "l2", True, F32, False, 1e-6),
+    (1300, 3, 2, 152, 88, False, "rms", True, BF16, False, 1e-6),
+    (27, 5, 1, 248, 248, True, "rms", True, BF16, False, 1e-6),
+    (35, 1, 1, 8, 8, False, "rms", True, F32, False, 1e-5),
+    (2500, 7, 2, 24, 8, False, "l2", False, BF16, False, 1e-6),
 ]
 
 
