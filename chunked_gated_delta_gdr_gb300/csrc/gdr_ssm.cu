@@ -140,27 +140,7 @@ __device__ __forceinline__ void entering_state(const SsmArgs &a, const Ranges &r
 __global__ void k_ssm_chain(const float *A, const Ranges rg, int D, int N) {
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, size = (int64_t)D * N;
   if (i >= size) return;
-  const float A2 = A[i] * kLog2e;
-  const int d = (int)(i / N);
-  float cur = 0.f;
-  constexpr int U = 16;
-  for (int r0 = 0; r0 < rg.n; r0 += U) {
-    float end[U], sum[U];
-    int rs[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool ok = r0 + u < rg.n - 1;  // the last range's end goes nowhere
-      end[u] = ok ? rg.state[(r0 + u) * size + i] : 0.f;
-      sum[u] = ok ? rg.sum[(int64_t)(r0 + u) * D + d] : 0.f;
-      rs[u] = ok ? rg.reset[r0 + u] : 1;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (r0 + u < rg.n) {
-        rg.state[(r0 + u) * size + i] = cur;
-        cur = rs[u] ? end[u] : fmaf(ex2(A2 * sum[u]), cur, end[u]);
-      }
-  }
+  chain_ranges(rg.state, rg.sum, rg.reset, rg.n, D, size, i, (int)(i / N), A[i] * kLog2e, false);
 }
 
 template <int LN>

@@ -262,6 +262,48 @@ inline bool states_ok(const SsmArgs &a) {
 
 inline int lanes_for(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
+// Replaces val[r] of state i, the end of range r from a zero state, by the state that enters the
+// range; with `back` the same for gradients, from the last range to the first.  A warp is alone on
+// its scheduler here and its instructions follow one another slowly: pointers that step from
+// range to range keep them few.
+__device__ __forceinline__ void chain_ranges(float *val, const float *sum, const int *reset, int n,
+                                             int D, int64_t size, int64_t i, int d, float A2,
+                                             bool back) {
+  const int64_t first = back ? n - 1 : 0;
+  val += first * size + i;
+  sum += first * D + d;
+  reset += first;
+  if (back) size = -size;
+  const int64_t dstep = back ? -(int64_t)D : D;
+  const int step = back ? -1 : 1;
+  float cur = 0.f;
+  auto batch = [&](auto U) {
+    float own[U.value], s[U.value];
+    int rs[U.value];
+    float *v = val;
+#pragma unroll
+    for (int u = 0; u < U.value; ++u) {
+      own[u] = *v;
+      s[u] = *sum;
+      rs[u] = *reset;
+      v += size;
+      sum += dstep;
+      reset += step;
+    }
+#pragma unroll
+    for (int u = 0; u < U.value; ++u) {
+      *val = cur;
+      cur = rs[u] ? own[u] : fmaf(mix::ex2(A2 * s[u]), cur, own[u]);
+      val += size;
+    }
+  };
+  int k = 0;
+  for (; k + 16 < n; k += 16) batch(std::integral_constant<int, 16>());
+  for (; k + 4 < n; k += 4) batch(std::integral_constant<int, 4>());
+  for (; k + 1 < n; ++k) batch(std::integral_constant<int, 1>());
+  *val = cur;  // the last range's end goes nowhere
+}
+
 constexpr int kChainRanges = 16;  // more ranges than this are chained by a kernel of its own
 
 // The ranges of the forward's scan, and what pass 1 leaves of each.

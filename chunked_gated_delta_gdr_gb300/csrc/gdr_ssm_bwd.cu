@@ -33,13 +33,17 @@ namespace {
 using namespace mix;
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kBwdCtas = 4;   // blocks on each SM
 constexpr int kBT = 8;        // tokens of a tile of pass 2
-constexpr int kRange = 64;    // tokens of a range
+constexpr int kRange = 64;    // tokens of a range at most
+// Ranges get shorter where the GPU has room for more blocks at once, and the chain over them stays
+// short.
+constexpr int kLeast = 16, kMostShort = 256;
 constexpr int kKept = kRange / kBT;  // states kept at most: tiles that continue a segment
 constexpr uint32_t kCols = 8 * (kKept + kBT);  // Tensor Memory columns: kept, then a tile's
 
 struct BwdWork {
-  int n;            // ranges
+  int range, n;     // tokens of a range, ranges
   float *state;     // [n][D][N]: states at the ranges' ends, then at their starts, then dA's parts
   float *grad;      // [n][D][N]: gradients at the ranges' starts, then at their ends
   float *sum;       // [n][D]: sum of dt
@@ -167,7 +171,7 @@ struct __align__(16) Tile1 {
 
 // Pass 1.
 template <typename E, int LN, bool VEC>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kBwdCtas)
     k_ssm_bwd_ends(const SsmArgs a, const BwdWork w, int tiles_per_group) {
   using Y = Lay<LN>;
   using R = TileRing<E, VEC, 2>;
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   Tile1<LN> &s = *reinterpret_cast<Tile1<LN> *>(smem_raw);
   uint4 *ring = reinterpret_cast<uint4 *>(&s + 1);
   const Place<LN> P(a, tiles_per_group);
-  const int t0 = P.r * kRange, n = min(kRange, a.T - t0);
+  const int t0 = P.r * w.range, n = min(w.range, a.T - t0);
   const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
   const int64_t c = P.c0 + lc;
   R xr(ring, a.x.p, c, a.x.st);
@@ -304,31 +308,9 @@ __global__ void __launch_bounds__(kThreads, 4)
 __global__ void k_ssm_bwd_chain(const float *A, const BwdWork w, int D, int N) {
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, size = (int64_t)D * N;
   if (i >= size) return;
-  const float A2 = A[i] * kLog2e;
-  const int d = (int)(i / N);
-  constexpr int U = 16;
   const bool back = blockIdx.y != 0;
-  float *val = back ? w.grad : w.state;
-  float cur = 0.f;
-  for (int r0 = 0; r0 < w.n; r0 += U) {
-    float own[U], sum[U];
-    int rs[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool ok = r0 + u < w.n;
-      const int64_t r = !ok ? 0 : back ? w.n - 1 - (r0 + u) : r0 + u;
-      own[u] = ok ? val[r * size + i] : 0.f;
-      sum[u] = ok ? w.sum[r * D + d] : 0.f;
-      rs[u] = ok ? w.reset[r] : 1;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (r0 + u < w.n) {
-        const int64_t r = back ? w.n - 1 - (r0 + u) : r0 + u;
-        val[r * size + i] = cur;
-        cur = rs[u] ? own[u] : fmaf(ex2(A2 * sum[u]), cur, own[u]);
-      }
-  }
+  chain_ranges(back ? w.grad : w.state, w.sum, w.reset, w.n, D, size, i, (int)(i / N),
+               A[i] * kLog2e, back);
 }
 
 template <int LN>
@@ -408,7 +390,7 @@ __device__ __forceinline__ int channel_sums(float (&v)[8], int lane) {
 
 // Pass 2.
 template <typename E, int LN, bool VEC>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kBwdCtas)
     k_ssm_bwd(const SsmArgs a, const BwdWork w, int tiles_per_group) {
   using Y = Lay<LN>;
   constexpr int NP = Y::NP, CH = Y::CH;
@@ -429,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     tc::tmem_alloc(&s.tmem, kCols);
     tc::tmem_relinquish();
   }
-  const int t0 = P.r * kRange, n = min(kRange, a.T - t0);
+  const int t0 = P.r * w.range, n = min(w.range, a.T - t0);
   const int lt = P.tid / (CH / M), lc = P.tid % (CH / M) * M, nv = max(0, min(M, P.nch - lc));
   const int64_t c = P.c0 + lc;
   const E *xp = reinterpret_cast<const E *>(a.x.p) + c, *dp = reinterpret_cast<const E *>(a.dt.p) + c;
@@ -748,9 +730,14 @@ __global__ void k_ssm_bc_sums(const float *bc, int64_t T, int G, int N, int NP, 
 
 BwdWork carve_bwd(void *work, int64_t T, int32_t D, int32_t N, int32_t G) {
   BwdWork w{};
-  w.n = (int)ceil_div64(T, kRange);
   const int LN = lanes_for(N);
-  const int64_t ctiles = channel_tiles(D, G, LN), R = w.n < 1 ? 1 : w.n;
+  const int64_t ctiles = channel_tiles(D, G, LN);
+  w.range = kRange;
+  while (w.range > kLeast && ceil_div64(T, w.range / 2) * ctiles <= sm_count() * kBwdCtas &&
+         ceil_div64(T, w.range / 2) <= kMostShort)
+    w.range /= 2;
+  w.n = (int)ceil_div64(T, w.range);
+  const int64_t R = w.n < 1 ? 1 : w.n;
   char *p = reinterpret_cast<char *>(work);
   size_t off = 0;
   auto take = [&](int64_t floats) {
