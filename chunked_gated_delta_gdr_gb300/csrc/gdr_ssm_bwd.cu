@@ -394,6 +394,10 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
     k_ssm_bwd(const SsmArgs a, const BwdWork w, int tiles_per_group) {
   using Y = Lay<LN>;
   constexpr int NP = Y::NP, CH = Y::CH;
+  // tokens of a tile unrolled: all of them outgrow the instruction cache (8,192 tokens of 2,048
+  // channels of 16 states with the forward: 848 us, by fours 824), but for two lanes a channel,
+  // where indexes in registers cost more (4,124 x 832 x 8: 176 and 198 us)
+  constexpr int kUnroll = LN > 2 ? 4 : kBT;
   constexpr int M = kBT * CH / kThreads;  // elements of x a thread has of a tile
   constexpr int LEFT = LN <= 4 ? 1 : LN / 4;  // channel sums left to a lane
   extern __shared__ __align__(16) char smem_raw[];
@@ -498,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
     fetch(q + 1, false);
     if (on) {
       __syncthreads();
-#pragma unroll
+#pragma unroll kUnroll
       for (int i = 0; i < kBT; ++i) advance(i, h);
       __syncthreads();
     }
@@ -551,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
 #pragma unroll
       for (int j = 0; j < 4; ++j) now[k][j] = before[k][j];
     keep8(hist, now);
-#pragma unroll
+#pragma unroll kUnroll
     for (int i = 0; i < kBT; ++i) {
       advance(i, now);
       if (i + 1 < kBT) keep8(hist + (i + 1) * 8, now);
@@ -566,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
     tc::tmem_st_wait();
     get8(hist + (kBT - 1) * 8, before);
     got8(before);
-#pragma unroll
+#pragma unroll kUnroll
     for (int i = kBT - 1; i >= 0; --i) {
       if (i > 0) get8(hist + (i - 1) * 8, next);
       const int at = i * Y::PT + P.pair;
