@@ -341,12 +341,90 @@ __device__ __forceinline__ void four(const float *p, int n, float (&f)[4]) {
 }
 
 // One token for each row: state slot idx[row] in place.  Bound by HBM: the states are read and
-// written once.  A thread holds 4 states of 4 neighbouring channels, so that a row's B and C serve
-// four channels and everything is read four elements at a time, all of it before anything is used.
-// VEC: every group of four (channels of a group, states) is whole and aligned.
-template <typename E, int LN, bool VEC>
+// written once.  A warp takes CW neighbouring channels of a row: LN lanes hold a channel's states,
+// 4 each, and K times PER channels follow one another, so that each of its K loads of states is one
+// run of 512 bytes.  What belongs to a channel alone (step size, skip, gate, output) is one lane's
+// each, and the sums over states come back to it.  128 rows of 4,096 x 16 states: 18 us with the
+// states in HBM (3.9 TB/s; launch, one fill and one drain of the GPU are half of it), 10 us from L2.
+template <typename E, int LN>
 __global__ void __launch_bounds__(kThreads)
     k_ssm_step(const SsmArgs a, float *state, int slots, const int32_t *idx, int cblocks) {
+  constexpr int PER = 32 / LN, K = LN < 8 ? LN : 8, CW = PER * K;
+  const int row = blockIdx.x / cblocks, lane = threadIdx.x & 31;
+  const int d0 = (blockIdx.x % cblocks * (kThreads / 32) + (threadIdx.x >> 5)) * CW;
+  if (d0 >= a.D) return;
+  const int slot = idx ? idx[row] : row, d = d0 + lane;
+  const bool own = lane < CW && d < a.D;  // lane's own channel
+  E *y = reinterpret_cast<E *>(a.y.p) + (int64_t)row * a.y.st + d;
+  if (slot < 0 || slot >= slots) {
+    if (own) st1(y, 0.f);
+    return;
+  }
+  const int g = lane / LN, nl = lane % LN, n0 = nl * 4;
+  const bool in = n0 < a.N;
+  const int64_t at = (int64_t)(d0 + g) * a.N + n0;
+  float *s = state + (int64_t)slot * a.D * a.N + at;
+  float4 h[K], A[K];
+#pragma unroll
+  for (int c = 0; c < K; ++c) {
+    const bool ok = in && d0 + g + c * PER < a.D;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    h[c] = ok ? *reinterpret_cast<const float4 *>(s + c * PER * a.N) : zero;
+    A[c] = ok ? *reinterpret_cast<const float4 *>(a.A + at + c * PER * a.N) : zero;
+  }
+  float B[4] = {0, 0, 0, 0}, C[4] = {0, 0, 0, 0}, x = 0.f, v = 0.f, z = 0.f, skip = 0.f;
+  if (in) {
+    const int grp = a.G == 1 ? 0 : d0 / (a.D / a.G);
+    four<true>(reinterpret_cast<const E *>(a.B) + (int64_t)row * a.B_st + grp * a.B_sg + n0, 4, B);
+    four<true>(reinterpret_cast<const E *>(a.C) + (int64_t)row * a.C_st + grp * a.C_sg + n0, 4, C);
+  }
+  if (own) {
+    x = ld1(reinterpret_cast<const E *>(a.x.p) + (int64_t)row * a.x.st + d);
+    v = ld1(reinterpret_cast<const E *>(a.dt.p) + (int64_t)row * a.dt.st + d);
+    if (a.z.p) z = ld1(reinterpret_cast<const E *>(a.z.p) + (int64_t)row * a.z.st + d);
+    if (a.dt_bias) v += a.dt_bias[d];
+    if (a.Dskip) skip = a.Dskip[d];
+    if (a.softplus) v = softplusf(v);
+  }
+  const float v2 = v * kLog2e, dx = v * x;
+  float part[K];
+#pragma unroll
+  for (int c = 0; c < K; ++c) {
+    const float w = __shfl_sync(0xffffffffu, v2, c * PER + g);
+    const float u = __shfl_sync(0xffffffffu, dx, c * PER + g);
+    h[c].x = fmaf(ex2(w * A[c].x), h[c].x, u * B[0]);
+    h[c].y = fmaf(ex2(w * A[c].y), h[c].y, u * B[1]);
+    h[c].z = fmaf(ex2(w * A[c].z), h[c].z, u * B[2]);
+    h[c].w = fmaf(ex2(w * A[c].w), h[c].w, u * B[3]);
+    if (in && d0 + g + c * PER < a.D) *reinterpret_cast<float4 *>(s + c * PER * a.N) = h[c];
+    part[c] = in ? fmaf(h[c].x, C[0], fmaf(h[c].y, C[1], fmaf(h[c].z, C[2], h[c].w * C[3]))) : 0.f;
+  }
+  // sums over a channel's lanes, each exchange halving what a lane sums
+#pragma unroll
+  for (int o = LN / 2, k = K; o > 0; o >>= 1) {
+    const bool hi = nl & o;
+    if (k > 1) {
+      k /= 2;
+#pragma unroll
+      for (int c = 0; c < k; ++c) {
+        const float send = hi ? part[c] : part[c + k];
+        part[c] = (hi ? part[c + k] : part[c]) + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+    } else {
+      part[0] += __shfl_xor_sync(0xffffffffu, part[0], o);
+    }
+  }
+  const int q = lane % CW;  // channel q's sum: lane q / PER (K of LN hold one) of group q % PER
+  float sum = __shfl_sync(0xffffffffu, part[0], q % PER * LN + q / PER * (LN / K));
+  sum = fmaf(skip, x, sum);
+  if (a.z.p) sum *= z * sigmoidf(z);
+  if (own) st1(y, sum);
+}
+
+// The same for any alignment and any groups: a thread holds 4 states of 4 neighbouring channels.
+template <typename E, int LN>
+__global__ void __launch_bounds__(kThreads)
+    k_ssm_step_any(const SsmArgs a, float *state, int slots, const int32_t *idx, int cblocks) {
   constexpr int CB = kThreads / LN * 4;  // channels of a block
   const int row = blockIdx.x / cblocks;
   const int d0 = blockIdx.x % cblocks * CB + threadIdx.x / LN * 4, n0 = threadIdx.x % LN * 4;
@@ -377,30 +455,24 @@ __global__ void __launch_bounds__(kThreads)
   if (on) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (VEC || c < nd) {
-        four<VEC>(s + c * a.N, nn, h[c]);
-        four<VEC>(a.A + at + c * a.N, nn, A[c]);
+      if (c < nd) {
+        four<false>(s + c * a.N, nn, h[c]);
+        four<false>(a.A + at + c * a.N, nn, A[c]);
       }
-    if (VEC) {
-      four<VEC>(Bp + d0 / Dg * a.B_sg, nn, B);
-      four<VEC>(Cp + d0 / Dg * a.C_sg, nn, C);
-    }
   }
   if (nd > 0) {
-    four<VEC>(reinterpret_cast<const E *>(a.x.p) + (int64_t)row * a.x.st + d0, nd, x);
-    four<VEC>(reinterpret_cast<const E *>(a.dt.p) + (int64_t)row * a.dt.st + d0, nd, dt);
-    if (a.z.p) four<VEC>(reinterpret_cast<const E *>(a.z.p) + (int64_t)row * a.z.st + d0, nd, z);
-    if (a.dt_bias) four<VEC>(a.dt_bias + d0, nd, bias);
-    if (a.Dskip) four<VEC>(a.Dskip + d0, nd, skip);
+    four<false>(reinterpret_cast<const E *>(a.x.p) + (int64_t)row * a.x.st + d0, nd, x);
+    four<false>(reinterpret_cast<const E *>(a.dt.p) + (int64_t)row * a.dt.st + d0, nd, dt);
+    if (a.z.p) four<false>(reinterpret_cast<const E *>(a.z.p) + (int64_t)row * a.z.st + d0, nd, z);
+    if (a.dt_bias) four<false>(a.dt_bias + d0, nd, bias);
+    if (a.Dskip) four<false>(a.Dskip + d0, nd, skip);
   }
   if (on) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      if (!VEC) {
-        if (c >= nd) break;
-        four<VEC>(Bp + (d0 + c) / Dg * a.B_sg, nn, B);
-        four<VEC>(Cp + (d0 + c) / Dg * a.C_sg, nn, C);
-      }
+      if (c >= nd) break;
+      four<false>(Bp + (d0 + c) / Dg * a.B_sg, nn, B);
+      four<false>(Cp + (d0 + c) / Dg * a.C_sg, nn, C);
       float v = dt[c] + bias[c];
       if (a.softplus) v = softplusf(v);
       const float dx = v * x[c];
@@ -409,14 +481,9 @@ __global__ void __launch_bounds__(kThreads)
         h[c][j] = fmaf(ex2(v * (A[c][j] * kLog2e)), h[c][j], dx * B[j]);
         part[c] = fmaf(h[c][j], C[j], part[c]);
       }
-      if (VEC) {
-        *reinterpret_cast<float4 *>(s + c * a.N) =
-            make_float4(h[c][0], h[c][1], h[c][2], h[c][3]);
-      } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < nn) s[c * a.N + j] = h[c][j];
-      }
+      for (int j = 0; j < 4; ++j)
+        if (j < nn) s[c * a.N + j] = h[c][j];
     }
   }
 #pragma unroll
@@ -489,20 +556,22 @@ cudaError_t fwd_by_lanes(const SsmArgs &a, bool vec, cudaStream_t stream) {
 template <typename E, int LN>
 cudaError_t run_step(const SsmArgs &a, float *state, int32_t slots, const int32_t *idx,
                      cudaStream_t stream) {
-  const int64_t cblocks = ceil_div64(a.D, kThreads / LN * 4);
-  const unsigned blocks = (unsigned)(cblocks * a.T);
-  const uintptr_t four = a.f32 ? 15 : 7;  // four activations
+  constexpr int CW = 32 / LN * (LN < 8 ? LN : 8);  // channels of a warp
+  const uintptr_t four = a.f32 ? 15 : 7;           // four elements of B and C
   auto fit = [&](const void *p, int64_t st, int64_t sg) {
     return (reinterpret_cast<uintptr_t>(p) & four) == 0 && ((st | sg) & 3) == 0;
   };
-  const bool vec = a.N % 4 == 0 && (a.D / a.G) % 4 == 0 && fit(a.B, a.B_st, a.B_sg) &&
-                   fit(a.C, a.C_st, a.C_sg) && fit(a.x.p, a.x.st, 0) &&
-                   fit(a.dt.p, a.dt.st, 0) && fit(a.z.p, a.z.st, 0) && aligned16(a.dt_bias) &&
-                   aligned16(a.Dskip);  // the entry point has checked the states and A
-  if (vec)
-    k_ssm_step<E, LN, true><<<blocks, kThreads, 0, stream>>>(a, state, slots, idx, (int)cblocks);
-  else
-    k_ssm_step<E, LN, false><<<blocks, kThreads, 0, stream>>>(a, state, slots, idx, (int)cblocks);
+  // (the entry point has checked the states' alignment)
+  if (a.N % 4 == 0 && aligned16(a.A) && (a.G == 1 || a.D / a.G % CW == 0) &&
+      fit(a.B, a.B_st, a.B_sg) && fit(a.C, a.C_st, a.C_sg)) {
+    const int64_t cblocks = ceil_div64(a.D, kThreads / 32 * CW);
+    k_ssm_step<E, LN><<<(unsigned)(cblocks * a.T), kThreads, 0, stream>>>(a, state, slots, idx,
+                                                                         (int)cblocks);
+  } else {
+    const int64_t cblocks = ceil_div64(a.D, kThreads / LN * 4);
+    k_ssm_step_any<E, LN><<<(unsigned)(cblocks * a.T), kThreads, 0, stream>>>(
+        a, state, slots, idx, (int)cblocks);
+  }
   return cudaGetLastError();
 }
 template <typename E>

@@ -303,7 +303,13 @@ def test_ssm_with_much_work(N, G, dtype, z, state):
                                                (4, 48, 5, 1, BF16, True),
                                                (3, 40, 64, 1, BF16, False),
                                                (3, 40, 8, 1, F32, False),
-                                               (3, 24, 30, 1, F32, True)])
+                                               (3, 24, 30, 1, F32, True),
+                                               (3, 128, 16, 2, BF16, False),
+                                               (4, 70, 12, 1, F32, False),
+                                               (3, 33, 32, 1, BF16, False),
+                                               (2, 9, 4, 1, BF16, False),
+                                               (3, 96, 64, 3, F32, False),
+                                               (3, 1000, 16, 1, BF16, False)])
 def test_ssm_step(B, D, N, G, dtype, odd):
     i = ssm_inputs(B, 1, D, N, G, dtype, True, True, True, True, False, B + D)
     gen = torch.Generator().manual_seed(9)
