@@ -227,6 +227,7 @@ using BwdAhead = Ahead<E, VEC, sizeof(E) == 2 ? 4 : 2, 2, TH>;
 template <typename E, int W, bool VEC, int TH>
 __global__ void __launch_bounds__(TH, kFwdCtas * kThreads / TH)
     k_conv_fwd(const ConvArgs a, int range, int cblocks, int nranges) {
+  after_previous();
   using R = FwdAhead<E, VEC, TH>;
   constexpr int G = R::G, S = R::S;
   __shared__ Marks m;
@@ -323,6 +324,7 @@ __global__ void __launch_bounds__(TH, kFwdCtas * kThreads / TH)
 template <typename E, int W, bool VEC, int TH>
 __global__ void __launch_bounds__(TH, kBwdCtas * kThreads / TH)
     k_conv_bwd(const ConvArgs a, int range, int cblocks, int nranges) {
+  after_previous();
   using R = BwdAhead<E, VEC, TH>;
   constexpr int G = R::G, S = R::S;
   __shared__ Marks m;
@@ -495,6 +497,7 @@ __global__ void __launch_bounds__(TH, kBwdCtas * kThreads / TH)
 // Sums the ranges' parts of dw and db: 32 channels a block, its 8 warps taking every 8th range.
 __global__ void __launch_bounds__(256)
     k_conv_sum(const float *work, int nranges, int C, int W, float *dw, float *db) {
+  after_previous<true>();
   __shared__ float part[8][32];
   const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane, k = blockIdx.y;
@@ -523,6 +526,7 @@ __global__ void __launch_bounds__(256)
 
 template <typename E, int W, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_conv_step(const ConvStepArgs a, int cblocks) {
+  after_previous<true>();
   const int c0 = (blockIdx.x % cblocks * kThreads + threadIdx.x) * 8, row = blockIdx.x / cblocks;
   const int nv = max(0, min(8, a.C - c0));
   if (nv == 0) return;
@@ -580,9 +584,8 @@ cudaError_t fwd_threads(const ConvArgs &a, const Plan &p, cudaStream_t stream) {
   if (blocks == 0) return cudaSuccess;
   constexpr int smem = FwdAhead<E, VEC, TH>::kSlots * 16;
   static_assert(smem <= 46 * 1024, "more shared memory than a launch has without asking");
-  k_conv_fwd<E, W, VEC, TH><<<(unsigned)blocks, TH, smem, stream>>>(a, p.range, p.cblocks,
-                                                                    p.nranges);
-  return cudaGetLastError();
+  return launch(k_conv_fwd<E, W, VEC, TH>, (unsigned)blocks, TH, smem, stream, a, p.range,
+                p.cblocks, p.nranges);
 }
 template <typename E, int W, bool VEC>
 cudaError_t run_fwd(const ConvArgs &a, cudaStream_t stream) {
@@ -596,14 +599,13 @@ cudaError_t bwd_threads(const ConvArgs &a, const Plan &p, cudaStream_t stream) {
   const int64_t blocks = (int64_t)p.cblocks * (p.nranges + (a.dh0 ? 1 : 0));
   constexpr int smem = 2 * BwdAhead<E, VEC, TH>::kSlots * 16;
   static_assert(smem <= 46 * 1024, "more shared memory than a launch has without asking");
-  if (blocks > 0)
-    k_conv_bwd<E, W, VEC, TH><<<(unsigned)blocks, TH, smem, stream>>>(a, p.range, p.cblocks,
-                                                                      p.nranges);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  k_conv_sum<<<dim3((unsigned)ceil_div64(a.C, 32), W + 1), 256, 0, stream>>>(
-      reinterpret_cast<const float *>(a.work), p.nranges, a.C, W, a.dw, a.db);
-  return cudaGetLastError();
+  cudaError_t e;
+  if (blocks > 0 &&
+      (e = launch(k_conv_bwd<E, W, VEC, TH>, (unsigned)blocks, TH, smem, stream, a, p.range,
+                  p.cblocks, p.nranges)) != cudaSuccess)
+    return e;
+  return launch(k_conv_sum, dim3((unsigned)ceil_div64(a.C, 32), W + 1), 256, 0, stream,
+                reinterpret_cast<const float *>(a.work), p.nranges, a.C, W, a.dw, a.db);
 }
 template <typename E, int W, bool VEC>
 cudaError_t run_bwd(const ConvArgs &a, cudaStream_t stream) {
@@ -615,8 +617,8 @@ cudaError_t run_bwd(const ConvArgs &a, cudaStream_t stream) {
 template <typename E, int W, bool VEC>
 cudaError_t run_step(const ConvStepArgs &a, cudaStream_t stream) {
   const int cblocks = (int)ceil_div64(a.C, kThreads * 8);
-  k_conv_step<E, W, VEC><<<(unsigned)((int64_t)cblocks * a.B), kThreads, 0, stream>>>(a, cblocks);
-  return cudaGetLastError();
+  return launch(k_conv_step<E, W, VEC>, (unsigned)((int64_t)cblocks * a.B), kThreads, 0, stream, a,
+                cblocks);
 }
 
 #define GDR_CONV_DISPATCH(run, f32, W, vec)                                              \

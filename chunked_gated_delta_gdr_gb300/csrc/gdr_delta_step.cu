@@ -15,6 +15,7 @@ namespace {
 // D rows x CT columns; 4 columns a thread, D * CT / 4 / THREADS rows a thread.
 template <int D, int CT, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_delta_step(const DeltaStepArgs a) {
+  after_previous<true>();
   constexpr int CL = CT / 4, RG = THREADS / CL, R = D / RG;  // column lanes, row groups, rows each
   __shared__ float ks[D], qs[D];
   __shared__ float4 red[2][RG][CL];
@@ -94,8 +95,7 @@ __global__ void __launch_bounds__(THREADS) k_delta_step(const DeltaStepArgs a) {
 template <int D, int CT, int THREADS>
 cudaError_t run(const DeltaStepArgs &a, cudaStream_t stream) {
   const int64_t blocks = (int64_t)a.B * a.H * (D / CT);
-  k_delta_step<D, CT, THREADS><<<(unsigned)blocks, THREADS, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch(k_delta_step<D, CT, THREADS>, (unsigned)blocks, THREADS, 0, stream, a);
 }
 
 }  // namespace

@@ -148,6 +148,7 @@ struct Ring {
 template <typename E, int LR, int LAY, bool BWD>
 __global__ void __launch_bounds__(kThreads, kCtas)
     k_qk(const QkArgs a, const Groups gr, int token_blocks) {
+  after_previous();
   using R = Ring<E, BWD>;
   constexpr int RP = kThreads / LR, U = R::U, S = R::S;
   __shared__ __align__(16) float ws[2][LR * 8];
@@ -414,6 +415,7 @@ __device__ __forceinline__ F warp_sum(F v) {
 // and this path is not the fast one.
 template <typename E, bool BWD>
 __global__ void __launch_bounds__(kThreads) k_qk_any(const QkArgs a, int64_t rows) {
+  after_previous();
   constexpr int M = 8;  // elements of a lane
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = kThreads / 32;
   const int heads = a.Hq + a.Hk, half = a.rot >> 1;
@@ -496,6 +498,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_any(const QkArgs a, int64_t row
 // dw: the blocks' parts, added by one block for each (tensor, 32 elements) in a fixed order.
 __global__ void __launch_bounds__(1024)
     k_qk_sum(const float *work, int blocks, int d, float *dwq, float *dwk) {
+  after_previous<true>();
   __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, j = blockIdx.y;
   const int e = blockIdx.x * 32 + lane;
@@ -570,10 +573,10 @@ cudaError_t run_fast(const QkArgs &a, int layout, cudaStream_t stream, int *bloc
   static_assert(smem + 2 * LR * 8 * 4 + kThreads * 8 * 4 <= 48 * 1024,
                 "more shared memory than a launch has without asking");
   if (layout == kNear)
-    k_qk<E, LR, kNear, BWD><<<(unsigned)blocks, kThreads, smem, stream>>>(a, gr, (int)tb);
-  else
-    k_qk<E, LR, kHalves, BWD><<<(unsigned)blocks, kThreads, smem, stream>>>(a, gr, (int)tb);
-  return cudaGetLastError();
+    return launch(k_qk<E, LR, kNear, BWD>, (unsigned)blocks, kThreads, smem, stream, a, gr,
+                  (int)tb);
+  return launch(k_qk<E, LR, kHalves, BWD>, (unsigned)blocks, kThreads, smem, stream, a, gr,
+                (int)tb);
 }
 
 template <typename E, bool BWD>
@@ -590,8 +593,7 @@ cudaError_t run(const QkArgs &a, cudaStream_t stream, int *blocks) {
   int64_t n = ceil_div64(rows, kThreads / 32);
   if (n > most_blocks()) n = most_blocks();
   *blocks = (int)n;
-  k_qk_any<E, BWD><<<(unsigned)n, kThreads, 0, stream>>>(a, rows);
-  return cudaGetLastError();
+  return launch(k_qk_any<E, BWD>, (unsigned)n, kThreads, 0, stream, a, rows);
 }
 
 }  // namespace
@@ -612,9 +614,8 @@ cudaError_t launch_qk_bwd(const QkArgs &a, cudaStream_t stream) {
   cudaError_t e = a.f32 ? mix::run<float, true>(a, stream, &blocks)
                         : mix::run<__nv_bfloat16, true>(a, stream, &blocks);
   if (e != cudaSuccess || (!a.dw[0] && !a.dw[1])) return e;
-  mix::k_qk_sum<<<dim3((unsigned)ceil_div64(a.d, 32), 2), 1024, 0, stream>>>(
-      reinterpret_cast<const float *>(a.work), blocks, a.d, a.dw[0], a.dw[1]);
-  return cudaGetLastError();
+  return mix::launch(mix::k_qk_sum, dim3((unsigned)ceil_div64(a.d, 32), 2), 1024, 0, stream,
+                     reinterpret_cast<const float *>(a.work), blocks, a.d, a.dw[0], a.dw[1]);
 }
 
 }  // namespace gdr

@@ -41,6 +41,7 @@ struct __align__(16) Tile1 {
 template <typename E, int LN, bool VEC>
 __global__ void __launch_bounds__(kThreads, kEndCtas)
     k_ssm_ends(const SsmArgs a, const Ranges rg, int tiles_per_group) {
+  after_previous();
   using Y = Lay<LN>;
   using R = TileRing<E, VEC, kAhead>;
   constexpr int L = Y::L, NP = Y::NP, CH = Y::CH, Q = R::S;
@@ -139,6 +140,7 @@ __device__ __forceinline__ void entering_state(const SsmArgs &a, const Ranges &r
 // The states that enter the ranges, in the places of their ends: by a kernel of its own where the
 // ranges are many (chained).
 __global__ void k_ssm_chain(const float *A, const Ranges rg, int D, int N) {
+  after_previous<true>();
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, size = (int64_t)D * N;
   if (i >= size) return;
   chain_ranges(rg.state, rg.sum, rg.reset, rg.n, D, size, i, (int)(i / N), A[i] * kLog2e, false);
@@ -159,6 +161,7 @@ struct __align__(16) Tile2 {  // shared memory of one tile of pass 2
 template <typename E, int LN, bool VEC>
 __global__ void __launch_bounds__(kThreads, kFwdCtas)
     k_ssm_fwd(const SsmArgs a, const Ranges rg, int tiles_per_group) {
+  after_previous();
   using Y = Lay<LN>;
   using R = TileRing<E, VEC, kAhead>;
   constexpr int L = Y::L, NP = Y::NP, CH = Y::CH, Q = R::S;
@@ -349,6 +352,7 @@ __device__ __forceinline__ void four(const float *p, int n, float (&f)[4]) {
 template <typename E, int LN>
 __global__ void __launch_bounds__(kThreads)
     k_ssm_step(const SsmArgs a, float *state, int slots, const int32_t *idx, int cblocks) {
+  after_previous<true>();
   constexpr int PER = 32 / LN, K = LN < 8 ? LN : 8, CW = PER * K;
   const int row = blockIdx.x / cblocks, lane = threadIdx.x & 31;
   const int d0 = (blockIdx.x % cblocks * (kThreads / 32) + (threadIdx.x >> 5)) * CW;
@@ -425,6 +429,7 @@ __global__ void __launch_bounds__(kThreads)
 template <typename E, int LN>
 __global__ void __launch_bounds__(kThreads)
     k_ssm_step_any(const SsmArgs a, float *state, int slots, const int32_t *idx, int cblocks) {
+  after_previous<true>();
   constexpr int CB = kThreads / LN * 4;  // channels of a block
   const int row = blockIdx.x / cblocks;
   const int d0 = blockIdx.x % cblocks * CB + threadIdx.x / LN * 4, n0 = threadIdx.x % LN * 4;
@@ -527,20 +532,19 @@ cudaError_t run_fwd(const SsmArgs &a, cudaStream_t stream) {
   if (c.rg.n > 1) {
     if (smem1 > 48 * 1024 && (e = allow_smem(k_ssm_ends<E, LN, VEC>, smem1)) != cudaSuccess)
       return e;
-    k_ssm_ends<E, LN, VEC>
-        <<<(unsigned)((int64_t)ctiles * (c.rg.n - 1)), kThreads, smem1, stream>>>(a, c.rg, tpg);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch(k_ssm_ends<E, LN, VEC>, (unsigned)((int64_t)ctiles * (c.rg.n - 1)), kThreads,
+                    smem1, stream, a, c.rg, tpg)) != cudaSuccess)
+      return e;
     if (c.rg.n > kChainRanges) {
-      k_ssm_chain<<<(unsigned)ceil_div64((int64_t)a.D * a.N, 128), 128, 0, stream>>>(a.A, c.rg,
-                                                                                     a.D, a.N);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      if ((e = launch(k_ssm_chain, (unsigned)ceil_div64((int64_t)a.D * a.N, 128), 128, 0, stream,
+                      a.A, c.rg, a.D, a.N)) != cudaSuccess)
+        return e;
     }
   }
   const int64_t blocks = (int64_t)ctiles * (c.rg.n + (a.ht ? 1 : 0));
   if (blocks == 0) return cudaSuccess;
   if (smem2 > 48 * 1024 && (e = allow_smem(k_ssm_fwd<E, LN, VEC>, smem2)) != cudaSuccess) return e;
-  k_ssm_fwd<E, LN, VEC><<<(unsigned)blocks, kThreads, smem2, stream>>>(a, c.rg, tpg);
-  return cudaGetLastError();
+  return launch(k_ssm_fwd<E, LN, VEC>, (unsigned)blocks, kThreads, smem2, stream, a, c.rg, tpg);
 }
 
 template <typename E>
@@ -565,14 +569,12 @@ cudaError_t run_step(const SsmArgs &a, float *state, int32_t slots, const int32_
   if (a.N % 4 == 0 && aligned16(a.A) && (a.G == 1 || a.D / a.G % CW == 0) &&
       fit(a.B, a.B_st, a.B_sg) && fit(a.C, a.C_st, a.C_sg)) {
     const int64_t cblocks = ceil_div64(a.D, kThreads / 32 * CW);
-    k_ssm_step<E, LN><<<(unsigned)(cblocks * a.T), kThreads, 0, stream>>>(a, state, slots, idx,
-                                                                         (int)cblocks);
-  } else {
-    const int64_t cblocks = ceil_div64(a.D, kThreads / LN * 4);
-    k_ssm_step_any<E, LN><<<(unsigned)(cblocks * a.T), kThreads, 0, stream>>>(
-        a, state, slots, idx, (int)cblocks);
+    return launch(k_ssm_step<E, LN>, (unsigned)(cblocks * a.T), kThreads, 0, stream, a, state,
+                  slots, idx, (int)cblocks);
   }
-  return cudaGetLastError();
+  const int64_t cblocks = ceil_div64(a.D, kThreads / LN * 4);
+  return launch(k_ssm_step_any<E, LN>, (unsigned)(cblocks * a.T), kThreads, 0, stream, a, state,
+                slots, idx, (int)cblocks);
 }
 template <typename E>
 cudaError_t step_by_lanes(const SsmArgs &a, float *state, int32_t slots, const int32_t *idx,

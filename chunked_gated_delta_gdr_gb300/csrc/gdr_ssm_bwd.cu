@@ -173,6 +173,7 @@ struct __align__(16) Tile1 {
 template <typename E, int LN, bool VEC>
 __global__ void __launch_bounds__(kThreads, kBwdCtas)
     k_ssm_bwd_ends(const SsmArgs a, const BwdWork w, int tiles_per_group) {
+  after_previous();
   using Y = Lay<LN>;
   using R = TileRing<E, VEC, 2>;
   constexpr int L = Y::L, NP = Y::NP, Q = R::S;
@@ -306,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
 
 // States forwards to the ranges' starts, gradients backwards to the ranges' ends.
 __global__ void k_ssm_bwd_chain(const float *A, const BwdWork w, int D, int N) {
+  after_previous<true>();
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, size = (int64_t)D * N;
   if (i >= size) return;
   const bool back = blockIdx.y != 0;
@@ -392,6 +394,7 @@ __device__ __forceinline__ int channel_sums(float (&v)[8], int lane) {
 template <typename E, int LN, bool VEC>
 __global__ void __launch_bounds__(kThreads, kBwdCtas)
     k_ssm_bwd(const SsmArgs a, const BwdWork w, int tiles_per_group) {
+  after_previous();
   using Y = Lay<LN>;
   constexpr int NP = Y::NP, CH = Y::CH;
   // tokens of a tile unrolled: all of them outgrow the instruction cache (8,192 tokens of 2,048
@@ -687,6 +690,7 @@ struct PartSums {
   int n;
 };
 __global__ void __launch_bounds__(256) k_ssm_part_sums(const PartSums p) {
+  after_previous<true>();
   __shared__ float part[8][32];
   const int y = blockIdx.y, lane = threadIdx.x & 31, k = threadIdx.x >> 5;
   const int64_t i = blockIdx.x * (int64_t)32 + lane;
@@ -716,6 +720,7 @@ __global__ void __launch_bounds__(256) k_ssm_part_sums(const PartSums p) {
 template <typename E>
 __global__ void k_ssm_bc_sums(const float *bc, int64_t T, int G, int N, int NP, int tpg, E *dB,
                               E *dC) {
+  after_previous();
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
   const int64_t t = i / (G * 2 * N);
   if (t >= T) return;
@@ -775,25 +780,27 @@ cudaError_t run_bwd(const SsmArgs &a, cudaStream_t stream) {
     return e;
   const int64_t size = (int64_t)a.D * a.N;
   if (w.n > 1) {
-    k_ssm_bwd_ends<E, LN, VEC>
-        <<<(unsigned)((int64_t)ctiles * w.n), kThreads, smem1, stream>>>(a, w, tpg);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    k_ssm_bwd_chain<<<dim3((unsigned)ceil_div64(size, 128), 2), 128, 0, stream>>>(a.A, w, a.D,
-                                                                                  a.N);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch(k_ssm_bwd_ends<E, LN, VEC>, (unsigned)((int64_t)ctiles * w.n), kThreads, smem1,
+                    stream, a, w, tpg)) != cudaSuccess)
+      return e;
+    if ((e = launch(k_ssm_bwd_chain, dim3((unsigned)ceil_div64(size, 128), 2), 128, 0, stream, a.A,
+                    w, a.D, a.N)) != cudaSuccess)
+      return e;
   }
   const int64_t blocks = (int64_t)ctiles * (w.n + (a.dh0 ? 1 : 0));
   if (blocks > 0) {
-    k_ssm_bwd<E, LN, VEC><<<(unsigned)blocks, kThreads, smem2, stream>>>(a, w, tpg);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch(k_ssm_bwd<E, LN, VEC>, (unsigned)blocks, kThreads, smem2, stream, a, w,
+                    tpg)) != cudaSuccess)
+      return e;
   }
   const PartSums ps{{w.state, w.pd, w.pb}, {a.dA, a.dD, a.ddt_bias}, {size, a.D, a.D}, w.n};
-  k_ssm_part_sums<<<dim3((unsigned)ceil_div64(size, 32), 3), 256, 0, stream>>>(ps);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.T == 0) return e;
-  k_ssm_bc_sums<E><<<(unsigned)ceil_div64((int64_t)a.T * a.G * 2 * a.N, 256), 256, 0, stream>>>(
-      w.bc, a.T, a.G, a.N, Lay<LN>::NP, tpg, reinterpret_cast<E *>(a.dB),
-      reinterpret_cast<E *>(a.dC));
-  return cudaGetLastError();
+  if ((e = launch(k_ssm_part_sums, dim3((unsigned)ceil_div64(size, 32), 3), 256, 0, stream, ps)) !=
+          cudaSuccess ||
+      a.T == 0)
+    return e;
+  return launch(k_ssm_bc_sums<E>, (unsigned)ceil_div64((int64_t)a.T * a.G * 2 * a.N, 256), 256, 0,
+                stream, w.bc, a.T, a.G, a.N, Lay<LN>::NP, tpg, reinterpret_cast<E *>(a.dB),
+                reinterpret_cast<E *>(a.dC));
 }
 
 template <typename E>

@@ -137,6 +137,7 @@ __device__ __forceinline__ void decay_pairs(const SsmArgs &a, const Wide &W, f2 
 template <typename E, int NS>
 __global__ void __launch_bounds__(kThreads, kCtas)
     k_ssm_wide_ends(const SsmArgs a, const Ranges rg, int tiles_per_group) {
+  after_previous();
   constexpr int S = Stages<E>::S;
   extern __shared__ __align__(16) char smem_raw[];
   auto &s = *reinterpret_cast<Shared<E, NS, 2> *>(smem_raw);
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 template <typename E, int NS>
 __global__ void __launch_bounds__(kThreads, kCtas)
     k_ssm_wide(const SsmArgs a, const Ranges rg, int tiles_per_group) {
+  after_previous();
   constexpr int S = Stages<E>::S;
   extern __shared__ __align__(16) char smem_raw[];
   auto &s = *reinterpret_cast<Shared<E, NS, 3> *>(smem_raw);
@@ -316,13 +318,12 @@ cudaError_t run_wide(const SsmArgs &a, int range, cudaStream_t stream) {
   if (smem1 > 48 * 1024 && (e = allow_smem(k_ssm_wide_ends<E, NS>, smem1)) != cudaSuccess) return e;
   if (smem2 > 48 * 1024 && (e = allow_smem(k_ssm_wide<E, NS>, smem2)) != cudaSuccess) return e;
   if (rg.n > 1) {
-    k_ssm_wide_ends<E, NS>
-        <<<(unsigned)((int64_t)ctiles * (rg.n - 1)), kThreads, smem1, stream>>>(a, rg, tpg);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch(k_ssm_wide_ends<E, NS>, (unsigned)((int64_t)ctiles * (rg.n - 1)), kThreads,
+                    smem1, stream, a, rg, tpg)) != cudaSuccess)
+      return e;
   }
-  k_ssm_wide<E, NS><<<(unsigned)((int64_t)ctiles * (rg.n + (a.ht ? 1 : 0))), kThreads, smem2,
-                      stream>>>(a, rg, tpg);
-  return cudaGetLastError();
+  return launch(k_ssm_wide<E, NS>, (unsigned)((int64_t)ctiles * (rg.n + (a.ht ? 1 : 0))), kThreads,
+                smem2, stream, a, rg, tpg);
 }
 
 }  // namespace
