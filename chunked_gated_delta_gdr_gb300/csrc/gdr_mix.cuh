@@ -494,6 +494,7 @@ struct QkArgs {
   mix::Param w[2];
   float *dw[2];
   const float *cos, *sin;
+  bool quads;  // a place's cosines and sines start on 16 bytes (set by the launcher)
   const int32_t *pos;
   void *work;
 };

@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kCtas = 4;    // blocks on each SM; each runs over many tokens
+constexpr int kAnyCtas = 10;  // for any strides, where only warps hide the loads' latency
 constexpr int kStages = 4;  // batches of rows on their way or in use (bf16)
 
 __device__ __forceinline__ int place_of(const QkArgs &a, int64_t t) {
@@ -66,15 +67,27 @@ __device__ __forceinline__ void group_sums(float (&v)[K], int gl, F f) {
 enum Layout { kNear, kHalves };
 
 // Cosines and sines of a lane's 8 elements, the sine with its sign for the forward rotation
-// (u_e cos + u_partner sin); all 8 elements are in the rotated part or none.
+// (u_e cos + u_partner sin).
 struct Angles {
   f2 c[4], s[4];
 };
 __device__ __forceinline__ void load_angles(const QkArgs &a, int64_t t, int e0, float4 &c,
                                             float4 &s) {
-  const int64_t base = (int64_t)place_of(a, t) * (a.rot >> 1) + (e0 >> 1);
-  c = *reinterpret_cast<const float4 *>(a.cos + base);
-  s = *reinterpret_cast<const float4 *>(a.sin + base);
+  const int half = a.rot >> 1, at = e0 >> 1;
+  const float *cos = a.cos + (int64_t)place_of(a, t) * half + at;
+  const float *sin = a.sin + (int64_t)place_of(a, t) * half + at;
+  if (a.quads) {
+    c = *reinterpret_cast<const float4 *>(cos);
+    s = *reinterpret_cast<const float4 *>(sin);
+  } else {  // the rotated part may end inside the lane's elements: no rotation behind it
+    float *cf = reinterpret_cast<float *>(&c), *sf = reinterpret_cast<float *>(&s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (at + i < half) {
+        cf[i] = cos[i];
+        sf[i] = sin[i];
+      }
+  }
 }
 template <int LAY>
 __device__ __forceinline__ Angles signed_angles(const float4 &c, const float4 &s) {
@@ -410,10 +423,11 @@ __device__ __forceinline__ F warp_sum(F v) {
 }
 
 // Any head size up to 256, any strides: one warp for each row, the row read again for the
-// partners of the rotation.  The backward's row sums and its last difference are in 64 bits: in a
-// head of a few elements r m and x r^3 (sum x m) / d nearly cancel (at d = 1 only eps is left),
-// and this path is not the fast one.
-template <typename E, bool BWD>
+// partners of the rotation (36,939 tokens of 15 heads of 232, half of each rotated by halves: 469 us
+// where interleaved pairs take the fast path's 100).  WIDE: the backward's row sums and its last
+// difference are in 64 bits, for heads of a few elements: there r m and x r^3 (sum x m) / d nearly
+// cancel (at d = 1 only eps is left).
+template <typename E, bool BWD, bool WIDE>
 __global__ void __launch_bounds__(kThreads) k_qk_any(const QkArgs a, int64_t rows) {
   after_previous();
   constexpr int M = 8;  // elements of a lane
@@ -428,7 +442,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_any(const QkArgs a, int64_t row
     const E *x = reinterpret_cast<const E *>(a.x[j]) + t * a.x_st[j] + hj * a.x_sh[j];
     const E *y = reinterpret_cast<const E *>(a.y[j]) + t * a.y_st[j] + hj * a.y_sh[j];
     const int64_t base = a.rot > 0 ? (int64_t)place_of(a, t) * half : 0;
-    using S = typename std::conditional<BWD, double, float>::type;
+    using S = typename std::conditional<WIDE, double, float>::type;
     S q = 0;
     for (int e = lane; e < a.d; e += 32) q += (S)ld1(x + e) * (S)ld1(x + e);
     q = warp_sum(q) / (S)(a.rms ? a.d : 1) + (S)a.eps;
@@ -531,10 +545,10 @@ bool rows_on(const QkArgs &a, bool bwd, int g) {
 }
 // The layout that the head size, the rotation and the alignment allow, or -1.
 int layout_of(const QkArgs &a, bool bwd) {
-  if (a.d % 8 != 0 || a.rot % 8 != 0 || !aligned16(a.cos) || !aligned16(a.sin)) return -1;
+  if (a.d % 8 != 0) return -1;
   const bool whole = rows_on(a, bwd, a.f32 ? 4 : 8);
   if (a.interleaved || a.rot == 0) return whole ? kNear : -1;
-  return rows_on(a, bwd, 4) ? kHalves : -1;
+  return a.rot % 8 == 0 && rows_on(a, bwd, 4) ? kHalves : -1;
 }
 
 int lanes_of(int d) {  // of a row's group: a power of two
@@ -580,7 +594,9 @@ cudaError_t run_fast(const QkArgs &a, int layout, cudaStream_t stream, int *bloc
 }
 
 template <typename E, bool BWD>
-cudaError_t run(const QkArgs &a, cudaStream_t stream, int *blocks) {
+cudaError_t run(const QkArgs &args, cudaStream_t stream, int *blocks) {
+  QkArgs a = args;
+  a.quads = a.rot % 8 == 0 && aligned16(a.cos) && aligned16(a.sin);
   *blocks = 0;
   const int64_t rows = a.T * (a.Hq + a.Hk);
   if (rows == 0) return cudaSuccess;
@@ -591,9 +607,12 @@ cudaError_t run(const QkArgs &a, cudaStream_t stream, int *blocks) {
     return run_fast<E, 32, BWD>(a, layout, stream, blocks);
   }
   int64_t n = ceil_div64(rows, kThreads / 32);
-  if (n > most_blocks()) n = most_blocks();
+  const int64_t most = (int64_t)sm_count() * kAnyCtas;
+  if (n > most) n = most;
   *blocks = (int)n;
-  return launch(k_qk_any<E, BWD>, (unsigned)n, kThreads, 0, stream, a, rows);
+  if (BWD && a.d <= 8)
+    return launch(k_qk_any<E, BWD, BWD>, (unsigned)n, kThreads, 0, stream, a, rows);
+  return launch(k_qk_any<E, BWD, false>, (unsigned)n, kThreads, 0, stream, a, rows);
 }
 
 }  // namespace
@@ -606,7 +625,7 @@ cudaError_t launch_qk_fwd(const QkArgs &a, cudaStream_t stream) {
 }
 
 size_t qk_bwd_workspace(int64_t, int32_t, int32_t, int32_t d) {
-  return align256((size_t)mix::most_blocks() * 2 * d * sizeof(float));
+  return align256((size_t)mix::sm_count() * mix::kAnyCtas * 2 * d * sizeof(float));
 }
 
 cudaError_t launch_qk_bwd(const QkArgs &a, cudaStream_t stream) {

@@ -355,6 +355,10 @@ QK = [  # T, Hq, Hk, d, rot, interleaved, norm, weights, type, odd strides, eps
     (27, 5, 1, 248, 248, True, "rms", True, BF16, False, 1e-6),
     (35, 1, 1, 8, 8, False, "rms", True, F32, False, 1e-5),
     (2500, 7, 2, 24, 8, False, "l2", False, BF16, False, 1e-6),
+    (23, 12, 3, 232, 116, True, "l2", True, BF16, False, 1e-6),
+    (19, 2, 1, 72, 36, True, "rms", True, F32, False, 1e-6),
+    (14, 2, 1, 64, 30, True, "rms", True, BF16, False, 1e-6),
+    (2100, 3, 1, 232, 116, False, "rms", True, BF16, False, 1e-6),
 ]
 
 
