@@ -347,8 +347,8 @@ __device__ __forceinline__ void four(const float *p, int n, float (&f)[4]) {
 // written once.  A warp takes CW neighbouring channels of a row: LN lanes hold a channel's states,
 // 4 each, and K times PER channels follow one another, so that each of its K loads of states is one
 // run of 512 bytes.  What belongs to a channel alone (step size, skip, gate, output) is one lane's
-// each, and the sums over states come back to it.  128 rows of 4,096 x 16 states: 18 us with the
-// states in HBM (3.9 TB/s; launch, one fill and one drain of the GPU are half of it), 10 us from L2.
+// each, and the sums over states come back to it.  128 rows of 4,096 x 16 states: 15.5 us with
+// the states in HBM (4.5 TB/s; one fill and one drain of the GPU are a third of it), 10 us from L2.
 template <typename E, int LN>
 __global__ void __launch_bounds__(kThreads)
     k_ssm_step(const SsmArgs a, float *state, int slots, const int32_t *idx, int cblocks) {

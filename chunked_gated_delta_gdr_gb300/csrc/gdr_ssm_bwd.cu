@@ -42,6 +42,15 @@ constexpr int kLeast = 16, kMostShort = 256;
 constexpr int kKept = kRange / kBT;  // states kept at most: tiles that continue a segment
 constexpr uint32_t kCols = 8 * (kKept + kBT);  // Tensor Memory columns: kept, then a tile's
 
+// e^{dt A}.  The approximate exponential falls short: by 2e-8 of its value on average for exponents
+// between -0.5 and -0.004, by 6e-9 for smaller ones (measured).  Over a range's tokens that adds up
+// in the states and, with the time they last as weight, in dA (at 4,067 tokens of 512 x 16 states
+// 9.7e-7 of dA's norm; 4.8e-7 with the middle of the two added to the exponent, at no cost).
+__device__ __forceinline__ float decay(float dt, float A2) {
+  constexpr float kShort = 1.9e-8f;  // 1.3e-8 / ln 2
+  return ex2(fmaf(dt, A2, kShort));
+}
+
 struct BwdWork {
   int range, n;     // tokens of a range, ranges
   float *state;     // [n][D][N]: states at the ranges' ends, then at their starts, then dA's parts
@@ -258,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
           S[k] += dt[k];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float e = ex2(dt[k] * A2[k][j]);
+            const float e = decay(dt[k], A2[k][j]);
             h[k][j] = fmaf(e, h[k][j], dx[k] * Bv[j]);
             pr[k][j] *= e;
             gs[k][j] = fmaf(pr[k][j], Cv[j] * dy[k], gs[k][j]);
@@ -485,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[k][j] = fmaf(ex2(dt[k] * A2[k][j]), v[k][j], dx[k] * Bv[j]);
+      for (int j = 0; j < 4; ++j) v[k][j] = fmaf(decay(dt[k], A2[k][j]), v[k][j], dx[k] * Bv[j]);
   };
 
   // the sweep: the state before each tile that continues a segment
@@ -593,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
           bc[j] = k ? fmaf(dx[k], g[k][j], bc[j]) : dx[k] * g[k][j];
           bc[4 + j] = k ? fmaf(dy[k], now[k][j], bc[4 + j]) : dy[k] * now[k][j];
           p = j ? fmaf(g[k][j], Bv[j], p) : g[k][j] * Bv[j];
-          g[k][j] *= ex2(dt[k] * A2[k][j]);
+          g[k][j] *= decay(dt[k], A2[k][j]);
           const float cr = g[k][j] * before[k][j];
           dA[k][j] = fmaf(dt[k], cr, dA[k][j]);
           cs = j ? fmaf(cr, A2[k][j], cs) : cr * A2[k][j];
