@@ -10,7 +10,7 @@
 // Bound by HBM: each row is read once and written once.  8 elements a lane, 16 bytes of bf16; a
 // group of lanes keeps one token's cosines and sines in registers while it runs over the token's
 // heads, q's and then k's.  65,536 tokens of 48 heads of 128 in bf16: 279 us, 5.8 TB/s of 6.8; the
-// backward 425 us.
+// backward 425 us, 5.7 TB/s.
 #include <type_traits>
 
 #include "gdr_mix.cuh"
