@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
           S[k] += dt[k];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            h[k][j] = fmaf(ex2(dt[k] * A2[k][j]), h[k][j], dx[k] * Bv[j]);
+            h[k][j] = fmaf(decay(dt[k], A2[k][j]), h[k][j], dx[k] * Bv[j]);
         }
       });
       __syncthreads();
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          h[k][j] = fmaf(ex2(dt[k] * A2[k][j]), h[k][j], dx[k] * Bv[j]);
+          h[k][j] = fmaf(decay(dt[k], A2[k][j]), h[k][j], dx[k] * Bv[j]);
         s.part[po[k] + i * Y::ST] =
             fmaf(h[k][0], C.x, fmaf(h[k][1], C.y, fmaf(h[k][2], C.z, h[k][3] * C.w)));
       }
@@ -397,10 +397,10 @@ __global__ void __launch_bounds__(kThreads)
   for (int c = 0; c < K; ++c) {
     const float w = __shfl_sync(0xffffffffu, v2, c * PER + g);
     const float u = __shfl_sync(0xffffffffu, dx, c * PER + g);
-    h[c].x = fmaf(ex2(w * A[c].x), h[c].x, u * B[0]);
-    h[c].y = fmaf(ex2(w * A[c].y), h[c].y, u * B[1]);
-    h[c].z = fmaf(ex2(w * A[c].z), h[c].z, u * B[2]);
-    h[c].w = fmaf(ex2(w * A[c].w), h[c].w, u * B[3]);
+    h[c].x = fmaf(decay(w, A[c].x), h[c].x, u * B[0]);
+    h[c].y = fmaf(decay(w, A[c].y), h[c].y, u * B[1]);
+    h[c].z = fmaf(decay(w, A[c].z), h[c].z, u * B[2]);
+    h[c].w = fmaf(decay(w, A[c].w), h[c].w, u * B[3]);
     if (in && d0 + g + c * PER < a.D) *reinterpret_cast<float4 *>(s + c * PER * a.N) = h[c];
     part[c] = in ? fmaf(h[c].x, C[0], fmaf(h[c].y, C[1], fmaf(h[c].z, C[2], h[c].w * C[3]))) : 0.f;
   }
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads)
       const float dx = v * x[c];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        h[c][j] = fmaf(ex2(v * (A[c][j] * kLog2e)), h[c][j], dx * B[j]);
+        h[c][j] = fmaf(decay(v, A[c][j] * kLog2e), h[c][j], dx * B[j]);
         part[c] = fmaf(h[c][j], C[j], part[c]);
       }
 #pragma unroll

@@ -43,15 +43,6 @@ constexpr int kLeast = 16, kMostShort = 256;
 constexpr int kKept = kRange / kBT;  // states kept at most: tiles that continue a segment
 constexpr uint32_t kCols = 8 * (kKept + kBT);  // Tensor Memory columns: kept, then a tile's
 
-// e^{dt A}.  The approximate exponential falls short: by 2e-8 of its value on average for exponents
-// between -0.5 and -0.004, by 6e-9 for smaller ones (measured).  Over a range's tokens that adds up
-// in the states and, with the time they last as weight, in dA (at 4,067 tokens of 512 x 16 states
-// 9.7e-7 of dA's norm; 4.8e-7 with the middle of the two added to the exponent, at no cost).
-__device__ __forceinline__ float decay(float dt, float A2) {
-  constexpr float kShort = 1.9e-8f;  // 1.3e-8 / ln 2
-  return ex2(fmaf(dt, A2, kShort));
-}
-
 struct BwdWork {
   int range, n;     // tokens of a range, ranges
   float *state;     // [n][D][N]: states at the ranges' ends, then at their starts, then dA's parts

@@ -608,3 +608,75 @@ def test_refusals():
     with pytest.raises(ValueError):
         gdr.delta_step(q, q, q, g, g.bfloat16(), st,
                        state_indices=torch.zeros(3, dtype=torch.int32, device=DEV))
+
+
+# ------------------------------------------------------------------ calls that follow one another
+
+def _chain(sync):
+    """Calls that each read what the one before wrote: a kernel is made ready while the one
+    before it runs, and must wait for its results all the same."""
+    gen = torch.Generator().manual_seed(5)
+    T, C, N = 700, 256, 16
+    x, w = dev(rn(gen, T, C, dtype=BF16)), dev(rn(gen, C, 4, std=0.5))
+    A, B = dev(-rn(gen, C, N).abs() - 0.1), dev(rn(gen, T, 1, N, dtype=BF16, std=0.3))
+    cu = torch.tensor([0, 300, 300, 700], dtype=torch.int32, device=DEV)
+    pool, ssm = torch.zeros(9, 3, C, dtype=BF16, device=DEV), torch.zeros(9, C, N, device=DEV)
+    slots = torch.tensor([4, 0, 7], dtype=torch.int32, device=DEV)
+    done = (lambda: torch.cuda.synchronize()) if sync else (lambda: None)
+    keep = []
+    for i in range(12):
+        y, _ = gdr.conv_fwd(x, w, cu_seqlens=cu)
+        done()
+        y, _ = gdr.ssm_fwd(y, y, A, B, B, cu_seqlens=cu)
+        done()
+        q, k = gdr.qk_fwd(y.view(T, 2, 128), y.view(T, 2, 128))
+        done()
+        dx, dw, _, _ = gdr.conv_bwd(x, w, q.view(T, C), cu_seqlens=cu)
+        done()
+        g = gdr.ssm_bwd(dx, dx, A, B, B, k.view(T, C), cu_seqlens=cu)
+        done()
+        x = gdr.qk_fwd(g[0].view(T, 2, 128), k)[0].view(T, C)
+        done()
+        for j in range(8):
+            s = gdr.conv_step(x[3 * j:3 * j + 3], w, pool, state_indices=slots)
+            done()
+            s = gdr.ssm_step(s, s, A, B[:3], B[:3], ssm, state_indices=slots)
+            done()
+        keep += [x, dw, g[2], s]
+    return keep + [pool, ssm]
+
+
+def test_calls_in_a_row_wait_for_each_other():
+    want = _chain(True)
+    for _ in range(3):
+        for a, b in zip(_chain(False), want):
+            assert torch.equal(a, b)
+
+
+def test_calls_in_a_graph_wait_for_each_other():
+    want = _chain(True)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        _chain(False)
+    torch.cuda.synchronize()
+    gen = torch.Generator().manual_seed(6)
+    T, C, N = 900, 128, 16
+    x, A = dev(rn(gen, T, C, dtype=BF16)), dev(-rn(gen, C, N).abs() - 0.1)
+    B = dev(rn(gen, T, 1, N, dtype=BF16, std=0.3))
+
+    def run():
+        y, ht = gdr.ssm_fwd(x, x, A, B, B, output_final_state=True)
+        return gdr.ssm_bwd(y, x, A, B, B, y)[:5] + (y, ht)
+
+    eager = run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        for a, b in zip(got, eager):
+            assert torch.equal(a, b)
+    for a, b in zip(_chain(False), want):
+        assert torch.equal(a, b)
