@@ -80,7 +80,6 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
     for (int tb = t0; tb < t1; tb += L) {
       issue(stage == 0 ? Q - 1 : stage - 1, tb + (Q - 1) * L);
       copies_wait<Q - 1>();
-      const int n = tb + lt < t1 ? nv : 0;
       put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, xr.get(stage),
                        dr.get(stage));
       stage = stage + 1 == Q ? 0 : stage + 1;
@@ -238,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
 
   int stage = 0;
   for (int tb = t0; tb < t1; tb += L) {
-    const int n = min(L, t1 - tb), k = lt < n ? nv : 0;
+    const int n = min(L, t1 - tb);
     issue(stage == 0 ? Q - 1 : stage - 1, tb + (Q - 1) * L);
     copies_wait<Q - 1>();
     put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, xr.get(stage),

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
   bool reset = false;  // a segment has started: nothing from here on reaches the state before
   int stage = 0;
   for (int i0 = 0; i0 < n; i0 += L) {
-    const int m = min(L, n - i0), t = t0 + i0 + lt, k = lt < m ? nv : 0;
+    const int m = min(L, n - i0);
     issue(stage == 0 ? Q - 1 : stage - 1, i0 + (Q - 1) * L);
     copies_wait<Q - 1>();
     put_pairs<E, LN>(s.pair, s.bias, a.softplus, lt, lc, xr.get(stage),
