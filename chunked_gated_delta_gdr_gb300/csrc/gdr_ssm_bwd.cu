@@ -245,15 +245,25 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
       rc.fetch(Cp, a.C_st, t0 + i0 + L, t0 + n, a.N);
     }
     __syncthreads();
-    auto scan = [&](int from, int to) {
+    // ENTERS: of the segment that enters the range, whose tokens' gradients reach the state before
+    // it; a later segment's do not, whatever they are (an infinity times 0 would be NaN)
+    auto scan = [&](auto ENTERS, int from, int to) {
       tile_tokens<L>(from, to, [&](int i) {
         const int at = i * Y::PT + P.pair;
         const float4 q = *reinterpret_cast<const float4 *>(&s.pair[at]);
-        const float2 dyv = *reinterpret_cast<const float2 *>(&s.dy[at]);
         const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
-        const float4 C = *reinterpret_cast<const float4 *>(&s.c[i * NP + P.nl * 4]);
-        const float dt[2] = {q.x, q.z}, dx[2] = {q.y, q.w}, dy[2] = {dyv.x, dyv.y};
-        const float Bv[4] = {B.x, B.y, B.z, B.w}, Cv[4] = {C.x, C.y, C.z, C.w};
+        const float dt[2] = {q.x, q.z}, dx[2] = {q.y, q.w}, Bv[4] = {B.x, B.y, B.z, B.w};
+        float dy[2], Cv[4];
+        if (ENTERS) {
+          const float2 d = *reinterpret_cast<const float2 *>(&s.dy[at]);
+          const float4 C = *reinterpret_cast<const float4 *>(&s.c[i * NP + P.nl * 4]);
+          dy[0] = d.x;
+          dy[1] = d.y;
+          Cv[0] = C.x;
+          Cv[1] = C.y;
+          Cv[2] = C.z;
+          Cv[3] = C.w;
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           S[k] += dt[k];
@@ -261,8 +271,10 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
           for (int j = 0; j < 4; ++j) {
             const float e = decay(dt[k], A2[k][j]);
             h[k][j] = fmaf(e, h[k][j], dx[k] * Bv[j]);
-            pr[k][j] *= e;
-            gs[k][j] = fmaf(pr[k][j], Cv[j] * dy[k], gs[k][j]);
+            if (ENTERS) {
+              pr[k][j] *= e;
+              gs[k][j] = fmaf(pr[k][j], Cv[j] * dy[k], gs[k][j]);
+            }
           }
         }
       });
@@ -273,23 +285,23 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
         P.read(a, next < a.n_seq ? a.h0 : nullptr, next, h);
         S[0] = S[1] = 0.f;
         reset = true;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) pr[k][j] = 0.f;
       }
       int e = i + 1;
       while (e < m && s.s.mark[i0 + e] < 0) ++e;
       const int seg = s.s.seg[i0 + i];
       if (seg >= 0 && seg < a.n_seq) {
-        scan(i, e);
-        if (!reset && s.s.mark[i0 + e] >= 0 && a.dht) {
-          float f[2][4];
-          P.read(a, a.dht, seg, f);
+        if (reset) {
+          scan(std::false_type(), i, e);
+        } else {
+          scan(std::true_type(), i, e);
+          if (s.s.mark[i0 + e] >= 0 && a.dht) {
+            float f[2][4];
+            P.read(a, a.dht, seg, f);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) gs[k][j] = fmaf(pr[k][j], f[k][j], gs[k][j]);
+              for (int j = 0; j < 4; ++j) gs[k][j] = fmaf(pr[k][j], f[k][j], gs[k][j]);
+          }
         }
       }
       i = e;
