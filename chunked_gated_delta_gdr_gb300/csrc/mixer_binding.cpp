@@ -188,7 +188,7 @@ int run(F f) {
   return status;
 }
 
-// x, weight, bias, h0, cu, activation, want_ht, out, ht
+// x, weight, bias, h0, cu, activation, want_ht, out, ht (a given one is written, wanted or not)
 ENTRY(conv_fwd, 9)
   const at::Tensor x = required(args[0], 2, "x"), w = required(args[1], 2, "weight");
   const at::Tensor b = tensor(args[2]), h0 = tensor(args[3]), cu = tensor(args[4]);
@@ -197,10 +197,7 @@ ENTRY(conv_fwd, 9)
   const Segments s(c, cu);
   at::Tensor y = tensor(args[7]), ht = tensor(args[8]);
   if (!y.defined()) y = empty(x.sizes(), x);
-  if (!truth(args[6]))
-    ht.reset();
-  else if (!ht.defined())
-    ht = empty({s.n, w.size(1) - 1, x.size(1)}, x);
+  if (truth(args[6]) && !ht.defined()) ht = empty({s.n, w.size(1) - 1, x.size(1)}, x);
   const int32_t act = activation(args[5]);
   gdr_tensor_t *dx = c.add(x), *dw = c.add(w), *db = c.add(b), *dh = c.add(h0), *dy = c.add(y),
                *dt = c.add(ht);
@@ -254,7 +251,7 @@ ENTRY(conv_step, 7)
   return wrap(y);
 EXIT
 
-// x, dt, A, B, C, D, z, dt_bias, softplus, h0, cu, want_ht, out, ht, workspace
+// x, dt, A, B, C, D, z, dt_bias, softplus, h0, cu, want_ht, out, ht (as above), workspace
 ENTRY(ssm_fwd, 15)
   const at::Tensor x = required(args[0], 2, "x"), B = required(args[3], 3, "B");
   const at::Tensor dt = tensor(args[1]), A = tensor(args[2]), C = tensor(args[4]),
@@ -266,10 +263,7 @@ ENTRY(ssm_fwd, 15)
   const int32_t sp = truth(args[8]);
   at::Tensor y = tensor(args[12]), ht = tensor(args[13]);
   if (!y.defined()) y = empty(x.sizes(), x);
-  if (!truth(args[11]))
-    ht.reset();
-  else if (!ht.defined())
-    ht = empty32({s.n, x.size(1), B.size(2)}, x);
+  if (truth(args[11]) && !ht.defined()) ht = empty32({s.n, x.size(1), B.size(2)}, x);
   const Scratch ws(c, tensor(args[14]),
                    gdr_ssm_fwd_workspace_bytes(x.size(0), (int32_t)x.size(1), (int32_t)B.size(2),
                                                (int32_t)B.size(1)),

@@ -48,7 +48,8 @@ def conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]
     x [T, C] bf16 or fp32; weight [C, W] (W = 2..4) and bias [C] fp32 or bf16; initial_state
     [N, W - 1, C] in x's type, the inputs before each segment, oldest first; cu_seqlens [N + 1]
     int32 (None: one segment); activation "silu" or None.  Returns (y [T, C], final_state
-    [N, W - 1, C] or None); ``out`` and ``final_state`` may give them.
+    [N, W - 1, C] or None); ``out`` and ``final_state`` may give them, and a final_state that is
+    given is written whatever output_final_state says.
     """
     if stream is not None:
         with torch.cuda.stream(stream):
@@ -103,7 +104,7 @@ def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     x, dt, z [T, Dm] and B, C [T, G, N] bf16 or fp32; A [Dm, N], D, dt_bias [Dm] fp32;
     initial_state [N_seq, Dm, N] fp32; cu_seqlens [N_seq + 1] int32 (None: one segment).
     Returns (y [T, Dm], final_state [N_seq, Dm, N] fp32 or None); ``out`` and ``final_state``
-    may give them.
+    may give them, and a final_state that is given is written whatever output_final_state says.
     """
     if stream is not None:
         with torch.cuda.stream(stream):
