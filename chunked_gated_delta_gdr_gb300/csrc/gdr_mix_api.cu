@@ -428,7 +428,6 @@ int gdr_ssm_step(const gdr_tensor_t *x, const gdr_tensor_t *dt, const gdr_tensor
   GDR_TRY(shaped(s, s.shape[0], a.D, a.N));
   GDR_TRY(packed(s));
   if (s.shape[0] > kMost) return GDR_ERR_SHAPE;
-  if (!aligned16(s.p) || !aligned16(a.A)) return GDR_ERR_ALIGN;
   if (!state_indices && s.shape[0] < a.T) return GDR_ERR_SHAPE;
   GDR_TRY(read_act(y, 2, &d, a.f32));
   GDR_TRY(shaped(d, a.T, a.D));

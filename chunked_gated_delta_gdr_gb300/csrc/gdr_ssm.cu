@@ -565,8 +565,7 @@ cudaError_t run_step(const SsmArgs &a, float *state, int32_t slots, const int32_
   auto fit = [&](const void *p, int64_t st, int64_t sg) {
     return (reinterpret_cast<uintptr_t>(p) & four) == 0 && ((st | sg) & 3) == 0;
   };
-  // (the entry point has checked the states' alignment)
-  if (a.N % 4 == 0 && aligned16(a.A) && (a.G == 1 || a.D / a.G % CW == 0) &&
+  if (a.N % 4 == 0 && aligned16(state) && aligned16(a.A) && (a.G == 1 || a.D / a.G % CW == 0) &&
       fit(a.B, a.B_st, a.B_sg) && fit(a.C, a.C_st, a.C_sg)) {
     const int64_t cblocks = ceil_div64(a.D, kThreads / 32 * CW);
     return launch(k_ssm_step<E, LN>, (unsigned)(cblocks * a.T), kThreads, 0, stream, a, state,

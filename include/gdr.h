@@ -443,8 +443,8 @@ size_t gdr_ssm_bwd_workspace_bytes(int64_t T, int32_t Dm, int32_t N, int32_t G);
 
 /*
  * gdr_ssm_step -- one token of gdr_ssm_fwd for each of the rows of x.
- *   x, dt, z, y [rows, Dm]; B, C [rows, G, N]; state [slots, Dm, N] f32 compact, 16-byte
- *   aligned, in place
+ *   x, dt, z, y [rows, Dm]; B, C [rows, G, N]; state [slots, Dm, N] f32 compact, in place
+ *   (the fast path takes N % 4 == 0 with A and state 16-byte aligned)
  */
 int gdr_ssm_step(const gdr_tensor_t *x, const gdr_tensor_t *dt, const gdr_tensor_t *A,
                  const gdr_tensor_t *B, const gdr_tensor_t *C, const gdr_tensor_t *D,
