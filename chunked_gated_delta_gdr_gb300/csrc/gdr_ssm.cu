@@ -52,13 +52,13 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
   const Place<LN> P(a, tiles_per_group);
   const int r0 = P.r * rg.range, t1 = min(a.T, r0 + rg.range);
   const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
-  R xr(ring, a.x.p, P.c0 + lc, a.x.st);
-  R dr(ring + R::kSlots, a.dt.p, P.c0 + lc, a.dt.st);
+  R xr(ring, a.x.p, P.c0 + lc, a.x.st, nv);
+  R dr(ring + R::kSlots, a.dt.p, P.c0 + lc, a.dt.st, nv);
   const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
   for (int i = P.tid; i < CH; i += kThreads)
-    s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
+    s.bias[i] = step_bias(a.dt_bias, P.c0, P.nch, i);
   float A2[2][4], h[2][4], S[2] = {0.f, 0.f};
-  P.decays(a, A2);
+  const float most = P.decays(a, A2);
   const SegCursor c = seg_find(a.cu, a.n_seq, a.T, t1, s.red);
   const int seg = c.j - 1;
   const bool covered = seg >= 0 && seg < a.n_seq, reset = seg >= 0 && c.b >= r0;
@@ -91,12 +91,13 @@ __global__ void __launch_bounds__(kThreads, kEndCtas)
             &s.pair[i * Y::PT + P.pair]);
         const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
         const float dt[2] = {d.x, d.z}, dx[2] = {d.y, d.w}, Bv[4] = {B.x, B.y, B.z, B.w};
+        const float more = raised(dt, most);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           S[k] += dt[k];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            h[k][j] = fmaf(decay(dt[k], A2[k][j]), h[k][j], dx[k] * Bv[j]);
+            h[k][j] = fmaf(decay(dt[k], A2[k][j], more), h[k][j], dx[k] * Bv[j]);
         }
       });
       __syncthreads();
@@ -179,15 +180,15 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
   }
   const int t0 = P.r * rg.range, t1 = min(a.T, t0 + rg.range);
   const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
-  R xr(ring, a.x.p, P.c0 + lc, a.x.st);
-  R dr(ring + R::kSlots, a.dt.p, P.c0 + lc, a.dt.st);
-  R zr(ring + 2 * R::kSlots, a.z.p, P.c0 + lc, a.z.st);
+  R xr(ring, a.x.p, P.c0 + lc, a.x.st, nv);
+  R dr(ring + R::kSlots, a.dt.p, P.c0 + lc, a.dt.st, nv);
+  R zr(ring + 2 * R::kSlots, a.z.p, P.c0 + lc, a.z.st, nv);
   const bool gated = a.z.p != nullptr;
   E *yp = reinterpret_cast<E *>(a.y.p) + P.c0 + lc;
   const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
   const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
   for (int i = P.tid; i < CH; i += kThreads) {
-    s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
+    s.bias[i] = step_bias(a.dt_bias, P.c0, P.nch, i);
     s.skip[i] = a.Dskip && i < P.nch ? a.Dskip[P.c0 + i] : 0.f;
   }
   BcTile<E, NP, L, VEC> rb, rc;
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
   rb.fetch(Bp, a.B_st, t0, t1, a.N);
   rc.fetch(Cp, a.C_st, t0, t1, a.N);
   float A2[2][4], h[2][4];
-  P.decays(a, A2);
+  const float most = P.decays(a, A2);
   SegCursor cursor = seg_find(a.cu, a.n_seq, a.T, t0, s.red);
   int seg = cursor.j - 1;
   const bool enters = P.r > 0 && seg >= 0 && seg < a.n_seq;
@@ -224,11 +225,12 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
       const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
       const float4 C = *reinterpret_cast<const float4 *>(&s.c[i * NP + P.nl * 4]);
       const float dt[2] = {d.x, d.z}, dx[2] = {d.y, d.w}, Bv[4] = {B.x, B.y, B.z, B.w};
+      const float more = raised(dt, most);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          h[k][j] = fmaf(decay(dt[k], A2[k][j]), h[k][j], dx[k] * Bv[j]);
+          h[k][j] = fmaf(decay(dt[k], A2[k][j], more), h[k][j], dx[k] * Bv[j]);
         s.part[po[k] + i * Y::ST] =
             fmaf(h[k][0], C.x, fmaf(h[k][1], C.y, fmaf(h[k][2], C.z, h[k][3] * C.w)));
       }
@@ -396,10 +398,12 @@ __global__ void __launch_bounds__(kThreads)
   for (int c = 0; c < K; ++c) {
     const float w = __shfl_sync(0xffffffffu, v2, c * PER + g);
     const float u = __shfl_sync(0xffffffffu, dx, c * PER + g);
-    h[c].x = fmaf(decay(w, A[c].x), h[c].x, u * B[0]);
-    h[c].y = fmaf(decay(w, A[c].y), h[c].y, u * B[1]);
-    h[c].z = fmaf(decay(w, A[c].z), h[c].z, u * B[2]);
-    h[c].w = fmaf(decay(w, A[c].w), h[c].w, u * B[3]);
+    const bool lasts = A[c].x == 0.f || A[c].y == 0.f || A[c].z == 0.f || A[c].w == 0.f;
+    const float more = raised(w, lasts ? 0.f : kShort);
+    h[c].x = fmaf(decay(w, A[c].x, more), h[c].x, u * B[0]);
+    h[c].y = fmaf(decay(w, A[c].y, more), h[c].y, u * B[1]);
+    h[c].z = fmaf(decay(w, A[c].z, more), h[c].z, u * B[2]);
+    h[c].w = fmaf(decay(w, A[c].w, more), h[c].w, u * B[3]);
     if (in && d0 + g + c * PER < a.D) *reinterpret_cast<float4 *>(s + c * PER * a.N) = h[c];
     part[c] = in ? fmaf(h[c].x, C[0], fmaf(h[c].y, C[1], fmaf(h[c].z, C[2], h[c].w * C[3]))) : 0.f;
   }
@@ -483,7 +487,8 @@ __global__ void __launch_bounds__(kThreads)
       const float dx = v * x[c];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        h[c][j] = fmaf(decay(v, A[c][j] * kLog2e), h[c][j], dx * B[j]);
+        const float more = raised(v, A[c][j] == 0.f ? 0.f : kShort);
+        h[c][j] = fmaf(decay(v, A[c][j] * kLog2e, more), h[c][j], dx * B[j]);
         part[c] = fmaf(h[c][j], C[j], part[c]);
       }
 #pragma unroll

@@ -16,6 +16,26 @@ namespace ssm {
 
 constexpr int kThreads = 128;
 
+// e^{dt A}, A2 = A log2 e (or dt's product with it, and A).  The approximate exponential falls
+// short: by 2e-8 of its value on average for exponents between -0.5 and -0.004, by 6e-9 for smaller
+// ones (measured).  Over a state's tokens that adds up, most of all in dA, whose terms weigh by the
+// time that states last (at 4,067 tokens of 512 x 16 states 9.7e-7 of dA's norm; 4.8e-7 with the
+// middle of the two added to the exponent).  A state that must last is kept exactly: with dt = 0
+// (the tokens behind a short tile's last, too) or A = 0 the exponent is 0, for which the instruction
+// promises 1.  So what is added is no more than |dt| (of either of a thread's two channels: one
+// minimum of three instead of two of two; 8,192 x 2,048 x 16, forward and backward: 806 us without,
+// 820 and 827), and nothing by a thread that holds a state with A = 0.
+constexpr float kShort = 1.9e-8f;  // 1.3e-8 / ln 2
+__device__ __forceinline__ float raised(float dt, float most) { return fminf(fabsf(dt), most); }
+__device__ __forceinline__ float raised(const float (&dt)[2], float most) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(dt[0])), "f"(fabsf(dt[1])), "f"(most));
+  return r;
+}
+__device__ __forceinline__ float decay(float dt, float A2, float more) {
+  return mix::ex2(fmaf(dt, A2, more));
+}
+
 template <int LN>
 struct Lay {
   static constexpr int NP = 4 * LN;      // states, padded
@@ -102,12 +122,18 @@ struct Place {
       }
     }
   }
-  __device__ __forceinline__ void decays(const SsmArgs &a, float (&A2)[2][4]) const {
+  // A2 = A log2 e; returns what decay's exponents may be raised by
+  __device__ __forceinline__ float decays(const SsmArgs &a, float (&A2)[2][4]) const {
     read(a, a.A, 0, A2);
+    float most = kShort;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) A2[k][j] *= mix::kLog2e;
+      for (int j = 0; j < 4; ++j) {
+        A2[k][j] *= mix::kLog2e;
+        if (A2[k][j] == 0.f && ch[k] < nch && nl * 4 + j < a.N) most = 0.f;
+      }
+    return most;
   }
 };
 
@@ -167,7 +193,7 @@ struct BcTile {
 
 // A thread's 8 elements of each tile of x (dt, z, dout) on their way into shared memory, S tiles
 // in a ring in which each thread reads only what it copied itself: they take no registers while
-// they wait.  Elements that were not copied (n = 0: no token or no channel) read as anything.
+// they wait.  Elements that were not copied read as anything (no token) or as 0 (no channel).
 // Without 16-byte alignment they wait in registers, one tile ahead.  issue is called for each tile
 // in turn, S - 1 tiles before its get.
 template <typename E, bool VEC, int S_>
@@ -179,9 +205,14 @@ struct TileRing {
   int64_t st;
   mix::Raw8<E> now, next;
 
-  __device__ __forceinline__ TileRing(uint4 *ring_, const void *base, int64_t at, int64_t st_)
+  __device__ __forceinline__ TileRing(uint4 *ring_, const void *base, int64_t at, int64_t st_,
+                                      int nv)
       : ring(ring_), p(reinterpret_cast<const E *>(base) + at), st(st_) {
-    if (!VEC) now = next = mix::zero8<E>();
+    if (!VEC) {
+      now = next = mix::zero8<E>();
+    } else if (nv == 0) {
+      for (int i = 0; i < S * P; ++i) ring[i * kThreads + threadIdx.x] = make_uint4(0, 0, 0, 0);
+    }
   }
   __device__ __forceinline__ void issue(int s, int t, int n) {
     if (VEC) {
@@ -204,6 +235,12 @@ struct TileRing {
     return r;
   }
 };
+
+// What a step's raw size is raised by; 1 where the block has no channel, whose step must not be 0
+// for the sake of the channel that shares its threads (raised).
+__device__ __forceinline__ float step_bias(const float *dt_bias, int c0, int nch, int i) {
+  return i >= nch ? 1.f : dt_bias ? dt_bias[c0 + i] : 0.f;
+}
 
 // (dt, dt x) of a thread's 8 elements of a tile.
 template <typename E, int LN>
@@ -261,16 +298,6 @@ inline bool states_ok(const SsmArgs &a) {
 }
 
 inline int lanes_for(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
-
-// e^{dt A}, A2 = A log2 e (or dt's product with it, and A).  The approximate exponential falls
-// short: by 2e-8 of its value on average for exponents between -0.5 and -0.004, by 6e-9 for smaller
-// ones (measured).  Over a state's tokens that adds up, most of all in dA, whose terms weigh by the
-// time that states last (at 4,067 tokens of 512 x 16 states 9.7e-7 of dA's norm; 4.8e-7 with the
-// middle of the two added to the exponent, at no cost).
-__device__ __forceinline__ float decay(float dt, float A2) {
-  constexpr float kShort = 1.9e-8f;  // 1.3e-8 / ln 2
-  return mix::ex2(fmaf(dt, A2, kShort));
-}
 
 // Replaces val[r] of state i, the end of range r from a zero state, by the state that enters the
 // range; with `back` the same for gradients, from the last range to the first.  A warp is alone on

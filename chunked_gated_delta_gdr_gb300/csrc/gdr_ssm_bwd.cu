@@ -185,10 +185,10 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
   const int t0 = P.r * w.range, n = min(w.range, a.T - t0);
   const int lt = P.tid / Y::CG, lc = P.tid % Y::CG * 8, nv = max(0, min(8, P.nch - lc));
   const int64_t c = P.c0 + lc;
-  R xr(ring, a.x.p, c, a.x.st);
-  R dr(ring + R::kSlots, a.dt.p, c, a.dt.st);
-  R gr(ring + 2 * R::kSlots, a.dout.p, c, a.dout.st);
-  R zr(ring + 3 * R::kSlots, a.z.p, c, a.z.st);
+  R xr(ring, a.x.p, c, a.x.st, nv);
+  R dr(ring + R::kSlots, a.dt.p, c, a.dt.st, nv);
+  R gr(ring + 2 * R::kSlots, a.dout.p, c, a.dout.st, nv);
+  R zr(ring + 3 * R::kSlots, a.z.p, c, a.z.st, nv);
   const bool gated = a.z.p != nullptr;
   const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
   const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
@@ -206,9 +206,9 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
   rb.fetch(Bp, a.B_st, t0, t0 + n, a.N);
   rc.fetch(Cp, a.C_st, t0, t0 + n, a.N);
   for (int i = P.tid; i < Y::CH; i += kThreads)
-    s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
+    s.bias[i] = step_bias(a.dt_bias, P.c0, P.nch, i);
   float A2[2][4], h[2][4], pr[2][4], gs[2][4], S[2] = {0.f, 0.f};
-  P.decays(a, A2);
+  const float most = P.decays(a, A2);
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -264,12 +264,13 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
           Cv[2] = C.z;
           Cv[3] = C.w;
         }
+        const float more = raised(dt, most);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           S[k] += dt[k];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float e = decay(dt[k], A2[k][j]);
+            const float e = decay(dt[k], A2[k][j], more);
             h[k][j] = fmaf(e, h[k][j], dx[k] * Bv[j]);
             if (ENTERS) {
               pr[k][j] *= e;
@@ -440,11 +441,11 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
   const E *Bp = reinterpret_cast<const E *>(a.B) + P.grp * a.B_sg;
   const E *Cp = reinterpret_cast<const E *>(a.C) + P.grp * a.C_sg;
   for (int i = P.tid; i < CH; i += kThreads) {
-    s.bias[i] = a.dt_bias && i < P.nch ? a.dt_bias[P.c0 + i] : 0.f;
+    s.bias[i] = step_bias(a.dt_bias, P.c0, P.nch, i);
     s.skip[i] = a.Dskip && i < P.nch ? a.Dskip[P.c0 + i] : 0.f;
   }
   float A2[2][4], h[2][4];
-  P.decays(a, A2);
+  const float most = P.decays(a, A2);
   range_segments(a, t0, n, s.s);
   if (P.warp == 0) {
     const int tiles = range_tiles(n, s.s, s.at);
@@ -495,10 +496,13 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
     const float4 q = *reinterpret_cast<const float4 *>(&s.pair[i * Y::PT + P.pair]);
     const float4 B = *reinterpret_cast<const float4 *>(&s.b[i * NP + P.nl * 4]);
     const float dt[2] = {q.x, q.z}, dx[2] = {q.y, q.w}, Bv[4] = {B.x, B.y, B.z, B.w};
+    const float more = raised(dt, most);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[k][j] = fmaf(decay(dt[k], A2[k][j]), v[k][j], dx[k] * Bv[j]);
+      for (int j = 0; j < 4; ++j)
+        v[k][j] = fmaf(decay(dt[k], A2[k][j], more), v[k][j], dx[k] * Bv[j]);
+    }
   };
 
   // the sweep: the state before each tile that continues a segment
@@ -596,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
       const float4 C = *reinterpret_cast<const float4 *>(&s.c[i * NP + P.nl * 4]);
       const float dt[2] = {v.x, v.z}, dx[2] = {v.y, v.w}, dy[2] = {dyv.x, dyv.y};
       const float Bv[4] = {B.x, B.y, B.z, B.w}, Cv[4] = {C.x, C.y, C.z, C.w};
+      const float more = raised(dt, most);
       float bc[8];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -606,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
           bc[j] = k ? fmaf(dx[k], g[k][j], bc[j]) : dx[k] * g[k][j];
           bc[4 + j] = k ? fmaf(dy[k], now[k][j], bc[4 + j]) : dy[k] * now[k][j];
           p = j ? fmaf(g[k][j], Bv[j], p) : g[k][j] * Bv[j];
-          g[k][j] *= decay(dt[k], A2[k][j]);
+          g[k][j] *= decay(dt[k], A2[k][j], more);
           const float cr = g[k][j] * before[k][j];
           dA[k][j] = fmaf(dt[k], cr, dA[k][j]);
           cs = j ? fmaf(cr, A2[k][j], cs) : cr * A2[k][j];

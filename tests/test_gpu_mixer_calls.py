@@ -79,3 +79,68 @@ def test_state_space_step_with_parameters_anywhere(N, a_off, s_off):
     yp, _ = gdr.ssm_fwd(x, dt, off(A, a_off), Bv, Cv)
     ya, _ = gdr.ssm_fwd(x, dt, A, Bv, Cv)
     assert_close(yp, ya.double().cpu(), 4, "prompt")
+
+
+# ------------------------------------------------------------------ steps of no length, states that last
+
+def states_kept(T, D, N, cu, zero, dtype=F32):
+    """Forward and backward of segments whose tokens must not change a state: steps of zero, or
+    A = 0 and nothing added."""
+    r = normal(T + D)
+    n = len(cu) - 1
+    x, B, C = r(T, D, dtype=dtype), r(T, 1, N, dtype=dtype), r(T, 1, N, dtype=dtype)
+    A, dt, h0, dht = -r(D, N).abs() - 0.1, r(T, D).abs().to(dtype), r(n, D, N), r(n, D, N)
+    if zero == "dt":
+        dt = torch.zeros_like(dt)
+    else:
+        A, x = torch.zeros_like(A), torch.zeros_like(x)
+    cud = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    _, ht = gdr.ssm_fwd(x, dt, A, B, C, dt_softplus=False, initial_state=h0, cu_seqlens=cud,
+                        output_final_state=True)
+    assert torch.equal(ht, h0), "states"
+    g = gdr.ssm_bwd(x, dt, A, B, C, torch.zeros_like(x), dt_softplus=False, initial_state=h0,
+                    cu_seqlens=cud, dfinal_state=dht)
+    assert torch.equal(g[8], dht), "gradients of the states"
+
+
+@pytest.mark.parametrize("zero", ["dt", "A"])
+@pytest.mark.parametrize("T,D,N,cu", [
+    (260, 64, 16, list(range(0, 261, 2))),    # tiles that a bound cuts short
+    (300, 48, 5, [0, 1, 100, 103, 300]),
+    (700, 36, 64, [0, 700]),
+    (1501, 2048, 16, [0, 700, 701, 1501]),
+    (1300, 4096, 8, [0, 1300]),
+    (5003, 4096, 16, [0, 2101, 5003]),        # one thread a channel
+])
+def test_states_that_must_last_are_kept_exactly(T, D, N, cu, zero):
+    states_kept(T, D, N, cu, zero)
+
+
+def test_states_beside_one_that_must_last():
+    """One state of each channel with A = 0, the others decaying."""
+    r = normal(6)
+    T, D, N = 600, 64, 16
+    A, h0 = -r(D, N).abs() - 0.1, r(1, D, N)
+    A[:, 3] = 0
+    x, B = torch.zeros(T, D, device=DEV), r(T, 1, N)
+    dt = r(T, D).abs() * 0.01
+    _, ht = gdr.ssm_fwd(x, dt, A, B, B, dt_softplus=False, initial_state=h0, output_final_state=True)
+    want = h0.double() * torch.exp(dt.double().sum(0)[:, None] * A.double())
+    assert torch.equal(ht[:, :, 3], h0[:, :, 3])
+    assert_close(ht, want, 600, "states")
+
+
+@pytest.mark.parametrize("zero", ["dt", "A"])
+@pytest.mark.parametrize("D,N,G", [(128, 16, 1), (100, 16, 2), (48, 5, 1), (64, 64, 1)])
+def test_steps_that_must_keep_a_state(D, N, G, zero):
+    r = normal(D)
+    x, B, C = r(3, D), r(3, G, N), r(3, G, N)
+    A, dt, st = -r(D, N).abs() - 0.1, r(3, D).abs(), r(3, D, N)
+    if zero == "dt":
+        dt = torch.zeros_like(dt)
+    else:
+        A, x = torch.zeros_like(A), torch.zeros_like(x)
+    pool = st.clone()
+    for _ in range(50):
+        gdr.ssm_step(x, dt, A, B, C, pool, dt_softplus=False)
+    assert torch.equal(pool, st)
