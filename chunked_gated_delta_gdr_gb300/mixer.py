@@ -14,6 +14,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _native as nat
+from ._autograd import first_only
 
 _ext = None
 
@@ -236,12 +237,13 @@ class _ShortConv(torch.autograd.Function):
             x, w, _grad(dy, x), b, h0, cu, ctx.activation,
             None if dht is None else dht.to(x.dtype).contiguous(),
             want_dinitial=h0 is not None and ctx.needs_input_grad[3])
-        return dx, _cast(dw, w), _cast(db, b), dh0, None, None, None
+        return first_only("short_conv", (dx, _cast(dw, w), _cast(db, b), dh0, None, None, None),
+                          x, w, b, h0, dy, dht)
 
 
 def short_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, activation="silu",
                output_final_state: bool = False):
-    """Differentiable ``conv_fwd``: (y, final_state or None)."""
+    """Differentiable ``conv_fwd``, once: (y, final_state or None)."""
     return _ShortConv.apply(x, weight, bias, initial_state, cu_seqlens, activation,
                             output_final_state)
 
@@ -264,12 +266,14 @@ class _SelectiveSsm(torch.autograd.Function):
             x, dt, A, B, C, _grad(dy, x), D, z, dt_bias, ctx.dt_softplus, h0, cu,
             None if dht is None else dht.float().contiguous(),
             want_dinitial=h0 is not None and ctx.needs_input_grad[9])
-        return dx, ddt, dA, dB, dC, dD, dz, dbias, None, dh0, None, None
+        return first_only("selective_ssm",
+                          (dx, ddt, dA, dB, dC, dD, dz, dbias, None, dh0, None, None),
+                          x, dt, A, B, C, D, z, dt_bias, h0, dy, dht)
 
 
 def selective_ssm(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = True,
                   initial_state=None, cu_seqlens=None, output_final_state: bool = False):
-    """Differentiable ``ssm_fwd``: (y, final_state or None)."""
+    """Differentiable ``ssm_fwd``, once: (y, final_state or None)."""
     return _SelectiveSsm.apply(x, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state,
                                cu_seqlens, output_final_state)
 
@@ -288,11 +292,12 @@ class _QkNormRotate(torch.autograd.Function):
         norm, eps, inter = ctx.options
         dq, dk, dqw, dkw = qk_bwd(q, k, _grad(dqo, q), _grad(dko, k), qw, kw, norm, eps, cos,
                                   sin, pos, inter)
-        return dq, dk, _cast(dqw, qw), _cast(dkw, kw), None, None, None, None, None, None
+        return first_only("qk_norm_rotate", (dq, dk, _cast(dqw, qw), _cast(dkw, kw), None, None,
+                                             None, None, None, None), q, k, qw, kw, dqo, dko)
 
 
 def qk_norm_rotate(q, k, q_weight=None, k_weight=None, norm: str = "rms", eps: float = 1e-6,
                    cos=None, sin=None, positions=None, interleaved: bool = False):
-    """Differentiable ``qk_fwd``: new (q, k)."""
+    """Differentiable ``qk_fwd``, once: new (q, k)."""
     return _QkNormRotate.apply(q, k, q_weight, k_weight, norm, eps, cos, sin, positions,
                                interleaved)

@@ -144,3 +144,29 @@ def test_steps_that_must_keep_a_state(D, N, G, zero):
     for _ in range(50):
         gdr.ssm_step(x, dt, A, B, C, pool, dt_softplus=False)
     assert torch.equal(pool, st)
+
+
+# ------------------------------------------------------------------ derivatives of derivatives
+
+def test_second_derivatives_are_refused():
+    """The backwards are kernels without a derivative: a loss of their gradients is an error, where
+    the gradients' share of it would otherwise be left out."""
+    r = normal(2)
+    x, w = r(20, 64).requires_grad_(), r(64, 4).requires_grad_()
+    A, B = (-r(64, 16).abs()).requires_grad_(), r(20, 1, 16)
+    q = r(20, 2, 64).requires_grad_()
+    for f, leaf in ((lambda: gdr.short_conv(x, w)[0], x),
+                    (lambda: gdr.selective_ssm(x, x, A, B, B)[0], A),
+                    (lambda: gdr.qk_norm_rotate(q, q)[0], q)):
+        for loss in (lambda y: (y * y).sum(), lambda y: y.sum()):  # with and without y's own gradient
+            value = loss(f())
+            grad, = torch.autograd.grad(value, leaf, create_graph=True)
+            with pytest.raises(RuntimeError, match="first derivatives only"):
+                (value + (grad * grad).sum()).backward()
+            plain, = torch.autograd.grad(loss(f()), leaf)
+            assert torch.equal(grad, plain)
+    # gradients that keep their graph can still be added up and set to zero
+    for _ in range(2):
+        gdr.short_conv(x, w)[0].sum().backward(create_graph=True)
+    torch.optim.SGD([x, w], 0.1).zero_grad(set_to_none=False)
+    assert float(x.grad.abs().sum()) == 0
