@@ -17,6 +17,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _native as nat
+from ._autograd import first_only
 
 _DT = {torch.bfloat16: nat.GDR_BF16, torch.float32: nat.GDR_F32, torch.int32: nat.GDR_I32}
 
@@ -410,15 +411,16 @@ class _ChunkGatedDeltaRule(torch.autograd.Function):
             initial_state=h0, cu_seqlens=cu,
             dht=None if dht is None else dht.float().contiguous(),
             want_dh0=h0 is not None and ctx.needs_input_grad[6])
-        return (dq.to(q.dtype), dk.to(k.dtype), dv.to(v.dtype), dg.to(g.dtype),
-                db.to(beta.dtype), None, dh0, None, None)
+        grads = (dq.to(q.dtype), dk.to(k.dtype), dv.to(v.dtype), dg.to(g.dtype),
+                 db.to(beta.dtype), None, dh0, None, None)
+        return first_only("chunk_gated_delta_rule", grads, q, k, v, g, beta, h0, do, dht)
 
 
 def chunk_gated_delta_rule(q, k, v, g, beta, scale: Optional[float] = None,
                            initial_state: Optional[torch.Tensor] = None,
                            output_final_state: bool = False,
                            cu_seqlens: Optional[torch.Tensor] = None):
-    """Differentiable chunked gated delta rule: (o, ht) = forward, gradients through
+    """Differentiable (once) chunked gated delta rule: (o, ht) = forward, gradients through
     ``chunk_bwd``.  Layouts as ``chunk_fwd``; device tensors only."""
     if scale is None:
         scale = q.shape[-1] ** -0.5

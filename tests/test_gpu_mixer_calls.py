@@ -170,3 +170,19 @@ def test_second_derivatives_are_refused():
         gdr.short_conv(x, w)[0].sum().backward(create_graph=True)
     torch.optim.SGD([x, w], 0.1).zero_grad(set_to_none=False)
     assert float(x.grad.abs().sum()) == 0
+
+
+def test_second_derivatives_of_the_chunk_function_are_refused():
+    from chunked_gated_delta_gdr_gb300.inputs import make_workload
+    w = make_workload("twice", 3, [70, 30], 1, 2, 64).to(DEV)
+    leaves = [t.detach().requires_grad_() for t in (w.q, w.k, w.v, w.g, w.beta)]
+
+    def value():
+        return gdr.chunk_gated_delta_rule(*leaves, scale=w.scale, cu_seqlens=w.cu_seqlens)[0].float().sum()
+
+    v = value()
+    grads = torch.autograd.grad(v, leaves, create_graph=True)
+    with pytest.raises(RuntimeError, match="first derivatives only"):
+        (v + sum((t.float() ** 2).sum() for t in grads)).backward()
+    for a, b in zip(torch.autograd.grad(value(), leaves), grads):
+        assert torch.equal(a, b)
