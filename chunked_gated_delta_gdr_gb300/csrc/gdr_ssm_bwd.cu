@@ -740,10 +740,11 @@ __global__ void k_ssm_bc_sums(const float *bc, int64_t T, int G, int N, int NP, 
                               E *dC) {
   after_previous();
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  const int64_t t = i / (G * 2 * N);
+  const int64_t row = (int64_t)G * 2 * N, t = i / row;  // of a token: past 32 bits for many groups
   if (t >= T) return;
-  const int rest = (int)(i % (G * 2 * N)), grp = rest / (2 * N), m = rest % N;
-  const int kind = rest / N & 1;  // 0: dB, 1: dC
+  const int64_t part = (i - t * row) / N;
+  const int m = (int)(i - t * row - part * N);
+  const int grp = (int)(part >> 1), kind = (int)(part & 1);  // 0: dB, 1: dC
   const float *q = bc + ((int64_t)grp * tpg * T + t) * (2 * NP) + kind * NP + m;
   const int64_t st = T * (2 * NP);
   float s[4] = {0, 0, 0, 0};

@@ -237,3 +237,28 @@ def test_norm_over_many_tokens_a_block(T, Hq, Hk, d, rot, inter, norm, dtype):
         assert_close(grads[j], lx.grad, 32, "dx")
         # a thread adds the rows that its block's lane groups share out: under 1 in 1,000
         assert_summed(grads[2 + j], lw.grad.reshape(T * h, d), T * h // 1000 + 100, "dw")
+
+
+def test_state_space_gradients_of_many_groups():
+    """A token's dB and dC of 2^24 groups of 64 states pass 32 bits of elements."""
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("needs 120 GB of free device memory")
+    T, G, N = 2, 1 << 24, 64
+    g = torch.Generator(device=DEV).manual_seed(7)
+    r = lambda *s: torch.empty(*s, dtype=BF16, device=DEV).normal_(generator=g)
+    x, dt, dy, B, C = r(T, G), r(T, G) - 3, r(T, G), r(T, G, N), r(T, G, N)
+    A = -torch.empty(G, N, device=DEV).uniform_(0.5, 2, generator=g)
+    _, _, _, dB, dC, _, _, _, _ = gdr.ssm_bwd(x, dt, A, B, C, dy, want_dinitial=False)
+    at = torch.cat([torch.arange(0, 64), torch.arange(G // 2 - 64, G // 2 + 64),
+                    torch.randint(0, G, (4000,), generator=torch.Generator().manual_seed(1)),
+                    torch.arange(G - 64, G)]).to(DEV)
+    xs, ds, gs = (t[:, at].double() for t in (x, dt, dy))
+    As, Bs, Cs = A[at].double(), B[:, at].double(), C[:, at].double()
+    v = torch.nn.functional.softplus(ds)
+    decay = torch.exp(v[1, :, None] * As)
+    u = (v * xs)[:, :, None] * Bs
+    h = torch.stack([u[0], decay * u[0] + u[1]])
+    grad = gs[:, :, None] * Cs
+    grad = torch.stack([grad[0] + decay * grad[1], grad[1]])
+    assert_close(dC[:, at], gs[:, :, None] * h, 8, "dC")
+    assert_close(dB[:, at], (v * xs)[:, :, None] * grad, 8, "dB")
