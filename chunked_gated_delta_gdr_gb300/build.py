@@ -42,6 +42,7 @@ def _deps():
     files = [os.path.join(CSRC, f) for f in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "gdr.h"))
+    files.append(os.path.join(CSRC, BINDING_SOURCE))
     files.append(os.path.abspath(__file__))
     return files
 
@@ -49,9 +50,8 @@ def _deps():
 def _stale() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    if os.path.getmtime(os.path.join(CSRC, BINDING_SOURCE)) > os.path.getmtime(BINDING):
-        return True
-    t = os.path.getmtime(LIB)
+    # the older of the two: a build may have replaced the library and failed at the binding
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
