@@ -595,9 +595,10 @@ cudaError_t step_by_lanes(const SsmArgs &a, float *state, int32_t slots, const i
 }  // namespace ssm
 
 size_t ssm_fwd_workspace(int64_t T, int32_t D, int32_t N, int32_t G) {
-  // the layout also goes by the tensors' alignment: room for either
+  // the layout also goes by the tensors' type and alignment: room for either (fp32 takes the wide one
+  // wherever bf16 does)
   const size_t lanes = ssm::carve_ranges(nullptr, T, D, N, ssm::range_for(T, D, N, G)).bytes;
-  const int wide = ssm::wide_range(T, D, N, G);
+  const int wide = ssm::wide_range(T, D, N, G, true);
   const size_t bytes = wide ? ssm::carve_ranges(nullptr, T, D, N, wide).bytes : 0;
   return bytes > lanes ? bytes : lanes;
 }
@@ -608,7 +609,7 @@ cudaError_t launch_ssm_fwd(const SsmArgs &args, cudaStream_t stream) {
   a.n4 = states_ok(a);
   const bool vec = (a.D / a.G) % 8 == 0 && rows_ok(a.x, a.f32) && rows_ok(a.dt, a.f32) &&
                    rows_ok(a.z, a.f32) && rows_ok(a.y, a.f32) && bc_ok(a);
-  const int wide = vec ? wide_range(a.T, a.D, a.N, a.G) : 0;
+  const int wide = vec ? wide_range(a.T, a.D, a.N, a.G, a.f32) : 0;
   if (wide) return launch_wide(a, wide, stream);
   return a.f32 ? fwd_by_lanes<float>(a, vec, stream)
                : fwd_by_lanes<__nv_bfloat16>(a, vec, stream);

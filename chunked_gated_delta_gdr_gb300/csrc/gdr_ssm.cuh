@@ -378,7 +378,7 @@ cudaError_t allow_smem(K k, int bytes) {
 
 // The layout of one thread a channel (gdr_ssm_wide.cu): its tokens of a range where it is worth
 // while (aligned rows), else 0.
-int wide_range(int64_t T, int32_t D, int32_t N, int32_t G);
+int wide_range(int64_t T, int32_t D, int32_t N, int32_t G, bool f32);
 cudaError_t launch_wide(const SsmArgs &a, int range, cudaStream_t stream);
 
 inline int64_t channel_tiles(int D, int G, int LN) {

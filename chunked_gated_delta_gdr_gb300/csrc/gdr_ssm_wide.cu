@@ -329,15 +329,22 @@ cudaError_t run_wide(const SsmArgs &a, int range, cudaStream_t stream) {
 
 }  // namespace
 
-int wide_range(int64_t T, int32_t D, int32_t N, int32_t G) {
+int wide_range(int64_t T, int32_t D, int32_t N, int32_t G, bool f32) {
   if (N > 16) return 0;
   const int64_t ctiles = G * ceil_div64(D / G, kThreads), room = (int64_t)sm_count() * kCtas;
-  // enough work: the blocks that run at once have 16 tiles of tokens each (with 13, at 8,192 x
-  // 2,048, this layout measured 15 % slower; with 67, at 20,468 x 4,096, 11 % faster), and the
-  // channels of a group fill at least 3 in 4 lanes
+  // enough work, 16 tiles of tokens for each block that could run, and the channels of a group fill
+  // at least 3 in 4 lanes.  Lanes / this layout in us, 16 states in bf16: 2,437 x 4,096 (8 tiles)
+  // 103 / 102, 4,869 (16) 196 / 181, 20,373 (67) 788 / 679; 8 states 133 / 125 with 16 tiles
   if (T * ctiles < room * 16 * kL || (int64_t)D * 4 < ctiles * kThreads * 3) return 0;
   int64_t n = room / ctiles;
-  if (n > kMost) n = kMost;
+  if (n > kMost) {
+    n = kMost;
+    // few channels: kMost ranges of them do not fill the GPU, however long the prompt.  bf16 with
+    // 67 tiles: 2,304 channels (95 % of the blocks) 792 / 714, 2,048 (84 %) 754 / 800, 1,024 (42 %)
+    // 756 / 1,022, 512 (21 %) 761 / 1,672.  fp32, whose rings leave the lanes fewer blocks an SM:
+    // 2,048 1,251 / 806, 1,024 1,250 / 1,030, 512 1,196 / 1,710
+    if (n * ctiles * 10 < room * (f32 ? 4 : 9)) return 0;
+  }
   if (n < 1) n = 1;
   return (int)(ceil_div64(ceil_div64(T, n), kL) * kL);
 }

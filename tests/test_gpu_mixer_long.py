@@ -262,3 +262,23 @@ def test_state_space_gradients_of_many_groups():
     grad = torch.stack([grad[0] + decay * grad[1], grad[1]])
     assert_close(dC[:, at], gs[:, :, None] * h, 8, "dC")
     assert_close(dB[:, at], (v * xs)[:, :, None] * grad, 8, "dB")
+
+
+@pytest.mark.parametrize("D,dtype", [(512, BF16), (1024, F32), (2304, BF16)])
+def test_state_space_long_prompts_of_few_channels(D, dtype):
+    """Prompts long enough for the layout of one thread a channel, on both sides of its rule."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    T, N = 17 * 16 * 4 * sms // -(-D // 128) + 5, 16
+    r = normal(D)
+    cu = [0, 1000, 1001, T - 77, T]
+    n = len(cu) - 1
+    x, dt, z = r(T, D, dtype=dtype), (r(T, D, std=0.5) - 3).to(dtype), r(T, D, dtype=dtype)
+    A, B, C = -torch.exp(r(D, N, std=0.5)), r(T, 1, N, dtype=dtype), r(T, 1, N, dtype=dtype)
+    skip, bias, h0 = r(D), r(D, std=0.3), r(n, D, N)
+    y, ht = gdr.ssm_fwd(x, dt, A, B, C, skip, z, bias, True, h0,
+                        torch.tensor(cu, dtype=torch.int32, device=DEV), True)
+    with torch.no_grad():
+        yr, hr, _ = ref.ssm(*[t.double() for t in (x, dt, A, B, C, skip, z, bias)], True,
+                            h0.double(), cu)
+    assert_close(y, yr, 400, "y")  # states last about 100 tokens
+    assert_close(ht, hr, 400, "final state")
