@@ -239,10 +239,18 @@ def test_norm_over_many_tokens_a_block(T, Hq, Hk, d, rot, inter, norm, dtype):
         assert_summed(grads[2 + j], lw.grad.reshape(T * h, d), T * h // 1000 + 100, "dw")
 
 
-def test_state_space_gradients_of_many_groups():
-    """A token's dB and dC of 2^24 groups of 64 states pass 32 bits of elements."""
+@pytest.fixture
+def memory():
+    """120 GB of device memory, given back afterwards."""
+    torch.cuda.empty_cache()
     if torch.cuda.mem_get_info()[0] < 120 << 30:
         pytest.skip("needs 120 GB of free device memory")
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_state_space_gradients_of_many_groups(memory):
+    """A token's dB and dC of 2^24 groups of 64 states pass 32 bits of elements."""
     T, G, N = 2, 1 << 24, 64
     g = torch.Generator(device=DEV).manual_seed(7)
     r = lambda *s: torch.empty(*s, dtype=BF16, device=DEV).normal_(generator=g)
