@@ -9,8 +9,8 @@
 //
 // Bound by HBM: each row is read once and written once.  8 elements a lane, 16 bytes of bf16; a
 // group of lanes keeps one token's cosines and sines in registers while it runs over the token's
-// heads, q's and then k's.  65,536 tokens of 48 heads of 128 in bf16: 279 us, 5.8 TB/s of 6.8; the
-// backward 425 us, 5.7 TB/s.
+// heads, q's and then k's.  65,536 tokens of 48 heads of 128 in bf16: 277 us, 5.8 TB/s of 6.8; the
+// backward 424 us, 5.7 TB/s.  L2 without a rotation 271 and 414.
 #include <type_traits>
 
 #include "gdr_mix.cuh"
@@ -423,8 +423,8 @@ __device__ __forceinline__ F warp_sum(F v) {
 }
 
 // Any head size up to 256, any strides: one warp for each row, the row read again for the
-// partners of the rotation (36,939 tokens of 15 heads of 232, half of each rotated by halves: 469 us
-// where interleaved pairs take the fast path's 100).  WIDE: the backward's row sums and its last
+// partners of the rotation (36,939 tokens of 15 heads of 232, half of each rotated by halves: 465 us
+// where interleaved pairs take the fast path's 98; backward 1,419 and 149).  WIDE: the backward's row sums and its last
 // difference are in 64 bits, for heads of a few elements: there r m and x r^3 (sum x m) / d nearly
 // cancel (at d = 1 only eps is left).
 template <typename E, bool BWD, bool WIDE>

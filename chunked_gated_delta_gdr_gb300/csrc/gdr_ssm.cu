@@ -12,8 +12,8 @@
 // prompt fills the GPU and ragged ones stay balanced.  Pass 1 runs each range from a zero state
 // and keeps the state at its end and the sum of dt (a range's decay is e^{A sum dt}); pass 2
 // chains the ends before its range, runs it from its true state and writes y.  When one range is
-// enough, only pass 2 runs.  1,537 tokens of 1,002 x 12 states in fp32: 34 us, the latency of the
-// passes; 2,048 of 4,096 x 16: 89 us.
+// enough, only pass 2 runs.  1,537 tokens of 1,002 x 12 states in fp32: 33 us, the latency of the
+// passes; 2,048 of 4,096 x 16: 92 us.
 #include "gdr_ssm.cuh"
 
 namespace gdr {
@@ -22,7 +22,12 @@ namespace {
 
 using namespace mix;
 
-constexpr int kFwdCtas = 4;  // blocks of pass 2 on each SM: the ranges are cut to run all at once
+// Blocks of pass 2 on each SM, by which the ranges are cut: all of them run at once for up to 16
+// states in bf16 and 8 in fp32.  A tile's tokens grow with the lanes of a channel, and the partial
+// sums of y with both: 74 KB a block for 17 to 32 states, 138 KB above (fp32 93 and 157, 67 for 9 to 16
+// states) leave 3 and 1 blocks (2 and 1, 3), so that the grid runs in up to four waves: 8,192 x
+// 2,048 x 16, 32 and 64 in bf16 160, 358 and 1,016 us.
+constexpr int kFwdCtas = 4;
 constexpr int kEndCtas = 5;
 constexpr int kAhead = 3;    // tiles in the rings
 constexpr int kLeast = 4;    // tiles of a range at least where there are over kFew ranges
@@ -349,8 +354,8 @@ __device__ __forceinline__ void four(const float *p, int n, float (&f)[4]) {
 // written once.  A warp takes CW neighbouring channels of a row: LN lanes hold a channel's states,
 // 4 each, and K times PER channels follow one another, so that each of its K loads of states is one
 // run of 512 bytes.  What belongs to a channel alone (step size, skip, gate, output) is one lane's
-// each, and the sums over states come back to it.  128 rows of 4,096 x 16 states: 15.5 us with
-// the states in HBM (4.5 TB/s; one fill and one drain of the GPU are a third of it), 10 us from L2.
+// each, and the sums over states come back to it.  128 rows of 4,096 x 16 states: 14.5 us with
+// the states in HBM (4.8 TB/s; one fill and one drain of the GPU are a third of it), 9.3 us from L2.
 template <typename E, int LN>
 __global__ void __launch_bounds__(kThreads)
     k_ssm_step(const SsmArgs a, float *state, int slots, const int32_t *idx, int cblocks) {
@@ -511,9 +516,9 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Tokens of a range: as many ranges as run at once, but no more than make a long chain.  Short
-// ranges shorten the two passes of little work: 339 tokens of 448 channels of 32 states 27 us in
-// ranges of four tiles, 19 us in ranges of one; 7,922 of 128 of 16 39 us and, with the chain over
-// two and a half times the ranges, 44.
+// ranges shorten the two passes of little work: 339 tokens of 448 channels of 32 states in fp32 27 us
+// in ranges of four tiles, 15 us in ranges of one, 1,537 of 1,002 of 12 36 and 32; 7,922 of 128 of 16
+// 29.7 us and, with the chain over two and a half times the ranges, 31.7.
 int range_for(int64_t T, int32_t D, int32_t N, int32_t G) {
   const int LN = lanes_for(N), tile = 4 * LN;
   const int64_t ctiles = channel_tiles(D, G, LN);

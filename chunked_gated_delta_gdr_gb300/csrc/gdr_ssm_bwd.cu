@@ -21,9 +21,11 @@
 // channels (dB, dC) go over the warp's lanes by a transposing butterfly, over its warps in shared
 // memory and over the blocks in a last kernel, always in the same order.
 //
-// About 16 products and 3 exponentials for each token, channel and state in pass 2, and 6 and 1 in
-// pass 1: bound by instruction issue and, with 16 warps an SM, its latencies: 60 % of the slots.
-// 8,192 tokens of 2,048 x 16 states in bf16: 640 us (pass 1 130, chain 22, pass 2 470).
+// 16 products and 3 exponentials for each token, channel and state in pass 2, of about 41 instructions (the
+// others move and sum: shared and Tensor Memory, the sums over channels), and 6 and 1 in pass 1: bound
+// by instruction issue and, with 16 warps an SM, its latencies: 60 % of the slots.  8,192 tokens of
+// 2,048 x 16 states in bf16: 650 us (under the profiler pass 1 131, chain 27, pass 2 475, sums 25); of 32
+// and 64 states 1,153 and 2,478 us.
 #include "gdr_ssm.cuh"
 #include "gdr_tc.cuh"
 
@@ -50,7 +52,7 @@ struct BwdWork {
   float *sum;       // [n][D]: sum of dt
   float *pd, *pb;   // [n][D]: parts of dD and ddt_bias
   int *reset;       // [n]
-  float *bc;        // [channel tiles][T][2][NP]: parts of dB and dC
+  float *bc;        // [channel tiles][T][2][NP]: parts of dB and dC, T x D x LN^2 / 8 bytes
   size_t bytes;
 };
 
@@ -413,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
   constexpr int NP = Y::NP, CH = Y::CH;
   // tokens of a tile unrolled: all of them outgrow the instruction cache (8,192 tokens of 2,048
   // channels of 16 states with the forward: 848 us, by fours 824), but for two lanes a channel,
-  // where indexes in registers cost more (4,124 x 832 x 8: 176 and 198 us)
+  // where indexes in registers cost more (4,124 x 832 x 8: 176 and 198 us) than the spills of the whole
+  // tile's addresses (160 to 360 bytes a thread)
   constexpr int kUnroll = LN > 2 ? 4 : kBT;
   constexpr int M = kBT * CH / kThreads;  // elements of x a thread has of a tile
   constexpr int LEFT = LN <= 4 ? 1 : LN / 4;  // channel sums left to a lane

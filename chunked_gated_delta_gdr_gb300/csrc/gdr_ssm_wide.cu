@@ -11,8 +11,9 @@
 // of them with 32 products: 49 cycles a warp and sub-partition), so that a token's 16 states cost
 // at least 98 cycles, with the step size, gate and traffic about 150; measured 195.
 //
-// Ranges, pass 1 and pass 2 are those of gdr_ssm.cu.  20,468 tokens of 4,096 x 16 states in bf16:
-// 682 us (257 and 423), 76 and 72 % of the issue slots.
+// Ranges, pass 1 and pass 2 are those of gdr_ssm.cu; the decays are the approximate exponential's as
+// they are, without what gdr_ssm.cuh's decay adds.  20,468 tokens of 4,096 x 16 states in bf16: 680 us
+// (258 and 427 under the profiler), 76 and 72 % of the issue slots.
 #include "gdr_ssm.cuh"
 
 namespace gdr {

@@ -5,7 +5,8 @@ Device tensors only; marshalling is in ``_mixer`` (csrc/mixer_binding.cpp): desc
 tensors, outputs and scratch from PyTorch's allocator, torch's current stream.  With ``stream``,
 that stream is made current for the call, so that what the call allocates belongs to it; inputs
 that another stream may reuse while the call runs are the caller's to keep
-(``Tensor.record_stream``).  Layouts and formulas are those of include/gdr.h.
+(``Tensor.record_stream``).  Outputs that are given must not overlap inputs.  Layouts and formulas
+are those of include/gdr.h.
 """
 from __future__ import annotations
 

@@ -429,7 +429,11 @@ size_t gdr_ssm_fwd_workspace_bytes(int64_t T, int32_t Dm, int32_t N, int32_t G);
  *   dx, ddt, dz [T, Dm] (dz iff z), dB, dC [T, G, N] compact: out, x's type
  *   dA [Dm, N], dD [Dm] (or NULL), ddt_bias [Dm] (or NULL), dh0 [n_seq, Dm, N] (or NULL):
  *   f32 compact out
- *   workspace  256-byte aligned, >= gdr_ssm_bwd_workspace_bytes(T, Dm, N, G) bytes
+ *   workspace  256-byte aligned, >= gdr_ssm_bwd_workspace_bytes(T, Dm, N, G) bytes.  Most of it holds
+ *   parts of dB and dC: T x Dm x L^2 / 8 bytes, L = 2, 4, 8, 16 for N up to 8, 16, 32, 64 (at
+ *   65,536 x 4,096 0.5 GB for N = 16, 2.1 for 32, 8.6 for 64).
+ * Infinities and NaN in one segment's inputs reach no other segment's outputs and gradients; the
+ * parameters' gradients sum over all segments.
  */
 int gdr_ssm_bwd(const gdr_tensor_t *x, const gdr_tensor_t *dt, const gdr_tensor_t *A,
                 const gdr_tensor_t *B, const gdr_tensor_t *C, const gdr_tensor_t *D,
