@@ -26,6 +26,21 @@ from .api import (  # noqa: F401
     wait_selftest,
     workspace_bytes,
 )
+from .block import (  # noqa: F401
+    attn_step,
+    cache_plan,
+    cache_write,
+    gated_norm,
+    gated_norm_bwd,
+    gated_norm_fwd,
+    gated_recurrence,
+    rec_bwd,
+    rec_fwd,
+    rec_step,
+    residual_norm,
+    residual_norm_bwd,
+    residual_norm_fwd,
+)
 from .mixer import (  # noqa: F401
     conv_bwd,
     conv_fwd,

@@ -72,6 +72,25 @@ SIGNATURES = {
                    + [_sz, _vp]),
     "gdr_qk_bwd_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
     "gdr_delta_step": (ctypes.c_int, [_vp] * 5 + [_f32] + [_vp] * 4),
+    "gdr_rec_fwd": (ctypes.c_int, [_vp] * 4 + [_i32] + [_vp] * 2 + [_i32] + [_vp] * 4),
+    "gdr_rec_checkpoint_rows": (_i64, [_i64]),
+    "gdr_rec_bwd": (ctypes.c_int, [_vp] * 4 + [_i32] + [_vp] * 2 + [_i32] + [_vp] * 9
+                    + [_sz, _vp]),
+    "gdr_rec_bwd_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
+    "gdr_rec_step": (ctypes.c_int, [_vp] * 4 + [_i32] + [_vp] * 4),
+    "gdr_gated_norm_fwd": (ctypes.c_int, [_vp] * 3 + [_i32, _f32] + [_vp] * 2),
+    "gdr_gated_norm_bwd": (ctypes.c_int, [_vp] * 3 + [_i32, _f32] + [_vp] * 5 + [_sz, _vp]),
+    "gdr_gated_norm_bwd_workspace_bytes": (_sz, [_i64, _i32, _i32]),
+    "gdr_residual_norm_fwd": (ctypes.c_int, [_vp] * 3 + [_i32] + [_vp] * 2 + [_f32] * 2
+                              + [_vp] * 3),
+    "gdr_residual_norm_bwd": (ctypes.c_int, [_vp] * 3 + [_i32] + [_vp] * 2 + [_f32] * 2
+                              + [_vp] * 8 + [_sz, _vp]),
+    "gdr_residual_norm_bwd_workspace_bytes": (_sz, [_i64, _i32]),
+    "gdr_attn_step": (ctypes.c_int, [_vp] * 5 + [_f32, _i32] + [_vp] * 2 + [_sz, _vp]),
+    "gdr_attn_step_workspace_bytes": (_sz, [_i32] * 4),
+    "gdr_cache_plan": (ctypes.c_int, [_vp] * 2 + [_i32] + [_vp] * 3 + [_i32] + [_vp] * 2 + [_i32]
+                       + [_vp] * 4),
+    "gdr_cache_write": (ctypes.c_int, [_vp] * 6),
     "gdr_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "gdr_version": (ctypes.c_int, []),
 }

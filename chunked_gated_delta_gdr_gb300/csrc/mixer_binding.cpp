@@ -1,10 +1,11 @@
-// mixer_binding.cpp -- the Python binding of the mixer's operators: argument marshalling only.
+// mixer_binding.cpp -- the Python binding of the mixer's and a hybrid block's operators: argument
+// marshalling only.
 //
 // A single-token call costs the GPU a few microseconds; describing its tensors from Python cost
 // three times that.  Here descriptors point straight at the tensors' sizes and strides, outputs
 // come from PyTorch's allocator, and the work goes to libgdr's C entry points on torch's current
-// stream.  Arguments are positional and complete: the Python functions in mixer.py give them
-// names, defaults and documentation.
+// stream.  Arguments are positional and complete: the Python functions in mixer.py and block.py
+// give them names, defaults and documentation.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -46,6 +47,20 @@ struct Call {
       default: refuse(PyExc_TypeError, "unsupported dtype: tensors are bfloat16 or float32");
     }
     if (t.dim() < 1 || t.dim() > 4) refuse(PyExc_ValueError, "tensors must have 1..4 dims");
+    g.data = t.numel() ? t.data_ptr() : nullptr;
+    g.ndim = (int32_t)t.dim();
+    for (int i = 0; i < 4; ++i) g.shape[i] = i < t.dim() ? t.size(i) : 0;
+    g.strides = t.strides().data();
+    return &g;
+  }
+  // int32 [rows, any], rows of any stride
+  gdr_tensor_t *table(const at::Tensor &t, const char *name) {
+    if (t.scalar_type() != at::kInt)
+      refuse(PyExc_TypeError, (std::string(name) + " must be int32").c_str());
+    if (!t.is_cuda() || t.get_device() != index)
+      refuse(PyExc_ValueError, "tensors must be on one CUDA device");
+    gdr_tensor_t &g = d[n++];
+    g.dtype = GDR_I32;
     g.data = t.numel() ? t.data_ptr() : nullptr;
     g.ndim = (int32_t)t.dim();
     for (int i = 0; i < 4; ++i) g.shape[i] = i < t.dim() ? t.size(i) : 0;
@@ -135,6 +150,21 @@ int32_t norm_of(PyObject *o) {
     if (PyUnicode_CompareWithASCIIString(o, "l2") == 0) return GDR_NORM_L2;
   }
   refuse(PyExc_ValueError, "norm must be 'rms' or 'l2'");
+}
+
+int32_t gate_activation(PyObject *o) {
+  if (PyUnicode_Check(o)) {
+    if (PyUnicode_CompareWithASCIIString(o, "silu") == 0) return GDR_ACT_SILU;
+    if (PyUnicode_CompareWithASCIIString(o, "sigmoid") == 0) return GDR_ACT_SIGMOID;
+  }
+  refuse(PyExc_ValueError, "activation must be 'silu' or 'sigmoid'");
+}
+int32_t whole(PyObject *o, const char *name) {
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) throw python_error();
+  if (v < -0x7ff00000L || v > 0x7ff00000L)
+    refuse(PyExc_ValueError, (std::string(name) + " is out of range").c_str());
+  return (int32_t)v;
 }
 
 struct Scratch {
@@ -411,6 +441,243 @@ ENTRY(delta_step, 9)
   return wrap(o);
 EXIT
 
+// x, r, A, i, normalize, h0, cu, want_ht, want_checkpoints, out, ht, checkpoints
+ENTRY(rec_fwd, 12)
+  const at::Tensor x = required(args[0], 2, "x");
+  const at::Tensor r = tensor(args[1]), A = tensor(args[2]), i = tensor(args[3]),
+                   h0 = tensor(args[5]), cu = tensor(args[6]);
+  Call c(x);
+  enter(guard, c);
+  const Segments s(c, cu);
+  const int32_t normalize = truth(args[4]);
+  at::Tensor y = tensor(args[9]), ht = tensor(args[10]), kept = tensor(args[11]);
+  if (!y.defined()) y = empty(x.sizes(), x);
+  if (truth(args[7]) && !ht.defined()) ht = empty32({s.n, x.size(1)}, x);
+  if (truth(args[8]) && !kept.defined())
+    kept = empty32({gdr_rec_checkpoint_rows(x.size(0)), x.size(1)}, x);
+  gdr_tensor_t *p[] = {c.add(x), c.add(r), c.add(i), c.add(A), c.add(h0), c.add(y), c.add(ht),
+                       c.add(kept)};
+  const cudaStream_t st = c.stream();
+  check(run([&] {
+          return gdr_rec_fwd(p[0], p[1], p[2], p[3], normalize, p[4], s.cu, s.n, p[5], p[6], p[7],
+                             st);
+        }),
+        "gdr_rec_fwd");
+  return tuple({y, ht, kept});
+EXIT
+
+// x, r, A, dy, i, normalize, h0, cu, dht, want_dh0, checkpoints, workspace
+ENTRY(rec_bwd, 12)
+  const at::Tensor x = required(args[0], 2, "x"), r = required(args[1], 2, "r");
+  const at::Tensor A = tensor(args[2]), dy = tensor(args[3]), i = tensor(args[4]),
+                   h0 = tensor(args[6]), cu = tensor(args[7]), dht = tensor(args[8]),
+                   kept = tensor(args[10]);
+  Call c(x);
+  enter(guard, c);
+  const Segments s(c, cu);
+  const int32_t normalize = truth(args[5]);
+  at::Tensor dx = empty(x.sizes(), x), dr = empty(r.sizes(), x), dA = empty32({x.size(1)}, x), di,
+             dh0;
+  if (i.defined()) di = empty(x.sizes(), x);
+  if (truth(args[9])) dh0 = empty32({s.n, x.size(1)}, x);
+  const Scratch ws(c, tensor(args[11]),
+                   gdr_rec_bwd_workspace_bytes(x.size(0), (int32_t)x.size(1), s.n, kept.defined()),
+                   x);
+  gdr_tensor_t *p[] = {c.add(x),  c.add(r),   c.add(i),  c.add(A),  c.add(h0), c.add(kept),
+                       c.add(dy), c.add(dht), c.add(dx), c.add(dr), c.add(di), c.add(dA),
+                       c.add(dh0)};
+  const cudaStream_t st = c.stream();
+  check(run([&] {
+          return gdr_rec_bwd(p[0], p[1], p[2], p[3], normalize, p[4], s.cu, s.n, p[5], p[6], p[7],
+                             p[8], p[9], p[10], p[11], p[12], ws.p, ws.n, st);
+        }),
+        "gdr_rec_bwd");
+  return tuple({dx, dr, dA, di, dh0});
+EXIT
+
+// x, r, A, state, i, normalize, idx, out
+ENTRY(rec_step, 8)
+  const at::Tensor x = required(args[0], 2, "x");
+  const at::Tensor r = tensor(args[1]), A = tensor(args[2]), state = tensor(args[3]),
+                   i = tensor(args[4]), idx = tensor(args[6]);
+  Call c(x);
+  enter(guard, c);
+  const int32_t normalize = truth(args[5]);
+  const int32_t *ix = c.ints(idx, x.size(0), "state_indices");
+  at::Tensor y = tensor(args[7]);
+  if (!y.defined()) y = empty(x.sizes(), x);
+  gdr_tensor_t *p[] = {c.add(x), c.add(r), c.add(i), c.add(A), c.add(state), c.add(y)};
+  const cudaStream_t st = c.stream();
+  check(run([&] {
+          return gdr_rec_step(p[0], p[1], p[2], p[3], normalize, p[4], ix, p[5], st);
+        }),
+        "gdr_rec_step");
+  return wrap(y);
+EXIT
+
+// x, z, weight, activation, eps, out
+ENTRY(gated_norm_fwd, 6)
+  const at::Tensor x = required(args[0], 3, "x");
+  const at::Tensor z = tensor(args[1]), w = tensor(args[2]);
+  Call c(x);
+  enter(guard, c);
+  const int32_t act = gate_activation(args[3]);
+  const float eps = (float)real(args[4]);
+  at::Tensor y = tensor(args[5]);
+  if (!y.defined()) y = empty(x.sizes(), x);
+  gdr_tensor_t *p[] = {c.add(x), c.add(z), c.add(w), c.add(y)};
+  const cudaStream_t st = c.stream();
+  check(run([&] { return gdr_gated_norm_fwd(p[0], p[1], p[2], act, eps, p[3], st); }),
+        "gdr_gated_norm_fwd");
+  return wrap(y);
+EXIT
+
+// x, z, dy, weight, activation, eps, workspace
+ENTRY(gated_norm_bwd, 7)
+  const at::Tensor x = required(args[0], 3, "x"), z = required(args[1], 3, "z");
+  const at::Tensor dy = tensor(args[2]), w = tensor(args[3]);
+  Call c(x);
+  enter(guard, c);
+  const int32_t act = gate_activation(args[4]);
+  const float eps = (float)real(args[5]);
+  at::Tensor dx = empty(x.sizes(), x), dz = empty(z.sizes(), x), dw;
+  if (w.defined()) dw = empty32({x.size(2)}, x);
+  const Scratch ws(c, tensor(args[6]),
+                   gdr_gated_norm_bwd_workspace_bytes(x.size(0), (int32_t)x.size(1),
+                                                      (int32_t)x.size(2)),
+                   x);
+  gdr_tensor_t *p[] = {c.add(x), c.add(z), c.add(w), c.add(dy), c.add(dx), c.add(dz), c.add(dw)};
+  const cudaStream_t st = c.stream();
+  check(run([&] {
+          return gdr_gated_norm_bwd(p[0], p[1], p[2], act, eps, p[3], p[4], p[5], p[6], ws.p, ws.n,
+                                    st);
+        }),
+        "gdr_gated_norm_bwd");
+  return tuple({dx, dz, dw});
+EXIT
+
+// x, residual, weight, post, post_weight, gate, scale, eps, out, residual_out
+ENTRY(residual_norm_fwd, 10)
+  const at::Tensor x = required(args[0], 2, "x");
+  const at::Tensor res = tensor(args[1]), w = tensor(args[2]), wp = tensor(args[4]),
+                   g = tensor(args[5]);
+  Call c(x);
+  enter(guard, c);
+  const int32_t post = truth(args[3]);
+  const float scale = (float)real(args[6]), eps = (float)real(args[7]);
+  at::Tensor y = tensor(args[8]), h = tensor(args[9]);
+  if (!y.defined()) y = empty(x.sizes(), x);
+  if (!h.defined()) h = empty(x.sizes(), res.defined() ? res : x);
+  gdr_tensor_t *p[] = {c.add(x), c.add(res), c.add(w), c.add(wp), c.add(g), c.add(y), c.add(h)};
+  const cudaStream_t st = c.stream();
+  check(run([&] {
+          return gdr_residual_norm_fwd(p[0], p[1], p[2], post, p[3], p[4], scale, eps, p[5], p[6],
+                                       st);
+        }),
+        "gdr_residual_norm_fwd");
+  return tuple({y, h});
+EXIT
+
+// x, residual, dy, dh, weight, post, post_weight, gate, scale, eps, workspace
+ENTRY(residual_norm_bwd, 11)
+  const at::Tensor x = required(args[0], 2, "x");
+  const at::Tensor res = tensor(args[1]), dy = tensor(args[2]), dh = tensor(args[3]),
+                   w = tensor(args[4]), wp = tensor(args[6]), g = tensor(args[7]);
+  Call c(x);
+  enter(guard, c);
+  const int32_t post = truth(args[5]);
+  const float scale = (float)real(args[8]), eps = (float)real(args[9]);
+  at::Tensor dx = empty(x.sizes(), x), dres, dw, dwp, dg;
+  if (res.defined()) dres = empty(x.sizes(), res);
+  if (w.defined()) dw = empty32({x.size(1)}, x);
+  if (wp.defined()) dwp = empty32({x.size(1)}, x);
+  if (g.defined()) dg = empty32({x.size(1)}, x);
+  const Scratch ws(c, tensor(args[10]),
+                   gdr_residual_norm_bwd_workspace_bytes(x.size(0), (int32_t)x.size(1)), x);
+  gdr_tensor_t *p[] = {c.add(x),  c.add(res), c.add(w),    c.add(wp), c.add(g),   c.add(dy),
+                       c.add(dh), c.add(dx),  c.add(dres), c.add(dw), c.add(dwp), c.add(dg)};
+  const cudaStream_t st = c.stream();
+  check(run([&] {
+          return gdr_residual_norm_bwd(p[0], p[1], p[2], post, p[3], p[4], scale, eps, p[5], p[6],
+                                       p[7], p[8], p[9], p[10], p[11], ws.p, ws.n, st);
+        }),
+        "gdr_residual_norm_bwd");
+  return tuple({dx, dres, dw, dwp, dg});
+EXIT
+
+// q, k_cache, v_cache, block_table, lengths, scale (None: d^-1/2), window, out, workspace
+ENTRY(attn_step, 9)
+  const at::Tensor q = required(args[0], 3, "q"), kc = required(args[1], 4, "k_cache"),
+                   table = required(args[3], 2, "block_table"),
+                   lens = required(args[4], 1, "lengths");
+  const at::Tensor vc = tensor(args[2]);
+  Call c(q);
+  enter(guard, c);
+  const float scale = args[5] == Py_None ? 1.f / std::sqrt((float)q.size(2)) : (float)real(args[5]);
+  const int32_t window = whole(args[6], "window");
+  const int32_t *ln = c.ints(lens, q.size(0), "lengths");
+  at::Tensor o = tensor(args[7]);
+  if (!o.defined()) o = empty(q.sizes(), q);
+  const Scratch ws(c, tensor(args[8]),
+                   gdr_attn_step_workspace_bytes((int32_t)q.size(0), (int32_t)q.size(1),
+                                                 (int32_t)kc.size(2), (int32_t)q.size(2)),
+                   q);
+  gdr_tensor_t *p[] = {c.add(q), c.add(kc), c.add(vc), c.table(table, "block_table"), c.add(o)};
+  const cudaStream_t st = c.stream();
+  check(run([&] {
+          return gdr_attn_step(p[0], p[1], p[2], p[3], ln, scale, window, p[4], ws.p, ws.n, st);
+        }),
+        "gdr_attn_step");
+  return wrap(o);
+EXIT
+
+// lengths, new_tokens, block_table, free_pages, taken, page_size, max_tokens, lengths_out, taken_out
+ENTRY(cache_plan, 9)
+  const at::Tensor lens = required(args[0], 1, "lengths"), fresh = required(args[1], 1, "new_tokens"),
+                   table = required(args[2], 2, "block_table"),
+                   pages = required(args[3], 1, "free_pages"), taken = required(args[4], 1, "taken");
+  Call c(lens);
+  enter(guard, c);
+  const int64_t B = lens.size(0);
+  const int32_t page = whole(args[5], "page_size"), most = whole(args[6], "max_tokens");
+  if (B > 0x7ff00000) refuse(PyExc_ValueError, "too many requests");
+  if (most < 0) refuse(PyExc_ValueError, "max_tokens must not be negative");
+  const int32_t *ln = c.ints(lens, B, "lengths"), *nw = c.ints(fresh, B, "new_tokens"),
+                *tk = c.ints(taken, 1, "taken");
+  c.ints(pages, -1, "free_pages");
+  at::Tensor lens_out = tensor(args[7]), taken_out = tensor(args[8]);
+  const auto opt = lens.options();
+  if (!lens_out.defined()) lens_out = at::empty({B}, opt);
+  if (!taken_out.defined()) taken_out = at::empty({1}, opt);
+  const int32_t *lo = c.ints(lens_out, B, "lengths_out"), *to = c.ints(taken_out, 1, "taken_out");
+  const at::Tensor slots = at::empty({most}, opt), pos = at::empty({most}, opt),
+                   cu = at::empty({B + 1}, opt);
+  gdr_tensor_t *p[] = {c.table(table, "block_table"), c.table(pages, "free_pages")};
+  const cudaStream_t st = c.stream();
+  int32_t *sp = most ? slots.data_ptr<int32_t>() : nullptr, *pp = most ? pos.data_ptr<int32_t>() : nullptr;
+  int32_t *cp = cu.data_ptr<int32_t>();
+  check(run([&] {
+          return gdr_cache_plan(ln, nw, (int32_t)B, p[0], p[1], tk, page, sp, pp, most, cp,
+                                const_cast<int32_t *>(lo), const_cast<int32_t *>(to), st);
+        }),
+        "gdr_cache_plan");
+  return tuple({slots, pos, cu, lens_out, taken_out});
+EXIT
+
+// k, v, k_cache, v_cache, slots
+ENTRY(cache_write, 5)
+  const at::Tensor k = required(args[0], 3, "k");
+  const at::Tensor v = tensor(args[1]), kc = tensor(args[2]), vc = tensor(args[3]),
+                   slots = required(args[4], 1, "slots");
+  Call c(k);
+  enter(guard, c);
+  const int32_t *sl = c.ints(slots, k.size(0), "slots");
+  gdr_tensor_t *p[] = {c.add(k), c.add(v), c.add(kc), c.add(vc)};
+  const cudaStream_t st = c.stream();
+  check(run([&] { return gdr_cache_write(p[0], p[1], p[2], p[3], sl, st); }), "gdr_cache_write");
+  Py_RETURN_NONE;
+EXIT
+
 PyObject *set_error(PyObject *, PyObject *type) {
   Py_XINCREF(type);
   Py_XDECREF(g_error);
@@ -423,6 +690,10 @@ PyObject *set_error(PyObject *, PyObject *type) {
 PyMethodDef kMethods[] = {METHOD(conv_fwd),  METHOD(conv_bwd), METHOD(conv_step),
                           METHOD(ssm_fwd),   METHOD(ssm_bwd),  METHOD(ssm_step),
                           METHOD(qk_fwd),    METHOD(qk_bwd),   METHOD(delta_step),
+                          METHOD(rec_fwd),   METHOD(rec_bwd),  METHOD(rec_step),
+                          METHOD(gated_norm_fwd),    METHOD(gated_norm_bwd),
+                          METHOD(residual_norm_fwd), METHOD(residual_norm_bwd),
+                          METHOD(attn_step), METHOD(cache_plan), METHOD(cache_write),
                           {"set_error", set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_mixer", nullptr, -1, kMethods,

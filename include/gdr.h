@@ -364,7 +364,7 @@ int gdr_chunk_out_noalloc(const gdr_tensor_t *q, const gdr_tensor_t *k,
  * - Deterministic: no atomics on results; parameter gradients are added in a fixed order.
  * - T, B and the channel count are at most 0x7ff00000.
  */
-enum gdr_activation { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 };
+enum gdr_activation { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1, GDR_ACT_SIGMOID = 2 };
 enum gdr_norm { GDR_NORM_RMS = 0, GDR_NORM_L2 = 1 };
 
 /*
@@ -494,6 +494,153 @@ int gdr_delta_step(const gdr_tensor_t *q, const gdr_tensor_t *k, const gdr_tenso
                    const gdr_tensor_t *g, const gdr_tensor_t *beta, float scale,
                    gdr_tensor_t *state, const int32_t *state_indices, gdr_tensor_t *o,
                    cudaStream_t stream);
+
+/*
+ * ---- The operators of a hybrid block beside its mixer ------------------------------------
+ *
+ * Gated linear recurrence, the norms behind and before a block with its gate and residual scale,
+ * and for attention layers between the mixers' the single-token attention over a paged key-value
+ * cache, with the cache's block tables, slots and writes.  Conventions as above.
+ */
+
+/*
+ * gdr_rec_fwd -- gated linear recurrence of each channel over the tokens of its segment:
+ *   a_t = exp(A[d] sigmoid(r_t)),  m_t = sqrt(1 - a_t^2) (normalize = 0: 1),
+ *   h_t = a_t h_{t-1} + m_t sigmoid(i_t) x_t (i NULL: no such gate),  y_t = h_t.
+ *   x, r, i, y  [T, D];  A [D] f32 compact, <= 0 (above, m is NaN)
+ *   h0, ht  [n_seq, D] f32 compact, or NULL (ht of an empty segment: h0's, or zeros)
+ *   checkpoints  [gdr_rec_checkpoint_rows(T), D] f32 compact out, or NULL: what gdr_rec_bwd would
+ *                compute again, the state before every eighth token
+ */
+int gdr_rec_fwd(const gdr_tensor_t *x, const gdr_tensor_t *r, const gdr_tensor_t *i,
+                const gdr_tensor_t *A, int32_t normalize, const gdr_tensor_t *h0,
+                const int32_t *cu_seqlens, int32_t n_seq, gdr_tensor_t *y, gdr_tensor_t *ht,
+                gdr_tensor_t *checkpoints, cudaStream_t stream);
+int64_t gdr_rec_checkpoint_rows(int64_t T);
+
+/*
+ * gdr_rec_bwd -- gradients of gdr_rec_fwd.
+ *   checkpoints  of the forward with the same inputs, or NULL: they are computed again
+ *   dy [T, D]; dht [n_seq, D] f32 or NULL;  dx, dr, di [T, D] (di iff i): out, x's type
+ *   dA [D], dh0 [n_seq, D] (or NULL): f32 compact out
+ *   workspace  256-byte aligned, >= gdr_rec_bwd_workspace_bytes(...) bytes
+ * Where a_t is 1 (A sigmoid(r) = 0) the normaliser has no derivative; its part counts as 0.
+ */
+int gdr_rec_bwd(const gdr_tensor_t *x, const gdr_tensor_t *r, const gdr_tensor_t *i,
+                const gdr_tensor_t *A, int32_t normalize, const gdr_tensor_t *h0,
+                const int32_t *cu_seqlens, int32_t n_seq, const gdr_tensor_t *checkpoints,
+                const gdr_tensor_t *dy, const gdr_tensor_t *dht, gdr_tensor_t *dx, gdr_tensor_t *dr,
+                gdr_tensor_t *di, gdr_tensor_t *dA, gdr_tensor_t *dh0, void *workspace,
+                size_t workspace_bytes, cudaStream_t stream);
+size_t gdr_rec_bwd_workspace_bytes(int64_t T, int32_t D, int32_t n_seq, int32_t has_checkpoints);
+
+/*
+ * gdr_rec_step -- one token of gdr_rec_fwd for each of the rows of x.
+ *   x, r, i, y [rows, D]; state [slots, D] f32 compact, in place
+ */
+int gdr_rec_step(const gdr_tensor_t *x, const gdr_tensor_t *r, const gdr_tensor_t *i,
+                 const gdr_tensor_t *A, int32_t normalize, gdr_tensor_t *state,
+                 const int32_t *state_indices, gdr_tensor_t *y, cudaStream_t stream);
+
+/*
+ * gdr_gated_norm_fwd -- the norm of each row (token, head) behind a mixer, times its gate:
+ *   y = x (mean x^2 + eps)^-1/2 weight f(z),  f(z) = z sigmoid(z) (GDR_ACT_SILU) or sigmoid(z)
+ *   (GDR_ACT_SIGMOID)
+ *   x, z, y [T, H, d], d = 1 .. 1024; weight [d] f32 or bf16, or NULL (ones).  y may be x or z.
+ */
+int gdr_gated_norm_fwd(const gdr_tensor_t *x, const gdr_tensor_t *z, const gdr_tensor_t *weight,
+                       int32_t activation, float eps, gdr_tensor_t *y, cudaStream_t stream);
+
+/*
+ * gdr_gated_norm_bwd -- gradients: dy -> dx, dz [T, H, d] (x's type), dweight [d] f32 (or NULL).
+ * workspace: 256-byte aligned, >= gdr_gated_norm_bwd_workspace_bytes(T, H, d) bytes.
+ */
+int gdr_gated_norm_bwd(const gdr_tensor_t *x, const gdr_tensor_t *z, const gdr_tensor_t *weight,
+                       int32_t activation, float eps, const gdr_tensor_t *dy, gdr_tensor_t *dx,
+                       gdr_tensor_t *dz, gdr_tensor_t *dweight, void *workspace,
+                       size_t workspace_bytes, cudaStream_t stream);
+size_t gdr_gated_norm_bwd_workspace_bytes(int64_t T, int32_t H, int32_t d);
+
+/*
+ * gdr_residual_norm_fwd -- between two blocks: the norm behind the first, its gate and residual
+ * scale, the residual, and the norm before the second:
+ *   u = x, or with post = 1  x (mean x^2 + eps)^-1/2 post_weight
+ *   h = residual + scale gate u,   y = h (mean h^2 + eps)^-1/2 weight
+ *   x, y [T, C], C = 1 .. 16384;  residual (NULL: zeros), h (NULL: not wanted) [T, C]: x's type, or
+ *   f32 beside x in bf16;  weight, post_weight, gate [C] f32 or bf16, or NULL (ones).
+ *   y is made of h before it is rounded.  h may be the residual, in place, and y may be x.
+ */
+int gdr_residual_norm_fwd(const gdr_tensor_t *x, const gdr_tensor_t *residual,
+                          const gdr_tensor_t *weight, int32_t post, const gdr_tensor_t *post_weight,
+                          const gdr_tensor_t *gate, float scale, float eps, gdr_tensor_t *y,
+                          gdr_tensor_t *h, cudaStream_t stream);
+
+/*
+ * gdr_residual_norm_bwd -- gradients of gdr_residual_norm_fwd (h is computed again from x and the
+ * residual).  dy, dx in x's type; dh (NULL: zeros), dresidual (or NULL) in the residual's; dweight,
+ * dpost_weight, dgate [C] f32 compact, each or NULL.
+ * workspace: 256-byte aligned, >= gdr_residual_norm_bwd_workspace_bytes(T, C) bytes.
+ */
+int gdr_residual_norm_bwd(const gdr_tensor_t *x, const gdr_tensor_t *residual,
+                          const gdr_tensor_t *weight, int32_t post, const gdr_tensor_t *post_weight,
+                          const gdr_tensor_t *gate, float scale, float eps, const gdr_tensor_t *dy,
+                          const gdr_tensor_t *dh, gdr_tensor_t *dx, gdr_tensor_t *dresidual,
+                          gdr_tensor_t *dweight, gdr_tensor_t *dpost_weight, gdr_tensor_t *dgate,
+                          void *workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t gdr_residual_norm_bwd_workspace_bytes(int64_t T, int32_t C);
+
+/*
+ * gdr_attn_step -- attention of one new token of each of B requests over a paged cache:
+ *   o[h] = sum_j p_j v_j,  p = softmax_j(scale q[h].k_j),  query head h reading key head
+ *   h / (Hq / Hk), over the keys at places max(0, n - window) .. n - 1 (window = 0: 0 .. n - 1), n =
+ *   lengths[b] (clamped to what the table holds).
+ *   q, o [B, Hq, d], k_cache, v_cache [pages, page_size, Hk, d] (any strides, innermost contiguous);
+ *   d = 1 .. 256, Hq % Hk == 0
+ *   block_table  int32 [B, width], rows of any stride: place j of request b is place j % page_size of
+ *                page block_table[b, j / page_size]; places on pages < 0 or >= pages are left out
+ *   lengths      DEVICE int32 [B], the new token's own key among them
+ * A row that sees no key gets zeros.  What the cache holds at other places is not looked at.
+ * width * page_size <= 0x7ff00000.  bf16 with 16-byte aligned cache rows and d % 8 == 0 takes the fast
+ * path.  workspace: 256-byte aligned, >= gdr_attn_step_workspace_bytes(B, Hq, Hk, d) bytes.
+ */
+int gdr_attn_step(const gdr_tensor_t *q, const gdr_tensor_t *k_cache, const gdr_tensor_t *v_cache,
+                  const gdr_tensor_t *block_table, const int32_t *lengths, float scale,
+                  int32_t window, gdr_tensor_t *o, void *workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+size_t gdr_attn_step_workspace_bytes(int32_t B, int32_t Hq, int32_t Hk, int32_t d);
+
+/*
+ * gdr_cache_plan -- pages, slots and positions of the new tokens of B requests, in their order.
+ *   lengths [B]     tokens that each request has in the cache (below 0: 0)
+ *   new_tokens [B]  tokens that it wants to add (below 0: 0)
+ *   block_table     int32 [B, width], rows of any stride, in place: the pages that request b needs
+ *                   more are written behind the ceil(lengths[b] / page_size) that it has
+ *   free_pages      int32 [F]: page numbers; those from *taken on are handed out in order
+ *   taken, taken_out   one int32 each: how many of free_pages are handed out, before and after
+ *   slots, positions   int32 [max_tokens] out, of the new tokens packed request by request: page *
+ *                   page_size + place (-1 on a page < 0) and the token's place in its request; behind
+ *                   the last token -1 and 0
+ *   cu_seqlens      int32 [B + 1] out: where each request's new tokens lie in them
+ *   lengths_out     int32 [B] out: lengths with the new tokens
+ * A request is given fewer tokens than it wants where its row of the table ends, where max_tokens
+ * are reached by the requests before it and its own, or where free_pages end; cu_seqlens and
+ * lengths_out say how many it was given.  All arrays are DEVICE arrays, compact but for the table;
+ * lengths_out may be lengths, and taken_out taken; a call that reads the same values again writes the
+ * same ones.  width * page_size <= 0x7ff00000.
+ */
+int gdr_cache_plan(const int32_t *lengths, const int32_t *new_tokens, int32_t B,
+                   gdr_tensor_t *block_table, const gdr_tensor_t *free_pages, const int32_t *taken,
+                   int32_t page_size, int32_t *slots, int32_t *positions, int32_t max_tokens,
+                   int32_t *cu_seqlens, int32_t *lengths_out, int32_t *taken_out,
+                   cudaStream_t stream);
+
+/*
+ * gdr_cache_write -- rows of k and v [T, Hk, d] into k_cache and v_cache [pages, page_size, Hk, d] at
+ * slots (DEVICE int32 [T], page * page_size + place); a slot outside the cache: a row that is not
+ * written.  A slot named by two rows is written by both, in no fixed order.
+ */
+int gdr_cache_write(const gdr_tensor_t *k, const gdr_tensor_t *v, gdr_tensor_t *k_cache,
+                    gdr_tensor_t *v_cache, const int32_t *slots, cudaStream_t stream);
 
 /* Human-readable text for a gdr_status code (static storage). */
 const char *gdr_status_string(int status);
