@@ -4,6 +4,7 @@
 #include <mutex>
 #include <string.h>
 
+#include "gdr_block.cuh"
 #include "gdr_bwd.cuh"
 #include "gdr_desc.cuh"
 #include "gdr_internal.cuh"
@@ -644,7 +645,9 @@ int gdr_debug_check_cu_seqlens(const int32_t *cu_seqlens, int32_t n_seq, int64_t
 
 int gdr_device_status(int32_t *status_out) {
   if (!status_out) return GDR_ERR_NULL;
-  return read_device_status(status_out) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+  if (read_device_status(status_out) != cudaSuccess) return GDR_ERR_CUDA;
+  if (*status_out == 0 && read_rec_status(status_out) != cudaSuccess) return GDR_ERR_CUDA;
+  return GDR_OK;
 }
 
 int gdr_debug_wait_selftest(uint32_t limit_us, cudaStream_t stream) {
@@ -657,7 +660,8 @@ int gdr_debug_wait_selftest(uint32_t limit_us, cudaStream_t stream) {
 }
 
 int gdr_clear_device_status(void) {
-  return clear_device_status() == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+  return clear_device_status() == cudaSuccess && clear_rec_status() == cudaSuccess ? GDR_OK
+                                                                                   : GDR_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -42,6 +42,9 @@ struct RecArgs {
 };
 constexpr int kRecEvery = 8;
 cudaError_t launch_rec_fwd(const RecArgs &a, cudaStream_t stream);
+// the status word of the recurrence's waits (0: none ran out)
+cudaError_t read_rec_status(int32_t *out);
+cudaError_t clear_rec_status();
 size_t rec_bwd_workspace(int64_t T, int32_t D, int32_t n_seq, bool kept);
 cudaError_t launch_rec_bwd(const RecArgs &a, bool kept, cudaStream_t stream);
 // rows of x, r, i, y are T requests; state [slots, D] in place

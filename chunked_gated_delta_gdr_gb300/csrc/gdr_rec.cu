@@ -17,13 +17,18 @@
 #include <initializer_list>
 
 #include "gdr_block.cuh"
+#include "gdr_tc.cuh"
 
 namespace gdr {
 namespace mix {
 namespace {
 
+// Nonzero once a wait for another block of a cluster ran out; read by gdr_device_status.
+__device__ int32_t g_rec_status = 0;
+constexpr uint64_t kRecWaitNs = 2000000000ull;  // 2 s a wait
+
 constexpr int kCh = 64;      // channels of a block: two a lane
-constexpr int kMostCl = 16;  // blocks of a cluster
+constexpr int kMostCl = 16;  // blocks of a cluster (over 8 with the device's consent)
 
 // ------------------------------------------------------------------ two neighbouring channels
 
@@ -89,35 +94,63 @@ __device__ __forceinline__ void st2(float *p, float lo, float hi, int nv) {
 
 // ------------------------------------------------------------------ one token of one channel
 
-// 1 - a^2 from L2 = log2 a: next to a = 1 by the series of 1 - e^y, y = 2 log a (the last term left
-// out is 5e-8 of it at the border), which keeps its relative accuracy there; else as it is written.
-__device__ __forceinline__ float rest_of(float L2, float a) {
-  const float y = L2 * 1.3862943611198906f;
-  float p = fmaf(y, 1.f / 720.f, 1.f / 120.f);
-  p = fmaf(p, y, 1.f / 24.f);
-  p = fmaf(p, y, 1.f / 6.f);
-  p = fmaf(p, y, 0.5f);
-  p = fmaf(p, y, 1.f);
-  return y > -0.25f ? -y * p : fmaf(-a, a, 1.f);
-}
-__device__ __forceinline__ float rsqrt_approx(float x) {
+__device__ __forceinline__ f2 both(float v) { return pair(v, v); }
+// sqrt(x) on the special-function unit (2^-23; NaN below 0)
+__device__ __forceinline__ float sqrt_approx(float x) {
   float y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// sqrt(s), 0 for 0 (the smallest normal number is far below what s can be); NaN for s < 0: A > 0
-__device__ __forceinline__ float root_of(float s) { return s * rsqrt_approx(s + 1.1754944e-38f); }
+template <typename E>
+__device__ __forceinline__ f2 wide(const Raw2<E> &r) {
+  return pair(r.lo(), r.hi());
+}
+
+// sqrt(1 - a^2) from L2 = log2 a: next to a = 1 by the series of 1 - 2^(2 L2) (the first term left out is
+// 4e-8 of it at the border, 2 ln a = -1/8), which keeps its relative accuracy there; else as it is
+// written.  NaN for a > 1 (A > 0).
+__device__ __forceinline__ f2 root_of(f2 L2, f2 a) {
+  f2 p = fma2(L2, both(-0.042667211f), both(-0.15389006f));
+  p = fma2(p, L2, both(-0.44403294f));
+  p = fma2(p, L2, both(-0.96090603f));
+  p = fma2(p, L2, both(-1.3862944f));
+  float lo, hi, l0, l1, a0, a1;
+  unpair(mul2(p, L2), lo, hi);
+  unpair(L2, l0, l1);
+  unpair(a, a0, a1);
+  return pair(sqrt_approx(l0 > -0.0901684f ? lo : fmaf(-a0, a0, 1.f)),
+              sqrt_approx(l1 > -0.0901684f ? hi : fmaf(-a1, a1, 1.f)));
+}
 
 struct Token {
-  float sr, a, m;
+  f2 sr, a, m;
 };
-__device__ __forceinline__ Token token(float r, float A2, int normalize) {
+// A2: A log2 e; sr: sigmoid(r)
+template <bool NORM>
+__device__ __forceinline__ Token token(f2 sr, f2 A2) {
   Token t;
-  t.sr = sigmoidf(r);
-  const float L2 = A2 * t.sr;
-  t.a = ex2(L2);
-  t.m = normalize ? root_of(rest_of(L2, t.a)) : 1.f;
+  t.sr = sr;
+  const f2 L2 = mul2(A2, sr);
+  float lo, hi;
+  unpair(L2, lo, hi);
+  t.a = pair(ex2(lo), ex2(hi));
+  t.m = NORM ? root_of(L2, t.a) : both(1.f);
   return t;
+}
+// Two sigmoids for one reciprocal, which is twice an exponential's time: 1 / (1 + e) (1 + f) times the other
+// factor.  q: the reciprocals; 0 where the product overflowed (both far below 0), and the two have to be
+// computed on their own.
+__device__ __forceinline__ void sigmoids(f2 r, f2 i, f2 &sr, f2 &si, float &q) {
+  float a, b, c, d;
+  unpair(mul2(r, both(-kLog2e)), a, b);
+  unpair(mul2(i, both(-kLog2e)), c, d);
+  const f2 e = add2(pair(ex2(a), ex2(b)), both(1.f)), f = add2(pair(ex2(c), ex2(d)), both(1.f));
+  unpair(mul2(e, f), a, b);
+  a = rcp(a);
+  b = rcp(b);
+  q = fminf(a, b);
+  sr = mul2(pair(a, b), f);
+  si = mul2(pair(a, b), e);
 }
 
 // ------------------------------------------------------------------ pairs (A, U): h -> A h + U
@@ -126,13 +159,36 @@ __device__ __forceinline__ Token token(float r, float A2, int normalize) {
 // infinite or NaN.  (A product of decays that underflows to 0 says the same of a state that is gone.)
 
 struct Map {
-  float A, U;
+  f2 A, U;
 };
-__device__ __forceinline__ float through(Map f, float h) { return f.A == 0.f ? f.U : fmaf(f.A, h, f.U); }
+__device__ __forceinline__ f2 pick(bool lo, bool hi, f2 yes, f2 no) {
+  float a, b, c, d;
+  unpair(yes, a, b);
+  unpair(no, c, d);
+  return pair(lo ? a : c, hi ? b : d);
+}
+__device__ __forceinline__ f2 through(Map f, f2 h) {
+  float lo, hi;
+  unpair(f.A, lo, hi);
+  return pick(lo == 0.f, hi == 0.f, f.U, fma2(f.A, h, f.U));
+}
 // first f, then g
 __device__ __forceinline__ Map then(Map f, Map g) {
-  return Map{g.A == 0.f ? 0.f : f.A * g.A, through(g, f.U)};
+  float lo, hi;
+  unpair(g.A, lo, hi);
+  return Map{pick(lo == 0.f, hi == 0.f, both(0.f), mul2(f.A, g.A)), through(g, f.U)};
 }
+// the same where neither holds a segment's start
+__device__ __forceinline__ Map then_inside(Map f, Map g) {
+  return Map{mul2(f.A, g.A), fma2(g.A, f.U, g.U)};
+}
+__device__ __forceinline__ float4 packed(Map f) {
+  float4 v;
+  unpair(f.A, v.x, v.y);
+  unpair(f.U, v.z, v.w);
+  return v;
+}
+__device__ __forceinline__ Map unpacked(float4 v) { return Map{pair(v.x, v.y), pair(v.z, v.w)}; }
 
 // ------------------------------------------------------------------ the cluster
 
@@ -152,18 +208,34 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-// *p of the block of this rank = v
+// No block ends while another may write to it.
+__device__ __forceinline__ void cluster_leave() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  cluster_wait();
+}
+__device__ __forceinline__ uint32_t at_rank(const void *p, int rank) {
+  uint32_t to;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(tc::smem_u32(p)), "r"(rank));
+  return to;
+}
+// *p of the block of this rank = v, before the next barrier of the cluster
 __device__ __forceinline__ void put(float4 *p, int rank, float4 v) {
-  uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p)), to;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(rank));
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.x), "f"(v.y),
-               "f"(v.z), "f"(v.w)
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at_rank(p, rank)), "f"(v.x),
+               "f"(v.y), "f"(v.z), "f"(v.w)
                : "memory");
+}
+// the same, counted as 16 bytes by that block's *bar
+__device__ __forceinline__ void send(float4 *p, uint64_t *bar, int rank, float4 v) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+          at_rank(p, rank)),
+      "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(at_rank(bar, rank))
+      : "memory");
 }
 
 template <typename... P, typename... A>
 cudaError_t launch_clusters(void (*kernel)(P...), int blocks, int cluster, int threads,
-                            cudaStream_t stream, A... args) {
+                            int smem, cudaStream_t stream, A... args) {
   cudaLaunchAttribute at[2] = {};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -173,17 +245,10 @@ cudaError_t launch_clusters(void (*kernel)(P...), int blocks, int cluster, int t
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)blocks);
   c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = (size_t)smem;
   c.stream = stream;
   c.attrs = at;
   c.numAttrs = 2;
-  if (cluster > 8) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return e;
-    }
-  }
   const cudaError_t e = cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
   if (e != cudaSuccess) cudaGetLastError();
   return e;
@@ -261,19 +326,108 @@ __device__ __forceinline__ bool tile_marks_back(const int32_t *bounds, int t0, i
   return any;
 }
 
-// ------------------------------------------------------------------ forward
+// ------------------------------------------------------------------ a warp's tokens
 
-constexpr int kFwdP = 4, kFwdK = 16;  // warps of a block, tokens of a thread
-constexpr int kBwdP = 4, kBwdK = kRecEvery;
+constexpr int kP = 8, kK = 8, kTile = kP * kK;  // warps of a block, tokens of a thread, of a block
+constexpr int kLook = kP / 2;  // the warp that looks up bounds: neither the first nor the last in order
+static_assert(kRecEvery == kK, "a kept state for each thread's tokens");
 
-template <int P, int K>
 struct Shared {
-  float4 warp[P][32];          // (A, U) of both channels, for each warp of the block
+  float4 warp[kP][32];           // (A, U) of both channels, for each warp of the block
   float4 block[2][kMostCl][32];  // and for each block of the cluster, by the step's parity
-  int mark[2][P * K + 1];
+  f2 front[kP][32];              // the state in front of each warp's tokens
+  uint64_t bar[2];               // every block's map is here
+  int mark[2][kTile + 1];
   int any[2], alive[2];
   int red[64];
+  __device__ __forceinline__ void init() {
+    if (threadIdx.x == 0) {
+      tc::mbar_init(&bar[0], 1);
+      tc::mbar_init(&bar[1], 1);
+      tc::fence_mbar_init();
+    }
+  }
 };
+
+// The N tensors of a step on their way into shared memory: a warp's rows of 64 channels come 16 bytes
+// at a time into one of two places of its own, a step ahead, and are read two channels a lane.
+// Without 16-byte alignment (RING false) they are loaded when they are used.
+template <typename E, bool RING, int N>
+struct Tokens {
+  static constexpr int kRow = kCh * (int)sizeof(E);          // bytes
+  static constexpr int kPlace = N * kK * kRow;               // of a warp's step
+  static constexpr int kBytes = RING ? 2 * kP * kPlace : 0;  // of a block
+  const E *p[N];  // at this block's first channel; null: not there
+  int64_t st[N];
+  unsigned char *mine;  // this warp's places
+  int lane, cols, nv, T;
+  const E *from[N];  // the lane's part of the next step's first rows
+
+  // rows from token t on are the first to come, then those `step` tokens on each time
+  __device__ __forceinline__ void start(int t) {
+    if (RING) {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        from[n] = p[n] + (int64_t)(t + lane / kL) * st[n] + lane % kL * (16 / (int)sizeof(E));
+    }
+  }
+  static constexpr int kL = kRow / 16, kR = 32 / kL;  // lanes of a row, rows of an instruction
+  __device__ __forceinline__ void issue(int place, int t, int step) {
+    if (RING) {
+      __syncwarp();  // the place was read by all lanes
+      const int left = lane % kL * (16 / (int)sizeof(E)) < cols ? T - t - lane / kL : 0;
+      unsigned char *to = mine + place * kPlace + lane * 16;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if (n == 2 && !p[n]) continue;
+        const E *q = from[n];
+#pragma unroll
+        for (int k = 0; k < kK; k += kR) {
+          if (k < left) copy16(reinterpret_cast<uint4 *>(to + (n * kK + k) * kRow), q);
+          q += kR * st[n];
+        }
+        from[n] += step * st[n];
+      }
+      copies_commit();
+    }
+  }
+  __device__ __forceinline__ void wait() const {
+    if (RING) {
+      copies_wait<1>();
+      __syncwarp();
+    }
+  }
+  // the lane's two channels of token t = t0 + k
+  __device__ __forceinline__ f2 get(int place, int n, int k, int t) const {
+    if (RING)
+      return wide(*reinterpret_cast<const Raw2<E> *>(mine + place * kPlace + (n * kK + k) * kRow +
+                                                     lane * 2 * (int)sizeof(E)));
+    return wide(ld2<false>(p[n] + (int64_t)t * st[n] + lane * 2, t < T ? nv : 0));
+  }
+  // The lane's two channels of a result's row, and then all rows from token t on to p: through the
+  // place of tensor n, which has been read, 16 bytes a lane.
+  __device__ __forceinline__ void stage(int place, int n, int k, f2 v) const {
+    float lo, hi;
+    unpair(v, lo, hi);
+    st2<true>(reinterpret_cast<E *>(mine + place * kPlace + (n * kK + k) * kRow) + lane * 2, lo, hi, 2);
+  }
+  __device__ __forceinline__ void flush(int place, int n, E *to, int64_t to_st, int t) const {
+    constexpr int L = kL, R = kR;
+    const int c = lane % L, row = lane / L;
+    const unsigned char *from = mine + place * kPlace + n * kK * kRow + row * kRow + c * 16;
+    to += (int64_t)(t + row) * to_st + c * (16 / (int)sizeof(E));
+    if (c * (16 / (int)sizeof(E)) < cols) {
+#pragma unroll
+      for (int k = 0; k < kK; k += R)
+        if (t + row + k < T)
+          *reinterpret_cast<uint4 *>(to + k * to_st) = *reinterpret_cast<const uint4 *>(from + k * kRow);
+    }
+  }
+};
+
+__device__ __forceinline__ int uniform_warp() {
+  return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+}
 
 // The segment of a warp's first token, from the marks of its tile: the highest index up to it.
 __device__ __forceinline__ int segment_at(const int *mark, int i, int alive) {
@@ -282,189 +436,326 @@ __device__ __forceinline__ int segment_at(const int *mark, int i, int alive) {
   return __reduce_max_sync(0xffffffffu, m);
 }
 
-// What the threads of a cluster exchange in a step: returns the state in front of this thread's
-// tokens (of two channels) and moves `carry` past the step.  f() runs where the block's last step is
-// done with, and what it writes is seen after the exchange.  BACK: warps and blocks in reverse.
-template <int P, int K, bool BACK, typename F>
-__device__ __forceinline__ void exchange(Shared<P, K> &s, int buf, const Map (&mine)[2],
-                                         float (&carry)[2], float (&front)[2], F f) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = cluster_rank(), size = cluster_size();
-  s.warp[warp][lane] = make_float4(mine[0].A, mine[0].U, mine[1].A, mine[1].U);
+// What the threads of a cluster exchange in step `turn`: returns the state in front of this thread's
+// tokens and moves `carry`, which the first warp has, past the step.  any: a segment may start in the
+// block's tokens.  f() runs in warp kLook where the block's last step is done with, and what it writes
+// is seen after the exchange.  BACK: warps and blocks in reverse.
+//
+// One warp chains the block's maps, for all of them would take most of the issue slots.  The block's map goes to all blocks as counted stores, so that nobody waits for this block's other
+// writes as at a cluster's barrier.  A place is written again two steps later: by a block that has seen
+// all maps of the step between, whose senders had read theirs of this one.
+template <bool BACK, typename F>
+__device__ __forceinline__ f2 exchange(Shared &s, int turn, int warp, bool any, Map mine, f2 &carry,
+                                       F f) {
+  const int lane = threadIdx.x & 31, buf = turn & 1;
+  s.warp[warp][lane] = packed(mine);
   __syncthreads();
-  f();
-  Map all[2] = {{1.f, 0.f}, {1.f, 0.f}}, pre[2] = {{1.f, 0.f}, {1.f, 0.f}};
+  if (warp == kLook) f();
+  if (warp == 0) {
+    const int rank = cluster_rank(), size = cluster_size();
+    Map all = unpacked(s.warp[BACK ? kP - 1 : 0][lane]);
+    if (any) {
+#pragma unroll 1
+      for (int j = 1; j < kP; ++j) all = then(all, unpacked(s.warp[BACK ? kP - 1 - j : j][lane]));
+    } else {
 #pragma unroll
-  for (int j = 0; j < P; ++j) {
-    const int w = BACK ? P - 1 - j : j;
-    if (w == warp) {
-      pre[0] = all[0];
-      pre[1] = all[1];
+      for (int j = 1; j < kP; ++j)
+        all = then_inside(all, unpacked(s.warp[BACK ? kP - 1 - j : j][lane]));
     }
-    const float4 v = s.warp[w][lane];
-    all[0] = then(all[0], Map{v.x, v.y});
-    all[1] = then(all[1], Map{v.z, v.w});
-  }
-  const float4 out = make_float4(all[0].A, all[0].U, all[1].A, all[1].U);
-  for (int to = warp; to < size; to += P) put(&s.block[buf][rank][lane], to, out);
-  cluster_arrive();
-  cluster_wait();
-  float h[2] = {carry[0], carry[1]};
-  for (int j = 0; j < size; ++j) {
-    const int b = BACK ? size - 1 - j : j;
-    if (b == rank) {
-      front[0] = h[0];
-      front[1] = h[1];
+    const float4 out = packed(all);
+#pragma unroll 2
+    for (int to = 0; to < size; ++to) send(&s.block[buf][rank][lane], &s.bar[buf], to, out);
+    if (lane == 0) tc::mbar_expect_tx(&s.bar[buf], size * 512);
+    __syncwarp();
+    if (!tc::mbar_wait(&s.bar[buf], turn >> 1 & 1, nullptr, kRecWaitNs))
+      atomicCAS(&g_rec_status, 0, BACK ? 0x602 : 0x601);  // the results are void; go on to the end
+    f2 h = carry, front = carry;
+#pragma unroll 4
+    for (int j = 0; j < size; ++j) {
+      const int b = BACK ? size - 1 - j : j;
+      const Map v = unpacked(s.block[buf][b][lane]);
+      if (b == rank) front = h;
+      h = through(v, h);
     }
-    const float4 v = s.block[buf][b][lane];
-    h[0] = through(Map{v.x, v.y}, h[0]);
-    h[1] = through(Map{v.z, v.w}, h[1]);
+    carry = h;
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      const int w = BACK ? kP - 1 - j : j;
+      s.front[w][lane] = front;
+      if (j < kP - 1) front = through(unpacked(s.warp[w][lane]), front);
+    }
   }
-  carry[0] = h[0];
-  carry[1] = h[1];
-  front[0] = through(pre[0], front[0]);
-  front[1] = through(pre[1], front[1]);
+  __syncthreads();
+  return s.front[warp][lane];
 }
 
-// OUT: y is written (without it only the kept states: the backward's first pass).
-template <typename E, bool VEC, bool OUT>
-__global__ void __launch_bounds__(kFwdP * 32, 4) k_rec_fwd(const RecArgs a) {
-  after_previous();
-  constexpr int P = kFwdP, K = kFwdK, N = P * K;
-  __shared__ Shared<P, K> s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = cluster_rank(), size = cluster_size();
-  const int c0 = (int)(blockIdx.x / size) * kCh + lane * 2, nv = max(0, min(2, a.D - c0));
-  const float A2[2] = {nv > 0 ? a.A[c0] * kLog2e : 0.f, nv > 1 ? a.A[c0 + 1] * kLog2e : 0.f};
-  const E *x = reinterpret_cast<const E *>(a.x.p) + c0, *r = reinterpret_cast<const E *>(a.r.p) + c0;
-  const E *ig = a.i.p ? reinterpret_cast<const E *>(a.i.p) + c0 : nullptr;
-  E *y = reinterpret_cast<E *>(a.y.p) + c0;
-  SegCursor cursor{0, 0, 0};
-  auto look = [&](int buf, int t0) {  // warp 0: the bounds of a tile
-    int alive = -1;
-    const bool any = t0 < a.T && tile_marks(a.cu, a.n_seq, a.T, t0, min(N, a.T - t0), s.mark[buf],
-                                            cursor, alive);
-    if (lane == 0) {
-      s.any[buf] = any;
-      s.alive[buf] = alive;
-    }
-  };
-  if (warp == 0) look(0, rank * N);
-  cluster_arrive();  // every block of the cluster runs before one writes to it
-  cluster_wait();
-  float carry[2] = {0.f, 0.f};
-  int buf = 0;
-  for (int base = 0; base < a.T; base += size * N, buf ^= 1) {
-    const int t0 = base + rank * N, tw = t0 + warp * K, left = a.T - tw;
-    float at[K][2], u[K][2];
-    {
-      Raw2<E> xr[K], rr[K], ir[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int64_t t = tw + k;
-        const int n = k < left ? nv : 0;
-        xr[k] = ld2<VEC>(x + t * a.x.st, n);
-        rr[k] = ld2<VEC>(r + t * a.r.st, n);
-        if (ig) ir[k] = ld2<VEC>(ig + t * a.i.st, n);
-      }
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const float xs[2] = {xr[k].lo(), xr[k].hi()}, rs[2] = {rr[k].lo(), rr[k].hi()};
-        float is[2] = {1.f, 1.f};
-        if (ig) {
-          is[0] = sigmoidf(ir[k].lo());
-          is[1] = sigmoidf(ir[k].hi());
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const Token v = token(rs[c], A2[c], a.normalize);
-          at[k][c] = k < left ? v.a : 1.f;
-          u[k][c] = k < left ? v.m * is[c] * xs[c] : 0.f;
-        }
-      }
-    }
-    // segments that start among this warp's tokens: their state goes into the first token
-    const bool any = s.any[buf];
-    int seg = s.alive[buf];
-    uint32_t starts = 0;
-    if (any) {
-      const int *mark = s.mark[buf];
-      seg = left > 0 ? segment_at(mark, warp * K, seg) : seg;
+// nv of two fp32 values at any address
+__device__ __forceinline__ f2 load_state(const float *p, int nv) {
+  return pair(nv > 0 ? p[0] : 0.f, nv > 1 ? p[1] : 0.f);
+}
+__device__ __forceinline__ void store_state(float *p, f2 v, int nv) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  if (nv > 0) p[0] = lo;
+  if (nv > 1) p[1] = hi;
+}
+template <bool VEC, typename E>
+__device__ __forceinline__ void store(E *p, f2 v, int nv) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  st2<VEC>(p, lo, hi, nv);
+}
+
+// ------------------------------------------------------------------ forward
+//
+// Of a block's eight warps seven hold tokens and one chains their maps.  The holders compute step s + 1
+// while the chain of step s is on its way through the cluster, and then run through step s: nobody
+// waits for a map that was sent just now.  Shared places are written again when a later meeting has
+// shown that they were read: maps and states two steps on, bounds (looked up two steps ahead) four.
+
+constexpr int kHold = kP - 1, kFwdTile = kHold * kK;  // warps with tokens, and a block's tokens
+
+struct FwdShared {
+  float4 warp[2][kHold][32];     // (A, U) of both channels, for each warp with tokens
+  float4 block[2][kMostCl][32];  // and for each block of the cluster
+  f2 front[2][kHold][32];        // the state in front of each warp's tokens
+  uint64_t bar[2];               // every block's map is here
+  int mark[4][kFwdTile + 1];
+  int any[4], alive[4];
+  int red[64];
+};
+
+// Meetings of holders and chain, two of each kind in turn.
+__device__ __forceinline__ void arrive(int id) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(kP * 32) : "memory");
+}
+__device__ __forceinline__ void meet(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(kP * 32) : "memory");
+}
+constexpr int kMaps = 1, kFronts = 3;
+
+// The chain warp's work in step s, once the holders' maps are there: the block's map to all blocks, and
+// from theirs the state in front of each warp.  The block's map goes out as counted stores, so that
+// nobody waits for this block's other writes as at a cluster's barrier.  A place is written again two
+// steps later: by a block that has seen all maps of the step between, whose senders had read this one's.
+template <int HOLD, typename S>
+__device__ __forceinline__ void chain(S &s, int step, bool any, f2 &carry) {
+  const int lane = threadIdx.x & 31, buf = step & 1, rank = cluster_rank(), size = cluster_size();
+  Map all = unpacked(s.warp[buf][0][lane]);
+  if (any) {
 #pragma unroll 1
-      for (int k = 0; k < K; ++k)
-        if (k < left && mark[warp * K + k] >= 0) starts |= 1u << k;
-      if (starts && a.h0) {
+    for (int j = 1; j < HOLD; ++j) all = then(all, unpacked(s.warp[buf][j][lane]));
+  } else {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-          if (starts >> k & 1) {
-            const int n = mark[warp * K + k];
-            if (n < a.n_seq) {
-              const float *q = a.h0 + (int64_t)n * a.D + c0;
-              if (nv > 0) u[k][0] = fmaf(at[k][0], q[0], u[k][0]);
-              if (nv > 1) u[k][1] = fmaf(at[k][1], q[1], u[k][1]);
-            }
-          }
-      }
-    }
-    Map mine[2] = {{1.f, 0.f}, {1.f, 0.f}};
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const bool first = starts >> k & 1;
-        mine[c].U = first ? u[k][c] : fmaf(at[k][c], mine[c].U, u[k][c]);
-        mine[c].A = first ? 0.f : mine[c].A * at[k][c];
-      }
-    float h[2];
-    exchange<P, K, false>(s, buf, mine, carry, h, [&] {
-      if (warp == 0) look(buf ^ 1, t0 + size * N);
-    });
-    if (left <= 0) continue;
-    if (!any && left >= K) {
-      const bool in = seg >= 0 && seg < a.n_seq;
-      const int n = in ? nv : 0;
-      E *to = y + (int64_t)tw * a.y.st;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (a.kept && k % kRecEvery == 0) {
-          float *q = a.kept + (int64_t)((tw + k) / kRecEvery) * a.D + c0;
-          st2<VEC>(q, h[0], h[1], nv);
-        }
-        h[0] = fmaf(at[k][0], h[0], u[k][0]);
-        h[1] = fmaf(at[k][1], h[1], u[k][1]);
-        if (OUT) st2<VEC>(to, h[0], h[1], n);
-        to += a.y.st;
-      }
-    } else {
-      const int *mark = s.mark[buf] + warp * K;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (k >= left) break;
-        if (a.kept && k % kRecEvery == 0) {
-          float *q = a.kept + (int64_t)((tw + k) / kRecEvery) * a.D + c0;
-          st2<VEC>(q, h[0], h[1], nv);
-        }
-        const bool first = starts >> k & 1;
-        if (first) seg = mark[k];
-        h[0] = first ? u[k][0] : fmaf(at[k][0], h[0], u[k][0]);
-        h[1] = first ? u[k][1] : fmaf(at[k][1], h[1], u[k][1]);
-        if (seg >= 0 && seg < a.n_seq) {
-          if (OUT) st2<VEC>(y + (int64_t)(tw + k) * a.y.st, h[0], h[1], nv);
-          if (a.ht && any && mark[k + 1] >= 0) {
-            float *q = a.ht + (int64_t)seg * a.D + c0;
-            if (nv > 0) q[0] = h[0];
-            if (nv > 1) q[1] = h[1];
-          }
-        }
-      }
-    }
+    for (int j = 1; j < HOLD; ++j) all = then_inside(all, unpacked(s.warp[buf][j][lane]));
   }
+  const float4 out = packed(all);
+#pragma unroll 2
+  for (int to = 0; to < size; ++to) send(&s.block[buf][rank][lane], &s.bar[buf], to, out);
+  if (lane == 0) tc::mbar_expect_tx(&s.bar[buf], size * 512);
+  __syncwarp();
+  if (!tc::mbar_wait(&s.bar[buf], step >> 1 & 1, nullptr, kRecWaitNs))
+    atomicCAS(&g_rec_status, 0, 0x601);  // the results are void; go on to the end
+  f2 h = carry, front = carry;
+#pragma unroll 4
+  for (int j = 0; j < size; ++j) {
+    const Map v = unpacked(s.block[buf][j][lane]);
+    if (j == rank) front = h;
+    h = through(v, h);
+  }
+  carry = h;
+#pragma unroll
+  for (int j = 0; j < HOLD; ++j) {
+    s.front[buf][j][lane] = front;
+    if (j < HOLD - 1) front = through(unpacked(s.warp[buf][j][lane]), front);
+  }
+}
+
+// A warp's tokens of a step: decays and inputs, and what starts among them.
+struct Step {
+  f2 at[kK], u[kK];
+  uint32_t starts;  // bit k: a segment starts with token k
+};
+
+// OUT: y is written (without it only the kept states: the backward's first pass).
+template <typename E, bool VEC, bool OUT, bool NORM>
+__global__ void __launch_bounds__(kP * 32, 2) k_rec_fwd(const RecArgs a) {
+  after_previous();
+  extern __shared__ __align__(16) unsigned char raw[];
+  __shared__ FwdShared s;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
+  const int rank = cluster_rank(), size = cluster_size();
+  const int cb = (int)(blockIdx.x / size) * kCh, c0 = cb + lane * 2, nv = max(0, min(2, a.D - c0));
+  const int stride = size * kFwdTile, steps = (a.T + stride - 1) / stride;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&s.bar[0], 1);
+    tc::mbar_init(&s.bar[1], 1);
+    tc::fence_mbar_init();
+  }
+  if (warp == kHold) {
+    SegCursor cursor{0, 0, 0};
+    auto look = [&](int step) {  // the bounds of a tile
+      const int buf = step & 3;
+      const int64_t t0 = (int64_t)step * stride + rank * kFwdTile;
+      int alive = -1;
+      const bool any = t0 < a.T && tile_marks(a.cu, a.n_seq, a.T, (int)t0, min(kFwdTile, a.T - (int)t0),
+                                              s.mark[buf], cursor, alive);
+      if (lane == 0) {
+        s.any[buf] = any;
+        s.alive[buf] = alive;
+      }
+      return any;
+    };
+    bool any0 = look(0), any1 = look(1);
+    cluster_arrive();  // every block of the cluster runs before one writes to it
+    cluster_wait();
+    f2 carry = both(0.f);
+    for (int step = 0; step < steps; ++step) {
+      meet(kMaps + (step & 1));
+      const bool any2 = look(step + 2);
+      chain<kHold>(s, step, any0, carry);
+      any0 = any1;
+      any1 = any2;
+      __syncwarp();
+      arrive(kFronts + (step & 1));
+    }
+  } else {
+    const f2 A2 = mul2(load_state(a.A + c0, nv), both(kLog2e));
+    using In = Tokens<E, VEC, 3>;
+    In in{{reinterpret_cast<const E *>(a.x.p) + cb, reinterpret_cast<const E *>(a.r.p) + cb,
+           a.i.p ? reinterpret_cast<const E *>(a.i.p) + cb : nullptr},
+          {a.x.st, a.r.st, a.i.st},
+          raw + warp * 2 * In::kPlace, lane, a.D - cb, nv, a.T};
+    const bool gate = a.i.p;
+    E *y = reinterpret_cast<E *>(a.y.p) + c0;
+    const int first = rank * kFwdTile + warp * kK;
+    in.start(first);
+    in.issue(0, first, stride);
+    in.issue(1, first + stride, stride);
+    cluster_arrive();
+    cluster_wait();
+
+    auto hold = [&](int step, Step &v) {  // the step's tokens, and their map for the chain
+      const int place = step & 1, tw = first + step * stride, left = a.T - tw;
+      in.wait();
+      auto make = [&](int k, f2 sr, f2 x) {
+        const Token t = token<NORM>(sr, A2);
+        v.at[k] = t.a;
+        v.u[k] = NORM ? mul2(t.m, x) : x;
+      };
+      bool alone = !gate;
+      if (gate) {
+        float q = 1.f;
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          f2 sr, si;
+          float p;
+          sigmoids(in.get(place, 1, k, tw + k), in.get(place, 2, k, tw + k), sr, si, p);
+          q = fminf(q, p);
+          make(k, sr, mul2(si, in.get(place, 0, k, tw + k)));
+        }
+        alone = __any_sync(0xffffffffu, q == 0.f);
+      }
+      if (alone) {
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          f2 x = in.get(place, 0, k, tw + k);
+          if (gate) x = mul2(x, sigmoid2(in.get(place, 2, k, tw + k)));
+          make(k, sigmoid2(in.get(place, 1, k, tw + k)), x);
+        }
+      }
+      // segments that start among the tokens: their state goes into the first one
+      const bool any = s.any[step & 3];
+      v.starts = 0;
+      if (any || left < kK) {
+        const int *mark = s.mark[step & 3] + warp * kK;
+        if (any && left > 0) {
+#pragma unroll 1
+          for (int k = 0; k < kK; ++k)
+            if (k < left && mark[k] >= 0) v.starts |= 1u << k;
+        }
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          if (k >= left) {
+            v.at[k] = both(1.f);
+            v.u[k] = both(0.f);
+          } else if (v.starts >> k & 1 && a.h0 && mark[k] < a.n_seq) {
+            v.u[k] = fma2(v.at[k], load_state(a.h0 + (int64_t)mark[k] * a.D + c0, nv), v.u[k]);
+          }
+        }
+      }
+      Map mine = {v.at[0], v.u[0]};
+      if (v.starts == 0) {
+#pragma unroll
+        for (int k = 1; k < kK; ++k) mine = Map{mul2(mine.A, v.at[k]), fma2(v.at[k], mine.U, v.u[k])};
+      } else {
+        if (v.starts & 1) mine.A = both(0.f);
+#pragma unroll
+        for (int k = 1; k < kK; ++k)
+          mine = v.starts >> k & 1 ? Map{both(0.f), v.u[k]}
+                                   : Map{mul2(mine.A, v.at[k]), fma2(v.at[k], mine.U, v.u[k])};
+      }
+      s.warp[step & 1][warp][lane] = packed(mine);
+      __syncwarp();
+      arrive(kMaps + (step & 1));
+    };
+    auto run = [&](int step, const Step &v) {  // through the tokens from their true state
+      const int tw = first + step * stride, left = a.T - tw;
+      meet(kFronts + (step & 1));
+      f2 h = s.front[step & 1][warp][lane];
+      if (left <= 0) return;
+      const bool any = s.any[step & 3];
+      int seg = s.alive[step & 3];
+      if (a.kept) store<VEC>(a.kept + (int64_t)(tw / kK) * a.D + c0, h, nv);
+      E *to = y + (int64_t)tw * a.y.st;
+      if (!any && left >= kK) {
+        const int n = seg >= 0 && seg < a.n_seq ? nv : 0;
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          h = fma2(v.at[k], h, v.u[k]);
+          if (OUT) store<VEC>(to, h, n);
+          to += a.y.st;
+        }
+      } else {
+        if (any) seg = segment_at(s.mark[step & 3], warp * kK, seg);
+        const int *mark = s.mark[step & 3] + warp * kK;
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          if (k >= left) break;
+          const bool starts = v.starts >> k & 1;
+          if (starts) seg = mark[k];
+          h = starts ? v.u[k] : fma2(v.at[k], h, v.u[k]);
+          if (seg >= 0 && seg < a.n_seq) {
+            if (OUT) store<VEC>(to, h, nv);
+            if (a.ht && any && mark[k + 1] >= 0) store_state(a.ht + (int64_t)seg * a.D + c0, h, nv);
+          }
+          to += a.y.st;
+        }
+      }
+    };
+    Step even, odd;
+    if (steps > 0) hold(0, even);
+    for (int step = 0; step < steps; step += 2) {
+      in.issue(0, first + (step + 2) * stride, stride);
+      if (step + 1 < steps) hold(step + 1, odd);
+      run(step, even);
+      if (step + 1 < steps) {
+        in.issue(1, first + (step + 3) * stride, stride);
+        if (step + 2 < steps) hold(step + 2, even);
+        run(step + 1, odd);
+      }
+    }
+    if (VEC) copies_wait<0>();
+  }
+  __syncthreads();
+  cluster_leave();
   // segments without tokens end as they start
   if (a.ht && rank == 0)
     for_empty_segments(a.cu, a.n_seq, a.T, s.red, [&](int n) {
-      if (warp == 0)
-        for (int c = 0; c < nv; ++c)
-          a.ht[(int64_t)n * a.D + c0 + c] = a.h0 ? a.h0[(int64_t)n * a.D + c0 + c] : 0.f;
+      if (warp == 0) {
+        const int64_t at = (int64_t)n * a.D + c0;
+        store_state(a.ht + at, a.h0 ? load_state(a.h0 + at, nv) : both(0.f), nv);
+      }
     });
 }
 
@@ -495,191 +786,200 @@ __global__ void __launch_bounds__(1024) k_rec_bounds(const int32_t *cu, int n, i
   }
 }
 
-template <typename E, bool VEC>
-__global__ void __launch_bounds__(kBwdP * 32, 3) k_rec_bwd(const RecArgs a, const int32_t *bounds) {
+template <typename E, bool VEC, bool NORM>
+__global__ void __launch_bounds__(kP * 32, 2) k_rec_bwd(const RecArgs a, const int32_t *bounds) {
   after_previous();
-  constexpr int P = kBwdP, K = kBwdK, N = P * K;
-  __shared__ Shared<P, K> s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  extern __shared__ __align__(16) unsigned char raw[];
+  __shared__ Shared s;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int rank = cluster_rank(), size = cluster_size();
-  const int c0 = (int)(blockIdx.x / size) * kCh + lane * 2, nv = max(0, min(2, a.D - c0));
-  const float A[2] = {nv > 0 ? a.A[c0] : 0.f, nv > 1 ? a.A[c0 + 1] : 0.f};
-  const E *x = reinterpret_cast<const E *>(a.x.p) + c0, *r = reinterpret_cast<const E *>(a.r.p) + c0;
-  const E *dy = reinterpret_cast<const E *>(a.dy.p) + c0;
-  const E *ig = a.i.p ? reinterpret_cast<const E *>(a.i.p) + c0 : nullptr;
+  const int cb = (int)(blockIdx.x / size) * kCh, c0 = cb + lane * 2, nv = max(0, min(2, a.D - c0));
+  const f2 A = load_state(a.A + c0, nv), A2 = mul2(A, both(kLog2e));
+  using In = Tokens<E, VEC, 4>;
+  In in{{reinterpret_cast<const E *>(a.x.p) + cb, reinterpret_cast<const E *>(a.r.p) + cb,
+               a.i.p ? reinterpret_cast<const E *>(a.i.p) + cb : nullptr,
+               reinterpret_cast<const E *>(a.dy.p) + cb},
+              {a.x.st, a.r.st, a.i.st, a.dy.st},
+              raw + warp * 2 * In::kPlace, lane, a.D - cb, nv, a.T};
+  const bool gate = a.i.p;
   E *dx = reinterpret_cast<E *>(a.dx.p) + c0, *dr = reinterpret_cast<E *>(a.dr.p) + c0;
   E *di = reinterpret_cast<E *>(a.di.p) + c0;
-  const int steps = (a.T + size * N - 1) / (size * N);
+  const int steps = (a.T + size * kTile - 1) / (size * kTile);
   BackCursor cursor{a.n_seq, bounds[a.n_seq]};
-  auto look = [&](int buf, int t0) {  // warp 0: the bounds of a tile
+  auto look = [&](int buf, int t0) {  // one warp: the bounds of a tile
     int alive = -1;
     const bool any = t0 >= 0 && t0 < a.T &&
-                     tile_marks_back(bounds, t0, min(N, a.T - t0), s.mark[buf], cursor, alive);
+                     tile_marks_back(bounds, t0, min(kTile, a.T - t0), s.mark[buf], cursor, alive);
     if (lane == 0) {
       s.any[buf] = any;
       s.alive[buf] = alive;
     }
   };
-  if (warp == 0) look(0, ((steps - 1) * size + rank) * N);
+  in.start(((steps - 1) * size + rank) * kTile + warp * kK);
+  if (steps > 0) in.issue(0, ((steps - 1) * size + rank) * kTile + warp * kK, -size * kTile);
+  if (warp == kLook) look(0, ((steps - 1) * size + rank) * kTile);
+  s.init();
   cluster_arrive();
   cluster_wait();
-  float carry[2] = {0.f, 0.f}, dA[2] = {0.f, 0.f};
-  int buf = 0;
-  for (int step = steps - 1; step >= 0; --step, buf ^= 1) {
-    const int t0 = (step * size + rank) * N, tw = t0 + warp * K, left = a.T - tw;
-    Raw2<E> xr[K], ir[K];
-    float g[K][2], sr[K][2], at[K][2], m[K][2], hb[K][2];
-    float h[2] = {0.f, 0.f};
-    if (left > 0) {
-      const Raw2<float> q = ld2<VEC>(a.kept + (int64_t)(tw / kRecEvery) * a.D + c0, nv);
-      h[0] = q.lo();
-      h[1] = q.hi();
+  f2 carry = both(0.f), dA = both(0.f);
+  const f2 one = both(1.f), minus = both(-1.f);
+  int turn = 0;
+  for (int step = steps - 1; step >= 0; --step, ++turn) {
+    const int buf = turn & 1;
+    const int t0 = (step * size + rank) * kTile, tw = t0 + warp * kK, left = a.T - tw;
+    f2 h = both(0.f);
+    if (left > 0) h = wide(ld2<VEC>(a.kept + (int64_t)(tw / kK) * a.D + c0, nv));
+    if (step > 0) in.issue(buf ^ 1, tw - size * kTile, -size * kTile);
+    else if (VEC) copies_commit();
+    in.wait();
+    f2 sr[kK], at[kK], m[kK], si[kK], g[kK], hb[kK];
+    bool alone = !gate;
+    if (gate) {
+      float q = 1.f;
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        float p;
+        sigmoids(in.get(buf, 1, k, tw + k), in.get(buf, 2, k, tw + k), sr[k], si[k], p);
+        q = fminf(q, p);
+      }
+      alone = __any_sync(0xffffffffu, q == 0.f);
     }
-    {
-      Raw2<E> rr[K], gr[K];
+    if (alone) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int64_t t = tw + k;
-        const int n = k < left ? nv : 0;
-        rr[k] = ld2<VEC>(r + t * a.r.st, n);
-        gr[k] = ld2<VEC>(dy + t * a.dy.st, n);
-        xr[k] = ld2<VEC>(x + t * a.x.st, n);
-        if (ig) ir[k] = ld2<VEC>(ig + t * a.i.st, n);
+      for (int k = 0; k < kK; ++k) {
+        sr[k] = sigmoid2(in.get(buf, 1, k, tw + k));
+        si[k] = gate ? sigmoid2(in.get(buf, 2, k, tw + k)) : one;
       }
+    }
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const float rs[2] = {rr[k].lo(), rr[k].hi()};
-        g[k][0] = gr[k].lo();
-        g[k][1] = gr[k].hi();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const Token v = token(rs[c], A[c] * kLog2e, a.normalize);
-          sr[k][c] = v.sr;
-          at[k][c] = k < left ? v.a : 1.f;
-          m[k][c] = v.m;
-        }
-      }
+    for (int k = 0; k < kK; ++k) {
+      const Token v = token<NORM>(sr[k], A2);
+      at[k] = v.a;
+      m[k] = v.m;
+      g[k] = in.get(buf, 3, k, tw + k);
     }
     const bool any = s.any[buf];
-    const int *mark = s.mark[buf] + warp * K;
-    const int seg0 = any && left > 0 ? segment_at(s.mark[buf], warp * K, s.alive[buf]) : s.alive[buf];
-    // bit k: a segment starts with token k (of K + 1)
-    uint32_t starts = 0;
-    if (any) {
+    const int *mark = s.mark[buf] + warp * kK;
+    int seg0 = s.alive[buf];
+    uint32_t starts = 0;  // bit k: a segment starts with token k (of kK + 1)
+    Map mine;
+    if (!any && left >= kK) {
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        hb[k] = h;
+        h = fma2(at[k], h, mul2(m[k], mul2(si[k], in.get(buf, 0, k, tw + k))));
+      }
+      mine = Map{at[kK - 1], mul2(at[kK - 1], g[kK - 1])};
+#pragma unroll
+      for (int k = kK - 2; k >= 0; --k)
+        mine = Map{mul2(mine.A, at[k]), mul2(at[k], add2(g[k], mine.U))};
+    } else {
+      if (any && left > 0) {
+        seg0 = segment_at(s.mark[buf], warp * kK, seg0);
 #pragma unroll 1
-      for (int k = 0; k <= K; ++k)
-        if (k <= left && mark[k] >= 0) starts |= 1u << k;
+        for (int k = 0; k <= kK; ++k)
+          if (k <= left && mark[k] >= 0) starts |= 1u << k;
+      }
+      // the states before the tokens, and the final states' gradients
+      int seg = seg0;
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        hb[k] = h;
+        if (k >= left) {
+          at[k] = one;
+          g[k] = both(0.f);
+          continue;
+        }
+        if (starts >> k & 1) {
+          seg = mark[k];
+          hb[k] = a.h0 && seg < a.n_seq ? load_state(a.h0 + (int64_t)seg * a.D + c0, nv) : both(0.f);
+        }
+        if (starts >> (k + 1) & 1 && seg >= 0 && seg < a.n_seq && a.dht)
+          g[k] = add2(g[k], load_state(a.dht + (int64_t)seg * a.D + c0, nv));
+        h = fma2(at[k], hb[k], mul2(m[k], mul2(si[k], in.get(buf, 0, k, tw + k))));
+      }
+      mine = Map{one, both(0.f)};
+#pragma unroll
+      for (int k = kK - 1; k >= 0; --k)
+        mine = starts >> (k + 1) & 1 ? Map{both(0.f), mul2(at[k], g[k])}
+                                     : Map{mul2(mine.A, at[k]), mul2(at[k], add2(g[k], mine.U))};
     }
-    // the states before the tokens, and the final states' gradients
-    int seg = seg0;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float is[2] = {1.f, 1.f};
-      if (ig) {
-        is[0] = sigmoidf(ir[k].lo());
-        is[1] = sigmoidf(ir[k].hi());
-      }
-      if (starts >> k & 1) {
-        seg = mark[k];
-        const float *q = a.h0 && seg < a.n_seq ? a.h0 + (int64_t)seg * a.D + c0 : nullptr;
-        h[0] = q && nv > 0 ? q[0] : 0.f;
-        h[1] = q && nv > 1 ? q[1] : 0.f;
-      }
-      const bool in = seg >= 0 && seg < a.n_seq;
-      if (starts >> (k + 1) & 1 && in && a.dht) {
-        const float *q = a.dht + (int64_t)seg * a.D + c0;
-        if (nv > 0) g[k][0] += q[0];
-        if (nv > 1) g[k][1] += q[1];
-      }
-      hb[k][0] = h[0];
-      hb[k][1] = h[1];
-      h[0] = fmaf(at[k][0], h[0], m[k][0] * is[0] * xr[k].lo());
-      h[1] = fmaf(at[k][1], h[1], m[k][1] * is[1] * xr[k].hi());
-    }
-    Map mine[2] = {{1.f, 0.f}, {1.f, 0.f}};
-#pragma unroll
-    for (int k = K - 1; k >= 0; --k)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const bool last = starts >> (k + 1) & 1;
-        const float in = last ? g[k][c] : g[k][c] + mine[c].U;
-        mine[c].A = last ? 0.f : mine[c].A * at[k][c];
-        mine[c].U = at[k][c] * in;
-      }
-    float c1[2];
-    exchange<P, K, true>(s, buf, mine, carry, c1, [&] {
-      if (warp == 0) look(buf ^ 1, t0 - size * N);
-    });
+    f2 c = exchange<true>(s, turn, warp, any, mine, carry, [&] { look(buf ^ 1, t0 - size * kTile); });
     if (left <= 0) continue;
-    seg = any ? -2 : seg0;
+    const bool inside = !any && left >= kK && seg0 >= 0 && seg0 < a.n_seq;
 #pragma unroll
-    for (int k = K - 1; k >= 0; --k) {
+    for (int k = kK - 1; k >= 0; --k) {
       if (k >= left) continue;
-      int own = seg;
-      if (any) own = segment_at(mark, k, seg0);
-      const bool in = own >= 0 && own < a.n_seq;
       const bool last = starts >> (k + 1) & 1;
-      float ox[2], orr[2], oi[2];
-      const float xs[2] = {xr[k].lo(), xr[k].hi()};
-      float is[2] = {1.f, 1.f};
-      if (ig) {
-        is[0] = sigmoidf(ir[k].lo());
-        is[1] = sigmoidf(ir[k].hi());
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float G = last ? g[k][c] : g[k][c] + c1[c];
-        const float dv = G * m[k][c], v = is[c] * xs[c];
+      const f2 x = in.get(buf, 0, k, tw + k), v = mul2(si[k], x);
+      const f2 G = last ? g[k] : add2(g[k], c);
+      const f2 ga = mul2(G, at[k]), dv = mul2(G, m[k]);
+      f2 past = hb[k];
+      if (NORM) {
         // the normaliser's part of d/dL; none where a is 1 and it has no derivative
-        const float ratio = a.normalize && m[k][c] != 0.f ? at[k][c] * rcp(m[k][c]) : 0.f;
-        const float dL = G * at[k][c] * (hb[k][c] - v * ratio);
-        ox[c] = in ? dv * is[c] : 0.f;
-        oi[c] = in ? dv * v * (1.f - is[c]) : 0.f;
-        orr[c] = in ? dL * A[c] * sr[k][c] * (1.f - sr[k][c]) : 0.f;
-        dA[c] += in ? dL * sr[k][c] : 0.f;
-        c1[c] = at[k][c] * G;
+        float lo, hi;
+        unpair(m[k], lo, hi);
+        const f2 ratio = mul2(at[k], pair(lo != 0.f ? rcp(lo) : 0.f, hi != 0.f ? rcp(hi) : 0.f));
+        past = fma2(mul2(v, minus), ratio, past);
       }
+      const f2 q = mul2(mul2(ga, past), sr[k]);  // dL sr
+      f2 ox = mul2(dv, si[k]), oi = mul2(mul2(dv, v), fma2(si[k], minus, one));
+      f2 orr = mul2(mul2(A, q), fma2(sr[k], minus, one));
+      c = ga;
       const int64_t t = tw + k;
-      st2<VEC>(dx + t * a.dx.st, ox[0], ox[1], nv);
-      st2<VEC>(dr + t * a.dr.st, orr[0], orr[1], nv);
-      if (ig) st2<VEC>(di + t * a.di.st, oi[0], oi[1], nv);
-      if (a.dh0 && in && starts >> k & 1) {
-        float *q = a.dh0 + (int64_t)own * a.D + c0;
-        if (nv > 0) q[0] = c1[0];
-        if (nv > 1) q[1] = c1[1];
+      if (inside) {
+        dA = add2(dA, q);
+      } else {
+        const int own = any ? segment_at(mark, k, seg0) : seg0;
+        if (own >= 0 && own < a.n_seq) {
+          dA = add2(dA, q);
+          if (a.dh0 && starts >> k & 1) store_state(a.dh0 + (int64_t)own * a.D + c0, c, nv);
+        } else {
+          ox = oi = orr = both(0.f);
+        }
       }
+      if (VEC) {
+        in.stage(buf, 0, k, ox);
+        in.stage(buf, 1, k, orr);
+        if (gate) in.stage(buf, 2, k, oi);
+      } else {
+        store<VEC>(dx + t * a.dx.st, ox, nv);
+        store<VEC>(dr + t * a.dr.st, orr, nv);
+        if (gate) store<VEC>(di + t * a.di.st, oi, nv);
+      }
+    }
+    if (VEC) {
+      __syncwarp();
+      in.flush(buf, 0, reinterpret_cast<E *>(a.dx.p) + cb, a.dx.st, tw);
+      in.flush(buf, 1, reinterpret_cast<E *>(a.dr.p) + cb, a.dr.st, tw);
+      if (gate) in.flush(buf, 2, reinterpret_cast<E *>(a.di.p) + cb, a.di.st, tw);
     }
   }
+  if (VEC) copies_wait<0>();
   // dA: the warps' sums in order, then the blocks' of the cluster
   __syncthreads();
-  s.warp[warp][lane] = make_float4(dA[0], dA[1], 0.f, 0.f);
+  s.warp[warp][lane] = packed(Map{dA, both(0.f)});
   __syncthreads();
   if (warp == 0) {
-    float4 v = s.warp[0][lane];
+    f2 v = unpacked(s.warp[0][lane]).A;
 #pragma unroll
-    for (int w = 1; w < P; ++w) {
-      v.x += s.warp[w][lane].x;
-      v.y += s.warp[w][lane].y;
-    }
-    put(&s.block[buf][rank][lane], 0, v);
+    for (int w = 1; w < kP; ++w) v = add2(v, unpacked(s.warp[w][lane]).A);
+    put(&s.block[turn & 1][rank][lane], 0, packed(Map{v, both(0.f)}));
   }
   cluster_arrive();
   cluster_wait();
   if (rank == 0) {
     if (warp == 0) {
-      float4 v = s.block[buf][0][lane];
-      for (int b = 1; b < size; ++b) {
-        v.x += s.block[buf][b][lane].x;
-        v.y += s.block[buf][b][lane].y;
-      }
-      if (nv > 0) a.dA[c0] = v.x;
-      if (nv > 1) a.dA[c0 + 1] = v.y;
+      f2 v = unpacked(s.block[turn & 1][0][lane]).A;
+      for (int b = 1; b < size; ++b) v = add2(v, unpacked(s.block[turn & 1][b][lane]).A);
+      store_state(a.dA + c0, v, nv);
     }
     if (a.dh0)
       for_empty_segments(a.cu, a.n_seq, a.T, s.red, [&](int n) {
-        if (warp == 0)
-          for (int c = 0; c < nv; ++c)
-            a.dh0[(int64_t)n * a.D + c0 + c] = a.dht ? a.dht[(int64_t)n * a.D + c0 + c] : 0.f;
+        if (warp == 0) {
+          const int64_t at = (int64_t)n * a.D + c0;
+          store_state(a.dh0 + at, a.dht ? load_state(a.dht + at, nv) : both(0.f), nv);
+        }
       });
   }
 }
@@ -704,52 +1004,102 @@ __global__ void __launch_bounds__(128) k_rec_step(const RecArgs a, float *state,
   const Raw2<float> h = ld2<VEC>(q, nv), A = ld2<VEC>(a.A + c0, nv);
   const Raw2<E> x = ld2<VEC>(reinterpret_cast<const E *>(a.x.p) + (int64_t)row * a.x.st + c0, nv);
   const Raw2<E> r = ld2<VEC>(reinterpret_cast<const E *>(a.r.p) + (int64_t)row * a.r.st + c0, nv);
-  float is[2] = {1.f, 1.f};
-  if (a.i.p) {
-    const Raw2<E> i =
-        ld2<VEC>(reinterpret_cast<const E *>(a.i.p) + (int64_t)row * a.i.st + c0, nv);
-    is[0] = sigmoidf(i.lo());
-    is[1] = sigmoidf(i.hi());
-  }
-  const Token u = token(r.lo(), A.lo() * kLog2e, a.normalize);
-  const Token v = token(r.hi(), A.hi() * kLog2e, a.normalize);
-  const float lo = fmaf(u.a, h.lo(), u.m * is[0] * x.lo());
-  const float hi = fmaf(v.a, h.hi(), v.m * is[1] * x.hi());
-  st2<VEC>(q, lo, hi, nv);
-  st2<VEC>(y, lo, hi, nv);
+  f2 u = wide(x);
+  if (a.i.p)
+    u = mul2(u, sigmoid2(wide(
+                    ld2<VEC>(reinterpret_cast<const E *>(a.i.p) + (int64_t)row * a.i.st + c0, nv))));
+  const f2 A2 = mul2(wide(A), both(kLog2e));
+  const Token v = a.normalize ? token<true>(sigmoid2(wide(r)), A2) : token<false>(sigmoid2(wide(r)), A2);
+  const f2 out = fma2(v.a, wide(h), mul2(v.m, u));
+  store<VEC>(q, out, nv);
+  store<VEC>(y, out, nv);
 }
 
 // ------------------------------------------------------------------ launches
 
-// Pairs of channels at addresses that are multiples of a pair.
+// Rows at multiples of n bytes, floats of pairs at multiples of 8.
 template <typename E>
-bool pairs(const RecArgs &a, std::initializer_list<Mat> mats, std::initializer_list<const void *> f) {
-  bool ok = a.D % 2 == 0;
+bool rows_fit(const RecArgs &a, int n, std::initializer_list<Mat> mats,
+              std::initializer_list<const void *> f) {
+  bool ok = a.D * (int64_t)sizeof(E) % n == 0;
   for (const Mat &m : mats)
-    ok = ok && reinterpret_cast<uintptr_t>(m.p) % (2 * sizeof(E)) == 0 && m.st % 2 == 0;
+    ok = ok && reinterpret_cast<uintptr_t>(m.p) % n == 0 && m.st * (int64_t)sizeof(E) % n == 0;
   for (const void *p : f) ok = ok && reinterpret_cast<uintptr_t>(p) % 8 == 0;
   return ok;
 }
 
-// Blocks of a cluster: as many as the tokens fill, while all blocks run at once.
-int cluster_for(int T, int D, int tile, int per_sm) {
-  const int64_t groups = (D + kCh - 1) / kCh, slots = (int64_t)sm_count() * per_sm;
-  int cl = 1;
-  while (cl < 8 && (int64_t)cl * tile < T && groups * cl * 2 <= slots) cl *= 2;
+// Clusters of `cl` blocks that run at once (asked for once for each device and size; -1: unknown).
+template <typename K>
+int clusters_at_once(K *kernel, int cl, int smem, std::atomic<int> (&known)[64][kMostCl + 1]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  if (dev >= 0 && dev < 64) {
+    const int n = known[dev][cl].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+  }
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)cl;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)cl);
+  c.blockDim = dim3(kP * 32);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  if (n > 0 && dev >= 0 && dev < 64) known[dev][cl].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Blocks of a cluster: as many as the tokens fill, while all clusters run at once (a cluster's blocks lie
+// in one part of the GPU, so that fewer fit than their number of blocks says).
+template <typename K>
+int cluster_for(K *kernel, int T, int D, int tile, int smem,
+                std::atomic<int> (&known)[64][kMostCl + 1]) {
+  const int64_t groups = (D + kCh - 1) / kCh, tiles = ceil_div64(T, tile);
+  int cl = tiles < 1 ? 1 : tiles > kMostCl ? kMostCl : (int)tiles;
+  while (cl > 1 && clusters_at_once(kernel, cl, smem, known) < groups) --cl;
   return cl;
 }
 
+template <auto kernel, typename... A>
+cudaError_t run_clusters(const RecArgs &a, int tile, int smem, cudaStream_t stream, A... more) {
+  static std::atomic<uint64_t> bytes{0}, size{0};
+  static std::atomic<int> known[64][kMostCl + 1];
+  cudaError_t e = set_once(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, bytes);
+  if (e == cudaSuccess) e = set_once(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, size);
+  if (e != cudaSuccess) return e;
+  const int cl = cluster_for(kernel, a.T, a.D, tile, smem, known);
+  return launch_clusters(kernel, (a.D + kCh - 1) / kCh * cl, cl, kP * 32, smem, stream, a, more...);
+}
+
+template <typename E, bool VEC, bool OUT, bool NORM>
+cudaError_t run_fwd_as(const RecArgs &a, cudaStream_t stream) {
+  return run_clusters<k_rec_fwd<E, VEC, OUT, NORM>>(a, kFwdTile, Tokens<E, VEC, 3>::kBytes, stream);
+}
 template <typename E, bool OUT>
 cudaError_t run_fwd(const RecArgs &a, cudaStream_t stream) {
-  const int cl = cluster_for(a.T, a.D, kFwdP * kFwdK, 4), groups = (a.D + kCh - 1) / kCh;
-  const bool vec = OUT ? pairs<E>(a, {a.x, a.r, a.i, a.y}, {a.kept})
-                       : pairs<E>(a, {a.x, a.r, a.i}, {a.kept});
-  return vec ? launch_clusters(k_rec_fwd<E, true, OUT>, groups * cl, cl, kFwdP * 32, stream, a)
-             : launch_clusters(k_rec_fwd<E, false, OUT>, groups * cl, cl, kFwdP * 32, stream, a);
+  const bool vec = OUT ? rows_fit<E>(a, 16, {a.x, a.r, a.i, a.y}, {a.kept})
+                       : rows_fit<E>(a, 16, {a.x, a.r, a.i}, {a.kept});
+  if (a.normalize)
+    return vec ? run_fwd_as<E, true, OUT, true>(a, stream)
+               : run_fwd_as<E, false, OUT, true>(a, stream);
+  return vec ? run_fwd_as<E, true, OUT, false>(a, stream)
+             : run_fwd_as<E, false, OUT, false>(a, stream);
 }
 
 size_t kept_bytes(int64_t T, int32_t D) {
   return align256((size_t)((T + kRecEvery - 1) / kRecEvery) * D * 4);
+}
+
+template <typename E, bool VEC, bool NORM>
+cudaError_t run_bwd_as(const RecArgs &a, const int32_t *bounds, cudaStream_t stream) {
+  return run_clusters<k_rec_bwd<E, VEC, NORM>>(a, kTile, Tokens<E, VEC, 4>::kBytes, stream, bounds);
 }
 
 template <typename E>
@@ -764,16 +1114,18 @@ cudaError_t run_bwd(RecArgs a, bool kept, cudaStream_t stream) {
     e = run_fwd<E, false>(a, stream);
     if (e != cudaSuccess) return e;
   }
-  const int cl = cluster_for(a.T, a.D, kBwdP * kBwdK, 3), groups = (a.D + kCh - 1) / kCh;
-  return pairs<E>(a, {a.x, a.r, a.i, a.dy, a.dx, a.dr, a.di}, {a.kept})
-             ? launch_clusters(k_rec_bwd<E, true>, groups * cl, cl, kBwdP * 32, stream, a, bounds)
-             : launch_clusters(k_rec_bwd<E, false>, groups * cl, cl, kBwdP * 32, stream, a, bounds);
+  const bool vec = rows_fit<E>(a, 16, {a.x, a.r, a.i, a.dy, a.dx, a.dr, a.di}, {a.kept});
+  if (a.normalize)
+    return vec ? run_bwd_as<E, true, true>(a, bounds, stream)
+               : run_bwd_as<E, false, true>(a, bounds, stream);
+  return vec ? run_bwd_as<E, true, false>(a, bounds, stream)
+             : run_bwd_as<E, false, false>(a, bounds, stream);
 }
 
 template <typename E>
 cudaError_t run_step(const RecArgs &a, float *state, int32_t slots, const int32_t *idx,
                      cudaStream_t stream) {
-  const bool vec = pairs<E>(a, {a.x, a.r, a.i, a.y}, {state, a.A});
+  const bool vec = a.D % 2 == 0 && rows_fit<E>(a, 2 * sizeof(E), {a.x, a.r, a.i, a.y}, {state, a.A});
   // rows beyond a grid's second dimension in further launches
   RecArgs p = a;
   for (int32_t row = 0; row < a.T; row += 65535) {
@@ -798,6 +1150,14 @@ cudaError_t run_step(const RecArgs &a, float *state, int32_t slots, const int32_
 
 }  // namespace
 }  // namespace mix
+
+cudaError_t read_rec_status(int32_t *out) {
+  return cudaMemcpyFromSymbol(out, mix::g_rec_status, sizeof(int32_t));
+}
+cudaError_t clear_rec_status() {
+  const int32_t zero = 0;
+  return cudaMemcpyToSymbol(mix::g_rec_status, &zero, sizeof(int32_t));
+}
 
 cudaError_t launch_rec_fwd(const RecArgs &a, cudaStream_t stream) {
   return a.f32 ? mix::run_fwd<float, true>(a, stream)

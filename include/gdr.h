@@ -290,7 +290,8 @@ int gdr_debug_check_cu_seqlens(const int32_t *cu_seqlens, int32_t n_seq, int64_t
 /*
  * Device status word of the fused kernel.  Every bounded wait inside the fused
  * kernel that runs out (after 2 s) sets a nonzero code here: 0x1xx producer,
- * 0x2xx MMA issuer, 0x3xx prep warps, 0x4xx state warps; the CTA then drains its
+ * 0x2xx MMA issuer, 0x3xx prep warps, 0x4xx state warps (0x6xx: the blocks of the gated
+ * linear recurrence, which wait for one another and go on to their end); the CTA then drains its
  * copies and MMAs in flight, releases its Tensor Memory and returns instead of
  * hanging.  gdr_device_status synchronises the current device and
  * reads the word; gdr_clear_device_status resets it.  0 means no wait ran out.
