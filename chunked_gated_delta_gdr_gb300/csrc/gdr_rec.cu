@@ -328,17 +328,21 @@ __device__ __forceinline__ bool tile_marks_back(const int32_t *bounds, int t0, i
 
 // ------------------------------------------------------------------ a warp's tokens
 
-constexpr int kP = 8, kK = 8, kTile = kP * kK;  // warps of a block, tokens of a thread, of a block
-constexpr int kLook = kP / 2;  // the warp that looks up bounds: neither the first nor the last in order
+constexpr int kP = 8, kK = 8;  // warps of a block, tokens of a thread
+constexpr int kHold = kP - 1, kTile = kHold * kK;  // warps with tokens, tokens of a block
 static_assert(kRecEvery == kK, "a kept state for each thread's tokens");
 
+// Of a block's eight warps seven hold tokens and one chains their maps.  The holders compute the maps of
+// step s + 1 while the chain of step s is on its way through the cluster, and then run through step
+// s: nobody waits for a map that was sent just now.  Places are written again when a later meeting
+// has shown that they were read: maps and states two steps on, bounds (looked up two steps ahead) four.
 struct Shared {
-  float4 warp[kP][32];           // (A, U) of both channels, for each warp of the block
-  float4 block[2][kMostCl][32];  // and for each block of the cluster, by the step's parity
-  f2 front[kP][32];              // the state in front of each warp's tokens
+  float4 warp[2][kHold][32];     // (A, U) of both channels, for each warp with tokens
+  float4 block[2][kMostCl][32];  // and for each block of the cluster
+  f2 front[2][kHold][32];        // the state in front of each warp's tokens
   uint64_t bar[2];               // every block's map is here
-  int mark[2][kTile + 1];
-  int any[2], alive[2];
+  int mark[4][kTile + 1];
+  int any[4], alive[4];
   int red[64];
   __device__ __forceinline__ void init() {
     if (threadIdx.x == 0) {
@@ -349,14 +353,23 @@ struct Shared {
   }
 };
 
+// Meetings of holders and chain, two of each kind in turn.
+__device__ __forceinline__ void arrive(int id) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(kP * 32) : "memory");
+}
+__device__ __forceinline__ void meet(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(kP * 32) : "memory");
+}
+constexpr int kMaps = 1, kFronts = 3;
+
 // The N tensors of a step on their way into shared memory: a warp's rows of 64 channels come 16 bytes
-// at a time into one of two places of its own, a step ahead, and are read two channels a lane.
+// at a time into one of S places of its own, a step ahead, and are read two channels a lane.
 // Without 16-byte alignment (RING false) they are loaded when they are used.
-template <typename E, bool RING, int N>
+template <typename E, bool RING, int N, int S>
 struct Tokens {
   static constexpr int kRow = kCh * (int)sizeof(E);          // bytes
   static constexpr int kPlace = N * kK * kRow;               // of a warp's step
-  static constexpr int kBytes = RING ? 2 * kP * kPlace : 0;  // of a block
+  static constexpr int kBytes = RING ? S * kHold * kPlace : 0;  // of a block
   const E *p[N];  // at this block's first channel; null: not there
   int64_t st[N];
   unsigned char *mine;  // this warp's places
@@ -404,26 +417,13 @@ struct Tokens {
                                                      lane * 2 * (int)sizeof(E)));
     return wide(ld2<false>(p[n] + (int64_t)t * st[n] + lane * 2, t < T ? nv : 0));
   }
-  // The lane's two channels of a result's row, and then all rows from token t on to p: through the
-  // place of tensor n, which has been read, 16 bytes a lane.
-  __device__ __forceinline__ void stage(int place, int n, int k, f2 v) const {
-    float lo, hi;
-    unpair(v, lo, hi);
-    st2<true>(reinterpret_cast<E *>(mine + place * kPlace + (n * kK + k) * kRow) + lane * 2, lo, hi, 2);
-  }
-  __device__ __forceinline__ void flush(int place, int n, E *to, int64_t to_st, int t) const {
-    constexpr int L = kL, R = kR;
-    const int c = lane % L, row = lane / L;
-    const unsigned char *from = mine + place * kPlace + n * kK * kRow + row * kRow + c * 16;
-    to += (int64_t)(t + row) * to_st + c * (16 / (int)sizeof(E));
-    if (c * (16 / (int)sizeof(E)) < cols) {
-#pragma unroll
-      for (int k = 0; k < kK; k += R)
-        if (t + row + k < T)
-          *reinterpret_cast<uint4 *>(to + k * to_st) = *reinterpret_cast<const uint4 *>(from + k * kRow);
-    }
-  }
 };
+
+// Bit k: a segment starts with token k of n, of which `left` are there.
+__device__ __forceinline__ uint32_t starts_of(const int *mark, int left, int n) {
+  const int k = threadIdx.x & 31;
+  return __ballot_sync(0xffffffffu, k < n && k <= left && left > 0 && mark[min(k, max(left, 0))] >= 0);
+}
 
 __device__ __forceinline__ int uniform_warp() {
   return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
@@ -434,59 +434,6 @@ __device__ __forceinline__ int segment_at(const int *mark, int i, int alive) {
   int m = alive;
   for (int j = threadIdx.x & 31; j <= i; j += 32) m = max(m, mark[j]);
   return __reduce_max_sync(0xffffffffu, m);
-}
-
-// What the threads of a cluster exchange in step `turn`: returns the state in front of this thread's
-// tokens and moves `carry`, which the first warp has, past the step.  any: a segment may start in the
-// block's tokens.  f() runs in warp kLook where the block's last step is done with, and what it writes
-// is seen after the exchange.  BACK: warps and blocks in reverse.
-//
-// One warp chains the block's maps, for all of them would take most of the issue slots.  The block's map goes to all blocks as counted stores, so that nobody waits for this block's other
-// writes as at a cluster's barrier.  A place is written again two steps later: by a block that has seen
-// all maps of the step between, whose senders had read theirs of this one.
-template <bool BACK, typename F>
-__device__ __forceinline__ f2 exchange(Shared &s, int turn, int warp, bool any, Map mine, f2 &carry,
-                                       F f) {
-  const int lane = threadIdx.x & 31, buf = turn & 1;
-  s.warp[warp][lane] = packed(mine);
-  __syncthreads();
-  if (warp == kLook) f();
-  if (warp == 0) {
-    const int rank = cluster_rank(), size = cluster_size();
-    Map all = unpacked(s.warp[BACK ? kP - 1 : 0][lane]);
-    if (any) {
-#pragma unroll 1
-      for (int j = 1; j < kP; ++j) all = then(all, unpacked(s.warp[BACK ? kP - 1 - j : j][lane]));
-    } else {
-#pragma unroll
-      for (int j = 1; j < kP; ++j)
-        all = then_inside(all, unpacked(s.warp[BACK ? kP - 1 - j : j][lane]));
-    }
-    const float4 out = packed(all);
-#pragma unroll 2
-    for (int to = 0; to < size; ++to) send(&s.block[buf][rank][lane], &s.bar[buf], to, out);
-    if (lane == 0) tc::mbar_expect_tx(&s.bar[buf], size * 512);
-    __syncwarp();
-    if (!tc::mbar_wait(&s.bar[buf], turn >> 1 & 1, nullptr, kRecWaitNs))
-      atomicCAS(&g_rec_status, 0, BACK ? 0x602 : 0x601);  // the results are void; go on to the end
-    f2 h = carry, front = carry;
-#pragma unroll 4
-    for (int j = 0; j < size; ++j) {
-      const int b = BACK ? size - 1 - j : j;
-      const Map v = unpacked(s.block[buf][b][lane]);
-      if (b == rank) front = h;
-      h = through(v, h);
-    }
-    carry = h;
-#pragma unroll
-    for (int j = 0; j < kP; ++j) {
-      const int w = BACK ? kP - 1 - j : j;
-      s.front[w][lane] = front;
-      if (j < kP - 1) front = through(unpacked(s.warp[w][lane]), front);
-    }
-  }
-  __syncthreads();
-  return s.front[warp][lane];
 }
 
 // nv of two fp32 values at any address
@@ -507,47 +454,23 @@ __device__ __forceinline__ void store(E *p, f2 v, int nv) {
 }
 
 // ------------------------------------------------------------------ forward
-//
-// Of a block's eight warps seven hold tokens and one chains their maps.  The holders compute step s + 1
-// while the chain of step s is on its way through the cluster, and then run through step s: nobody
-// waits for a map that was sent just now.  Shared places are written again when a later meeting has
-// shown that they were read: maps and states two steps on, bounds (looked up two steps ahead) four.
-
-constexpr int kHold = kP - 1, kFwdTile = kHold * kK;  // warps with tokens, and a block's tokens
-
-struct FwdShared {
-  float4 warp[2][kHold][32];     // (A, U) of both channels, for each warp with tokens
-  float4 block[2][kMostCl][32];  // and for each block of the cluster
-  f2 front[2][kHold][32];        // the state in front of each warp's tokens
-  uint64_t bar[2];               // every block's map is here
-  int mark[4][kFwdTile + 1];
-  int any[4], alive[4];
-  int red[64];
-};
-
-// Meetings of holders and chain, two of each kind in turn.
-__device__ __forceinline__ void arrive(int id) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(kP * 32) : "memory");
-}
-__device__ __forceinline__ void meet(int id) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(kP * 32) : "memory");
-}
-constexpr int kMaps = 1, kFronts = 3;
 
 // The chain warp's work in step s, once the holders' maps are there: the block's map to all blocks, and
 // from theirs the state in front of each warp.  The block's map goes out as counted stores, so that
 // nobody waits for this block's other writes as at a cluster's barrier.  A place is written again two
 // steps later: by a block that has seen all maps of the step between, whose senders had read this one's.
-template <int HOLD, typename S>
-__device__ __forceinline__ void chain(S &s, int step, bool any, f2 &carry) {
+// BACK: warps and blocks in reverse.
+template <bool BACK>
+__device__ __forceinline__ void chain(Shared &s, int step, bool any, f2 &carry) {
   const int lane = threadIdx.x & 31, buf = step & 1, rank = cluster_rank(), size = cluster_size();
-  Map all = unpacked(s.warp[buf][0][lane]);
+  auto map = [&](int j) { return unpacked(s.warp[buf][BACK ? kHold - 1 - j : j][lane]); };
+  Map all = map(0);
   if (any) {
 #pragma unroll 1
-    for (int j = 1; j < HOLD; ++j) all = then(all, unpacked(s.warp[buf][j][lane]));
+    for (int j = 1; j < kHold; ++j) all = then(all, map(j));
   } else {
 #pragma unroll
-    for (int j = 1; j < HOLD; ++j) all = then_inside(all, unpacked(s.warp[buf][j][lane]));
+    for (int j = 1; j < kHold; ++j) all = then_inside(all, map(j));
   }
   const float4 out = packed(all);
 #pragma unroll 2
@@ -555,19 +478,20 @@ __device__ __forceinline__ void chain(S &s, int step, bool any, f2 &carry) {
   if (lane == 0) tc::mbar_expect_tx(&s.bar[buf], size * 512);
   __syncwarp();
   if (!tc::mbar_wait(&s.bar[buf], step >> 1 & 1, nullptr, kRecWaitNs))
-    atomicCAS(&g_rec_status, 0, 0x601);  // the results are void; go on to the end
+    atomicCAS(&g_rec_status, 0, BACK ? 0x602 : 0x601);  // the results are void; go on to the end
   f2 h = carry, front = carry;
 #pragma unroll 4
   for (int j = 0; j < size; ++j) {
-    const Map v = unpacked(s.block[buf][j][lane]);
-    if (j == rank) front = h;
+    const int b = BACK ? size - 1 - j : j;
+    const Map v = unpacked(s.block[buf][b][lane]);
+    if (b == rank) front = h;
     h = through(v, h);
   }
   carry = h;
 #pragma unroll
-  for (int j = 0; j < HOLD; ++j) {
-    s.front[buf][j][lane] = front;
-    if (j < HOLD - 1) front = through(unpacked(s.warp[buf][j][lane]), front);
+  for (int j = 0; j < kHold; ++j) {
+    s.front[buf][BACK ? kHold - 1 - j : j][lane] = front;
+    if (j < kHold - 1) front = through(map(j), front);
   }
 }
 
@@ -582,23 +506,19 @@ template <typename E, bool VEC, bool OUT, bool NORM>
 __global__ void __launch_bounds__(kP * 32, 2) k_rec_fwd(const RecArgs a) {
   after_previous();
   extern __shared__ __align__(16) unsigned char raw[];
-  __shared__ FwdShared s;
+  __shared__ Shared s;
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int rank = cluster_rank(), size = cluster_size();
   const int cb = (int)(blockIdx.x / size) * kCh, c0 = cb + lane * 2, nv = max(0, min(2, a.D - c0));
-  const int stride = size * kFwdTile, steps = (a.T + stride - 1) / stride;
-  if (threadIdx.x == 0) {
-    tc::mbar_init(&s.bar[0], 1);
-    tc::mbar_init(&s.bar[1], 1);
-    tc::fence_mbar_init();
-  }
+  const int stride = size * kTile, steps = (a.T + stride - 1) / stride;
+  s.init();
   if (warp == kHold) {
     SegCursor cursor{0, 0, 0};
     auto look = [&](int step) {  // the bounds of a tile
       const int buf = step & 3;
-      const int64_t t0 = (int64_t)step * stride + rank * kFwdTile;
+      const int64_t t0 = (int64_t)step * stride + rank * kTile;
       int alive = -1;
-      const bool any = t0 < a.T && tile_marks(a.cu, a.n_seq, a.T, (int)t0, min(kFwdTile, a.T - (int)t0),
+      const bool any = t0 < a.T && tile_marks(a.cu, a.n_seq, a.T, (int)t0, min(kTile, a.T - (int)t0),
                                               s.mark[buf], cursor, alive);
       if (lane == 0) {
         s.any[buf] = any;
@@ -613,7 +533,7 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_fwd(const RecArgs a) {
     for (int step = 0; step < steps; ++step) {
       meet(kMaps + (step & 1));
       const bool any2 = look(step + 2);
-      chain<kHold>(s, step, any0, carry);
+      chain<false>(s, step, any0, carry);
       any0 = any1;
       any1 = any2;
       __syncwarp();
@@ -621,14 +541,14 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_fwd(const RecArgs a) {
     }
   } else {
     const f2 A2 = mul2(load_state(a.A + c0, nv), both(kLog2e));
-    using In = Tokens<E, VEC, 3>;
+    using In = Tokens<E, VEC, 3, 2>;
     In in{{reinterpret_cast<const E *>(a.x.p) + cb, reinterpret_cast<const E *>(a.r.p) + cb,
            a.i.p ? reinterpret_cast<const E *>(a.i.p) + cb : nullptr},
           {a.x.st, a.r.st, a.i.st},
           raw + warp * 2 * In::kPlace, lane, a.D - cb, nv, a.T};
     const bool gate = a.i.p;
     E *y = reinterpret_cast<E *>(a.y.p) + c0;
-    const int first = rank * kFwdTile + warp * kK;
+    const int first = rank * kTile + warp * kK;
     in.start(first);
     in.issue(0, first, stride);
     in.issue(1, first + stride, stride);
@@ -794,184 +714,241 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_bwd(const RecArgs a, const i
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int rank = cluster_rank(), size = cluster_size();
   const int cb = (int)(blockIdx.x / size) * kCh, c0 = cb + lane * 2, nv = max(0, min(2, a.D - c0));
-  const f2 A = load_state(a.A + c0, nv), A2 = mul2(A, both(kLog2e));
-  using In = Tokens<E, VEC, 4>;
-  In in{{reinterpret_cast<const E *>(a.x.p) + cb, reinterpret_cast<const E *>(a.r.p) + cb,
-               a.i.p ? reinterpret_cast<const E *>(a.i.p) + cb : nullptr,
-               reinterpret_cast<const E *>(a.dy.p) + cb},
-              {a.x.st, a.r.st, a.i.st, a.dy.st},
-              raw + warp * 2 * In::kPlace, lane, a.D - cb, nv, a.T};
-  const bool gate = a.i.p;
-  E *dx = reinterpret_cast<E *>(a.dx.p) + c0, *dr = reinterpret_cast<E *>(a.dr.p) + c0;
-  E *di = reinterpret_cast<E *>(a.di.p) + c0;
-  const int steps = (a.T + size * kTile - 1) / (size * kTile);
-  BackCursor cursor{a.n_seq, bounds[a.n_seq]};
-  auto look = [&](int buf, int t0) {  // one warp: the bounds of a tile
-    int alive = -1;
-    const bool any = t0 >= 0 && t0 < a.T &&
-                     tile_marks_back(bounds, t0, min(kTile, a.T - t0), s.mark[buf], cursor, alive);
-    if (lane == 0) {
-      s.any[buf] = any;
-      s.alive[buf] = alive;
-    }
-  };
-  in.start(((steps - 1) * size + rank) * kTile + warp * kK);
-  if (steps > 0) in.issue(0, ((steps - 1) * size + rank) * kTile + warp * kK, -size * kTile);
-  if (warp == kLook) look(0, ((steps - 1) * size + rank) * kTile);
-  s.init();
-  cluster_arrive();
-  cluster_wait();
-  f2 carry = both(0.f), dA = both(0.f);
+  const int stride = size * kTile, steps = (a.T + stride - 1) / stride;
   const f2 one = both(1.f), minus = both(-1.f);
-  int turn = 0;
-  for (int step = steps - 1; step >= 0; --step, ++turn) {
-    const int buf = turn & 1;
-    const int t0 = (step * size + rank) * kTile, tw = t0 + warp * kK, left = a.T - tw;
-    f2 h = both(0.f);
-    if (left > 0) h = wide(ld2<VEC>(a.kept + (int64_t)(tw / kK) * a.D + c0, nv));
-    if (step > 0) in.issue(buf ^ 1, tw - size * kTile, -size * kTile);
-    else if (VEC) copies_commit();
-    in.wait();
-    f2 sr[kK], at[kK], m[kK], si[kK], g[kK], hb[kK];
-    bool alone = !gate;
-    if (gate) {
-      float q = 1.f;
-#pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        float p;
-        sigmoids(in.get(buf, 1, k, tw + k), in.get(buf, 2, k, tw + k), sr[k], si[k], p);
-        q = fminf(q, p);
+  f2 dA = both(0.f);
+  s.init();
+  if (warp == kHold) {
+    BackCursor cursor{a.n_seq, bounds[a.n_seq]};
+    auto look = [&](int step) {  // the bounds of a tile
+      const int buf = step & 3, t0 = (steps - 1 - step) * stride + rank * kTile;
+      int alive = -1;
+      const bool any = step < steps && t0 < a.T &&
+                       tile_marks_back(bounds, t0, min(kTile, a.T - t0), s.mark[buf], cursor, alive);
+      if (lane == 0) {
+        s.any[buf] = any;
+        s.alive[buf] = alive;
       }
-      alone = __any_sync(0xffffffffu, q == 0.f);
+      return any;
+    };
+    bool any0 = look(0), any1 = look(1);
+    cluster_arrive();  // every block of the cluster runs before one writes to it
+    cluster_wait();
+    f2 carry = both(0.f);
+    for (int step = 0; step < steps; ++step) {
+      meet(kMaps + (step & 1));
+      const bool any2 = look(step + 2);
+      chain<true>(s, step, any0, carry);
+      any0 = any1;
+      any1 = any2;
+      __syncwarp();
+      arrive(kFronts + (step & 1));
     }
-    if (alone) {
+  } else {
+    const f2 A = load_state(a.A + c0, nv), A2 = mul2(A, both(kLog2e));
+    using In = Tokens<E, VEC, 4, 3>;
+    In in{{reinterpret_cast<const E *>(a.x.p) + cb, reinterpret_cast<const E *>(a.r.p) + cb,
+           a.i.p ? reinterpret_cast<const E *>(a.i.p) + cb : nullptr,
+           reinterpret_cast<const E *>(a.dy.p) + cb},
+          {a.x.st, a.r.st, a.i.st, a.dy.st},
+          raw + warp * 3 * In::kPlace, lane, a.D - cb, nv, a.T};
+    const bool gate = a.i.p;
+    E *dx = reinterpret_cast<E *>(a.dx.p) + c0, *dr = reinterpret_cast<E *>(a.dr.p) + c0;
+    E *di = reinterpret_cast<E *>(a.di.p) + c0;
+    const int first = (steps - 1) * stride + rank * kTile + warp * kK;
+    in.start(first);
+    in.issue(0, steps > 0 ? first : a.T, -stride);
+    in.issue(1, steps > 1 ? first - stride : a.T, -stride);
+    cluster_arrive();
+    cluster_wait();
+
+    auto decay_of = [&](f2 sr) {
+      float lo, hi;
+      unpair(mul2(A2, sr), lo, hi);
+      return pair(ex2(lo), ex2(hi));
+    };
+    // the state that a segment starts from, the gradient of the one it ends with
+    auto origin = [&](int n) {
+      return a.h0 && n < a.n_seq ? load_state(a.h0 + (int64_t)n * a.D + c0, nv) : both(0.f);
+    };
+    auto ending = [&](int n) {
+      return a.dht && n >= 0 && n < a.n_seq ? load_state(a.dht + (int64_t)n * a.D + c0, nv) : both(0.f);
+    };
+    // what a step's tokens have among them; one that ends with the last does not count
+    auto starts_in = [&](int step, int left) {
+      return s.any[step & 3] ? starts_of(s.mark[step & 3] + warp * kK, left, kK + 1) : 0u;
+    };
+    auto hold = [&](int place, int step) {  // the map of the step's tokens, for the chain
+      const int tw = first - step * stride, left = a.T - tw;
+      in.wait();
+      const uint32_t starts = starts_in(step, left);
+      Map mine = {one, both(0.f)};
+      if (starts == 0 && left >= kK) {
+        f2 at[kK];
 #pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        sr[k] = sigmoid2(in.get(buf, 1, k, tw + k));
-        si[k] = gate ? sigmoid2(in.get(buf, 2, k, tw + k)) : one;
-      }
-    }
+        for (int k = 0; k < kK; ++k) at[k] = decay_of(sigmoid2(in.get(place, 1, k, tw + k)));
+        mine = Map{at[kK - 1], mul2(at[kK - 1], in.get(place, 3, kK - 1, tw + kK - 1))};
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      const Token v = token<NORM>(sr[k], A2);
-      at[k] = v.a;
-      m[k] = v.m;
-      g[k] = in.get(buf, 3, k, tw + k);
-    }
-    const bool any = s.any[buf];
-    const int *mark = s.mark[buf] + warp * kK;
-    int seg0 = s.alive[buf];
-    uint32_t starts = 0;  // bit k: a segment starts with token k (of kK + 1)
-    Map mine;
-    if (!any && left >= kK) {
-#pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        hb[k] = h;
-        h = fma2(at[k], h, mul2(m[k], mul2(si[k], in.get(buf, 0, k, tw + k))));
-      }
-      mine = Map{at[kK - 1], mul2(at[kK - 1], g[kK - 1])};
-#pragma unroll
-      for (int k = kK - 2; k >= 0; --k)
-        mine = Map{mul2(mine.A, at[k]), mul2(at[k], add2(g[k], mine.U))};
-    } else {
-      if (any && left > 0) {
-        seg0 = segment_at(s.mark[buf], warp * kK, seg0);
+        for (int k = kK - 2; k >= 0; --k)
+          mine = Map{mul2(mine.A, at[k]), mul2(at[k], add2(in.get(place, 3, k, tw + k), mine.U))};
+      } else if (left > 0) {
+        const int *mark = s.mark[step & 3];
 #pragma unroll 1
-        for (int k = 0; k <= kK; ++k)
-          if (k <= left && mark[k] >= 0) starts |= 1u << k;
-      }
-      // the states before the tokens, and the final states' gradients
-      int seg = seg0;
-#pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        hb[k] = h;
-        if (k >= left) {
-          at[k] = one;
-          g[k] = both(0.f);
-          continue;
+        for (int k = min(kK, left) - 1; k >= 0; --k) {
+          const f2 at = decay_of(sigmoid2(in.get(place, 1, k, tw + k)));
+          f2 g = in.get(place, 3, k, tw + k);
+          if (starts >> (k + 1) & 1) {
+            g = add2(g, ending(segment_at(mark, warp * kK + k, s.alive[step & 3])));
+            mine = Map{both(0.f), mul2(at, g)};
+          } else {
+            mine = Map{mul2(mine.A, at), mul2(at, add2(g, mine.U))};
+          }
         }
-        if (starts >> k & 1) {
-          seg = mark[k];
-          hb[k] = a.h0 && seg < a.n_seq ? load_state(a.h0 + (int64_t)seg * a.D + c0, nv) : both(0.f);
-        }
-        if (starts >> (k + 1) & 1 && seg >= 0 && seg < a.n_seq && a.dht)
-          g[k] = add2(g[k], load_state(a.dht + (int64_t)seg * a.D + c0, nv));
-        h = fma2(at[k], hb[k], mul2(m[k], mul2(si[k], in.get(buf, 0, k, tw + k))));
       }
-      mine = Map{one, both(0.f)};
-#pragma unroll
-      for (int k = kK - 1; k >= 0; --k)
-        mine = starts >> (k + 1) & 1 ? Map{both(0.f), mul2(at[k], g[k])}
-                                     : Map{mul2(mine.A, at[k]), mul2(at[k], add2(g[k], mine.U))};
-    }
-    f2 c = exchange<true>(s, turn, warp, any, mine, carry, [&] { look(buf ^ 1, t0 - size * kTile); });
-    if (left <= 0) continue;
-    const bool inside = !any && left >= kK && seg0 >= 0 && seg0 < a.n_seq;
-#pragma unroll
-    for (int k = kK - 1; k >= 0; --k) {
-      if (k >= left) continue;
-      const bool last = starts >> (k + 1) & 1;
-      const f2 x = in.get(buf, 0, k, tw + k), v = mul2(si[k], x);
-      const f2 G = last ? g[k] : add2(g[k], c);
-      const f2 ga = mul2(G, at[k]), dv = mul2(G, m[k]);
-      f2 past = hb[k];
+      s.warp[step & 1][warp][lane] = packed(mine);
+      __syncwarp();
+      arrive(kMaps + (step & 1));
+    };
+    // The gradients of one token from its parts; G: dL/dh.  Moves dA on.
+    auto grads = [&](f2 G, f2 at, f2 m, f2 sr, f2 si, f2 x, f2 before, f2 &ox, f2 &orr, f2 &oi) {
+      const f2 w = mul2(si, x), dv = mul2(G, m);
+      f2 past = before;
       if (NORM) {
         // the normaliser's part of d/dL; none where a is 1 and it has no derivative
         float lo, hi;
-        unpair(m[k], lo, hi);
-        const f2 ratio = mul2(at[k], pair(lo != 0.f ? rcp(lo) : 0.f, hi != 0.f ? rcp(hi) : 0.f));
-        past = fma2(mul2(v, minus), ratio, past);
+        unpair(m, lo, hi);
+        const f2 ratio = mul2(at, pair(lo != 0.f ? rcp(lo) : 0.f, hi != 0.f ? rcp(hi) : 0.f));
+        past = fma2(mul2(w, minus), ratio, past);
       }
-      const f2 q = mul2(mul2(ga, past), sr[k]);  // dL sr
-      f2 ox = mul2(dv, si[k]), oi = mul2(mul2(dv, v), fma2(si[k], minus, one));
-      f2 orr = mul2(mul2(A, q), fma2(sr[k], minus, one));
-      c = ga;
-      const int64_t t = tw + k;
-      if (inside) {
-        dA = add2(dA, q);
-      } else {
-        const int own = any ? segment_at(mark, k, seg0) : seg0;
+      const f2 q = mul2(mul2(mul2(G, at), past), sr);  // dL sr
+      ox = mul2(dv, si);
+      oi = mul2(mul2(dv, w), fma2(si, minus, one));
+      orr = mul2(mul2(A, q), fma2(sr, minus, one));
+      return q;
+    };
+    auto run = [&](int place, int step) {  // the gradients of the step's tokens
+      const int tw = first - step * stride, left = a.T - tw;
+      f2 h = both(0.f);
+      if (left > 0) h = wide(ld2<VEC>(a.kept + (int64_t)(tw / kK) * a.D + c0, nv));
+      const uint32_t starts = starts_in(step, left);
+      int seg = s.alive[step & 3];
+      if (s.any[step & 3] && left > 0) seg = segment_at(s.mark[step & 3], warp * kK, seg);
+      if (starts == 0 && left >= kK && seg >= 0 && seg < a.n_seq) {
+        f2 sr[kK], si[kK], at[kK], m[kK], hb[kK];
+        bool alone = !gate;
+        if (gate) {
+          float q = 1.f;
+#pragma unroll
+          for (int k = 0; k < kK; ++k) {
+            float p;
+            sigmoids(in.get(place, 1, k, tw + k), in.get(place, 2, k, tw + k), sr[k], si[k], p);
+            q = fminf(q, p);
+          }
+          alone = __any_sync(0xffffffffu, q == 0.f);
+        }
+        if (alone) {
+#pragma unroll
+          for (int k = 0; k < kK; ++k) {
+            sr[k] = sigmoid2(in.get(place, 1, k, tw + k));
+            si[k] = gate ? sigmoid2(in.get(place, 2, k, tw + k)) : one;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          at[k] = decay_of(sr[k]);
+          m[k] = NORM ? root_of(mul2(A2, sr[k]), at[k]) : one;
+          hb[k] = h;
+          h = fma2(at[k], h, mul2(m[k], mul2(si[k], in.get(place, 0, k, tw + k))));
+        }
+        meet(kFronts + (step & 1));
+        f2 c = s.front[step & 1][warp][lane];
+        const int64_t t = tw + kK - 1;
+        E *px = dx + t * a.dx.st, *pr = dr + t * a.dr.st, *pi = di + t * a.di.st;
+#pragma unroll
+        for (int k = kK - 1; k >= 0; --k) {
+          f2 ox, orr, oi;
+          const f2 G = add2(in.get(place, 3, k, tw + k), c);
+          dA = add2(dA, grads(G, at[k], m[k], sr[k], si[k], in.get(place, 0, k, tw + k), hb[k], ox, orr,
+                              oi));
+          c = mul2(at[k], G);
+          store<VEC>(px, ox, nv);
+          store<VEC>(pr, orr, nv);
+          if (gate) store<VEC>(pi, oi, nv);
+          px -= a.dx.st;
+          pr -= a.dr.st;
+          pi -= a.di.st;
+        }
+        return;
+      }
+      // one by one: where a segment starts, before and behind all of them, behind the last token
+      const int *mark = s.mark[step & 3] + warp * kK;
+      f2 hb[kK];  // not in registers
+      auto part = [&](int k, f2 &sr, f2 &si, f2 &at, f2 &m) {
+        sr = sigmoid2(in.get(place, 1, k, tw + k));
+        si = gate ? sigmoid2(in.get(place, 2, k, tw + k)) : one;
+        at = decay_of(sr);
+        m = NORM ? root_of(mul2(A2, sr), at) : one;
+      };
+      f2 sr, si, at, m;
+#pragma unroll 1
+      for (int k = 0; k < min(kK, left); ++k) {
+        if (starts >> k & 1) h = origin(mark[k]);
+        hb[k] = h;
+        part(k, sr, si, at, m);
+        h = fma2(at, h, mul2(m, mul2(si, in.get(place, 0, k, tw + k))));
+      }
+      meet(kFronts + (step & 1));
+      f2 c = s.front[step & 1][warp][lane];
+#pragma unroll 1
+      for (int k = min(kK, left) - 1; k >= 0; --k) {
+        const int own = s.any[step & 3] ? segment_at(mark, k, seg) : seg;
+        part(k, sr, si, at, m);
+        f2 G = in.get(place, 3, k, tw + k), ox, orr, oi;
+        G = starts >> (k + 1) & 1 ? add2(G, ending(own)) : add2(G, c);
+        const f2 q = grads(G, at, m, sr, si, in.get(place, 0, k, tw + k), hb[k], ox, orr, oi);
+        c = mul2(at, G);
         if (own >= 0 && own < a.n_seq) {
           dA = add2(dA, q);
           if (a.dh0 && starts >> k & 1) store_state(a.dh0 + (int64_t)own * a.D + c0, c, nv);
         } else {
           ox = oi = orr = both(0.f);
         }
-      }
-      if (VEC) {
-        in.stage(buf, 0, k, ox);
-        in.stage(buf, 1, k, orr);
-        if (gate) in.stage(buf, 2, k, oi);
-      } else {
+        const int64_t t = tw + k;
         store<VEC>(dx + t * a.dx.st, ox, nv);
         store<VEC>(dr + t * a.dr.st, orr, nv);
         if (gate) store<VEC>(di + t * a.di.st, oi, nv);
       }
+    };
+    if (steps > 0) hold(0, 0);
+    int place = 0;  // of the step that is run
+    auto after = [](int p) { return p == 2 ? 0 : p + 1; };
+#pragma unroll 1
+    for (int step = 0; step < steps; ++step) {
+      const int next = after(place);
+      // the step after next into the place of the one before this
+      in.issue(after(next), step + 2 < steps ? first - (step + 2) * stride : a.T, -stride);
+      if (step + 1 < steps) hold(next, step + 1);
+      run(place, step);
+      place = next;
     }
-    if (VEC) {
-      __syncwarp();
-      in.flush(buf, 0, reinterpret_cast<E *>(a.dx.p) + cb, a.dx.st, tw);
-      in.flush(buf, 1, reinterpret_cast<E *>(a.dr.p) + cb, a.dr.st, tw);
-      if (gate) in.flush(buf, 2, reinterpret_cast<E *>(a.di.p) + cb, a.di.st, tw);
-    }
+    if (VEC) copies_wait<0>();
   }
-  if (VEC) copies_wait<0>();
   // dA: the warps' sums in order, then the blocks' of the cluster
   __syncthreads();
-  s.warp[warp][lane] = packed(Map{dA, both(0.f)});
+  if (warp < kHold) s.warp[0][warp][lane] = packed(Map{dA, both(0.f)});
   __syncthreads();
   if (warp == 0) {
-    f2 v = unpacked(s.warp[0][lane]).A;
+    f2 v = unpacked(s.warp[0][0][lane]).A;
 #pragma unroll
-    for (int w = 1; w < kP; ++w) v = add2(v, unpacked(s.warp[w][lane]).A);
-    put(&s.block[turn & 1][rank][lane], 0, packed(Map{v, both(0.f)}));
+    for (int w = 1; w < kHold; ++w) v = add2(v, unpacked(s.warp[0][w][lane]).A);
+    put(&s.block[steps & 1][rank][lane], 0, packed(Map{v, both(0.f)}));
   }
   cluster_arrive();
   cluster_wait();
   if (rank == 0) {
     if (warp == 0) {
-      f2 v = unpacked(s.block[turn & 1][0][lane]).A;
-      for (int b = 1; b < size; ++b) v = add2(v, unpacked(s.block[turn & 1][b][lane]).A);
+      f2 v = unpacked(s.block[steps & 1][0][lane]).A;
+      for (int b = 1; b < size; ++b) v = add2(v, unpacked(s.block[steps & 1][b][lane]).A);
       store_state(a.dA + c0, v, nv);
     }
     if (a.dh0)
@@ -1080,7 +1057,7 @@ cudaError_t run_clusters(const RecArgs &a, int tile, int smem, cudaStream_t stre
 
 template <typename E, bool VEC, bool OUT, bool NORM>
 cudaError_t run_fwd_as(const RecArgs &a, cudaStream_t stream) {
-  return run_clusters<k_rec_fwd<E, VEC, OUT, NORM>>(a, kFwdTile, Tokens<E, VEC, 3>::kBytes, stream);
+  return run_clusters<k_rec_fwd<E, VEC, OUT, NORM>>(a, kTile, Tokens<E, VEC, 3, 2>::kBytes, stream);
 }
 template <typename E, bool OUT>
 cudaError_t run_fwd(const RecArgs &a, cudaStream_t stream) {
@@ -1099,7 +1076,7 @@ size_t kept_bytes(int64_t T, int32_t D) {
 
 template <typename E, bool VEC, bool NORM>
 cudaError_t run_bwd_as(const RecArgs &a, const int32_t *bounds, cudaStream_t stream) {
-  return run_clusters<k_rec_bwd<E, VEC, NORM>>(a, kTile, Tokens<E, VEC, 4>::kBytes, stream, bounds);
+  return run_clusters<k_rec_bwd<E, VEC, NORM>>(a, kTile, Tokens<E, VEC, 4, 3>::kBytes, stream, bounds);
 }
 
 template <typename E>
