@@ -18,40 +18,17 @@ namespace gdr {
 namespace mix {
 namespace {
 
-// The sum of v over the TPR threads of a row, in all of them.  Up to 32: lanes of a warp; else the
-// whole block, and `phase` names one of two places in red (which the next sum must not share).
+// The sum of v over groups of TPR lanes, in all of them.
 template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float (*red)[32], int phase) {
+__device__ __forceinline__ float lane_sum(float v) {
 #pragma unroll
-  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (TPR > 32) {
-    constexpr int W = TPR / 32;
-    if ((threadIdx.x & 31) == 0) red[phase][threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[phase][0];
-#pragma unroll
-    for (int w = 1; w < W; ++w) v += red[phase][w];
-  }
+  for (int o = TPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 template <int TPR>
-__device__ __forceinline__ float2 row_sum2(float2 v, float2 (*red)[32], int phase) {
-#pragma unroll
-  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
-  if (TPR > 32) {
-    constexpr int W = TPR / 32;
-    if ((threadIdx.x & 31) == 0) red[phase][threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[phase][0];
-#pragma unroll
-    for (int w = 1; w < W; ++w) {
-      v.x += red[phase][w].x;
-      v.y += red[phase][w].y;
-    }
-  }
+__device__ __forceinline__ float2 lane_sum2(float2 v) {
+  v.x = lane_sum<TPR>(v.x);
+  v.y = lane_sum<TPR>(v.y);
   return v;
 }
 
@@ -180,7 +157,7 @@ __global__ void __launch_bounds__(kGated) k_gated_fwd(const GatedArgs a, int64_t
     }
     at.next();
     load();
-    sum = row_sum<TPR>(sum, nullptr, 0);
+    sum = lane_sum<TPR>(sum);
     const float r = rsqrtf(fmaf(sum, inv, a.eps));
     if (!now.ok()) continue;
 #pragma unroll
@@ -247,7 +224,7 @@ __global__ void __launch_bounds__(kGated) k_gated_bwd(const GatedArgs a, int64_t
         sum.x = fmaf(xs[j][k], xs[j][k], sum.x);
         sum.y = fmaf(gs[j][k], xs[j][k], sum.y);
       }
-    sum = row_sum2<TPR>(sum, nullptr, 0);
+    sum = lane_sum2<TPR>(sum);
     const float r = rsqrtf(fmaf(sum.x, inv, a.eps));
     if (!now.ok()) continue;
     const float back = r * r * sum.y * inv;
@@ -342,296 +319,805 @@ cudaError_t run_gated_for(const GatedArgs &a, bool bwd, cudaStream_t stream) {
 }
 
 // ------------------------------------------------------------------ residual norm
+//
+// A row is held by LANES lanes of a warp, several rows side by side, or (LANES 0) by a whole block of as
+// many warps as it fills with NV vectors of 8 columns a thread.  Rows come by cp.async into a ring in
+// which each thread reads only what it copied itself, and stay packed in registers; products are in
+// pairs.
 
-// A row of x and the residual to u (behind the block's norm and without the gate) and h.
-template <int TPR, int NV, bool VEC>
-struct Row {
-  float rx;  // the first norm's factor
-  __device__ __forceinline__ void make(const ResidArgs &a, float (&x)[NV][8], float (&res)[NV][8],
-                                       const int (&n)[NV], int gl, float2 (*red)[32], int &phase) {
-    rx = 1.f;
-    if (a.post) {
-      float2 s = make_float2(0.f, 0.f);
+__device__ __forceinline__ f2 twice(float v) { return pair(v, v); }
+__device__ __forceinline__ float total(f2 v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return lo + hi;
+}
+
+// Sums over the threads of a row, in all of them.  With whole blocks `phase` names one of two places in
+// red (which the next sum must not share).
+template <int LANES>
+__device__ __forceinline__ float2 row_sum2(float2 v, float2 (*red)[32], int &phase) {
+  constexpr int L = LANES ? LANES : 32;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s.x = fmaf(x[j][k], x[j][k], s.x);
-      s = row_sum2<TPR>(s, red, phase);
-      phase ^= 1;
-      rx = rsqrtf(fmaf(s.x, 1.f / a.C, a.eps));
-    }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (gl + j * TPR) * 8;
-      float p[8], g[8];
-      params8<VEC>(a.wp, c, n[j], p);
-      params8<VEC>(a.g, c, n[j], g);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) res[j][k] = fmaf(a.scale * g[k], x[j][k] * rx * p[k], res[j][k]);
-    }
+  for (int o = L / 2; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
   }
-};
-
-template <typename E, typename R, int TPR, int NV, bool VEC>
-__global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_resid_fwd(const ResidArgs a) {
-  after_previous<true>();
-  constexpr int TH = TPR > 128 ? TPR : TPR > 32 ? TPR : 128, RB = TH / TPR;
-  __shared__ float2 red[2][32];
-  const int gl = threadIdx.x % TPR;
-  int n[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) n[j] = max(0, min(8, a.C - (gl + j * TPR) * 8));
-  int phase = 0;
-  const int step = gridDim.x * RB;
-  for (int64_t base = (int64_t)blockIdx.x * RB; base < a.T; base += step) {
-    const int64_t t = base + threadIdx.x / TPR;
-    const bool ok = t < a.T;
-    float x[NV][8], h[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (gl + j * TPR) * 8, m = ok ? n[j] : 0;
-      unpack8(ld8<VEC>(reinterpret_cast<const E *>(a.x.p) + t * a.x.st + c, m), x[j]);
-      unpack8(a.res.p ? ld8<VEC>(reinterpret_cast<const R *>(a.res.p) + t * a.res.st + c, m)
-                      : zero8<R>(),
-              h[j]);
+  if (LANES == 0) {
+    const int warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) red[phase][threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = red[phase][0];
+    for (int w = 1; w < warps; ++w) {
+      v.x += red[phase][w].x;
+      v.y += red[phase][w].y;
     }
-    Row<TPR, NV, VEC> row;
-    row.make(a, x, h, n, gl, red, phase);
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s.x = k < n[j] ? fmaf(h[j][k], h[j][k], s.x) : s.x;
-    s = row_sum2<TPR>(s, red, phase);
     phase ^= 1;
-    const float r = rsqrtf(fmaf(s.x, 1.f / a.C, a.eps));
-    if (!ok) continue;
+  }
+  return v;
+}
+
+// 8 parameters from column c on in pairs; null: ones.
+template <bool VEC>
+__device__ __forceinline__ void params4(const Param &w, int64_t c, int n, f2 (&f)[4]) {
+  float v[8];
+  params8<VEC>(w, c, n, v);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (gl + j * TPR) * 8;
-      if (a.h.p)
-        st8<VEC>(reinterpret_cast<R *>(a.h.p) + t * a.h.st + c, pack8(h[j], R{}), n[j]);
-      float w[8];
-      params8<VEC>(a.w, c, n[j], w);
+  for (int i = 0; i < 4; ++i) f[i] = pair(v[2 * i], v[2 * i + 1]);
+}
+// Columns behind the row's end (their parameters are zeros, or ones where there are none): zeros.
+__device__ __forceinline__ void keep(f2 (&f)[4], int n) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) h[j][k] *= r * w[k];
-      st8<VEC>(reinterpret_cast<E *>(a.y.p) + t * a.y.st + c, pack8(h[j], E{}), n[j]);
-    }
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpair(f[i], lo, hi);
+    f[i] = pair(2 * i < n ? lo : 0.f, 2 * i + 1 < n ? hi : 0.f);
   }
 }
 
-// The rows of a block on their way into shared memory, `depth` of them: each thread reads only what
-// it copied itself.  Without 16-byte alignment, and where a row is too long (fp32, over 8,192 columns),
-// rows are loaded when they are used.
-template <typename E, typename R, int TPR, int NV, bool VEC, int TH>
-struct Rows4 {
-  static constexpr int PE = sizeof(E) / 2, PR = sizeof(R) / 2, U = 2 * NV * (PE + PR);
-  static constexpr bool kRing = VEC && U * TH * 16 <= 200 * 1024;
+// A thread's columns of one row.
+template <int LANES, int NV>
+struct Cols {
+  int gl, tpr, group, groups;
+  int n[NV];
+  __device__ __forceinline__ Cols(int C) {
+    tpr = LANES ? LANES : blockDim.x;
+    gl = threadIdx.x % tpr;
+    group = threadIdx.x / tpr;
+    groups = blockDim.x / tpr;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) n[j] = max(0, min(8, C - at(j)));
+  }
+  __device__ __forceinline__ int at(int j) const { return (gl + j * tpr) * 8; }
+};
+
+// The rows of N tensors on their way into shared memory, `depth` of them.  Without 16-byte alignment,
+// and where a row is too long for it (ring null), rows are loaded when they are used.
+template <typename E, typename R, int NV, bool VEC>
+struct Ring {
+  static constexpr int PE = sizeof(E) / 2, PR = sizeof(R) / 2;
   uint4 *ring;
-  template <typename X, int P>
+  int units;  // 16-byte parts of a thread's row
+  __device__ __forceinline__ uint4 *place(int s, int unit) const {
+    return ring + (s * units + unit) * blockDim.x + threadIdx.x;
+  }
+  template <typename X>
   __device__ __forceinline__ void copy(int s, int unit, const Mat &m, int64_t t, int c) const {
     const X *p = reinterpret_cast<const X *>(m.p) + t * m.st + c;
 #pragma unroll
-    for (int i = 0; i < P; ++i) copy16(ring + (s * U + unit + i) * TH + threadIdx.x, p + i * (16 / sizeof(X)));
+    for (int i = 0; i < (int)sizeof(X) / 2; ++i) copy16(place(s, unit + i), p + i * (16 / sizeof(X)));
   }
-  __device__ __forceinline__ void issue(const ResidArgs &a, int s, int64_t t, const int (&n)[NV],
-                                        int gl) const {
-    if (kRing) {
+  template <typename X>
+  __device__ __forceinline__ Raw8<X> get(int s, int unit, const Mat &m, int64_t t, int c, int n) const {
+    Raw8<X> r = zero8<X>();
+    if (!m.p) return r;
+    if (VEC && ring) {
+      uint4 *w = reinterpret_cast<uint4 *>(&r);
+      if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(X) / 2; ++i) w[i] = *place(s, unit + i);
+      }
+    } else {
+      r = ld8<VEC>(reinterpret_cast<const X *>(m.p) + t * m.st + c, n);
+    }
+    return r;
+  }
+  // x, residual (, dy, dh): the first unit of each tensor's vector j
+  __device__ __forceinline__ int x(int j) const { return j * PE; }
+  __device__ __forceinline__ int res(int j) const { return NV * PE + j * PR; }
+  __device__ __forceinline__ int dy(int j) const { return NV * (PE + PR) + j * PE; }
+  __device__ __forceinline__ int dh(int j) const { return NV * (2 * PE + PR) + j * PR; }
+  template <bool BWD, int LANES>
+  __device__ __forceinline__ void issue(const ResidArgs &a, int s, int64_t t,
+                                        const Cols<LANES, NV> &cols) const {
+    if (VEC && ring) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (gl + j * TPR) * 8;
-        if (t < a.T && n[j] > 0) {
-          copy<E, PE>(s, j * PE, a.x, t, c);
-          copy<E, PE>(s, (NV + j) * PE, a.dy, t, c);
-          if (a.res.p) copy<R, PR>(s, 2 * NV * PE + j * PR, a.res, t, c);
-          if (a.dh.p) copy<R, PR>(s, 2 * NV * PE + (NV + j) * PR, a.dh, t, c);
+        const int c = cols.at(j);
+        if (t < a.T && cols.n[j] > 0) {
+          copy<E>(s, x(j), a.x, t, c);
+          if (a.res.p) copy<R>(s, res(j), a.res, t, c);
+          if (BWD) copy<E>(s, dy(j), a.dy, t, c);
+          if (BWD && a.dh.p) copy<R>(s, dh(j), a.dh, t, c);
         }
       }
       copies_commit();
     }
   }
-  template <typename X, int P>
-  __device__ __forceinline__ Raw8<X> get(int s, int unit, const Mat &m, int64_t t, int c, int n) const {
-    Raw8<X> r = zero8<X>();
-    if (kRing) {
-      uint4 *w = reinterpret_cast<uint4 *>(&r);
-      if (m.p && n > 0) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) w[i] = ring[(s * U + unit + i) * TH + threadIdx.x];
-      }
-    } else if (m.p) {
-      r = ld8<VEC>(reinterpret_cast<const X *>(m.p) + t * m.st + c, n);
-    }
-    return r;
-  }
-};
-
-template <typename E, typename R, int TPR, int NV, bool VEC>
-__global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_resid_bwd(const ResidArgs a, int depth) {
-  after_previous();
-  constexpr int TH = TPR > 32 ? TPR : 128, RB = TH / TPR;
-  extern __shared__ __align__(16) uint4 ring[];
-  __shared__ float2 red[2][32];
-  const Rows4<E, R, TPR, NV, VEC, TH> in{ring};
-  using I = Rows4<E, R, TPR, NV, VEC, TH>;
-  const int gl = threadIdx.x % TPR, group = threadIdx.x / TPR;
-  int n[NV];
-  float dw[NV][8], dp[NV][8], dg[NV][8];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    n[j] = max(0, min(8, a.C - (gl + j * TPR) * 8));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) dw[j][k] = dp[j][k] = dg[j][k] = 0.f;
-  }
-  const int step = gridDim.x * RB;
-  const int64_t first = (int64_t)blockIdx.x * RB + group;
-  for (int s = 0; s < depth - 1; ++s) in.issue(a, s, first + (int64_t)s * step, n, gl);
-  int phase = 0, stage = 0;
-  const float inv = 1.f / a.C;
-  for (int64_t base = (int64_t)blockIdx.x * RB; base < a.T; base += step) {
-    const int64_t t = base + group;
-    const bool ok = t < a.T;
-    // into the place of the row before; the oldest of `depth` rows is there then
-    in.issue(a, stage == 0 ? depth - 1 : stage - 1, t + (int64_t)(depth - 1) * step, n, gl);
-    if (I::kRing) {
-      if (depth == 3) copies_wait<2>();
+  __device__ __forceinline__ void wait(int depth) const {  // the oldest of `depth` rows is there
+    if (VEC && ring) {
+      if (depth >= 4) copies_wait<3>();
+      else if (depth == 3) copies_wait<2>();
       else if (depth == 2) copies_wait<1>();
       else copies_wait<0>();
     }
-    float x[NV][8], h[NV][8], dy[NV][8], dh[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (gl + j * TPR) * 8, m = ok ? n[j] : 0;
-      unpack8(in.template get<E, I::PE>(stage, j * I::PE, a.x, t, c, m), x[j]);
-      unpack8(in.template get<E, I::PE>(stage, (NV + j) * I::PE, a.dy, t, c, m), dy[j]);
-      unpack8(in.template get<R, I::PR>(stage, 2 * NV * I::PE + j * I::PR, a.res, t, c, m), h[j]);
-      unpack8(in.template get<R, I::PR>(stage, 2 * NV * I::PE + (NV + j) * I::PR, a.dh, t, c, m), dh[j]);
-    }
-    stage = stage + 1 == depth ? 0 : stage + 1;
-    Row<TPR, NV, VEC> row;
-    row.make(a, x, h, n, gl, red, phase);
-    float2 s = make_float2(0.f, 0.f);
-    float w[8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      params8<VEC>(a.w, (gl + j * TPR) * 8, n[j], w);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < n[j]) {
-          s.x = fmaf(h[j][k], h[j][k], s.x);
-          s.y = fmaf(dy[j][k] * w[k], h[j][k], s.y);
-        }
-    }
-    s = row_sum2<TPR>(s, red, phase);
-    phase ^= 1;
-    const float r = rsqrtf(fmaf(s.x, inv, a.eps)), back = r * r * s.y * inv;
-    float2 q = make_float2(0.f, 0.f);
-    if (ok) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (gl + j * TPR) * 8;
-      float p[8], g[8];
-      params8<VEC>(a.w, c, n[j], w);
-      params8<VEC>(a.wp, c, n[j], p);
-      params8<VEC>(a.g, c, n[j], g);
-      float e[8];
-      if (TPR == 1) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] = k < n[j] ? dy[j][k] * w[k] : 0.f;
-        row_back(h[j], e, a.C, a.eps, e);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        dw[j][k] = fmaf(dy[j][k], h[j][k] * r, dw[j][k]);
-        dh[j][k] = TPR > 1 ? fmaf(r, fmaf(-h[j][k], back, dy[j][k] * w[k]), dh[j][k]) : dh[j][k] + e[k];
-        const float dv = a.scale * dh[j][k], xn = x[j][k] * row.rx, du = dv * g[k];
-        dg[j][k] = fmaf(dv, xn * p[k], dg[j][k]);
-        dp[j][k] = fmaf(du, xn, dp[j][k]);
-        dy[j][k] = du * p[k];  // with the norm behind the block: e
-        if (k < n[j]) q.x = fmaf(dy[j][k], x[j][k], q.x);
-      }
-      if (a.dres.p)
-        st8<VEC>(reinterpret_cast<R *>(a.dres.p) + t * a.dres.st + c, pack8(dh[j], R{}), n[j]);
-    }
-    }
-    float bx = 0.f;
-    if (a.post) {
-      q = row_sum2<TPR>(q, red, phase);
-      phase ^= 1;
-      bx = row.rx * row.rx * q.x * inv;
-    }
-    if (!ok) continue;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (TPR > 1) dy[j][k] = row.rx * fmaf(-x[j][k], bx, dy[j][k]);
-      if (TPR == 1 && a.post) row_back(x[j], dy[j], a.C, a.eps, dy[j]);
-      st8<VEC>(reinterpret_cast<E *>(a.dx.p) + t * a.dx.st + (gl + j * TPR) * 8, pack8(dy[j], E{}),
-               n[j]);
-    }
   }
-  if (I::kRing) copies_wait<0>();
-  // the block's parts of dw, dw_post and dgate, its row groups in order
-  float *out = reinterpret_cast<float *>(a.work) + (int64_t)blockIdx.x * 3 * a.C;
-  if (RB == 1) {
+};
+
+// u (behind the block's norm, without the gate) enters the residual: h.  Returns the norm's factor.
+template <typename E, int LANES, int NV, bool VEC>
+__device__ __forceinline__ float make_h(const ResidArgs &a, const Raw8<E> (&x)[NV], f2 (&h)[NV][4],
+                                        const Cols<LANES, NV> &cols, float2 (*red)[32], int &phase) {
+  float rx = 1.f;
+  if (a.post) {
+    f2 q = twice(0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      f2 v[4];
+      unpack4(x[j], v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q = fma2(v[i], v[i], q);
+    }
+    rx = rsqrtf(fmaf(row_sum2<LANES>(make_float2(total(q), 0.f), red, phase).x, 1.f / a.C, a.eps));
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    f2 v[4], p[4];
+    unpack4(x[j], v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], twice(a.scale * rx));
+    if (a.wp.p) {
+      params4<VEC>(a.wp, cols.at(j), cols.n[j], p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], p[i]);
+    }
+    if (a.g.p) {
+      params4<VEC>(a.g, cols.at(j), cols.n[j], p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[j][i] = fma2(v[i], p[i], h[j][i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[j][i] = add2(v[i], h[j][i]);
+    }
+    if (cols.n[j] < 8) keep(h[j], cols.n[j]);
+  }
+  return rx;
+}
+
+constexpr int kResidMost = 512;  // threads of a block
+
+template <typename E, typename R, int LANES, int NV, bool VEC>
+__global__ void __launch_bounds__(LANES ? 128 : kResidMost, LANES ? 1 : 2)
+    k_resid_fwd_long(const ResidArgs a, int depth) {
+  after_previous<true>();
+  extern __shared__ __align__(16) uint4 ring[];
+  __shared__ float2 red[2][32];
+  const Cols<LANES, NV> cols(a.C);
+  using I = Ring<E, R, NV, VEC>;
+  const I in{depth ? ring : nullptr, NV * (I::PE + I::PR)};
+  const int step = gridDim.x * cols.groups;
+  const int64_t first = (int64_t)blockIdx.x * cols.groups + cols.group;
+  for (int s = 0; s < depth - 1; ++s) in.template issue<false>(a, s, first + (int64_t)s * step, cols);
+  int phase = 0, stage = 0;
+  for (int64_t base = (int64_t)blockIdx.x * cols.groups; base < a.T; base += step) {
+    const int64_t t = base + cols.group;
+    const bool ok = t < a.T;
+    if (depth) {
+      in.template issue<false>(a, stage == 0 ? depth - 1 : stage - 1, t + (int64_t)(depth - 1) * step, cols);
+      in.wait(depth);
+    }
+    Raw8<E> x[NV];
+    f2 h[NV][4];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int m = ok ? cols.n[j] : 0;
+      x[j] = in.template get<E>(stage, in.x(j), a.x, t, cols.at(j), m);
+      unpack4(in.template get<R>(stage, in.res(j), a.res, t, cols.at(j), m), h[j]);
+    }
+    stage = stage + 1 >= depth ? 0 : stage + 1;
+    make_h<E, LANES, NV, VEC>(a, x, h, cols, red, phase);
+    f2 q = twice(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < n[j]) {
-          const int c = (gl + j * TPR) * 8 + k;
-          if (a.dw) out[c] = dw[j][k];
-          if (a.dwp) out[a.C + c] = dp[j][k];
-          if (a.dg) out[2 * a.C + c] = dg[j][k];
+      for (int i = 0; i < 4; ++i) q = fma2(h[j][i], h[j][i], q);
+    const float2 s = row_sum2<LANES>(make_float2(total(q), 0.f), red, phase);
+    const float r = rsqrtf(fmaf(s.x, 1.f / a.C, a.eps));
+    if (!ok) continue;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = cols.at(j);
+      if (a.h.p)
+        st8<VEC>(reinterpret_cast<R *>(a.h.p) + t * a.h.st + c, pack4<R>(h[j]), cols.n[j]);
+      f2 w[4];
+      params4<VEC>(a.w, c, cols.n[j], w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[j][i] = mul2(mul2(h[j][i], twice(r)), w[i]);
+      st8<VEC>(reinterpret_cast<E *>(a.y.p) + t * a.y.st + c, pack4<E>(h[j]), cols.n[j]);
+    }
+  }
+  if (VEC) copies_wait<0>();
+}
+
+// r (e - n mean(e n)) for a row of up to 8 columns in one thread (row_back), in pairs
+__device__ __forceinline__ void row_back(const f2 (&x)[4], const f2 (&e)[4], int columns, float eps,
+                                         f2 (&out)[4]) {
+  float xs[8], es[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    unpair(x[i], xs[2 * i], xs[2 * i + 1]);
+    unpair(e[i], es[2 * i], es[2 * i + 1]);
+  }
+  row_back(xs, es, columns, eps, es);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = pair(es[2 * i], es[2 * i + 1]);
+}
+
+template <typename E, typename R, int LANES, int NV, bool VEC>
+__global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_long(const ResidArgs a, int depth) {
+  after_previous();
+  extern __shared__ __align__(16) uint4 ring[];
+  __shared__ float2 red[2][32];
+  const Cols<LANES, NV> cols(a.C);
+  using I = Ring<E, R, NV, VEC>;
+  const I in{depth ? ring : nullptr, 2 * NV * (I::PE + I::PR)};
+  f2 dw[NV][4], dp[NV][4], dg[NV][4];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dw[j][i] = dp[j][i] = dg[j][i] = twice(0.f);
+  const int step = gridDim.x * cols.groups;
+  const int64_t first = (int64_t)blockIdx.x * cols.groups + cols.group;
+  for (int s = 0; s < depth - 1; ++s) in.template issue<true>(a, s, first + (int64_t)s * step, cols);
+  int phase = 0, stage = 0;
+  const float inv = 1.f / a.C;
+  for (int64_t base = (int64_t)blockIdx.x * cols.groups; base < a.T; base += step) {
+    const int64_t t = base + cols.group;
+    const bool ok = t < a.T;
+    if (depth) {  // into the place of the row before
+      in.template issue<true>(a, stage == 0 ? depth - 1 : stage - 1, t + (int64_t)(depth - 1) * step, cols);
+      in.wait(depth);
+    }
+    Raw8<E> x[NV], dy[NV];
+    f2 h[NV][4];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int m = ok ? cols.n[j] : 0;
+      x[j] = in.template get<E>(stage, in.x(j), a.x, t, cols.at(j), m);
+      dy[j] = in.template get<E>(stage, in.dy(j), a.dy, t, cols.at(j), m);
+      unpack4(in.template get<R>(stage, in.res(j), a.res, t, cols.at(j), m), h[j]);
+    }
+    const float rx = make_h<E, LANES, NV, VEC>(a, x, h, cols, red, phase);
+    f2 q = twice(0.f), p = twice(0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      f2 w[4], e[4];
+      params4<VEC>(a.w, cols.at(j), cols.n[j], w);
+      unpack4(dy[j], e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        q = fma2(h[j][i], h[j][i], q);
+        p = fma2(mul2(e[i], w[i]), h[j][i], p);
+      }
+    }
+    const float2 s = row_sum2<LANES>(make_float2(total(q), total(p)), red, phase);
+    const float r = rsqrtf(fmaf(s.x, inv, a.eps)), back = r * r * s.y * inv;
+    q = twice(0.f);
+    f2 du[NV][4];  // the gradient behind the gate; with the norm behind the block, times its weight
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = cols.at(j);
+        f2 w[4], e[4], g[4], xs[4];
+        params4<VEC>(a.w, c, cols.n[j], w);
+        unpack4(dy[j], e);
+        unpack4(in.template get<R>(stage, in.dh(j), a.dh, t, c, cols.n[j]), g);
+        unpack4(x[j], xs);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dw[j][i] = fma2(e[i], mul2(h[j][i], twice(r)), dw[j][i]);
+          e[i] = mul2(e[i], w[i]);
         }
+        if (LANES == 1) {
+          row_back(h[j], e, a.C, a.eps, e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) g[i] = add2(g[i], e[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            g[i] = fma2(twice(r), fma2(h[j][i], twice(-back), e[i]), g[i]);
+        }
+        if (a.dres.p)
+          st8<VEC>(reinterpret_cast<R *>(a.dres.p) + t * a.dres.st + c, pack4<R>(g), cols.n[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          g[i] = mul2(g[i], twice(a.scale));
+          e[i] = mul2(xs[i], twice(rx));
+        }
+        if (a.wp.p) {
+          params4<VEC>(a.wp, c, cols.n[j], w);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = twice(1.f);
+        }
+        if (a.g.p) {
+          f2 gate[4];
+          params4<VEC>(a.g, c, cols.n[j], gate);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dg[j][i] = fma2(g[i], mul2(e[i], w[i]), dg[j][i]);
+            g[i] = mul2(g[i], gate[i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dp[j][i] = fma2(g[i], e[i], dp[j][i]);
+          du[j][i] = mul2(g[i], w[i]);
+        }
+        if (a.post) {
+          if (cols.n[j] < 8) keep(du[j], cols.n[j]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q = fma2(du[j][i], xs[i], q);
+        }
+      }
+    }
+    stage = stage + 1 >= depth ? 0 : stage + 1;
+    float bx = 0.f;
+    if (a.post) bx = rx * rx * row_sum2<LANES>(make_float2(total(q), 0.f), red, phase).x * inv;
+    if (!ok) continue;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      f2 xs[4];
+      unpack4(x[j], xs);
+      if (LANES == 1 && a.post) {
+        row_back(xs, du[j], a.C, a.eps, du[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) du[j][i] = mul2(twice(rx), fma2(xs[i], twice(-bx), du[j][i]));
+      }
+      st8<VEC>(reinterpret_cast<E *>(a.dx.p) + t * a.dx.st + cols.at(j), pack4<E>(du[j]), cols.n[j]);
+    }
+  }
+  if (VEC) copies_wait<0>();
+  // the block's parts of dw, dw_post and dgate, its row groups in order
+  float *out = reinterpret_cast<float *>(a.work) + (int64_t)blockIdx.x * 3 * a.C;
+  if (LANES == 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f2 v[3] = {dw[j][i], dp[j][i], dg[j][i]};
+#pragma unroll
+        for (int b = 0; b < 3; ++b) {
+          if (!(b == 0 ? a.dw : b == 1 ? a.dwp : a.dg)) continue;
+          float lo, hi;
+          unpair(v[b], lo, hi);
+          float *to = out + (int64_t)b * a.C + cols.at(j) + 2 * i;
+          if (2 * i < cols.n[j]) to[0] = lo;
+          if (2 * i + 1 < cols.n[j]) to[1] = hi;
+        }
+      }
   } else {
-    __shared__ float sums[RB == 1 ? 1 : RB * TPR * NV * 8];
-    constexpr int L = TPR * NV * 8;
-    for (int i = 0; i < 3; ++i) {
-      if (!(i == 0 ? a.dw : i == 1 ? a.dwp : a.dg)) continue;
+    constexpr int L = (LANES ? LANES : 1) * NV * 8;
+    __shared__ float sums[LANES ? 128 / (LANES ? LANES : 1) * L : 1];
+    for (int b = 0; b < 3; ++b) {
+      if (!(b == 0 ? a.dw : b == 1 ? a.dwp : a.dg)) continue;
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          sums[group * L + (gl + j * TPR) * 8 + k] = i == 0 ? dw[j][k] : i == 1 ? dp[j][k] : dg[j][k];
+        for (int i = 0; i < 4; ++i) {
+          float *to = &sums[cols.group * L + cols.at(j) + 2 * i];
+          unpair(b == 0 ? dw[j][i] : b == 1 ? dp[j][i] : dg[j][i], to[0], to[1]);
+        }
       __syncthreads();
-      for (int c = threadIdx.x; c < a.C; c += TH) {
+      for (int c = threadIdx.x; c < a.C; c += 128) {
         float v = sums[c];
-#pragma unroll
-        for (int g = 1; g < RB; ++g) v += sums[g * L + c];
-        out[i * a.C + c] = v;
+        for (int g = 1; g < 128 / (LANES ? LANES : 1); ++g) v += sums[g * L + c];
+        out[(int64_t)b * a.C + c] = v;
       }
     }
   }
 }
 
-// Blocks of the backward: as many as run at once; each leaves one row of parts.
-constexpr int resid_per_sm(int threads) { return threads >= 512 ? 1 : threads >= 256 ? 2 : 4; }
+// ------------------------------------------------------------------ rows of up to 8,192 columns
+//
+// One vector of 8 columns a thread, whose parameters stay in registers, and NR rows at a time, which
+// share the exchanges between warps.
 
-template <typename E, typename R, int TPR, int NV, bool VEC>
+// Sums of K values over the threads of a row, in all of them: a butterfly in which half of the values
+// change places while there is more than one, and for whole blocks the same once more over the
+// warps' sums.
+// The values from `from` to `to` count, the others come out as anything.
+template <int LANES, int K>
+__device__ __forceinline__ void row_sums(float (&v)[K], float (*red)[32 * 4], int &phase, int from = 0,
+                                         int to = K) {
+  static_assert(K == 1 || K == 2 || K == 4, "values");
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (k < from || k >= to) v[k] = 0.f;
+  constexpr int L = LANES ? LANES : 32;
+  const int lane = threadIdx.x & 31;
+  if (LANES) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    return;
+  }
+  float m = v[0];  // value lane % K, summed over more and more lanes
+  if (K == 4) {
+    const bool up = lane & 2;
+    const float a = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 2);
+    const float b = (up ? v[K - 1] : v[K > 1 ? 1 : 0]) +
+                    __shfl_xor_sync(0xffffffffu, up ? v[K > 1 ? 1 : 0] : v[K - 1], 2);
+    m = (lane & 1 ? b : a) + __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+  } else if (K == 2) {
+    m = (lane & 1 ? v[K - 1] : v[0]) + __shfl_xor_sync(0xffffffffu, lane & 1 ? v[0] : v[K - 1], 1);
+  }
+#pragma unroll
+  for (int o = K; o < 32; o <<= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+  const int warps = blockDim.x >> 5;
+  if (lane < K) red[phase][(threadIdx.x >> 5) * K + lane] = m;
+  __syncthreads();
+  m = 0.f;
+  for (int i = lane; i < warps * K; i += 32) m += red[phase][i];
+#pragma unroll
+  for (int o = K; o < 32; o <<= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, m, k);
+  phase ^= 1;
+}
+
+// A thread's parameters: weight, post_weight, and scale times gate; zeros behind the last column.
+struct Params {
+  f2 w[4], p[4], g[4];
+  __device__ __forceinline__ Params(const ResidArgs &a, int c, int n) {
+    params4<true>(a.w, c, n, w);
+    params4<true>(a.wp, c, n, p);
+    params4<true>(a.g, c, n, g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i] = n > 0 ? mul2(g[i], twice(a.scale)) : twice(0.f);
+  }
+};
+
+// The rows of a step: x, residual (, dy, dh) of NR rows, one vector a thread.
+template <typename E, typename R, int NR, bool BWD>
+struct Ahead {
+  static constexpr int PE = sizeof(E) / 2, PR = sizeof(R) / 2;
+  static constexpr int kX = 0, kRes = PE, kDy = PE + PR, kDh = 2 * PE + PR;
+  static constexpr int kRow = (BWD ? 2 : 1) * (PE + PR), kUnits = NR * kRow;
+  uint4 *ring;
+  const ResidArgs &a;
+  int c, n;
+  __device__ __forceinline__ uint4 *place(int s, int r, int unit) const {
+    return ring + (s * kUnits + r * kRow + unit) * blockDim.x + threadIdx.x;
+  }
+  template <typename X>
+  __device__ __forceinline__ void copy(int s, int r, int unit, const Mat &m, int64_t t) const {
+    const X *p = reinterpret_cast<const X *>(m.p) + t * m.st + c;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(X) / 2; ++i) copy16(place(s, r, unit + i), p + i * (16 / sizeof(X)));
+  }
+  __device__ __forceinline__ void issue(int s, int64_t t) const {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      if (t + r < a.T && n > 0) {
+        copy<E>(s, r, kX, a.x, t + r);
+        if (a.res.p) copy<R>(s, r, kRes, a.res, t + r);
+        if (BWD) copy<E>(s, r, kDy, a.dy, t + r);
+        if (BWD && a.dh.p) copy<R>(s, r, kDh, a.dh, t + r);
+      }
+    }
+    copies_commit();
+  }
+  __device__ __forceinline__ void wait(int depth) const {  // the oldest of `depth` steps is there
+    if (depth >= 4) copies_wait<3>();
+    else if (depth == 3) copies_wait<2>();
+    else if (depth == 2) copies_wait<1>();
+    else copies_wait<0>();
+  }
+  template <typename X>
+  __device__ __forceinline__ Raw8<X> get(int s, int r, int unit, bool there) const {
+    Raw8<X> v = zero8<X>();
+    uint4 *w = reinterpret_cast<uint4 *>(&v);
+    if (there) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(X) / 2; ++i) w[i] = *place(s, r, unit + i);
+    }
+    return v;
+  }
+};
+
+// The sums of x^2 over this thread's columns of a step's rows, from the ring.
+template <typename E, typename In, int NR>
+__device__ __forceinline__ void squares(const In &in, int s, int64_t t, float *sum) {
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    f2 v[4], q = twice(0.f);
+    unpack4(in.template get<E>(s, r, In::kX, t + r < in.a.T && in.n > 0), v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q = fma2(v[i], v[i], q);
+    sum[r] = total(q);
+  }
+}
+
+// Both kernels take the first norm's sums of the step after this one along with this one's last sums:
+// one exchange less a step.
+
+template <typename E, typename R, int LANES, int NR>
+__global__ void __launch_bounds__(LANES ? 128 : 1024, 1) k_resid_fwd(const ResidArgs a, int depth) {
+  after_previous<true>();
+  extern __shared__ __align__(16) uint4 ring[];
+  __shared__ float red[2][32 * 4];
+  const Cols<LANES, 1> cols(a.C);
+  const int c = cols.at(0), n = cols.n[0];
+  using In = Ahead<E, R, NR, false>;
+  const In in{ring, a, c, n};
+  const int step = gridDim.x * cols.groups * NR;
+  const int64_t first = ((int64_t)blockIdx.x * cols.groups + cols.group) * NR;
+  for (int s = 0; s < depth - 1; ++s) in.issue(s, first + (int64_t)s * step);
+  const Params par(a, c, n);
+  int phase = 0, stage = 0;
+  const float inv = 1.f / a.C;
+  float sum[2 * NR];  // of h^2, and of x^2 in the next step
+  in.wait(depth - 1);
+  if (a.post) {
+    squares<E, In, NR>(in, 0, first, sum + NR);
+    row_sums<LANES, 2 * NR>(sum, red, phase, NR);
+  }
+  for (int64_t base = (int64_t)blockIdx.x * cols.groups * NR; base < a.T; base += step) {
+    const int64_t t = base + cols.group * NR;
+    in.issue(stage == 0 ? depth - 1 : stage - 1, t + (int64_t)(depth - 1) * step);
+    f2 h[NR][4];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const bool there = t + r < a.T && n > 0;
+      const float rx = a.post ? rsqrtf(fmaf(sum[NR + r], inv, a.eps)) : 1.f;
+      f2 v[4], q = twice(0.f);
+      unpack4(in.template get<E>(stage, r, In::kX, there), v);
+      unpack4(in.template get<R>(stage, r, In::kRes, there && a.res.p), h[r]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[r][i] = fma2(mul2(mul2(v[i], twice(rx)), par.p[i]), par.g[i], h[r][i]);
+        q = fma2(h[r][i], h[r][i], q);
+      }
+      sum[r] = n > 0 ? total(q) : 0.f;
+    }
+    stage = stage + 1 == depth ? 0 : stage + 1;
+    in.wait(depth - 1);
+    if (a.post) {
+      squares<E, In, NR>(in, stage, t + step, sum + NR);
+      row_sums<LANES, 2 * NR>(sum, red, phase);
+    } else {
+      row_sums<LANES, 2 * NR>(sum, red, phase, 0, NR);
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      if (t + r >= a.T || n <= 0) continue;
+      if (a.h.p)
+        st8<true>(reinterpret_cast<R *>(a.h.p) + (t + r) * a.h.st + c, pack4<R>(h[r]), 8);
+      const float f = rsqrtf(fmaf(sum[r], inv, a.eps));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[r][i] = mul2(mul2(h[r][i], twice(f)), par.w[i]);
+      st8<true>(reinterpret_cast<E *>(a.y.p) + (t + r) * a.y.st + c, pack4<E>(h[r]), 8);
+    }
+  }
+  copies_wait<0>();
+}
+
+template <typename E, typename R, int LANES, int NR>
+__global__ void __launch_bounds__(LANES ? 128 : 512, 1) k_resid_bwd(const ResidArgs a, int depth) {
+  after_previous();
+  extern __shared__ __align__(16) uint4 ring[];
+  __shared__ float red[2][32 * 4];
+  const Cols<LANES, 1> cols(a.C);
+  const int c = cols.at(0), n = cols.n[0];
+  using In = Ahead<E, R, NR, true>;
+  const In in{ring, a, c, n};
+  const int step = gridDim.x * cols.groups * NR;
+  const int64_t first = ((int64_t)blockIdx.x * cols.groups + cols.group) * NR;
+  for (int s = 0; s < depth - 1; ++s) in.issue(s, first + (int64_t)s * step);
+  const Params par(a, c, n);
+  f2 dw[4], dp[4], dg[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dw[i] = dp[i] = dg[i] = twice(0.f);
+  int phase = 0, stage = 0;
+  const float inv = 1.f / a.C;
+  float last[2 * NR];  // the sums of the norm behind the block, and of x^2 in the next step
+  in.wait(depth - 1);
+  if (a.post) {
+    squares<E, In, NR>(in, 0, first, last + NR);
+    row_sums<LANES, 2 * NR>(last, red, phase, NR);
+  }
+  for (int64_t base = (int64_t)blockIdx.x * cols.groups * NR; base < a.T; base += step) {
+    const int64_t t = base + cols.group * NR;
+    in.issue(stage == 0 ? depth - 1 : stage - 1, t + (int64_t)(depth - 1) * step);
+    f2 h[NR][4];  // then the gradient behind the gate; with the norm behind the block, times its weight
+    float sum[2 * NR], rx[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const bool there = t + r < a.T && n > 0;
+      rx[r] = a.post ? rsqrtf(fmaf(last[NR + r], inv, a.eps)) : 1.f;
+      f2 v[4], e[4], q = twice(0.f), p = twice(0.f);
+      unpack4(in.template get<E>(stage, r, In::kX, there), v);
+      unpack4(in.template get<E>(stage, r, In::kDy, there), e);
+      unpack4(in.template get<R>(stage, r, In::kRes, there && a.res.p), h[r]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[r][i] = fma2(mul2(mul2(v[i], twice(rx[r])), par.p[i]), par.g[i], h[r][i]);
+        q = fma2(h[r][i], h[r][i], q);
+        p = fma2(mul2(e[i], par.w[i]), h[r][i], p);
+      }
+      sum[2 * r] = n > 0 ? total(q) : 0.f;
+      sum[2 * r + 1] = n > 0 ? total(p) : 0.f;
+    }
+    row_sums<LANES, 2 * NR>(sum, red, phase);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      last[r] = 0.f;
+      if (t + r >= a.T || n <= 0) continue;
+      const float f = rsqrtf(fmaf(sum[2 * r], inv, a.eps)), back = f * f * sum[2 * r + 1] * inv;
+      f2 e[4], g[4], v[4], q = twice(0.f);
+      unpack4(in.template get<E>(stage, r, In::kDy, true), e);
+      unpack4(in.template get<R>(stage, r, In::kDh, a.dh.p), g);
+      if (LANES == 1) {
+        f2 ew[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ew[i] = mul2(e[i], par.w[i]);
+          dw[i] = fma2(e[i], mul2(h[r][i], twice(f)), dw[i]);
+        }
+        row_back(h[r], ew, a.C, a.eps, ew);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[i] = add2(g[i], ew[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dw[i] = fma2(e[i], mul2(h[r][i], twice(f)), dw[i]);
+          g[i] = fma2(twice(f), fma2(h[r][i], twice(-back), mul2(e[i], par.w[i])), g[i]);
+        }
+      }
+      if (a.dres.p)
+        st8<true>(reinterpret_cast<R *>(a.dres.p) + (t + r) * a.dres.st + c, pack4<R>(g), 8);
+      unpack4(in.template get<E>(stage, r, In::kX, true), v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = mul2(v[i], twice(rx[r]));  // n_x
+        dg[i] = fma2(g[i], mul2(v[i], par.p[i]), dg[i]);  // but for the scale
+        g[i] = mul2(g[i], par.g[i]);
+        dp[i] = fma2(g[i], v[i], dp[i]);
+        h[r][i] = mul2(g[i], par.p[i]);
+        q = fma2(h[r][i], v[i], q);
+      }
+      last[r] = total(q);
+    }
+    const int here = stage;
+    stage = stage + 1 == depth ? 0 : stage + 1;
+    in.wait(depth - 1);
+    if (a.post) {
+      squares<E, In, NR>(in, stage, t + step, last + NR);
+      row_sums<LANES, 2 * NR>(last, red, phase);
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      if (t + r >= a.T || n <= 0) continue;
+      if (a.post) {
+        f2 v[4];
+        unpack4(in.template get<E>(here, r, In::kX, true), v);
+        if (LANES == 1) {
+          row_back(v, h[r], a.C, a.eps, h[r]);
+        } else {
+          const float b = -rx[r] * last[r] * inv;  // n_x mean(e n_x) = x times this
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[r][i] = mul2(twice(rx[r]), fma2(v[i], twice(b), h[r][i]));
+        }
+      }
+      st8<true>(reinterpret_cast<E *>(a.dx.p) + (t + r) * a.dx.st + c, pack4<E>(h[r]), 8);
+    }
+  }
+  copies_wait<0>();
+  // the block's parts of dw, dw_post and dgate, its row groups in order
+  float *out = reinterpret_cast<float *>(a.work) + (int64_t)blockIdx.x * 3 * a.C;
+  constexpr int L = LANES ? LANES : 1;
+  __shared__ float sums[LANES ? 128 * 8 : 1];
+#pragma unroll
+  for (int b = 0; b < 3; ++b) {
+    if (!(b == 0 ? a.dw : b == 1 ? a.dwp : a.dg)) continue;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      unpair(b == 0 ? dw[i] : b == 1 ? dp[i] : mul2(dg[i], twice(a.scale)), v[2 * i], v[2 * i + 1]);
+    float *to = out + (int64_t)b * a.C;
+    if (LANES == 0) {
+      if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) to[c + i] = v[i];
+      }
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sums[cols.group * L * 8 + c + i] = v[i];
+      __syncthreads();
+      for (int col = threadIdx.x; col < a.C; col += 128) {
+        float s = sums[col];
+        for (int g = 1; g < 128 / L; ++g) s += sums[g * L * 8 + col];
+        to[col] = s;
+      }
+    }
+  }
+}
+
+// Threads that share the register file and shared memory of a multiprocessor in the backward.
+constexpr int kResidThreads = 512, kResidBlocks = 4;
+
+template <typename E, typename R, int LANES, int NV, bool VEC>
+cudaError_t run_resid_long(const ResidArgs &a, bool bwd, cudaStream_t stream) {
+  // a block of as many warps as a row fills, or 128 threads with a row for every LANES of them
+  const int th = LANES ? 128 : (a.C + NV * 256 - 1) / (NV * 256) * 32;
+  const int64_t need = ceil_div64(a.T, LANES ? 128 / LANES : 1);
+  using I = Ring<E, R, NV, VEC>;
+  const int unit = (bwd ? 2 : 1) * NV * (I::PE + I::PR) * th * 16;
+  int per_sm = (bwd ? kResidThreads : 1024) / th;
+  per_sm = per_sm < 1 ? 1 : bwd && per_sm > kResidBlocks ? kResidBlocks : per_sm;
+  const int64_t most = (int64_t)sm_count() * per_sm, blocks = need < most ? need : most;
+  // rows ahead: what shared memory holds, up to four, and no more than a block has
+  int depth = VEC ? 200 * 1024 / per_sm / unit : 0;
+  const int64_t turns = ceil_div64(need, blocks);
+  depth = depth > 4 ? 4 : depth;
+  if (turns < depth) depth = (int)turns;
+  const int smem = depth * unit;
+  static std::atomic<uint64_t> done[2];
+  cudaError_t e = cudaSuccess;
+  if (smem > 32 * 1024)  // with the static shared memory above what needs no consent
+    e = bwd ? set_once(k_resid_bwd_long<E, R, LANES, NV, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       200 * 1024, done[1])
+            : set_once(k_resid_fwd_long<E, R, LANES, NV, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       200 * 1024, done[0]);
+  if (e != cudaSuccess) return e;
+  if (!bwd)
+    return launch(k_resid_fwd_long<E, R, LANES, NV, VEC>, (unsigned)blocks, th, smem, stream, a, depth);
+  e = launch(k_resid_bwd_long<E, R, LANES, NV, VEC>, (unsigned)blocks, th, smem, stream, a, depth);
+  if (e != cudaSuccess || !(a.dw || a.dwp || a.dg)) return e;
+  return launch(k_sum_parts, dim3((unsigned)((a.C + 31) / 32), 3), 256, 0, stream,
+                reinterpret_cast<const float *>(a.work), (int)blocks, (int64_t)3 * a.C, a.C, a.dw,
+                a.dwp, a.dg);
+}
+
+template <typename E, typename R, int LANES, int NR>
 cudaError_t run_resid(const ResidArgs &a, bool bwd, cudaStream_t stream) {
-  constexpr int TH = TPR > 32 ? TPR : 128, RB = TH / TPR;
-  const int64_t need = ceil_div64(a.T, RB);
-  if (!bwd) {
-    const int64_t most = (int64_t)sm_count() * (2048 / TH);
-    return launch(k_resid_fwd<E, R, TPR, NV, VEC>, (unsigned)(need < most ? need : most), TH, 0,
-                  stream, a);
-  }
-  using I = Rows4<E, R, TPR, NV, VEC, TH>;
-  constexpr int unit = I::U * TH * 16, per_sm = resid_per_sm(TH);
-  constexpr int fit = 200 * 1024 / per_sm / unit, depth = fit >= 3 ? 3 : fit == 2 ? 2 : 1;
-  constexpr int smem = I::kRing ? depth * unit : 0;
-  const int64_t most = (int64_t)sm_count() * per_sm;
-  const int64_t blocks = need < most ? need : most;
-  if (smem > 32 * 1024) {  // with the static shared memory above what needs no consent
-    static std::atomic<uint64_t> done{0};
-    const cudaError_t e = set_once(k_resid_bwd<E, R, TPR, NV, VEC>,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem, done);
-    if (e != cudaSuccess) return e;
-  }
-  cudaError_t e = launch(k_resid_bwd<E, R, TPR, NV, VEC>, (unsigned)blocks, TH, smem, stream, a, depth);
+  const int th = LANES ? 128 : (a.C + 255) / 256 * 32;
+  const int64_t need = ceil_div64(a.T, (LANES ? 128 / LANES : 1) * NR);
+  const int unit = (bwd ? Ahead<E, R, NR, true>::kUnits : Ahead<E, R, NR, false>::kUnits) * th * 16;
+  int per_sm = (bwd ? kResidThreads : 1024) / th;
+  per_sm = per_sm < 1 ? 1 : bwd && per_sm > kResidBlocks ? kResidBlocks : per_sm;
+  const int64_t most = (int64_t)sm_count() * per_sm, blocks = need < most ? need : most;
+  // steps ahead: what shared memory holds, up to four, and no more than a block has
+  const int64_t turns = ceil_div64(need, blocks);
+  int depth = 200 * 1024 / per_sm / unit;
+  depth = depth > 4 ? 4 : depth;
+  if (turns < depth) depth = (int)turns;
+  if (depth < 2) depth = 2;  // the step that is worked on, and the next one's first sums
+  const int smem = depth * unit;
+  static std::atomic<uint64_t> done[2];
+  cudaError_t e = cudaSuccess;
+  if (smem > 32 * 1024)  // with the static shared memory above what needs no consent
+    e = bwd ? set_once(k_resid_bwd<E, R, LANES, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       200 * 1024, done[1])
+            : set_once(k_resid_fwd<E, R, LANES, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       200 * 1024, done[0]);
+  if (e != cudaSuccess) return e;
+  if (!bwd) return launch(k_resid_fwd<E, R, LANES, NR>, (unsigned)blocks, th, smem, stream, a, depth);
+  e = launch(k_resid_bwd<E, R, LANES, NR>, (unsigned)blocks, th, smem, stream, a, depth);
   if (e != cudaSuccess || !(a.dw || a.dwp || a.dg)) return e;
   return launch(k_sum_parts, dim3((unsigned)((a.C + 31) / 32), 3), 256, 0, stream,
                 reinterpret_cast<const float *>(a.work), (int)blocks, (int64_t)3 * a.C, a.C, a.dw,
@@ -646,22 +1132,23 @@ cudaError_t run_resid_for(const ResidArgs &a, bool bwd, cudaStream_t stream) {
   vec = vec && (bwd ? fits16(a.dy, e) && fits16(a.dh, f) && fits16(a.dx, e) && fits16(a.dres, f)
                     : fits16(a.y, e) && fits16(a.h, f));
   const int C = a.C;
-  if (C <= 8)
-    return vec ? run_resid<E, R, 1, 1, true>(a, bwd, stream) : run_resid<E, R, 1, 1, false>(a, bwd, stream);
   if (!vec) {
-    if (C <= 512) return run_resid<E, R, 32, 2, false>(a, bwd, stream);
-    if (C <= 4096) return run_resid<E, R, 512, 1, false>(a, bwd, stream);
-    return run_resid<E, R, 512, 4, false>(a, bwd, stream);
+    if (C <= 8) return run_resid_long<E, R, 1, 1, false>(a, bwd, stream);
+    if (C <= 256) return run_resid_long<E, R, 32, 1, false>(a, bwd, stream);
+    if (C <= 8192) return run_resid_long<E, R, 0, 2, false>(a, bwd, stream);
+    return run_resid_long<E, R, 0, 4, false>(a, bwd, stream);
   }
-  if (C <= 64) return run_resid<E, R, 8, 1, true>(a, bwd, stream);
-  if (C <= 128) return run_resid<E, R, 16, 1, true>(a, bwd, stream);
-  if (C <= 256) return run_resid<E, R, 32, 1, true>(a, bwd, stream);
-  if (C <= 512) return run_resid<E, R, 64, 1, true>(a, bwd, stream);
-  if (C <= 1024) return run_resid<E, R, 128, 1, true>(a, bwd, stream);
-  if (C <= 2048) return run_resid<E, R, 256, 1, true>(a, bwd, stream);
-  if (C <= 4096) return run_resid<E, R, 512, 1, true>(a, bwd, stream);
-  if (C <= 8192) return run_resid<E, R, 512, 2, true>(a, bwd, stream);
-  return run_resid<E, R, 512, 4, true>(a, bwd, stream);
+  if (C <= 8) return run_resid<E, R, 1, 1>(a, bwd, stream);
+  if (C <= 64) return run_resid<E, R, 8, 1>(a, bwd, stream);
+  if (C <= 128) return run_resid<E, R, 16, 1>(a, bwd, stream);
+  if (C <= 256) return run_resid<E, R, 32, 1>(a, bwd, stream);
+  if (C <= (bwd ? 4096 : 8192)) {
+    // two rows at a time where there are enough, and shared memory and registers hold them
+    const bool two = sizeof(E) == 2 && a.T >= 4 * sm_count() && (bwd || C <= 4096);
+    return two ? run_resid<E, R, 0, 2>(a, bwd, stream) : run_resid<E, R, 0, 1>(a, bwd, stream);
+  }
+  if (C <= 8192) return run_resid_long<E, R, 0, 2, true>(a, bwd, stream);
+  return run_resid_long<E, R, 0, 4, true>(a, bwd, stream);
 }
 cudaError_t run_resid_any(const ResidArgs &a, bool bwd, cudaStream_t stream) {
   if (a.f32) return run_resid_for<float, float>(a, bwd, stream);
@@ -699,7 +1186,7 @@ cudaError_t launch_resid_fwd(const ResidArgs &a, cudaStream_t stream) {
 }
 size_t resid_bwd_workspace(int64_t T, int32_t C) {
   // one row of parts a block: no more blocks than rows, and four a multiprocessor at most
-  const int64_t most = (int64_t)mix::sm_count() * 4;
+  const int64_t most = (int64_t)mix::sm_count() * mix::kResidBlocks;
   return align256((size_t)(T < most ? T : most) * 3 * C * 4);
 }
 cudaError_t launch_resid_bwd(const ResidArgs &a, cudaStream_t stream) {
