@@ -29,15 +29,18 @@ __device__ __forceinline__ float low() { return __uint_as_float(0xff800000u); } 
 
 // ------------------------------------------------------------------ dealing out the work
 
-struct Span {  // the keys of a request that its token sees
-  int first, end;
+// The keys of a request that its token sees, first .. end - 1, in units from base on: a warp's 16 keys
+// start at a multiple of 16, and lie on one page where pages hold a multiple of that.
+struct Span {
+  int base, first, end;
   __device__ __forceinline__ Span(const AttnArgs &a, int b) {
     const int64_t room = (int64_t)a.width * a.page;
     const int64_t n = max((int64_t)0, min((int64_t)a.lens[b], room));
     end = (int)n;
     first = a.window > 0 && n > a.window ? (int)(n - a.window) : 0;
+    base = first & ~15;
   }
-  __device__ __forceinline__ int units() const { return (int)(((int64_t)end - first + kUnit - 1) / kUnit); }
+  __device__ __forceinline__ int units() const { return (int)(((int64_t)end - base + kUnit - 1) / kUnit); }
 };
 
 // All threads: the sum of v over the block.  red: 32 values.
@@ -149,11 +152,12 @@ struct AttnSmem {
 
 // Where a block is in the sequence of units: a warp's walk over requests, pairs and units.
 struct Cursor {
-  int b, pair, unit, units, first, end;
+  int b, pair, unit, units, base, first, end;
   __device__ __forceinline__ void request(const AttnArgs &a) {
     // past the requests without keys
     for (; b < a.B; ++b) {
       const Span s(a, b);
+      base = s.base;
       first = s.first;
       end = s.end;
       units = s.units();
@@ -200,53 +204,80 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
       (&s.ring[warp][0][0][0])[i] = make_uint4(0, 0, 0, 0);
   __syncwarp();
 
-  // The copies of one unit: lane r looks up row r's place, 32 / parts rows go out at a time.
+  // The copies of one unit.  A unit's pages are looked up while the one before it is copied.
   const __nv_bfloat16 *kp = reinterpret_cast<const __nv_bfloat16 *>(a.k.p);
   const __nv_bfloat16 *vp = reinterpret_cast<const __nv_bfloat16 *>(a.v.p);
-  uint32_t ok[S];  // of each place in the ring: which of its rows are there
-  auto issue = [&](int stage, bool in, uint32_t &good) {
-    good = 0;
+  const bool one_page = a.page % 16 == 0;
+  int page = -1;  // of key `lane` of 16 (one page: of all of them)
+  auto look = [&] {
+    const int key = ahead.base + ahead.unit * kUnit + warp * 16 + (one_page ? 0 : lane & 15);
+    page = -1;
+    if (ahead.units > 0 && key < ahead.end) page = a.table[ahead.b * a.table_st + key / a.page];
+  };
+  auto issue = [&](int place, bool in) -> uint32_t {  // which of the 16 keys are there
+    uint32_t good = 0;
     if (in) {
-      const int key = ahead.first + ahead.unit * kUnit + warp * 16 + (lane & 15);
-      int page = -1, place = 0;
-      if (key < ahead.end) {
-        page = a.table[ahead.b * a.table_st + key / a.page];
-        place = key % a.page;
-      }
-      const bool fine = page >= 0 && page < a.pages;
+      const int key0 = ahead.base + ahead.unit * kUnit + warp * 16, key = key0 + (lane & 15);
+      const bool fine = key >= ahead.first && key < ahead.end && page >= 0 && page < a.pages;
       good = __ballot_sync(0xffffffffu, fine) & 0xffffu;
       const int head = ahead.pair / groups;
-      const int64_t ka = fine ? page * a.k.sp + place * a.k.st + head * a.k.sh : 0;
-      const int64_t va = fine ? page * a.v.sp + place * a.v.st + head * a.v.sh : 0;
-      uint4 *ks = s.ring[warp][stage][0], *vs = s.ring[warp][stage][1];
-#pragma unroll
-      for (int i = 0; i < 16 * C / 32; ++i) {
-        const int r = (i * 32 + lane) / C, c = (i * 32 + lane) % C;
-        const int64_t kr = __shfl_sync(0xffffffffu, ka, r), vr = __shfl_sync(0xffffffffu, va, r);
-        const bool there = good >> r & 1;
+      uint4 *ks = s.ring[warp][place][0], *vs = s.ring[warp][place][1];
+      if (one_page) {
+        const int r0 = lane / C, c = lane % C;  // C <= 32
+        const int at0 = key0 % a.page + r0;
+        const __nv_bfloat16 *k = kp, *v = vp;
+        if (good) {
+          k += page * a.k.sp + at0 * a.k.st + head * a.k.sh + c * 8;
+          v += page * a.v.sp + at0 * a.v.st + head * a.v.sh + c * 8;
+        }
         if (c < parts) {
-          copy16(ks + r * C + (c ^ (r & 7)), kp + kr + c * 8, there);
-          copy16(vs + r * C + (c ^ (r & 7)), vp + vr + c * 8, there);
+#pragma unroll
+          for (int i = 0; i < 16 * C / 32; ++i) {
+            const int r = r0 + i * (32 / C);
+            const bool there = good >> r & 1;
+            copy16(ks + r * C + (c ^ (r & 7)), there ? k : kp, there);
+            copy16(vs + r * C + (c ^ (r & 7)), there ? v : vp, there);
+            k += (32 / C) * a.k.st;
+            v += (32 / C) * a.v.st;
+          }
+        }
+      } else {
+        const int at0 = key % a.page;
+        const int64_t ka = fine ? page * a.k.sp + at0 * a.k.st + head * a.k.sh : 0;
+        const int64_t va = fine ? page * a.v.sp + at0 * a.v.st + head * a.v.sh : 0;
+#pragma unroll 2
+        for (int i = 0; i < 16 * C / 32; ++i) {
+          const int r = (i * 32 + lane) / C, c = (i * 32 + lane) % C;
+          const int64_t kr = __shfl_sync(0xffffffffu, ka, r), vr = __shfl_sync(0xffffffffu, va, r);
+          const bool there = good >> r & 1;
+          if (c < parts) {
+            copy16(ks + r * C + (c ^ (r & 7)), kp + kr + c * 8, there);
+            copy16(vs + r * C + (c ^ (r & 7)), vp + vr + c * 8, there);
+          }
         }
       }
       ahead.next(a, pairs);
+      look();
     }
     copies_commit();
+    return good;
   };
+  look();
+  uint64_t ok = 0;  // of the units on their way, 16 keys each
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(i, w0 + i < w1, ok[i]);
+  for (int i = 0; i < S - 1; ++i) ok |= (uint64_t)issue(i, w0 + i < w1) << (16 * i);
 
   uint32_t q[D / 16][4];
   float o[D / 8][4], m[2], l[2];
   const float scale = a.scale * kLog2e;
   bool fresh = true;
   bool whole_start = at.unit == 0;  // the pair's first unit is in this range
-  int64_t u = w0;
-  while (u < w1) {
-#pragma unroll
-    for (int stage = 0; stage < S; ++stage) {
-      if (u >= w1) break;
-      issue((stage + S - 1) % S, u + S - 1 < w1, ok[(stage + S - 1) % S]);
+  int stage = 0;
+#pragma unroll 1
+  for (int64_t u = w0; u < w1;) {
+    {
+      const uint32_t good = (uint32_t)ok & 0xffffu;
+      ok = ok >> 16 | (uint64_t)issue(stage == 0 ? S - 1 : stage - 1, u + S - 1 < w1) << (16 * (S - 2));
       copies_wait<S - 1>();
       __syncwarp();
       const int head = at.pair / groups, row0 = at.pair % groups * kRows;
@@ -284,7 +315,6 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
         }
       }
       // scores in powers of two; keys that are not there count for nothing
-      const uint32_t good = ok[stage];
       float top[2] = {low(), low()};
 #pragma unroll
       for (int n = 0; n < 2; ++n)
@@ -343,6 +373,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
         }
       }
       __syncwarp();  // the ring's place is free for the copies of the next turn
+      stage = stage + 1 == S ? 0 : stage + 1;
       ++u;
       const bool pair_ends = at.unit + 1 == at.units;
       if (pair_ends || u == w1) {
@@ -448,15 +479,18 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
   copies_wait<0>();
 }
 
-// Joins the parts of the pairs that lie in several ranges, one block a pair; rows without keys get
-// zeros.
+// Joins the parts of the pairs that lie in several ranges, one block a pair and query head; rows
+// without keys get zeros.  The warps take every fourth part, a lane D / 32 columns.
 template <int D>
-__global__ void __launch_bounds__(128) k_attn_join(const AttnArgs a, int groups, int ctas) {
+__global__ void __launch_bounds__(128) k_attn_join(const AttnArgs a, int groups, int ctas, int rows) {
   after_previous<true>();
+  constexpr int N = D / 32;
   __shared__ int64_t red[32];
+  __shared__ float ms[4], ls[4], os[4][D];
   const int pairs = a.Hk * groups, G = a.Hq / a.Hk;
-  const int b = blockIdx.x / pairs, pair = blockIdx.x % pairs;
-  const int head = pair / groups, row0 = pair % groups * kRows;
+  const int r = blockIdx.x % rows, b = blockIdx.x / rows / pairs, pair = blockIdx.x / rows % pairs;
+  const int head = pair / groups, h = pair % groups * kRows + r;
+  if (h >= G) return;
   int64_t all, before;
   count_units(a, b, red, all, before);
   const int units = Span(a, b).units();
@@ -464,38 +498,63 @@ __global__ void __launch_bounds__(128) k_attn_join(const AttnArgs a, int groups,
   const int64_t u0 = before * pairs + (int64_t)pair * units, u1 = u0 + units;
   const int64_t c0 = u0 / share, c1 = units > 0 ? (u1 - 1) / share : c0;
   if (units > 0 && c0 == c1) return;
-  const float *w = reinterpret_cast<const float *>(a.work);
-  const int rows = min(kRows, G - row0);
-  __nv_bfloat16 *op = reinterpret_cast<__nv_bfloat16 *>(a.o.p) + b * a.o.st;
-  // a warp takes every fourth row, a lane two columns at a time
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < rows; r += 4) {
-    uint32_t *to = reinterpret_cast<uint32_t *>(op + (int64_t)(head * G + row0 + r) * a.o.sh);
-    float m = low();
-    if (units > 0) {
-      for (int64_t c = c0 + lane; c <= c1; c += 32)
-        m = fmaxf(m, w[(c * 2 + (c == c0 && u0 > c0 * share ? 1 : 0)) * kPart<D> + kRows * D + r]);
+  float m = low(), l = 0.f, acc[N] = {};
+  if (units > 0) {
+    // a range's part 0 is the pair that it starts in, part 1 the one that it ends in
+    const float *w = reinterpret_cast<const float *>(a.work) + (u0 > c0 * share ? kPart<D> : 0);
+    for (int64_t c = c0 + warp; c <= c1; c += 16) {
+      float pm[4], pl[4], po[4][N];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    }
-    const float by = m == low() ? 0.f : m;
-    float l = 0.f, acc[D / 64][2] = {};
-    if (units > 0)
-      for (int64_t c = c0; c <= c1; ++c) {
-        const float *p = w + (c * 2 + (c == c0 && u0 > c0 * share ? 1 : 0)) * kPart<D>;
-        const float f = ex2(p[kRows * D + r] - by);
-        l += p[kRows * D + kRows + r] * f;
+      for (int i = 0; i < 4; ++i) {
+        const int64_t at = c + 4 * i;
+        const float *p = (at == c0 ? w : reinterpret_cast<const float *>(a.work)) + at * 2 * kPart<D>;
+        const bool in = at <= c1;
+        pm[i] = in ? p[kRows * D + r] : low();
+        pl[i] = in ? p[kRows * D + kRows + r] : 0.f;
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          const float2 x = *reinterpret_cast<const float2 *>(p + r * D + j * 64 + lane * 2);
-          acc[j][0] = fmaf(x.x, f, acc[j][0]);
-          acc[j][1] = fmaf(x.y, f, acc[j][1]);
-        }
+        for (int j = 0; j < N; ++j) po[i][j] = in ? p[r * D + j * 32 + lane] : 0.f;
       }
-    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+      float to = m;
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j)
-      if (j * 64 + lane * 2 < a.d) to[j * 32 + lane] = pack2(acc[j][0] * inv, acc[j][1] * inv);
+      for (int i = 0; i < 4; ++i) to = fmaxf(to, pm[i]);
+      const float by = to == low() ? 0.f : to, f = ex2(m - by);
+      m = to;
+      l *= f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] *= f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float g = ex2(pm[i] - by);
+        l = fmaf(pl[i], g, l);
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = fmaf(po[i][j], g, acc[j]);
+      }
+    }
+  }
+  if (lane == 0) {
+    ms[warp] = m;
+    ls[warp] = l;
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) os[warp][j * 32 + lane] = acc[j];
+  __syncthreads();
+  m = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
+  const float by = m == low() ? 0.f : m;
+  float f[4];
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    f[w] = ex2(ms[w] - by);
+    l = fmaf(ls[w], f[w], l);
+  }
+  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+  __nv_bfloat16 *op = reinterpret_cast<__nv_bfloat16 *>(a.o.p) + b * a.o.st + (int64_t)(head * G + h) * a.o.sh;
+  for (int c = threadIdx.x; c < a.d; c += 128) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) v = fmaf(os[w][c], f[w], v);
+    op[c] = __float2bfloat16_rn(v * inv);
   }
 }
 
@@ -581,8 +640,9 @@ cudaError_t run_split(const AttnArgs &a, cudaStream_t stream) {
   e = launch(k_attn_split<D, S>, (unsigned)ctas, kWarps * 32, smem, stream, a, groups,
              G < kRows ? G : kRows);
   if (e != cudaSuccess) return e;
-  return launch(k_attn_join<D>, (unsigned)((int64_t)a.B * a.Hk * groups), 128, 0, stream, a, groups,
-                ctas);
+  const int rows = G < kRows ? G : kRows;
+  return launch(k_attn_join<D>, (unsigned)((int64_t)a.B * a.Hk * groups * rows), 128, 0, stream, a, groups,
+                ctas, rows);
 }
 
 bool fits16(const Pages &h) {

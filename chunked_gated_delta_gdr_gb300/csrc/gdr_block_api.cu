@@ -349,7 +349,7 @@ int gdr_attn_step(const gdr_tensor_t *q, const gdr_tensor_t *k_cache, const gdr_
   GDR_TRY(alike(k, v));
   if (k.shape[3] != a.d) return GDR_ERR_SHAPE;
   const int64_t Hk = k.shape[2];
-  if (B > kMost || Hq < 1 || Hq > 0xffff || B * Hq > 0x7fffffff) return GDR_ERR_SHAPE;
+  if (B > kMost || Hq < 1 || Hq > 0xffff || B * Hq > 0x3fffffff) return GDR_ERR_SHAPE;
   if (Hq % Hk != 0) return GDR_ERR_HEADS;
   GDR_TRY(read_table(block_table, B, k.shape[1], false, &t));
   if (!lengths && B > 0) return GDR_ERR_NULL;

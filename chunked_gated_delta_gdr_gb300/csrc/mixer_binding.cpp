@@ -115,6 +115,22 @@ at::Tensor empty(at::IntArrayRef sizes, const at::Tensor &like) {
 at::Tensor empty32(at::IntArrayRef sizes, const at::Tensor &like) {
   return at::empty(sizes, at::TensorOptions().dtype(at::kFloat).device(like.device()));
 }
+// Several compact tensors of `like`'s type out of one allocation (256 bytes apart): allocating each costs
+// the host a microsecond.
+struct Parts {
+  at::Tensor all;
+  int64_t at = 0;
+  Parts(int64_t count, const at::Tensor &like)
+      : all(at::empty({count}, at::TensorOptions().dtype(like.scalar_type()).device(like.device()))) {}
+  at::Tensor next(int64_t n) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::TensorImpl::VIEW, c10::Storage(all.storage()), all.key_set(), all.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(at);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    at += (n + 63) / 64 * 64;
+    return t;
+  }
+};
 PyObject *wrap(const at::Tensor &t) {
   if (!t.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(t);
@@ -646,12 +662,12 @@ ENTRY(cache_plan, 9)
                 *tk = c.ints(taken, 1, "taken");
   c.ints(pages, -1, "free_pages");
   at::Tensor lens_out = tensor(args[7]), taken_out = tensor(args[8]);
-  const auto opt = lens.options();
-  if (!lens_out.defined()) lens_out = at::empty({B}, opt);
-  if (!taken_out.defined()) taken_out = at::empty({1}, opt);
+  // the results in one allocation
+  Parts parts(2 * (int64_t)most + 2 * B + 2 + 5 * 64, lens);
+  const at::Tensor slots = parts.next(most), pos = parts.next(most), cu = parts.next(B + 1);
+  if (!lens_out.defined()) lens_out = parts.next(B);
+  if (!taken_out.defined()) taken_out = parts.next(1);
   const int32_t *lo = c.ints(lens_out, B, "lengths_out"), *to = c.ints(taken_out, 1, "taken_out");
-  const at::Tensor slots = at::empty({most}, opt), pos = at::empty({most}, opt),
-                   cu = at::empty({B + 1}, opt);
   gdr_tensor_t *p[] = {c.table(table, "block_table"), c.table(pages, "free_pages")};
   const cudaStream_t st = c.stream();
   int32_t *sp = most ? slots.data_ptr<int32_t>() : nullptr, *pp = most ? pos.data_ptr<int32_t>() : nullptr;
