@@ -21,7 +21,7 @@ namespace gdr {
 namespace mix {
 namespace {
 
-constexpr int kRows = 16;           // query heads of a pair
+constexpr int kRows = 16;           // query heads of a pair at most
 constexpr int kWarps = 4, kUnit = 16 * kWarps;  // keys of a unit
 constexpr int kMostCtas = 1024;     // blocks with parts in the workspace
 
@@ -129,6 +129,12 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// an 8 x 8 matrix of a warp's pairs, transposed
+__device__ __forceinline__ uint32_t turned(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 // two values as bf16, and what that leaves of them
 __device__ __forceinline__ uint32_t split2(float x, float y, uint32_t &rest) {
   const uint32_t hi = pack2(x, y);
@@ -138,16 +144,19 @@ __device__ __forceinline__ uint32_t split2(float x, float y, uint32_t &rest) {
 
 // ------------------------------------------------------------------ the split kernel
 
-// One (request, key head, 16 of its query heads); parts in the workspace are O [16][D], m and l [16].
+// A part of a (request, key head, group of query heads): O [16][D], m and l [16].
 template <int D>
 constexpr int kPart = kRows * D + 2 * kRows;
 
-template <int D, int S>
+// H: query heads of a pair, 8 or 16
+template <int D, int H, int S>
 struct AttnSmem {
   uint4 ring[kWarps][S][2][16 * D / 8];  // each warp's keys and values, rows of 16-byte parts
-  float out[2][kRows * D];
-  float m[kWarps][kRows], l[kWarps][kRows];
+  float out[2][H * D];
+  float m[kWarps][H], l[kWarps][H];
   int64_t red[32], found[2];
+  // element (head, column) of a warp's output: a lane's heads 2 t, 2 t + 1 beside 8 columns
+  static __device__ __forceinline__ int at(int h, int c) { return h * D + (c ^ ((h >> 1 & 3) << 3)); }
 };
 
 // Where a block is in the sequence of units: a warp's walk over requests, pairs and units.
@@ -175,12 +184,17 @@ struct Cursor {
   }
 };
 
-template <int D, int S>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
-    k_attn_split(const AttnArgs a, int groups, int rows) {
+// blocks on each multiprocessor: what shared memory and registers hold
+constexpr int attn_per_sm(int D, int H) { return D == 256 ? 1 : H == 8 ? 3 : 2; }
+
+template <int D, int H, int S>
+__global__ void __launch_bounds__(kWarps * 32, attn_per_sm(D, H))
+    k_attn_split(const AttnArgs a, int groups) {
   after_previous<true>();
   extern __shared__ __align__(128) unsigned char raw[];
-  AttnSmem<D, S> &s = *reinterpret_cast<AttnSmem<D, S> *>(raw);
+  using Smem = AttnSmem<D, H, S>;
+  Smem &s = *reinterpret_cast<Smem *>(raw);
+  constexpr int NT = H / 8;  // tiles of 8 query heads
   constexpr int C = D / 8;  // 16-byte parts of a row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int pairs = a.Hk * groups, G = a.Hq / a.Hk, parts = a.d / 8;
@@ -267,214 +281,217 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) ok |= (uint64_t)issue(i, w0 + i < w1) << (16 * i);
 
-  uint32_t q[D / 16][4];
-  float o[D / 8][4], m[2], l[2];
+  // Products with keys and values as the first factor, so that a tile of 8 heads is enough: scores
+  // [16 keys, 8 heads], outputs [16 columns, 8 heads].  A lane has heads 2 t4 and 2 t4 + 1 of both.
+  uint32_t q[D / 16][NT][2];
+  float o[D / 16][NT][4], m[NT][2], l[NT][2];
   const float scale = a.scale * kLog2e;
   bool fresh = true;
   bool whole_start = at.unit == 0;  // the pair's first unit is in this range
   int stage = 0;
 #pragma unroll 1
   for (int64_t u = w0; u < w1;) {
+    const uint32_t good = (uint32_t)ok & 0xffffu;
+    ok = ok >> 16 | (uint64_t)issue(stage == 0 ? S - 1 : stage - 1, u + S - 1 < w1) << (16 * (S - 2));
+    copies_wait<S - 1>();
+    __syncwarp();
+    const int head = at.pair / groups, row0 = at.pair % groups * H;
+    if (fresh) {  // a pair's queries, and nothing seen yet
+      fresh = false;
+      const __nv_bfloat16 *qp = reinterpret_cast<const __nv_bfloat16 *>(a.q.p) + at.b * a.q.st;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int h = row0 + n * 8 + g;
+        const uint32_t *qh = reinterpret_cast<const uint32_t *>(qp + (int64_t)(head * G + h) * a.q.sh);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          q[k][n][0] = 16 * k < a.d && h < G ? qh[8 * k + t4] : 0;
+          q[k][n][1] = 16 * k + 8 < a.d && h < G ? qh[8 * k + 4 + t4] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
+        m[n][0] = m[n][1] = low();
+        l[n][0] = l[n][1] = 0.f;
+      }
+    }
+    const uint32_t kbase = static_cast<uint32_t>(__cvta_generic_to_shared(s.ring[warp][stage][0]));
+    const uint32_t vbase = static_cast<uint32_t>(__cvta_generic_to_shared(s.ring[warp][stage][1]));
+    float c[NT][4];
     {
-      const uint32_t good = (uint32_t)ok & 0xffffu;
-      ok = ok >> 16 | (uint64_t)issue(stage == 0 ? S - 1 : stage - 1, u + S - 1 < w1) << (16 * (S - 2));
-      copies_wait<S - 1>();
-      __syncwarp();
-      const int head = at.pair / groups, row0 = at.pair % groups * kRows;
-      if (fresh) {  // a pair's queries, and nothing seen yet
-        fresh = false;
-        const __nv_bfloat16 *qp = reinterpret_cast<const __nv_bfloat16 *>(a.q.p) + at.b * a.q.st;
-        const int h0 = row0 + g, h1 = row0 + g + 8;
-        const uint32_t *q0 = reinterpret_cast<const uint32_t *>(qp + (int64_t)(head * G + h0) * a.q.sh);
-        const uint32_t *q1 = reinterpret_cast<const uint32_t *>(qp + (int64_t)(head * G + h1) * a.q.sh);
+      float e[2][NT][4];  // even and odd steps: two shorter chains
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const bool lo = 16 * k < a.d, hi = 16 * k + 8 < a.d;
-          q[k][0] = lo && h0 < G ? q0[8 * k + t4] : 0;
-          q[k][1] = lo && h1 < G ? q1[8 * k + t4] : 0;
-          q[k][2] = hi && h0 < G ? q0[8 * k + 4 + t4] : 0;
-          q[k][3] = hi && h1 < G ? q1[8 * k + 4 + t4] : 0;
-        }
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-        m[0] = m[1] = low();
-        l[0] = l[1] = 0.f;
+        for (int i = 0; i < 4; ++i) e[0][n][i] = e[1][n][i] = 0.f;
+      const int r = lane & 15, half = lane >> 4;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t x[4];
+        ldm4(x, kbase + (r * C + ((2 * k + half) ^ (r & 7))) * 16);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma(e[k & 1][n], x, q[k][n][0], q[k][n][1]);
       }
-      const uint4 *ks = s.ring[warp][stage][0], *vs = s.ring[warp][stage][1];
-      const uint32_t kbase = static_cast<uint32_t>(__cvta_generic_to_shared(ks));
-      const uint32_t vbase = static_cast<uint32_t>(__cvta_generic_to_shared(vs));
-      float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      {
-        const int r = (lane & 7) + (lane >> 4) * 8, half = lane >> 3 & 1;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t b[4];
-          ldm4(b, kbase + (r * C + ((2 * k + half) ^ (r & 7))) * 16);
-          mma(c[0], q[k], b[0], b[1]);
-          mma(c[1], q[k], b[2], b[3]);
-        }
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[n][i] = (e[0][n][i] + e[1][n][i]) * scale;
+    }
+    // scores in powers of two; keys that are not there count for nothing
+    if (good != 0xffffu) {
+      const bool lo = good >> g & 1, hi = good >> (g + 8) & 1;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        c[n][0] = lo ? c[n][0] : low();
+        c[n][1] = lo ? c[n][1] : low();
+        c[n][2] = hi ? c[n][2] : low();
+        c[n][3] = hi ? c[n][3] : low();
       }
-      // scores in powers of two; keys that are not there count for nothing
-      float top[2] = {low(), low()};
+    }
+    bool moved = false;
+    float to[NT][2], shift[NT][2];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          c[n][e] *= scale;
-          if (good != 0xffffu && !(good >> (8 * n + 2 * t4 + (e & 1)) & 1)) c[n][e] = low();
-          top[e >> 1] = fmaxf(top[e >> 1], c[n][e]);
-        }
-      bool moved = false;
-      float to[2], shift[2];
+      for (int i = 0; i < 2; ++i) to[n][i] = fmaxf(c[n][i], c[n][2 + i]);
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) to[n][i] = fmaxf(to[n][i], __shfl_xor_sync(0xffffffffu, to[n][i], w));
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-        to[i] = fmaxf(m[i], top[i]);
-        moved |= to[i] != m[i];
-        shift[i] = to[i] == low() ? 0.f : to[i];  // nothing seen: all weights 2^-inf
+        to[n][i] = fmaxf(m[n][i], to[n][i]);
+        moved |= to[n][i] != m[n][i];
+        shift[n][i] = to[n][i] == low() ? 0.f : to[n][i];  // nothing seen: all weights 2^-inf
       }
-      if (__any_sync(0xffffffffu, moved)) {
-        const float f0 = ex2(m[0] - shift[0]), f1 = ex2(m[1] - shift[1]);
-        l[0] *= f0;
-        l[1] *= f1;
+    if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          o[j][0] *= f0;
-          o[j][1] *= f0;
-          o[j][2] *= f1;
-          o[j][3] *= f1;
-        }
-        m[0] = to[0];
-        m[1] = to[1];
-      }
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          c[n][e] = ex2(c[n][e] - shift[e >> 1]);
-          l[e >> 1] += c[n][e];
-        }
-      uint32_t p[4], rest[4];
-      p[0] = split2(c[0][0], c[0][1], rest[0]);
-      p[1] = split2(c[0][2], c[0][3], rest[1]);
-      p[2] = split2(c[1][0], c[1][1], rest[2]);
-      p[3] = split2(c[1][2], c[1][3], rest[3]);
-      {
-        const int r = lane & 15, half = lane >> 4;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          uint32_t b[4];
-          ldm4t(b, vbase + (r * C + ((2 * j + half) ^ (r & 7))) * 16);
-          mma(o[2 * j], p, b[0], b[1]);
-          mma(o[2 * j + 1], p, b[2], b[3]);
-          mma(o[2 * j], rest, b[0], b[1]);
-          mma(o[2 * j + 1], rest, b[2], b[3]);
-        }
-      }
-      __syncwarp();  // the ring's place is free for the copies of the next turn
-      stage = stage + 1 == S ? 0 : stage + 1;
-      ++u;
-      const bool pair_ends = at.unit + 1 == at.units;
-      if (pair_ends || u == w1) {
-        // the warps' parts become one: their maxima and sums, then their outputs two by two
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        }
-        if (t4 == 0) {
-          s.m[warp][g] = m[0];
-          s.m[warp][g + 8] = m[1];
-          s.l[warp][g] = l[0];
-          s.l[warp][g + 8] = l[1];
-        }
-        __syncthreads();
-        float M[2], L[2];
+          const float f = ex2(m[n][i] - shift[n][i]);
+          l[n][i] *= f;
+          m[n][i] = to[n][i];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = g + 8 * i;
-          M[i] = s.m[0][r];
-#pragma unroll
-          for (int w = 1; w < kWarps; ++w) M[i] = fmaxf(M[i], s.m[w][r]);
-          const float by = M[i] == low() ? 0.f : M[i];
-          L[i] = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) L[i] += s.l[w][r] * ex2(s.m[w][r] - by);
-          const float f = ex2(m[i] - by);
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            o[j][2 * i] *= f;
-            o[j][2 * i + 1] *= f;
+          for (int j = 0; j < D / 16; ++j) {
+            o[j][n][i] *= f;
+            o[j][n][2 + i] *= f;
           }
         }
-        auto place = [&](int slot, int r, int j) {
-          return reinterpret_cast<float2 *>(&s.out[slot][r * D + ((j * 8 + 2 * t4) ^ ((r & 3) << 3))]);
-        };
-        auto give = [&](int slot) {
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            *place(slot, g, j) = make_float2(o[j][0], o[j][1]);
-            if (rows > 8) *place(slot, g + 8, j) = make_float2(o[j][2], o[j][3]);
-          }
-        };
-        auto take = [&](int slot) {
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            const float2 x = *place(slot, g, j);
-            o[j][0] += x.x;
-            o[j][1] += x.y;
-            if (rows > 8) {
-              const float2 y = *place(slot, g + 8, j);
-              o[j][2] += y.x;
-              o[j][3] += y.y;
-            }
-          }
-        };
-        if (warp >= 2) give(warp - 2);
-        __syncthreads();
-        if (warp < 2) take(warp);
-        if (warp == 1) give(1);
-        __syncthreads();
-        if (warp == 0) {
-          take(1);
-          if (pair_ends && whole_start) {
-            __nv_bfloat16 *op = reinterpret_cast<__nv_bfloat16 *>(a.o.p) + at.b * a.o.st;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int h = row0 + g + 8 * i;
-              if (h >= G) continue;
-              const float inv = L[i] > 0.f ? 1.f / L[i] : L[i] == 0.f ? 0.f : L[i];
-              uint32_t *to_ = reinterpret_cast<uint32_t *>(op + (int64_t)(head * G + h) * a.o.sh);
-#pragma unroll
-              for (int j = 0; j < D / 8; ++j)
-                if (8 * j < a.d)
-                  to_[4 * j + t4] = pack2(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
-            }
-          } else {
-            // part 0: the pair that the range starts in; part 1: the one that it ends in
-            const bool first = u - (at.unit + 1) <= w0;
-            float *w = reinterpret_cast<float *>(a.work) +
-                       ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * kPart<D>;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int r = g + 8 * i;
-#pragma unroll
-              for (int j = 0; j < D / 8; ++j)
-                *reinterpret_cast<float2 *>(w + r * D + j * 8 + 2 * t4) =
-                    make_float2(o[j][2 * i], o[j][2 * i + 1]);
-              if (t4 == 0) {
-                w[kRows * D + r] = M[i];
-                w[kRows * D + kRows + r] = L[i];
-              }
-            }
-          }
-        }
-        fresh = true;
-        whole_start = true;
-      }
-      at.next(a, pairs);
     }
+    uint32_t p[NT][2], rest[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[n][i] = ex2(c[n][i] - shift[n][i & 1]);
+        l[n][i & 1] += c[n][i];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        p[n][i] = split2(c[n][2 * i], c[n][2 * i + 1], rest[n][i]);
+        p[n][i] = turned(p[n][i]);
+        rest[n][i] = turned(rest[n][i]);
+      }
+    }
+    {
+      const int r = (lane & 7) + (lane >> 4) * 8, half = lane >> 3 & 1;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t x[4];
+        ldm4t(x, vbase + (r * C + ((2 * j + half) ^ (r & 7))) * 16);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma(o[j][n], x, p[n][0], p[n][1]);
+          mma(o[j][n], x, rest[n][0], rest[n][1]);
+        }
+      }
+    }
+    __syncwarp();  // the ring's place is free for the copies of the next turn
+    stage = stage + 1 == S ? 0 : stage + 1;
+    ++u;
+    const bool pair_ends = at.unit + 1 == at.units;
+    if (pair_ends || u == w1) {
+      // the warps' parts become one: their maxima and sums, then their outputs two by two
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          for (int w = 4; w < 32; w <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], w);
+          if (g == 0) {
+            s.m[warp][n * 8 + 2 * t4 + i] = m[n][i];
+            s.l[warp][n * 8 + 2 * t4 + i] = l[n][i];
+          }
+        }
+      __syncthreads();
+      auto most = [&](int h) {
+        float v = s.m[0][h];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) v = fmaxf(v, s.m[w][h]);
+        return v;
+      };
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float M = most(n * 8 + 2 * t4 + i), f = ex2(m[n][i] - (M == low() ? 0.f : M));
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            o[j][n][i] *= f;
+            o[j][n][2 + i] *= f;
+          }
+        }
+      float *mine = s.out[warp & 1];
+#pragma unroll
+      for (int turn = 0; turn < 2; ++turn) {
+        if (warp >> 1 == 1 - turn) {
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float &to_ = mine[Smem::at(n * 8 + 2 * t4 + (i & 1), 16 * j + (i >> 1) * 8 + g)];
+                to_ = turn == 0 ? o[j][n][i] : to_ + o[j][n][i];
+              }
+        }
+        __syncthreads();
+      }
+      const int rows = min(H, G - row0);
+      const bool done = pair_ends && whole_start;
+      // part 0: the pair that the range starts in; part 1: the one that it ends in
+      float *part = reinterpret_cast<float *>(a.work) +
+                    ((int64_t)blockIdx.x * 2 + (u - (at.unit + 1) <= w0 ? 0 : 1)) * kPart<D>;
+      for (int i = threadIdx.x; i < rows * (D / 2); i += kWarps * 32) {
+        const int h = i / (D / 2), col = i % (D / 2) * 2, from = Smem::at(h, col);
+        const float x = s.out[0][from] + s.out[1][from], y = s.out[0][from + 1] + s.out[1][from + 1];
+        const float M = most(h), by = M == low() ? 0.f : M;
+        float L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) L += s.l[w][h] * ex2(s.m[w][h] - by);
+        if (done) {
+          const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
+          if (col < a.d) {
+            __nv_bfloat16 *op = reinterpret_cast<__nv_bfloat16 *>(a.o.p) + at.b * a.o.st;
+            *reinterpret_cast<uint32_t *>(op + (int64_t)(head * G + row0 + h) * a.o.sh + col) =
+                pack2(x * inv, y * inv);
+          }
+        } else {
+          *reinterpret_cast<float2 *>(part + h * D + col) = make_float2(x, y);
+          if (col == 0) {
+            part[kRows * D + h] = M;
+            part[kRows * D + kRows + h] = L;
+          }
+        }
+      }
+      fresh = true;
+      whole_start = true;
+      __syncthreads();  // what the warps left for one another has been read
+    }
+    at.next(a, pairs);
   }
   copies_wait<0>();
 }
@@ -482,14 +499,14 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
 // Joins the parts of the pairs that lie in several ranges, one block a pair and query head; rows
 // without keys get zeros.  The warps take every fourth part, a lane D / 32 columns.
 template <int D>
-__global__ void __launch_bounds__(128) k_attn_join(const AttnArgs a, int groups, int ctas, int rows) {
+__global__ void __launch_bounds__(128) k_attn_join(const AttnArgs a, int groups, int per_group, int ctas, int rows) {
   after_previous<true>();
   constexpr int N = D / 32;
   __shared__ int64_t red[32];
   __shared__ float ms[4], ls[4], os[4][D];
   const int pairs = a.Hk * groups, G = a.Hq / a.Hk;
   const int r = blockIdx.x % rows, b = blockIdx.x / rows / pairs, pair = blockIdx.x / rows % pairs;
-  const int head = pair / groups, h = pair % groups * kRows + r;
+  const int head = pair / groups, h = pair % groups * per_group + r;
   if (h >= G) return;
   int64_t all, before;
   count_units(a, b, red, all, before);
@@ -626,23 +643,22 @@ __global__ void __launch_bounds__(kPlainWarps * 32) k_attn_plain(const AttnArgs 
 // ------------------------------------------------------------------ launches
 
 int wide_for(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
-int ctas_for(int D) { return min(kMostCtas, sm_count() * (D == 256 ? 1 : 2)); }
+int ctas_for(int D, int H) { return min(kMostCtas, sm_count() * attn_per_sm(D, H)); }
 
-template <int D, int S>
+template <int D, int H, int S>
 cudaError_t run_split(const AttnArgs &a, cudaStream_t stream) {
-  const int G = a.Hq / a.Hk, groups = (G + kRows - 1) / kRows, ctas = ctas_for(D);
-  constexpr int smem = sizeof(AttnSmem<D, S>);
-  static_assert(smem <= (D == 256 ? 227 : 113) * 1024, "shared memory of a block");
+  const int G = a.Hq / a.Hk, groups = (G + H - 1) / H, ctas = ctas_for(D, H);
+  constexpr int smem = sizeof(AttnSmem<D, H, S>);
+  static_assert((smem + 1024) * attn_per_sm(D, H) <= 228 * 1024, "shared memory of the blocks");
   static std::atomic<uint64_t> done{0};
   cudaError_t e =
-      set_once(k_attn_split<D, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, done);
+      set_once(k_attn_split<D, H, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem, done);
   if (e != cudaSuccess) return e;
-  e = launch(k_attn_split<D, S>, (unsigned)ctas, kWarps * 32, smem, stream, a, groups,
-             G < kRows ? G : kRows);
+  e = launch(k_attn_split<D, H, S>, (unsigned)ctas, kWarps * 32, smem, stream, a, groups);
   if (e != cudaSuccess) return e;
-  const int rows = G < kRows ? G : kRows;
-  return launch(k_attn_join<D>, (unsigned)((int64_t)a.B * a.Hk * groups * rows), 128, 0, stream, a, groups,
-                ctas, rows);
+  const int rows = G < H ? G : H;
+  return launch(k_attn_join<D>, (unsigned)((int64_t)a.B * a.Hk * groups * rows), 128, 0, stream, a,
+                groups, H, ctas, rows);
 }
 
 bool fits16(const Pages &h) {
@@ -657,16 +673,21 @@ bool fits4(const Heads &h) {
 
 size_t attn_workspace(int32_t B, int32_t Hq, int32_t Hk, int32_t d) {
   const int D = mix::wide_for(d);
-  return align256((size_t)mix::ctas_for(D) * 2 * (mix::kRows * D + 2 * mix::kRows) * 4);
+  return align256((size_t)mix::ctas_for(D, 8) * 2 * (mix::kRows * D + 2 * mix::kRows) * 4);
 }
 
 cudaError_t launch_attn_step(const AttnArgs &a, cudaStream_t stream) {
   if (a.B == 0) return cudaSuccess;
   if (!a.f32 && a.d % 8 == 0 && mix::fits16(a.k) && mix::fits16(a.v) && mix::fits4(a.q) &&
       mix::fits4(a.o)) {
-    if (a.d <= 64) return mix::run_split<64, 5>(a, stream);
-    if (a.d <= 128) return mix::run_split<128, 3>(a, stream);
-    return mix::run_split<256, 3>(a, stream);
+    if (a.Hq / a.Hk <= 8) {
+      if (a.d <= 64) return mix::run_split<64, 8, 4>(a, stream);
+      if (a.d <= 128) return mix::run_split<128, 8, 2>(a, stream);
+      return mix::run_split<256, 8, 3>(a, stream);
+    }
+    if (a.d <= 64) return mix::run_split<64, 16, 5>(a, stream);
+    if (a.d <= 128) return mix::run_split<128, 16, 3>(a, stream);
+    return mix::run_split<256, 16, 2>(a, stream);
   }
   const unsigned blocks = (unsigned)((int64_t)a.B * a.Hq);
   return a.f32 ? mix::launch(mix::k_attn_plain<float>, blocks, mix::kPlainWarps * 32, 0, stream, a)
