@@ -497,13 +497,15 @@ __global__ void __launch_bounds__(kWarps * 32, attn_per_sm(D, H))
 }
 
 // Joins the parts of the pairs that lie in several ranges, one block a pair and query head; rows
-// without keys get zeros.  The warps take every fourth part, a lane D / 32 columns.
+// without keys get zeros.  The warps take every eighth part, a lane D / 32 columns.
+constexpr int kJoin = 8;  // warps
+
 template <int D>
-__global__ void __launch_bounds__(128) k_attn_join(const AttnArgs a, int groups, int per_group, int ctas, int rows) {
+__global__ void __launch_bounds__(kJoin * 32) k_attn_join(const AttnArgs a, int groups, int per_group, int ctas, int rows) {
   after_previous<true>();
   constexpr int N = D / 32;
   __shared__ int64_t red[32];
-  __shared__ float ms[4], ls[4], os[4][D];
+  __shared__ float ms[kJoin], ls[kJoin], os[kJoin][D];
   const int pairs = a.Hk * groups, G = a.Hq / a.Hk;
   const int r = blockIdx.x % rows, b = blockIdx.x / rows / pairs, pair = blockIdx.x / rows % pairs;
   const int head = pair / groups, h = pair % groups * per_group + r;
@@ -520,11 +522,11 @@ __global__ void __launch_bounds__(128) k_attn_join(const AttnArgs a, int groups,
   if (units > 0) {
     // a range's part 0 is the pair that it starts in, part 1 the one that it ends in
     const float *w = reinterpret_cast<const float *>(a.work) + (u0 > c0 * share ? kPart<D> : 0);
-    for (int64_t c = c0 + warp; c <= c1; c += 16) {
+    for (int64_t c = c0 + warp; c <= c1; c += 4 * kJoin) {
       float pm[4], pl[4], po[4][N];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t at = c + 4 * i;
+        const int64_t at = c + kJoin * i;
         const float *p = (at == c0 ? w : reinterpret_cast<const float *>(a.work)) + at * 2 * kPart<D>;
         const bool in = at <= c1;
         pm[i] = in ? p[kRows * D + r] : low();
@@ -556,21 +558,23 @@ __global__ void __launch_bounds__(128) k_attn_join(const AttnArgs a, int groups,
 #pragma unroll
   for (int j = 0; j < N; ++j) os[warp][j * 32 + lane] = acc[j];
   __syncthreads();
-  m = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
+  m = ms[0];
+#pragma unroll
+  for (int w = 1; w < kJoin; ++w) m = fmaxf(m, ms[w]);
   const float by = m == low() ? 0.f : m;
-  float f[4];
+  float f[kJoin];
   l = 0.f;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < kJoin; ++w) {
     f[w] = ex2(ms[w] - by);
     l = fmaf(ls[w], f[w], l);
   }
   const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
   __nv_bfloat16 *op = reinterpret_cast<__nv_bfloat16 *>(a.o.p) + b * a.o.st + (int64_t)(head * G + h) * a.o.sh;
-  for (int c = threadIdx.x; c < a.d; c += 128) {
+  for (int c = threadIdx.x; c < a.d; c += kJoin * 32) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) v = fmaf(os[w][c], f[w], v);
+    for (int w = 0; w < kJoin; ++w) v = fmaf(os[w][c], f[w], v);
     op[c] = __float2bfloat16_rn(v * inv);
   }
 }
@@ -657,7 +661,7 @@ cudaError_t run_split(const AttnArgs &a, cudaStream_t stream) {
   e = launch(k_attn_split<D, H, S>, (unsigned)ctas, kWarps * 32, smem, stream, a, groups);
   if (e != cudaSuccess) return e;
   const int rows = G < H ? G : H;
-  return launch(k_attn_join<D>, (unsigned)((int64_t)a.B * a.Hk * groups * rows), 128, 0, stream, a,
+  return launch(k_attn_join<D>, (unsigned)((int64_t)a.B * a.Hk * groups * rows), kJoin * 32, 0, stream, a,
                 groups, H, ctas, rows);
 }
 

@@ -60,28 +60,60 @@ __device__ __forceinline__ void params8(const Param &w, int64_t c, int n, float 
   }
 }
 
-// out[c] = the sum of parts[b][c] over n blocks, in order: eight warps take every eighth.
-__global__ void __launch_bounds__(256) k_sum_parts(const float *parts, int n, int64_t stride,
-                                                   int count, float *out0, float *out1,
-                                                   float *out2) {
+__device__ __forceinline__ f2 twice(float v) { return pair(v, v); }
+__device__ __forceinline__ float total(f2 v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return lo + hi;
+}
+
+// 8 parameters from column c on in pairs; null: ones.
+template <bool VEC>
+__device__ __forceinline__ void params4(const Param &w, int64_t c, int n, f2 (&f)[4]) {
+  float v[8];
+  params8<VEC>(w, c, n, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = pair(v[2 * i], v[2 * i + 1]);
+}
+// r (e - n mean(e n)) for a row of up to 8 columns in one thread (row_back), in pairs
+__device__ __forceinline__ void row_back(const f2 (&x)[4], const f2 (&e)[4], int columns, float eps,
+                                         f2 (&out)[4]) {
+  float xs[8], es[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    unpair(x[i], xs[2 * i], xs[2 * i + 1]);
+    unpair(e[i], es[2 * i], es[2 * i + 1]);
+  }
+  row_back(xs, es, columns, eps, es);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = pair(es[2 * i], es[2 * i + 1]);
+}
+
+// out[c] = the sum of parts[b][c] over n blocks, in order: 32 warps take every 32nd.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32) k_sum_parts(const float *parts, int n, int64_t stride,
+                                                              int count, float *out0, float *out1,
+                                                              float *out2) {
   after_previous();
-  __shared__ float red[8][33];
+  __shared__ float red[kSumWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  float *out = blockIdx.y == 0 ? out0 : blockIdx.y == 1 ? out1 : out2;
+  if (!out) return;
   const float *p = parts + (int64_t)blockIdx.y * count + c;
   float v = 0.f;
   if (c < count) {
-#pragma unroll 4
-    for (int b = warp; b < n; b += 8) v += p[b * stride];
+#pragma unroll 8
+    for (int b = warp; b < n; b += kSumWarps) v += p[b * stride];
   }
   red[warp][lane] = v;
   __syncthreads();
-  float *out = blockIdx.y == 0 ? out0 : blockIdx.y == 1 ? out1 : out2;
-  if (warp == 0 && c < count && out) {
+  // a warp a column: its parts' sums by a butterfly
+  v = red[lane][warp];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) v += red[w][lane];
-    out[c] = v;
-  }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int col = blockIdx.x * 32 + warp;
+  if (lane == 0 && col < count) out[col] = v;
 }
 
 // ------------------------------------------------------------------ gated norm of heads
@@ -169,85 +201,120 @@ __global__ void __launch_bounds__(kGated) k_gated_fwd(const GatedArgs a, int64_t
   }
 }
 
+// Rows come by cp.async into a ring in which each thread reads only what it copied itself, `depth` of
+// them (0: rows are loaded when they are used); products in pairs.
 template <typename E, int TPR, int NV, bool VEC>
-__global__ void __launch_bounds__(kGated) k_gated_bwd(const GatedArgs a, int64_t turns) {
+__global__ void __launch_bounds__(kGated, NV == 4 ? 1 : 2) k_gated_bwd(const GatedArgs a, int64_t turns, int depth) {
   after_previous();
-  constexpr int RB = kGated / TPR;
-  extern __shared__ float sums[];  // [RB][TPR * NV * 8]
+  constexpr int RB = kGated / TPR, P = sizeof(E) / 2;
+  extern __shared__ __align__(16) uint4 ring[];  // then the blocks' parts of dw
   const int gl = threadIdx.x % TPR, group = threadIdx.x / TPR;
-  Walk at(a.T, a.H, (int64_t)blockIdx.x * RB + group, (int64_t)gridDim.x * RB);
-  float w[NV][8], dw[NV][8];
+  Walk at(a.T, a.H, (int64_t)blockIdx.x * RB + group, (int64_t)gridDim.x * RB), ahead = at;
+  f2 w[NV][4], dw[NV][4];
   int n[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (gl + j * TPR) * 8;
     n[j] = max(0, min(8, a.d - c));
-    params8<VEC>(a.w, c, n[j], w[j]);
+    params4<VEC>(a.w, c, n[j], w[j]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dw[j][k] = 0.f;
+    for (int i = 0; i < 4; ++i) dw[j][i] = twice(0.f);
   }
-  const float inv = 1.f / a.d;
-  Raw8<E> x[NV], z[NV], dy[NV];
-  auto load = [&] {
+  auto place = [&](int s, int unit) { return ring + (s * 3 * NV * P + unit) * kGated + threadIdx.x; };
+  auto issue = [&](int s) {
+    if (VEC && ahead.ok()) {
+      const E *p[3] = {row_of<E>(a.x, ahead), row_of<E>(a.z, ahead), row_of<E>(a.dy, ahead)};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (gl + j * TPR) * 8, m = at.ok() ? n[j] : 0;
-      x[j] = ld8<VEC>(row_of<E>(a.x, at) + c, m);
-      z[j] = ld8<VEC>(row_of<E>(a.z, at) + c, m);
-      dy[j] = ld8<VEC>(row_of<E>(a.dy, at) + c, m);
+      for (int j = 0; j < NV; ++j)
+        if (n[j] > 0) {
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+              copy16(place(s, (j * 3 + k) * P + i), p[k] + (gl + j * TPR) * 8 + i * (16 / sizeof(E)));
+        }
     }
+    copies_commit();
+    ahead.next();
   };
-  load();
-  for (int64_t i = 0; i < turns; ++i) {
-    const Walk now = at;
-    float xs[NV][8], zs[NV][8], gs[NV][8];
-    float2 sum = make_float2(0.f, 0.f);
+  auto get = [&](int s, int j, int k, const Heads &m) {
+    Raw8<E> r = zero8<E>();
+    if (VEC) {
+      uint4 *q = reinterpret_cast<uint4 *>(&r);
+      if (at.ok() && n[j] > 0) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      unpack8(x[j], xs[j]);
-      unpack8(z[j], zs[j]);
-      unpack8(dy[j], gs[j]);
+        for (int i = 0; i < P; ++i) q[i] = *place(s, (j * 3 + k) * P + i);
+      }
+    } else {
+      r = ld8<VEC>(row_of<E>(m, at) + (gl + j * TPR) * 8, at.ok() ? n[j] : 0);
     }
-    at.next();
-    load();
-    float f[NV][8];  // f(z), then f'(z) dy w x
+    return r;
+  };
+  if (VEC)
+    for (int s = 0; s < depth - 1; ++s) issue(s);
+  const float inv = 1.f / a.d;
+  int stage = 0;
+  for (int64_t t = 0; t < turns; ++t) {
+    if (VEC) {
+      issue(stage == 0 ? depth - 1 : stage - 1);
+      if (depth >= 4) copies_wait<3>();
+      else if (depth == 3) copies_wait<2>();
+      else if (depth == 2) copies_wait<1>();
+      else copies_wait<0>();
+    }
+    f2 x[NV][4], e[NV][4], f[NV][4], d[NV][4];  // x; dy w f(z); dy w f'(z) x; dy f(z) x
+    f2 q = twice(0.f), p = twice(0.f);
+    const f2 one = twice(1.f), minus = twice(-1.f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      f2 z[4];
+      unpack4(get(stage, j, 0, a.x), x[j]);
+      unpack4(get(stage, j, 1, a.z), z);
+      unpack4(get(stage, j, 2, a.dy), e[j]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float s = sigmoidf(zs[j][k]), v = a.silu ? zs[j][k] * s : s;
-        const float dv = a.silu ? dsilu(zs[j][k], s) : s * (1.f - s);
-        const float q = gs[j][k] * xs[j][k];  // dy x
-        f[j][k] = q * w[j][k] * dv;
-        zs[j][k] = q * v;              // dw's term but for r
-        gs[j][k] = gs[j][k] * w[j][k] * v;  // e
-        sum.x = fmaf(xs[j][k], xs[j][k], sum.x);
-        sum.y = fmaf(gs[j][k], xs[j][k], sum.y);
+      for (int i = 0; i < 4; ++i) {
+        const f2 s = sigmoid2(z[i]), g = a.silu ? mul2(z[i], s) : s;
+        const f2 dg = a.silu ? dsilu2(z[i], s) : mul2(s, fma2(s, minus, one));
+        const f2 yx = mul2(e[j][i], x[j][i]);
+        d[j][i] = mul2(yx, g);
+        f[j][i] = mul2(mul2(yx, w[j][i]), dg);
+        e[j][i] = mul2(mul2(e[j][i], w[j][i]), g);
+        q = fma2(x[j][i], x[j][i], q);
+        p = fma2(e[j][i], x[j][i], p);
       }
-    sum = lane_sum2<TPR>(sum);
-    const float r = rsqrtf(fmaf(sum.x, inv, a.eps));
+    }
+    stage = stage + 1 >= depth ? 0 : stage + 1;
+    const float2 sum = lane_sum2<TPR>(make_float2(total(q), total(p)));
+    const Walk now = at;
+    at.next();
     if (!now.ok()) continue;
-    const float back = r * r * sum.y * inv;
+    const float r = rsqrtf(fmaf(sum.x, inv, a.eps)), back = r * r * sum.y * inv;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        dw[j][k] = fmaf(zs[j][k], r, dw[j][k]);
-        f[j][k] *= r;
-        if (TPR > 1) xs[j][k] = r * fmaf(-xs[j][k], back, gs[j][k]);
+      for (int i = 0; i < 4; ++i) {
+        dw[j][i] = fma2(d[j][i], twice(r), dw[j][i]);
+        f[j][i] = mul2(f[j][i], twice(r));
+        if (TPR > 1) e[j][i] = mul2(twice(r), fma2(x[j][i], twice(-back), e[j][i]));
       }
-      if (TPR == 1) row_back(xs[j], gs[j], a.d, a.eps, xs[j]);
+      if (TPR == 1) row_back(x[j], e[j], a.d, a.eps, e[j]);
       const int c = (gl + j * TPR) * 8;
-      st8<VEC>(row_of<E>(a.dx, now) + c, pack8(xs[j], E{}), n[j]);
-      st8<VEC>(row_of<E>(a.dz, now) + c, pack8(f[j], E{}), n[j]);
+      st8<VEC>(row_of<E>(a.dx, now) + c, pack4<E>(e[j]), n[j]);
+      st8<VEC>(row_of<E>(a.dz, now) + c, pack4<E>(f[j]), n[j]);
     }
   }
   if (!a.dw) return;
   constexpr int L = TPR * NV * 8;
+  float *sums = reinterpret_cast<float *>(ring);  // [RB][L]
+  copies_wait<0>();
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sums[group * L + (gl + j * TPR) * 8 + k] = dw[j][k];
+    for (int i = 0; i < 4; ++i) {
+      float *to = sums + group * L + (gl + j * TPR) * 8 + 2 * i;
+      unpair(dw[j][i], to[0], to[1]);
+    }
   __syncthreads();
   float *out = reinterpret_cast<float *>(a.work) + (int64_t)blockIdx.x * a.d;
   for (int c = threadIdx.x; c < a.d; c += kGated) {
@@ -276,7 +343,7 @@ int64_t gated_blocks(int64_t rows, int rows_per_block, int per_sm) {
   const int64_t most = (int64_t)sm_count() * per_sm, need = ceil_div64(rows, rows_per_block);
   return need < most ? need : most;
 }
-constexpr int kGatedPerSm = 8, kGatedBwdPerSm = 3;
+constexpr int kGatedPerSm = 8, kGatedBwdPerSm = 2;
 
 template <typename E, int TPR, int NV, bool VEC>
 cudaError_t run_gated(const GatedArgs &a, bool bwd, cudaStream_t stream) {
@@ -287,12 +354,22 @@ cudaError_t run_gated(const GatedArgs &a, bool bwd, cudaStream_t stream) {
     return launch(k_gated_fwd<E, TPR, NV, VEC>, (unsigned)blocks, kGated, 0, stream, a,
                   ceil_div64(rows, blocks * RB));
   }
-  const int64_t blocks = gated_blocks(rows, RB, kGatedBwdPerSm);
-  const int smem = a.dw ? RB * TPR * NV * 8 * 4 : 0;
-  cudaError_t e = launch(k_gated_bwd<E, TPR, NV, VEC>, (unsigned)blocks, kGated, smem, stream, a,
-                         ceil_div64(rows, blocks * RB));
+  const int64_t blocks = gated_blocks(rows, RB, kGatedBwdPerSm), turns = ceil_div64(rows, blocks * RB);
+  // rows ahead: up to four, what shared memory holds, and no more than a block has
+  constexpr int unit = 3 * NV * (int)sizeof(E) / 2 * kGated * 16, fit = 96 * 1024 / unit;
+  static_assert(fit >= 1, "a row fits");
+  const int depth = !VEC ? 0 : turns < (fit < 4 ? fit : 4) ? (int)turns : fit < 4 ? fit : 4;
+  constexpr int sums = RB * TPR * NV * 8 * 4;
+  const int smem = depth * unit > sums ? depth * unit : sums;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = set_once(k_gated_bwd<E, TPR, NV, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024,
+                 done);
+  if (e != cudaSuccess) return e;
+  e = launch(k_gated_bwd<E, TPR, NV, VEC>, (unsigned)blocks, kGated, smem, stream, a, turns, depth);
   if (e != cudaSuccess || !a.dw) return e;
-  return launch(k_sum_parts, dim3((unsigned)((a.d + 31) / 32)), 256, 0, stream,
+  return launch(k_sum_parts, dim3((unsigned)((a.d + 31) / 32)), kSumWarps * 32, 0, stream,
                 reinterpret_cast<const float *>(a.work), (int)blocks, (int64_t)a.d, a.d, a.dw,
                 (float *)nullptr, (float *)nullptr);
 }
@@ -325,13 +402,6 @@ cudaError_t run_gated_for(const GatedArgs &a, bool bwd, cudaStream_t stream) {
 // which each thread reads only what it copied itself, and stay packed in registers; products are in
 // pairs.
 
-__device__ __forceinline__ f2 twice(float v) { return pair(v, v); }
-__device__ __forceinline__ float total(f2 v) {
-  float lo, hi;
-  unpair(v, lo, hi);
-  return lo + hi;
-}
-
 // Sums over the threads of a row, in all of them.  With whole blocks `phase` names one of two places in
 // red (which the next sum must not share).
 template <int LANES>
@@ -356,14 +426,6 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2 (*red)[32], int &pha
   return v;
 }
 
-// 8 parameters from column c on in pairs; null: ones.
-template <bool VEC>
-__device__ __forceinline__ void params4(const Param &w, int64_t c, int n, f2 (&f)[4]) {
-  float v[8];
-  params8<VEC>(w, c, n, v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = pair(v[2 * i], v[2 * i + 1]);
-}
 // Columns behind the row's end (their parameters are zeros, or ones where there are none): zeros.
 __device__ __forceinline__ void keep(f2 (&f)[4], int n) {
 #pragma unroll
@@ -546,20 +608,6 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, LANES ? 1 : 2)
     }
   }
   if (VEC) copies_wait<0>();
-}
-
-// r (e - n mean(e n)) for a row of up to 8 columns in one thread (row_back), in pairs
-__device__ __forceinline__ void row_back(const f2 (&x)[4], const f2 (&e)[4], int columns, float eps,
-                                         f2 (&out)[4]) {
-  float xs[8], es[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    unpair(x[i], xs[2 * i], xs[2 * i + 1]);
-    unpair(e[i], es[2 * i], es[2 * i + 1]);
-  }
-  row_back(xs, es, columns, eps, es);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) out[i] = pair(es[2 * i], es[2 * i + 1]);
 }
 
 template <typename E, typename R, int LANES, int NV, bool VEC>
@@ -1088,7 +1136,8 @@ cudaError_t run_resid_long(const ResidArgs &a, bool bwd, cudaStream_t stream) {
     return launch(k_resid_fwd_long<E, R, LANES, NV, VEC>, (unsigned)blocks, th, smem, stream, a, depth);
   e = launch(k_resid_bwd_long<E, R, LANES, NV, VEC>, (unsigned)blocks, th, smem, stream, a, depth);
   if (e != cudaSuccess || !(a.dw || a.dwp || a.dg)) return e;
-  return launch(k_sum_parts, dim3((unsigned)((a.C + 31) / 32), 3), 256, 0, stream,
+  return launch(k_sum_parts, dim3((unsigned)((a.C + 31) / 32), 3), kSumWarps * 32, 0,
+                stream,
                 reinterpret_cast<const float *>(a.work), (int)blocks, (int64_t)3 * a.C, a.C, a.dw,
                 a.dwp, a.dg);
 }
@@ -1119,7 +1168,8 @@ cudaError_t run_resid(const ResidArgs &a, bool bwd, cudaStream_t stream) {
   if (!bwd) return launch(k_resid_fwd<E, R, LANES, NR>, (unsigned)blocks, th, smem, stream, a, depth);
   e = launch(k_resid_bwd<E, R, LANES, NR>, (unsigned)blocks, th, smem, stream, a, depth);
   if (e != cudaSuccess || !(a.dw || a.dwp || a.dg)) return e;
-  return launch(k_sum_parts, dim3((unsigned)((a.C + 31) / 32), 3), 256, 0, stream,
+  return launch(k_sum_parts, dim3((unsigned)((a.C + 31) / 32), 3), kSumWarps * 32, 0,
+                stream,
                 reinterpret_cast<const float *>(a.work), (int)blocks, (int64_t)3 * a.C, a.C, a.dw,
                 a.dwp, a.dg);
 }
