@@ -133,29 +133,42 @@ __global__ void __launch_bounds__(256) k_cache_slots(const PlanArgs a) {
   a.slots[t] = slot;
 }
 
-// U: a unit of copying.  A warp a token: its heads' units of keys and values side by side.
+// U: a unit of copying.  A warp a token: four units a lane of keys and of values are on their way
+// before the slot is looked at.
 template <typename U>
 __global__ void __launch_bounds__(256) k_cache_write(const WriteArgs a, int per_head) {
   after_previous<true>();
   const int lane = threadIdx.x & 31, units = a.Hk * per_head;
   constexpr int E = sizeof(U);
   const int e = a.f32 ? 4 : 2;
-  for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < a.T; t += (int64_t)gridDim.x * 8) {
+  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t < a.T) {
     const int slot = a.slots[t];
-    if (slot < 0 || slot / a.page >= a.pages) continue;
-    const int page = slot / a.page, place = slot % a.page;
     const char *k = reinterpret_cast<const char *>(a.k.p) + t * a.k.st * e;
     const char *v = reinterpret_cast<const char *>(a.v.p) + t * a.v.st * e;
-    char *kc = reinterpret_cast<char *>(a.kc.p) + (page * a.kc.sp + place * a.kc.st) * e;
-    char *vc = reinterpret_cast<char *>(a.vc.p) + (page * a.vc.sp + place * a.vc.st) * e;
-#pragma unroll 4
-    for (int i = lane; i < units; i += 32) {
-      const int h = i / per_head;
-      const int64_t c = (int64_t)(i - h * per_head) * E;
-      const U x = *reinterpret_cast<const U *>(k + h * a.k.sh * e + c);
-      const U y = *reinterpret_cast<const U *>(v + h * a.v.sh * e + c);
-      *reinterpret_cast<U *>(kc + h * a.kc.sh * e + c) = x;
-      *reinterpret_cast<U *>(vc + h * a.vc.sh * e + c) = y;
+    for (int base = 0; base < units; base += 128) {
+      U x[4], y[4];
+      int h[4];
+      int64_t c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = base + j * 32 + lane;
+        if (i >= units) continue;
+        h[j] = i / per_head;
+        c[j] = (int64_t)(i - h[j] * per_head) * E;
+        x[j] = *reinterpret_cast<const U *>(k + h[j] * a.k.sh * e + c[j]);
+        y[j] = *reinterpret_cast<const U *>(v + h[j] * a.v.sh * e + c[j]);
+      }
+      const int page = slot / a.page, place = slot % a.page;
+      if (slot < 0 || page >= a.pages) break;
+      char *kc = reinterpret_cast<char *>(a.kc.p) + (page * a.kc.sp + place * a.kc.st) * e;
+      char *vc = reinterpret_cast<char *>(a.vc.p) + (page * a.vc.sp + place * a.vc.st) * e;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (base + j * 32 + lane >= units) continue;
+        *reinterpret_cast<U *>(kc + h[j] * a.kc.sh * e + c[j]) = x[j];
+        *reinterpret_cast<U *>(vc + h[j] * a.vc.sh * e + c[j]) = y[j];
+      }
     }
   }
 }
@@ -183,8 +196,7 @@ cudaError_t launch_cache_plan(const PlanArgs &a, cudaStream_t stream) {
 cudaError_t launch_cache_write(const WriteArgs &a, cudaStream_t stream) {
   if (a.T == 0 || a.pages == 0) return cudaSuccess;
   const int e = a.f32 ? 4 : 2;
-  const int64_t need = ceil_div64(a.T, 8), most = (int64_t)mix::sm_count() * 8;
-  const unsigned grid = (unsigned)(need < most ? need : most);
+  const unsigned grid = (unsigned)ceil_div64(a.T, 8);
   if (a.d * e % 16 == 0 && mix::fits16(a.k, e) && mix::fits16(a.v, e) && mix::fits16(a.kc, e) &&
       mix::fits16(a.vc, e))
     return mix::launch(mix::k_cache_write<uint4>, grid, 256, 0, stream, a, a.d * e / 16);

@@ -152,8 +152,11 @@ __device__ __forceinline__ float gate_of(float z, int silu) {
   return silu ? z * s : s;
 }
 
+// Blocks of the forward on each multiprocessor: all run at once.
+constexpr int gated_per_sm(int NV) { return NV == 1 ? 5 : NV == 2 ? 3 : 1; }
+
 template <typename E, int TPR, int NV, bool VEC>
-__global__ void __launch_bounds__(kGated) k_gated_fwd(const GatedArgs a, int64_t turns) {
+__global__ void __launch_bounds__(kGated, gated_per_sm(NV)) k_gated_fwd(const GatedArgs a, int64_t turns) {
   after_previous();
   constexpr int RB = kGated / TPR;
   const int gl = threadIdx.x % TPR;
@@ -343,14 +346,14 @@ int64_t gated_blocks(int64_t rows, int rows_per_block, int per_sm) {
   const int64_t most = (int64_t)sm_count() * per_sm, need = ceil_div64(rows, rows_per_block);
   return need < most ? need : most;
 }
-constexpr int kGatedPerSm = 8, kGatedBwdPerSm = 2;
+constexpr int kGatedBwdPerSm = 2;
 
 template <typename E, int TPR, int NV, bool VEC>
 cudaError_t run_gated(const GatedArgs &a, bool bwd, cudaStream_t stream) {
   constexpr int RB = kGated / TPR;
   const int64_t rows = (int64_t)a.T * a.H;
   if (!bwd) {
-    const int64_t blocks = gated_blocks(rows, RB, kGatedPerSm);
+    const int64_t blocks = gated_blocks(rows, RB, gated_per_sm(NV));
     return launch(k_gated_fwd<E, TPR, NV, VEC>, (unsigned)blocks, kGated, 0, stream, a,
                   ceil_div64(rows, blocks * RB));
   }
