@@ -106,35 +106,49 @@ __device__ __forceinline__ f2 wide(const Raw2<E> &r) {
   return pair(r.lo(), r.hi());
 }
 
-// sqrt(1 - a^2) from L2 = log2 a: next to a = 1 by the series of 1 - 2^(2 L2) (the first term left out is
-// 4e-8 of it at the border, 2 ln a = -1/8), which keeps its relative accuracy there; else as it is
-// written.  NaN for a > 1 (A > 0).
-__device__ __forceinline__ f2 root_of(f2 L2, f2 a) {
-  f2 p = fma2(L2, both(-0.042667211f), both(-0.15389006f));
-  p = fma2(p, L2, both(-0.44403294f));
-  p = fma2(p, L2, both(-0.96090603f));
-  p = fma2(p, L2, both(-1.3862944f));
-  float lo, hi, l0, l1, a0, a1;
-  unpair(mul2(p, L2), lo, hi);
+// a = 2^L2 and 1 - a^2.  Next to a = 1 both come from the series of d = 1 - a (the first term left out is
+// 1e-9 of it at the border, ln a = -1/16): the special-function unit's 2^x falls short by 2e-8 on
+// average, which a state that lasts for hundreds of tokens adds up, and 1 - a^2 would lose its
+// relative accuracy (8,192 x 2,560: error of dA 6.2e-6 of its norm without the series for a).  Nothing
+// is added to a state with A = 0, and nothing taken from it: d = 0.
+__device__ __forceinline__ f2 short_of_one(f2 L2) {
+  f2 p = fma2(L2, both(-0.0013333558f), both(-0.0096181291f));
+  p = fma2(p, L2, both(-0.055504109f));
+  p = fma2(p, L2, both(-0.24022651f));
+  p = fma2(p, L2, both(-0.69314718f));
+  return mul2(p, L2);
+}
+constexpr float kNear = -0.09016844f;  // L2 above: the series
+__device__ __forceinline__ f2 decay_of(f2 L2) {
+  const f2 near = fma2(short_of_one(L2), both(-1.f), both(1.f));
+  float l0, l1, n0, n1;
   unpair(L2, l0, l1);
-  unpair(a, a0, a1);
-  return pair(sqrt_approx(l0 > -0.0901684f ? lo : fmaf(-a0, a0, 1.f)),
-              sqrt_approx(l1 > -0.0901684f ? hi : fmaf(-a1, a1, 1.f)));
+  unpair(near, n0, n1);
+  return pair(l0 > kNear ? n0 : ex2(l0), l1 > kNear ? n1 : ex2(l1));
 }
 
 struct Token {
   f2 sr, a, m;
 };
-// A2: A log2 e; sr: sigmoid(r)
+// A2: A log2 e; sr: sigmoid(r).  m is NaN for a > 1 (A > 0).
 template <bool NORM>
 __device__ __forceinline__ Token token(f2 sr, f2 A2) {
   Token t;
   t.sr = sr;
-  const f2 L2 = mul2(A2, sr);
-  float lo, hi;
-  unpair(L2, lo, hi);
-  t.a = pair(ex2(lo), ex2(hi));
-  t.m = NORM ? root_of(L2, t.a) : both(1.f);
+  const f2 L2 = mul2(A2, sr), d = short_of_one(L2), near = fma2(d, both(-1.f), both(1.f));
+  float l0, l1, n0, n1, a0, a1;
+  unpair(L2, l0, l1);
+  unpair(near, n0, n1);
+  a0 = l0 > kNear ? n0 : ex2(l0);
+  a1 = l1 > kNear ? n1 : ex2(l1);
+  t.a = pair(a0, a1);
+  t.m = both(1.f);
+  if (NORM) {
+    float s0, s1;
+    unpair(mul2(d, add2(near, both(1.f))), s0, s1);
+    t.m = pair(sqrt_approx(l0 > kNear ? s0 : fmaf(-a0, a0, 1.f)),
+               sqrt_approx(l1 > kNear ? s1 : fmaf(-a1, a1, 1.f)));
+  }
   return t;
 }
 // Two sigmoids for one reciprocal, which is twice an exponential's time: 1 / (1 + e) (1 + f) times the other
@@ -762,11 +776,6 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_bwd(const RecArgs a, const i
     cluster_arrive();
     cluster_wait();
 
-    auto decay_of = [&](f2 sr) {
-      float lo, hi;
-      unpair(mul2(A2, sr), lo, hi);
-      return pair(ex2(lo), ex2(hi));
-    };
     // the state that a segment starts from, the gradient of the one it ends with
     auto origin = [&](int n) {
       return a.h0 && n < a.n_seq ? load_state(a.h0 + (int64_t)n * a.D + c0, nv) : both(0.f);
@@ -786,7 +795,7 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_bwd(const RecArgs a, const i
       if (starts == 0 && left >= kK) {
         f2 at[kK];
 #pragma unroll
-        for (int k = 0; k < kK; ++k) at[k] = decay_of(sigmoid2(in.get(place, 1, k, tw + k)));
+        for (int k = 0; k < kK; ++k) at[k] = decay_of(mul2(A2, sigmoid2(in.get(place, 1, k, tw + k))));
         mine = Map{at[kK - 1], mul2(at[kK - 1], in.get(place, 3, kK - 1, tw + kK - 1))};
 #pragma unroll
         for (int k = kK - 2; k >= 0; --k)
@@ -795,7 +804,7 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_bwd(const RecArgs a, const i
         const int *mark = s.mark[step & 3];
 #pragma unroll 1
         for (int k = min(kK, left) - 1; k >= 0; --k) {
-          const f2 at = decay_of(sigmoid2(in.get(place, 1, k, tw + k)));
+          const f2 at = decay_of(mul2(A2, sigmoid2(in.get(place, 1, k, tw + k))));
           f2 g = in.get(place, 3, k, tw + k);
           if (starts >> (k + 1) & 1) {
             g = add2(g, ending(segment_at(mark, warp * kK + k, s.alive[step & 3])));
@@ -855,8 +864,9 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_bwd(const RecArgs a, const i
         }
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
-          at[k] = decay_of(sr[k]);
-          m[k] = NORM ? root_of(mul2(A2, sr[k]), at[k]) : one;
+          const Token v = token<NORM>(sr[k], A2);
+          at[k] = v.a;
+          m[k] = v.m;
           hb[k] = h;
           h = fma2(at[k], h, mul2(m[k], mul2(si[k], in.get(place, 0, k, tw + k))));
         }
@@ -886,8 +896,9 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_bwd(const RecArgs a, const i
       auto part = [&](int k, f2 &sr, f2 &si, f2 &at, f2 &m) {
         sr = sigmoid2(in.get(place, 1, k, tw + k));
         si = gate ? sigmoid2(in.get(place, 2, k, tw + k)) : one;
-        at = decay_of(sr);
-        m = NORM ? root_of(mul2(A2, sr), at) : one;
+        const Token v = token<NORM>(sr, A2);
+        at = v.a;
+        m = v.m;
       };
       f2 sr, si, at, m;
 #pragma unroll 1
