@@ -25,7 +25,7 @@ BINDING_SOURCE = "mixer_binding.cpp"
 SOURCES = ["gdr_api.cu", "gdr_index.cu", "gdr_staged.cu", "gdr_fused.cu", "gdr_split.cu",
            "gdr_bwd.cu", "gdr_bwd_tc.cu", "gdr_mix_api.cu", "gdr_conv.cu", "gdr_ssm.cu",
            "gdr_ssm_wide.cu", "gdr_ssm_bwd.cu", "gdr_qk.cu", "gdr_delta_step.cu", "gdr_block_api.cu",
-           "gdr_rec.cu", "gdr_norm.cu", "gdr_attn.cu", "gdr_cache.cu"]
+           "gdr_rec.cu", "gdr_rec_bwd.cu", "gdr_norm.cu", "gdr_attn.cu", "gdr_cache.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
               "--expt-relaxed-constexpr"]

@@ -42,7 +42,11 @@ struct RecArgs {
 };
 constexpr int kRecEvery = 8;
 cudaError_t launch_rec_fwd(const RecArgs &a, cudaStream_t stream);
-// the status word of the recurrence's waits (0: none ran out)
+// the states that the backward starts from, without y
+cudaError_t launch_rec_states(const RecArgs &a, cudaStream_t stream);
+// the status words of the recurrence's waits (0: none ran out)
+cudaError_t read_rec_bwd_status(int32_t *out);
+cudaError_t clear_rec_bwd_status();
 cudaError_t read_rec_status(int32_t *out);
 cudaError_t clear_rec_status();
 size_t rec_bwd_workspace(int64_t T, int32_t D, int32_t n_seq, bool kept);
