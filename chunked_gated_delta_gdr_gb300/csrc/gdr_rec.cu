@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_fwd(const RecArgs a) {
       if (SUB > 1) h = through(v.front, h);
       const bool any = s.any[step & 3];
       int seg = s.alive[step & 3];
-      if (any && a.T - first - step * stride > 0)
+      if (SUB > 1 && any && a.T - first - step * stride > 0)
         seg = segments_at<SUB>(s.mark[step & 3], warp * kK * SUB, seg);
       if (left <= 0) return;
       if (a.kept) store<VEC>(a.kept + (int64_t)(tw / kK) * a.D + c0, h, nv);
@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_fwd(const RecArgs a) {
           to += a.y.st;
         }
       } else {
+        if (SUB == 1 && any) seg = segment_at(s.mark[step & 3], warp * kK, seg);
         const int *mark = s.mark[step & 3] + mine0;
 #pragma unroll
         for (int k = 0; k < kK; ++k) {

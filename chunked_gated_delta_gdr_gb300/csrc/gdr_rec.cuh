@@ -670,7 +670,7 @@ inline int groups_of_lanes(int T, int D) {
       best = blocks;
       sub = s;
     }
-    if (2 * blocks >= 3 * (int64_t)sm_count()) break;
+    if (2 * blocks >= 3 * (int64_t)sm_count() || tiles <= kMostCl) break;
   }
   return sub;
 }
