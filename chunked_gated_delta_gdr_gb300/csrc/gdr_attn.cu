@@ -496,22 +496,50 @@ __global__ void __launch_bounds__(kWarps * 32, attn_per_sm(D, H))
   copies_wait<0>();
 }
 
-// Joins the parts of the pairs that lie in several ranges, one block a pair and query head; rows
-// without keys get zeros.  The warps take every eighth part, a lane D / 32 columns.
+// Joins the parts of the pairs that lie in several ranges, one block a query head of a pair; rows
+// without keys get zeros.  The warps take every eighth part, a lane D / 32 columns.  A block looks for
+// its pair by its number; where there are more pairs than ranges (BY_RANGE), by the range that the pair
+// starts in, as at most one goes on behind a range's end, and most pairs have nothing to join.
 constexpr int kJoin = 8;  // warps
 
-template <int D>
+template <int D, bool BY_RANGE>
 __global__ void __launch_bounds__(kJoin * 32) k_attn_join(const AttnArgs a, int groups, int per_group, int ctas, int rows) {
   after_previous<true>();
   constexpr int N = D / 32;
-  __shared__ int64_t red[32];
+  __shared__ int64_t red[32], found[2];
   __shared__ float ms[kJoin], ls[kJoin], os[kJoin][D];
   const int pairs = a.Hk * groups, G = a.Hq / a.Hk;
-  const int r = blockIdx.x % rows, b = blockIdx.x / rows / pairs, pair = blockIdx.x / rows % pairs;
+  const int r = blockIdx.x % rows;
+  int b, pair;
+  int64_t all, before;
+  if (BY_RANGE) {
+    const int c = blockIdx.x / rows;
+    for (int i = c; i < a.B; i += ctas) {
+      if (Span(a, i).units() > 0) continue;
+      __nv_bfloat16 *op = reinterpret_cast<__nv_bfloat16 *>(a.o.p) + i * a.o.st;
+      for (int p = 0; p < pairs; ++p) {
+        const int h = p % groups * per_group + r;
+        if (h >= G) continue;
+        for (int d = threadIdx.x; d < a.d; d += kJoin * 32)
+          op[(int64_t)(p / groups * G + h) * a.o.sh + d] = __float2bfloat16_rn(0.f);
+      }
+    }
+    count_units(a, 0, red, all, before);
+    const int64_t share = share_of(all * pairs, ctas), end = (c + 1) * share;
+    if (end >= all * pairs) return;  // the last range
+    int64_t start;
+    b = find_request(a, pairs, end - 1, red, found, start);
+    const int units = Span(a, b).units();
+    pair = (int)((end - 1 - start) / units);
+    before = start / pairs;
+    if (start + (int64_t)pair * units < c * share) return;  // an earlier range's
+  } else {
+    b = blockIdx.x / rows / pairs, pair = blockIdx.x / rows % pairs;
+    if (pair % groups * per_group + r >= G) return;
+    count_units(a, b, red, all, before);
+  }
   const int head = pair / groups, h = pair % groups * per_group + r;
   if (h >= G) return;
-  int64_t all, before;
-  count_units(a, b, red, all, before);
   const int units = Span(a, b).units();
   const int64_t share = share_of(all * pairs, ctas);
   const int64_t u0 = before * pairs + (int64_t)pair * units, u1 = u0 + units;
@@ -661,8 +689,12 @@ cudaError_t run_split(const AttnArgs &a, cudaStream_t stream) {
   e = launch(k_attn_split<D, H, S>, (unsigned)ctas, kWarps * 32, smem, stream, a, groups);
   if (e != cudaSuccess) return e;
   const int rows = G < H ? G : H;
-  return launch(k_attn_join<D>, (unsigned)((int64_t)a.B * a.Hk * groups * rows), kJoin * 32, 0, stream, a,
-                groups, H, ctas, rows);
+  const int64_t all = (int64_t)a.B * a.Hk * groups;
+  if (all <= ctas)
+    return launch(k_attn_join<D, false>, (unsigned)(all * rows), kJoin * 32, 0, stream, a, groups, H,
+                  ctas, rows);
+  return launch(k_attn_join<D, true>, (unsigned)(ctas * rows), kJoin * 32, 0, stream, a, groups, H,
+                ctas, rows);
 }
 
 bool fits16(const Pages &h) {

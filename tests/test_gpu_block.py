@@ -418,6 +418,19 @@ def test_attn_step(lens, Hq, Hk, d, ps, window, dtype):
     ref.assert_attention(o, want, tol)
 
 
+# more pairs of request and head than blocks: pairs that end where a block's range ends or go on over several
+# ranges, rows without keys among them
+@pytest.mark.parametrize("lens,Hq,Hk,d", [
+    ([7 * i % 13 for i in range(400)], 8, 4, 64), ([64] * 700, 2, 1, 128), ([64] * 703, 2, 1, 128),
+    ([0, 9000] + [50 * i % 201 for i in range(350)] + [0], 40, 2, 96), ([0] * 900, 3, 1, 64),
+    ([1] * 640 + [7000], 2, 1, 200), ([20 * i % 333 for i in range(320)], 9, 9, 40)])
+def test_attn_step_many_requests(lens, Hq, Hk, d):
+    q, kc, vc, table, n = attn_inputs(lens, Hq, Hk, d, 16, BF16)
+    o = gdr.attn_step(dev(q), dev(kc), dev(vc), dev(table), dev(n))
+    want, tol = ref.attention(q, kc, vc, table, lens, d ** -0.5, 0)
+    ref.assert_attention(o, want, tol)
+
+
 def test_attn_step_masked_places():
     # infinities and NaN left of the window; pages that are not there; lengths beyond the table
     lens, ps, window = [200, 90, 150, 40], 16, 50
