@@ -8,12 +8,19 @@
 //   dx = G m si,  di = G m x si (1 - si),  dL = G a_t (h_{t-1} - si x a_t / m_t)  (L = log a_t),
 //   dr = dL A sr (1 - sr),  dA = sum_t dL sr.
 //
-// One pass over the data: a cluster of blocks walks along the tokens of 64 channels, all of them with
-// the same step of CL * P * K tokens.  A thread holds two channels of K neighbouring tokens in
-// registers and reduces them to one pair (A, U): h_out = A h_in + U.  The pairs of a block's warps meet
-// in its shared memory, those of the cluster's blocks in everyone's (distributed shared memory), and
-// each thread then runs through its tokens from its true state.  The alternative, ranges that are
-// scanned from a zero state, chained and scanned again, reads and computes everything twice.
+// One pass over the data: a cluster of blocks walks along the tokens of 64, 32 or 16 channels, all of them
+// with the same step.  A lane holds two channels of eight neighbouring tokens in registers and reduces
+// them to one pair (A, U): h_out = A h_in + U.  The pairs of a block's warps meet in its shared memory,
+// those of the cluster's blocks in everyone's (distributed shared memory), and each lane then runs
+// through its tokens from its true state.  The alternative, ranges that are scanned from a zero state,
+// chained and scanned again, reads and computes everything twice.
+//
+// What bounds it: latency, before HBM.  32,768 x 4,096 in bf16 with an input gate: 264 us for 158 of bytes
+// (60 % of a copy's rate); 16 warps an SM, as many as 128 registers a thread leave, issue in about half of
+// the cycles: most of what they wait for is an instruction's own latency (decay, normaliser and two
+// gates are 3 exponentials, a reciprocal and a square root a token) and the chain's meetings.  Without an eighth
+// warp for the chain, all eight waited for each step's maps.  Two reciprocals a token instead of one for both
+// gates, products without pairs, and steps that wait for their own copies were each slower and are gone.
 #include "gdr_rec.cuh"
 
 namespace gdr {
@@ -105,16 +112,19 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_fwd(const RecArgs a) {
           q = fminf(q, p);
           make(k, sr, mul2(si, in.get(place, 0, k, tw + k)));
         }
-        // places that no token or channel was copied to hold anything: they do not decide
-        const bool whole = a.T - first - step * stride >= kK * SUB;
-        alone = !whole || __any_sync(0xffffffffu, nv > 0 && q == 0.f);
+        alone = __any_sync(0xffffffffu, q == 0.f);
       }
       if (alone) {
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
-          f2 x = in.get(place, 0, k, tw + k);
-          if (gate) x = mul2(x, sigmoid2(in.get(place, 2, k, tw + k)));
-          make(k, sigmoid2(in.get(place, 1, k, tw + k)), x);
+          const f2 x = in.get(place, 0, k, tw + k), r = in.get(place, 1, k, tw + k);
+          if (gate) {
+            f2 sr, si;
+            sigmoids_apart(r, in.get(place, 2, k, tw + k), sr, si);
+            make(k, sr, mul2(si, x));
+          } else {
+            make(k, sigmoid2(r), x);
+          }
         }
       }
       // segments that start among the tokens: their state goes into the first one

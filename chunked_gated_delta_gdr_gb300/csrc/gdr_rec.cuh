@@ -157,6 +157,17 @@ __device__ __forceinline__ void sigmoids(f2 r, f2 i, f2 &sr, f2 &si, float &q) {
   sr = mul2(pair(a, b), f);
   si = mul2(pair(a, b), e);
 }
+// The same for every value, to the bit where the reciprocals are not 0: a token's results do not depend on
+// which of the two its warp takes, nor so on the tokens of other sequences beside it or on what is left in
+// places that no token was copied to.
+__device__ __forceinline__ void sigmoids_apart(f2 r, f2 i, f2 &sr, f2 &si) {
+  float q;
+  sigmoids(r, i, sr, si, q);
+  if (q == 0.f) {
+    sr = sigmoid2(r);
+    si = sigmoid2(i);
+  }
+}
 
 // ------------------------------------------------------------------ pairs (A, U): h -> A h + U
 //
@@ -658,8 +669,12 @@ cudaError_t run_clusters(const RecArgs &a, int sub, int smem, cudaStream_t strea
   return launch_clusters(kernel, (int)ceil_div64(a.D, channels_of(sub)) * cl, cl, kP * 32, smem, stream, a, more...);
 }
 
-// Groups of lanes: as few as fill three quarters of the blocks that run at once (two a multiprocessor), or
-// those that give the most blocks.
+// Groups of lanes: as few as fill the blocks that run at once (two a multiprocessor), or those that give the
+// most blocks; no more for tokens that are four steps or fewer of the largest clusters.  Forward and
+// backward with 1, 2 and 4 groups in us, bf16: 65,536 x 128 102 + 172, 64 + 101, 56 + 94; 30,000 x 512
+// 73 + 135, 58 + 96, 55 + 88; 30,000 x 1,024 96 + 188, 83 + 156, 91 + 157; 8,192 x 2,560 56 + 104, 62 + 111,
+// 97 + 169; 32,768 x 4,096 277 + 544, 297 + 555, 339 + 608; 4,096 x 1,024 20 + 31, 21 + 35, 21 + 38;
+// 1,500 x 680 11 + 17, 11 + 19, 14 + 24; 10 x 64 6 + 9, with 4 groups 8 + 12.
 inline int groups_of_lanes(int T, int D) {
   int64_t best = 0;
   int sub = 1;
@@ -670,7 +685,7 @@ inline int groups_of_lanes(int T, int D) {
       best = blocks;
       sub = s;
     }
-    if (2 * blocks >= 3 * (int64_t)sm_count() || tiles <= kMostCl) break;
+    if (blocks >= 2 * (int64_t)sm_count() || tiles <= 4 * kMostCl) break;
   }
   return sub;
 }

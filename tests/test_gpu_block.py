@@ -179,6 +179,27 @@ def test_rec_values_outside_the_segments_and_in_others_reach_nothing():
         assert torch.equal(dh0[[0, 2]], gclean[4][[0, 2]])
 
 
+@pytest.mark.parametrize("T,D", [(61, 64), (1200, 40), (6000, 34)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rec_values_of_others_change_no_bit(T, D, dtype):
+    # gates whose e^-v overflow together, in one of the sequences that a warp's tokens belong to
+    cut = [0, T // 3 + 2, T - T // 4 - 1, T]
+    cud = torch.tensor(cut, dtype=torch.int32, device=DEV)
+    s = rec_inputs(T, 3, D, dtype, True, True, T)
+    far = {k: v.clone() for k, v in s.items()}
+    far["r"][cut[1]:cut[2]] = far["i"][cut[1]:cut[2]] = -70.0
+    out = []
+    for v in (s, far):
+        f = [dev(v[k]) for k in ("x", "r", "A", "i")]
+        y, ht, _ = gdr.rec_fwd(*f, True, dev(s["h0"]), cud, True)
+        dx, dr, _, di, dh0 = gdr.rec_bwd(f[0], f[1], f[2], dev(s["dy"]), f[3], True, dev(s["h0"]), cud,
+                                         dev(s["dht"]))
+        out.append([torch.cat((t[:cut[1]], t[cut[2]:])) for t in (y, dx, dr, di)] +
+                   [t[[0, 2]] for t in (ht, dh0)])
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
 def test_rec_states_that_last():
     # A = 0 and closed gates: a = 1, the state stays as it is, and nothing is added to it
     T, D = 700, 66
