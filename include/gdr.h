@@ -537,7 +537,8 @@ size_t gdr_rec_bwd_workspace_bytes(int64_t T, int32_t D, int32_t n_seq, int32_t 
 
 /*
  * gdr_rec_step -- one token of gdr_rec_fwd for each of the rows of x.
- *   x, r, i, y [rows, D]; state [slots, D] f32 compact, in place
+ *   x, r, i, y [rows, D]; state [slots, D] f32 compact, in place.  Rows name different slots: of a slot
+ *   that two of them name, either may have read or written first.
  */
 int gdr_rec_step(const gdr_tensor_t *x, const gdr_tensor_t *r, const gdr_tensor_t *i,
                  const gdr_tensor_t *A, int32_t normalize, gdr_tensor_t *state,
