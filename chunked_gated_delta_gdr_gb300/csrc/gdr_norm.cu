@@ -11,8 +11,13 @@
 //   dx = r_x (e - n_x mean(e n_x)),  dw_post = sum du n_x.
 // h is computed again from x and the residual rather than read: it was rounded when it was stored.
 //
-// Bound by HBM: every tensor is read or written once, a row stays in registers between its sums.
+// Bound by HBM: every tensor is read or written once, a row stays in registers between its sums.  Gated
+// norm of 65,536 x 32 x 128 in bf16: 239 us, a copy's rate.  8,191 x 16 x 128, both directions: 47 us for 40
+// of bytes.  Residual norm of 16,384 x 4,096 in bf16 with both norms and a gate: forward 85 us for 79 of
+// bytes; backward 162 for 119: 16 warps of 124 registers an SM, of which 2.2 are ready in a cycle that issues,
+// so that instructions count as much as bytes.
 #include "gdr_block.cuh"
+#include "gdr_cluster.cuh"
 
 namespace gdr {
 namespace mix {
@@ -455,71 +460,14 @@ struct Cols {
   __device__ __forceinline__ int at(int j) const { return (gl + j * tpr) * 8; }
 };
 
-// The rows of N tensors on their way into shared memory, `depth` of them.  Without 16-byte alignment,
-// and where a row is too long for it (ring null), rows are loaded when they are used.
-template <typename E, typename R, int NV, bool VEC>
-struct Ring {
-  static constexpr int PE = sizeof(E) / 2, PR = sizeof(R) / 2;
-  uint4 *ring;
-  int units;  // 16-byte parts of a thread's row
-  __device__ __forceinline__ uint4 *place(int s, int unit) const {
-    return ring + (s * units + unit) * blockDim.x + threadIdx.x;
-  }
-  template <typename X>
-  __device__ __forceinline__ void copy(int s, int unit, const Mat &m, int64_t t, int c) const {
-    const X *p = reinterpret_cast<const X *>(m.p) + t * m.st + c;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(X) / 2; ++i) copy16(place(s, unit + i), p + i * (16 / sizeof(X)));
-  }
-  template <typename X>
-  __device__ __forceinline__ Raw8<X> get(int s, int unit, const Mat &m, int64_t t, int c, int n) const {
-    Raw8<X> r = zero8<X>();
-    if (!m.p) return r;
-    if (VEC && ring) {
-      uint4 *w = reinterpret_cast<uint4 *>(&r);
-      if (n > 0) {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(X) / 2; ++i) w[i] = *place(s, unit + i);
-      }
-    } else {
-      r = ld8<VEC>(reinterpret_cast<const X *>(m.p) + t * m.st + c, n);
-    }
-    return r;
-  }
-  // x, residual (, dy, dh): the first unit of each tensor's vector j
-  __device__ __forceinline__ int x(int j) const { return j * PE; }
-  __device__ __forceinline__ int res(int j) const { return NV * PE + j * PR; }
-  __device__ __forceinline__ int dy(int j) const { return NV * (PE + PR) + j * PE; }
-  __device__ __forceinline__ int dh(int j) const { return NV * (2 * PE + PR) + j * PR; }
-  template <bool BWD, int LANES>
-  __device__ __forceinline__ void issue(const ResidArgs &a, int s, int64_t t,
-                                        const Cols<LANES, NV> &cols) const {
-    if (VEC && ring) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = cols.at(j);
-        if (t < a.T && cols.n[j] > 0) {
-          copy<E>(s, x(j), a.x, t, c);
-          if (a.res.p) copy<R>(s, res(j), a.res, t, c);
-          if (BWD) copy<E>(s, dy(j), a.dy, t, c);
-          if (BWD && a.dh.p) copy<R>(s, dh(j), a.dh, t, c);
-        }
-      }
-      copies_commit();
-    }
-  }
-  __device__ __forceinline__ void wait(int depth) const {  // the oldest of `depth` rows is there
-    if (VEC && ring) {
-      if (depth >= 4) copies_wait<3>();
-      else if (depth == 3) copies_wait<2>();
-      else if (depth == 2) copies_wait<1>();
-      else copies_wait<0>();
-    }
-  }
-};
+// n columns of row t from column c on, the others 0; no tensor: zeros.
+template <typename X>
+__device__ __forceinline__ Raw8<X> row_part(const Mat &m, int64_t t, int c, int n) {
+  return m.p ? ld8<false>(reinterpret_cast<const X *>(m.p) + t * m.st + c, n) : zero8<X>();
+}
 
 // u (behind the block's norm, without the gate) enters the residual: h.  Returns the norm's factor.
-template <typename E, int LANES, int NV, bool VEC>
+template <typename E, int LANES, int NV>
 __device__ __forceinline__ float make_h(const ResidArgs &a, const Raw8<E> (&x)[NV], f2 (&h)[NV][4],
                                         const Cols<LANES, NV> &cols, float2 (*red)[32], int &phase) {
   float rx = 1.f;
@@ -541,12 +489,12 @@ __device__ __forceinline__ float make_h(const ResidArgs &a, const Raw8<E> (&x)[N
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], twice(a.scale * rx));
     if (a.wp.p) {
-      params4<VEC>(a.wp, cols.at(j), cols.n[j], p);
+      params4<false>(a.wp, cols.at(j), cols.n[j], p);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], p[i]);
     }
     if (a.g.p) {
-      params4<VEC>(a.g, cols.at(j), cols.n[j], p);
+      params4<false>(a.g, cols.at(j), cols.n[j], p);
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[j][i] = fma2(v[i], p[i], h[j][i]);
     } else {
@@ -560,36 +508,26 @@ __device__ __forceinline__ float make_h(const ResidArgs &a, const Raw8<E> (&x)[N
 
 constexpr int kResidMost = 512;  // threads of a block
 
-template <typename E, typename R, int LANES, int NV, bool VEC>
+template <typename E, typename R, int LANES, int NV>
 __global__ void __launch_bounds__(LANES ? 128 : kResidMost, LANES ? 1 : 2)
-    k_resid_fwd_long(const ResidArgs a, int depth) {
+    k_resid_fwd_any(const ResidArgs a) {
   after_previous<true>();
-  extern __shared__ __align__(16) uint4 ring[];
   __shared__ float2 red[2][32];
   const Cols<LANES, NV> cols(a.C);
-  using I = Ring<E, R, NV, VEC>;
-  const I in{depth ? ring : nullptr, NV * (I::PE + I::PR)};
   const int step = gridDim.x * cols.groups;
-  const int64_t first = (int64_t)blockIdx.x * cols.groups + cols.group;
-  for (int s = 0; s < depth - 1; ++s) in.template issue<false>(a, s, first + (int64_t)s * step, cols);
-  int phase = 0, stage = 0;
+  int phase = 0;
   for (int64_t base = (int64_t)blockIdx.x * cols.groups; base < a.T; base += step) {
     const int64_t t = base + cols.group;
     const bool ok = t < a.T;
-    if (depth) {
-      in.template issue<false>(a, stage == 0 ? depth - 1 : stage - 1, t + (int64_t)(depth - 1) * step, cols);
-      in.wait(depth);
-    }
     Raw8<E> x[NV];
     f2 h[NV][4];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int m = ok ? cols.n[j] : 0;
-      x[j] = in.template get<E>(stage, in.x(j), a.x, t, cols.at(j), m);
-      unpack4(in.template get<R>(stage, in.res(j), a.res, t, cols.at(j), m), h[j]);
+      x[j] = row_part<E>(a.x, t, cols.at(j), m);
+      unpack4(row_part<R>(a.res, t, cols.at(j), m), h[j]);
     }
-    stage = stage + 1 >= depth ? 0 : stage + 1;
-    make_h<E, LANES, NV, VEC>(a, x, h, cols, red, phase);
+    make_h<E, LANES, NV>(a, x, h, cols, red, phase);
     f2 q = twice(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -602,57 +540,47 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, LANES ? 1 : 2)
     for (int j = 0; j < NV; ++j) {
       const int c = cols.at(j);
       if (a.h.p)
-        st8<VEC>(reinterpret_cast<R *>(a.h.p) + t * a.h.st + c, pack4<R>(h[j]), cols.n[j]);
+        st8<false>(reinterpret_cast<R *>(a.h.p) + t * a.h.st + c, pack4<R>(h[j]), cols.n[j]);
       f2 w[4];
-      params4<VEC>(a.w, c, cols.n[j], w);
+      params4<false>(a.w, c, cols.n[j], w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[j][i] = mul2(mul2(h[j][i], twice(r)), w[i]);
-      st8<VEC>(reinterpret_cast<E *>(a.y.p) + t * a.y.st + c, pack4<E>(h[j]), cols.n[j]);
+      st8<false>(reinterpret_cast<E *>(a.y.p) + t * a.y.st + c, pack4<E>(h[j]), cols.n[j]);
     }
   }
-  if (VEC) copies_wait<0>();
 }
 
-template <typename E, typename R, int LANES, int NV, bool VEC>
-__global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_long(const ResidArgs a, int depth) {
+template <typename E, typename R, int LANES, int NV>
+__global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_any(const ResidArgs a) {
   after_previous();
-  extern __shared__ __align__(16) uint4 ring[];
   __shared__ float2 red[2][32];
   const Cols<LANES, NV> cols(a.C);
-  using I = Ring<E, R, NV, VEC>;
-  const I in{depth ? ring : nullptr, 2 * NV * (I::PE + I::PR)};
   f2 dw[NV][4], dp[NV][4], dg[NV][4];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[j][i] = dp[j][i] = dg[j][i] = twice(0.f);
   const int step = gridDim.x * cols.groups;
-  const int64_t first = (int64_t)blockIdx.x * cols.groups + cols.group;
-  for (int s = 0; s < depth - 1; ++s) in.template issue<true>(a, s, first + (int64_t)s * step, cols);
-  int phase = 0, stage = 0;
+  int phase = 0;
   const float inv = 1.f / a.C;
   for (int64_t base = (int64_t)blockIdx.x * cols.groups; base < a.T; base += step) {
     const int64_t t = base + cols.group;
     const bool ok = t < a.T;
-    if (depth) {  // into the place of the row before
-      in.template issue<true>(a, stage == 0 ? depth - 1 : stage - 1, t + (int64_t)(depth - 1) * step, cols);
-      in.wait(depth);
-    }
     Raw8<E> x[NV], dy[NV];
     f2 h[NV][4];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int m = ok ? cols.n[j] : 0;
-      x[j] = in.template get<E>(stage, in.x(j), a.x, t, cols.at(j), m);
-      dy[j] = in.template get<E>(stage, in.dy(j), a.dy, t, cols.at(j), m);
-      unpack4(in.template get<R>(stage, in.res(j), a.res, t, cols.at(j), m), h[j]);
+      x[j] = row_part<E>(a.x, t, cols.at(j), m);
+      dy[j] = row_part<E>(a.dy, t, cols.at(j), m);
+      unpack4(row_part<R>(a.res, t, cols.at(j), m), h[j]);
     }
-    const float rx = make_h<E, LANES, NV, VEC>(a, x, h, cols, red, phase);
+    const float rx = make_h<E, LANES, NV>(a, x, h, cols, red, phase);
     f2 q = twice(0.f), p = twice(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       f2 w[4], e[4];
-      params4<VEC>(a.w, cols.at(j), cols.n[j], w);
+      params4<false>(a.w, cols.at(j), cols.n[j], w);
       unpack4(dy[j], e);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -669,9 +597,9 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_long(
       for (int j = 0; j < NV; ++j) {
         const int c = cols.at(j);
         f2 w[4], e[4], g[4], xs[4];
-        params4<VEC>(a.w, c, cols.n[j], w);
+        params4<false>(a.w, c, cols.n[j], w);
         unpack4(dy[j], e);
-        unpack4(in.template get<R>(stage, in.dh(j), a.dh, t, c, cols.n[j]), g);
+        unpack4(row_part<R>(a.dh, t, c, cols.n[j]), g);
         unpack4(x[j], xs);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -688,21 +616,21 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_long(
             g[i] = fma2(twice(r), fma2(h[j][i], twice(-back), e[i]), g[i]);
         }
         if (a.dres.p)
-          st8<VEC>(reinterpret_cast<R *>(a.dres.p) + t * a.dres.st + c, pack4<R>(g), cols.n[j]);
+          st8<false>(reinterpret_cast<R *>(a.dres.p) + t * a.dres.st + c, pack4<R>(g), cols.n[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           g[i] = mul2(g[i], twice(a.scale));
           e[i] = mul2(xs[i], twice(rx));
         }
         if (a.wp.p) {
-          params4<VEC>(a.wp, c, cols.n[j], w);
+          params4<false>(a.wp, c, cols.n[j], w);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = twice(1.f);
         }
         if (a.g.p) {
           f2 gate[4];
-          params4<VEC>(a.g, c, cols.n[j], gate);
+          params4<false>(a.g, c, cols.n[j], gate);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             dg[j][i] = fma2(g[i], mul2(e[i], w[i]), dg[j][i]);
@@ -721,7 +649,6 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_long(
         }
       }
     }
-    stage = stage + 1 >= depth ? 0 : stage + 1;
     float bx = 0.f;
     if (a.post) bx = rx * rx * row_sum2<LANES>(make_float2(total(q), 0.f), red, phase).x * inv;
     if (!ok) continue;
@@ -735,10 +662,9 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_long(
 #pragma unroll
         for (int i = 0; i < 4; ++i) du[j][i] = mul2(twice(rx), fma2(xs[i], twice(-bx), du[j][i]));
       }
-      st8<VEC>(reinterpret_cast<E *>(a.dx.p) + t * a.dx.st + cols.at(j), pack4<E>(du[j]), cols.n[j]);
+      st8<false>(reinterpret_cast<E *>(a.dx.p) + t * a.dx.st + cols.at(j), pack4<E>(du[j]), cols.n[j]);
     }
   }
-  if (VEC) copies_wait<0>();
   // the block's parts of dw, dw_post and dgate, its row groups in order
   float *out = reinterpret_cast<float *>(a.work) + (int64_t)blockIdx.x * 3 * a.C;
   if (LANES == 0) {
@@ -780,17 +706,23 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_long(
   }
 }
 
-// ------------------------------------------------------------------ rows of up to 8,192 columns
+// ------------------------------------------------------------------ rows of 16-byte vectors
 //
 // One vector of 8 columns a thread, whose parameters stay in registers, and NR rows at a time, which
-// share the exchanges between warps.
+// share the exchanges between warps.  Rows of more columns than a block holds so (forward 8,192, backward
+// 4,096, whose three gradients leave room for 512 threads) lie on a cluster of blocks (WIDE): 2 and 4
+// vectors a thread in one block spilled (backward of 8,192 x 8,192 in bf16 381 us, on two blocks 233;
+// 4,096 x 16,384 554, on four 256; forward of the latter 146, on two 110).
 
 // Sums of K values over the threads of a row, in all of them: a butterfly in which half of the values
 // change places while there is more than one, and for whole blocks the same once more over the
 // warps' sums.
-// The values from `from` to `to` count, the others come out as anything.
-template <int LANES, int K>
-__device__ __forceinline__ void row_sums(float (&v)[K], float (*red)[32 * 4], int &phase, int from = 0,
+// The values from `from` to `to` count, the others come out as anything.  WIDE: over the blocks of a
+// cluster, whose sums go to every one of them; a place is written again after a barrier that its readers
+// came to behind their reading.
+constexpr int kSums = 32 * 8;  // of a row: 64 warps' or 32 of two values, 64 of four
+template <int LANES, int K, bool WIDE>
+__device__ __forceinline__ void row_sums(float (&v)[K], float (*red)[kSums], int &phase, int from = 0,
                                          int to = K) {
   static_assert(K == 1 || K == 2 || K == 4, "values");
 #pragma unroll
@@ -817,9 +749,19 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float (*red)[32 * 4], in
   }
 #pragma unroll
   for (int o = K; o < 32; o <<= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-  const int warps = blockDim.x >> 5;
-  if (lane < K) red[phase][(threadIdx.x >> 5) * K + lane] = m;
-  __syncthreads();
+  int warps = blockDim.x >> 5;
+  if (WIDE) {  // to all blocks of the cluster
+    const int size = cluster_size(), at = (cluster_rank() * warps + (int)(threadIdx.x >> 5)) * K + lane;
+    if (lane < K)
+      for (int b = 0; b < size; ++b)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at_rank(&red[phase][at], b)), "f"(m) : "memory");
+    cluster_arrive();
+    cluster_wait();
+    warps *= size;
+  } else {
+    if (lane < K) red[phase][(threadIdx.x >> 5) * K + lane] = m;
+    __syncthreads();
+  }
   m = 0.f;
   for (int i = lane; i < warps * K; i += 32) m += red[phase][i];
 #pragma unroll
@@ -905,28 +847,34 @@ __device__ __forceinline__ void squares(const In &in, int s, int64_t t, float *s
 // Both kernels take the first norm's sums of the step after this one along with this one's last sums:
 // one exchange less a step.
 
-template <typename E, typename R, int LANES, int NR>
+template <typename E, typename R, int LANES, int NR, bool WIDE>
 __global__ void __launch_bounds__(LANES ? 128 : 1024, 1) k_resid_fwd(const ResidArgs a, int depth) {
   after_previous<true>();
   extern __shared__ __align__(16) uint4 ring[];
-  __shared__ float red[2][32 * 4];
+  __shared__ float red[2][kSums];
   const Cols<LANES, 1> cols(a.C);
-  const int c = cols.at(0), n = cols.n[0];
+  const int size = WIDE ? cluster_size() : 1, block = blockIdx.x / size, blocks = gridDim.x / size;
+  const int c = cols.at(0) + (WIDE ? cluster_rank() * (int)blockDim.x * 8 : 0);
+  const int n = WIDE ? max(0, min(8, a.C - c)) : cols.n[0];
   using In = Ahead<E, R, NR, false>;
   const In in{ring, a, c, n};
-  const int step = gridDim.x * cols.groups * NR;
-  const int64_t first = ((int64_t)blockIdx.x * cols.groups + cols.group) * NR;
+  const int step = blocks * cols.groups * NR;
+  const int64_t first = ((int64_t)block * cols.groups + cols.group) * NR;
   for (int s = 0; s < depth - 1; ++s) in.issue(s, first + (int64_t)s * step);
   const Params par(a, c, n);
+  if (WIDE) {  // every block of the cluster runs before one writes to it
+    cluster_arrive();
+    cluster_wait();
+  }
   int phase = 0, stage = 0;
   const float inv = 1.f / a.C;
   float sum[2 * NR];  // of h^2, and of x^2 in the next step
   in.wait(depth - 1);
   if (a.post) {
     squares<E, In, NR>(in, 0, first, sum + NR);
-    row_sums<LANES, 2 * NR>(sum, red, phase, NR);
+    row_sums<LANES, 2 * NR, WIDE>(sum, red, phase, NR);
   }
-  for (int64_t base = (int64_t)blockIdx.x * cols.groups * NR; base < a.T; base += step) {
+  for (int64_t base = (int64_t)block * cols.groups * NR; base < a.T; base += step) {
     const int64_t t = base + cols.group * NR;
     in.issue(stage == 0 ? depth - 1 : stage - 1, t + (int64_t)(depth - 1) * step);
     f2 h[NR][4];
@@ -948,9 +896,9 @@ __global__ void __launch_bounds__(LANES ? 128 : 1024, 1) k_resid_fwd(const Resid
     in.wait(depth - 1);
     if (a.post) {
       squares<E, In, NR>(in, stage, t + step, sum + NR);
-      row_sums<LANES, 2 * NR>(sum, red, phase);
+      row_sums<LANES, 2 * NR, WIDE>(sum, red, phase);
     } else {
-      row_sums<LANES, 2 * NR>(sum, red, phase, 0, NR);
+      row_sums<LANES, 2 * NR, WIDE>(sum, red, phase, 0, NR);
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -966,31 +914,37 @@ __global__ void __launch_bounds__(LANES ? 128 : 1024, 1) k_resid_fwd(const Resid
   copies_wait<0>();
 }
 
-template <typename E, typename R, int LANES, int NR>
+template <typename E, typename R, int LANES, int NR, bool WIDE>
 __global__ void __launch_bounds__(LANES ? 128 : 512, 1) k_resid_bwd(const ResidArgs a, int depth) {
   after_previous();
   extern __shared__ __align__(16) uint4 ring[];
-  __shared__ float red[2][32 * 4];
+  __shared__ float red[2][kSums];
   const Cols<LANES, 1> cols(a.C);
-  const int c = cols.at(0), n = cols.n[0];
+  const int size = WIDE ? cluster_size() : 1, block = blockIdx.x / size, blocks = gridDim.x / size;
+  const int c = cols.at(0) + (WIDE ? cluster_rank() * (int)blockDim.x * 8 : 0);
+  const int n = WIDE ? max(0, min(8, a.C - c)) : cols.n[0];
   using In = Ahead<E, R, NR, true>;
   const In in{ring, a, c, n};
-  const int step = gridDim.x * cols.groups * NR;
-  const int64_t first = ((int64_t)blockIdx.x * cols.groups + cols.group) * NR;
+  const int step = blocks * cols.groups * NR;
+  const int64_t first = ((int64_t)block * cols.groups + cols.group) * NR;
   for (int s = 0; s < depth - 1; ++s) in.issue(s, first + (int64_t)s * step);
   const Params par(a, c, n);
   f2 dw[4], dp[4], dg[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dw[i] = dp[i] = dg[i] = twice(0.f);
+  if (WIDE) {  // every block of the cluster runs before one writes to it
+    cluster_arrive();
+    cluster_wait();
+  }
   int phase = 0, stage = 0;
   const float inv = 1.f / a.C;
   float last[2 * NR];  // the sums of the norm behind the block, and of x^2 in the next step
   in.wait(depth - 1);
   if (a.post) {
     squares<E, In, NR>(in, 0, first, last + NR);
-    row_sums<LANES, 2 * NR>(last, red, phase, NR);
+    row_sums<LANES, 2 * NR, WIDE>(last, red, phase, NR);
   }
-  for (int64_t base = (int64_t)blockIdx.x * cols.groups * NR; base < a.T; base += step) {
+  for (int64_t base = (int64_t)block * cols.groups * NR; base < a.T; base += step) {
     const int64_t t = base + cols.group * NR;
     in.issue(stage == 0 ? depth - 1 : stage - 1, t + (int64_t)(depth - 1) * step);
     f2 h[NR][4];  // then the gradient behind the gate; with the norm behind the block, times its weight
@@ -1012,7 +966,7 @@ __global__ void __launch_bounds__(LANES ? 128 : 512, 1) k_resid_bwd(const ResidA
       sum[2 * r] = n > 0 ? total(q) : 0.f;
       sum[2 * r + 1] = n > 0 ? total(p) : 0.f;
     }
-    row_sums<LANES, 2 * NR>(sum, red, phase);
+    row_sums<LANES, 2 * NR, WIDE>(sum, red, phase);
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       last[r] = 0.f;
@@ -1057,7 +1011,7 @@ __global__ void __launch_bounds__(LANES ? 128 : 512, 1) k_resid_bwd(const ResidA
     in.wait(depth - 1);
     if (a.post) {
       squares<E, In, NR>(in, stage, t + step, last + NR);
-      row_sums<LANES, 2 * NR>(last, red, phase);
+      row_sums<LANES, 2 * NR, WIDE>(last, red, phase);
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -1078,7 +1032,7 @@ __global__ void __launch_bounds__(LANES ? 128 : 512, 1) k_resid_bwd(const ResidA
   }
   copies_wait<0>();
   // the block's parts of dw, dw_post and dgate, its row groups in order
-  float *out = reinterpret_cast<float *>(a.work) + (int64_t)blockIdx.x * 3 * a.C;
+  float *out = reinterpret_cast<float *>(a.work) + (int64_t)block * 3 * a.C;
   constexpr int L = LANES ? LANES : 1;
   __shared__ float sums[LANES ? 128 * 8 : 1];
 #pragma unroll
@@ -1111,38 +1065,24 @@ __global__ void __launch_bounds__(LANES ? 128 : 512, 1) k_resid_bwd(const ResidA
 // Threads that share the register file and shared memory of a multiprocessor in the backward.
 constexpr int kResidThreads = 512, kResidBlocks = 4;
 
-template <typename E, typename R, int LANES, int NV, bool VEC>
-cudaError_t run_resid_long(const ResidArgs &a, bool bwd, cudaStream_t stream) {
+cudaError_t sum_parts(const ResidArgs &a, int64_t blocks, cudaStream_t stream) {
+  if (!(a.dw || a.dwp || a.dg)) return cudaSuccess;
+  return launch(k_sum_parts, dim3((unsigned)((a.C + 31) / 32), 3), kSumWarps * 32, 0, stream,
+                reinterpret_cast<const float *>(a.work), (int)blocks, (int64_t)3 * a.C, a.C, a.dw, a.dwp,
+                a.dg);
+}
+
+template <typename E, typename R, int LANES, int NV>
+cudaError_t run_resid_unaligned(const ResidArgs &a, bool bwd, cudaStream_t stream) {
   // a block of as many warps as a row fills, or 128 threads with a row for every LANES of them
   const int th = LANES ? 128 : (a.C + NV * 256 - 1) / (NV * 256) * 32;
   const int64_t need = ceil_div64(a.T, LANES ? 128 / LANES : 1);
-  using I = Ring<E, R, NV, VEC>;
-  const int unit = (bwd ? 2 : 1) * NV * (I::PE + I::PR) * th * 16;
   int per_sm = (bwd ? kResidThreads : 1024) / th;
   per_sm = per_sm < 1 ? 1 : bwd && per_sm > kResidBlocks ? kResidBlocks : per_sm;
   const int64_t most = (int64_t)sm_count() * per_sm, blocks = need < most ? need : most;
-  // rows ahead: what shared memory holds, up to four, and no more than a block has
-  int depth = VEC ? 200 * 1024 / per_sm / unit : 0;
-  const int64_t turns = ceil_div64(need, blocks);
-  depth = depth > 4 ? 4 : depth;
-  if (turns < depth) depth = (int)turns;
-  const int smem = depth * unit;
-  static std::atomic<uint64_t> done[2];
-  cudaError_t e = cudaSuccess;
-  if (smem > 32 * 1024)  // with the static shared memory above what needs no consent
-    e = bwd ? set_once(k_resid_bwd_long<E, R, LANES, NV, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       200 * 1024, done[1])
-            : set_once(k_resid_fwd_long<E, R, LANES, NV, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       200 * 1024, done[0]);
-  if (e != cudaSuccess) return e;
-  if (!bwd)
-    return launch(k_resid_fwd_long<E, R, LANES, NV, VEC>, (unsigned)blocks, th, smem, stream, a, depth);
-  e = launch(k_resid_bwd_long<E, R, LANES, NV, VEC>, (unsigned)blocks, th, smem, stream, a, depth);
-  if (e != cudaSuccess || !(a.dw || a.dwp || a.dg)) return e;
-  return launch(k_sum_parts, dim3((unsigned)((a.C + 31) / 32), 3), kSumWarps * 32, 0,
-                stream,
-                reinterpret_cast<const float *>(a.work), (int)blocks, (int64_t)3 * a.C, a.C, a.dw,
-                a.dwp, a.dg);
+  if (!bwd) return launch(k_resid_fwd_any<E, R, LANES, NV>, (unsigned)blocks, th, 0, stream, a);
+  const cudaError_t e = launch(k_resid_bwd_any<E, R, LANES, NV>, (unsigned)blocks, th, 0, stream, a);
+  return e == cudaSuccess ? sum_parts(a, blocks, stream) : e;
 }
 
 template <typename E, typename R, int LANES, int NR>
@@ -1163,18 +1103,39 @@ cudaError_t run_resid(const ResidArgs &a, bool bwd, cudaStream_t stream) {
   static std::atomic<uint64_t> done[2];
   cudaError_t e = cudaSuccess;
   if (smem > 32 * 1024)  // with the static shared memory above what needs no consent
-    e = bwd ? set_once(k_resid_bwd<E, R, LANES, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = bwd ? set_once(k_resid_bwd<E, R, LANES, NR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        200 * 1024, done[1])
-            : set_once(k_resid_fwd<E, R, LANES, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            : set_once(k_resid_fwd<E, R, LANES, NR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        200 * 1024, done[0]);
   if (e != cudaSuccess) return e;
-  if (!bwd) return launch(k_resid_fwd<E, R, LANES, NR>, (unsigned)blocks, th, smem, stream, a, depth);
-  e = launch(k_resid_bwd<E, R, LANES, NR>, (unsigned)blocks, th, smem, stream, a, depth);
-  if (e != cudaSuccess || !(a.dw || a.dwp || a.dg)) return e;
-  return launch(k_sum_parts, dim3((unsigned)((a.C + 31) / 32), 3), kSumWarps * 32, 0,
-                stream,
-                reinterpret_cast<const float *>(a.work), (int)blocks, (int64_t)3 * a.C, a.C, a.dw,
-                a.dwp, a.dg);
+  if (!bwd)
+    return launch(k_resid_fwd<E, R, LANES, NR, false>, (unsigned)blocks, th, smem, stream, a, depth);
+  e = launch(k_resid_bwd<E, R, LANES, NR, false>, (unsigned)blocks, th, smem, stream, a, depth);
+  return e == cudaSuccess ? sum_parts(a, blocks, stream) : e;
+}
+
+// Rows of a cluster of blocks, as few as hold them.
+template <typename E, typename R, int NR>
+cudaError_t run_resid_wide(const ResidArgs &a, bool bwd, cudaStream_t stream) {
+  static std::atomic<uint64_t> done[2];
+  static std::atomic<int> known[2][64][kMostCl + 1];
+  const auto kernel = bwd ? k_resid_bwd<E, R, 0, NR, true> : k_resid_fwd<E, R, 0, NR, true>;
+  const int most = bwd ? 512 : 1024, cl = (a.C + most * 8 - 1) / (most * 8);
+  const int th = (a.C + cl * 256 - 1) / (cl * 256) * 32;
+  const int unit = (bwd ? Ahead<E, R, NR, true>::kUnits : Ahead<E, R, NR, false>::kUnits) * th * 16;
+  cudaError_t e = set_once(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024, done[bwd]);
+  if (e != cudaSuccess) return e;
+  int clusters = clusters_at_once(kernel, cl, most, 200 * 1024, known[bwd]);
+  if (clusters < 1) clusters = sm_count() / cl;
+  const int64_t need = ceil_div64(a.T, NR);
+  if (need < clusters) clusters = (int)need;
+  const int64_t turns = ceil_div64(need, clusters);
+  int depth = 200 * 1024 / unit;
+  depth = depth > 4 ? 4 : depth;
+  if (turns < depth) depth = (int)turns;
+  if (depth < 2) depth = 2;
+  e = launch_clusters(kernel, clusters * cl, cl, th, depth * unit, stream, a, depth);
+  return e == cudaSuccess && bwd ? sum_parts(a, clusters, stream) : e;
 }
 
 template <typename E, typename R>
@@ -1186,22 +1147,22 @@ cudaError_t run_resid_for(const ResidArgs &a, bool bwd, cudaStream_t stream) {
                     : fits16(a.y, e) && fits16(a.h, f));
   const int C = a.C;
   if (!vec) {
-    if (C <= 8) return run_resid_long<E, R, 1, 1, false>(a, bwd, stream);
-    if (C <= 256) return run_resid_long<E, R, 32, 1, false>(a, bwd, stream);
-    if (C <= 8192) return run_resid_long<E, R, 0, 2, false>(a, bwd, stream);
-    return run_resid_long<E, R, 0, 4, false>(a, bwd, stream);
+    if (C <= 8) return run_resid_unaligned<E, R, 1, 1>(a, bwd, stream);
+    if (C <= 256) return run_resid_unaligned<E, R, 32, 1>(a, bwd, stream);
+    if (C <= 8192) return run_resid_unaligned<E, R, 0, 2>(a, bwd, stream);
+    return run_resid_unaligned<E, R, 0, 4>(a, bwd, stream);
   }
   if (C <= 8) return run_resid<E, R, 1, 1>(a, bwd, stream);
   if (C <= 64) return run_resid<E, R, 8, 1>(a, bwd, stream);
   if (C <= 128) return run_resid<E, R, 16, 1>(a, bwd, stream);
   if (C <= 256) return run_resid<E, R, 32, 1>(a, bwd, stream);
-  if (C <= (bwd ? 4096 : 8192)) {
-    // two rows at a time where there are enough, and shared memory and registers hold them
-    const bool two = sizeof(E) == 2 && a.T >= 4 * sm_count() && (bwd || C <= 4096);
-    return two ? run_resid<E, R, 0, 2>(a, bwd, stream) : run_resid<E, R, 0, 1>(a, bwd, stream);
+  // two rows at a time where there are enough, and shared memory and registers hold them
+  const bool wide = C > (bwd ? 4096 : 8192);
+  if constexpr (sizeof(E) == 2) {
+    if (a.T >= 4 * sm_count() && (bwd || wide || C <= 4096))
+      return wide ? run_resid_wide<E, R, 2>(a, bwd, stream) : run_resid<E, R, 0, 2>(a, bwd, stream);
   }
-  if (C <= 8192) return run_resid_long<E, R, 0, 2, true>(a, bwd, stream);
-  return run_resid_long<E, R, 0, 4, true>(a, bwd, stream);
+  return wide ? run_resid_wide<E, R, 1>(a, bwd, stream) : run_resid<E, R, 0, 1>(a, bwd, stream);
 }
 cudaError_t run_resid_any(const ResidArgs &a, bool bwd, cudaStream_t stream) {
   if (a.f32) return run_resid_for<float, float>(a, bwd, stream);

@@ -9,7 +9,7 @@
 #include <initializer_list>
 
 #include "gdr_block.cuh"
-#include "gdr_tc.cuh"
+#include "gdr_cluster.cuh"
 
 namespace gdr {
 namespace mix {
@@ -18,8 +18,6 @@ namespace {
 // Nonzero once a wait for another block of a cluster ran out; read by gdr_device_status.
 __device__ int32_t g_rec_status = 0;
 constexpr uint64_t kRecWaitNs = 2000000000ull;  // 2 s a wait
-
-constexpr int kMostCl = 16;  // blocks of a cluster (over 8 with the device's consent)
 
 // ------------------------------------------------------------------ two neighbouring channels
 
@@ -206,34 +204,8 @@ __device__ __forceinline__ float4 packed(Map f) {
 }
 __device__ __forceinline__ Map unpacked(float4 v) { return Map{pair(v.x, v.y), pair(v.z, v.w)}; }
 
-// ------------------------------------------------------------------ the cluster
+// ------------------------------------------------------------------ to the cluster's blocks
 
-__device__ __forceinline__ int cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return (int)r;
-}
-__device__ __forceinline__ int cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return (int)r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-// No block ends while another may write to it.
-__device__ __forceinline__ void cluster_leave() {
-  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
-  cluster_wait();
-}
-__device__ __forceinline__ uint32_t at_rank(const void *p, int rank) {
-  uint32_t to;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(tc::smem_u32(p)), "r"(rank));
-  return to;
-}
 // *p of the block of this rank = v, before the next barrier of the cluster
 __device__ __forceinline__ void put(float4 *p, int rank, float4 v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at_rank(p, rank)), "f"(v.x),
@@ -247,27 +219,6 @@ __device__ __forceinline__ void send(float4 *p, uint64_t *bar, int rank, float4 
           at_rank(p, rank)),
       "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(at_rank(bar, rank))
       : "memory");
-}
-
-template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*kernel)(P...), int blocks, int cluster, int threads,
-                            int smem, cudaStream_t stream, A... args) {
-  cudaLaunchAttribute at[2] = {};
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)cluster;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)blocks);
-  c.blockDim = dim3((unsigned)threads);
-  c.dynamicSmemBytes = (size_t)smem;
-  c.stream = stream;
-  c.attrs = at;
-  c.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
-  if (e != cudaSuccess) cudaGetLastError();
-  return e;
 }
 
 // ------------------------------------------------------------------ segment bounds of tiles
@@ -619,34 +570,6 @@ bool rows_fit(const RecArgs &a, int n, std::initializer_list<Mat> mats,
   return ok;
 }
 
-// Clusters of `cl` blocks that run at once (asked for once for each device and size; -1: unknown).
-template <typename K>
-int clusters_at_once(K *kernel, int cl, int smem, std::atomic<int> (&known)[64][kMostCl + 1]) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-  if (dev >= 0 && dev < 64) {
-    const int n = known[dev][cl].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-  }
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = (unsigned)cl;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)cl);
-  c.blockDim = dim3(kP * 32);
-  c.dynamicSmemBytes = (size_t)smem;
-  c.attrs = &at;
-  c.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) != cudaSuccess) {
-    cudaGetLastError();
-    return -1;
-  }
-  if (n > 0 && dev >= 0 && dev < 64) known[dev][cl].store(n, std::memory_order_relaxed);
-  return n;
-}
-
 // Blocks of a cluster: as many as the tokens fill, while all clusters run at once (a cluster's blocks lie
 // in one part of the GPU, so that fewer fit than their number of blocks says).
 template <typename K>
@@ -654,7 +577,7 @@ int cluster_for(K *kernel, int T, int D, int sub, int smem,
                 std::atomic<int> (&known)[64][kMostCl + 1]) {
   const int64_t groups = ceil_div64(D, channels_of(sub)), tiles = ceil_div64(T, tile_of(sub));
   int cl = tiles < 1 ? 1 : tiles > kMostCl ? kMostCl : (int)tiles;
-  while (cl > 1 && clusters_at_once(kernel, cl, smem, known) < groups) --cl;
+  while (cl > 1 && clusters_at_once(kernel, cl, kP * 32, smem, known) < groups) --cl;
   return cl;
 }
 

@@ -317,6 +317,11 @@ RESID = [  # tokens, columns, type, residual's type (None: no residual), weight,
     (6, 2048, BF16, BF16, False, "plain", False, False), (40, 24, BF16, BF16, True, True, True, False),
     (611, 1024, BF16, BF16, True, True, True, False), (5, 777, BF16, F32, True, True, True, True),
     (0, 64, BF16, BF16, True, True, True, False), (2000, 256, F32, F32, True, False, True, False),
+    # rows on clusters of blocks, one row at a time and two, one step and several
+    (1, 4104, F32, F32, True, True, True, False), (700, 4104, BF16, BF16, True, True, True, False),
+    (640, 8192, BF16, BF16, True, False, True, False), (90, 8200, F32, F32, True, True, True, False),
+    (777, 8200, BF16, F32, True, "plain", False, False), (5, 12296, BF16, BF16, True, True, True, False),
+    (613, 16384, BF16, F32, True, True, True, False), (611, 12000, BF16, None, False, True, True, False),
 ]
 
 
