@@ -406,9 +406,9 @@ cudaError_t run_gated_for(const GatedArgs &a, bool bwd, cudaStream_t stream) {
 // ------------------------------------------------------------------ residual norm
 //
 // A row is held by LANES lanes of a warp, several rows side by side, or (LANES 0) by a whole block of as
-// many warps as it fills with NV vectors of 8 columns a thread.  Rows come by cp.async into a ring in
-// which each thread reads only what it copied itself, and stay packed in registers; products are in
-// pairs.
+// many warps as it fills.  Products are in pairs.  Of two forms the first takes rows at any address, NV times
+// 8 columns a thread, and loads them when they are used, element by element; the second takes rows at
+// multiples of 16 bytes by cp.async into a ring in which each thread reads only what it copied itself.
 
 // Sums over the threads of a row, in all of them.  With whole blocks `phase` names one of two places in
 // red (which the next sum must not share).
@@ -444,32 +444,88 @@ __device__ __forceinline__ void keep(f2 (&f)[4], int n) {
   }
 }
 
-// A thread's columns of one row.
-template <int LANES, int NV>
+// A thread's 8 columns of one row.
+template <int LANES>
 struct Cols {
-  int gl, tpr, group, groups;
-  int n[NV];
+  int first, n, group, groups;
   __device__ __forceinline__ Cols(int C) {
-    tpr = LANES ? LANES : blockDim.x;
-    gl = threadIdx.x % tpr;
+    const int tpr = LANES ? LANES : blockDim.x;
+    first = threadIdx.x % tpr * 8;
     group = threadIdx.x / tpr;
     groups = blockDim.x / tpr;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) n[j] = max(0, min(8, C - at(j)));
+    n = max(0, min(8, C - first));
   }
-  __device__ __forceinline__ int at(int j) const { return (gl + j * tpr) * 8; }
 };
 
+// Rows at any address: a thread has every S-th of 8 S columns, so that a warp's loads of one element a lane
+// lie side by side (S = 32, but for rows in one thread; 4,000 x 4,098 in bf16 with neighbouring columns
+// a thread: forward 114 us, backward 324; so: 50 and 270).
+template <int LANES, int NV>
+struct Spread {
+  static constexpr int S = LANES == 1 ? 1 : 32;
+  int group, groups, first, tpr;
+  int n[NV];  // of the thread's columns, those that are there
+  __device__ __forceinline__ Spread(int C) {
+    tpr = LANES ? LANES : blockDim.x;
+    const int gl = threadIdx.x % tpr;
+    group = threadIdx.x / tpr;
+    groups = blockDim.x / tpr;
+    first = gl / S * 8 * S + gl % S;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) n[j] = max(0, min(8, (C - at(j) + S - 1) / S));
+  }
+  __device__ __forceinline__ int at(int j) const { return first + j * tpr * 8; }
+  __device__ __forceinline__ int at(int j, int i) const { return at(j) + i * S; }
+};
+template <int S>
+__device__ __forceinline__ Raw8<__nv_bfloat16> gather8(const __nv_bfloat16 *p, int n) {
+  const unsigned short *s = reinterpret_cast<const unsigned short *>(p);
+  uint32_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = i < n ? s[i * S] : 0;
+  Raw8<__nv_bfloat16> r;
+  r.a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  return r;
+}
+template <int S>
+__device__ __forceinline__ Raw8<float> gather8(const float *p, int n) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i * S] : 0.f;
+  return pack8(v, float{});
+}
+template <int S, typename X>
+__device__ __forceinline__ void scatter8(X *p, const f2 (&f)[4], int n) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpair(f[i], v[2 * i], v[2 * i + 1]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) st1(p + i * S, v[i]);
+}
 // n columns of row t from column c on, the others 0; no tensor: zeros.
-template <typename X>
+template <int S, typename X>
 __device__ __forceinline__ Raw8<X> row_part(const Mat &m, int64_t t, int c, int n) {
-  return m.p ? ld8<false>(reinterpret_cast<const X *>(m.p) + t * m.st + c, n) : zero8<X>();
+  return m.p ? gather8<S>(reinterpret_cast<const X *>(m.p) + t * m.st + c, n) : zero8<X>();
+}
+// Parameters; null: ones.
+template <int S>
+__device__ __forceinline__ void params_by(const Param &w, int c, int n, f2 (&f)[4]) {
+  if (!w.p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = twice(1.f);
+  } else if (w.bf16) {
+    unpack4(gather8<S>(reinterpret_cast<const __nv_bfloat16 *>(w.p) + c, n), f);
+  } else {
+    unpack4(gather8<S>(reinterpret_cast<const float *>(w.p) + c, n), f);
+  }
 }
 
 // u (behind the block's norm, without the gate) enters the residual: h.  Returns the norm's factor.
 template <typename E, int LANES, int NV>
 __device__ __forceinline__ float make_h(const ResidArgs &a, const Raw8<E> (&x)[NV], f2 (&h)[NV][4],
-                                        const Cols<LANES, NV> &cols, float2 (*red)[32], int &phase) {
+                                        const Spread<LANES, NV> &cols, float2 (*red)[32], int &phase) {
+  constexpr int S = Spread<LANES, NV>::S;
   float rx = 1.f;
   if (a.post) {
     f2 q = twice(0.f);
@@ -489,12 +545,12 @@ __device__ __forceinline__ float make_h(const ResidArgs &a, const Raw8<E> (&x)[N
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], twice(a.scale * rx));
     if (a.wp.p) {
-      params4<false>(a.wp, cols.at(j), cols.n[j], p);
+      params_by<S>(a.wp, cols.at(j), cols.n[j], p);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], p[i]);
     }
     if (a.g.p) {
-      params4<false>(a.g, cols.at(j), cols.n[j], p);
+      params_by<S>(a.g, cols.at(j), cols.n[j], p);
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[j][i] = fma2(v[i], p[i], h[j][i]);
     } else {
@@ -513,7 +569,8 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, LANES ? 1 : 2)
     k_resid_fwd_any(const ResidArgs a) {
   after_previous<true>();
   __shared__ float2 red[2][32];
-  const Cols<LANES, NV> cols(a.C);
+  const Spread<LANES, NV> cols(a.C);
+  constexpr int S = Spread<LANES, NV>::S;
   const int step = gridDim.x * cols.groups;
   int phase = 0;
   for (int64_t base = (int64_t)blockIdx.x * cols.groups; base < a.T; base += step) {
@@ -524,8 +581,8 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, LANES ? 1 : 2)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int m = ok ? cols.n[j] : 0;
-      x[j] = row_part<E>(a.x, t, cols.at(j), m);
-      unpack4(row_part<R>(a.res, t, cols.at(j), m), h[j]);
+      x[j] = row_part<S, E>(a.x, t, cols.at(j), m);
+      unpack4(row_part<S, R>(a.res, t, cols.at(j), m), h[j]);
     }
     make_h<E, LANES, NV>(a, x, h, cols, red, phase);
     f2 q = twice(0.f);
@@ -540,12 +597,12 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, LANES ? 1 : 2)
     for (int j = 0; j < NV; ++j) {
       const int c = cols.at(j);
       if (a.h.p)
-        st8<false>(reinterpret_cast<R *>(a.h.p) + t * a.h.st + c, pack4<R>(h[j]), cols.n[j]);
+        scatter8<S>(reinterpret_cast<R *>(a.h.p) + t * a.h.st + c, h[j], cols.n[j]);
       f2 w[4];
-      params4<false>(a.w, c, cols.n[j], w);
+      params_by<S>(a.w, c, cols.n[j], w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[j][i] = mul2(mul2(h[j][i], twice(r)), w[i]);
-      st8<false>(reinterpret_cast<E *>(a.y.p) + t * a.y.st + c, pack4<E>(h[j]), cols.n[j]);
+      scatter8<S>(reinterpret_cast<E *>(a.y.p) + t * a.y.st + c, h[j], cols.n[j]);
     }
   }
 }
@@ -554,7 +611,8 @@ template <typename E, typename R, int LANES, int NV>
 __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_any(const ResidArgs a) {
   after_previous();
   __shared__ float2 red[2][32];
-  const Cols<LANES, NV> cols(a.C);
+  const Spread<LANES, NV> cols(a.C);
+  constexpr int S = Spread<LANES, NV>::S;
   f2 dw[NV][4], dp[NV][4], dg[NV][4];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -571,16 +629,16 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_any(c
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int m = ok ? cols.n[j] : 0;
-      x[j] = row_part<E>(a.x, t, cols.at(j), m);
-      dy[j] = row_part<E>(a.dy, t, cols.at(j), m);
-      unpack4(row_part<R>(a.res, t, cols.at(j), m), h[j]);
+      x[j] = row_part<S, E>(a.x, t, cols.at(j), m);
+      dy[j] = row_part<S, E>(a.dy, t, cols.at(j), m);
+      unpack4(row_part<S, R>(a.res, t, cols.at(j), m), h[j]);
     }
     const float rx = make_h<E, LANES, NV>(a, x, h, cols, red, phase);
     f2 q = twice(0.f), p = twice(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       f2 w[4], e[4];
-      params4<false>(a.w, cols.at(j), cols.n[j], w);
+      params_by<S>(a.w, cols.at(j), cols.n[j], w);
       unpack4(dy[j], e);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -597,9 +655,9 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_any(c
       for (int j = 0; j < NV; ++j) {
         const int c = cols.at(j);
         f2 w[4], e[4], g[4], xs[4];
-        params4<false>(a.w, c, cols.n[j], w);
+        params_by<S>(a.w, c, cols.n[j], w);
         unpack4(dy[j], e);
-        unpack4(row_part<R>(a.dh, t, c, cols.n[j]), g);
+        unpack4(row_part<S, R>(a.dh, t, c, cols.n[j]), g);
         unpack4(x[j], xs);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -616,21 +674,21 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_any(c
             g[i] = fma2(twice(r), fma2(h[j][i], twice(-back), e[i]), g[i]);
         }
         if (a.dres.p)
-          st8<false>(reinterpret_cast<R *>(a.dres.p) + t * a.dres.st + c, pack4<R>(g), cols.n[j]);
+          scatter8<S>(reinterpret_cast<R *>(a.dres.p) + t * a.dres.st + c, g, cols.n[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           g[i] = mul2(g[i], twice(a.scale));
           e[i] = mul2(xs[i], twice(rx));
         }
         if (a.wp.p) {
-          params4<false>(a.wp, c, cols.n[j], w);
+          params_by<S>(a.wp, c, cols.n[j], w);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = twice(1.f);
         }
         if (a.g.p) {
           f2 gate[4];
-          params4<false>(a.g, c, cols.n[j], gate);
+          params_by<S>(a.g, c, cols.n[j], gate);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             dg[j][i] = fma2(g[i], mul2(e[i], w[i]), dg[j][i]);
@@ -662,7 +720,7 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_any(c
 #pragma unroll
         for (int i = 0; i < 4; ++i) du[j][i] = mul2(twice(rx), fma2(xs[i], twice(-bx), du[j][i]));
       }
-      st8<false>(reinterpret_cast<E *>(a.dx.p) + t * a.dx.st + cols.at(j), pack4<E>(du[j]), cols.n[j]);
+      scatter8<S>(reinterpret_cast<E *>(a.dx.p) + t * a.dx.st + cols.at(j), du[j], cols.n[j]);
     }
   }
   // the block's parts of dw, dw_post and dgate, its row groups in order
@@ -678,9 +736,9 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_any(c
           if (!(b == 0 ? a.dw : b == 1 ? a.dwp : a.dg)) continue;
           float lo, hi;
           unpair(v[b], lo, hi);
-          float *to = out + (int64_t)b * a.C + cols.at(j) + 2 * i;
-          if (2 * i < cols.n[j]) to[0] = lo;
-          if (2 * i + 1 < cols.n[j]) to[1] = hi;
+          float *to = out + (int64_t)b * a.C;
+          if (2 * i < cols.n[j]) to[cols.at(j, 2 * i)] = lo;
+          if (2 * i + 1 < cols.n[j]) to[cols.at(j, 2 * i + 1)] = hi;
         }
       }
   } else {
@@ -693,8 +751,9 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_any(c
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float *to = &sums[cols.group * L + cols.at(j) + 2 * i];
-          unpair(b == 0 ? dw[j][i] : b == 1 ? dp[j][i] : dg[j][i], to[0], to[1]);
+          float *to = &sums[cols.group * L];
+          unpair(b == 0 ? dw[j][i] : b == 1 ? dp[j][i] : dg[j][i], to[cols.at(j, 2 * i)],
+                 to[cols.at(j, 2 * i + 1)]);
         }
       __syncthreads();
       for (int c = threadIdx.x; c < a.C; c += 128) {
@@ -711,7 +770,7 @@ __global__ void __launch_bounds__(LANES ? 128 : kResidMost, 1) k_resid_bwd_any(c
 // One vector of 8 columns a thread, whose parameters stay in registers, and NR rows at a time, which
 // share the exchanges between warps.  Rows of more columns than a block holds so (forward 8,192, backward
 // 4,096, whose three gradients leave room for 512 threads) lie on a cluster of blocks (WIDE): 2 and 4
-// vectors a thread in one block spilled (backward of 8,192 x 8,192 in bf16 381 us, on two blocks 233;
+// vectors a thread in one block spilled (backward of 8,192 x 8,192 in bf16 381 us, on two blocks 235;
 // 4,096 x 16,384 554, on four 256; forward of the latter 146, on two 110).
 
 // Sums of K values over the threads of a row, in all of them: a butterfly in which half of the values
@@ -852,10 +911,10 @@ __global__ void __launch_bounds__(LANES ? 128 : 1024, 1) k_resid_fwd(const Resid
   after_previous<true>();
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float red[2][kSums];
-  const Cols<LANES, 1> cols(a.C);
+  const Cols<LANES> cols(a.C);
   const int size = WIDE ? cluster_size() : 1, block = blockIdx.x / size, blocks = gridDim.x / size;
-  const int c = cols.at(0) + (WIDE ? cluster_rank() * (int)blockDim.x * 8 : 0);
-  const int n = WIDE ? max(0, min(8, a.C - c)) : cols.n[0];
+  const int c = cols.first + (WIDE ? cluster_rank() * (int)blockDim.x * 8 : 0);
+  const int n = WIDE ? max(0, min(8, a.C - c)) : cols.n;
   using In = Ahead<E, R, NR, false>;
   const In in{ring, a, c, n};
   const int step = blocks * cols.groups * NR;
@@ -919,10 +978,10 @@ __global__ void __launch_bounds__(LANES ? 128 : 512, 1) k_resid_bwd(const ResidA
   after_previous();
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float red[2][kSums];
-  const Cols<LANES, 1> cols(a.C);
+  const Cols<LANES> cols(a.C);
   const int size = WIDE ? cluster_size() : 1, block = blockIdx.x / size, blocks = gridDim.x / size;
-  const int c = cols.at(0) + (WIDE ? cluster_rank() * (int)blockDim.x * 8 : 0);
-  const int n = WIDE ? max(0, min(8, a.C - c)) : cols.n[0];
+  const int c = cols.first + (WIDE ? cluster_rank() * (int)blockDim.x * 8 : 0);
+  const int n = WIDE ? max(0, min(8, a.C - c)) : cols.n;
   using In = Ahead<E, R, NR, true>;
   const In in{ring, a, c, n};
   const int step = blocks * cols.groups * NR;
@@ -1149,6 +1208,7 @@ cudaError_t run_resid_for(const ResidArgs &a, bool bwd, cudaStream_t stream) {
   if (!vec) {
     if (C <= 8) return run_resid_unaligned<E, R, 1, 1>(a, bwd, stream);
     if (C <= 256) return run_resid_unaligned<E, R, 32, 1>(a, bwd, stream);
+    if (C <= 4096) return run_resid_unaligned<E, R, 0, 1>(a, bwd, stream);
     if (C <= 8192) return run_resid_unaligned<E, R, 0, 2>(a, bwd, stream);
     return run_resid_unaligned<E, R, 0, 4>(a, bwd, stream);
   }

@@ -322,6 +322,10 @@ RESID = [  # tokens, columns, type, residual's type (None: no residual), weight,
     (640, 8192, BF16, BF16, True, False, True, False), (90, 8200, F32, F32, True, True, True, False),
     (777, 8200, BF16, F32, True, "plain", False, False), (5, 12296, BF16, BF16, True, True, True, False),
     (613, 16384, BF16, F32, True, True, True, False), (611, 12000, BF16, None, False, True, True, False),
+    # rows off 16 bytes, of every number of threads
+    (9, 7, BF16, BF16, True, True, True, False), (200, 33, F32, F32, True, True, True, False),
+    (500, 250, BF16, F32, True, True, True, False), (333, 2049, BF16, BF16, True, True, True, False),
+    (170, 5001, F32, F32, True, "plain", True, False), (160, 8191, BF16, BF16, True, True, True, False),
 ]
 
 
