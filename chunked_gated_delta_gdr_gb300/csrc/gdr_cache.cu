@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kPlan) k_cache_plan(const PlanArgs a, int toke
     const int64_t tok0 = granted;
     granted += total;
     __syncthreads();
-    // new pages of this round, in the order of the requests
+    // new pages of these requests, in their order
     for (int p = p0 + tid; p < p1; p += nt) {
       const int r = row_of_place(page_end, rows, p);
       const int before = r > 0 ? page_end[r - 1] : p0;
