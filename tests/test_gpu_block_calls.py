@@ -124,6 +124,40 @@ def test_on_another_stream_and_two_at_once():
             assert same(p, want[n][0]) and same(q, want[n][1]), n
 
 
+@pytest.mark.parametrize("T,C,dtype", [(640, 12296, BF16), (300, 8200, F32), (45, 16384, BF16)])
+def test_rows_on_clusters_in_place_at_once_and_captured(T, C, dtype):
+    """Rows that several blocks share: outputs over their inputs, two streams, a replayed graph."""
+    r = normal(7)
+    x, res, dy, dh = (r(T, C, dtype=dtype) for _ in range(4))
+    w, wp, g = 1 + r(C), 1 + r(C), r(C)
+    opts = (w, wp, g, 0.7)
+    fwd = lambda: gdr.residual_norm_fwd(x, res, *opts)
+    bwd = lambda: gdr.residual_norm_bwd(x, res, dy, dh, *opts)
+    want, back = fwd(), bwd()
+    a, b = x.clone(), res.clone()
+    gdr.residual_norm_fwd(a, b, *opts, out=a, residual_out=b)
+    assert same((a, b), want)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append((fwd(), bwd()))
+    torch.cuda.synchronize()
+    for p, q in got:
+        assert same(p, want) and same(q, back)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        taped, taped_back = fwd(), bwd()
+    for _ in range(3):
+        for t in (*taped, *taped_back):
+            t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(taped, want) and same(taped_back, back)
+
+
 def test_the_stream_argument():
     r = normal(4)
     x, g, A = r(300, 128, dtype=BF16), r(300, 128, dtype=BF16), decays(r, 128)
