@@ -183,8 +183,11 @@ def cache_plan(lengths: torch.Tensor, new_tokens: torch.Tensor, block_table: tor
     [F] int32, handed out in order from the taken-th on, taken [1] int32.  Returns (slots
     [max_tokens], positions [max_tokens], cu_seqlens [B + 1], lengths [B] and taken [1] afterwards),
     int32: a token's slot is page * page_size + place; behind the last token slots are -1.  A request
-    is given fewer tokens where its row, max_tokens or free_pages end.  ``lengths_out`` may be
-    lengths and ``taken_out`` taken, so that a captured step goes on from its own results.
+    is given fewer tokens where its row, max_tokens or free_pages end; those of the requests behind it then
+    follow at once, so that rows that lie as they were asked for find theirs by cu_seqlens: token j of
+    request b at cu_seqlens[b] + j where that is below cu_seqlens[b + 1], and nowhere else.
+    ``lengths_out`` may be lengths and ``taken_out`` taken, so that a captured step goes on from its own
+    results.
     """
     if stream is not None:
         with torch.cuda.stream(stream):

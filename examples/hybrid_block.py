@@ -120,7 +120,7 @@ class Cache:
         self.table = torch.full((requests, -(-longest // page)), -1, **i32)
         self.free = torch.arange(pages, **i32)
         self.taken, self.lengths = torch.zeros(1, **i32), torch.zeros(requests, **i32)
-        self.one = torch.ones(requests, **i32)
+        self.one, self.rows = torch.ones(requests, **i32), torch.arange(requests, device=device)
         self.rooms = [b.room(self) for b in model.blocks]
 
 
@@ -140,6 +140,17 @@ def packed(lengths, device="cuda"):
     return Place(lengths=lengths, starts=starts[:-1], positions=pos,
                  cu=torch.tensor(starts, dtype=I32, device=device),
                  slots=torch.arange(len(lengths), dtype=I32, device=device))
+
+
+def granted(plan, request, token):
+    """Slots and positions of a call's rows, from what cache_plan returned: row t is new token token[t] of
+    request[t].  The plan packs the tokens that it grants, so that behind a request that is given fewer
+    than it wants they are not where its rows are.  Rows that were given nothing: slot -1."""
+    slots, positions, cu = plan[:3]
+    at = cu[request] + token
+    given = at < cu[request + 1]
+    at = at.clamp(max=slots.shape[0] - 1)
+    return torch.where(given, slots[at], -1), torch.where(given, positions[at], 0), given
 
 
 class HybridBlocks(nn.Module):
@@ -167,23 +178,28 @@ class HybridBlocks(nn.Module):
         """Differentiable: packed [T, hidden] -> [T, hidden]."""
         return self.through(hidden, [lambda y, b=b: b(y, at) for b in self.blocks], gdr.residual_norm)
 
+    def plan(self, cache, new, most):
+        return gdr.cache_plan(cache.lengths, new, cache.table, cache.free, cache.taken, cache.page, most,
+                              cache.lengths, cache.taken)
+
     @torch.no_grad()
     def prefill(self, hidden, at, cache):
-        """Packed prompts of the cache's requests, in their order."""
+        """Packed prompts of the cache's requests, in their order.  Tokens for which there is no room are left
+        out of the cache: cache.lengths then says less than their prompt's length."""
         new = torch.tensor(at.lengths, dtype=I32, device=cache.device)
-        at.cells, _, _, _, _ = gdr.cache_plan(cache.lengths, new, cache.table, cache.free, cache.taken,
-                                              cache.page, hidden.shape[0], cache.lengths, cache.taken)
+        request = torch.repeat_interleave(cache.rows, new.long(), output_size=hidden.shape[0])
+        at.cells, _, _ = granted(self.plan(cache, new, hidden.shape[0]), request, at.positions)
         return self.through(hidden, [lambda y, b=b, r=r: b.prefill(y, at, r)
                                      for b, r in zip(self.blocks, cache.rooms)],
                             gdr.residual_norm_fwd)
 
     @torch.no_grad()
     def step(self, hidden, cache):
-        """One token of each request: hidden [requests, hidden]."""
-        cells, pos, _, _, _ = gdr.cache_plan(cache.lengths, cache.one, cache.table, cache.free,
-                                             cache.taken, cache.page, cache.requests, cache.lengths,
-                                             cache.taken)
-        at = Place(cells=cells, positions=pos, slots=None, table=cache.table, seen=cache.lengths)
+        """One token of each request: hidden [requests, hidden].  A request without room for it is a padded row:
+        its states and pages stay as they are, and its row of the result means nothing."""
+        cells, pos, given = granted(self.plan(cache, cache.one, cache.requests), cache.rows, 0)
+        at = Place(cells=cells, positions=pos, slots=torch.where(given, cache.rows, -1).to(I32),
+                   table=cache.table, seen=torch.where(given, cache.lengths, 0))
         return self.through(hidden, [lambda y, b=b, r=r: b.step(y, at, r)
                                      for b, r in zip(self.blocks, cache.rooms)],
                             gdr.residual_norm_fwd)

@@ -625,8 +625,10 @@ size_t gdr_attn_step_workspace_bytes(int32_t B, int32_t Hq, int32_t Hk, int32_t 
  *   cu_seqlens      int32 [B + 1] out: where each request's new tokens lie in them
  *   lengths_out     int32 [B] out: lengths with the new tokens
  * A request is given fewer tokens than it wants where its row of the table ends, where max_tokens
- * are reached by the requests before it and its own, or where free_pages end; cu_seqlens and
- * lengths_out say how many it was given.  All arrays are DEVICE arrays, compact but for the table;
+ * are reached by what the requests before it and it want (each up to its row's end), or where
+ * free_pages end; cu_seqlens and lengths_out say how many it was given.  Nothing is left out in
+ * slots and positions for what it was not given: token j of request b is at cu_seqlens[b] + j if that
+ * is below cu_seqlens[b + 1], and otherwise nowhere.  All arrays are DEVICE arrays, compact but for the table;
  * lengths_out may be lengths, and taken_out taken; a call that reads the same values again writes the
  * same ones.  width * page_size <= 0x7ff00000.
  */
