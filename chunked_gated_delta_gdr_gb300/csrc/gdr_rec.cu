@@ -149,10 +149,10 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_fwd(const RecArgs a) {
 #pragma unroll
         for (int k = 1; k < kK; ++k) mine = Map{mul2(mine.A, v.at[k]), fma2(v.at[k], mine.U, v.u[k])};
       } else {
-        if (v.starts & 1) mine.A = both(0.f);
+        if (v.starts & 1) mine.A = start_mark();
 #pragma unroll
         for (int k = 1; k < kK; ++k)
-          mine = v.starts >> k & 1 ? Map{both(0.f), v.u[k]}
+          mine = v.starts >> k & 1 ? Map{start_mark(), v.u[k]}
                                    : Map{mul2(mine.A, v.at[k]), fma2(v.at[k], mine.U, v.u[k])};
       }
       if (SUB > 1) __syncwarp();

@@ -169,8 +169,10 @@ __device__ __forceinline__ void sigmoids_apart(f2 r, f2 i, f2 &sr, f2 &si) {
 
 // ------------------------------------------------------------------ pairs (A, U): h -> A h + U
 //
-// A = 0 says that the pair holds a segment's start: what comes before it is not looked at, be it
-// infinite or NaN.  (A product of decays that underflows to 0 says the same of a state that is gone.)
+// A = -0 says that the pair holds a segment's start: what comes before it is not looked at, be it
+// infinite or NaN.  Decays are never negative, so that no product of them is -0 but one with such a
+// pair in it.  A product that underflowed to +0 is a product like any other: an infinity or NaN in
+// front of it is still one behind it (0 times it is NaN).
 
 struct Map {
   f2 A, U;
@@ -181,16 +183,20 @@ __device__ __forceinline__ f2 pick(bool lo, bool hi, f2 yes, f2 no) {
   unpair(no, c, d);
   return pair(lo ? a : c, hi ? b : d);
 }
+__device__ __forceinline__ f2 start_mark() { return both(-0.f); }
+__device__ __forceinline__ bool is_start(float A) { return __float_as_uint(A) == 0x80000000u; }
 __device__ __forceinline__ f2 through(Map f, f2 h) {
   float lo, hi;
   unpair(f.A, lo, hi);
-  return pick(lo == 0.f, hi == 0.f, f.U, fma2(f.A, h, f.U));
+  return pick(is_start(lo), is_start(hi), f.U, fma2(f.A, h, f.U));
 }
 // first f, then g
 __device__ __forceinline__ Map then(Map f, Map g) {
-  float lo, hi;
-  unpair(g.A, lo, hi);
-  return Map{pick(lo == 0.f, hi == 0.f, both(0.f), mul2(f.A, g.A)), through(g, f.U)};
+  float f0, f1, g0, g1;
+  unpair(f.A, f0, f1);
+  unpair(g.A, g0, g1);
+  return Map{pick(is_start(f0) || is_start(g0), is_start(f1) || is_start(g1), start_mark(), mul2(f.A, g.A)),
+             through(g, f.U)};
 }
 // the same where neither holds a segment's start
 __device__ __forceinline__ Map then_inside(Map f, Map g) {

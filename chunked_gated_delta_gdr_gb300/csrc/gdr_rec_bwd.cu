@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_bwd(const RecArgs a, const i
           f2 g = in.get(place, 3, k, tw + k);
           if (starts >> (k + 1) & 1) {
             g = add2(g, ending(own_segment(starts, mark, k, seg)));
-            mine = Map{both(0.f), mul2(at, g)};
+            mine = Map{start_mark(), mul2(at, g)};
           } else {
             mine = Map{mul2(mine.A, at), mul2(at, add2(g, mine.U))};
           }

@@ -512,6 +512,9 @@ int gdr_delta_step(const gdr_tensor_t *q, const gdr_tensor_t *k, const gdr_tenso
  *   h0, ht  [n_seq, D] f32 compact, or NULL (ht of an empty segment: h0's, or zeros)
  *   checkpoints  [gdr_rec_checkpoint_rows(T), D] f32 compact out, or NULL: what gdr_rec_bwd would
  *                compute again, the state before every eighth token
+ * A state that is infinite or NaN is so, one or the other, for the rest of its segment in its channel,
+ * however far the decays behind it reach (a product of them that underflowed times an infinity is NaN);
+ * the gradients likewise, towards the segment's start.  Other segments and channels see nothing of it.
  */
 int gdr_rec_fwd(const gdr_tensor_t *x, const gdr_tensor_t *r, const gdr_tensor_t *i,
                 const gdr_tensor_t *A, int32_t normalize, const gdr_tensor_t *h0,

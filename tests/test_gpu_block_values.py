@@ -85,3 +85,74 @@ def test_attention_weights_have_32_bits():
     for h in range(2):
         bad = (o[:, h] - want).abs() > tol
         assert not bad.any(), (int(bad.sum()), float(((o[:, h] - want).abs() / tol).max()))
+
+
+# ------------------------------------------------------------------ gated linear recurrence
+
+REC = [(300, 64, [0, 300]), (2000, 64, [0, 900, 2000]), (6000, 34, [0, 40, 40, 5900, 6000]), (900, 2600, [0, 900]),
+       (65, 16, [0, 65])]
+
+
+@pytest.mark.parametrize("T,D,cu", REC)
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_recurrence_keeps_infinities_and_nan_to_the_segments_end(T, D, cu, norm, dtype):
+    # decays of e^-9 to 1: their products over a block's tokens underflow to 0.  A NaN in a channel's state,
+    # and an infinity, are there until the segment ends; other channels, and segments behind it, do not see them.
+    x, r, i = (rn(k, T, D, dtype=dtype) for k in (1, 2, 3))
+    A = torch.full((D,), -9.0)
+    h0 = rn(4, len(cu) - 1, D)
+    long = max(range(len(cu) - 1), key=lambda n: cu[n + 1] - cu[n])
+    s, e = cu[long], cu[long + 1]
+    at = [s, s + (e - s) // 5]
+    bad = x.clone()
+    bad[at[0], 0], bad[at[1], 1], bad[at[0], 2], bad[at[1], D - 1] = float("nan"), float("nan"), INF, -INF
+    h0_bad = h0.clone()
+    h0_bad[long, 4] = INF
+    cud = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    place = lambda t: t.to(DEV)
+    run = lambda x, h0: gdr.rec_fwd(place(x), place(r), place(A), place(i), norm, place(h0), cud, True)[:2]
+    y, ht = (t.float().cpu() for t in run(bad, h0_bad))
+    yc, hc = (t.float().cpu() for t in run(x, h0))
+    lost = torch.zeros(T, D, dtype=torch.bool)
+    for t, c in ((at[0], 0), (at[1], 1), (at[0], 2), (at[1], D - 1), (s, 4)):
+        lost[t:e, c] = True
+    assert torch.equal(~torch.isfinite(y), lost)
+    assert torch.equal(y[~lost], yc[~lost])
+    gone = torch.zeros_like(hc, dtype=torch.bool)
+    gone[long] = lost[e - 1]
+    assert torch.equal(~torch.isfinite(ht), gone) and torch.equal(ht[~gone], hc[~gone])
+    assert torch.isnan(y[at[0]:e, 0]).all() and torch.isnan(ht[long, 0])
+
+
+@pytest.mark.parametrize("T,D,cu", REC)
+@pytest.mark.parametrize("norm", [True, False])
+def test_recurrence_gradients_keep_infinities_and_nan(T, D, cu, norm):
+    # the same for the gradient of the state, towards the segment's start
+    x, r, i, dy = (rn(k, T, D) for k in (1, 2, 3, 5))
+    A = torch.full((D,), -9.0)
+    n = len(cu) - 1
+    h0, dht = rn(4, n, D), rn(6, n, D)
+    long = max(range(n), key=lambda k: cu[k + 1] - cu[k])
+    s, e = cu[long], cu[long + 1]
+    t1 = e - 1 - (e - s) // 5
+    bad, dht_bad = dy.clone(), dht.clone()
+    bad[t1, 0], bad[t1, 1], bad[e - 1, 2] = float("nan"), INF, float("nan")
+    dht_bad[long, 4] = -INF
+    cud = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    d = lambda t: t.to(DEV)
+    back = lambda dy, dht: [t.cpu() for t in gdr.rec_bwd(d(x), d(r), d(A), d(dy), d(i), norm, d(h0), cud, d(dht))]
+    dx, dr, dA, di, dh0 = back(bad, dht_bad)
+    clean = back(dy, dht)
+    lost = torch.zeros(T, D, dtype=torch.bool)
+    for t, c in ((t1, 0), (t1, 1), (e - 1, 2), (e - 1, 4)):
+        lost[s:t + 1, c] = True
+    for a, c in zip((dx, dr, di), (clean[0], clean[1], clean[3])):
+        assert torch.equal(a[~lost], c[~lost])
+        assert not torch.isfinite(a[lost]).any()
+    assert torch.equal(~torch.isfinite(dh0[long]), lost[s])
+    keep = torch.ones_like(dh0, dtype=torch.bool)
+    keep[long] = ~lost[s]
+    assert torch.equal(dh0[keep], clean[4][keep])
+    cols = ~lost.any(0)
+    assert torch.equal(dA[cols], clean[2][cols]) and not torch.isfinite(dA[~cols]).any()
