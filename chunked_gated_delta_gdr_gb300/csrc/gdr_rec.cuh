@@ -95,8 +95,8 @@ __device__ __forceinline__ f2 wide(const Raw2<E> &r) {
   return pair(r.lo(), r.hi());
 }
 
-// a = 2^L2 and 1 - a^2.  Next to a = 1 both come from the series of d = 1 - a (the first term left out is
-// 1e-9 of it at the border, ln a = -1/16): the special-function unit's 2^x falls short by 2e-8 on
+// a = 2^L2 and 1 - a^2.  Next to a = 1, above it too, both come from the series of d = 1 - a (the first term
+// left out is 1e-9 of it at the border, |ln a| = 1/16): the special-function unit's 2^x falls short by 2e-8 on
 // average, which a state that lasts for hundreds of tokens adds up, and 1 - a^2 would lose its
 // relative accuracy (8,192 x 2,560: error of dA 6.2e-6 of its norm without the series for a).  Nothing
 // is added to a state with A = 0, and nothing taken from it: d = 0.
@@ -107,13 +107,13 @@ __device__ __forceinline__ f2 short_of_one(f2 L2) {
   p = fma2(p, L2, both(-0.69314718f));
   return mul2(p, L2);
 }
-constexpr float kNear = -0.09016844f;  // L2 above: the series
+constexpr float kNear = 0.09016844f;  // |L2| below: the series
 __device__ __forceinline__ f2 decay_of(f2 L2) {
   const f2 near = fma2(short_of_one(L2), both(-1.f), both(1.f));
   float l0, l1, n0, n1;
   unpair(L2, l0, l1);
   unpair(near, n0, n1);
-  return pair(l0 > kNear ? n0 : ex2(l0), l1 > kNear ? n1 : ex2(l1));
+  return pair(fabsf(l0) < kNear ? n0 : ex2(l0), fabsf(l1) < kNear ? n1 : ex2(l1));
 }
 
 struct Token {
@@ -128,15 +128,15 @@ __device__ __forceinline__ Token token(f2 sr, f2 A2) {
   float l0, l1, n0, n1, a0, a1;
   unpair(L2, l0, l1);
   unpair(near, n0, n1);
-  a0 = l0 > kNear ? n0 : ex2(l0);
-  a1 = l1 > kNear ? n1 : ex2(l1);
+  a0 = fabsf(l0) < kNear ? n0 : ex2(l0);
+  a1 = fabsf(l1) < kNear ? n1 : ex2(l1);
   t.a = pair(a0, a1);
   t.m = both(1.f);
   if (NORM) {
     float s0, s1;
     unpair(mul2(d, add2(near, both(1.f))), s0, s1);
-    t.m = pair(sqrt_approx(l0 > kNear ? s0 : fmaf(-a0, a0, 1.f)),
-               sqrt_approx(l1 > kNear ? s1 : fmaf(-a1, a1, 1.f)));
+    t.m = pair(sqrt_approx(fabsf(l0) < kNear ? s0 : fmaf(-a0, a0, 1.f)),
+               sqrt_approx(fabsf(l1) < kNear ? s1 : fmaf(-a1, a1, 1.f)));
   }
   return t;
 }

@@ -508,7 +508,8 @@ int gdr_delta_step(const gdr_tensor_t *q, const gdr_tensor_t *k, const gdr_tenso
  * gdr_rec_fwd -- gated linear recurrence of each channel over the tokens of its segment:
  *   a_t = exp(A[d] sigmoid(r_t)),  m_t = sqrt(1 - a_t^2) (normalize = 0: 1),
  *   h_t = a_t h_{t-1} + m_t sigmoid(i_t) x_t (i NULL: no such gate),  y_t = h_t.
- *   x, r, i, y  [T, D];  A [D] f32 compact, <= 0 (above, m is NaN)
+ *   x, r, i, y  [T, D];  A [D] f32 compact, <= 0 (above it a > 1: with normalize m is NaN, and
+ *     so is y; without it the recurrence is the same formula, of states that grow)
  *   h0, ht  [n_seq, D] f32 compact, or NULL (ht of an empty segment: h0's, or zeros)
  *   checkpoints  [gdr_rec_checkpoint_rows(T), D] f32 compact out, or NULL: what gdr_rec_bwd would
  *                compute again, the state before every eighth token

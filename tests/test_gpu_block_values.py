@@ -5,7 +5,7 @@ import torch
 
 import block_testlib as ref
 import chunked_gated_delta_gdr_gb300 as gdr
-from mixer_testlib import BF16, F32
+from mixer_testlib import BF16, F32, leaf
 
 pytestmark = pytest.mark.gpu
 
@@ -156,3 +156,67 @@ def test_recurrence_gradients_keep_infinities_and_nan(T, D, cu, norm):
     assert torch.equal(dh0[keep], clean[4][keep])
     cols = ~lost.any(0)
     assert torch.equal(dA[cols], clean[2][cols]) and not torch.isfinite(dA[~cols]).any()
+
+
+def growing(T, D, seed):
+    """Inputs whose decays are above 1, with A from 0.001 to 3, the series' border among A sigmoid(r)."""
+    s = dict(x=rn(seed, T, D), r=rn(seed + 1, T, D), i=rn(seed + 2, T, D), h0=rn(seed + 3, 1, D), dy=rn(seed + 4, T, D),
+             dht=rn(seed + 5, 1, D))
+    s["A"] = 0.001 * 3000.0 ** torch.linspace(0, 1, D)
+    s["r"][:, 0::5] = 20.0  # sigmoid(r) = 1
+    border = s["A"][5::10]
+    border.copy_(0.0625 + 1e-3 * torch.linspace(-1, 1, len(border)))
+    return s
+
+
+def within(got, want, bound, name):
+    off = (got.cpu().double() - want.detach()).abs()
+    assert bool((off <= bound).all()), f"{name}: {float((off / bound).max())} of the bound"
+
+
+@pytest.mark.parametrize("T,D", [(6, 64), (6, 130)])
+def test_recurrence_that_grows(T, D):
+    # A > 0 without the normaliser: the same formula.  A decay's relative error is 2^-22 of the exponential and,
+    # |A sigmoid(r)| being 3 at most, 3 times some 8 roundings of 2^-24 of its argument: 7 * 2^-22, and 8 * 2^-22 = e
+    # for a token's product and sum with it.  With M_t = a M_{t-1} + |u_t|, which no state is above, errors add
+    # up to (t + 1) e M_t; with N_t = |dy_t| + a N_{t+1} those of the gradient of h_t to (T - t) e N_t.  A product
+    # of both has the errors of both and 8 roundings of its own at most, and 1 - sigmoid is off by
+    # 2^-22 absolutely.
+    s = growing(T, D, 20)
+    dev = {k: v.to(DEV) for k, v in s.items()}
+    y, ht, kept = gdr.rec_fwd(dev["x"], dev["r"], dev["A"], dev["i"], False, dev["h0"], None, True, True)
+    leaves = {k: leaf(s[k]) for k in ("x", "r", "A", "i", "h0")}
+    yr, hr, _ = ref.rec(leaves["x"], leaves["r"], leaves["A"], leaves["i"], False, leaves["h0"], [0, T])
+    ((yr * s["dy"].double()).sum() + (hr * s["dht"].double()).sum()).backward()
+    d = {k: v.double() for k, v in s.items()}
+    sr, si = torch.sigmoid(d["r"]), torch.sigmoid(d["i"])
+    a, e = torch.exp(d["A"] * sr), 8 * 2.0 ** -22
+    M, N = [d["h0"][0].abs()], [d["dht"][0].abs()]
+    for t in range(T):
+        M.append(a[t] * M[-1] + (si[t] * d["x"][t]).abs())
+        k = T - 1 - t
+        N.append(d["dy"][k].abs() + (N[-1] if t == 0 else a[k + 1] * N[-1]))
+    before, M = torch.stack(M[:-1]), torch.stack(M[1:])
+    N = torch.stack(N[:0:-1])
+    within(y, yr, torch.arange(1, T + 1)[:, None] * e * M, "y")
+    within(ht, hr, T * e * M[-1:], "final state")
+    dx, dr, dA, di, dh0 = gdr.rec_bwd(dev["x"], dev["r"], dev["A"], dev["dy"], dev["i"], False, dev["h0"], None,
+                                      dev["dht"], checkpoints=kept)
+    q = N * a * before * sr
+    within(dx, leaves["x"].grad, (T + 1) * e * N * si, "dx")
+    within(di, leaves["i"].grad, N * d["x"].abs() * si * ((T + 1) * e * (1 - si) + 2.0 ** -22), "di")
+    within(dr, leaves["r"].grad, q * d["A"] * ((2 * T + 2) * e * (1 - sr) + 2.0 ** -22), "dr")
+    within(dA, leaves["A"].grad, (3 * T + 2) * e * q.sum(0), "dA")
+    within(dh0, leaves["h0"].grad, (T + 1) * e * (a[0] * N[0])[None], "dh0")
+    state = dev["h0"].clone()
+    one = gdr.rec_step(dev["x"][:1], dev["r"][:1], dev["A"], state, dev["i"][:1], False)
+    within(one, yr[:1], e * M[:1], "step")
+    within(state, yr[:1], e * M[:1], "state of a step")
+
+
+def test_recurrence_that_grows_has_no_normaliser():
+    s = growing(6, 64, 30)
+    dev = {k: v.to(DEV) for k, v in s.items()}
+    y, _, _ = gdr.rec_fwd(dev["x"], dev["r"], dev["A"], dev["i"], True, dev["h0"])
+    assert torch.isnan(y).all()
+    assert torch.isnan(gdr.rec_step(dev["x"][:1], dev["r"][:1], dev["A"], dev["h0"], dev["i"][:1])).all()
