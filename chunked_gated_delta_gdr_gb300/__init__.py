@@ -19,6 +19,7 @@ from .api import (  # noqa: F401
     chunk_prep,
     clear_device_status,
     device_status,
+    rec_wait_selftest,
     split_pieces,
     split_plan,
     stage_workspace_bytes,

@@ -54,6 +54,7 @@ SIGNATURES = {
     "gdr_debug_check_cu_seqlens": (ctypes.c_int, [_vp, _i32, _i64, _vp, _vp, _vp]),
     "gdr_device_status": (ctypes.c_int, [_vp]),
     "gdr_debug_wait_selftest": (ctypes.c_int, [ctypes.c_uint32, _vp]),
+    "gdr_debug_rec_wait_selftest": (ctypes.c_int, [ctypes.c_uint32, _i32, _vp]),
     "gdr_clear_device_status": (ctypes.c_int, []),
     # tensors of the mixer's operators are passed as addresses of descriptors
     "gdr_conv_fwd": (ctypes.c_int, [_vp] * 5 + [_i32] * 2 + [_vp] * 3),

@@ -612,5 +612,11 @@ def wait_selftest(limit_us: int = 2000, stream=None) -> None:
     nat.check(nat.lib().gdr_debug_wait_selftest(limit_us, _stream(stream)), "gdr_debug_wait_selftest")
 
 
+def rec_wait_selftest(limit_us: int = 2000, steps: int = 100, stream=None) -> None:
+    """Run the recurrence's bounded-wait self-test (see gdr_debug_rec_wait_selftest)."""
+    nat.check(nat.lib().gdr_debug_rec_wait_selftest(limit_us, steps, _stream(stream)),
+              "gdr_debug_rec_wait_selftest")
+
+
 def clear_device_status() -> None:
     nat.check(nat.lib().gdr_clear_device_status(), "gdr_clear_device_status")

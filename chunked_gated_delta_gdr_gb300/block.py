@@ -36,10 +36,11 @@ def rec_fwd(x: torch.Tensor, r: torch.Tensor, A: torch.Tensor, i: Optional[torch
         a = exp(A sigmoid(r)),  h = a h + sqrt(1 - a^2) sigmoid(i) x,  y = h
 
     x, r, i [T, D] bf16 or fp32 (i None: no such gate); A [D] fp32, not above 0 (where it
-    is, the root is NaN); normalize False: 1 in place of the root, and A of any sign; initial_state [N, D] fp32; cu_seqlens [N + 1] int32 (None: one segment).
-    Returns (y [T, D], final_state [N, D] fp32 or None, checkpoints or None): the last are what
-    ``rec_bwd`` of the same inputs would otherwise compute again.  ``out``, ``final_state`` and
-    ``checkpoints`` [ceil(T / 8), D] fp32 may give them; what is given is written.
+    is, the root is NaN); normalize False: 1 in place of the root, and A of any sign; initial_state
+    [N, D] fp32; cu_seqlens [N + 1] int32 (None: one segment).  Returns (y [T, D], final_state [N, D]
+    fp32 or None, checkpoints or None): the last are what ``rec_bwd`` of the same inputs would
+    otherwise compute again.  ``out``, ``final_state`` and ``checkpoints`` [ceil(T / 8), D] fp32 may
+    give them; what is given is written.
     """
     if stream is not None:
         with torch.cuda.stream(stream):

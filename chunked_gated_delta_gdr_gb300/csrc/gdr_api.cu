@@ -659,6 +659,13 @@ int gdr_debug_wait_selftest(uint32_t limit_us, cudaStream_t stream) {
              : GDR_ERR_CUDA;
 }
 
+int gdr_debug_rec_wait_selftest(uint32_t limit_us, int32_t steps, cudaStream_t stream) {
+  if (limit_us < 1000 || limit_us > 1000000u || steps < 1 || steps > 1000000) return GDR_ERR_SHAPE;
+  int r;
+  if ((r = device_ok())) return r;
+  return launch_rec_wait_selftest(limit_us, steps, stream) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+}
+
 int gdr_clear_device_status(void) {
   return clear_device_status() == cudaSuccess && clear_rec_status() == cudaSuccess ? GDR_OK
                                                                                    : GDR_ERR_CUDA;

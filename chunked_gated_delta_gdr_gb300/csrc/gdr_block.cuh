@@ -49,6 +49,7 @@ cudaError_t read_rec_bwd_status(int32_t *out);
 cudaError_t clear_rec_bwd_status();
 cudaError_t read_rec_status(int32_t *out);
 cudaError_t clear_rec_status();
+cudaError_t launch_rec_wait_selftest(uint32_t limit_us, int32_t steps, cudaStream_t stream);
 size_t rec_bwd_workspace(int64_t T, int32_t D, int32_t n_seq, bool kept);
 cudaError_t launch_rec_bwd(const RecArgs &a, bool kept, cudaStream_t stream);
 // rows of x, r, i, y are T requests; state [slots, D] in place

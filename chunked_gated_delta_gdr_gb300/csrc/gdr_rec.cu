@@ -68,10 +68,11 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_fwd(const RecArgs a) {
     cluster_arrive();  // every block of the cluster runs before one writes to it
     cluster_wait();
     f2 carry = both(0.f);
+    bool lost = false;
     for (int step = 0; step < steps; ++step) {
       meet(kMaps + (step & 1));
       const bool any2 = look(step + 2);
-      chain<false, SUB>(s, step, any0, carry);
+      chain<false, SUB>(s, step, any0, carry, lost);
       any0 = any1;
       any1 = any2;
       __syncwarp();
@@ -221,6 +222,25 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_fwd(const RecArgs a) {
     });
 }
 
+// ------------------------------------------------------------------ waits that run out
+
+// The chain of the first of a cluster's two blocks, of which the second sends nothing: its first wait runs
+// out, the others are not begun.
+__global__ void __launch_bounds__(32) k_rec_wait_selftest(int steps, uint64_t limit_ns) {
+  __shared__ Shared<1> s;
+  s.init();
+  for (int i = threadIdx.x; i < 2 * kHold * 32; i += 32) (&s.warp[0][0][0])[i] = packed(Map{both(1.f), both(0.f)});
+  cluster_arrive();
+  cluster_wait();
+  if (cluster_rank() == 0) {
+    f2 carry = both(0.f);
+    bool lost = false;
+    for (int step = 0; step < steps; ++step) chain<false, 1>(s, step, false, carry, lost, limit_ns);
+  }
+  __syncwarp();
+  cluster_leave();
+}
+
 // ------------------------------------------------------------------ single tokens
 
 // Two channels of one request a thread.
@@ -317,6 +337,10 @@ cudaError_t clear_rec_status() {
   const int32_t zero = 0;
   const cudaError_t e = cudaMemcpyToSymbol(mix::g_rec_status, &zero, sizeof(int32_t));
   return e == cudaSuccess ? clear_rec_bwd_status() : e;
+}
+
+cudaError_t launch_rec_wait_selftest(uint32_t limit_us, int32_t steps, cudaStream_t stream) {
+  return mix::launch_clusters(mix::k_rec_wait_selftest, 2, 2, 32, 0, stream, steps, (uint64_t)limit_us * 1000);
 }
 
 cudaError_t launch_rec_states(const RecArgs &a, cudaStream_t stream) {

@@ -17,7 +17,7 @@ namespace {
 
 // Nonzero once a wait for another block of a cluster ran out; read by gdr_device_status.
 __device__ int32_t g_rec_status = 0;
-constexpr uint64_t kRecWaitNs = 2000000000ull;  // 2 s a wait
+constexpr uint64_t kRecWaitNs = 2000000000ull;  // 2 s, once a block
 
 // ------------------------------------------------------------------ two neighbouring channels
 
@@ -497,8 +497,12 @@ __device__ __forceinline__ void store(E *p, f2 v, int nv) {
 // nobody waits for this block's other writes as at a cluster's barrier.  A place is written again two
 // steps later: by a block that has seen all maps of the step between, whose senders had read this one's.
 // BACK: warps and blocks in reverse.  Only the lanes of one group have maps of their own.
+// lost: a wait of this block ran out.  The results are void then, and it neither sends nor waits any more,
+// but goes on to the end, where the cluster's blocks meet: the others, which miss its maps, do the same within
+// one wait of their own.
 template <bool BACK, int SUB>
-__device__ __forceinline__ void chain(Shared<SUB> &s, int step, bool any, f2 &carry) {
+__device__ __forceinline__ void chain(Shared<SUB> &s, int step, bool any, f2 &carry, bool &lost,
+                                      uint64_t limit_ns = kRecWaitNs) {
   constexpr int L = 32 / SUB;
   const int lane = place_of<SUB>(threadIdx.x & 31), buf = step & 1, rank = cluster_rank(), size = cluster_size();
   const bool speaks = SUB == 1 || (threadIdx.x & 31) < L;
@@ -512,13 +516,15 @@ __device__ __forceinline__ void chain(Shared<SUB> &s, int step, bool any, f2 &ca
     for (int j = 1; j < kHold; ++j) all = then_inside(all, map(j));
   }
   const float4 out = packed(all);
+  if (!lost) {
 #pragma unroll 2
-  for (int to = 0; to < size; ++to)
-    if (speaks) send(&s.block[buf][rank][lane], &s.bar[buf], to, out);
-  if ((threadIdx.x & 31) == 0) tc::mbar_expect_tx(&s.bar[buf], size * L * 16);
-  __syncwarp();
-  if (!tc::mbar_wait(&s.bar[buf], step >> 1 & 1, nullptr, kRecWaitNs))
-    atomicCAS(&g_rec_status, 0, BACK ? 0x602 : 0x601);  // the results are void; go on to the end
+    for (int to = 0; to < size; ++to)
+      if (speaks) send(&s.block[buf][rank][lane], &s.bar[buf], to, out);
+    if ((threadIdx.x & 31) == 0) tc::mbar_expect_tx(&s.bar[buf], size * L * 16);
+    __syncwarp();
+    lost = __any_sync(0xffffffffu, !tc::mbar_wait(&s.bar[buf], step >> 1 & 1, nullptr, limit_ns));
+    if (lost) atomicCAS(&g_rec_status, 0, BACK ? 0x602 : 0x601);
+  }
   f2 h = carry, front = carry;
 #pragma unroll 4
   for (int j = 0; j < size; ++j) {

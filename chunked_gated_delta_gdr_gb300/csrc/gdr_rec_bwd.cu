@@ -67,10 +67,11 @@ __global__ void __launch_bounds__(kP * 32, 2) k_rec_bwd(const RecArgs a, const i
     cluster_arrive();  // every block of the cluster runs before one writes to it
     cluster_wait();
     f2 carry = both(0.f);
+    bool lost = false;
     for (int step = 0; step < steps; ++step) {
       meet(kMaps + (step & 1));
       const bool any2 = look(step + 2);
-      chain<true, SUB>(s, step, any0, carry);
+      chain<true, SUB>(s, step, any0, carry, lost);
       any0 = any1;
       any1 = any2;
       __syncwarp();

@@ -290,10 +290,12 @@ int gdr_debug_check_cu_seqlens(const int32_t *cu_seqlens, int32_t n_seq, int64_t
 /*
  * Device status word of the fused kernel.  Every bounded wait inside the fused
  * kernel that runs out (after 2 s) sets a nonzero code here: 0x1xx producer,
- * 0x2xx MMA issuer, 0x3xx prep warps, 0x4xx state warps (0x6xx: the blocks of the gated
- * linear recurrence, which wait for one another and go on to their end); the CTA then drains its
+ * 0x2xx MMA issuer, 0x3xx prep warps, 0x4xx state warps; the CTA then drains its
  * copies and MMAs in flight, releases its Tensor Memory and returns instead of
- * hanging.  gdr_device_status synchronises the current device and
+ * hanging.  The blocks of the gated linear recurrence, which wait for one another, set 0x601
+ * (forward) or 0x602 (backward): a block whose wait ran out waits no more and goes on to its end, and
+ * those that wait for it do the same, so that a cluster of blocks loses two waits' time at most.
+ * gdr_device_status synchronises the current device and
  * reads the word; gdr_clear_device_status resets it.  0 means no wait ran out.
  */
 int gdr_device_status(int32_t *status_out);
@@ -309,6 +311,12 @@ int gdr_clear_device_status(void);
  */
 #define GDR_STATUS_WAIT_SELFTEST 0x7001
 int gdr_debug_wait_selftest(uint32_t limit_us, cudaStream_t stream);
+/*
+ * The same for the gated linear recurrence's blocks: one that misses another's results in each of `steps`
+ * (1..1000000) steps gives up after `limit_us` microseconds (1000..1000000) in the first, waits in none
+ * of the others, and records 0x601.
+ */
+int gdr_debug_rec_wait_selftest(uint32_t limit_us, int32_t steps, cudaStream_t stream);
 
 /*
  * gdr_chunk_out_noalloc -- gdr_chunk_out for callers that cannot allocate device memory.
