@@ -426,6 +426,7 @@ int gdr_cache_write(const gdr_tensor_t *k, const gdr_tensor_t *v, gdr_tensor_t *
   if (d.shape[0] > kMost || kc.shape[2] != d.shape[1] || kc.shape[3] != d.shape[2])
     return GDR_ERR_SHAPE;
   if (d.shape[1] * d.shape[2] > kMost) return GDR_ERR_SHAPE;
+  if (kc.shape[0] * kc.shape[1] > (int64_t)1 << 31) return GDR_ERR_SHAPE;  // places that no slot names
   if (!slots && d.shape[0] > 0) return GDR_ERR_NULL;
   GDR_TRY(device_ok());
   a.T = (int32_t)d.shape[0];

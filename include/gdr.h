@@ -632,7 +632,8 @@ size_t gdr_attn_step_workspace_bytes(int32_t B, int32_t Hq, int32_t Hk, int32_t 
  *   free_pages      int32 [F]: page numbers; those from *taken on are handed out in order
  *   taken, taken_out   one int32 each: how many of free_pages are handed out, before and after
  *   slots, positions   int32 [max_tokens] out, of the new tokens packed request by request: page *
- *                   page_size + place (-1 on a page < 0) and the token's place in its request; behind
+ *                   page_size + place (-1 on a page < 0, or above 2^31 - 1: gdr_cache_write refuses caches
+ *                   of so many places) and the token's place in its request; behind
  *                   the last token -1 and 0
  *   cu_seqlens      int32 [B + 1] out: where each request's new tokens lie in them
  *   lengths_out     int32 [B] out: lengths with the new tokens
@@ -653,7 +654,7 @@ int gdr_cache_plan(const int32_t *lengths, const int32_t *new_tokens, int32_t B,
 /*
  * gdr_cache_write -- rows of k and v [T, Hk, d] into k_cache and v_cache [pages, page_size, Hk, d] at
  * slots (DEVICE int32 [T], page * page_size + place); a slot outside the cache: a row that is not
- * written.  A slot named by two rows is written by both, in no fixed order.
+ * written.  A slot named by two rows is written by both, in no fixed order.  pages * page_size <= 2^31.
  */
 int gdr_cache_write(const gdr_tensor_t *k, const gdr_tensor_t *v, gdr_tensor_t *k_cache,
                     gdr_tensor_t *v_cache, const int32_t *slots, cudaStream_t stream);
