@@ -613,7 +613,8 @@ size_t gdr_residual_norm_bwd_workspace_bytes(int64_t T, int32_t C);
  *   block_table  int32 [B, width], rows of any stride: place j of request b is place j % page_size of
  *                page block_table[b, j / page_size]; places on pages < 0 or >= pages are left out
  *   lengths      DEVICE int32 [B], the new token's own key among them
- * A row that sees no key gets zeros.  What the cache holds at other places is not looked at.
+ * A row that sees no key gets zeros, and so does one whose scores all are -infinity; an infinite value of a
+ * key that it sees makes its elements infinite (NaN where both signs meet).  What the cache holds at other places is not looked at.
  * width * page_size <= 0x7ff00000.  bf16 with 16-byte aligned cache rows and d % 8 == 0 takes the fast
  * path.  workspace: 256-byte aligned, >= gdr_attn_step_workspace_bytes(B, Hq, Hk, d) bytes.
  */

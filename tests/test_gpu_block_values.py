@@ -87,6 +87,24 @@ def test_attention_weights_have_32_bits():
         assert not bad.any(), (int(bad.sum()), float(((o[:, h] - want).abs() / tol).max()))
 
 
+@pytest.mark.parametrize("Hq,Hk,d,n", [(4, 2, 64, 70), (16, 1, 128, 1000), (3, 3, 200, 5)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attention_of_infinite_scores(Hq, Hk, d, n, dtype):
+    # scores of -infinity: weights of 0; nothing else there: zeros.  Request 0 has only such keys, request 1 one
+    # key beside them, whose weight is 1.
+    page, pages = 16, 2 * -(-n // 16)
+    q, kc, vc = rn(1, 2, Hq, d, dtype=dtype), rn(2, pages, page, Hk, d, dtype=dtype), rn(3, pages, page, Hk, d,
+                                                                                         dtype=dtype)
+    q[..., 0], kc[..., 0] = 1.0, -INF
+    table = torch.arange(pages, dtype=torch.int32).view(2, -1)
+    j = n // 3
+    kc[table[1, j // page], j % page, :, 0] = 0.0
+    o = gdr.attn_step(q.to(DEV), kc.to(DEV), vc.to(DEV), table.to(DEV),
+                      torch.full((2,), n, dtype=torch.int32, device=DEV)).cpu()
+    assert not o[0].any()
+    assert torch.equal(o[1], vc[table[1, j // page], j % page].repeat_interleave(Hq // Hk, 0))
+
+
 # ------------------------------------------------------------------ gated linear recurrence
 
 REC = [(300, 64, [0, 300]), (2000, 64, [0, 900, 2000]), (6000, 34, [0, 40, 40, 5900, 6000]), (900, 2600, [0, 900]),
