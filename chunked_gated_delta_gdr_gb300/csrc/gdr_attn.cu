@@ -2,7 +2,8 @@
 //
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = e^{scale q.k_j - max},  j over the request's last keys.
 //
-// Bound by HBM: keys and values are read once, for all of the query heads that share them.
+// Bound by HBM: keys and values are read once for up to 16 query heads that share them, once more for
+// every further 16 (64 requests of 4,096 keys, 2 key heads of 128: 128 us with 64 query heads, 232 with 128).
 // The work is cut over the keys, whatever the requests' lengths are: all (request, head) pairs' keys
 // in a row, in units of 64, are dealt to the blocks in equal ranges, which every block finds from
 // the lengths on the device.  A block keeps a running maximum, sum and output for each pair in its
@@ -10,16 +11,17 @@
 // kernel, in order.
 //
 // A warp takes 16 keys of a unit: its rows come by cp.async into a ring of its own, so that no barrier
-// is needed before a range's end, and go through mma.sync (16 query rows, of which a group of fewer
-// heads leaves some empty): its rate is far above what HBM feeds, and one instruction needs no
-// accumulator in Tensor Memory that the softmax would have to fetch.  Scores, maxima, sums and
-// outputs are fp32; the probabilities go to the second product as three bf16 parts each, which hold all of
-// their 24 bits (two parts, 17 bits, were no faster: 64 requests of up to 16,384 keys 192 us, 190 with three).
+// is needed before a range's end, and go through mma.sync with the 16 keys (or 16 columns of the values) as
+// its rows and one or two tiles of 8 query heads as its columns, of which a group of fewer heads leaves
+// some empty: its rate is far above what HBM feeds, and one instruction needs no accumulator in Tensor
+// Memory that the softmax would have to fetch.  Scores, maxima, sums and outputs are fp32; the probabilities
+// go to the second product as three bf16 parts each, which hold all of their 24 bits (with two parts, 17
+// bits, the case below takes 192 us as well).
 //
-// 64 requests of up to 16,384 keys, 32 / 4 heads of 128: 192 us, 87 % of a copy's rate.  One request of 32,768
+// 64 requests of up to 16,384 keys, 32 / 4 heads of 128: 192 us, 86 % of a copy's rate.  One request of 32,768
 // keys, 32 / 8 heads: 33 us for 20 of bytes; start, drain and the second kernel are the rest.  8 heads a tile and
 // three blocks an SM where they fit; heads over 128 leave room for one block of four warps (146 requests of
-// 3,314 keys x 256: 59 us for 41 of bytes).
+// 3,314 keys x 256: 60 us for 41 of bytes).
 #include "gdr_block.cuh"
 
 namespace gdr {
@@ -621,7 +623,9 @@ __global__ void __launch_bounds__(kJoin * 32) k_attn_join(const AttnArgs a, int 
 // ------------------------------------------------------------------ any type, size and alignment
 //
 // One block for a request's query head: its warps take every 16th key, a lane 8 of the head's
-// elements.
+// elements.  Every query head reads its keys again, and one request fills as many blocks as it has heads:
+// far from the bytes (64 requests of 4,096 keys, 32 / 4 heads of 128: 2,131 us in fp32 for 158, 2,002 in bf16 off
+// 16 bytes for 79; one of 32,768 keys, 32 / 8 heads, in fp32: 2,363 for 40).
 
 constexpr int kPlainWarps = 16;
 

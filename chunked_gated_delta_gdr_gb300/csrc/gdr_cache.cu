@@ -189,6 +189,8 @@ bool fits16(const Pages &h, int e) {
 cudaError_t launch_cache_plan(const PlanArgs &a, cudaStream_t stream) {
   // few tokens: all in one launch (a block writes some 2,000 in the time of a second launch)
   const int both = a.most <= 4096;
+  // a small block starts sooner and has shorter sums (256 requests of a token: 3.3 us, 4.5 with 1,024
+  // threads), and writes many tokens more slowly (1,024 of them: 5.2 and 4.8)
   const int threads = a.B <= 256 && a.most <= 1024 ? 256 : mix::kPlan;
   const cudaError_t e = mix::launch(mix::k_cache_plan, 1, threads, 0, stream, a, both);
   if (e != cudaSuccess || both) return e;

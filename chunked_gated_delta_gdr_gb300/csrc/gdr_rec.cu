@@ -15,7 +15,7 @@
 // through its tokens from its true state.  The alternative, ranges that are scanned from a zero state,
 // chained and scanned again, reads and computes everything twice.
 //
-// What bounds it: latency, before HBM.  32,768 x 4,096 in bf16 with an input gate: 264 us for 158 of bytes
+// What bounds it: latency, before HBM.  32,768 x 4,096 in bf16 with an input gate: 260 us for 158 of bytes
 // (60 % of a copy's rate); 16 warps an SM, as many as 128 registers a thread leave, issue in about half of
 // the cycles: most of what they wait for is an instruction's own latency (decay, normaliser and two
 // gates are 3 exponentials, a reciprocal and a square root a token) and the chain's meetings.  The chain
@@ -278,7 +278,9 @@ template <typename E, int MODE, int SUB, bool OUT, bool NORM>
 cudaError_t run_fwd_as(const RecArgs &a, cudaStream_t stream) {
   return run_clusters<k_rec_fwd<E, MODE, SUB, OUT, NORM>>(a, SUB, Tokens<E, MODE, 3, 2, SUB>::kBytes, stream);
 }
-// The lanes' groups go by the sizes alone, so that the states are the same with and without y.
+// The lanes' groups go by the sizes alone, so that the states are the same with and without y.  Without the
+// normaliser there is one group, for fewer instances to compile: few channels then cost what the
+// table at groups_of_lanes has for one (65,536 x 128: 1.8 times the time).
 template <typename E, int MODE, bool OUT, bool NORM>
 cudaError_t run_fwd_by(const RecArgs &a, cudaStream_t stream) {
   if (NORM) {

@@ -604,9 +604,11 @@ cudaError_t run_clusters(const RecArgs &a, int sub, int smem, cudaStream_t strea
   return launch_clusters(kernel, (int)ceil_div64(a.D, channels_of(sub)) * cl, cl, kP * 32, smem, stream, a, more...);
 }
 
-// Groups of lanes: as few as fill the blocks that run at once (two a multiprocessor), or those that give the
-// most blocks; no more for tokens that are four steps or fewer of the largest clusters.  Forward and
-// backward with 1, 2 and 4 groups in us, bf16: 65,536 x 128 102 + 172, 64 + 101, 56 + 94; 30,000 x 512
+// Groups of lanes: as few as fill the blocks that run at once, or those that give the most blocks; no more for
+// tokens that are four steps or fewer of the largest clusters.  Blocks that run at once are counted as two
+// a multiprocessor, as they are in bf16, for which the rule was made; the fp32 backward's rows ahead
+// (172,032 bytes) leave room for one.  The rule takes two groups where one is the better by a little
+// (4,096 x 1,024).  Forward and backward with 1, 2 and 4 groups in us, bf16: 65,536 x 128 102 + 172, 64 + 101, 56 + 94; 30,000 x 512
 // 73 + 135, 58 + 96, 55 + 88; 30,000 x 1,024 96 + 188, 83 + 156, 91 + 157; 8,192 x 2,560 56 + 104, 62 + 111,
 // 97 + 169; 32,768 x 4,096 277 + 544, 297 + 555, 339 + 608; 4,096 x 1,024 20 + 31, 21 + 35, 21 + 38;
 // 1,500 x 680 11 + 17, 11 + 19, 14 + 24; 10 x 64 6 + 9, with 4 groups 8 + 12.

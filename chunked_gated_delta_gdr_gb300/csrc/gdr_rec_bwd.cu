@@ -1,9 +1,9 @@
 // gdr_rec_bwd.cu -- the backward of the gated linear recurrence (formulas in gdr_rec.cu): the same walk
 // from the last token to the first, over the states that the forward kept before every kK-th token.  A
 // step's maps need the decays and dy alone; its gradients are computed while the next step's maps are on
-// their way.  8,192 x 2,560 in bf16: 100 us for 36 of bytes (x, r, i, dy, dx, dr, di), bound as the
-// forward is: 16 warps an SM, which recompute each state from the last one kept, where that costs no bytes
-// (keeping all of them in fp32 would be 84 MB more written and read, 25 us of a copy).
+// their way.  8,192 x 2,560: 100 us in bf16 for 43 of bytes (x, r, i, dy, dx, dr, di), 134 in fp32 for 86, bound as
+// the forward is: 16 warps an SM (8 in fp32), which recompute each state from the last one kept, where that
+// costs no bytes (keeping all of them in fp32 would be 84 MB more written and read, 25 us of a copy).
 #include "gdr_rec.cuh"
 
 namespace gdr {
