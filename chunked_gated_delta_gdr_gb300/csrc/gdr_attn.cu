@@ -729,7 +729,8 @@ size_t attn_workspace(int32_t B, int32_t Hq, int32_t Hk, int32_t d) {
 
 cudaError_t launch_attn_step(const AttnArgs &a, cudaStream_t stream) {
   if (a.B == 0) return cudaSuccess;
-  if (!a.f32 && a.d % 8 == 0 && mix::fits16(a.k) && mix::fits16(a.v) && mix::fits4(a.q) &&
+  // (a cache without pages has no address that a copy, even of nothing, may name)
+  if (!a.f32 && a.pages > 0 && a.d % 8 == 0 && mix::fits16(a.k) && mix::fits16(a.v) && mix::fits4(a.q) &&
       mix::fits4(a.o)) {
     if (a.Hq / a.Hk <= 8) {
       if (a.d <= 64) return mix::run_split<64, 8, 4>(a, stream);

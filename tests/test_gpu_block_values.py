@@ -105,6 +105,27 @@ def test_attention_of_infinite_scores(Hq, Hk, d, n, dtype):
     assert torch.equal(o[1], vc[table[1, j // page], j % page].repeat_interleave(Hq // Hk, 0))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_cache_without_pages(dtype):
+    # and tables without columns, and plans and writes of nothing
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    q = rn(1, 3, 4, 64, dtype=dtype).to(DEV)
+    empty = torch.empty(0, 16, 2, 64, dtype=dtype, device=DEV)
+    some = rn(2, 2, 16, 2, 64, dtype=dtype).to(DEV)
+    table = torch.zeros(3, 4, dtype=torch.int32, device=DEV)
+    assert not gdr.attn_step(q, empty, empty, table, i32(5, 0, 40)).any()
+    assert not gdr.attn_step(q, some, some, table[:, :0], i32(5, 0, 40)).any()
+    before = some.clone()
+    gdr.cache_write(q[:, :2], q[:, :2], empty, empty, i32(0, 1, 2))
+    gdr.cache_write(q[:0, :2], q[:0, :2], some, some, i32())
+    assert torch.equal(some, before)
+    slots, pos, cu, lens, taken = gdr.cache_plan(i32(), i32(), table[:0], i32(3, 4), i32(1), 16, 5)
+    assert slots.tolist() == [-1] * 5 and pos.tolist() == [0] * 5 and cu.tolist() == [0]
+    assert lens.tolist() == [] and taken.tolist() == [1]
+    slots, pos, cu, lens, taken = gdr.cache_plan(i32(), i32(), table[:0], i32(), i32(0), 16, 9000)
+    assert slots.tolist() == [-1] * 9000 and not pos.any() and cu.tolist() == [0]
+
+
 # ------------------------------------------------------------------ gated linear recurrence
 
 REC = [(300, 64, [0, 300]), (2000, 64, [0, 900, 2000]), (6000, 34, [0, 40, 40, 5900, 6000]), (900, 2600, [0, 900]),
